@@ -55,7 +55,8 @@ typedef enum {
   LTK_ERR_UNSUPPORTED = 6   /* shape or mode the library does not implement   */
 } ltk_status;
 
-typedef enum { LTK_BF16 = 0, LTK_FP8_E4M3 = 1 } ltk_dtype;
+/* LTK_F16 is a type of the paged cache's inputs only. */
+typedef enum { LTK_BF16 = 0, LTK_FP8_E4M3 = 1, LTK_F16 = 2 } ltk_dtype;
 
 /*
  * Handle configuration (fixed at ltk_create).
@@ -301,6 +302,121 @@ ltk_status ltk_decoupled_topk_noalloc(int dtype, int causal, const void* q, cons
  */
 ltk_status ltk_litedsa_pack(const int* topk_idx, int T, int k, int group, int* union_idx,
                             int* union_len, unsigned int* masks, void* stream);
+
+/*
+ * Paged key/value cache held in 8 bits, and the attention that reads it (the
+ * layer around the indexer: keys and values are appended, the indexer chooses
+ * keys, the attention reads them).
+ *
+ * Cache of one layer (device memory, owned by the caller):
+ *   k_codes, v_codes  e4m3 codes [num_pages, heads, page, dim];
+ *   k_scale, v_scale  fp32 [num_pages, heads]; the value held is code * scale.
+ * page is 16, 32, 64 or 128 tokens, dim 64 or 128.
+ *
+ * A handle binds the four buffers and owns a workspace of a few tens of MiB on
+ * the device it was created on.  Calls on one handle must not overlap on the
+ * GPU (one stream, or synchronise).  They neither allocate nor synchronise and
+ * read the batch on the device, so they can be captured in a CUDA graph.
+ */
+typedef struct {
+  long long num_pages;
+  int heads;
+  int dim;
+  int page;
+  void* k_codes;
+  void* v_codes;
+  float* k_scale;
+  float* v_scale;
+} ltk_kv_config;
+
+typedef struct ltk_kv ltk_kv;
+
+/*
+ * The step's batch: B sequences with N new tokens (queries) in all.
+ *   page_table  device int32 [B, table_width]: pages of each sequence in order;
+ *   seq_lens    device int32 [B]: cached tokens of each sequence, this step's
+ *               new ones among them;
+ *   cu_q        device int32 [B + 1]: tokens cu_q[b] .. cu_q[b+1]-1 are
+ *               sequence b's (0 of them is allowed), cu_q[B] = N.
+ * New token i of sequence b has position seq_lens[b] - n_b + i, n_b its number
+ * of new tokens.  Its position p is row p % page of page page_table[b, p / page].
+ * A page number outside [0, num_pages), a negative position or one past a
+ * rotation table sets the handle's device status to LTK_ERR_ARG: nothing is
+ * written for such a page, and queries that see it get NaN.
+ */
+typedef struct {
+  const int* page_table;
+  int table_width;
+  const int* seq_lens;
+  const int* cu_q;
+  int B;
+  int N;
+} ltk_kv_batch;
+
+ltk_status ltk_kv_create(const ltk_kv_config* cfg, ltk_kv** out);
+
+/* Frees the handle and its workspace (synchronises the device first), not the
+ * cache.  NULL is accepted. */
+void ltk_kv_destroy(ltk_kv* h);
+
+/*
+ * Appends the batch's N new tokens.
+ *   dtype       LTK_BF16 or LTK_F16: type of k, v, q and q_out.
+ *   k, v        device [N, heads, dim]; consecutive tokens k_stride / v_stride
+ *               elements apart (a multiple of 8, so slices of a fused
+ *               projection's output serve as they are).
+ *   cos_table,  device fp32 [table_rows, rot / 2], row p the angles of position
+ *   sin_table   p, or both NULL for no rotation.  The first rot elements of each
+ *               key (and query) head are rotated, rot a multiple of 16:
+ *               elements i and i + rot/2 form a pair, or 2i and 2i + 1 when
+ *               interleaved is 1.
+ *   q, q_out    device [N, q_heads, dim], rotated the same way from q (tokens
+ *               q_stride elements apart) to the contiguous q_out; both NULL to
+ *               leave queries out.  q_out must not overlap q, except that
+ *               q_out == q with contiguous tokens rotates in place.
+ * Each touched (page, head) gets the scale 2^e, e the smallest exponent >= -40
+ * with max|x| <= 448 * 2^e over its tokens; a page that already held tokens
+ * never lowers e, and when e grows its held codes are rounded again.  A token
+ * whose key or value row of a head holds a NaN, an infinity or a value beyond
+ * 448 * 2^40 is held in that head as a NaN key row and a zero value row: every
+ * query that sees it gets NaN, no other query does.
+ */
+ltk_status ltk_kv_append(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* k,
+                         long long k_stride, const void* v, long long v_stride,
+                         const float* cos_table, const float* sin_table, int table_rows, int rot,
+                         int interleaved, const void* q, long long q_stride, int q_heads,
+                         void* q_out, void* stream);
+
+/*
+ * Attention of the batch's N queries over their sequences' cached tokens:
+ *   out = softmax(scale * q . K) V over keys j with j <= p (p the query's
+ *   position) and, when window > 0, j > p - window or j < sinks.
+ *   q           device [N, q_heads, dim], tokens q_stride elements apart;
+ *               q_heads a multiple of the cache's heads; query head i reads KV
+ *               head i / (q_heads / heads).
+ *   max_q       the largest number of queries of one sequence, as a hint for the
+ *               choice of kernel (0: unknown); results are right for any value.
+ *   out         device [N, q_heads, dim] in dtype;  lse device fp32 [N, q_heads]
+ *               (natural logarithm of the sum of exponentials) or NULL.
+ * A query that sees no key gets 0 and -inf.  Value codes must not be NaN
+ * (ltk_kv_append never writes one); rows past a sequence's length are not read.
+ */
+ltk_status ltk_kv_attention(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q,
+                            long long q_stride, int q_heads, int max_q, float scale, int window,
+                            int sinks, void* out, float* lse, void* stream);
+
+/*
+ * The same over chosen keys: idx device int32 [N, k] holds distinct positions in
+ * each query's own sequence (ltk_indexer_topk's out_idx when the chunk is one
+ * sequence); an entry below 0 or beyond the query's position is an empty slot.
+ */
+ltk_status ltk_kv_attention_selected(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q,
+                                     long long q_stride, int q_heads, const int* idx, int k,
+                                     float scale, void* out, float* lse, void* stream);
+
+/* First error raised on the device by the handle's calls so far (0: none) and
+ * clears it; synchronises the stream. */
+ltk_status ltk_kv_status(ltk_kv* h, int* device_status, void* stream);
 
 /* Statistics of the last compute call (synchronises its stream). */
 ltk_status ltk_get_stats(ltk_handle* h, ltk_stats* out);

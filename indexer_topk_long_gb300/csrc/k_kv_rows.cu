@@ -1,0 +1,706 @@
+// k_kv_rows.cu -- attention over the paged e4m3 cache for few query rows per KV
+// head (decode): each code is read once and meets at most 16 rows, so the cache
+// stream bounds the kernel.
+//
+//   t_j = c_row * ks_j * (q . k_j) + log2(vs_j)       (exponents in base 2)
+//   w_j = 2^(t_j - M),  O = sum_j w_j * vcode_j,  l = sum_j w_j / vs_j
+//   out = O / l,  lse = (M + log2 l) ln 2
+//
+// ks, vs are the blocks' scales.  Folding log2(vs) into the exponent keeps the
+// weights that meet the value codes at most 2^(kBoost + kSlack) for any scales,
+// so they go to the matrix product as f16: 11 significant bits down to 2^-24 of
+// the running maximum's weight.  Sums, M and l are fp32.  K and V codes become f16
+// exactly; queries (bf16 or f16) become f16 after a power-of-two scaling of the
+// row, exact but for elements below 2^-22 of the row's largest.
+//
+// Work: the (sequence or query, 16-row group, KV head) units' key tiles of 128
+// form one line that is cut into equal pieces, one per CTA, so ragged lengths
+// need no plan on the host.  A unit cut by a border is merged by the last of its
+// CTAs in a fixed order.  Each of a CTA's 8 warps takes 16 keys of a tile through
+// its own ring of asynchronous 16-byte copies (no block barrier in the loop).
+#include "kv_internal.cuh"
+
+namespace ltk {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kWarpKeys = 16;
+constexpr int kTileKeys = kWarps * kWarpKeys;
+constexpr int kStages = 4;
+constexpr float kMinusHuge = -1e30f;     // running maximum of a row that has seen nothing
+// A weight at the running maximum is 2^kBoost; the maximum is only moved when a
+// score exceeds it by more than kSlack, so weights stay below 2^15 < f16's 65504.
+constexpr float kBoost = 8.f;
+constexpr float kSlack = 7.f;
+
+template <int D>
+struct RowsSmem {
+  static constexpr int kStageBytes = kWarpKeys * D * 2;
+  static constexpr int kMetaFloats = 3 * kWarpKeys;           // ks, vs, valid of each key
+  static constexpr int kWarpBytes = kStages * (kStageBytes + kMetaFloats * 4);
+  static constexpr int kMergeBytes = kWarps * kRowsPerUnit * (D + 2) * 4;
+  static constexpr int kBytes = kWarps * kWarpBytes + kMergeBytes;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Row r (0..15) and 16-byte chunk of a stage's K or V half: byte offset.  Lanes
+// of one quarter warp read chunks of two neighbouring rows (K) or one or two
+// chunks of four rows of equal parity (V); the placement keeps each on distinct
+// banks.
+template <int D>
+__device__ __forceinline__ int place(int r, int chunk) {
+  if constexpr (D == 128) {
+    return r * 128 + ((chunk ^ (r & 6) ^ ((r & 1) << 2)) << 4);
+  } else {
+    const int slot = (r & ~1) | ((r ^ (r >> 1)) & 1);
+    return slot * 64 + ((chunk ^ (((slot >> 2) & 1) << 1)) << 4);
+  }
+}
+
+struct Unit {
+  int q0;          // first query of the unit's sequence (selected: the query)
+  int nq;          // its queries (selected: 1)
+  int pos0;        // position of the first
+  int len;         // cached tokens (selected: list length)
+  int head;        // KV head
+  int row0;        // first row of the unit: row r is query r / group, head r % group
+  int tile0;       // first tile of the unit's window
+  int skip;        // tiles [0, skip) are the sinks'
+  int b;
+};
+
+// Where a cursor stands: unit u of its sequence, key tile t of n_tiles.
+struct Cursor {
+  long long at;          // linear position
+  long long left;        // positions to go
+  int t, n_tiles;
+  int u;                 // unit within the sequence (dense) or -1
+  long long unit;        // unit number (selected)
+  Unit w;
+};
+
+__device__ __forceinline__ int groups_of(int rows) { return (rows + kRowsPerUnit - 1) / kRowsPerUnit; }
+
+// Key tiles of sequence s that some query sees: sinks' tiles, then from the first
+// query's window start to the end.
+__device__ __forceinline__ int tiles_of(const AttnParams& p, const KvSeq& s, int* skip, int* tile0) {
+  if (s.nq == 0 || s.len == 0) return 0;
+  const int n = (s.len + kTileKeys - 1) / kTileKeys;
+  *skip = 0;
+  *tile0 = 0;
+  if (p.window <= 0) return n;
+  const int lo = max(s.pos0 - p.window + 1, 0) / kTileKeys;
+  const int sk = min((min(p.sinks, s.len) + kTileKeys - 1) / kTileKeys, lo);
+  *skip = sk;
+  *tile0 = lo;
+  return sk + n - lo;
+}
+
+template <bool SEL>
+__device__ __forceinline__ void enter_unit(const AttnParams& p, Cursor& c) {
+  if constexpr (SEL) {
+    const int rg = groups_of(p.group);
+    const int per = rg * p.cache.heads;
+    const int n = static_cast<int>(c.unit / per), r = static_cast<int>(c.unit % per);
+    const int b = kv_seq_of_query(p.batch, n);
+    const KvSeq s = kv_seq(p.batch, p.cache, b);
+    c.w.b = b;
+    c.w.q0 = n;
+    c.w.nq = 1;
+    c.w.pos0 = (n >= s.q0 && n < s.q0 + s.nq) ? min(s.pos0 + n - s.q0, s.len - 1) : -1;
+    c.w.len = p.k;
+    c.w.head = r / rg;
+    c.w.row0 = (r % rg) * kRowsPerUnit;
+    c.w.skip = c.w.tile0 = 0;
+    c.n_tiles = (p.k + kTileKeys - 1) / kTileKeys;
+  } else {
+    const int rg = groups_of(c.w.nq * p.group);
+    c.w.head = c.u / rg;
+    c.w.row0 = (c.u % rg) * kRowsPerUnit;
+  }
+}
+
+// Dense: stand on unit u of sequence b (whose tile count is known to be > 0).
+__device__ __forceinline__ void enter_seq(const AttnParams& p, Cursor& c, int b) {
+  const KvSeq s = kv_seq(p.batch, p.cache, b);
+  c.w.b = b;
+  c.w.q0 = s.q0;
+  c.w.nq = s.nq;
+  c.w.pos0 = s.pos0;
+  c.w.len = s.len;
+  c.n_tiles = tiles_of(p, s, &c.w.skip, &c.w.tile0);
+}
+
+// One tile forward.
+template <bool SEL>
+__device__ __forceinline__ void advance(const AttnParams& p, Cursor& c) {
+  ++c.at;
+  --c.left;
+  if (++c.t < c.n_tiles || c.left <= 0) return;
+  c.t = 0;
+  if constexpr (SEL) {
+    ++c.unit;
+    enter_unit<SEL>(p, c);
+  } else {
+    if (++c.u >= groups_of(c.w.nq * p.group) * p.cache.heads) {
+      c.u = 0;
+      int b = c.w.b;
+      do {
+        enter_seq(p, c, ++b);
+      } while (c.n_tiles == 0 && b + 1 < p.batch.B);
+    }
+    enter_unit<SEL>(p, c);
+  }
+}
+
+struct Feed {            // what the next tile's copies need, fetched a step ahead
+  int key;               // selected: this lane's key position (lanes 0-15), -1 none
+  int page;              // dense: the tile's page
+  bool live;             // dense: the tile's 16 keys begin before the length
+};
+
+template <int D, bool SEL>
+__global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p, const int grid) {
+  using S = RowsSmem<D>;
+  constexpr int KS = D / 16;             // k-steps of the score product
+  constexpr int NT = D / 8;              // n-tiles of the value product
+  constexpr int CPR = D / 16;            // 16-byte chunks in a row of codes
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ long long sh_total, sh_start;
+  __shared__ long long sh_warp[kWarps];
+  __shared__ int sh_b;
+  __shared__ int sh_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, cq = lane & 3;
+
+  // --- this CTA's piece of the line -------------------------------------------------------
+  long long total;
+  int n_cta = grid;                      // CTAs with work: every one has a tile at least
+  Cursor head{};
+  if constexpr (SEL) {
+    const int tiles = (p.k + kTileKeys - 1) / kTileKeys;
+    total = static_cast<long long>(p.batch.N) * groups_of(p.group) * p.cache.heads * tiles;
+    n_cta = static_cast<int>(min(static_cast<long long>(grid), total));
+  } else {
+    const int each = (p.batch.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * each, p.batch.B), b1 = min(b0 + each, p.batch.B);
+    long long mine = 0;
+    int sk, t0;
+    for (int b = b0; b < b1; ++b) {
+      const KvSeq s = kv_seq(p.batch, p.cache, b);
+      mine += static_cast<long long>(tiles_of(p, s, &sk, &t0)) * groups_of(s.nq * p.group) * p.cache.heads;
+    }
+    long long incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) sh_warp[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine;
+    total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sh_warp[w];
+      total += sh_warp[w];
+    }
+    n_cta = static_cast<int>(min(static_cast<long long>(grid), max(total, 1ll)));
+    const long long start = blockIdx.x * total / n_cta;
+    if (mine > 0 && start >= before && start < before + mine) {
+      long long x = before;
+      for (int b = b0; b < b1; ++b) {
+        const KvSeq s = kv_seq(p.batch, p.cache, b);
+        const long long n = static_cast<long long>(tiles_of(p, s, &sk, &t0)) * groups_of(s.nq * p.group) * p.cache.heads;
+        if (start < x + n) {
+          sh_b = b;
+          sh_start = x;
+          break;
+        }
+        x += n;
+      }
+    }
+    __syncthreads();
+  }
+  const long long start = blockIdx.x * total / n_cta;
+  const long long end = blockIdx.x < n_cta ? (blockIdx.x + 1) * total / n_cta : start;
+  if (start < end) {
+    head.at = start;
+    head.left = end - start;
+    if constexpr (SEL) {
+      const int tiles = (p.k + kTileKeys - 1) / kTileKeys;
+      head.unit = start / tiles;
+      head.t = static_cast<int>(start % tiles);
+    } else {
+      enter_seq(p, head, sh_b);
+      const long long in = start - sh_start;
+      head.u = static_cast<int>(in / head.n_tiles);
+      head.t = static_cast<int>(in % head.n_tiles);
+    }
+    enter_unit<SEL>(p, head);
+  }
+
+  unsigned char* ring = smem + warp * S::kWarpBytes;
+  float* meta = reinterpret_cast<float*>(ring + kStages * S::kStageBytes);
+  const uint32_t ring_u = smem_u32(ring), meta_u = smem_u32(meta);
+  float* merge_o = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);     // [warp][16][D]
+  float* merge_ml = merge_o + kWarps * kRowsPerUnit * D;                        // [warp][16][2]
+
+  // --- producer: one tile's 16 keys of this warp into a stage -----------------------------
+  Cursor pc = head;                      // producer cursor
+  Feed feed{-1, -1, false};
+  auto fetch = [&]() {                   // index or page of the next tile to produce
+    feed = Feed{-1, -1, false};
+    if (pc.left <= 0) return;
+    if constexpr (SEL) {
+      const int slot = pc.t * kTileKeys + warp * kWarpKeys + lane;
+      if (lane < kWarpKeys && slot < p.k) {
+        const int key = __ldg(p.idx + static_cast<size_t>(pc.w.q0) * p.k + slot);
+        feed.key = key >= 0 && key <= pc.w.pos0 ? key : -1;
+      }
+      feed.live = true;
+    } else {
+      const int tile = pc.t < pc.w.skip ? pc.t : pc.t - pc.w.skip + pc.w.tile0;
+      const int key0 = tile * kTileKeys + warp * kWarpKeys;
+      feed.live = key0 < pc.w.len;
+      if (feed.live)
+        feed.page = __ldg(p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (key0 >> p.cache.page_log2));
+    }
+  };
+  int stage_in = 0;
+  auto produce = [&]() {
+    if (pc.left > 0) {
+      const uint32_t kd = ring_u + stage_in * S::kStageBytes, vd = kd + kWarpKeys * D;
+      float* m = meta + stage_in * S::kMetaFloats;
+      const uint32_t mu = meta_u + stage_in * S::kMetaFloats * 4;
+      if constexpr (SEL) {
+        int page = -1, off = 0;
+        if (feed.key >= 0) {
+          page = __ldg(p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (feed.key >> p.cache.page_log2));
+          off = feed.key & (p.cache.page - 1);
+          if (page < 0 || page >= p.cache.num_pages) {
+            raise_status(p.status, kDevArg);
+            page = -2;
+          }
+        }
+        long long row = -1;
+        if (page >= 0) row = (static_cast<long long>(page) * p.cache.heads + pc.w.head) * p.cache.page + off;
+        if (lane < kWarpKeys) {
+          m[2 * kWarpKeys + lane] = feed.key >= 0 ? 1.f : 0.f;
+          if (page >= 0) {
+            const size_t blk = static_cast<size_t>(page) * p.cache.heads + pc.w.head;
+            cp_async4(mu + lane * 4, p.cache.k_scale + blk);
+            cp_async4(mu + (kWarpKeys + lane) * 4, p.cache.v_scale + blk);
+          } else {
+            m[lane] = page == -2 ? __int_as_float(0x7FC00000) : 1.f;
+            m[kWarpKeys + lane] = 1.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < CPR / 2; ++i) {
+          const int r = i * (32 / CPR) + lane / CPR, ch = lane % CPR;
+          const long long rr = __shfl_sync(0xFFFFFFFFu, row, r);
+          const size_t o = rr >= 0 ? static_cast<size_t>(rr) * D + ch * 16 : 0;
+          cp_async16(kd + place<D>(r, ch), p.cache.k_codes + o, rr >= 0);
+          cp_async16(vd + place<D>(r, ch), p.cache.v_codes + o, rr >= 0);
+        }
+      } else if (feed.live) {
+        const int tile = pc.t < pc.w.skip ? pc.t : pc.t - pc.w.skip + pc.w.tile0;
+        const int key0 = tile * kTileKeys + warp * kWarpKeys;
+        const bool known = feed.page >= 0 && feed.page < p.cache.num_pages;
+        if (!known) raise_status(p.status, kDevArg);
+        const size_t blk = known ? static_cast<size_t>(feed.page) * p.cache.heads + pc.w.head : 0;
+        if (lane == 0) {
+          if (known) {
+            cp_async4(mu, p.cache.k_scale + blk);
+            cp_async4(mu + 4, p.cache.v_scale + blk);
+          } else {
+            m[0] = __int_as_float(0x7FC00000);
+            m[1] = 1.f;
+          }
+        }
+        const size_t o = (blk * p.cache.page + (key0 & (p.cache.page - 1))) * D + lane * 16;
+#pragma unroll
+        for (int i = 0; i < CPR / 2; ++i) {
+          const int r = i * (32 / CPR) + lane / CPR, ch = lane % CPR;
+          const bool on = known && key0 + r < pc.w.len;
+          const size_t oo = on ? o + i * 512 : 0;
+          cp_async16(kd + place<D>(r, ch), p.cache.k_codes + oo, on);
+          cp_async16(vd + place<D>(r, ch), p.cache.v_codes + oo, on);
+        }
+      }
+      advance<SEL>(p, pc);
+      fetch();
+    }
+    cp_commit();
+    stage_in = stage_in + 1 == kStages ? 0 : stage_in + 1;
+  };
+  fetch();
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) produce();
+
+  // Dense: rows of sequences whose queries see no token have no tile on the line.
+  if constexpr (!SEL) {
+    for (long long n = blockIdx.x; n < p.batch.N; n += grid) {
+      const KvSeq s = kv_seq(p.batch, p.cache, kv_seq_of_query(p.batch, static_cast<int>(n)));
+      if (s.len > 0 && n >= s.q0 && n < s.q0 + s.nq) continue;
+      for (int i = tid; i < p.q_heads * D; i += kThreads) reinterpret_cast<uint16_t*>(p.out)[n * p.q_heads * D + i] = 0;
+      if (p.lse != nullptr)
+        for (int i = tid; i < p.q_heads; i += kThreads) p.lse[n * p.q_heads + i] = -__int_as_float(0x7F800000);
+    }
+  }
+
+  // --- consumer ---------------------------------------------------------------------------
+  uint32_t qf[KS][4];
+  float o[NT][4];
+  float M[2], l[2], crow[2];
+  int prow[2];                           // query position of rows g, g + 8
+  int stage_out = 0;
+
+#pragma unroll 1
+  while (head.left > 0) {
+    // a unit's piece: tiles [head.t, t_end)
+    const int t_begin = head.t;
+    const int t_end = static_cast<int>(min(static_cast<long long>(head.n_tiles), head.t + head.left));
+    const int rows_all = head.w.nq * p.group;
+#pragma unroll
+    for (int hlf = 0; hlf < 2; ++hlf) {
+      const int r = head.w.row0 + g + 8 * hlf;
+      const bool on = r < rows_all;
+      const int qi = r / p.group;
+      prow[hlf] = on ? (SEL ? head.w.pos0 : head.w.pos0 + qi) : -1;
+      uint4 raw[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+      if (on) {
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + (static_cast<size_t>(head.w.q0) + qi) * p.q_stride +
+                              static_cast<size_t>(head.w.head * p.group + r % p.group) * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)   // chunk cq of each 64 elements: 16 elements, 32 bytes
+          raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (i >> 1) * 64 + cq * 16) + (i & 1));
+      }
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t ws[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = kv_unpack16(ws[j], p.bf16);
+          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+      // the row's largest element goes to [2^8, 2^9)
+      int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8;
+      e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
+      const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      crow[hlf] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t ws[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = kv_unpack16(ws[j], p.bf16);
+          // words 2 i' and 2 i' + 1 of a chunk are k-step i' (bytes 0-1 and 2-3 of a code word)
+          const int word = i * 4 + j;
+          qf[word >> 1][hlf + 2 * (word & 1)] = kv_pack16(f.x * by, f.y * by, false);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    M[0] = M[1] = kMinusHuge;
+    l[0] = l[1] = 0.f;
+    const int p_lo = SEL ? 0 : head.w.pos0 + head.w.row0 / p.group;
+    const int p_hi = SEL ? 0 : head.w.pos0 + min(head.w.row0 + kRowsPerUnit - 1, rows_all - 1) / p.group;
+
+#pragma unroll 1
+    for (int t = t_begin; t < t_end; ++t) {
+      __syncwarp();                      // the stage that is filled next has been read by every lane
+      produce();
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const unsigned char* kp = ring + stage_out * S::kStageBytes;
+      const unsigned char* vp = kp + kWarpKeys * D;
+      const float* m = meta + stage_out * S::kMetaFloats;
+      stage_out = stage_out + 1 == kStages ? 0 : stage_out + 1;
+      const int tile = SEL ? t : (t < head.w.skip ? t : t - head.w.skip + head.w.tile0);
+      const int key0 = tile * kTileKeys + warp * kWarpKeys;
+      if (!SEL && (key0 >= head.w.len || key0 > p_hi)) continue;
+
+      float s[2][4] = {};
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half) {
+        const uint4 a = *reinterpret_cast<const uint4*>(kp + place<D>(g, half * 4 + cq));
+        const uint4 b = *reinterpret_cast<const uint4*>(kp + place<D>(g + 8, half * 4 + cq));
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mma_f16(s[0], qf[half * 4 + i], e4m3x2_to_f16x2(aw[i] & 0xFFFFu), e4m3x2_to_f16x2(aw[i] >> 16));
+          mma_f16(s[1], qf[half * 4 + i], e4m3x2_to_f16x2(bw[i] & 0xFFFFu), e4m3x2_to_f16x2(bw[i] >> 16));
+        }
+      }
+      // element e of s[n]: row g + 8 (e >> 1), key 2 cq + (e & 1) + 8 n
+      float ks[4], lv[4], iv[4];
+      bool valid[4];
+      if constexpr (SEL) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float2 a = *reinterpret_cast<const float2*>(m + 8 * n + 2 * cq);
+          const float2 b = *reinterpret_cast<const float2*>(m + kWarpKeys + 8 * n + 2 * cq);
+          const float2 z = *reinterpret_cast<const float2*>(m + 2 * kWarpKeys + 8 * n + 2 * cq);
+          ks[2 * n] = a.x;
+          ks[2 * n + 1] = a.y;
+          lv[2 * n] = __log2f(b.x) + kBoost;
+          lv[2 * n + 1] = __log2f(b.y) + kBoost;
+          iv[2 * n] = __frcp_rn(b.x);
+          iv[2 * n + 1] = __frcp_rn(b.y);
+          valid[2 * n] = z.x != 0.f;
+          valid[2 * n + 1] = z.y != 0.f;
+        }
+      } else {
+        const float2 sc = *reinterpret_cast<const float2*>(m);
+        const float lg = __log2f(sc.y) + kBoost, inv = __frcp_rn(sc.y);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ks[i] = sc.x;
+          lv[i] = lg;
+          iv[i] = inv;
+          valid[i] = true;
+        }
+      }
+      const bool inside = !SEL && key0 + kWarpKeys - 1 <= p_lo &&
+                          (p.window <= 0 || key0 > p_hi - p.window || key0 + kWarpKeys <= p.sinks);
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int hlf = e >> 1, kk = 2 * n + (e & 1);
+          float x = fmaf(s[n][e] * ks[kk], crow[hlf], lv[kk]);
+          if constexpr (SEL) {
+            if (!valid[kk]) x = -__int_as_float(0x7F800000);
+          } else if (!inside) {
+            const int key = key0 + 8 * n + 2 * cq + (e & 1);
+            const bool seen = key <= prow[hlf] && (p.window <= 0 || key > prow[hlf] - p.window || key < p.sinks);
+            if (!seen) x = -__int_as_float(0x7F800000);
+          }
+          s[n][e] = x;
+          over = over || x > M[hlf] + (kSlack + kBoost);
+        }
+      if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+        for (int hlf = 0; hlf < 2; ++hlf) {
+          float mx = fmaxf(fmaxf(s[0][2 * hlf], s[0][2 * hlf + 1]), fmaxf(s[1][2 * hlf], s[1][2 * hlf + 1])) - kBoost;
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+          const float next = fmaxf(M[hlf], mx);
+          const float by = exp2_approx(M[hlf] - next);
+          M[hlf] = next;
+          l[hlf] *= by;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            o[i][2 * hlf] *= by;
+            o[i][2 * hlf + 1] *= by;
+          }
+        }
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int hlf = 0; hlf < 2; ++hlf) {
+          const float w0 = exp2_approx(s[n][2 * hlf] - M[hlf]), w1 = exp2_approx(s[n][2 * hlf + 1] - M[hlf]);
+          l[hlf] = fmaf(w0, iv[2 * n], fmaf(w1, iv[2 * n + 1], l[hlf]));
+          pf[hlf + 2 * n] = kv_pack16(w0, w1, false);
+        }
+      // values: this lane's keys 2 cq, 2 cq + 1 (and + 8), its g-th D / 8 elements
+      uint32_t vw[4][D / 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * cq + (i & 1) + 8 * (i >> 1);
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vp + place<D>(r, g));
+          vw[i][0] = x.x;
+          vw[i][1] = x.y;
+          vw[i][2] = x.z;
+          vw[i][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(vp + place<D>(r, g >> 1) + (g & 1) * 8);
+          vw[i][0] = x.x;
+          vw[i][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        const uint32_t x[4] = {vw[0][w], vw[1][w], vw[2][w], vw[3][w]};
+        const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), a23 = __byte_perm(x[0], x[1], 0x7362);
+        const uint32_t b01 = __byte_perm(x[2], x[3], 0x5140), b23 = __byte_perm(x[2], x[3], 0x7362);
+        mma_f16(o[w * 4], pf, e4m3x2_to_f16x2(a01 & 0xFFFFu), e4m3x2_to_f16x2(b01 & 0xFFFFu));
+        mma_f16(o[w * 4 + 1], pf, e4m3x2_to_f16x2(a01 >> 16), e4m3x2_to_f16x2(b01 >> 16));
+        mma_f16(o[w * 4 + 2], pf, e4m3x2_to_f16x2(a23 & 0xFFFFu), e4m3x2_to_f16x2(b23 & 0xFFFFu));
+        mma_f16(o[w * 4 + 3], pf, e4m3x2_to_f16x2(a23 >> 16), e4m3x2_to_f16x2(b23 >> 16));
+      }
+    }
+
+    // --- the piece's end: warps of the CTA, then CTAs of the unit -------------------------
+#pragma unroll
+    for (int hlf = 0; hlf < 2; ++hlf) {
+      l[hlf] += __shfl_xor_sync(0xFFFFFFFFu, l[hlf], 1);
+      l[hlf] += __shfl_xor_sync(0xFFFFFFFFu, l[hlf], 2);
+      const int r = g + 8 * hlf;
+      if (cq == 0) {
+        merge_ml[(warp * kRowsPerUnit + r) * 2] = M[hlf];
+        merge_ml[(warp * kRowsPerUnit + r) * 2 + 1] = l[hlf];
+      }
+      // element e of n-tile nt is column (2 cq + e) * NT + nt
+      float* dst = merge_o + (warp * kRowsPerUnit + r) * D;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int nt = 0; nt < NT; nt += 4) {
+          const int chunk = ((2 * cq + e) * NT + nt) >> 2;
+          const int at = chunk ^ (((chunk >> 3) & 3) | ((r & 1) << 2));
+          *reinterpret_cast<float4*>(dst + at * 4) =
+              make_float4(o[nt][2 * hlf + e], o[nt + 1][2 * hlf + e], o[nt + 2][2 * hlf + e], o[nt + 3][2 * hlf + e]);
+        }
+    }
+    __syncthreads();
+    const int rows = min(rows_all - head.w.row0, kRowsPerUnit);
+    const bool whole = t_begin == 0 && t_end == head.n_tiles;
+    // Contributors of this unit and its place in the workspace.
+    const long long u0 = head.at - t_begin, u1 = u0 + head.n_tiles;       // the unit on the line
+    const int c0 = static_cast<int>(((u0 + 1) * n_cta - 1) / total), c1 = static_cast<int>((u1 * n_cta - 1) / total);
+    constexpr int kSlot = kRowsPerUnit * (D + 2);
+    float* mine = p.part + static_cast<size_t>(2 * blockIdx.x + (t_begin == 0 ? 1 : 0)) * kSlot;
+    auto write_row = [&](int r, int ch, float4 v, float m2, float sum) {
+      const int row = head.w.row0 + r;
+      const size_t at = (static_cast<size_t>(head.w.q0) + row / p.group) * p.q_heads + head.w.head * p.group + row % p.group;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint2 w;
+      w.x = kv_pack16(v.x * inv, v.y * inv, p.bf16);
+      w.y = kv_pack16(v.z * inv, v.w * inv, p.bf16);
+      reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at * D)[ch] = w;
+      if (ch == 0 && p.lse != nullptr)
+        p.lse[at] = sum == 0.f ? -__int_as_float(0x7F800000) : (m2 - kBoost + log2f(sum)) * 0.69314718055994530942f;
+    };
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), ch = i % (D / 4);
+      float mx = kMinusHuge;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, merge_ml[(w * kRowsPerUnit + r) * 2]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float by = exp2_approx(merge_ml[(w * kRowsPerUnit + r) * 2] - mx);
+        sum = fmaf(merge_ml[(w * kRowsPerUnit + r) * 2 + 1], by, sum);
+        const int at = ch ^ (((ch >> 3) & 3) | ((r & 1) << 2));
+        const float4 v = *reinterpret_cast<const float4*>(merge_o + (w * kRowsPerUnit + r) * D + at * 4);
+        acc.x = fmaf(v.x, by, acc.x);
+        acc.y = fmaf(v.y, by, acc.y);
+        acc.z = fmaf(v.z, by, acc.z);
+        acc.w = fmaf(v.w, by, acc.w);
+      }
+      if (whole) {
+        write_row(r, ch, acc, mx, sum);
+      } else {
+        __stcg(reinterpret_cast<float4*>(mine + kRowsPerUnit * 2 + r * D) + ch, acc);
+        if (ch == 0) __stcg(reinterpret_cast<float2*>(mine) + r, make_float2(mx, sum));
+      }
+    }
+    if (!whole) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) sh_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
+      __syncthreads();
+      if (sh_last) {
+        __threadfence();
+        for (int i = tid; i < rows * (D / 4); i += kThreads) {
+          const int r = i / (D / 4), ch = i % (D / 4);
+          float mx = kMinusHuge, sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int cta = c0; cta <= c1; ++cta) {
+            const float* src = p.part + static_cast<size_t>(2 * cta + (cta == c0 ? 1 : 0)) * kSlot;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(src) + r);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + kRowsPerUnit * 2 + r * D) + ch);
+            const float next = fmaxf(mx, ml.x);
+            const float a = exp2_approx(mx - next), b = exp2_approx(ml.x - next);
+            mx = next;
+            sum = sum * a + ml.y * b;
+            acc.x = acc.x * a + v.x * b;
+            acc.y = acc.y * a + v.y * b;
+            acc.z = acc.z * a + v.z * b;
+            acc.w = acc.w * a + v.w * b;
+          }
+          write_row(r, ch, acc, mx, sum);
+        }
+        if (tid == 0) p.counters[c0] = 0;
+      }
+    }
+    __syncthreads();
+    // to the next unit
+    const int n = t_end - t_begin;
+    head.at += n - 1;
+    head.left -= n - 1;
+    head.t = t_end - 1;
+    advance<SEL>(p, head);
+  }
+  cp_wait<0>();
+}
+
+template <int D, bool SEL>
+const void* rows_fn() {
+  return reinterpret_cast<const void*>(kv_rows_kernel<D, SEL>);
+}
+
+}  // namespace
+
+size_t kv_rows_part_floats(int num_sms) { return static_cast<size_t>(2) * num_sms * kRowsPerUnit * (128 + 2); }
+int kv_rows_counters(int num_sms) { return num_sms; }
+
+cudaError_t kv_rows_init() {
+  const void* fns[4] = {rows_fn<128, false>(), rows_fn<128, true>(), rows_fn<64, false>(), rows_fn<64, true>()};
+  for (int i = 0; i < 4; ++i) {
+    const cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               i < 2 ? RowsSmem<128>::kBytes : RowsSmem<64>::kBytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_kv_rows(const AttnParams& p, int num_sms, cudaStream_t stream) {
+  const bool sel = p.idx != nullptr;
+  if (p.dim == 128) {
+    if (sel) kv_rows_kernel<128, true><<<num_sms, kThreads, RowsSmem<128>::kBytes, stream>>>(p, num_sms);
+    else kv_rows_kernel<128, false><<<num_sms, kThreads, RowsSmem<128>::kBytes, stream>>>(p, num_sms);
+  } else {
+    if (sel) kv_rows_kernel<64, true><<<num_sms, kThreads, RowsSmem<64>::kBytes, stream>>>(p, num_sms);
+    else kv_rows_kernel<64, false><<<num_sms, kThreads, RowsSmem<64>::kBytes, stream>>>(p, num_sms);
+  }
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace ltk

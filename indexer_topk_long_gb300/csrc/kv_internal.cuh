@@ -1,0 +1,156 @@
+// kv_internal.cuh -- paged 8-bit key/value cache: layout, batch description and
+// device helpers shared by the append and attention kernels.
+//
+// Cache of one layer: codes [num_pages, heads, page, dim] (e4m3), one fp32 scale
+// for each (page, head); a held value is code * scale.  The pages of sequence b
+// are page_table[b, 0..]; its token at position p lies in page
+// page_table[b, p / page], row p % page.  Offsets into the cache are 64-bit.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "ltk_internal.cuh"
+
+namespace ltk {
+
+// Range of a block's scale exponent: scale = 2^e, kKvMinExp <= e <= kKvMaxExp.
+// Within it the ratio of two blocks' scales stays far inside fp32 (see the
+// attention kernels, which fold log2(v_scale) into the exponent of a weight).
+constexpr int kKvMinExp = -40;
+constexpr int kKvMaxExp = 40;
+constexpr int kDevArg = 1;               // device status: an index outside its table
+
+struct KvCache {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scale;
+  float* v_scale;
+  long long num_pages;
+  int heads;                             // KV heads
+  int page;                              // tokens per page: 16, 32, 64 or 128
+  int page_log2;
+};
+
+struct KvBatch {
+  const int* page_table;                 // [B, width]
+  const int* seq_lens;                   // [B] cached tokens, this step's among them
+  const int* cu_q;                       // [B + 1] first query (token) of each sequence
+  int width;
+  int B;
+  int N;
+};
+
+// Queries [q0, q0 + nq) of sequence b, its length and the position of its
+// first query.  Values outside the tables' bounds are clamped to them.
+struct KvSeq {
+  int q0, nq, len, pos0;
+};
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int b) {
+  KvSeq s;
+  s.q0 = min(max(__ldg(bt.cu_q + b), 0), bt.N);
+  s.nq = min(max(__ldg(bt.cu_q + b + 1), s.q0), bt.N) - s.q0;
+  const long long room = static_cast<long long>(bt.width) << c.page_log2;
+  s.len = static_cast<int>(min(static_cast<long long>(max(__ldg(bt.seq_lens + b), 0)), room));
+  s.pos0 = s.len - s.nq;                 // negative when a sequence is shorter than its queries
+  return s;
+}
+
+// Sequence of query n: the last b with cu_q[b] <= n.
+__device__ __forceinline__ int kv_seq_of_query(const KvBatch& bt, int n) {
+  int lo = 0, hi = bt.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(bt.cu_q + mid) <= n) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Codes (byte offset) of row `off` of (page, head).
+__device__ __forceinline__ size_t kv_row(const KvCache& c, long long page, int head, int off, int dim) {
+  return ((static_cast<size_t>(page) * c.heads + head) * c.page + off) * dim;
+}
+
+// Two e4m3 codes to two f16 values (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two_codes));
+  return r;
+}
+
+// 2^x, one MUFU instruction (2 ulp); 0 for -inf and for results below fp32's normal range.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float kv_load16(const void* p, size_t i, bool bf16) {
+  return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
+              : __half2float(reinterpret_cast<const __half*>(p)[i]);
+}
+// Two packed 16-bit values to fp32.
+__device__ __forceinline__ float2 kv_unpack16(uint32_t w, bool bf16) {
+  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ uint32_t kv_pack16(float lo, float hi, bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+struct AppendParams {
+  KvCache cache;
+  KvBatch batch;
+  int dim;
+  int bf16;                              // else f16
+  const void* k;                         // [N, heads, dim], rows k_stride elements apart
+  const void* v;
+  long long k_stride, v_stride;
+  const float* cos;                      // [table_rows, rot / 2], null: no rotation
+  const float* sin;
+  int rot;
+  int table_rows;
+  int interleaved;
+  const void* q;                         // [N, q_heads, dim] or null
+  long long q_stride;
+  int q_heads;
+  void* q_out;                           // [N, q_heads, dim] contiguous
+  int* status;
+};
+cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream);
+
+struct AttnParams {
+  KvCache cache;
+  KvBatch batch;
+  int dim;
+  int bf16;
+  const void* q;                         // [N, q_heads, dim], rows q_stride elements apart
+  long long q_stride;
+  int q_heads;
+  int group;                             // q_heads / cache.heads
+  float scale_log2;                      // softmax scale * log2(e)
+  int window;                            // 0: none
+  int sinks;
+  const int* idx;                        // [N, k] selected positions, or null (dense)
+  int k;
+  void* out;                             // [N, q_heads, dim]
+  float* lse;                            // [N, q_heads] or null
+  float* part;                           // workspace: partial results
+  int* counters;                         // workspace: zero between calls
+  int* status;
+};
+
+// Attention for few rows per KV head (k_kv_rows.cu).
+constexpr int kRowsPerUnit = 16;
+size_t kv_rows_part_floats(int num_sms);   // workspace floats
+int kv_rows_counters(int num_sms);
+cudaError_t kv_rows_init();                // kernel attributes on the current device
+cudaError_t launch_kv_rows(const AttnParams& p, int num_sms, cudaStream_t stream);
+
+}  // namespace ltk

@@ -1,0 +1,250 @@
+"""Paged key/value cache held in 8 bits and the attention that reads it: binding
+over the ``ltk_kv_*`` entry points (argument checks and marshalling only).
+
+    cache = PagedKVCache(num_pages, heads, dim, page=64)
+    q = cache.append(k, v, page_table, seq_lens, cu_q, cos, sin, q=q)      # rotate, quantise, store
+    out, lse = cache.attention(q, page_table, seq_lens, cu_q)              # causal, optional window
+    out, lse = cache.attention_selected(q, idx, page_table, seq_lens, cu_q)  # the indexer's keys
+
+The batch is three int32 CUDA tensors: ``page_table`` [B, width], ``seq_lens``
+[B] (cached tokens, this step's among them) and ``cu_q`` [B + 1] (first new
+token of each sequence).  Nothing is copied to the host.  Calls on one cache
+share its workspace: issue them on one stream, or synchronise between streams.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from . import ltk
+from .ltk import KvBatch, KvConfig, LTK_BF16, LTK_F16
+
+DTYPES = {"torch.bfloat16": LTK_BF16, "torch.float16": LTK_F16}
+
+
+def _fail(name: str, what: str):
+    raise ValueError(f"{name}: {what}")
+
+
+def _device_ok(t, name: str, device) -> None:
+    if t.device != device:
+        _fail(name, f"expected a tensor on {device}, got one on {t.device}")
+
+
+def _ints(t, name: str, shape, device) -> None:
+    import torch
+    if t.dtype != torch.int32:
+        _fail(name, f"expected int32 elements, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        _fail(name, f"expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        _fail(name, "must be contiguous")
+    _device_ok(t, name, device)
+
+
+def _rows(t, name: str, n: int, dim: int, device, dtype=None) -> tuple[int, int]:
+    """[n, heads, dim] of 16-bit elements, each token's heads contiguous and tokens
+    a multiple of 8 elements apart; returns (heads, token stride)."""
+    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != dim:
+        _fail(name, f"expected shape ({n}, heads, {dim}), got {tuple(t.shape)}")
+    if str(t.dtype) not in DTYPES:
+        _fail(name, f"expected bfloat16 or float16 elements, got {t.dtype}")
+    if dtype is not None and t.dtype != dtype:
+        _fail(name, f"expected {dtype} elements like the others, got {t.dtype}")
+    _device_ok(t, name, device)
+    heads = t.shape[1]
+    if heads < 1:
+        _fail(name, "has no heads")
+    stride = t.stride(0) if n > 1 else heads * dim
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        _fail(name, "each token's heads must be contiguous")
+    if stride % 8 or stride < heads * dim or t.data_ptr() % 16:
+        _fail(name, "tokens must start on 16-byte boundaries and not overlap")
+    return heads, stride
+
+
+def check_batch(page_table, seq_lens, cu_q, n: int, device) -> KvBatch:
+    if page_table.dim() != 2:
+        _fail("page_table", f"expected a 2-D tensor, got shape {tuple(page_table.shape)}")
+    b, width = page_table.shape
+    _ints(page_table, "page_table", (b, width), device)
+    _ints(seq_lens, "seq_lens", (b,), device)
+    _ints(cu_q, "cu_q", (b + 1,), device)
+    return KvBatch(page_table.data_ptr(), width, seq_lens.data_ptr(), cu_q.data_ptr(), b, n)
+
+
+class PagedKVCache:
+    """One layer's cache and its ``ltk_kv`` handle on the current device.
+
+    Without the four buffers the cache is allocated, zeroed.  ``k_codes`` and
+    ``v_codes`` are uint8 (or float8_e4m3fn) [num_pages, heads, page, dim],
+    ``k_scale`` and ``v_scale`` fp32 [num_pages, heads]."""
+
+    def __init__(self, num_pages: int, heads: int, dim: int, page: int = 64, k_codes=None, v_codes=None,
+                 k_scale=None, v_scale=None):
+        import torch
+        self.h = None
+        self.lib = ltk.load_library()
+        self.num_pages, self.heads, self.dim, self.page = int(num_pages), int(heads), int(dim), int(page)
+        given = [t is not None for t in (k_codes, v_codes, k_scale, v_scale)]
+        if any(given) and not all(given):
+            raise ValueError("k_codes, v_codes, k_scale, v_scale: give all four or none")
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        codes, scales = (self.num_pages, self.heads, self.page, self.dim), (self.num_pages, self.heads)
+        if not all(given):
+            k_codes, v_codes = (torch.zeros(codes, dtype=torch.uint8, device=self.device) for _ in range(2))
+            k_scale, v_scale = (torch.zeros(scales, dtype=torch.float32, device=self.device) for _ in range(2))
+        for t, name, shape, size in ((k_codes, "k_codes", codes, 1), (v_codes, "v_codes", codes, 1),
+                                     (k_scale, "k_scale", scales, 4), (v_scale, "v_scale", scales, 4)):
+            if tuple(t.shape) != shape:
+                _fail(name, f"expected shape {shape}, got {tuple(t.shape)}")
+            if size == 4 and t.dtype != torch.float32:
+                _fail(name, f"expected float32 elements, got {t.dtype}")
+            if size == 1 and t.dtype not in (torch.uint8, torch.float8_e4m3fn):
+                _fail(name, f"expected uint8 or float8_e4m3fn elements, got {t.dtype}")
+            if not t.is_contiguous():
+                _fail(name, "must be contiguous")
+            _device_ok(t, name, self.device)
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        cfg = KvConfig(self.num_pages, self.heads, self.dim, self.page, k_codes.data_ptr(), v_codes.data_ptr(),
+                       k_scale.data_ptr(), v_scale.data_ptr())
+        # the handle's workspace must not be set up before the buffers' own stream has made them
+        torch.cuda.current_stream().synchronize()
+        h = ctypes.c_void_p()
+        ltk._check(self.lib.ltk_kv_create(ctypes.byref(cfg), ctypes.byref(h)), "ltk_kv_create")
+        self.h = h
+
+    # -- helpers ---------------------------------------------------------------
+    def _begin(self, stream, tensors):
+        """The stream to launch on, and a context in which outputs belong to it.
+        Tensors of the caller's are kept from reuse until the call on another
+        stream is done."""
+        import contextlib
+
+        import torch
+        if self.h is None:
+            raise ValueError("the cache is closed")
+        cur = torch.cuda.current_stream(self.device)
+        if stream is None or stream == cur:
+            return cur, contextlib.nullcontext()
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return stream, torch.cuda.stream(stream)
+
+    def _outputs(self, q, out, lse):
+        import torch
+        n, heads, dim = q.shape
+        if out is None:
+            out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
+        elif tuple(out.shape) != (n, heads, dim) or out.dtype != q.dtype or not out.is_contiguous() \
+                or out.device != q.device:
+            _fail("out", f"expected a contiguous {q.dtype} tensor of shape {(n, heads, dim)} on {q.device}")
+        if lse is None:
+            lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
+        elif tuple(lse.shape) != (n, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() \
+                or lse.device != q.device:
+            _fail("lse", f"expected a contiguous float32 tensor of shape {(n, heads)} on {q.device}")
+        return out, lse
+
+    def _scale(self, scale) -> float:
+        return 1.0 / math.sqrt(self.dim) if scale is None else float(scale)
+
+    # -- API -------------------------------------------------------------------
+    def append(self, k, v, page_table, seq_lens, cu_q, cos=None, sin=None, interleaved: bool = False, q=None,
+               q_out=None, stream=None):
+        """Stores the new tokens' k, v [N, heads, dim]; keys and q are rotated by the rows
+        of cos, sin [positions, rot / 2] when given.  Returns the rotated q (None without q)."""
+        import torch
+        n = int(k.shape[0])
+        batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
+        kh, ks = _rows(k, "k", n, self.dim, self.device)
+        vh, vs = _rows(v, "v", n, self.dim, self.device, k.dtype)
+        if kh != self.heads or vh != self.heads:
+            _fail("k" if kh != self.heads else "v", f"expected {self.heads} heads")
+        rot = rows = 0
+        if (cos is None) != (sin is None):
+            raise ValueError("cos, sin: give both or neither")
+        if cos is not None:
+            for t, name in ((cos, "cos"), (sin, "sin")):
+                if t.dim() != 2 or t.shape != cos.shape or t.dtype != torch.float32 or not t.is_contiguous():
+                    _fail(name, "expected contiguous float32 tables of equal shape [positions, rot / 2]")
+                _device_ok(t, name, self.device)
+            rows, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
+        qh = qs = 0
+        if q is not None:
+            qh, qs = _rows(q, "q", n, self.dim, self.device, k.dtype)
+        st, within = self._begin(stream, (k, v, page_table, seq_lens, cu_q, cos, sin, q, q_out, self.k_codes,
+                                          self.v_codes, self.k_scale, self.v_scale))
+        with within:
+            if q is not None and q_out is None:
+                q_out = torch.empty((n, qh, self.dim), dtype=q.dtype, device=q.device)
+            if q_out is not None:
+                if q is None:
+                    raise ValueError("q_out: given without q")
+                if tuple(q_out.shape) != (n, qh, self.dim) or q_out.dtype != q.dtype or not q_out.is_contiguous() \
+                        or q_out.device != q.device:
+                    _fail("q_out", f"expected a contiguous {q.dtype} tensor of shape {(n, qh, self.dim)}")
+            ltk._check(self.lib.ltk_kv_append(
+                self.h, ctypes.byref(batch), DTYPES[str(k.dtype)], k.data_ptr(), ks, v.data_ptr(), vs,
+                ltk._ptr(cos), ltk._ptr(sin), rows, rot, 1 if interleaved else 0, ltk._ptr(q), qs, qh,
+                ltk._ptr(q_out), st.cuda_stream), "ltk_kv_append")
+        return q_out
+
+    def attention(self, q, page_table, seq_lens, cu_q, max_q: int | None = None, scale: float | None = None,
+                  window: int = 0, sinks: int = 0, out=None, lse=None, stream=None):
+        """Causal attention of q [N, q_heads, dim] over the cached tokens; with ``window`` > 0 a
+        query at p sees keys j > p - window and the first ``sinks`` keys.  ``max_q`` (the most
+        queries of one sequence) only helps choose a kernel.  Returns (out, lse)."""
+        n = int(q.shape[0])
+        batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
+        heads, qs = _rows(q, "q", n, self.dim, self.device)
+        if max_q is None:
+            max_q = -(-n // max(batch.B, 1))
+        st, within = self._begin(stream, (q, page_table, seq_lens, cu_q, out, lse, self.k_codes, self.v_codes,
+                                          self.k_scale, self.v_scale))
+        with within:
+            out, lse = self._outputs(q, out, lse)
+            ltk._check(self.lib.ltk_kv_attention(
+                self.h, ctypes.byref(batch), DTYPES[str(q.dtype)], q.data_ptr(), qs, heads, int(max_q),
+                self._scale(scale), int(window), int(sinks), out.data_ptr(), lse.data_ptr(), st.cuda_stream),
+                "ltk_kv_attention")
+        return out, lse
+
+    def attention_selected(self, q, idx, page_table, seq_lens, cu_q, scale: float | None = None, out=None,
+                           lse=None, stream=None):
+        """Attention of each query over its own key positions idx [N, k] (int32, -1 = empty
+        slot), e.g. the indices IndexerTopK returns.  Returns (out, lse)."""
+        n = int(q.shape[0])
+        batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
+        heads, qs = _rows(q, "q", n, self.dim, self.device)
+        if idx.dim() != 2:
+            _fail("idx", f"expected a 2-D [queries, k] tensor, got shape {tuple(idx.shape)}")
+        _ints(idx, "idx", (n, idx.shape[1]), self.device)
+        st, within = self._begin(stream, (q, idx, page_table, seq_lens, cu_q, out, lse, self.k_codes, self.v_codes,
+                                          self.k_scale, self.v_scale))
+        with within:
+            out, lse = self._outputs(q, out, lse)
+            ltk._check(self.lib.ltk_kv_attention_selected(
+                self.h, ctypes.byref(batch), DTYPES[str(q.dtype)], q.data_ptr(), qs, heads, idx.data_ptr(),
+                int(idx.shape[1]), self._scale(scale), out.data_ptr(), lse.data_ptr(), st.cuda_stream),
+                "ltk_kv_attention_selected")
+        return out, lse
+
+    def status(self, stream=None) -> int:
+        """First error the device raised since the last call (0: none); synchronises the stream."""
+        st, _ = self._begin(stream, ())
+        value = ctypes.c_int(0)
+        ltk._check(self.lib.ltk_kv_status(self.h, ctypes.byref(value), st.cuda_stream), "ltk_kv_status")
+        return value.value
+
+    def close(self) -> None:
+        if getattr(self, "h", None):
+            self.lib.ltk_kv_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

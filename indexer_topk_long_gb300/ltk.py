@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 HEADER = os.path.join(ROOT, "include", "ltk.h")
 
-LTK_BF16, LTK_FP8_E4M3 = 0, 1
+LTK_BF16, LTK_FP8_E4M3, LTK_F16 = 0, 1, 2
 STATUS = {0: "LTK_OK", 1: "LTK_ERR_ARG", 2: "LTK_ERR_CUDA", 3: "LTK_ERR_NOMEM",
           4: "LTK_ERR_OVERFLOW", 5: "LTK_ERR_TIMEOUT", 6: "LTK_ERR_UNSUPPORTED"}
 
@@ -50,8 +50,21 @@ class Stats(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class KvConfig(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_longlong), ("heads", ctypes.c_int), ("dim", ctypes.c_int),
+                ("page", ctypes.c_int), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_width", ctypes.c_int),
+                ("seq_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("B", ctypes.c_int),
+                ("N", ctypes.c_int)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _LL = ctypes.c_longlong
 _SIGS = {
     "ltk_abi_version": (_I, []),
@@ -69,6 +82,14 @@ _SIGS = {
     "ltk_get_stats": (_I, [_P, ctypes.POINTER(Stats)]),
     "ltk_decoupled_topk_noalloc": (_I, [_I, _I, _P, _P, _P, _P, _P, _P, _I, _LL, _I, _P, _P, _P, _P]),
     "ltk_litedsa_pack": (_I, [_P, _I, _I, _I, _P, _P, _P, _P]),
+    "ltk_kv_create": (_I, [ctypes.POINTER(KvConfig), ctypes.POINTER(_P)]),
+    "ltk_kv_destroy": (None, [_P]),
+    "ltk_kv_append": (_I, [_P, ctypes.POINTER(KvBatch), _I, _P, _LL, _P, _LL, _P, _P, _I, _I, _I, _P, _LL,
+                           _I, _P, _P]),
+    "ltk_kv_attention": (_I, [_P, ctypes.POINTER(KvBatch), _I, _P, _LL, _I, _I, _F, _I, _I, _P, _P, _P]),
+    "ltk_kv_attention_selected": (_I, [_P, ctypes.POINTER(KvBatch), _I, _P, _LL, _I, _P, _I, _F, _P, _P,
+                                       _P]),
+    "ltk_kv_status": (_I, [_P, ctypes.POINTER(_I), _P]),
 }
 
 _LIB = None
