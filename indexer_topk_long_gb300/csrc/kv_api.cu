@@ -1,5 +1,6 @@
 // kv_api.cu -- C ABI of the paged 8-bit key/value cache: validation on the host,
 // the handle with its workspace, and the launches of append and attention.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -80,13 +81,15 @@ ltk_status ltk_kv_create(const ltk_kv_config* cfg, ltk_kv** out) {
   h->dim = cfg->dim;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
+  const size_t part_floats = std::max(kv_rows_part_floats(h->num_sms), kv_tile_part_floats(h->num_sms));
   const size_t counters = static_cast<size_t>(kv_rows_counters(h->num_sms)) * 4;
-  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part), kv_rows_part_floats(h->num_sms) * 4);
+  if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part), part_floats * 4);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->counters), counters);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->status), 4);
   if (e == cudaSuccess) e = cudaMemset(h->counters, 0, counters);
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, 4);
   if (e == cudaSuccess) e = kv_rows_init();
+  if (e == cudaSuccess) e = kv_tile_init();
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the workspace is zero for calls on any stream
   if (e != cudaSuccess) {
     const ltk_status s = kv_cuda_fail(e, "ltk_kv_create");
@@ -182,7 +185,11 @@ static ltk_status kv_attend(ltk_kv* h, const ltk_kv_batch* batch, int dtype, con
   p.part = h->part;
   p.counters = h->counters;
   p.status = h->status;
-  return kv_cuda_fail(launch_kv_rows(p, h->num_sms, static_cast<cudaStream_t>(stream)), "kv attention");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const long long rows = static_cast<long long>(p.group) * (idx != nullptr ? 1 : max_q > 0 ? max_q : batch->N);
+  const cudaError_t e = rows <= kRowsPerUnit ? launch_kv_rows(p, h->num_sms, st)
+                                             : launch_kv_tile(p, max_q > 0 ? max_q : batch->N, h->num_sms, st);
+  return kv_cuda_fail(e, "kv attention");
 }
 
 ltk_status ltk_kv_attention(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q, long long q_stride,
