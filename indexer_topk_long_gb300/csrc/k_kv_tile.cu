@@ -19,7 +19,10 @@
 //               holds them twice, so the streams' threads sit on different schedulers.
 // Roles: warps 0-3 and 4-7 softmax, 8-11 loader (codes from global memory through
 // registers, e4m3 to f16, 128-byte-swizzled shared memory; a listed key is as good
-// as a paged one), warp 12 issues the MMAs.
+// as a paged one), warp 12 issues the MMAs, warp 13 walks the CTA's work, warps 14
+// and 15 bring the queries.
+// Work: all units' key tiles form one line, cut into equal pieces, one per CTA; a
+// unit cut by a border is merged by the last of its CTAs in a fixed order.
 #include "kv_internal.cuh"
 
 namespace ltk {
@@ -27,13 +30,16 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;
+// Registers a thread: 128 at launch, moved from the last warpgroup to the others.
+constexpr int kRegsMain = 136, kRegsRest = 104;
+static_assert(3 * kRegsMain + kRegsRest == 4 * 128, "register split");
 constexpr float kMinusHuge = -1e30f;
 constexpr float kBoost = 8.f;            // as in the kernel for few rows
 constexpr float kSlack = 7.f;
 
-struct Unit {                            // one work item, written by the loader
-  int n_tiles;                           // key tiles; -1: no more items
+struct Unit {                            // a piece of a work unit
+  int n_tiles;                           // key tiles; -1: no more pieces
   int first;                             // ordinal of the first of them
   int rows;                              // live rows
   int row0;                              // first row: row r is query q0 + r / group, head r % group
@@ -42,7 +48,10 @@ struct Unit {                            // one work item, written by the loader
   int p_lo, p_hi;                        // smallest and largest position of the rows
   int head;
   int skip, tile0;                       // ordinals below skip are the sinks' tiles, the rest start at tile0
-  int item;
+  int b;                                 // sequence
+  int len;                               // cached tokens (listed: list length)
+  int part;                              // -1: the whole unit; else its place in the workspace
+  int c0, c1;                            // CTAs that hold the unit's pieces
 };
 
 struct Meta {                            // scales of a key tile's eight 16-key groups
@@ -54,14 +63,17 @@ struct Meta {                            // scales of a key tile's eight 16-key 
 
 struct Ctrl {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2];
-  uint64_t ufull[2], uempty[2], qempty, mfull, mempty, drained;
+  uint64_t ufull[2], uempty[2], qfull[2], qempty, mfull, mempty, drained, wg[2];
   uint32_t tmem;
   int abort_flag;
+  int last[2];
   Unit unit[2];
   Meta meta[4];
   // score factor of each row by unit slot: pair mode [2][256]; solo mode [2][128], then
   // stream 1's (M, l) [128][2]
   float rowf[512];
+  long long at, left;                    // the CTA's piece of the line
+  int slot, head, t;                     // where it begins
 };
 
 template <int D>
@@ -152,70 +164,70 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
 struct TileParams {
   AttnParams a;
   int pair;                              // 1: pair mode
-  int n_split;                           // pieces of each unit's key tiles
   int row_tiles;                         // listed keys: row tiles of a group
-  long long items;
+  int slots;                             // row tiles over all sequences (an upper bound when dense)
 };
 
 __device__ __forceinline__ int unit_rows(const TileParams& p) { return p.pair ? 2 * kTileRows : kTileRows; }
 
-// Dense units are numbered without a scan: sequence b's start at
+// Dense row tiles are numbered without a scan: sequence b's start at
 // cu_q[b] * group / rows + b, which leaves room for every row tile.
 __device__ __forceinline__ long long slot_start(const TileParams& p, int b) {
   return static_cast<long long>(__ldg(p.a.batch.cu_q + b)) * p.a.group / unit_rows(p) + b;
 }
 
-// Work item to unit; false: nothing there.
+// Row tile `slot`: its fields, and the number of its key tiles (at least 1 on the
+// line, so that rows that see nothing are written too); 0: nothing there.  `b`:
+// where to begin looking for the sequence, -1 anywhere.
 template <bool SEL>
-__device__ bool decode_item(const TileParams& p, long long item, Unit& u, int& b, int& len) {
+__device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& tiles) {
   const AttnParams& a = p.a;
-  const int s = static_cast<int>(item % p.n_split);
-  const long long rest = item / p.n_split;
-  u.item = static_cast<int>(min(item, 0x7FFFFFFFll));
-  u.head = static_cast<int>(rest % a.cache.heads);
-  const long long slot = rest / a.cache.heads;
-  int total;
   if constexpr (SEL) {
-    const int n = static_cast<int>(slot / p.row_tiles);
-    u.row0 = static_cast<int>(slot % p.row_tiles) * kTileRows;
+    const int n = slot / p.row_tiles;
+    u.row0 = (slot - n * p.row_tiles) * kTileRows;
     u.rows = min(a.group - u.row0, kTileRows);
-    b = kv_seq_of_query(a.batch, n);
-    const KvSeq q = kv_seq(a.batch, a.cache, b);
+    u.b = kv_seq_of_query(a.batch, n);
+    const KvSeq q = kv_seq(a.batch, a.cache, u.b);
     u.q0 = n;
     u.pos0 = (n >= q.q0 && n < q.q0 + q.nq) ? q.pos0 + n - q.q0 : -1;
     u.p_lo = u.p_hi = u.pos0;
     u.skip = u.tile0 = 0;
-    len = a.k;
-    total = (a.k + kKeys - 1) / kKeys;
+    u.len = a.k;
+    tiles = (a.k + kKeys - 1) / kKeys;
+    return tiles;
   } else {
-    int lo = 0, hi = a.batch.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (slot_start(p, mid) <= slot) lo = mid; else hi = mid - 1;
+    if (b < 0) {
+      int lo = 0, hi = a.batch.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (slot_start(p, mid) <= slot) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+    } else {
+      while (b + 1 < a.batch.B && slot_start(p, b + 1) <= slot) ++b;
     }
-    b = lo;
+    u.b = b;
     const KvSeq q = kv_seq(a.batch, a.cache, b);
     const long long row0 = (slot - slot_start(p, b)) * unit_rows(p);
     const long long all = static_cast<long long>(q.nq) * a.group;
-    if (row0 < 0 || row0 >= all) return false;
+    tiles = 0;
+    if (row0 < 0 || row0 >= all) return 0;
     u.row0 = static_cast<int>(row0);
     u.rows = static_cast<int>(min(all - row0, static_cast<long long>(unit_rows(p))));
     u.q0 = q.q0;
     u.pos0 = q.pos0;
     u.p_lo = q.pos0 + u.row0 / a.group;
     u.p_hi = q.pos0 + (u.row0 + u.rows - 1) / a.group;
-    len = q.len;
+    u.len = q.len;
     u.skip = u.tile0 = 0;
-    total = u.p_hi >= 0 ? u.p_hi / kKeys + 1 : 0;
-    if (total > 0 && a.window > 0) {
+    tiles = u.p_hi >= 0 ? u.p_hi / kKeys + 1 : 0;
+    if (tiles > 0 && a.window > 0) {
       u.tile0 = max(u.p_lo - a.window + 1, 0) / kKeys;
       u.skip = min((min(a.sinks, u.p_hi + 1) + kKeys - 1) / kKeys, u.tile0);
-      total = u.skip + total - u.tile0;
+      tiles = u.skip + tiles - u.tile0;
     }
+    return max(tiles, 1);
   }
-  u.first = static_cast<int>(static_cast<long long>(total) * s / p.n_split);
-  u.n_tiles = static_cast<int>(static_cast<long long>(total) * (s + 1) / p.n_split) - u.first;
-  return true;
 }
 
 // --- loader ---------------------------------------------------------------------------------
@@ -259,183 +271,76 @@ __device__ __forceinline__ void store_codes(uint32_t base, int row, int chunk, c
                : "memory");
 }
 
-// What a lane holds of one key tile on its way to shared memory.
-template <int D>
-struct Tile {
-  uint4 k[Map<D>::NI], v[Map<D>::NI];
-  float ks[Map<D>::NI], vs[Map<D>::NI];  // listed: per row; dense: [0], [1] the warp's two groups
-  uint32_t valid;                        // bit i: row i is live
-};
-template <int D>
-struct Ids {
-  int key[Map<D>::NI];                   // listed: key position or -1
-  int page[Map<D>::NI];                  // listed: per row; dense: [0], [1]
-};
-
-template <int D, bool SEL>
-__device__ __forceinline__ void fetch_keys(const TileParams& p, const Unit& u, int ord, int w, int lane, Ids<D>& ids) {
-  if constexpr (SEL) {
-#pragma unroll
-    for (int i = 0; i < Map<D>::NI; ++i) {
-      const int at = ord * kKeys + 32 * w + Map<D>::row(lane, i);
-      ids.key[i] = at < p.a.k ? __ldg(p.a.idx + static_cast<size_t>(u.q0) * p.a.k + at) : -1;
-    }
-  }
-}
 __device__ __forceinline__ int tile_of(const Unit& u, int ord) { return ord < u.skip ? ord : ord - u.skip + u.tile0; }
-
-template <int D, bool SEL>
-__device__ __forceinline__ void fetch_pages(const TileParams& p, const Unit& u, int b, int len, int ord, int w, Ids<D>& ids) {
-  const int* table = p.a.batch.page_table + static_cast<size_t>(b) * p.a.batch.width;
-  if constexpr (SEL) {
-#pragma unroll
-    for (int i = 0; i < Map<D>::NI; ++i) {
-      if (ids.key[i] < 0 || ids.key[i] > u.pos0) ids.key[i] = -1;
-      ids.page[i] = ids.key[i] >= 0 ? __ldg(table + (ids.key[i] >> p.a.cache.page_log2)) : -1;
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int key = tile_of(u, ord) * kKeys + 32 * w + 16 * h;
-      ids.page[h] = key < len ? __ldg(table + (key >> p.a.cache.page_log2)) : -1;
-    }
-  }
-}
-
-// Row i's place in the cache, -1 if it has none.
-template <int D, bool SEL>
-__device__ __forceinline__ long long row_at(const TileParams& p, const Unit& u, int len, int ord, int w, int lane, int i,
-                                            const Ids<D>& ids) {
-  const KvCache& c = p.a.cache;
-  int page, off;
-  if constexpr (SEL) {
-    page = ids.page[i];
-    off = ids.key[i] & (c.page - 1);
-    if (ids.key[i] < 0) return -1;
-  } else {
-    constexpr int kPerGroup = Map<D>::NI / 2;
-    page = ids.page[i / kPerGroup];
-    const int key = tile_of(u, ord) * kKeys + 32 * w + Map<D>::row(lane, i);
-    if (key >= len) return -1;
-    off = key & (c.page - 1);
-  }
-  if (page < 0 || page >= c.num_pages) return -1;
-  return (static_cast<long long>(page) * c.heads + u.head) * c.page + off;
-}
-
-template <int D, bool SEL>
-__device__ __forceinline__ void load_half(const TileParams& p, const Unit& u, int len, int ord, int w, int lane, const Ids<D>& ids,
-                                          bool values, Tile<D>& t) {
-  const KvCache& c = p.a.cache;
-  const uint8_t* codes = values ? c.v_codes : c.k_codes;
-  const float* scale = values ? c.v_scale : c.k_scale;
-  uint32_t valid = 0;
-#pragma unroll
-  for (int i = 0; i < Map<D>::NI; ++i) {
-    const long long r = row_at<D, SEL>(p, u, len, ord, w, lane, i, ids);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (r >= 0) x = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<size_t>(r) * D) + Map<D>::chunk(lane));
-    if (values) t.v[i] = x; else t.k[i] = x;
-    if constexpr (SEL) {
-      const bool listed = ids.key[i] >= 0;
-      float sc = 0.f;
-      if (r >= 0) {
-        sc = __ldg(scale + static_cast<size_t>(ids.page[i]) * c.heads + u.head);
-      } else if (listed && !values) {    // a page outside the pool: the key is NaN
-        sc = __int_as_float(0x7FC00000);
-        raise_status(p.a.status, kDevArg);
-      }
-      if (values) t.vs[i] = sc; else t.ks[i] = sc;
-      if (listed) valid |= 1u << i;
-    }
-  }
-  if constexpr (!SEL) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int key = tile_of(u, ord) * kKeys + 32 * w + 16 * h;
-      float sc = 1.f;
-      if (ids.page[h] >= 0 && ids.page[h] < c.num_pages) {
-        sc = __ldg(scale + static_cast<size_t>(ids.page[h]) * c.heads + u.head);
-      } else if (key < len && !values) {
-        sc = __int_as_float(0x7FC00000);
-        raise_status(p.a.status, kDevArg);
-      }
-      if (values) t.vs[h] = sc; else t.ks[h] = sc;
-    }
-  }
-  if (!values) t.valid = valid;
-}
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 // Listed keys come from blocks of different scales: the codes are multiplied by
 // 64 * scale / (largest scale of the 16-key group), exact in f16 for ratios down
 // to 2^-21 (an e4m3 code is a multiple of 2^-9, f16's smallest step 2^-24).
-template <int D>
-__device__ __forceinline__ float group_scale(const float (&s)[Map<D>::NI], int h) {
-  constexpr int kPer = Map<D>::NI / 2;
-  float m = 0.f;
+// s: this lane's row's scale; returns the group's (its lanes are 16 apart).
+__device__ __forceinline__ float group_scale(float s) {
+  float m = fmaxf(s, 0.f);               // a NaN (page outside the pool) counts as 0
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) m = fmaxf(m, s[h * kPer + i]);
-  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-  m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-  if constexpr (D == 64) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   return m > 0.f ? m : 1.f;
 }
 
+// A warp's 32 rows of codes to registers; row[i]: the lane's i-th row's place in the cache.
+template <int D>
+__device__ __forceinline__ void load_rows(const uint8_t* codes, const uint32_t (&row)[Map<D>::NI], int lane, uint4 (&x)[Map<D>::NI]) {
+#pragma unroll
+  for (int i = 0; i < Map<D>::NI; ++i) {
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (row[i] != kNoRow)
+      x[i] = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<size_t>(row[i]) * D) + Map<D>::chunk(lane));
+  }
+}
 template <int D, bool SEL>
-__device__ __forceinline__ void store_half(uint32_t base, int w, int lane, const uint4 (&x)[Map<D>::NI], const float (&s)[Map<D>::NI],
-                                           float (&group)[2]) {
-  constexpr int kPer = Map<D>::NI / 2;
-  if constexpr (SEL) {
+__device__ __forceinline__ void store_rows(uint32_t base, int w, int lane, const uint4 (&x)[Map<D>::NI], uint32_t factor) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float top = group_scale<D>(s, h);
-      const float inv = 64.f / top;
-      group[h] = top * (1.f / 64.f);
-#pragma unroll
-      for (int i = h * kPer; i < (h + 1) * kPer; ++i)
-        store_codes<D, true>(base, 32 * w + Map<D>::row(lane, i), Map<D>::chunk(lane), x[i], __float2half2_rn(s[i] * inv));
-    }
-  } else {
-    group[0] = s[0];
-    group[1] = s[1];
-#pragma unroll
-    for (int i = 0; i < Map<D>::NI; ++i)
-      store_codes<D, false>(base, 32 * w + Map<D>::row(lane, i), Map<D>::chunk(lane), x[i], __half2());
+  for (int i = 0; i < Map<D>::NI; ++i) {
+    const int r = Map<D>::row(lane, i);
+    uint32_t by = 0;
+    if constexpr (SEL) by = __shfl_sync(0xFFFFFFFFu, factor, r);
+    store_codes<D, SEL>(base, 32 * w + r, Map<D>::chunk(lane), x[i], *reinterpret_cast<const __half2*>(&by));
   }
 }
 
-// Query rows [r0, r0 + 128) of the unit to an operand tile; factor[r] = what turns
-// the products into base-2 exponents.  `mask`: rows repeat with this period.
+// Query rows [r0, r0 + 128) of the unit to an operand tile by two warps (w = 0, 1);
+// factor[r] = what turns the products into base-2 exponents.  Rows repeat with
+// period mask + 1.
 template <int D>
-__device__ void load_queries(const TileParams& p, const Unit& u, uint32_t base, float* factor, int r0, int mask, int w, int lane) {
-  constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = 32 / RPP;
+__device__ __forceinline__ void load_queries(const TileParams& p, const Unit& u, uint32_t base, float* factor, int r0, int mask, int w,
+                                             int lane) {
+  constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = 64 / RPP, AT_ONCE = 4;
   const AttnParams& a = p.a;
   const int j = lane % LPR, sub = lane / LPR;
+  const int need = min(u.rows - r0, mask + 1);                // rows past it are never used
 #pragma unroll 1
-  for (int p0 = 0; p0 < PASSES; p0 += 4) {
-    uint4 raw[4];
+  for (int p0 = 0; p0 < PASSES; p0 += AT_ONCE) {
+    if (64 * w + p0 * RPP >= need && mask == 127) break;
+    uint4 raw[AT_ONCE];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int local = 32 * w + (p0 + i) * RPP + sub;
-      const int r = r0 + (local & mask);
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int r = r0 + ((64 * w + (p0 + i) * RPP + sub) & mask);
       raw[i] = make_uint4(0, 0, 0, 0);
       if (r < u.rows) {
         const int row = u.row0 + r;
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (static_cast<size_t>(u.q0) + row / a.group) * a.q_stride +
-                              static_cast<size_t>(u.head * a.group + row % a.group) * D;
+        const int qi = row / a.group;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (static_cast<size_t>(u.q0) + qi) * a.q_stride +
+                              static_cast<size_t>(u.head * a.group + row - qi * a.group) * D;
         raw[i] = __ldg(reinterpret_cast<const uint4*>(src) + j);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int local = 32 * w + (p0 + i) * RPP + sub;
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int local = 64 * w + (p0 + i) * RPP + sub;
       const uint32_t ws[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      float2 f[4];
       float amax = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        f[e] = kv_unpack16(ws[e], a.bf16);
-        amax = fmaxf(amax, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
+        const float2 f = kv_unpack16(ws[e], a.bf16);
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
       }
 #pragma unroll
       for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
@@ -445,7 +350,10 @@ __device__ void load_queries(const TileParams& p, const Unit& u, uint32_t base, 
       if (j == 0) factor[local] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
       uint32_t h[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = kv_pack16(f[q].x * by, f[q].y * by, false);
+      for (int q = 0; q < 4; ++q) {
+        const float2 f = kv_unpack16(ws[q], a.bf16);
+        h[q] = kv_pack16(f.x * by, f.y * by, false);
+      }
       const uint32_t line = base + (j >> 3) * (kTileRows * 128) + local * 128;
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(line + (((j & 7) ^ (local & 7)) << 4)), "r"(h[0]), "r"(h[1]),
                    "r"(h[2]), "r"(h[3])
@@ -454,9 +362,37 @@ __device__ void load_queries(const TileParams& p, const Unit& u, uint32_t base, 
   }
 }
 
+// Two fp32 products and sums at once.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 template <int D, bool SEL>
-__global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p) {
+__global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_constant__ TileParams p) {
   using S = TileShape<D>;
+  constexpr int NI = Map<D>::NI;
   extern __shared__ __align__(1024) unsigned char smem[];
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + S::kQ + 2 * S::kStage + S::kMerge);
   const uint32_t q_sm = smem_u32(smem), stage_sm = q_sm + S::kQ;
@@ -470,19 +406,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
   if (warp == 12) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&ctrl->kfull[i]), 128);
+        mbar_init(smem_u32(&ctrl->kfull[i]), 4);
         mbar_init(smem_u32(&ctrl->kempty[i]), 1);
-        mbar_init(smem_u32(&ctrl->vfull[i]), 128);
+        mbar_init(smem_u32(&ctrl->vfull[i]), 4);
         mbar_init(smem_u32(&ctrl->vempty[i]), 1);
         mbar_init(smem_u32(&ctrl->sfull[i]), 2);
-        mbar_init(smem_u32(&ctrl->pfull[i]), 128);
+        mbar_init(smem_u32(&ctrl->pfull[i]), 4);
         mbar_init(smem_u32(&ctrl->ofull[i]), 1);
-        mbar_init(smem_u32(&ctrl->ufull[i]), 128);
-        mbar_init(smem_u32(&ctrl->uempty[i]), 256 + 2);
+        mbar_init(smem_u32(&ctrl->ufull[i]), 1);
+        mbar_init(smem_u32(&ctrl->uempty[i]), 8 + 4 + 2 + 2);
+        mbar_init(smem_u32(&ctrl->qfull[i]), 2);
+        mbar_init(smem_u32(&ctrl->wg[i]), 128);
       }
       mbar_init(smem_u32(&ctrl->qempty), 1);
-      mbar_init(smem_u32(&ctrl->mfull), 128);
-      mbar_init(smem_u32(&ctrl->mempty), 128);
+      mbar_init(smem_u32(&ctrl->mfull), 4);
+      mbar_init(smem_u32(&ctrl->mempty), 4);
       mbar_init(smem_u32(&ctrl->drained), 1);
       ctrl->abort_flag = 0;
       mbar_fence_init();
@@ -490,97 +428,162 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
     __syncwarp();
     tmem_alloc(smem_u32(&ctrl->tmem), 512);
   }
+
+  // --- this CTA's piece of the line (head, row tile, key tile), every CTA one tile at least ---
+  long long total;
+  int n_cta = gridDim.x;
+  {
+    Unit u;
+    int tiles;
+    if constexpr (SEL) {
+      tiles = (a.k + kKeys - 1) / kKeys;
+      total = static_cast<long long>(p.slots) * a.cache.heads * tiles;
+      n_cta = static_cast<int>(min(static_cast<long long>(n_cta), total));
+      if (tid == 0) {
+        const long long at = blockIdx.x * total / n_cta;
+        const long long unit = at / tiles;
+        ctrl->at = at;
+        ctrl->left = blockIdx.x < n_cta ? (blockIdx.x + 1) * total / n_cta - at : 0;
+        ctrl->t = static_cast<int>(at - unit * tiles);
+        ctrl->head = static_cast<int>(unit % a.cache.heads);
+        ctrl->slot = static_cast<int>(unit / a.cache.heads);
+      }
+    } else {
+      long long* sums = reinterpret_cast<long long*>(smem);   // free until the first queries come
+      const int each = (p.slots + kThreads - 1) / kThreads;
+      const int s0 = min(tid * each, p.slots), s1 = min(s0 + each, p.slots);
+      long long mine = 0;
+      int b = -1;
+      for (int s = s0; s < s1; ++s) {
+        mine += decode_slot<SEL>(p, s, b, u, tiles);
+        b = u.b;
+      }
+      long long incl = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) sums[warp] = incl;
+      if (tid == 0) ctrl->left = 0;
+      __syncthreads();
+      long long before = incl - mine, one = 0;                // one: a head's tiles
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        one += sums[w];
+      }
+      total = one * a.cache.heads;
+      n_cta = static_cast<int>(min(static_cast<long long>(n_cta), max(total, 1ll)));
+      if (total > 0 && blockIdx.x < n_cta) {
+        const long long at = blockIdx.x * total / n_cta;
+        const long long in = at % one;
+        if (in >= before && in < before + mine) {
+          long long x = before;
+          b = -1;
+          for (int s = s0; s < s1; ++s) {
+            const int n = decode_slot<SEL>(p, s, b, u, tiles);
+            b = u.b;
+            if (in < x + n) {
+              ctrl->at = at;
+              ctrl->left = (blockIdx.x + 1) * total / n_cta - at;
+              ctrl->t = static_cast<int>(in - x);
+              ctrl->slot = s;
+              ctrl->head = static_cast<int>(at / one);
+              break;
+            }
+            x += n;
+          }
+        }
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem;
 
-  if (warp >= 8 && warp < 12) {
-    // ================= loader =================
-    const int w = warp - 8;
-    const int ltid = tid - 256;
-    int un = 0;                          // units published
-    int cnt[2] = {0, 0};                 // tiles loaded by stream (pair mode: [0] counts all)
-    bool ok = true;
-    for (long long item = blockIdx.x; ok; item += gridDim.x) {
-      Unit u;
-      int b = 0, len = 0;
-      const bool more = item < p.items;
-      if (more && !decode_item<SEL>(p, item, u, b, len)) continue;
-      Ids<D> ids;
-      Tile<D> t;
-      if (more && u.n_tiles > 0) {
-        fetch_keys<D, SEL>(p, u, u.first, w, lane, ids);
-        fetch_pages<D, SEL>(p, u, b, len, u.first, w, ids);
-        load_half<D, SEL>(p, u, len, u.first, w, lane, ids, false, t);
-        load_half<D, SEL>(p, u, len, u.first, w, lane, ids, true, t);
-        if (u.n_tiles > 1) fetch_keys<D, SEL>(p, u, u.first + 1, w, lane, ids);
-      }
-      const int us = un & 1;
-      if (un >= 2 && !mbar_wait(smem_u32(&ctrl->uempty[us]), ((un >> 1) - 1) & 1, abort_flag, status)) break;
-      if (!more) u.n_tiles = -1;
-      if (ltid == 0) ctrl->unit[us] = u;
-      if (more && u.n_tiles > 0) {
-        if (pair) {
-          if (un >= 1 && !mbar_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
-          load_queries<D>(p, u, q_sm, ctrl->rowf + us * 256, 0, 127, w, lane);
-          if (u.rows > kTileRows) load_queries<D>(p, u, q_sm + S::kOperand, ctrl->rowf + us * 256 + 128, kTileRows, 127, w, lane);
-        } else {
-          load_queries<D>(p, u, q_sm + us * S::kOperand, ctrl->rowf + us * 128, 0, u.rows <= 64 ? 63 : 127, w, lane);
+  if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == 13) {
+      // ================= the CTA's pieces, one after the other =================
+      if (lane == 0) {
+        long long at = ctrl->at, left = ctrl->left;
+        int slot = ctrl->slot, head = ctrl->head, t = ctrl->t, b = -1;
+        for (int un = 0;; ++un) {
+          Unit u{};
+          int tiles = 0, n = 0;
+          if (left > 0) {
+            while ((n = decode_slot<SEL>(p, slot, b, u, tiles)) == 0) b = u.b, ++slot;   // a live slot lies ahead
+            b = u.b;
+            const int end = static_cast<int>(min(static_cast<long long>(n), t + left));
+            const long long u0 = at - t, u1 = u0 + n;
+            u.head = head;
+            u.first = t;
+            u.n_tiles = min(end, tiles) - t;
+            u.c0 = static_cast<int>(((u0 + 1) * n_cta - 1) / total);
+            u.c1 = static_cast<int>((u1 * n_cta - 1) / total);
+            u.part = t == 0 && end == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (t == 0 ? 1 : 0);
+            at += end - t;
+            left -= end - t;
+            t = 0;
+            if constexpr (SEL) {
+              if (++head == a.cache.heads) {
+                head = 0;
+                ++slot;
+              }
+            } else if (++slot == p.slots) {
+              slot = 0;
+              ++head;
+              b = -1;
+            }
+          } else {
+            u.n_tiles = -1;
+          }
+          if (!SEL && left > 0) {
+            // the rest of the row tiles may be empty up to the next head
+            Unit v;
+            int vt;
+            while (decode_slot<SEL>(p, slot, b, v, vt) == 0) {
+              b = v.b;
+              if (++slot == p.slots) {
+                slot = 0;
+                ++head;
+                b = -1;
+              }
+            }
+          }
+          const int us = un & 1;
+          if (un >= 2 && !mbar_wait(smem_u32(&ctrl->uempty[us]), ((un >> 1) - 1) & 1, abort_flag, status)) break;
+          ctrl->unit[us] = u;
+          mbar_arrive(smem_u32(&ctrl->ufull[us]));
+          if (u.n_tiles < 0) break;
         }
-        fence_async_smem();
       }
-      mbar_arrive(smem_u32(&ctrl->ufull[us]));
-      ++un;
-      if (!more) break;
-#pragma unroll 1
-      for (int i = 0; i < u.n_tiles; ++i) {
-        const int ord = u.first + i;
-        const bool next = i + 1 < u.n_tiles;
-        const int x = pair ? 0 : i & 1;
-        const int n = cnt[x];
-        const int st = pair ? n & 1 : x, use = pair ? n >> 1 : n;
-        const int slot = pair ? n & 3 : x * 2 + (n & 1);
-        if (next) fetch_pages<D, SEL>(p, u, b, len, ord + 1, w, ids);
-        if (use > 0 && !mbar_wait(smem_u32(&ctrl->kempty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
-        float gk[2], gv[2];
-        store_half<D, SEL>(stage_sm + st * S::kStage, w, lane, t.k, t.ks, gk);
-        // the tile's scales, before K is announced
-        Meta& m = ctrl->meta[slot];
-        if constexpr (SEL) {
-          gv[0] = group_scale<D>(t.vs, 0) * (1.f / 64.f);
-          gv[1] = group_scale<D>(t.vs, 1) * (1.f / 64.f);
-          uint32_t bits = 0;
-#pragma unroll
-          for (int r = 0; r < Map<D>::NI; ++r)
-            if ((t.valid >> r) & 1u) bits |= 1u << Map<D>::row(lane, r);
-          bits = __reduce_or_sync(0xFFFFFFFFu, bits);
-          if (lane == 0) m.valid[w] = bits;
-        } else {
-          gv[0] = t.vs[0];
-          gv[1] = t.vs[1];
+    } else if (warp >= 14) {
+      // ================= queries =================
+      for (int un = 0;; ++un) {
+        const int us = un & 1;
+        if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
+        const Unit u = ctrl->unit[us];
+        if (u.n_tiles < 0) break;
+        if (u.n_tiles > 0) {
+          if (pair) {
+            if (un >= 1 && !mbar_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
+            load_queries<D>(p, u, q_sm, ctrl->rowf + us * 256, 0, 127, warp - 14, lane);
+            if (u.rows > kTileRows)
+              load_queries<D>(p, u, q_sm + S::kOperand, ctrl->rowf + us * 256 + 128, kTileRows, 127, warp - 14, lane);
+          } else {
+            load_queries<D>(p, u, q_sm + us * S::kOperand, ctrl->rowf + us * 128, 0, u.rows <= 64 ? 63 : 127, warp - 14, lane);
+          }
+          fence_async_smem();
         }
-        if (lane < 2) {
-          m.ks[2 * w + lane] = lane ? gk[1] : gk[0];
-          const float g = lane ? gv[1] : gv[0];
-          m.lv[2 * w + lane] = __log2f(g) + kBoost;
-          m.iv[2 * w + lane] = __frcp_rn(g);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ctrl->qfull[us]));
+          mbar_arrive(smem_u32(&ctrl->uempty[us]));
         }
-        fence_async_smem();
-        mbar_arrive(smem_u32(&ctrl->kfull[st]));
-        if (next) load_half<D, SEL>(p, u, len, ord + 1, w, lane, ids, false, t);
-        if (use > 0 && !mbar_wait(smem_u32(&ctrl->vempty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
-        store_half<D, SEL>(stage_sm + st * S::kStage + S::kOperand, w, lane, t.v, t.vs, gv);
-        fence_async_smem();
-        mbar_arrive(smem_u32(&ctrl->vfull[st]));
-        if (next) load_half<D, SEL>(p, u, len, ord + 1, w, lane, ids, true, t);
-        if (i + 2 < u.n_tiles) fetch_keys<D, SEL>(p, u, ord + 2, w, lane, ids);
-        ++cnt[x];
       }
-    }
-  } else if (warp == 12) {
-    // ================= MMA issue =================
-    if (lane == 0) {
+    } else if (lane == 0) {
+      // ================= MMA issue =================
       constexpr uint32_t id_qk = idesc_f16(kTileRows, kKeys, false), id_pv = idesc_f16(kTileRows, D, true);
       auto qk = [&](int x, uint32_t q_tile, int st) {
 #pragma unroll
@@ -608,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
           const int n = ctrl->unit[us].n_tiles;
           const bool two = ctrl->unit[us].rows > kTileRows;
           if (n < 0) break;
+          if (!mbar_wait(smem_u32(&ctrl->qfull[us]), (nu >> 1) & 1, abort_flag, status)) break;
           ++nu;
           if (n > 0) {
             if (!mbar_wait(smem_u32(&ctrl->kfull[c & 1]), (c >> 1) & 1, abort_flag, status)) break;
@@ -654,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
         int cu[2] = {0, 0}, left[2] = {0, 0}, cnt[2] = {0, 0}, fresh[2] = {1, 1};
         bool pending[2] = {false, false}, done[2] = {false, false};
         uint64_t since = globaltimer_ns();
+        int idle = 0;
         while (!(done[0] && done[1])) {
           bool progress = false;
 #pragma unroll
@@ -678,6 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
               const int us = cu[x] & 1;
               if (!mbar_test(smem_u32(&ctrl->ufull[us]), (cu[x] >> 1) & 1)) break;
               const int n = ctrl->unit[us].n_tiles;
+              if (n >= 0 && !mbar_test(smem_u32(&ctrl->qfull[us]), (cu[x] >> 1) & 1)) break;
               progress = true;
               if (n < 0) {
                 done[x] = true;
@@ -698,8 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
             progress = true;
           }
           if (progress) {
-            since = globaltimer_ns();
-          } else {
+            idle = 0;
+          } else if ((++idle & 255) == 0) {
+            if (idle == 256) since = globaltimer_ns();
             if (*abort_flag) break;
             if (globaltimer_ns() - since > kWaitLimitNs) {
               *abort_flag = 1;
@@ -714,28 +721,189 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
       mbar_drain(smem_u32(&ctrl->drained), 0);
     }
     __syncwarp();
+  } else if (warp >= 8) {
+    // ================= loader =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMain));
+    const int w = warp - 8;
+    const KvCache& c = a.cache;
+    int cnt[2] = {0, 0};                 // tiles loaded by stream (pair mode: [0] counts all)
+    bool ok = true;
+    for (int un = 0; ok; ++un) {
+      const int us = un & 1;
+      if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
+      const Unit u = ctrl->unit[us];
+      if (u.n_tiles < 0) break;
+      const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width;
+      const int end = u.first + u.n_tiles;
+      // A tile's lookups run ahead of its data.  Listed: lane = row; position two tiles
+      // ahead, page and place one ahead.  Dense: the pages of the warp's two groups.
+      auto key_of = [&](int ord) {
+        const int i = ord * kKeys + 32 * w + lane;
+        if (ord >= end || i >= a.k) return -1;
+        const int key = __ldg(a.idx + static_cast<size_t>(u.q0) * a.k + i);
+        return key <= u.pos0 ? max(key, -1) : -1;
+      };
+      auto page_of = [&](int key) { return key >= 0 ? __ldg(table + (key >> c.page_log2)) : -1; };
+      int key1 = -1, page1 = -1, page1b = -1, key2 = -1;
+      float ks = 1.f, vs = 1.f;          // listed: the lane's row; dense: lanes 0, 1 the groups
+      bool valid = false;
+      uint32_t row[NI];
+      // places and scales of tile `ord` from its lookups (listed: key1, page1; dense: page1, page1b)
+      auto place_tile = [&](int ord, float& k_sc, float& v_sc, bool& live) {
+        if constexpr (SEL) {
+          uint32_t mine = kNoRow;
+          live = key1 >= 0;
+          k_sc = v_sc = 0.f;
+          if (live) {
+            if (page1 >= 0 && page1 < c.num_pages) {
+              const uint32_t blk = static_cast<uint32_t>(page1) * c.heads + u.head;
+              mine = blk * c.page + (key1 & (c.page - 1));
+              k_sc = __ldg(c.k_scale + blk);
+              v_sc = __ldg(c.v_scale + blk);
+            } else {
+              raise_status(status, kDevArg);
+              k_sc = __int_as_float(0x7FC00000);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < NI; ++i) row[i] = __shfl_sync(0xFFFFFFFFu, mine, Map<D>::row(lane, i));
+        } else {
+          const int key = tile_of(u, ord) * kKeys + 32 * w;
+          uint32_t blk[2];
+          bool known[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int pg = h ? page1b : page1;
+            known[h] = pg >= 0 && pg < c.num_pages;
+            blk[h] = known[h] ? static_cast<uint32_t>(pg) * c.heads + u.head : 0;
+            if (!known[h] && key + 16 * h < u.len) raise_status(status, kDevArg);
+          }
+          const int h = lane & 1;
+          const bool kn = h ? known[1] : known[0];
+          const uint32_t bk = h ? blk[1] : blk[0];
+          k_sc = kn ? __ldg(c.k_scale + bk) : key + 16 * h < u.len ? __int_as_float(0x7FC00000) : 1.f;
+          v_sc = kn ? __ldg(c.v_scale + bk) : 1.f;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            constexpr int kPer = NI / 2;
+            const int at = key + Map<D>::row(lane, i);
+            row[i] = known[i / kPer] && at < u.len ? blk[i / kPer] * c.page + (at & (c.page - 1)) : kNoRow;
+          }
+        }
+      };
+      auto look = [&](int ord) {         // dense: pages of tile `ord`
+        if constexpr (!SEL) {
+          const int key = tile_of(u, ord) * kKeys + 32 * w;
+          page1 = ord < end && key < u.len ? __ldg(table + (key >> c.page_log2)) : -1;
+          page1b = ord < end && key + 16 < u.len ? __ldg(table + ((key + 16) >> c.page_log2)) : -1;
+        }
+      };
+      uint4 kx[NI], vx[NI];
+      if (u.n_tiles > 0) {
+        if constexpr (SEL) {
+          key1 = key_of(u.first);
+          key2 = key_of(u.first + 1);
+          page1 = page_of(key1);
+        } else {
+          look(u.first);
+        }
+        place_tile(u.first, ks, vs, valid);
+        load_rows<D>(c.k_codes, row, lane, kx);
+        load_rows<D>(c.v_codes, row, lane, vx);
+        if constexpr (SEL) {
+          key1 = key2;
+          page1 = page_of(key1);
+          key2 = key_of(u.first + 2);
+        } else {
+          look(u.first + 1);
+        }
+      }
+#pragma unroll 1
+      for (int ord = u.first; ord < end; ++ord) {
+        const bool next = ord + 1 < end;
+        const int x = pair ? 0 : (ord - u.first) & 1;
+        const int n = cnt[x];
+        const int st = pair ? n & 1 : x, use = pair ? n >> 1 : n;
+        Meta& m = ctrl->meta[pair ? n & 3 : x * 2 + (n & 1)];
+        float ks1 = 1.f, vs1 = 1.f;
+        bool valid1 = false;
+        if (next) place_tile(ord + 1, ks1, vs1, valid1);
+        uint32_t k_by = 0, v_by = 0;
+        float kg = ks, vg = vs;
+        if constexpr (SEL) {
+          const float kt = group_scale(ks), vt = group_scale(vs);
+          const __half2 kh = __float2half2_rn(ks * (64.f / kt)), vh = __float2half2_rn(vs * (64.f / vt));
+          k_by = *reinterpret_cast<const uint32_t*>(&kh);
+          v_by = *reinterpret_cast<const uint32_t*>(&vh);
+          kg = kt * (1.f / 64.f);
+          vg = vt * (1.f / 64.f);
+        }
+        if (use > 0 && !mbar_wait(smem_u32(&ctrl->kempty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
+        if constexpr (SEL) {
+          const uint32_t bits = __ballot_sync(0xFFFFFFFFu, valid);
+          if (lane == 0) m.valid[w] = bits;
+          if ((lane & 15) == 0) {
+            m.ks[2 * w + (lane >> 4)] = kg;
+            m.lv[2 * w + (lane >> 4)] = __log2f(vg) + kBoost;
+            m.iv[2 * w + (lane >> 4)] = __frcp_rn(vg);
+          }
+        } else {
+          if (lane < 2) {
+            m.ks[2 * w + lane] = kg;
+            m.lv[2 * w + lane] = __log2f(vg) + kBoost;
+            m.iv[2 * w + lane] = __frcp_rn(vg);
+          }
+        }
+        store_rows<D, SEL>(stage_sm + st * S::kStage, w, lane, kx, k_by);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->kfull[st]));
+        if (next) load_rows<D>(c.k_codes, row, lane, kx);
+        if constexpr (SEL) {
+          key1 = key2;
+          page1 = page_of(key1);
+          key2 = key_of(ord + 3);
+        } else {
+          look(ord + 2);
+        }
+        if (use > 0 && !mbar_wait(smem_u32(&ctrl->vempty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
+        store_rows<D, SEL>(stage_sm + st * S::kStage + S::kOperand, w, lane, vx, v_by);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->vfull[st]));
+        if (next) load_rows<D>(c.v_codes, row, lane, vx);
+        ks = ks1;
+        vs = vs1;
+        valid = valid1;
+        ++cnt[x];
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl->uempty[us]));
+    }
   } else {
     // ================= softmax =================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMain));
     const int x = warp >> 2;             // stream
     const int r = tid & 127;             // tensor-memory lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + x * kKeys, o_col = tmem + lanes + 256 + x * D;
     const float inf = __int_as_float(0x7F800000);
-    int sn = 0, on = 0, mn = 0;          // scores, results and merges seen
+    int sn = 0, on = 0, mn = 0, wn = 0;  // scores, results, merges and meetings seen
     int pc = 0;                          // pair mode: tiles seen by the CTA
     for (int un = 0;; ++un) {
       const int us = un & 1;
       if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const Unit u = ctrl->unit[us];
       if (u.n_tiles < 0) break;
+      if (!mbar_wait(smem_u32(&ctrl->qfull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const bool twice = !pair && u.rows <= 64;
       const int row = pair ? x * kTileRows + r : twice ? r & 63 : r;
       const bool live = row < u.rows && (!twice || (r >> 6) == x);
       const bool warp_live = __any_sync(0xFFFFFFFFu, live);
       const int mine = pair ? (x == 0 || u.rows > kTileRows ? u.n_tiles : 0) : x == 0 ? (u.n_tiles + 1) >> 1 : u.n_tiles >> 1;
-      const int qi = (u.row0 + row) / a.group;
-      const int pos = live ? (SEL ? u.pos0 : u.pos0 + qi) : -1;
-      const float f = mine > 0 ? (pair ? ctrl->rowf[us * 256 + row] : ctrl->rowf[us * 128 + r]) : 0.f;
+      const int pos = live ? (SEL ? u.pos0 : u.pos0 + (u.row0 + row) / a.group) : -1;
+      const float f = live && mine > 0 ? (pair ? ctrl->rowf[us * 256 + row] : ctrl->rowf[us * 128 + r]) : 0.f;
       float M = kMinusHuge, l = 0.f;
       bool ok = true;
 #pragma unroll 1
@@ -748,89 +916,126 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
         if (warp_live) {
           const int key0 = tile_of(u, ord) * kKeys;
           bool masked;
-          uint32_t vw[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
           if constexpr (SEL) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) vw[c] = m.valid[c];
-            masked = (vw[0] & vw[1] & vw[2] & vw[3]) != 0xFFFFFFFFu;
+            masked = (m.valid[0] & m.valid[1] & m.valid[2] & m.valid[3]) != 0xFFFFFFFFu;
           } else {
-            masked = !(key0 + kKeys - 1 <= u.p_lo &&
-                       (a.window <= 0 || key0 > u.p_hi - a.window || key0 + kKeys <= a.sinks));
-            if (masked) {
-              // this row's visible keys of the tile as bits
+            masked = !(key0 + kKeys - 1 <= u.p_lo && (a.window <= 0 || key0 > u.p_hi - a.window || key0 + kKeys <= a.sinks));
+          }
+          bool slow = masked || i == 0;
+          if (!slow) {
+            // One pass with the maximum as it stands; weights stay in registers until it is
+            // known that none outgrew the slack.
+            uint32_t pk[64];
+            float mx = -inf;
+            float l1 = l;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float s[32];
+              tmem_ld32(s_col + 32 * c, s);
+              tmem_ld32_wait(s);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float fa = f * m.ks[2 * c + h], fb = m.lv[2 * c + h] - M;
+                const uint64_t fa2 = pack2(fa, fa), fb2 = pack2(fb, fb);
+                uint64_t sum = 0;
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                  const float2 t = unpack2(fma2(pack2(s[16 * h + e], s[16 * h + e + 1]), fa2, fb2));
+                  mx = fmaxf(fmaxf(mx, t.x), t.y);
+                  const float w0 = exp2_approx(t.x), w1 = exp2_approx(t.y);
+                  sum = add2(sum, pack2(w0, w1));
+                  pk[16 * c + 8 * h + e / 2] = pack_f16(w0, w1);
+                }
+                const float2 sm = unpack2(sum);
+                l1 = fmaf(sm.x + sm.y, m.iv[2 * c + h], l1);
+              }
+            }
+            slow = __any_sync(0xFFFFFFFFu, mx > kBoost + kSlack);
+            if (!slow) {
+              l = l1;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pk[16 * c + e];
+                tmem_st16(s_col + 16 * c, w);
+              }
+            }
+          }
+          if (slow) {
+            // this row's visible keys of 32 columns as bits
+            auto seen_of = [&](int c) -> uint32_t {
+              if (!masked) return 0xFFFFFFFFu;
+              if constexpr (SEL) {
+                return m.valid[c];
+              } else {
                 auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };   // keys < n
                 const int k0 = key0 + 32 * c;
                 uint32_t seen = below(pos + 1 - k0);
                 if (a.window > 0) seen &= ~below(pos - a.window + 1 - k0) | below(a.sinks - k0);
-                vw[c] = seen;
+                return seen;
+              }
+            };
+            float mx = -inf;
+            float s[32];
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(s_col + 32 * c, s);
+              const uint32_t seen = seen_of(c);
+              tmem_ld32_wait(s);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float g = -inf;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) g = fmaxf(g, (seen >> (16 * h + e)) & 1u ? s[16 * h + e] : -inf);
+                mx = fmaxf(mx, fmaf(g, f * m.ks[2 * c + h], m.lv[2 * c + h]));
               }
             }
-          }
-          float mx = -inf;
-          float s[32];
+            if (__any_sync(0xFFFFFFFFu, mx > M + (kBoost + kSlack))) {
+              const float top = fmaxf(M, mx - kBoost);
+              const float by = exp2_approx(M - top);
+              M = top;
+              l *= by;
+              if (i > 0) {               // scores are complete, so the last value product is too
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  tmem_ld32(o_col + 32 * c, s);
+                  tmem_ld32_wait(s);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(s_col + 32 * c, s);
-            tmem_ld32_wait(s);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) s[e] = (vw[c] >> e) & 1u ? s[e] : -inf;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float g = s[16 * h];
-#pragma unroll
-              for (int e = 1; e < 16; ++e) g = fmaxf(g, s[16 * h + e]);
-              mx = fmaxf(mx, fmaf(g, f * m.ks[2 * c + h], m.lv[2 * c + h]));
-            }
-          }
-          if (__any_sync(0xFFFFFFFFu, mx > M + (kBoost + kSlack))) {
-            const float next = fmaxf(M, mx - kBoost);
-            const float by = exp2_approx(M - next);
-            M = next;
-            l *= by;
-            if (i > 0) {                 // scores are complete, so the last value product is too
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                tmem_ld32(o_col + 32 * c, s);
-                tmem_ld32_wait(s);
-#pragma unroll
-                for (int e = 0; e < 32; ++e) s[e] *= by;
-                tmem_st32f(o_col + 32 * c, s);
+                  for (int e = 0; e < 32; ++e) s[e] *= by;
+                  tmem_st32f(o_col + 32 * c, s);
+                }
               }
-              tmem_st_wait();
             }
-          }
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(s_col + 32 * c, s);
+              const uint32_t seen = seen_of(c);
+              tmem_ld32_wait(s);
+              uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32(s_col + 32 * c, s);
-            tmem_ld32_wait(s);
-            if (masked) {
+              for (int h = 0; h < 2; ++h) {
+                const float fa = f * m.ks[2 * c + h], fb = m.lv[2 * c + h] - M;
+                float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) s[e] = (vw[c] >> e) & 1u ? s[e] : -inf;
-            }
-            uint32_t pk[16];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float fa = f * m.ks[2 * c + h], fb = m.lv[2 * c + h] - M;
-              float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const float w0 = exp2_approx(fmaf(s[16 * h + e], fa, fb)), w1 = exp2_approx(fmaf(s[16 * h + e + 1], fa, fb));
-                sum0 += w0;
-                sum1 += w1;
-                pk[8 * h + e / 2] = kv_pack16(w0, w1, false);
+                for (int e = 0; e < 16; e += 2) {
+                  const float s0 = (seen >> (16 * h + e)) & 1u ? fmaf(s[16 * h + e], fa, fb) : -inf;
+                  const float s1 = (seen >> (16 * h + e + 1)) & 1u ? fmaf(s[16 * h + e + 1], fa, fb) : -inf;
+                  const float w0 = exp2_approx(s0), w1 = exp2_approx(s1);
+                  sum0 += w0;
+                  sum1 += w1;
+                  pk[8 * h + e / 2] = pack_f16(w0, w1);
+                }
+                l = fmaf(sum0 + sum1, m.iv[2 * c + h], l);
               }
-              l = fmaf(sum0 + sum1, m.iv[2 * c + h], l);
+              tmem_st16(s_col + 16 * c, pk);
             }
-            tmem_st16(s_col + 16 * c, pk);
           }
           tmem_st_wait();
         }
         tc_fence_before();
-        mbar_arrive(smem_u32(&ctrl->pfull[x]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->pfull[x]));
       }
       if (!ok) break;
       pc += u.n_tiles;
@@ -844,10 +1049,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
       float by0 = 1.f, by1 = 0.f;
       const int partner = twice ? (r & 63) : r;           // row of the hand-over buffer
       const int rounds = twice || D == 64 ? 1 : 2;        // 64-column rounds when 128 rows fill the buffer
-      constexpr int kCols = D;
       float* ml = ctrl->rowf + 256;
+      const bool writer = pair ? x == 0 || u.rows > kTileRows : x == 0;
       if (merged && x == 1) {
-        const int cols = kCols / rounds;
+        const int cols = D / rounds;
         for (int h = 0; h < rounds && ok; ++h) {
           if (mn > 0 && !mbar_wait(smem_u32(&ctrl->mempty), (mn - 1) & 1, abort_flag, status)) { ok = false; break; }
           ++mn;
@@ -856,6 +1061,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
             ml[2 * partner + 1] = l;
           }
           if (warp_live) {
+#pragma unroll 1
             for (int c = 0; c < cols / 32; ++c) {
               float s[32];
               tmem_ld32(o_col + h * cols + 32 * c, s);
@@ -866,90 +1072,150 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
                     make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
             }
           }
-          mbar_arrive(smem_u32(&ctrl->mfull));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctrl->mfull));
         }
         if (!ok) break;
       }
-      if (!merged || x == 0) {
-        if (!(x == 1 && (!pair || u.rows <= kTileRows))) {
-          // this thread's row goes out: whole result, or a part when the keys are split
-          const bool part = p.n_split > 1;
-          float* pd = nullptr;
-          size_t at = 0;
-          if (live) {
-            const int rr = u.row0 + row;
-            at = (static_cast<size_t>(u.q0) + rr / a.group) * a.q_heads + u.head * a.group + rr % a.group;
-            if (part) pd = a.part + static_cast<size_t>(u.item) * unit_rows(p) * (D + 2);
-          }
-          for (int h = 0; h < (merged ? rounds : 1) && ok; ++h) {
-            const int cols = merged ? kCols / rounds : kCols;
-            if (merged) {
-              if (!mbar_wait(smem_u32(&ctrl->mfull), mn & 1, abort_flag, status)) { ok = false; break; }
-              ++mn;
-              if (h == 0) {
-                const float M1 = ml[2 * partner], l1 = ml[2 * partner + 1];
-                const float next = fmaxf(M, M1);
-                by0 = exp2_approx(M - next);
-                by1 = exp2_approx(M1 - next);
-                M = next;
-                l = l * by0 + l1 * by1;
-              }
+      if (writer) {
+        // this thread's row goes out: whole result, or a piece to be joined
+        const bool part = u.part >= 0;
+        const int rows_max = unit_rows(p);
+        constexpr int kRowFloats = D + 2;
+        float* pd = a.part + static_cast<size_t>(max(u.part, 0)) * rows_max * kRowFloats;
+        size_t at = 0;
+        if (live) {
+          const int rr = u.row0 + row;
+          const int qi = rr / a.group;
+          at = (static_cast<size_t>(u.q0) + qi) * a.q_heads + u.head * a.group + (rr - qi * a.group);
+        }
+        auto write_out = [&](int col, const float (&s)[32], float inv) {
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at * D + col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(kv_pack16(s[8 * e] * inv, s[8 * e + 1] * inv, a.bf16),
+                                kv_pack16(s[8 * e + 2] * inv, s[8 * e + 3] * inv, a.bf16),
+                                kv_pack16(s[8 * e + 4] * inv, s[8 * e + 5] * inv, a.bf16),
+                                kv_pack16(s[8 * e + 6] * inv, s[8 * e + 7] * inv, a.bf16));
+        };
+        for (int h = 0; h < (merged ? rounds : 1) && ok; ++h) {
+          const int cols = merged ? D / rounds : D;
+          if (merged) {
+            if (!mbar_wait(smem_u32(&ctrl->mfull), mn & 1, abort_flag, status)) { ok = false; break; }
+            ++mn;
+            if (h == 0) {
+              const float M1 = ml[2 * partner], l1 = ml[2 * partner + 1];
+              const float top = fmaxf(M, M1);
+              by0 = exp2_approx(M - top);
+              by1 = exp2_approx(M1 - top);
+              M = top;
+              l = l * by0 + l1 * by1;
             }
-            const float inv = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            if (warp_live) {
-              for (int c = 0; c < cols / 32; ++c) {
-                float s[32];
-                if (mine > 0) {
-                  tmem_ld32(o_col + h * cols + 32 * c, s);
-                  tmem_ld32_wait(s);
-                }
+          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          if (warp_live) {
+#pragma unroll 1
+            for (int c = 0; c < cols / 32; ++c) {
+              float s[32];
+              if (mine > 0) {
+                tmem_ld32(o_col + h * cols + 32 * c, s);
+                tmem_ld32_wait(s);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[e] = 0.f;
+              }
+              if (merged) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                  float4 o1 = make_float4(0.f, 0.f, 0.f, 0.f);
-                  if (merged) o1 = *reinterpret_cast<const float4*>(merge + partner * cols + (((c * 8 + e) ^ (r & 7)) << 2));
-                  const float* of = reinterpret_cast<const float*>(&o1);
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const float own = mine > 0 ? s[4 * e + q] * by0 : 0.f;
-                    s[4 * e + q] = merged ? fmaf(of[q], by1, own) * inv : own * inv;
-                  }
+                  const float4 o1 = *reinterpret_cast<const float4*>(merge + partner * cols + (((c * 8 + e) ^ (r & 7)) << 2));
+                  s[4 * e] = fmaf(o1.x, by1, s[4 * e] * by0);
+                  s[4 * e + 1] = fmaf(o1.y, by1, s[4 * e + 1] * by0);
+                  s[4 * e + 2] = fmaf(o1.z, by1, s[4 * e + 2] * by0);
+                  s[4 * e + 3] = fmaf(o1.w, by1, s[4 * e + 3] * by0);
                 }
-                if (live) {
-                  const int col = h * cols + 32 * c;
-                  if (part) {
-                    float4* dst = reinterpret_cast<float4*>(pd + unit_rows(p) * 2 + static_cast<size_t>(row) * D + col);
+              }
+              if (live) {
+                const int col = h * cols + 32 * c;
+                if (part) {
+                  // column-major in pieces of four, so that a warp's stores lie side by side
+                  float4* dst = reinterpret_cast<float4*>(pd + rows_max * 2) + static_cast<size_t>(col / 4) * rows_max + row;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
-                  } else {
-                    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at * D + col);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                      dst[e] = make_uint4(kv_pack16(s[8 * e], s[8 * e + 1], a.bf16), kv_pack16(s[8 * e + 2], s[8 * e + 3], a.bf16),
-                                          kv_pack16(s[8 * e + 4], s[8 * e + 5], a.bf16),
-                                          kv_pack16(s[8 * e + 6], s[8 * e + 7], a.bf16));
-                  }
+                  for (int e = 0; e < 8; ++e)
+                    __stcg(dst + static_cast<size_t>(e) * rows_max, make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]));
+                } else {
+                  write_out(col, s, inv);
                 }
               }
             }
-            if (merged) mbar_arrive(smem_u32(&ctrl->mempty));
           }
-          if (!ok) break;
-          if (live) {
-            if (part) {
-              pd[2 * row] = M;
-              pd[2 * row + 1] = l;
-            } else if (a.lse != nullptr) {
-              a.lse[at] = l == 0.f ? -inf : (M - kBoost + log2f(l)) * 0.69314718055994530942f;
+          __syncwarp();
+          if (merged && lane == 0) mbar_arrive(smem_u32(&ctrl->mempty));
+        }
+        if (!ok) break;
+        auto write_lse = [&](float m2, float sum) {
+          if (a.lse != nullptr) a.lse[at] = sum == 0.f ? -inf : (m2 - kBoost + log2f(sum)) * 0.69314718055994530942f;
+        };
+        if (!part) {
+          if (live) write_lse(M, l);
+        } else {
+          if (live) __stcg(reinterpret_cast<float2*>(pd) + row, make_float2(M, l));
+          // the last of the unit's CTAs joins the pieces in their order
+          __threadfence();
+          mbar_arrive(smem_u32(&ctrl->wg[x]));
+          if (!mbar_wait(smem_u32(&ctrl->wg[x]), wn & 1, abort_flag, status)) break;
+          ++wn;
+          if (r == 0) {
+            int* count = a.counters + 2 * u.c0 + x;
+            const bool last = atomicAdd(count, 1) == u.c1 - u.c0;
+            if (last) *count = 0;
+            ctrl->last[x] = last;
+          }
+          mbar_arrive(smem_u32(&ctrl->wg[x]));
+          if (!mbar_wait(smem_u32(&ctrl->wg[x]), wn & 1, abort_flag, status)) break;
+          ++wn;
+          if (*reinterpret_cast<volatile int*>(&ctrl->last[x]) && live) {
+            __threadfence();
+            const size_t slot_floats = static_cast<size_t>(rows_max) * kRowFloats;
+            float top = kMinusHuge, sum = 0.f;
+            for (int cta = u.c0; cta <= u.c1; ++cta) {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part + (2 * cta + (cta == u.c0 ? 1 : 0)) * slot_floats) + row);
+              const float next = fmaxf(top, v.x);
+              sum = sum * exp2_approx(top - next) + v.y * exp2_approx(v.x - next);
+              top = next;
             }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float s[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[e] = 0.f;
+#pragma unroll 1
+              for (int cta = u.c0; cta <= u.c1; ++cta) {
+                const float* src = a.part + (2 * cta + (cta == u.c0 ? 1 : 0)) * slot_floats;
+                const float by = exp2_approx(__ldcg(src + 2 * row) - top);
+                const float4* o4 = reinterpret_cast<const float4*>(src + rows_max * 2) + static_cast<size_t>(8 * c) * rows_max + row;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 v = __ldcg(o4 + static_cast<size_t>(e) * rows_max);
+                  s[4 * e] = fmaf(v.x, by, s[4 * e]);
+                  s[4 * e + 1] = fmaf(v.y, by, s[4 * e + 1]);
+                  s[4 * e + 2] = fmaf(v.z, by, s[4 * e + 2]);
+                  s[4 * e + 3] = fmaf(v.w, by, s[4 * e + 3]);
+                }
+              }
+              write_out(32 * c, s, inv);
+            }
+            write_lse(top, sum);
           }
         }
       }
       tc_fence_before();
-      mbar_arrive(smem_u32(&ctrl->uempty[us]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl->uempty[us]));
     }
     // dense: queries that belong to no sequence have no unit
     if constexpr (!SEL) {
-      if (x == 1 && p.n_split == 1) {
+      if (x == 1) {
         for (long long n = blockIdx.x * 128ll + r; n < a.batch.N; n += gridDim.x * 128ll) {
           const KvSeq q = kv_seq(a.batch, a.cache, kv_seq_of_query(a.batch, static_cast<int>(n)));
           if (n >= q.q0 && n < q.q0 + q.nq) continue;
@@ -969,74 +1235,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const TileParams p
   }
 }
 
-// Joins the parts of split units in their order: one CTA per unit.
-template <int D, bool SEL>
-__global__ void __launch_bounds__(256) kv_join_kernel(const TileParams p) {
-  const AttnParams& a = p.a;
-  const int rows_max = unit_rows(p);
-  Unit u;
-  int b, len;
-  const long long base = static_cast<long long>(blockIdx.x) * p.n_split;
-  const bool there = decode_item<SEL>(p, base, u, b, len);
-  if (there) {
-    for (int i = threadIdx.x; i < u.rows * (D / 4); i += 256) {
-      const int r = i / (D / 4), ch = i % (D / 4);
-      float M = kMinusHuge, l = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < p.n_split; ++s) {
-        const float* src = a.part + static_cast<size_t>(base + s) * rows_max * (D + 2);
-        const float2 ml = *reinterpret_cast<const float2*>(src + 2 * r);
-        const float4 v = *reinterpret_cast<const float4*>(src + rows_max * 2 + static_cast<size_t>(r) * D + ch * 4);
-        const float next = fmaxf(M, ml.x);
-        const float x = exp2_approx(M - next), y = exp2_approx(ml.x - next);
-        M = next;
-        l = l * x + ml.y * y;
-        acc = make_float4(acc.x * x + v.x * y, acc.y * x + v.y * y, acc.z * x + v.z * y, acc.w * x + v.w * y);
-      }
-      const int rr = u.row0 + r;
-      const size_t at = (static_cast<size_t>(u.q0) + rr / a.group) * a.q_heads + u.head * a.group + rr % a.group;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at * D)[ch] =
-          make_uint2(kv_pack16(acc.x * inv, acc.y * inv, a.bf16), kv_pack16(acc.z * inv, acc.w * inv, a.bf16));
-      if (ch == 0 && a.lse != nullptr)
-        a.lse[at] = l == 0.f ? -__int_as_float(0x7F800000) : (M - kBoost + log2f(l)) * 0.69314718055994530942f;
-    }
-  }
-  if constexpr (!SEL) {
-    for (long long n = blockIdx.x; n < a.batch.N; n += gridDim.x) {
-      const KvSeq q = kv_seq(a.batch, a.cache, kv_seq_of_query(a.batch, static_cast<int>(n)));
-      if (n >= q.q0 && n < q.q0 + q.nq) continue;
-      uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + n * a.q_heads * D;
-      for (int i = threadIdx.x; i < a.q_heads * D; i += 256) o[i] = 0;
-      if (a.lse != nullptr)
-        for (int i = threadIdx.x; i < a.q_heads; i += 256) a.lse[n * a.q_heads + i] = -__int_as_float(0x7F800000);
-    }
-  }
-}
-
-constexpr int kSplitItems = 2;           // split units fill at most this many waves of CTAs
-
-template <int D, bool SEL>
-cudaError_t launch_tile(TileParams& p, long long units, int num_sms, cudaStream_t stream) {
-  const int grid = static_cast<int>(p.items < num_sms ? p.items : num_sms);
-  kv_tile_kernel<D, SEL><<<grid, kThreads, TileShape<D>::kBytes, stream>>>(p);
-  count_launches(1);
-  if (p.n_split > 1) {
-    kv_join_kernel<D, SEL><<<static_cast<unsigned>(units), 256, 0, stream>>>(p);
-    count_launches(1);
-  }
-  return cudaGetLastError();
-}
-
 template <int D, bool SEL>
 cudaError_t init_tile() {
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_tile_kernel<D, SEL>), cudaFuncAttributeMaxDynamicSharedMemorySize,
                               TileShape<D>::kBytes);
 }
 
+template <int D, bool SEL>
+cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
+  kv_tile_kernel<D, SEL><<<num_sms, kThreads, TileShape<D>::kBytes, stream>>>(p);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-size_t kv_tile_part_floats(int num_sms) { return static_cast<size_t>(kSplitItems) * num_sms * 2 * kTileRows * (128 + 2); }
+size_t kv_tile_part_floats(int num_sms) { return static_cast<size_t>(2) * num_sms * 2 * kTileRows * (128 + 2); }
+int kv_tile_counters(int num_sms) { return 2 * num_sms; }
 
 cudaError_t kv_tile_init() {
   cudaError_t e = init_tile<128, false>();
@@ -1050,25 +1265,16 @@ cudaError_t launch_kv_tile(const AttnParams& a, int max_q, int num_sms, cudaStre
   TileParams p{};
   p.a = a;
   const bool sel = a.idx != nullptr;
-  long long units, tiles;
   if (sel) {
     p.row_tiles = (a.group + kTileRows - 1) / kTileRows;
-    units = static_cast<long long>(a.batch.N) * p.row_tiles * a.cache.heads;
-    tiles = (a.k + kKeys - 1) / kKeys;
+    p.slots = a.batch.N * p.row_tiles;
   } else {
     p.pair = static_cast<long long>(max_q) * a.group > kTileRows;
     const int rows = p.pair ? 2 * kTileRows : kTileRows;
-    units = (static_cast<long long>(a.batch.N) * a.group / rows + a.batch.B) * a.cache.heads;
-    tiles = (static_cast<long long>(a.batch.width) * a.cache.page + kKeys - 1) / kKeys;
+    p.slots = static_cast<int>(static_cast<long long>(a.batch.N) * a.group / rows) + a.batch.B;
   }
-  // Too few units to fill the GPU: cut each one's keys, two key tiles to a piece at least.
-  const long long room = static_cast<long long>(kSplitItems) * num_sms / units;
-  const long long most = (tiles + 1) / 2;
-  const long long split = room < most ? room : most;
-  p.n_split = static_cast<int>(split > 1 ? split : 1);
-  p.items = units * p.n_split;
-  if (a.dim == 128) return sel ? launch_tile<128, true>(p, units, num_sms, stream) : launch_tile<128, false>(p, units, num_sms, stream);
-  return sel ? launch_tile<64, true>(p, units, num_sms, stream) : launch_tile<64, false>(p, units, num_sms, stream);
+  if (a.dim == 128) return sel ? launch_tile<128, true>(p, num_sms, stream) : launch_tile<128, false>(p, num_sms, stream);
+  return sel ? launch_tile<64, true>(p, num_sms, stream) : launch_tile<64, false>(p, num_sms, stream);
 }
 
 }  // namespace ltk

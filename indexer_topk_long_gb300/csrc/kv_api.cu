@@ -65,6 +65,8 @@ ltk_status ltk_kv_create(const ltk_kv_config* cfg, ltk_kv** out) {
   if (cfg == nullptr || cfg->num_pages < 1 || cfg->heads < 1) return LTK_ERR_ARG;
   if (cfg->num_pages > INT_MAX || cfg->heads > 65535) return LTK_ERR_ARG;
   if (cfg->page != 16 && cfg->page != 32 && cfg->page != 64 && cfg->page != 128) return LTK_ERR_UNSUPPORTED;
+  // a code row's number is 32 bits in the kernels (more rows than that do not fit the device)
+  if (cfg->num_pages * cfg->heads > 0xFFFFFFFEll / cfg->page) return LTK_ERR_UNSUPPORTED;
   if (cfg->dim != 64 && cfg->dim != 128) return LTK_ERR_UNSUPPORTED;
   if (!kv_aligned(cfg->k_codes) || !kv_aligned(cfg->v_codes)) return LTK_ERR_ARG;
   if (!kv_aligned(cfg->k_scale) || !kv_aligned(cfg->v_scale)) return LTK_ERR_ARG;
@@ -82,7 +84,7 @@ ltk_status ltk_kv_create(const ltk_kv_config* cfg, ltk_kv** out) {
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
   const size_t part_floats = std::max(kv_rows_part_floats(h->num_sms), kv_tile_part_floats(h->num_sms));
-  const size_t counters = static_cast<size_t>(kv_rows_counters(h->num_sms)) * 4;
+  const size_t counters = static_cast<size_t>(std::max(kv_rows_counters(h->num_sms), kv_tile_counters(h->num_sms))) * 4;
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part), part_floats * 4);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->counters), counters);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->status), 4);

@@ -155,6 +155,7 @@ cudaError_t launch_kv_rows(const AttnParams& p, int num_sms, cudaStream_t stream
 
 // Attention for many rows per KV head, on the tensor cores (k_kv_tile.cu).
 size_t kv_tile_part_floats(int num_sms);
+int kv_tile_counters(int num_sms);
 cudaError_t kv_tile_init();
 cudaError_t launch_kv_tile(const AttnParams& p, int max_q, int num_sms, cudaStream_t stream);
 
