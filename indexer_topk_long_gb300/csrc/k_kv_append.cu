@@ -107,15 +107,15 @@ __device__ __forceinline__ uint2 rescale_codes(uint2 w, float by) {
   uint32_t in[2] = {w.x, w.y}, out[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint32_t r = 0;
+    uint32_t h[2];
+    e4m3x4_to_f16(in[i], h[0], h[1]);
+    out[i] = 0;
 #pragma unroll
     for (int hlf = 0; hlf < 2; ++hlf) {
-      const uint32_t h2 = e4m3x2_to_f16x2((in[i] >> (16 * hlf)) & 0xFFFFu);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-      r |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f.x * by, f.y * by), __NV_SATFINITE, __NV_E4M3))
-           << (16 * hlf);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[hlf]));
+      out[i] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(f.x * by, f.y * by), __NV_SATFINITE, __NV_E4M3))
+                << (16 * hlf);
     }
-    out[i] = r;
   }
   return make_uint2(out[0], out[1]);
 }

@@ -457,8 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
         const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          mma_f16(s[0], qf[half * 4 + i], e4m3x2_to_f16x2(aw[i] & 0xFFFFu), e4m3x2_to_f16x2(aw[i] >> 16));
-          mma_f16(s[1], qf[half * 4 + i], e4m3x2_to_f16x2(bw[i] & 0xFFFFu), e4m3x2_to_f16x2(bw[i] >> 16));
+          uint32_t a0, a1, b0, b1;
+          e4m3x4_to_f16(aw[i], a0, a1);
+          e4m3x4_to_f16(bw[i], b0, b1);
+          mma_f16(s[0], qf[half * 4 + i], a0, a1);
+          mma_f16(s[1], qf[half * 4 + i], b0, b1);
         }
       }
       // element e of s[n]: row g + 8 (e >> 1), key 2 cq + (e & 1) + 8 n
@@ -557,10 +560,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
         const uint32_t x[4] = {vw[0][w], vw[1][w], vw[2][w], vw[3][w]};
         const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), a23 = __byte_perm(x[0], x[1], 0x7362);
         const uint32_t b01 = __byte_perm(x[2], x[3], 0x5140), b23 = __byte_perm(x[2], x[3], 0x7362);
-        mma_f16(o[w * 4], pf, e4m3x2_to_f16x2(a01 & 0xFFFFu), e4m3x2_to_f16x2(b01 & 0xFFFFu));
-        mma_f16(o[w * 4 + 1], pf, e4m3x2_to_f16x2(a01 >> 16), e4m3x2_to_f16x2(b01 >> 16));
-        mma_f16(o[w * 4 + 2], pf, e4m3x2_to_f16x2(a23 & 0xFFFFu), e4m3x2_to_f16x2(b23 & 0xFFFFu));
-        mma_f16(o[w * 4 + 3], pf, e4m3x2_to_f16x2(a23 >> 16), e4m3x2_to_f16x2(b23 >> 16));
+        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+        e4m3x4_to_f16(a01, a0, a1);
+        e4m3x4_to_f16(a23, a2, a3);
+        e4m3x4_to_f16(b01, b0, b1);
+        e4m3x4_to_f16(b23, b2, b3);
+        mma_f16(o[w * 4], pf, a0, b0);
+        mma_f16(o[w * 4 + 1], pf, a1, b1);
+        mma_f16(o[w * 4 + 2], pf, a2, b2);
+        mma_f16(o[w * 4 + 3], pf, a3, b3);
       }
     }
 

@@ -17,10 +17,10 @@
 //   solo mode:  one row tile, the streams take alternate key tiles and their
 //               results are merged at the end.  With at most 64 rows the tile
 //               holds them twice, so the streams' threads sit on different schedulers.
-// Roles: warps 0-3 and 4-7 softmax, 8-11 loader (codes from global memory through
-// registers, e4m3 to f16, 128-byte-swizzled shared memory; a listed key is as good
-// as a paged one), warp 12 issues the MMAs, warp 13 walks the CTA's work, warps 14
-// and 15 bring the queries.
+// Roles: warps 0-3 and 4-7 softmax, 8-11 key loader, 12-15 value loader (codes from
+// global memory through registers, e4m3 to f16, 128-byte-swizzled shared memory; a
+// listed key is as good as a paged one), warp 16 issues the MMAs, warp 17 walks the
+// CTA's work, warps 18 and 19 bring the queries.
 // Work: all units' key tiles form one line, cut into equal pieces, one per CTA; a
 // unit cut by a border is merged by the last of its CTAs in a fixed order.
 #include "kv_internal.cuh"
@@ -30,10 +30,11 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;
-constexpr int kThreads = 16 * 32;
-// Registers a thread: 128 at launch, moved from the last warpgroup to the others.
-constexpr int kRegsMain = 136, kRegsRest = 104;
-static_assert(3 * kRegsMain + kRegsRest == 4 * 128, "register split");
+constexpr int kThreads = 20 * 32;
+constexpr int kLoaders = 4;              // warps for each operand, 32 keys of a tile each
+// Registers a thread: 96 at launch, moved from the loaders and the last warpgroup to the softmax.
+constexpr int kRegsSoftmax = 120, kRegsLoad = 72, kRegsRest = 96;
+static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsRest <= 5 * 96, "register split");
 constexpr float kMinusHuge = -1e30f;
 constexpr float kBoost = 8.f;            // as in the kernel for few rows
 constexpr float kSlack = 7.f;
@@ -98,11 +99,26 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// MMAs are issued by one lane that elect.sync picks.  Behind elect.sync the compiler
+// keeps descriptors in uniform registers and an MMA costs four instructions; behind
+// `lane == 0` it moved each operand there first, and with busy softmax warps on the
+// scheduler a 128-cube took 780 to 2800 cycles to issue instead of 513 to 590.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
 
@@ -144,17 +160,13 @@ __device__ __forceinline__ void tmem_st32f(uint32_t a, const float (&v)[32]) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Descriptor of the value operand: rows of 128 bytes hold 64 consecutive d of one
-// key (N contiguous), 8-row atoms 1024 bytes apart along the keys (stride offset),
-// 128-byte-wide halves `lead` bytes apart along d (leading offset).
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(lead >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
+// Descriptor of an operand in 128-byte-swizzled rows (8-row atoms 1024 bytes apart).
+// Scores' operands have the contraction contiguous (leading offset unused); the value
+// operand's rows of 128 bytes hold 64 consecutive d of one key (N contiguous), and its
+// 128-byte-wide halves lie `lead` bytes apart along d.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t lead) {
+  return static_cast<uint64_t>(((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16)) |
+         (static_cast<uint64_t>((1024u >> 4) | (1u << 14) | (2u << 29)) << 32);
 }
 // f16 operands, fp32 result; the second operand with N contiguous when b_mn.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
@@ -231,45 +243,17 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
 }
 
 // --- loader ---------------------------------------------------------------------------------
-// Thread mapping of a 128-key tile: warp w holds rows 32 w .. 32 w + 31 (two whole
+// Thread mapping of an operand's 128-key tile: warp w holds the keys 32 w .. (two
 // 16-key groups); a lane's NI rows and its 16-byte chunk of codes are chosen so that
 // a quarter warp's 16-byte shared stores fall on distinct banks (two rows of
-// different parity, four chunks).
+// different parity, four chunks).  Row i is row 0 plus kStep * i.
 template <int D>
 struct Map {
   static constexpr int NI = D == 128 ? 8 : 4;
-  static __device__ __forceinline__ int row(int lane, int i) {
-    return D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) + 4 * i : (lane >> 2) + 8 * i;
-  }
+  static constexpr int kStep = 32 / NI;
+  static __device__ __forceinline__ int row0(int lane) { return D == 128 ? (lane >> 4) * 2 + ((lane >> 2) & 1) : lane >> 2; }
   static __device__ __forceinline__ int chunk(int lane) { return D == 128 ? (lane & 3) + 4 * ((lane >> 3) & 1) : lane & 3; }
 };
-
-// 16 codes to two swizzled 16-byte chunks of f16 (by != 0: times an f16x2 factor).
-template <int D, bool SCALED>
-__device__ __forceinline__ void store_codes(uint32_t base, int row, int chunk, const uint4& codes, __half2 by) {
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[2 * i] = e4m3x2_to_f16x2(w[i] & 0xFFFFu);
-    h[2 * i + 1] = e4m3x2_to_f16x2(w[i] >> 16);
-  }
-  if constexpr (SCALED) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), by);
-      h[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-  }
-  const uint32_t line = base + (chunk >> 2) * (kKeys * 128) + row * 128;
-  const int c0 = (2 * chunk) & 7;
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(line + ((c0 ^ (row & 7)) << 4)), "r"(h[0]), "r"(h[1]), "r"(h[2]),
-               "r"(h[3])
-               : "memory");
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(line + (((c0 + 1) ^ (row & 7)) << 4)), "r"(h[4]), "r"(h[5]),
-               "r"(h[6]), "r"(h[7])
-               : "memory");
-}
 
 __device__ __forceinline__ int tile_of(const Unit& u, int ord) { return ord < u.skip ? ord : ord - u.skip + u.tile0; }
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;
@@ -277,7 +261,7 @@ constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 // Listed keys come from blocks of different scales: the codes are multiplied by
 // 64 * scale / (largest scale of the 16-key group), exact in f16 for ratios down
 // to 2^-21 (an e4m3 code is a multiple of 2^-9, f16's smallest step 2^-24).
-// s: this lane's row's scale; returns the group's (its lanes are 16 apart).
+// s: this lane's row's scale; returns its group's.
 __device__ __forceinline__ float group_scale(float s) {
   float m = fmaxf(s, 0.f);               // a NaN (page outside the pool) counts as 0
 #pragma unroll
@@ -285,24 +269,35 @@ __device__ __forceinline__ float group_scale(float s) {
   return m > 0.f ? m : 1.f;
 }
 
-// A warp's 32 rows of codes to registers; row[i]: the lane's i-th row's place in the cache.
-template <int D>
-__device__ __forceinline__ void load_rows(const uint8_t* codes, const uint32_t (&row)[Map<D>::NI], int lane, uint4 (&x)[Map<D>::NI]) {
-#pragma unroll
-  for (int i = 0; i < Map<D>::NI; ++i) {
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (row[i] != kNoRow)
-      x[i] = __ldg(reinterpret_cast<const uint4*>(codes + static_cast<size_t>(row[i]) * D) + Map<D>::chunk(lane));
-  }
+// Codes pass the little L1 that the operands leave: page tables and indices stay in it.
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
+
+// A warp's 32 rows of codes (16 a lane and row) to swizzled f16 rows.  at: the lane's
+// place of row 0's first chunk of f16 in the operand; rows kStep apart lie kStep * 128
+// bytes apart, and their swizzle differs in one bit where kStep is 4.
 template <int D, bool SEL>
-__device__ __forceinline__ void store_rows(uint32_t base, int w, int lane, const uint4 (&x)[Map<D>::NI], uint32_t factor) {
+__device__ __forceinline__ void store_rows(uint32_t at, int lane, const uint4 (&x)[Map<D>::NI], uint32_t factor) {
 #pragma unroll
   for (int i = 0; i < Map<D>::NI; ++i) {
-    const int r = Map<D>::row(lane, i);
-    uint32_t by = 0;
-    if constexpr (SEL) by = __shfl_sync(0xFFFFFFFFu, factor, r);
-    store_codes<D, SEL>(base, 32 * w + r, Map<D>::chunk(lane), x[i], *reinterpret_cast<const __half2*>(&by));
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t h[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) e4m3x4_to_f16(w[e], h[2 * e], h[2 * e + 1]);
+    if constexpr (SEL) {
+      const uint32_t by = __shfl_sync(0xFFFFFFFFu, factor, Map<D>::row0(lane) + Map<D>::kStep * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[e]), *reinterpret_cast<const __half2*>(&by));
+        h[e] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    const uint32_t to = (at ^ ((Map<D>::kStep * i & 7) << 4)) + Map<D>::kStep * i * 128;
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to ^ 16u), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
   }
 }
 
@@ -397,24 +392,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + S::kQ + 2 * S::kStage + S::kMerge);
   const uint32_t q_sm = smem_u32(smem), stage_sm = q_sm + S::kQ;
   float* merge = reinterpret_cast<float*>(smem + S::kQ + 2 * S::kStage);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // uniform
   const AttnParams& a = p.a;
   const bool pair = p.pair != 0;
   volatile int* abort_flag = &ctrl->abort_flag;
   int* status = a.status;
 
-  if (warp == 12) {
+  if (warp == 16) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
-        mbar_init(smem_u32(&ctrl->kfull[i]), 4);
+        mbar_init(smem_u32(&ctrl->kfull[i]), kLoaders);
         mbar_init(smem_u32(&ctrl->kempty[i]), 1);
-        mbar_init(smem_u32(&ctrl->vfull[i]), 4);
+        mbar_init(smem_u32(&ctrl->vfull[i]), kLoaders);
         mbar_init(smem_u32(&ctrl->vempty[i]), 1);
         mbar_init(smem_u32(&ctrl->sfull[i]), 2);
         mbar_init(smem_u32(&ctrl->pfull[i]), 4);
         mbar_init(smem_u32(&ctrl->ofull[i]), 1);
         mbar_init(smem_u32(&ctrl->ufull[i]), 1);
-        mbar_init(smem_u32(&ctrl->uempty[i]), 8 + 4 + 2 + 2);
+        mbar_init(smem_u32(&ctrl->uempty[i]), 8 + 2 * kLoaders + 2 + 2);
         mbar_init(smem_u32(&ctrl->qfull[i]), 2);
         mbar_init(smem_u32(&ctrl->wg[i]), 128);
       }
@@ -501,9 +496,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem;
 
-  if (warp >= 12) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == 13) {
+    if (warp == 17) {
       // ================= the CTA's pieces, one after the other =================
       if (lane == 0) {
         long long at = ctrl->at, left = ctrl->left;
@@ -558,21 +553,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
           if (u.n_tiles < 0) break;
         }
       }
-    } else if (warp >= 14) {
+    } else if (warp >= 18) {
       // ================= queries =================
       for (int un = 0;; ++un) {
         const int us = un & 1;
         if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
-        const Unit u = ctrl->unit[us];
+        const Unit& u = ctrl->unit[us];
         if (u.n_tiles < 0) break;
         if (u.n_tiles > 0) {
           if (pair) {
             if (un >= 1 && !mbar_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
-            load_queries<D>(p, u, q_sm, ctrl->rowf + us * 256, 0, 127, warp - 14, lane);
+            load_queries<D>(p, u, q_sm, ctrl->rowf + us * 256, 0, 127, warp - 18, lane);
             if (u.rows > kTileRows)
-              load_queries<D>(p, u, q_sm + S::kOperand, ctrl->rowf + us * 256 + 128, kTileRows, 127, warp - 14, lane);
+              load_queries<D>(p, u, q_sm + S::kOperand, ctrl->rowf + us * 256 + 128, kTileRows, 127, warp - 18, lane);
           } else {
-            load_queries<D>(p, u, q_sm + us * S::kOperand, ctrl->rowf + us * 128, 0, u.rows <= 64 ? 63 : 127, warp - 14, lane);
+            load_queries<D>(p, u, q_sm + us * S::kOperand, ctrl->rowf + us * 128, 0, u.rows <= 64 ? 63 : 127, warp - 18, lane);
           }
           fence_async_smem();
         }
@@ -582,24 +577,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
           mbar_arrive(smem_u32(&ctrl->uempty[us]));
         }
       }
-    } else if (lane == 0) {
+    } else if (elect_one()) {
       // ================= MMA issue =================
+      auto commit = [&](uint64_t* bar) { tc_commit(smem_u32(bar)); };
+      auto arrive = [&](uint64_t* bar) { mbar_arrive(smem_u32(bar)); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(smem_u32(bar), parity, abort_flag, status); };
+      auto test = [&](uint64_t* bar, uint32_t parity) { return mbar_test(smem_u32(bar), parity); };
       constexpr uint32_t id_qk = idesc_f16(kTileRows, kKeys, false), id_pv = idesc_f16(kTileRows, D, true);
       auto qk = [&](int x, uint32_t q_tile, int st) {
+        const uint64_t q_d = operand_desc(q_tile, 16), k_d = operand_desc(stage_sm + st * S::kStage, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (kTileRows * 128) + (k & 3) * 32;
-          tc_mma<false>(tmem + x * kKeys, smem_desc_sw128(q_tile + off), smem_desc_sw128(stage_sm + st * S::kStage + off), id_qk,
-                        k > 0);
+          const uint32_t off = ((k >> 2) * (kTileRows * 128) + (k & 3) * 32) >> 4;
+          mma_ss(tmem + x * kKeys, q_d + off, k_d + off, id_qk, k > 0);
         }
-        tc_commit(smem_u32(&ctrl->sfull[x]));
-        mbar_arrive(smem_u32(&ctrl->sfull[x]));   // passes on what the loader wrote beside K
+        commit(&ctrl->sfull[x]);
+        arrive(&ctrl->sfull[x]);         // passes on what the loader wrote beside K
       };
       auto pv = [&](int x, int st, bool first) {
-        const uint32_t v = stage_sm + st * S::kStage + S::kOperand;
+        const uint64_t v_d = operand_desc(stage_sm + st * S::kStage + S::kOperand, kKeys * 128);
+        const uint32_t d = tmem + 256 + x * D, w = tmem + x * kKeys;
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + 256 + x * D, tmem + x * kKeys + k * 8, desc_mn(v + k * 2048, kKeys * 128), id_pv, !first || k > 0);
+        for (int k = 0; k < kKeys / 16; ++k) mma_ts(d, w + k * 8, v_d + k * (2048 >> 4), id_pv, !first || k > 0);
       };
       if (pair) {
         int c = 0, nu = 0;
@@ -607,49 +606,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         bool ok = true;
         while (ok) {
           const int us = nu & 1;
-          if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (nu >> 1) & 1, abort_flag, status)) break;
+          if (!wait(&ctrl->ufull[us], (nu >> 1) & 1)) break;
           const int n = ctrl->unit[us].n_tiles;
           const bool two = ctrl->unit[us].rows > kTileRows;
           if (n < 0) break;
-          if (!mbar_wait(smem_u32(&ctrl->qfull[us]), (nu >> 1) & 1, abort_flag, status)) break;
+          if (!wait(&ctrl->qfull[us], (nu >> 1) & 1)) break;
           ++nu;
           if (n > 0) {
-            if (!mbar_wait(smem_u32(&ctrl->kfull[c & 1]), (c >> 1) & 1, abort_flag, status)) break;
+            if (!wait(&ctrl->kfull[c & 1], (c >> 1) & 1)) break;
             tc_fence_after();
             qk(0, q_sm, c & 1);
             if (two) qk(1, q_sm + S::kOperand, c & 1);
-            tc_commit(smem_u32(&ctrl->kempty[c & 1]));
+            commit(&ctrl->kempty[c & 1]);
             for (int i = 0; i < n && ok; ++i, ++c) {
               const int st = c & 1, ns = (c + 1) & 1;
               const bool next = i + 1 < n;
-              if (!mbar_wait(smem_u32(&ctrl->vfull[st]), (c >> 1) & 1, abort_flag, status) ||
-                  !mbar_wait(smem_u32(&ctrl->pfull[0]), sp[0] & 1, abort_flag, status)) { ok = false; break; }
+              if (!wait(&ctrl->vfull[st], (c >> 1) & 1) ||
+                  !wait(&ctrl->pfull[0], sp[0] & 1)) { ok = false; break; }
               ++sp[0];
               tc_fence_after();
               pv(0, st, i == 0);
-              if (!next) tc_commit(smem_u32(&ctrl->ofull[0]));
+              if (!next) commit(&ctrl->ofull[0]);
               if (next) {
-                if (!mbar_wait(smem_u32(&ctrl->kfull[ns]), ((c + 1) >> 1) & 1, abort_flag, status)) { ok = false; break; }
+                if (!wait(&ctrl->kfull[ns], ((c + 1) >> 1) & 1)) { ok = false; break; }
                 tc_fence_after();
                 qk(0, q_sm, ns);
               }
               if (two) {
-                if (!mbar_wait(smem_u32(&ctrl->pfull[1]), sp[1] & 1, abort_flag, status)) { ok = false; break; }
+                if (!wait(&ctrl->pfull[1], sp[1] & 1)) { ok = false; break; }
                 ++sp[1];
                 tc_fence_after();
                 pv(1, st, i == 0);
               }
-              tc_commit(smem_u32(&ctrl->vempty[st]));
+              commit(&ctrl->vempty[st]);
               if (two && next) qk(1, q_sm + S::kOperand, ns);
-              if (two && !next) tc_commit(smem_u32(&ctrl->ofull[1]));
-              if (next) tc_commit(smem_u32(&ctrl->kempty[ns]));
+              if (two && !next) commit(&ctrl->ofull[1]);
+              if (next) commit(&ctrl->kempty[ns]);
             }
-            tc_commit(smem_u32(&ctrl->qempty));
+            commit(&ctrl->qempty);
           } else {
-            mbar_arrive(smem_u32(&ctrl->qempty));
+            arrive(&ctrl->qempty);
           }
-          mbar_arrive(smem_u32(&ctrl->uempty[us]));
-          mbar_arrive(smem_u32(&ctrl->uempty[us]));
+          arrive(&ctrl->uempty[us]);
+          arrive(&ctrl->uempty[us]);
         }
       } else {
         // Each stream walks its own key tiles through the units.  Neither may hold up the
@@ -665,25 +664,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
           for (int x = 0; x < 2; ++x) {
             if (done[x]) continue;
             if (pending[x]) {
-              if (!mbar_test(smem_u32(&ctrl->pfull[x]), cnt[x] & 1) || !mbar_test(smem_u32(&ctrl->vfull[x]), cnt[x] & 1)) continue;
+              if (!test(&ctrl->pfull[x], cnt[x] & 1) || !test(&ctrl->vfull[x], cnt[x] & 1)) continue;
               tc_fence_after();
               pv(x, x, fresh[x]);
               fresh[x] = 0;
-              tc_commit(smem_u32(&ctrl->vempty[x]));
+              commit(&ctrl->vempty[x]);
               pending[x] = false;
               progress = true;
               ++cnt[x];
               if (--left[x] == 0) {
-                tc_commit(smem_u32(&ctrl->ofull[x]));
-                tc_commit(smem_u32(&ctrl->uempty[cu[x] & 1]));
+                commit(&ctrl->ofull[x]);
+                commit(&ctrl->uempty[cu[x] & 1]);
                 ++cu[x];
               }
             }
             while (left[x] == 0) {       // the stream's next unit with a tile for it
               const int us = cu[x] & 1;
-              if (!mbar_test(smem_u32(&ctrl->ufull[us]), (cu[x] >> 1) & 1)) break;
+              if (!test(&ctrl->ufull[us], (cu[x] >> 1) & 1)) break;
               const int n = ctrl->unit[us].n_tiles;
-              if (n >= 0 && !mbar_test(smem_u32(&ctrl->qfull[us]), (cu[x] >> 1) & 1)) break;
+              if (n >= 0 && !test(&ctrl->qfull[us], (cu[x] >> 1) & 1)) break;
               progress = true;
               if (n < 0) {
                 done[x] = true;
@@ -692,14 +691,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
               left[x] = x == 0 ? (n + 1) >> 1 : n >> 1;
               fresh[x] = 1;
               if (left[x] == 0) {
-                mbar_arrive(smem_u32(&ctrl->uempty[us]));
+                arrive(&ctrl->uempty[us]);
                 ++cu[x];
               }
             }
-            if (left[x] == 0 || !mbar_test(smem_u32(&ctrl->kfull[x]), cnt[x] & 1)) continue;
+            if (left[x] == 0 || !test(&ctrl->kfull[x], cnt[x] & 1)) continue;
             tc_fence_after();
             qk(x, q_sm + (cu[x] & 1) * S::kOperand, x);
-            tc_commit(smem_u32(&ctrl->kempty[x]));
+            commit(&ctrl->kempty[x]);
             pending[x] = true;
             progress = true;
           }
@@ -717,21 +716,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         }
       }
       // every MMA issued has finished before the tensor memory is given back
-      tc_commit(smem_u32(&ctrl->drained));
+      commit(&ctrl->drained);
       mbar_drain(smem_u32(&ctrl->drained), 0);
     }
     __syncwarp();
   } else if (warp >= 8) {
-    // ================= loader =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMain));
-    const int w = warp - 8;
+    // ================= loaders =================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    const bool values = warp >= 8 + kLoaders;
+    const int w = (warp - 8) & (kLoaders - 1);
     const KvCache& c = a.cache;
+    const uint8_t* codes = values ? c.v_codes : c.k_codes;
+    uint64_t* full = values ? ctrl->vfull : ctrl->kfull;
+    uint64_t* empty = values ? ctrl->vempty : ctrl->kempty;
+    const int lrow = Map<D>::row0(lane), lchunk = Map<D>::chunk(lane);
+    const uint32_t at0 = stage_sm + (values ? S::kOperand : 0) + (lchunk >> 2) * (kKeys * 128) + (32 * w + lrow) * 128 +
+                         ((((2 * lchunk) & 7) ^ (lrow & 7)) << 4);
     int cnt[2] = {0, 0};                 // tiles loaded by stream (pair mode: [0] counts all)
     bool ok = true;
     for (int un = 0; ok; ++un) {
       const int us = un & 1;
       if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
-      const Unit u = ctrl->unit[us];
+      const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
       const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width;
       const int end = u.first + u.n_tiles;
@@ -744,61 +750,78 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         return key <= u.pos0 ? max(key, -1) : -1;
       };
       auto page_of = [&](int key) { return key >= 0 ? __ldg(table + (key >> c.page_log2)) : -1; };
-      int key1 = -1, page1 = -1, page1b = -1, key2 = -1;
-      float ks = 1.f, vs = 1.f;          // listed: the lane's row; dense: lanes 0, 1 the groups
-      bool valid = false;
-      uint32_t row[NI];
-      // places and scales of tile `ord` from its lookups (listed: key1, page1; dense: page1, page1b)
-      auto place_tile = [&](int ord, float& k_sc, float& v_sc, bool& live) {
+      int key1 = -1, page1 = -1, page2 = -1, key2 = -1;
+      auto look = [&](int ord) {         // dense: pages of tile `ord`'s groups
+        const int key = tile_of(u, ord) * kKeys + 32 * w;
+        page1 = ord < end && key < u.len ? __ldg(table + (key >> c.page_log2)) : -1;
+        page2 = ord < end && key + 16 < u.len ? __ldg(table + ((key + 16) >> c.page_log2)) : -1;
+      };
+      // Where a tile's rows are: listed, the lane's row; dense, the groups' first rows and
+      // how many of the 32 there are.
+      struct Place {
+        uint32_t row, row2;
+        int rows;
+        float ks, vs;                    // listed: the lane's row's; dense: group (lane & 1)'s
+        bool listed;
+      };
+      auto place_tile = [&](int ord) {
+        Place t{kNoRow, kNoRow, 0, 0.f, 0.f, false};
         if constexpr (SEL) {
-          uint32_t mine = kNoRow;
-          live = key1 >= 0;
-          k_sc = v_sc = 0.f;
-          if (live) {
+          t.listed = key1 >= 0;
+          if (t.listed) {
             if (page1 >= 0 && page1 < c.num_pages) {
               const uint32_t blk = static_cast<uint32_t>(page1) * c.heads + u.head;
-              mine = blk * c.page + (key1 & (c.page - 1));
-              k_sc = __ldg(c.k_scale + blk);
-              v_sc = __ldg(c.v_scale + blk);
+              t.row = blk * c.page + (key1 & (c.page - 1));
+              t.ks = __ldg(c.k_scale + blk);
+              t.vs = __ldg(c.v_scale + blk);
             } else {
               raise_status(status, kDevArg);
-              k_sc = __int_as_float(0x7FC00000);
+              t.ks = __int_as_float(0x7FC00000);
             }
           }
-#pragma unroll
-          for (int i = 0; i < NI; ++i) row[i] = __shfl_sync(0xFFFFFFFFu, mine, Map<D>::row(lane, i));
         } else {
           const int key = tile_of(u, ord) * kKeys + 32 * w;
-          uint32_t blk[2];
-          bool known[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int pg = h ? page1b : page1;
-            known[h] = pg >= 0 && pg < c.num_pages;
-            blk[h] = known[h] ? static_cast<uint32_t>(pg) * c.heads + u.head : 0;
-            if (!known[h] && key + 16 * h < u.len) raise_status(status, kDevArg);
-          }
+          t.rows = u.len - key;
+          const bool known1 = page1 >= 0 && page1 < c.num_pages, known2 = page2 >= 0 && page2 < c.num_pages;
+          const uint32_t b1 = known1 ? static_cast<uint32_t>(page1) * c.heads + u.head : 0;
+          const uint32_t b2 = known2 ? static_cast<uint32_t>(page2) * c.heads + u.head : 0;
+          if (known1) t.row = b1 * c.page + (key & (c.page - 1));
+          if (known2) t.row2 = b2 * c.page + ((key + 16) & (c.page - 1));
           const int h = lane & 1;
-          const bool kn = h ? known[1] : known[0];
-          const uint32_t bk = h ? blk[1] : blk[0];
-          k_sc = kn ? __ldg(c.k_scale + bk) : key + 16 * h < u.len ? __int_as_float(0x7FC00000) : 1.f;
-          v_sc = kn ? __ldg(c.v_scale + bk) : 1.f;
+          t.ks = t.vs = 1.f;
+          if (h ? known2 : known1) {
+            t.ks = __ldg(c.k_scale + (h ? b2 : b1));
+            t.vs = __ldg(c.v_scale + (h ? b2 : b1));
+          } else if (key + 16 * h < u.len) {
+            raise_status(status, kDevArg);
+            t.ks = __int_as_float(0x7FC00000);
+          }
+        }
+        return t;
+      };
+      uint4 x[NI];
+      auto load_tile = [&](const Place& t) {
+        if constexpr (SEL) {
 #pragma unroll
           for (int i = 0; i < NI; ++i) {
-            constexpr int kPer = NI / 2;
-            const int at = key + Map<D>::row(lane, i);
-            row[i] = known[i / kPer] && at < u.len ? blk[i / kPer] * c.page + (at & (c.page - 1)) : kNoRow;
+            const uint32_t r = __shfl_sync(0xFFFFFFFFu, t.row, lrow + Map<D>::kStep * i);
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r != kNoRow) x[i] = load_codes(codes + static_cast<size_t>(r) * D + lchunk * 16);
+          }
+        } else {
+          const uint8_t* p1 = codes + (static_cast<size_t>(t.row) + lrow) * D + lchunk * 16;
+          const uint8_t* p2 = codes + (static_cast<size_t>(t.row2) + lrow) * D + lchunk * 16;
+          const int n1 = t.row != kNoRow ? t.rows - lrow : 0, n2 = t.row2 != kNoRow ? t.rows - lrow : 0;
+#pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int r = Map<D>::kStep * i;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r < (i < NI / 2 ? n1 : n2))
+              x[i] = load_codes((i < NI / 2 ? p1 : p2) + (i < NI / 2 ? r : r - 16) * D);
           }
         }
       };
-      auto look = [&](int ord) {         // dense: pages of tile `ord`
-        if constexpr (!SEL) {
-          const int key = tile_of(u, ord) * kKeys + 32 * w;
-          page1 = ord < end && key < u.len ? __ldg(table + (key >> c.page_log2)) : -1;
-          page1b = ord < end && key + 16 < u.len ? __ldg(table + ((key + 16) >> c.page_log2)) : -1;
-        }
-      };
-      uint4 kx[NI], vx[NI];
+      Place cur{};
       if (u.n_tiles > 0) {
         if constexpr (SEL) {
           key1 = key_of(u.first);
@@ -807,9 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         } else {
           look(u.first);
         }
-        place_tile(u.first, ks, vs, valid);
-        load_rows<D>(c.k_codes, row, lane, kx);
-        load_rows<D>(c.v_codes, row, lane, vx);
+        cur = place_tile(u.first);
+        load_tile(cur);
         if constexpr (SEL) {
           key1 = key2;
           page1 = page_of(key1);
@@ -820,45 +842,42 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
       }
 #pragma unroll 1
       for (int ord = u.first; ord < end; ++ord) {
-        const bool next = ord + 1 < end;
-        const int x = pair ? 0 : (ord - u.first) & 1;
-        const int n = cnt[x];
-        const int st = pair ? n & 1 : x, use = pair ? n >> 1 : n;
-        Meta& m = ctrl->meta[pair ? n & 3 : x * 2 + (n & 1)];
-        float ks1 = 1.f, vs1 = 1.f;
-        bool valid1 = false;
-        if (next) place_tile(ord + 1, ks1, vs1, valid1);
-        uint32_t k_by = 0, v_by = 0;
-        float kg = ks, vg = vs;
+        const int sx = pair ? 0 : (ord - u.first) & 1;
+        const int n = cnt[sx];
+        const int st = pair ? n & 1 : sx, use = pair ? n >> 1 : n;
+        Place next{};
+        if (ord + 1 < end) next = place_tile(ord + 1);
+        uint32_t factor = 0;
+        float kg = cur.ks, vg = cur.vs;
         if constexpr (SEL) {
-          const float kt = group_scale(ks), vt = group_scale(vs);
-          const __half2 kh = __float2half2_rn(ks * (64.f / kt)), vh = __float2half2_rn(vs * (64.f / vt));
-          k_by = *reinterpret_cast<const uint32_t*>(&kh);
-          v_by = *reinterpret_cast<const uint32_t*>(&vh);
-          kg = kt * (1.f / 64.f);
-          vg = vt * (1.f / 64.f);
-        }
-        if (use > 0 && !mbar_wait(smem_u32(&ctrl->kempty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
-        if constexpr (SEL) {
-          const uint32_t bits = __ballot_sync(0xFFFFFFFFu, valid);
-          if (lane == 0) m.valid[w] = bits;
-          if ((lane & 15) == 0) {
-            m.ks[2 * w + (lane >> 4)] = kg;
-            m.lv[2 * w + (lane >> 4)] = __log2f(vg) + kBoost;
-            m.iv[2 * w + (lane >> 4)] = __frcp_rn(vg);
-          }
-        } else {
-          if (lane < 2) {
-            m.ks[2 * w + lane] = kg;
-            m.lv[2 * w + lane] = __log2f(vg) + kBoost;
-            m.iv[2 * w + lane] = __frcp_rn(vg);
+          const float top = group_scale(values ? cur.vs : cur.ks);
+          const __half2 f2 = __float2half2_rn((values ? cur.vs : cur.ks) * (64.f / top));
+          factor = *reinterpret_cast<const uint32_t*>(&f2);
+          if (!values) {
+            kg = top * (1.f / 64.f);
+            vg = group_scale(cur.vs) * (1.f / 64.f);
           }
         }
-        store_rows<D, SEL>(stage_sm + st * S::kStage, w, lane, kx, k_by);
+        const float lv = __log2f(vg) + kBoost, iv = __frcp_rn(vg);
+        if (use > 0 && !mbar_wait(smem_u32(&empty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
+        if (!values) {                   // the tile's scales go with its keys
+          Meta& m = ctrl->meta[pair ? n & 3 : sx * 2 + (n & 1)];
+          if constexpr (SEL) {
+            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, cur.listed);
+            if (lane == 0) m.valid[w] = bits;
+          }
+          const int gi = SEL ? lane >> 4 : lane & 1;
+          if (SEL ? (lane & 15) == 0 : lane < 2) {
+            m.ks[2 * w + gi] = kg;
+            m.lv[2 * w + gi] = lv;
+            m.iv[2 * w + gi] = iv;
+          }
+        }
+        store_rows<D, SEL>(at0 + st * S::kStage, lane, x, factor);
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctrl->kfull[st]));
-        if (next) load_rows<D>(c.k_codes, row, lane, kx);
+        if (lane == 0) mbar_arrive(smem_u32(&full[st]));
+        if (ord + 1 < end) load_tile(next);
         if constexpr (SEL) {
           key1 = key2;
           page1 = page_of(key1);
@@ -866,16 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         } else {
           look(ord + 2);
         }
-        if (use > 0 && !mbar_wait(smem_u32(&ctrl->vempty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
-        store_rows<D, SEL>(stage_sm + st * S::kStage + S::kOperand, w, lane, vx, v_by);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctrl->vfull[st]));
-        if (next) load_rows<D>(c.v_codes, row, lane, vx);
-        ks = ks1;
-        vs = vs1;
-        valid = valid1;
-        ++cnt[x];
+        cur = next;
+        ++cnt[sx];
       }
       if (!ok) break;
       __syncwarp();
@@ -883,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
     }
   } else {
     // ================= softmax =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMain));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int x = warp >> 2;             // stream
     const int r = tid & 127;             // tensor-memory lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -894,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
     for (int un = 0;; ++un) {
       const int us = un & 1;
       if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
-      const Unit u = ctrl->unit[us];
+      const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
       if (!mbar_wait(smem_u32(&ctrl->qfull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const bool twice = !pair && u.rows <= 64;
@@ -921,48 +932,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
           } else {
             masked = !(key0 + kKeys - 1 <= u.p_lo && (a.window <= 0 || key0 > u.p_hi - a.window || key0 + kKeys <= a.sinks));
           }
-          bool slow = masked || i == 0;
-          if (!slow) {
-            // One pass with the maximum as it stands; weights stay in registers until it is
-            // known that none outgrew the slack.
-            uint32_t pk[64];
-            float mx = -inf;
-            float l1 = l;
+          // Columns from here on still want their weights: all when the tile is masked or the
+          // unit's first, else none, or those from where a weight outgrew the slack.
+          int from = masked || i == 0 ? 0 : 4;
+          if (from != 0) {
+            // One pass with the maximum as it stands, half a tile at a time; a half's weights
+            // stay in registers until it is known that none outgrew the slack (a group's sum
+            // bounds each of its weights), since they take the place of scores.
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float s[32];
-              tmem_ld32(s_col + 32 * c, s);
-              tmem_ld32_wait(s);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float fa = f * m.ks[2 * c + h], fb = m.lv[2 * c + h] - M;
-                const uint64_t fa2 = pack2(fa, fa), fb2 = pack2(fb, fb);
-                uint64_t sum = 0;
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  const float2 t = unpack2(fma2(pack2(s[16 * h + e], s[16 * h + e + 1]), fa2, fb2));
-                  mx = fmaxf(fmaxf(mx, t.x), t.y);
-                  const float w0 = exp2_approx(t.x), w1 = exp2_approx(t.y);
-                  sum = add2(sum, pack2(w0, w1));
-                  pk[16 * c + 8 * h + e / 2] = pack_f16(w0, w1);
-                }
-                const float2 sm = unpack2(sum);
-                l1 = fmaf(sm.x + sm.y, m.iv[2 * c + h], l1);
-              }
-            }
-            slow = __any_sync(0xFFFFFFFFu, mx > kBoost + kSlack);
-            if (!slow) {
-              l = l1;
+            for (int hf = 0; hf < 2; ++hf) {
+              uint32_t pk[32];
+              float s[2][16];
+              float l1 = l, most = 0.f;
+              tmem_ld32x16(s_col + 64 * hf, s[0]);
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
+                float (&v)[16] = s[c & 1];
+                tmem_wait_ld_tied(v);
+                if (c < 3) tmem_ld32x16(s_col + 64 * hf + 16 * (c + 1), s[(c + 1) & 1]);
+                const float fa = f * m.ks[4 * hf + c], fb = m.lv[4 * hf + c] - M;
+                const uint64_t fa2 = pack2(fa, fa), fb2 = pack2(fb, fb);
+                uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                  const float2 t0 = unpack2(fma2(pack2(v[e], v[e + 1]), fa2, fb2)), t1 = unpack2(fma2(pack2(v[e + 2], v[e + 3]), fa2, fb2));
+                  const float w0 = exp2_approx(t0.x), w1 = exp2_approx(t0.y), w2 = exp2_approx(t1.x), w3 = exp2_approx(t1.y);
+                  sum0 = add2(sum0, pack2(w0, w1));
+                  sum1 = add2(sum1, pack2(w2, w3));
+                  pk[8 * c + e / 2] = pack_f16(w0, w1);
+                  pk[8 * c + e / 2 + 1] = pack_f16(w2, w3);
+                }
+                const float2 sm = unpack2(add2(sum0, sum1));
+                most = fmaxf(most, sm.x + sm.y);
+                l1 = fmaf(sm.x + sm.y, m.iv[4 * hf + c], l1);
+              }
+              if (__any_sync(0xFFFFFFFFu, most > 32768.f)) {
+                from = 2 * hf;
+                break;
+              }
+              l = l1;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[e] = pk[16 * c + e];
-                tmem_st16(s_col + 16 * c, w);
+                tmem_st16(s_col + 32 * hf + 16 * c, w);
               }
             }
           }
-          if (slow) {
+          if (from < 4) {
             // this row's visible keys of 32 columns as bits
             auto seen_of = [&](int c) -> uint32_t {
               if (!masked) return 0xFFFFFFFFu;
@@ -977,19 +995,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
               }
             };
             float mx = -inf;
-            float s[32];
+            float s[16];
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(s_col + 32 * c, s);
-              const uint32_t seen = seen_of(c);
-              tmem_ld32_wait(s);
+            for (int c = 2 * from; c < 8; ++c) {
+              tmem_ld32x16(s_col + 16 * c, s);
+              const uint32_t seen = seen_of(c >> 1) >> (16 * (c & 1));
+              tmem_wait_ld_tied(s);
+              float g = -inf;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float g = -inf;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) g = fmaxf(g, (seen >> (16 * h + e)) & 1u ? s[16 * h + e] : -inf);
-                mx = fmaxf(mx, fmaf(g, f * m.ks[2 * c + h], m.lv[2 * c + h]));
-              }
+              for (int e = 0; e < 16; ++e) g = fmaxf(g, (seen >> e) & 1u ? s[e] : -inf);
+              mx = fmaxf(mx, fmaf(g, f * m.ks[c], m.lv[c]));
             }
             if (__any_sync(0xFFFFFFFFu, mx > M + (kBoost + kSlack))) {
               const float top = fmaxf(M, mx - kBoost);
@@ -998,37 +1013,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
               l *= by;
               if (i > 0) {               // scores are complete, so the last value product is too
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                  tmem_ld32(o_col + 32 * c, s);
-                  tmem_ld32_wait(s);
+                for (int c = 0; c < D / 16; ++c) {
+                  tmem_ld32x16(o_col + 16 * c, s);
+                  tmem_wait_ld_tied(s);
+                  uint32_t w[16];
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) s[e] *= by;
-                  tmem_st32f(o_col + 32 * c, s);
+                  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(s[e] * by);
+                  tmem_st16(o_col + 16 * c, w);
+                }
+              }
+              if (from != 0) {           // the first half's weights are there already
+                const __half2 by2 = __float2half2_rn(by);
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                  tmem_st_wait();
+                  tmem_ld32x16(s_col + 16 * c, s);
+                  tmem_wait_ld_tied(s);
+                  uint32_t w[16];
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const uint32_t x2 = __float_as_uint(s[e]);
+                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x2), by2);
+                    w[e] = *reinterpret_cast<const uint32_t*>(&v);
+                  }
+                  tmem_st16(s_col + 16 * c, w);
                 }
               }
             }
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(s_col + 32 * c, s);
-              const uint32_t seen = seen_of(c);
-              tmem_ld32_wait(s);
+            for (int c = 2 * from; c < 8; c += 2) {
               uint32_t pk[16];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float fa = f * m.ks[2 * c + h], fb = m.lv[2 * c + h] - M;
+                tmem_ld32x16(s_col + 16 * (c + h), s);
+                const uint32_t seen = seen_of(c >> 1) >> (16 * h);
+                const float fa = f * m.ks[c + h], fb = m.lv[c + h] - M;
+                tmem_wait_ld_tied(s);
                 float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) {
-                  const float s0 = (seen >> (16 * h + e)) & 1u ? fmaf(s[16 * h + e], fa, fb) : -inf;
-                  const float s1 = (seen >> (16 * h + e + 1)) & 1u ? fmaf(s[16 * h + e + 1], fa, fb) : -inf;
+                  const float s0 = (seen >> e) & 1u ? fmaf(s[e], fa, fb) : -inf;
+                  const float s1 = (seen >> (e + 1)) & 1u ? fmaf(s[e + 1], fa, fb) : -inf;
                   const float w0 = exp2_approx(s0), w1 = exp2_approx(s1);
                   sum0 += w0;
                   sum1 += w1;
                   pk[8 * h + e / 2] = pack_f16(w0, w1);
                 }
-                l = fmaf(sum0 + sum1, m.iv[2 * c + h], l);
+                l = fmaf(sum0 + sum1, m.iv[c + h], l);
               }
-              tmem_st16(s_col + 16 * c, pk);
+              tmem_st16(s_col + 8 * c, pk);
             }
           }
           tmem_st_wait();
@@ -1229,7 +1262,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -72,11 +72,11 @@ __device__ __forceinline__ size_t kv_row(const KvCache& c, long long page, int h
   return ((static_cast<size_t>(page) * c.heads + head) * c.page + off) * dim;
 }
 
-// Two e4m3 codes to two f16 values (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(two_codes));
-  return r;
+// Four e4m3 codes to four f16 values (exact), in order: lo holds the first two.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
 // 2^x, one MUFU instruction (2 ulp); 0 for -inf and for results below fp32's normal range.
