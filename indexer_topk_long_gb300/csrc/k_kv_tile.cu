@@ -741,20 +741,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
       if (u.n_tiles < 0) break;
       const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width;
       const int end = u.first + u.n_tiles;
-      // A tile's lookups run ahead of its data.  Listed: lane = row; position two tiles
-      // ahead, page and place one ahead.  Dense: the pages of the warp's two groups.
+      // A tile's lookups run ahead of its data, each a whole tile ahead of its use: its
+      // page (listed: first its key) is asked for two tiles before its codes are.
+      struct Look {
+        int key;                         // listed: lane's row's position
+        int page, page2;                 // listed: the row's page; dense: the warp's two groups'
+      };
       auto key_of = [&](int ord) {
         const int i = ord * kKeys + 32 * w + lane;
-        if (ord >= end || i >= a.k) return -1;
-        const int key = __ldg(a.idx + static_cast<size_t>(u.q0) * a.k + i);
-        return key <= u.pos0 ? max(key, -1) : -1;
+        return ord < end && i < a.k ? __ldg(a.idx + static_cast<size_t>(u.q0) * a.k + i) : -1;
       };
-      auto page_of = [&](int key) { return key >= 0 ? __ldg(table + (key >> c.page_log2)) : -1; };
-      int key1 = -1, page1 = -1, page2 = -1, key2 = -1;
-      auto look = [&](int ord) {         // dense: pages of tile `ord`'s groups
-        const int key = tile_of(u, ord) * kKeys + 32 * w;
-        page1 = ord < end && key < u.len ? __ldg(table + (key >> c.page_log2)) : -1;
-        page2 = ord < end && key + 16 < u.len ? __ldg(table + ((key + 16) >> c.page_log2)) : -1;
+      auto look = [&](int ord, int key) {
+        Look k{-1, -1, -1};
+        if constexpr (SEL) {
+          k.key = key <= u.pos0 ? key : -1;
+          if (k.key >= 0) k.page = __ldg(table + (k.key >> c.page_log2));
+        } else if (ord < end) {
+          const int first = tile_of(u, ord) * kKeys + 32 * w;
+          if (first < u.len) k.page = __ldg(table + (first >> c.page_log2));
+          if (first + 16 < u.len) k.page2 = __ldg(table + ((first + 16) >> c.page_log2));
+        }
+        return k;
       };
       // Where a tile's rows are: listed, the lane's row; dense, the groups' first rows and
       // how many of the 32 there are.
@@ -764,14 +771,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         float ks, vs;                    // listed: the lane's row's; dense: group (lane & 1)'s
         bool listed;
       };
-      auto place_tile = [&](int ord) {
+      auto place_tile = [&](int ord, const Look& k) {
         Place t{kNoRow, kNoRow, 0, 0.f, 0.f, false};
         if constexpr (SEL) {
-          t.listed = key1 >= 0;
+          t.listed = k.key >= 0;
           if (t.listed) {
-            if (page1 >= 0 && page1 < c.num_pages) {
-              const uint32_t blk = static_cast<uint32_t>(page1) * c.heads + u.head;
-              t.row = blk * c.page + (key1 & (c.page - 1));
+            if (k.page >= 0 && k.page < c.num_pages) {
+              const uint32_t blk = static_cast<uint32_t>(k.page) * c.heads + u.head;
+              t.row = blk * c.page + (k.key & (c.page - 1));
               t.ks = __ldg(c.k_scale + blk);
               t.vs = __ldg(c.v_scale + blk);
             } else {
@@ -782,9 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         } else {
           const int key = tile_of(u, ord) * kKeys + 32 * w;
           t.rows = u.len - key;
-          const bool known1 = page1 >= 0 && page1 < c.num_pages, known2 = page2 >= 0 && page2 < c.num_pages;
-          const uint32_t b1 = known1 ? static_cast<uint32_t>(page1) * c.heads + u.head : 0;
-          const uint32_t b2 = known2 ? static_cast<uint32_t>(page2) * c.heads + u.head : 0;
+          const bool known1 = k.page >= 0 && k.page < c.num_pages, known2 = k.page2 >= 0 && k.page2 < c.num_pages;
+          const uint32_t b1 = known1 ? static_cast<uint32_t>(k.page) * c.heads + u.head : 0;
+          const uint32_t b2 = known2 ? static_cast<uint32_t>(k.page2) * c.heads + u.head : 0;
           if (known1) t.row = b1 * c.page + (key & (c.page - 1));
           if (known2) t.row2 = b2 * c.page + ((key + 16) & (c.page - 1));
           const int h = lane & 1;
@@ -822,23 +829,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         }
       };
       Place cur{};
+      Look near{}, far{};                // of the next tile and the one after it
+      int far_key = -1;                  // listed: of the tile after those
       if (u.n_tiles > 0) {
+        int key = -1, near_key = -1, then_key = -1;
         if constexpr (SEL) {
-          key1 = key_of(u.first);
-          key2 = key_of(u.first + 1);
-          page1 = page_of(key1);
-        } else {
-          look(u.first);
+          key = key_of(u.first);
+          near_key = key_of(u.first + 1);
+          then_key = key_of(u.first + 2);
+          far_key = key_of(u.first + 3);
         }
-        cur = place_tile(u.first);
+        const Look first = look(u.first, key);
+        near = look(u.first + 1, near_key);
+        far = look(u.first + 2, then_key);
+        cur = place_tile(u.first, first);
         load_tile(cur);
-        if constexpr (SEL) {
-          key1 = key2;
-          page1 = page_of(key1);
-          key2 = key_of(u.first + 2);
-        } else {
-          look(u.first + 1);
-        }
       }
 #pragma unroll 1
       for (int ord = u.first; ord < end; ++ord) {
@@ -846,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         const int n = cnt[sx];
         const int st = pair ? n & 1 : sx, use = pair ? n >> 1 : n;
         Place next{};
-        if (ord + 1 < end) next = place_tile(ord + 1);
+        if (ord + 1 < end) next = place_tile(ord + 1, near);
         uint32_t factor = 0;
         float kg = cur.ks, vg = cur.vs;
         if constexpr (SEL) {
@@ -878,13 +883,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&full[st]));
         if (ord + 1 < end) load_tile(next);
-        if constexpr (SEL) {
-          key1 = key2;
-          page1 = page_of(key1);
-          key2 = key_of(ord + 3);
-        } else {
-          look(ord + 2);
-        }
+        near = far;
+        far = look(ord + 3, far_key);
+        if constexpr (SEL) far_key = key_of(ord + 4);
         cur = next;
         ++cnt[sx];
       }
