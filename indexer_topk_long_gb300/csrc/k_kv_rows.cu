@@ -13,10 +13,10 @@
 // exactly; queries (bf16 or f16) become f16 after a power-of-two scaling of the
 // row, exact but for elements below 2^-22 of the row's largest.
 //
-// Work: the (sequence or query, 16-row group, KV head) units' key tiles of 128
+// Work: the (sequence or query, 16-row group, KV head) units' key tiles of 256
 // form one line that is cut into equal pieces, one per CTA, so ragged lengths
 // need no plan on the host.  A unit cut by a border is merged by the last of its
-// CTAs in a fixed order.  Each of a CTA's 8 warps takes 16 keys of a tile through
+// CTAs in a fixed order.  Each of a CTA's 8 warps takes 32 keys of a tile through
 // its own ring of asynchronous 16-byte copies (no block barrier in the loop).
 #include "kv_internal.cuh"
 
@@ -25,9 +25,10 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kWarpKeys = 16;
+constexpr int kGroups = 2;               // 16-key groups a warp takes from a tile
+constexpr int kWarpKeys = 16 * kGroups;
 constexpr int kTileKeys = kWarps * kWarpKeys;
-constexpr int kStages = 4;
+constexpr int kStages = 2;               // 8 KB each and warp at D = 128: 64 KB in flight an SM
 constexpr float kMinusHuge = -1e30f;     // running maximum of a row that has seen nothing
 // A weight at the running maximum is 2^kBoost; the maximum is only moved when a
 // score exceeds it by more than kSlack, so weights stay below 2^15 < f16's 65504.
@@ -63,7 +64,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Row r (0..15) and 16-byte chunk of a stage's K or V half: byte offset.  Lanes
+// Row r of a 16-key group and 16-byte chunk: byte offset in the group's codes.  Lanes
 // of one quarter warp read chunks of two neighbouring rows (K) or one or two
 // chunks of four rows of equal parity (V); the placement keeps each on distinct
 // banks.
@@ -91,8 +92,7 @@ struct Unit {
 
 // Where a cursor stands: unit u of its sequence, key tile t of n_tiles.
 struct Cursor {
-  long long at;          // linear position
-  long long left;        // positions to go
+  int left;              // tiles to go
   int t, n_tiles;
   int u;                 // unit within the sequence (dense) or -1
   long long unit;        // unit number (selected)
@@ -154,7 +154,6 @@ __device__ __forceinline__ void enter_seq(const AttnParams& p, Cursor& c, int b)
 // One tile forward.
 template <bool SEL>
 __device__ __forceinline__ void advance(const AttnParams& p, Cursor& c) {
-  ++c.at;
   --c.left;
   if (++c.t < c.n_tiles || c.left <= 0) return;
   c.t = 0;
@@ -174,9 +173,8 @@ __device__ __forceinline__ void advance(const AttnParams& p, Cursor& c) {
 }
 
 struct Feed {            // what the next tile's copies need, fetched a step ahead
-  int key;               // selected: this lane's key position (lanes 0-15), -1 none
-  int page;              // dense: the tile's page
-  bool live;             // dense: the tile's 16 keys begin before the length
+  int key;               // selected: this lane's key position as listed, -1 none
+  int page[kGroups];     // dense: the groups' pages, -1 beyond the length
 };
 
 template <int D, bool SEL>
@@ -243,8 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
   const long long start = blockIdx.x * total / n_cta;
   const long long end = blockIdx.x < n_cta ? (blockIdx.x + 1) * total / n_cta : start;
   if (start < end) {
-    head.at = start;
-    head.left = end - start;
+    head.left = static_cast<int>(end - start);
     if constexpr (SEL) {
       const int tiles = (p.k + kTileKeys - 1) / kTileKeys;
       head.unit = start / tiles;
@@ -264,25 +261,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
   float* merge_o = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);     // [warp][16][D]
   float* merge_ml = merge_o + kWarps * kRowsPerUnit * D;                        // [warp][16][2]
 
-  // --- producer: one tile's 16 keys of this warp into a stage -----------------------------
+  // --- producer: one tile's 32 keys of this warp into a stage -----------------------------
   Cursor pc = head;                      // producer cursor
-  Feed feed{-1, -1, false};
-  auto fetch = [&]() {                   // index or page of the next tile to produce
-    feed = Feed{-1, -1, false};
+  Feed feed;
+  auto fetch = [&]() {                   // index or pages of the next tile to produce
+    feed.key = -1;
+#pragma unroll
+    for (int h = 0; h < kGroups; ++h) feed.page[h] = -1;
     if (pc.left <= 0) return;
     if constexpr (SEL) {
       const int slot = pc.t * kTileKeys + warp * kWarpKeys + lane;
-      if (lane < kWarpKeys && slot < p.k) {
-        const int key = __ldg(p.idx + static_cast<size_t>(pc.w.q0) * p.k + slot);
-        feed.key = key >= 0 && key <= pc.w.pos0 ? key : -1;
-      }
-      feed.live = true;
+      if (slot < p.k) feed.key = __ldg(p.idx + static_cast<size_t>(pc.w.q0) * p.k + slot);
     } else {
       const int tile = pc.t < pc.w.skip ? pc.t : pc.t - pc.w.skip + pc.w.tile0;
       const int key0 = tile * kTileKeys + warp * kWarpKeys;
-      feed.live = key0 < pc.w.len;
-      if (feed.live)
-        feed.page = __ldg(p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (key0 >> p.cache.page_log2));
+      const int* table = p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width;
+#pragma unroll
+      for (int h = 0; h < kGroups; ++h)
+        if (key0 + 16 * h < pc.w.len) feed.page[h] = __ldg(table + ((key0 + 16 * h) >> p.cache.page_log2));
     }
   };
   int stage_in = 0;
@@ -291,60 +287,70 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
       const uint32_t kd = ring_u + stage_in * S::kStageBytes, vd = kd + kWarpKeys * D;
       float* m = meta + stage_in * S::kMetaFloats;
       const uint32_t mu = meta_u + stage_in * S::kMetaFloats * 4;
+      constexpr int kPer = CPR / 2;      // copies of a group, lane and operand
+      const int cr = lane / CPR, ch = lane % CPR;
       if constexpr (SEL) {
-        int page = -1, off = 0;
-        if (feed.key >= 0) {
-          page = __ldg(p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (feed.key >> p.cache.page_log2));
-          off = feed.key & (p.cache.page - 1);
+        const int key = feed.key <= pc.w.pos0 ? feed.key : -1;
+        int page = -1;
+        if (key >= 0) {
+          page = __ldg(p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (key >> p.cache.page_log2));
           if (page < 0 || page >= p.cache.num_pages) {
             raise_status(p.status, kDevArg);
             page = -2;
           }
         }
         long long row = -1;
-        if (page >= 0) row = (static_cast<long long>(page) * p.cache.heads + pc.w.head) * p.cache.page + off;
-        if (lane < kWarpKeys) {
-          m[2 * kWarpKeys + lane] = feed.key >= 0 ? 1.f : 0.f;
-          if (page >= 0) {
-            const size_t blk = static_cast<size_t>(page) * p.cache.heads + pc.w.head;
-            cp_async4(mu + lane * 4, p.cache.k_scale + blk);
-            cp_async4(mu + (kWarpKeys + lane) * 4, p.cache.v_scale + blk);
-          } else {
-            m[lane] = page == -2 ? __int_as_float(0x7FC00000) : 1.f;
-            m[kWarpKeys + lane] = 1.f;
-          }
+        m[2 * kWarpKeys + lane] = key >= 0 ? 1.f : 0.f;
+        if (page >= 0) {
+          const size_t blk = static_cast<size_t>(page) * p.cache.heads + pc.w.head;
+          row = static_cast<long long>(blk) * p.cache.page + (key & (p.cache.page - 1));
+          cp_async4(mu + lane * 4, p.cache.k_scale + blk);
+          cp_async4(mu + (kWarpKeys + lane) * 4, p.cache.v_scale + blk);
+        } else {
+          m[lane] = page == -2 ? __int_as_float(0x7FC00000) : 1.f;
+          m[kWarpKeys + lane] = 1.f;
         }
 #pragma unroll
-        for (int i = 0; i < CPR / 2; ++i) {
-          const int r = i * (32 / CPR) + lane / CPR, ch = lane % CPR;
-          const long long rr = __shfl_sync(0xFFFFFFFFu, row, r);
-          const size_t o = rr >= 0 ? static_cast<size_t>(rr) * D + ch * 16 : 0;
-          cp_async16(kd + place<D>(r, ch), p.cache.k_codes + o, rr >= 0);
-          cp_async16(vd + place<D>(r, ch), p.cache.v_codes + o, rr >= 0);
-        }
-      } else if (feed.live) {
+        for (int h = 0; h < kGroups; ++h)
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int r = i * (32 / CPR) + cr;
+            const long long rr = __shfl_sync(0xFFFFFFFFu, row, 16 * h + r);
+            const size_t o = rr >= 0 ? static_cast<size_t>(rr) * D + ch * 16 : 0;
+            const uint32_t at = 16 * h * D + place<D>(r, ch);
+            cp_async16(kd + at, p.cache.k_codes + o, rr >= 0);
+            cp_async16(vd + at, p.cache.v_codes + o, rr >= 0);
+          }
+      } else {
         const int tile = pc.t < pc.w.skip ? pc.t : pc.t - pc.w.skip + pc.w.tile0;
         const int key0 = tile * kTileKeys + warp * kWarpKeys;
-        const bool known = feed.page >= 0 && feed.page < p.cache.num_pages;
-        if (!known) raise_status(p.status, kDevArg);
-        const size_t blk = known ? static_cast<size_t>(feed.page) * p.cache.heads + pc.w.head : 0;
-        if (lane == 0) {
-          if (known) {
-            cp_async4(mu, p.cache.k_scale + blk);
-            cp_async4(mu + 4, p.cache.v_scale + blk);
-          } else {
-            m[0] = __int_as_float(0x7FC00000);
-            m[1] = 1.f;
-          }
-        }
-        const size_t o = (blk * p.cache.page + (key0 & (p.cache.page - 1))) * D + lane * 16;
 #pragma unroll
-        for (int i = 0; i < CPR / 2; ++i) {
-          const int r = i * (32 / CPR) + lane / CPR, ch = lane % CPR;
-          const bool on = known && key0 + r < pc.w.len;
-          const size_t oo = on ? o + i * 512 : 0;
-          cp_async16(kd + place<D>(r, ch), p.cache.k_codes + oo, on);
-          cp_async16(vd + place<D>(r, ch), p.cache.v_codes + oo, on);
+        for (int h = 0; h < kGroups; ++h) {
+          const int first = key0 + 16 * h;
+          if (first >= pc.w.len) break;
+          const bool known = feed.page[h] >= 0 && feed.page[h] < p.cache.num_pages;
+          if (!known) raise_status(p.status, kDevArg);
+          const size_t blk = known ? static_cast<size_t>(feed.page[h]) * p.cache.heads + pc.w.head : 0;
+          if (lane == 0) {
+            if (known) {
+              cp_async4(mu + 8 * h, p.cache.k_scale + blk);
+              cp_async4(mu + 8 * h + 4, p.cache.v_scale + blk);
+            } else {
+              m[2 * h] = __int_as_float(0x7FC00000);
+              m[2 * h + 1] = 1.f;
+            }
+          }
+          const size_t o = (blk * p.cache.page + (first & (p.cache.page - 1))) * D + lane * 16;
+          const int rows = known ? pc.w.len - first : 0;      // of the group's 16
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int r = i * (32 / CPR) + cr;
+            const bool on = r < rows;
+            const size_t oo = on ? o + i * 512 : 0;
+            const uint32_t at = 16 * h * D + place<D>(r, ch);
+            cp_async16(kd + at, p.cache.k_codes + oo, on);
+            cp_async16(vd + at, p.cache.v_codes + oo, on);
+          }
         }
       }
       advance<SEL>(p, pc);
@@ -374,12 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
   float M[2], l[2], crow[2];
   int prow[2];                           // query position of rows g, g + 8
   int stage_out = 0;
+  long long at = start;                  // where head stands on the line
 
 #pragma unroll 1
   while (head.left > 0) {
     // a unit's piece: tiles [head.t, t_end)
     const int t_begin = head.t;
-    const int t_end = static_cast<int>(min(static_cast<long long>(head.n_tiles), head.t + head.left));
+    const int t_end = min(head.n_tiles, head.t + head.left);
     const int rows_all = head.w.nq * p.group;
 #pragma unroll
     for (int hlf = 0; hlf < 2; ++hlf) {
@@ -449,76 +456,84 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
       const int key0 = tile * kTileKeys + warp * kWarpKeys;
       if (!SEL && (key0 >= head.w.len || key0 > p_hi)) continue;
 
-      float s[2][4] = {};
+      float s[kGroups][2][4] = {};
 #pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-        const uint4 a = *reinterpret_cast<const uint4*>(kp + place<D>(g, half * 4 + cq));
-        const uint4 b = *reinterpret_cast<const uint4*>(kp + place<D>(g + 8, half * 4 + cq));
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+      for (int half = 0; half < D / 64; ++half)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t a0, a1, b0, b1;
-          e4m3x4_to_f16(aw[i], a0, a1);
-          e4m3x4_to_f16(bw[i], b0, b1);
-          mma_f16(s[0], qf[half * 4 + i], a0, a1);
-          mma_f16(s[1], qf[half * 4 + i], b0, b1);
+        for (int h = 0; h < kGroups; ++h) {
+          const uint4 a = *reinterpret_cast<const uint4*>(kp + 16 * h * D + place<D>(g, half * 4 + cq));
+          const uint4 b = *reinterpret_cast<const uint4*>(kp + 16 * h * D + place<D>(g + 8, half * 4 + cq));
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t a0, a1, b0, b1;
+            e4m3x4_to_f16(aw[i], a0, a1);
+            e4m3x4_to_f16(bw[i], b0, b1);
+            mma_f16(s[h][0], qf[half * 4 + i], a0, a1);
+            mma_f16(s[h][1], qf[half * 4 + i], b0, b1);
+          }
         }
-      }
-      // element e of s[n]: row g + 8 (e >> 1), key 2 cq + (e & 1) + 8 n
-      float ks[4], lv[4], iv[4];
-      bool valid[4];
-      if constexpr (SEL) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float2 a = *reinterpret_cast<const float2*>(m + 8 * n + 2 * cq);
-          const float2 b = *reinterpret_cast<const float2*>(m + kWarpKeys + 8 * n + 2 * cq);
-          const float2 z = *reinterpret_cast<const float2*>(m + 2 * kWarpKeys + 8 * n + 2 * cq);
-          ks[2 * n] = a.x;
-          ks[2 * n + 1] = a.y;
-          lv[2 * n] = __log2f(b.x) + kBoost;
-          lv[2 * n + 1] = __log2f(b.y) + kBoost;
-          iv[2 * n] = __frcp_rn(b.x);
-          iv[2 * n + 1] = __frcp_rn(b.y);
-          valid[2 * n] = z.x != 0.f;
-          valid[2 * n + 1] = z.y != 0.f;
-        }
-      } else {
-        const float2 sc = *reinterpret_cast<const float2*>(m);
-        const float lg = __log2f(sc.y) + kBoost, inv = __frcp_rn(sc.y);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ks[i] = sc.x;
-          lv[i] = lg;
-          iv[i] = inv;
-          valid[i] = true;
-        }
-      }
+      // element e of s[h][n]: row g + 8 (e >> 1), key 16 h + 8 n + 2 cq + (e & 1)
       const bool inside = !SEL && key0 + kWarpKeys - 1 <= p_lo &&
                           (p.window <= 0 || key0 > p_hi - p.window || key0 + kWarpKeys <= p.sinks);
-      bool over = false;
+      float iv[kGroups][SEL ? 4 : 1];    // 1 / vs: of each of the lane's keys, or of the group
+      float mx[2] = {-__int_as_float(0x7F800000), -__int_as_float(0x7F800000)};
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int h = 0; h < kGroups; ++h) {
+        float ks[4], lv[4];
+        bool valid[4];
+        if constexpr (SEL) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int hlf = e >> 1, kk = 2 * n + (e & 1);
-          float x = fmaf(s[n][e] * ks[kk], crow[hlf], lv[kk]);
-          if constexpr (SEL) {
-            if (!valid[kk]) x = -__int_as_float(0x7F800000);
-          } else if (!inside) {
-            const int key = key0 + 8 * n + 2 * cq + (e & 1);
-            const bool seen = key <= prow[hlf] && (p.window <= 0 || key > prow[hlf] - p.window || key < p.sinks);
-            if (!seen) x = -__int_as_float(0x7F800000);
+          for (int n = 0; n < 2; ++n) {
+            const int at0 = 16 * h + 8 * n + 2 * cq;
+            const float2 a = *reinterpret_cast<const float2*>(m + at0);
+            const float2 b = *reinterpret_cast<const float2*>(m + kWarpKeys + at0);
+            const float2 z = *reinterpret_cast<const float2*>(m + 2 * kWarpKeys + at0);
+            ks[2 * n] = a.x;
+            ks[2 * n + 1] = a.y;
+            lv[2 * n] = __log2f(b.x) + kBoost;
+            lv[2 * n + 1] = __log2f(b.y) + kBoost;
+            iv[h][2 * n] = __frcp_rn(b.x);
+            iv[h][2 * n + 1] = __frcp_rn(b.y);
+            valid[2 * n] = z.x != 0.f;
+            valid[2 * n + 1] = z.y != 0.f;
           }
-          s[n][e] = x;
-          over = over || x > M[hlf] + (kSlack + kBoost);
+        } else {
+          // a group beyond the length was not copied: its keys are masked, its values skipped
+          const float2 sc = key0 + 16 * h < head.w.len ? *reinterpret_cast<const float2*>(m + 2 * h) : make_float2(1.f, 1.f);
+          const float lg = __log2f(sc.y) + kBoost;
+          iv[h][0] = __frcp_rn(sc.y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ks[i] = sc.x;
+            lv[i] = lg;
+          }
         }
-      if (__any_sync(0xFFFFFFFFu, over)) {
+        const float f0 = ks[0] * crow[0], f1 = ks[0] * crow[1];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int hlf = e >> 1, kk = 2 * n + (e & 1);
+            float x = SEL ? fmaf(s[h][n][e] * ks[kk], crow[hlf], lv[kk]) : fmaf(s[h][n][e], hlf ? f1 : f0, lv[0]);
+            if constexpr (SEL) {
+              if (!valid[kk]) x = -__int_as_float(0x7F800000);
+            } else if (!inside) {
+              const int key = key0 + 16 * h + 8 * n + 2 * cq + (e & 1);
+              const bool seen = key <= prow[hlf] && (p.window <= 0 || key > prow[hlf] - p.window || key < p.sinks);
+              if (!seen) x = -__int_as_float(0x7F800000);
+            }
+            s[h][n][e] = x;
+            mx[hlf] = fmaxf(mx[hlf], x);
+          }
+      }
+      if (__any_sync(0xFFFFFFFFu, mx[0] > M[0] + (kSlack + kBoost) || mx[1] > M[1] + (kSlack + kBoost))) {
 #pragma unroll
         for (int hlf = 0; hlf < 2; ++hlf) {
-          float mx = fmaxf(fmaxf(s[0][2 * hlf], s[0][2 * hlf + 1]), fmaxf(s[1][2 * hlf], s[1][2 * hlf + 1])) - kBoost;
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-          const float next = fmaxf(M[hlf], mx);
+          float top = mx[hlf] - kBoost;
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          const float next = fmaxf(M[hlf], top);
           const float by = exp2_approx(M[hlf] - next);
           M[hlf] = next;
           l[hlf] *= by;
@@ -529,46 +544,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
           }
         }
       }
-      uint32_t pf[4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int h = 0; h < kGroups; ++h) {
+        if (!SEL && key0 + 16 * h >= head.w.len) break;       // not copied
+        uint32_t pf[4];
 #pragma unroll
         for (int hlf = 0; hlf < 2; ++hlf) {
-          const float w0 = exp2_approx(s[n][2 * hlf] - M[hlf]), w1 = exp2_approx(s[n][2 * hlf + 1] - M[hlf]);
-          l[hlf] = fmaf(w0, iv[2 * n], fmaf(w1, iv[2 * n + 1], l[hlf]));
-          pf[hlf + 2 * n] = kv_pack16(w0, w1, false);
-        }
-      // values: this lane's keys 2 cq, 2 cq + 1 (and + 8), its g-th D / 8 elements
-      uint32_t vw[4][D / 32];
+          float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * cq + (i & 1) + 8 * (i >> 1);
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vp + place<D>(r, g));
-          vw[i][0] = x.x;
-          vw[i][1] = x.y;
-          vw[i][2] = x.z;
-          vw[i][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(vp + place<D>(r, g >> 1) + (g & 1) * 8);
-          vw[i][0] = x.x;
-          vw[i][1] = x.y;
+          for (int n = 0; n < 2; ++n) {
+            const float w0 = exp2_approx(s[h][n][2 * hlf] - M[hlf]), w1 = exp2_approx(s[h][n][2 * hlf + 1] - M[hlf]);
+            if constexpr (SEL) l[hlf] = fmaf(w0, iv[h][2 * n], fmaf(w1, iv[h][2 * n + 1], l[hlf]));
+            else sum += w0 + w1;
+            pf[hlf + 2 * n] = kv_pack16(w0, w1, false);
+          }
+          if constexpr (!SEL) l[hlf] = fmaf(sum, iv[h][0], l[hlf]);
         }
-      }
+        // values: this lane's keys 2 cq, 2 cq + 1 (and + 8), its g-th D / 8 elements
+        uint32_t vw[4][D / 32];
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        const uint32_t x[4] = {vw[0][w], vw[1][w], vw[2][w], vw[3][w]};
-        const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), a23 = __byte_perm(x[0], x[1], 0x7362);
-        const uint32_t b01 = __byte_perm(x[2], x[3], 0x5140), b23 = __byte_perm(x[2], x[3], 0x7362);
-        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-        e4m3x4_to_f16(a01, a0, a1);
-        e4m3x4_to_f16(a23, a2, a3);
-        e4m3x4_to_f16(b01, b0, b1);
-        e4m3x4_to_f16(b23, b2, b3);
-        mma_f16(o[w * 4], pf, a0, b0);
-        mma_f16(o[w * 4 + 1], pf, a1, b1);
-        mma_f16(o[w * 4 + 2], pf, a2, b2);
-        mma_f16(o[w * 4 + 3], pf, a3, b3);
+        for (int i = 0; i < 4; ++i) {
+          const int r = 2 * cq + (i & 1) + 8 * (i >> 1);
+          const unsigned char* row = vp + 16 * h * D;
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(row + place<D>(r, g));
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+            vw[i][2] = x.z;
+            vw[i][3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(row + place<D>(r, g >> 1) + (g & 1) * 8);
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint32_t x[4] = {vw[0][w], vw[1][w], vw[2][w], vw[3][w]};
+          const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), a23 = __byte_perm(x[0], x[1], 0x7362);
+          const uint32_t b01 = __byte_perm(x[2], x[3], 0x5140), b23 = __byte_perm(x[2], x[3], 0x7362);
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          e4m3x4_to_f16(a01, a0, a1);
+          e4m3x4_to_f16(a23, a2, a3);
+          e4m3x4_to_f16(b01, b0, b1);
+          e4m3x4_to_f16(b23, b2, b3);
+          mma_f16(o[w * 4], pf, a0, b0);
+          mma_f16(o[w * 4 + 1], pf, a1, b1);
+          mma_f16(o[w * 4 + 2], pf, a2, b2);
+          mma_f16(o[w * 4 + 3], pf, a3, b3);
+        }
       }
     }
 
@@ -598,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
     const int rows = min(rows_all - head.w.row0, kRowsPerUnit);
     const bool whole = t_begin == 0 && t_end == head.n_tiles;
     // Contributors of this unit and its place in the workspace.
-    const long long u0 = head.at - t_begin, u1 = u0 + head.n_tiles;       // the unit on the line
+    const long long u0 = at - t_begin, u1 = u0 + head.n_tiles;       // the unit on the line
     const int c0 = static_cast<int>(((u0 + 1) * n_cta - 1) / total), c1 = static_cast<int>((u1 * n_cta - 1) / total);
     constexpr int kSlot = kRowsPerUnit * (D + 2);
     float* mine = p.part + static_cast<size_t>(2 * blockIdx.x + (t_begin == 0 ? 1 : 0)) * kSlot;
@@ -670,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
     __syncthreads();
     // to the next unit
     const int n = t_end - t_begin;
-    head.at += n - 1;
+    at += n;
     head.left -= n - 1;
     head.t = t_end - 1;
     advance<SEL>(p, head);

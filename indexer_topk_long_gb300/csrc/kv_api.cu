@@ -51,6 +51,17 @@ bool rows_ok(const void* p, long long stride, int heads, int dim) {
   return kv_aligned(p) && stride >= static_cast<long long>(heads) * dim && stride % 8 == 0;
 }
 
+// The kernel for few rows reads a head's keys once for every 16 rows, the tile kernel once
+// for 128, at some 25 us more to start.  Listed keys: the first takes 16-row, 256-key pieces
+// at 3.5 us each and SM.
+bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
+  const long long rows = static_cast<long long>(p.group) * (p.idx != nullptr ? 1 : max_q);
+  if (rows <= kRowsPerUnit) return true;
+  if (p.idx == nullptr) return false;
+  const long long pieces = static_cast<long long>(p.batch.N) * p.cache.heads * ((p.group + 15) / 16) * ((p.k + 255) / 256);
+  return pieces <= 8ll * num_sms;
+}
+
 KvBatch batch_of(const ltk_kv_batch* b) {
   return KvBatch{b->page_table, b->seq_lens, b->cu_q, b->table_width, b->B, b->N};
 }
@@ -188,9 +199,9 @@ static ltk_status kv_attend(ltk_kv* h, const ltk_kv_batch* batch, int dtype, con
   p.counters = h->counters;
   p.status = h->status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const long long rows = static_cast<long long>(p.group) * (idx != nullptr ? 1 : max_q > 0 ? max_q : batch->N);
-  const cudaError_t e = rows <= kRowsPerUnit ? launch_kv_rows(p, h->num_sms, st)
-                                             : launch_kv_tile(p, max_q > 0 ? max_q : batch->N, h->num_sms, st);
+  const int most_q = max_q > 0 ? max_q : batch->N;
+  const cudaError_t e = kv_use_rows(p, most_q, h->num_sms) ? launch_kv_rows(p, h->num_sms, st)
+                                                           : launch_kv_tile(p, most_q, h->num_sms, st);
   return kv_cuda_fail(e, "kv attention");
 }
 

@@ -57,8 +57,12 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int
   return s;
 }
 
-// Sequence of query n: the last b with cu_q[b] <= n.
+// Sequence of query n: the last b with cu_q[b] <= n.  First looked for where it is
+// when every sequence has as many queries (a decode step: one look, no search).
 __device__ __forceinline__ int kv_seq_of_query(const KvBatch& bt, int n) {
+  const int guess = static_cast<int>(static_cast<long long>(n) * bt.B / bt.N);
+  const int at = __ldg(bt.cu_q + guess), next = __ldg(bt.cu_q + guess + 1);
+  if (at <= n && n < next) return guess;
   int lo = 0, hi = bt.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;

@@ -45,18 +45,22 @@ def _ints(t, name: str, shape, device) -> None:
 def _rows(t, name: str, n: int, dim: int, device, dtype=None) -> tuple[int, int]:
     """[n, heads, dim] of 16-bit elements, each token's heads contiguous and tokens
     a multiple of 8 elements apart; returns (heads, token stride)."""
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != dim:
-        _fail(name, f"expected shape ({n}, heads, {dim}), got {tuple(t.shape)}")
-    if str(t.dtype) not in DTYPES:
-        _fail(name, f"expected bfloat16 or float16 elements, got {t.dtype}")
-    if dtype is not None and t.dtype != dtype:
-        _fail(name, f"expected {dtype} elements like the others, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != dim:
+        _fail(name, f"expected shape ({n}, heads, {dim}), got {tuple(shape)}")
+    if dtype is None:
+        if str(t.dtype) not in DTYPES:
+            _fail(name, f"expected bfloat16 or float16 elements, got {t.dtype}")
+    elif t.dtype is not dtype:
+        _fail(name, f"expected {dtype} elements like the others, got {t.dtype}" if str(t.dtype) in DTYPES
+              else f"expected bfloat16 or float16 elements, got {t.dtype}")
     _device_ok(t, name, device)
-    heads = t.shape[1]
+    heads = shape[1]
     if heads < 1:
         _fail(name, "has no heads")
-    stride = t.stride(0) if n > 1 else heads * dim
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    s0, s1, s2 = t.stride()
+    stride = s0 if n > 1 else heads * dim
+    if s2 != 1 or (heads > 1 and s1 != dim):
         _fail(name, "each token's heads must be contiguous")
     if stride % 8 or stride < heads * dim or t.data_ptr() % 16:
         _fail(name, "tokens must start on 16-byte boundaries and not overlap")
@@ -64,9 +68,10 @@ def _rows(t, name: str, n: int, dim: int, device, dtype=None) -> tuple[int, int]
 
 
 def check_batch(page_table, seq_lens, cu_q, n: int, device) -> KvBatch:
-    if page_table.dim() != 2:
-        _fail("page_table", f"expected a 2-D tensor, got shape {tuple(page_table.shape)}")
-    b, width = page_table.shape
+    shape = page_table.shape
+    if len(shape) != 2:
+        _fail("page_table", f"expected a 2-D tensor, got shape {tuple(shape)}")
+    b, width = shape
     _ints(page_table, "page_table", (b, width), device)
     _ints(seq_lens, "seq_lens", (b,), device)
     _ints(cu_q, "cu_q", (b + 1,), device)
@@ -90,6 +95,7 @@ class PagedKVCache:
         if any(given) and not all(given):
             raise ValueError("k_codes, v_codes, k_scale, v_scale: give all four or none")
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._torch, self._index, self._raw_stream = torch, self.device.index, torch._C._cuda_getCurrentRawStream
         codes, scales = (self.num_pages, self.heads, self.page, self.dim), (self.num_pages, self.heads)
         if not all(given):
             k_codes, v_codes = (torch.zeros(codes, dtype=torch.uint8, device=self.device) for _ in range(2))
@@ -115,35 +121,36 @@ class PagedKVCache:
         self.h = h
 
     # -- helpers ---------------------------------------------------------------
-    def _begin(self, stream, tensors):
-        """The stream to launch on, and a context in which outputs belong to it.
-        Tensors of the caller's are kept from reuse until the call on another
-        stream is done."""
-        import contextlib
-
-        import torch
+    def _begin(self, stream, tensors) -> int:
+        """The stream to launch on (its handle).  Tensors of the caller's that another
+        stream than the current one reads or writes are kept from reuse until it has."""
         if self.h is None:
             raise ValueError("the cache is closed")
-        cur = torch.cuda.current_stream(self.device)
-        if stream is None or stream == cur:
-            return cur, contextlib.nullcontext()
+        current = self._raw_stream(self._index)
+        if stream is None or stream.cuda_stream == current:
+            return current
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-        return stream, torch.cuda.stream(stream)
+        return stream.cuda_stream
 
-    def _outputs(self, q, out, lse):
-        import torch
-        n, heads, dim = q.shape
+    def _new(self, stream, shape, like, dtype=None):
+        """An output that belongs to the stream the call runs on."""
+        if stream is None:
+            return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+        with self._torch.cuda.stream(stream):
+            return like.new_empty(shape, dtype=dtype or like.dtype)
+
+    def _outputs(self, stream, q, n, heads, out, lse):
+        f32 = self._torch.float32
+        shape = (n, heads, self.dim)
         if out is None:
-            out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
-        elif tuple(out.shape) != (n, heads, dim) or out.dtype != q.dtype or not out.is_contiguous() \
-                or out.device != q.device:
-            _fail("out", f"expected a contiguous {q.dtype} tensor of shape {(n, heads, dim)} on {q.device}")
+            out = self._new(stream, shape, q)
+        elif tuple(out.shape) != shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
+            _fail("out", f"expected a contiguous {q.dtype} tensor of shape {shape} on {q.device}")
         if lse is None:
-            lse = torch.empty((n, heads), dtype=torch.float32, device=q.device)
-        elif tuple(lse.shape) != (n, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() \
-                or lse.device != q.device:
+            lse = self._new(stream, (n, heads), q, f32)
+        elif tuple(lse.shape) != (n, heads) or lse.dtype != f32 or not lse.is_contiguous() or lse.device != q.device:
             _fail("lse", f"expected a contiguous float32 tensor of shape {(n, heads)} on {q.device}")
         return out, lse
 
@@ -155,8 +162,7 @@ class PagedKVCache:
                q_out=None, stream=None):
         """Stores the new tokens' k, v [N, heads, dim]; keys and q are rotated by the rows
         of cos, sin [positions, rot / 2] when given.  Returns the rotated q (None without q)."""
-        import torch
-        n = int(k.shape[0])
+        n = k.shape[0]
         batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
         kh, ks = _rows(k, "k", n, self.dim, self.device)
         vh, vs = _rows(v, "v", n, self.dim, self.device, k.dtype)
@@ -167,28 +173,28 @@ class PagedKVCache:
             raise ValueError("cos, sin: give both or neither")
         if cos is not None:
             for t, name in ((cos, "cos"), (sin, "sin")):
-                if t.dim() != 2 or t.shape != cos.shape or t.dtype != torch.float32 or not t.is_contiguous():
+                if t.dim() != 2 or t.shape != cos.shape or t.dtype != self._torch.float32 or not t.is_contiguous():
                     _fail(name, "expected contiguous float32 tables of equal shape [positions, rot / 2]")
                 _device_ok(t, name, self.device)
-            rows, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
+            rows, rot = cos.shape[0], 2 * cos.shape[1]
         qh = qs = 0
         if q is not None:
             qh, qs = _rows(q, "q", n, self.dim, self.device, k.dtype)
-        st, within = self._begin(stream, (k, v, page_table, seq_lens, cu_q, cos, sin, q, q_out, self.k_codes,
-                                          self.v_codes, self.k_scale, self.v_scale))
-        with within:
-            if q is not None and q_out is None:
-                q_out = torch.empty((n, qh, self.dim), dtype=q.dtype, device=q.device)
-            if q_out is not None:
-                if q is None:
-                    raise ValueError("q_out: given without q")
-                if tuple(q_out.shape) != (n, qh, self.dim) or q_out.dtype != q.dtype or not q_out.is_contiguous() \
-                        or q_out.device != q.device:
-                    _fail("q_out", f"expected a contiguous {q.dtype} tensor of shape {(n, qh, self.dim)}")
-            ltk._check(self.lib.ltk_kv_append(
-                self.h, ctypes.byref(batch), DTYPES[str(k.dtype)], k.data_ptr(), ks, v.data_ptr(), vs,
-                ltk._ptr(cos), ltk._ptr(sin), rows, rot, 1 if interleaved else 0, ltk._ptr(q), qs, qh,
-                ltk._ptr(q_out), st.cuda_stream), "ltk_kv_append")
+        if q_out is not None:
+            if q is None:
+                raise ValueError("q_out: given without q")
+            if tuple(q_out.shape) != (n, qh, self.dim) or q_out.dtype != q.dtype or not q_out.is_contiguous() \
+                    or q_out.device != q.device:
+                _fail("q_out", f"expected a contiguous {q.dtype} tensor of shape {(n, qh, self.dim)}")
+        st = self._begin(stream, (k, v, page_table, seq_lens, cu_q, cos, sin, q, q_out, self.k_codes,
+                                  self.v_codes, self.k_scale, self.v_scale))
+        if q is not None and q_out is None:
+            q_out = self._new(stream, (n, qh, self.dim), q)
+        ltk._check(self.lib.ltk_kv_append(
+            self.h, ctypes.byref(batch), DTYPES[str(k.dtype)], k.data_ptr(), ks, v.data_ptr(), vs,
+            None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(), rows, rot,
+            1 if interleaved else 0, None if q is None else q.data_ptr(), qs, qh,
+            None if q_out is None else q_out.data_ptr(), st), "ltk_kv_append")
         return q_out
 
     def attention(self, q, page_table, seq_lens, cu_q, max_q: int | None = None, scale: float | None = None,
@@ -196,46 +202,42 @@ class PagedKVCache:
         """Causal attention of q [N, q_heads, dim] over the cached tokens; with ``window`` > 0 a
         query at p sees keys j > p - window and the first ``sinks`` keys.  ``max_q`` (the most
         queries of one sequence) only helps choose a kernel.  Returns (out, lse)."""
-        n = int(q.shape[0])
+        n = q.shape[0]
         batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
         heads, qs = _rows(q, "q", n, self.dim, self.device)
         if max_q is None:
             max_q = -(-n // max(batch.B, 1))
-        st, within = self._begin(stream, (q, page_table, seq_lens, cu_q, out, lse, self.k_codes, self.v_codes,
-                                          self.k_scale, self.v_scale))
-        with within:
-            out, lse = self._outputs(q, out, lse)
-            ltk._check(self.lib.ltk_kv_attention(
-                self.h, ctypes.byref(batch), DTYPES[str(q.dtype)], q.data_ptr(), qs, heads, int(max_q),
-                self._scale(scale), int(window), int(sinks), out.data_ptr(), lse.data_ptr(), st.cuda_stream),
-                "ltk_kv_attention")
+        st = self._begin(stream, (q, page_table, seq_lens, cu_q, out, lse, self.k_codes, self.v_codes, self.k_scale,
+                                  self.v_scale))
+        out, lse = self._outputs(stream, q, n, heads, out, lse)
+        ltk._check(self.lib.ltk_kv_attention(
+            self.h, ctypes.byref(batch), DTYPES[str(q.dtype)], q.data_ptr(), qs, heads, max_q, self._scale(scale),
+            window, sinks, out.data_ptr(), lse.data_ptr(), st), "ltk_kv_attention")
         return out, lse
 
     def attention_selected(self, q, idx, page_table, seq_lens, cu_q, scale: float | None = None, out=None,
                            lse=None, stream=None):
         """Attention of each query over its own key positions idx [N, k] (int32, -1 = empty
         slot), e.g. the indices IndexerTopK returns.  Returns (out, lse)."""
-        n = int(q.shape[0])
+        n = q.shape[0]
         batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
         heads, qs = _rows(q, "q", n, self.dim, self.device)
         if idx.dim() != 2:
             _fail("idx", f"expected a 2-D [queries, k] tensor, got shape {tuple(idx.shape)}")
         _ints(idx, "idx", (n, idx.shape[1]), self.device)
-        st, within = self._begin(stream, (q, idx, page_table, seq_lens, cu_q, out, lse, self.k_codes, self.v_codes,
-                                          self.k_scale, self.v_scale))
-        with within:
-            out, lse = self._outputs(q, out, lse)
-            ltk._check(self.lib.ltk_kv_attention_selected(
-                self.h, ctypes.byref(batch), DTYPES[str(q.dtype)], q.data_ptr(), qs, heads, idx.data_ptr(),
-                int(idx.shape[1]), self._scale(scale), out.data_ptr(), lse.data_ptr(), st.cuda_stream),
-                "ltk_kv_attention_selected")
+        st = self._begin(stream, (q, idx, page_table, seq_lens, cu_q, out, lse, self.k_codes, self.v_codes, self.k_scale,
+                                  self.v_scale))
+        out, lse = self._outputs(stream, q, n, heads, out, lse)
+        ltk._check(self.lib.ltk_kv_attention_selected(
+            self.h, ctypes.byref(batch), DTYPES[str(q.dtype)], q.data_ptr(), qs, heads, idx.data_ptr(), idx.shape[1],
+            self._scale(scale), out.data_ptr(), lse.data_ptr(), st), "ltk_kv_attention_selected")
         return out, lse
 
     def status(self, stream=None) -> int:
         """First error the device raised since the last call (0: none); synchronises the stream."""
-        st, _ = self._begin(stream, ())
+        st = self._begin(stream, ())
         value = ctypes.c_int(0)
-        ltk._check(self.lib.ltk_kv_status(self.h, ctypes.byref(value), st.cuda_stream), "ltk_kv_status")
+        ltk._check(self.lib.ltk_kv_status(self.h, ctypes.byref(value), st), "ltk_kv_status")
         return value.value
 
     def close(self) -> None:
