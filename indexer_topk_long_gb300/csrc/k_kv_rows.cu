@@ -13,17 +13,18 @@
 // exactly; queries (bf16 or f16) become f16 after a power-of-two scaling of the
 // row, exact but for elements below 2^-22 of the row's largest.
 //
-// Work: the (sequence or query, 16-row group, KV head) units' key tiles of 256
+// Work: the (sequence or query, 16-row group, KV head) units' key tiles of 128
 // form one line that is cut into equal pieces, one per CTA, so ragged lengths
 // need no plan on the host.  A unit cut by a border is merged by the last of its
-// CTAs in a fixed order.  Each of a CTA's 8 warps takes 32 keys of a tile through
+// CTAs in a fixed order.  Each of a CTA's 4 warps takes 32 keys of a tile through
 // its own ring of asynchronous 16-byte copies (no block barrier in the loop).
 #include "kv_internal.cuh"
 
 namespace ltk {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kCtasPerSm = 2;            // one merges a piece while the other streams
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroups = 2;               // 16-key groups a warp takes from a tile
 constexpr int kWarpKeys = 16 * kGroups;
@@ -178,7 +179,7 @@ struct Feed {            // what the next tile's copies need, fetched a step ahe
 };
 
 template <int D, bool SEL>
-__global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p, const int grid) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const AttnParams p, const int grid) {
   using S = RowsSmem<D>;
   constexpr int KS = D / 16;             // k-steps of the score product
   constexpr int NT = D / 8;              // n-tiles of the value product
@@ -602,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_rows_kernel(const AttnParams p
       l[hlf] += __shfl_xor_sync(0xFFFFFFFFu, l[hlf], 1);
       l[hlf] += __shfl_xor_sync(0xFFFFFFFFu, l[hlf], 2);
       const int r = g + 8 * hlf;
+      if (head.w.row0 + r >= rows_all) continue;               // no such row
       if (cq == 0) {
         merge_ml[(warp * kRowsPerUnit + r) * 2] = M[hlf];
         merge_ml[(warp * kRowsPerUnit + r) * 2 + 1] = l[hlf];
@@ -709,8 +711,8 @@ const void* rows_fn() {
 
 }  // namespace
 
-size_t kv_rows_part_floats(int num_sms) { return static_cast<size_t>(2) * num_sms * kRowsPerUnit * (128 + 2); }
-int kv_rows_counters(int num_sms) { return num_sms; }
+size_t kv_rows_part_floats(int num_sms) { return static_cast<size_t>(2) * kCtasPerSm * num_sms * kRowsPerUnit * (128 + 2); }
+int kv_rows_counters(int num_sms) { return kCtasPerSm * num_sms; }
 
 cudaError_t kv_rows_init() {
   const void* fns[4] = {rows_fn<128, false>(), rows_fn<128, true>(), rows_fn<64, false>(), rows_fn<64, true>()};
@@ -724,12 +726,13 @@ cudaError_t kv_rows_init() {
 
 cudaError_t launch_kv_rows(const AttnParams& p, int num_sms, cudaStream_t stream) {
   const bool sel = p.idx != nullptr;
+  const int grid = kCtasPerSm * num_sms;
   if (p.dim == 128) {
-    if (sel) kv_rows_kernel<128, true><<<num_sms, kThreads, RowsSmem<128>::kBytes, stream>>>(p, num_sms);
-    else kv_rows_kernel<128, false><<<num_sms, kThreads, RowsSmem<128>::kBytes, stream>>>(p, num_sms);
+    if (sel) kv_rows_kernel<128, true><<<grid, kThreads, RowsSmem<128>::kBytes, stream>>>(p, grid);
+    else kv_rows_kernel<128, false><<<grid, kThreads, RowsSmem<128>::kBytes, stream>>>(p, grid);
   } else {
-    if (sel) kv_rows_kernel<64, true><<<num_sms, kThreads, RowsSmem<64>::kBytes, stream>>>(p, num_sms);
-    else kv_rows_kernel<64, false><<<num_sms, kThreads, RowsSmem<64>::kBytes, stream>>>(p, num_sms);
+    if (sel) kv_rows_kernel<64, true><<<grid, kThreads, RowsSmem<64>::kBytes, stream>>>(p, grid);
+    else kv_rows_kernel<64, false><<<grid, kThreads, RowsSmem<64>::kBytes, stream>>>(p, grid);
   }
   count_launches(1);
   return cudaGetLastError();
