@@ -64,14 +64,13 @@ struct Meta {                            // scales of a key tile's eight 16-key 
 
 struct Ctrl {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2];
-  uint64_t ufull[2], uempty[2], qfull[2], qempty, mfull, mempty, drained, wg[2];
+  uint64_t ufull[2], uempty[2], qfull[2], qempty, qraw, mfull, mempty, drained, wg[2];
   uint32_t tmem;
   int abort_flag;
   int last[2];
   Unit unit[2];
   Meta meta[4];
-  // score factor of each row by unit slot: pair mode [2][256]; solo mode [2][128], then
-  // stream 1's (M, l) [128][2]
+  // solo mode: score factor of each row by unit slot [2][128], then stream 1's (M, l) [128][2]
   float rowf[512];
   long long at, left;                    // the CTA's piece of the line
   int slot, head, t;                     // where it begins
@@ -301,60 +300,66 @@ __device__ __forceinline__ void store_rows(uint32_t at, int lane, const uint4 (&
   }
 }
 
-// Query rows [r0, r0 + 128) of the unit to an operand tile by two warps (w = 0, 1);
-// factor[r] = what turns the products into base-2 exponents.  Rows repeat with
-// period mask + 1.
+// Queries come in two steps, since a round trip to memory for every few rows would hold
+// up the next unit: all rows by asynchronous copies to where their f16 form will stand
+// (16-bit elements either way), then converted in place.
+//
+// Step 1, warps w = 0, 1: rows [r0, r0 + 128) of the unit; rows repeat with period mask + 1,
+// rows past the unit's are zero.
 template <int D>
-__device__ __forceinline__ void load_queries(const TileParams& p, const Unit& u, uint32_t base, float* factor, int r0, int mask, int w,
-                                             int lane) {
-  constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = 64 / RPP, AT_ONCE = 4;
+__device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u, uint32_t base, int r0, int mask, int w, int lane) {
+  constexpr int LPR = D / 8, RPP = 32 / LPR;
   const AttnParams& a = p.a;
-  const int j = lane % LPR, sub = lane / LPR;
-  const int need = min(u.rows - r0, mask + 1);                // rows past it are never used
+  const int j = lane % LPR;
 #pragma unroll 1
-  for (int p0 = 0; p0 < PASSES; p0 += AT_ONCE) {
-    if (64 * w + p0 * RPP >= need && mask == 127) break;
-    uint4 raw[AT_ONCE];
+  for (int local = 64 * w + lane / LPR; local < 64 * w + 64; local += RPP) {
+    const int r = r0 + (local & mask);
+    const bool on = r < u.rows;
+    const int row = on ? u.row0 + r : 0;
+    const int qi = row / a.group;
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (static_cast<size_t>(u.q0) + qi) * a.q_stride +
+                          static_cast<size_t>(u.head * a.group + row - qi * a.group) * D + j * 8;
+    const uint32_t to = base + (j >> 3) * (kTileRows * 128) + local * 128 + (((j & 7) ^ (local & 7)) << 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(on ? src : reinterpret_cast<const uint16_t*>(a.q)),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+  }
+}
+// Step 2, one thread for a row of the tile: the row times a power of two that takes its
+// largest element to [2^8, 2^9), as f16; returns what turns the products into base-2
+// exponents.
+template <int D>
+__device__ __forceinline__ float convert_query(const AttnParams& a, uint32_t base, int row) {
+  auto at = [&](int c) { return base + (c >> 3) * (kTileRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
+  auto load = [&](int c, uint32_t (&w)[4]) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at(c)));
+  };
+  float amax = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t w[4];
+    load(c, w);
 #pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) {
-      const int r = r0 + ((64 * w + (p0 + i) * RPP + sub) & mask);
-      raw[i] = make_uint4(0, 0, 0, 0);
-      if (r < u.rows) {
-        const int row = u.row0 + r;
-        const int qi = row / a.group;
-        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (static_cast<size_t>(u.q0) + qi) * a.q_stride +
-                              static_cast<size_t>(u.head * a.group + row - qi * a.group) * D;
-        raw[i] = __ldg(reinterpret_cast<const uint4*>(src) + j);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) {
-      const int local = 64 * w + (p0 + i) * RPP + sub;
-      const uint32_t ws[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      float amax = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = kv_unpack16(ws[e], a.bf16);
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-      int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8;      // the largest element to [2^8, 2^9)
-      e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
-      const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      if (j == 0) factor[local] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      uint32_t h[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 f = kv_unpack16(ws[q], a.bf16);
-        h[q] = kv_pack16(f.x * by, f.y * by, false);
-      }
-      const uint32_t line = base + (j >> 3) * (kTileRows * 128) + local * 128;
-      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(line + (((j & 7) ^ (local & 7)) << 4)), "r"(h[0]), "r"(h[1]),
-                   "r"(h[2]), "r"(h[3])
-                   : "memory");
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = kv_unpack16(w[e], a.bf16);
+      amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
     }
   }
+  int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8;
+  e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
+  const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    uint32_t w[4];
+    load(c, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = kv_unpack16(w[i], a.bf16);
+      w[i] = kv_pack16(f.x * by, f.y * by, false);
+    }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(c)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+  }
+  return a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
 // Two fp32 products and sums at once.
@@ -410,10 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         mbar_init(smem_u32(&ctrl->ofull[i]), 1);
         mbar_init(smem_u32(&ctrl->ufull[i]), 1);
         mbar_init(smem_u32(&ctrl->uempty[i]), 8 + 2 * kLoaders + 2 + 2);
-        mbar_init(smem_u32(&ctrl->qfull[i]), 2);
+        mbar_init(smem_u32(&ctrl->qfull[i]), pair ? 8 : 2);
         mbar_init(smem_u32(&ctrl->wg[i]), 128);
       }
       mbar_init(smem_u32(&ctrl->qempty), 1);
+      mbar_init(smem_u32(&ctrl->qraw), 2);
       mbar_init(smem_u32(&ctrl->mfull), 4);
       mbar_init(smem_u32(&ctrl->mempty), 4);
       mbar_init(smem_u32(&ctrl->drained), 1);
@@ -561,19 +567,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         const Unit& u = ctrl->unit[us];
         if (u.n_tiles < 0) break;
         if (u.n_tiles > 0) {
-          if (pair) {
+          const int w = warp - 18;
+          if (pair) {                    // one buffer; the softmax threads convert their rows
             if (un >= 1 && !mbar_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
-            load_queries<D>(p, u, q_sm, ctrl->rowf + us * 256, 0, 127, warp - 18, lane);
-            if (u.rows > kTileRows)
-              load_queries<D>(p, u, q_sm + S::kOperand, ctrl->rowf + us * 256 + 128, kTileRows, 127, warp - 18, lane);
-          } else {
-            load_queries<D>(p, u, q_sm + us * S::kOperand, ctrl->rowf + us * 128, 0, u.rows <= 64 ? 63 : 127, warp - 18, lane);
+            copy_queries<D>(p, u, q_sm, 0, 127, w, lane);
+            if (u.rows > kTileRows) copy_queries<D>(p, u, q_sm + S::kOperand, kTileRows, 127, w, lane);
+          } else {                       // two buffers, converted here ahead of their use
+            copy_queries<D>(p, u, q_sm + us * S::kOperand, 0, u.rows <= 64 ? 63 : 127, w, lane);
           }
-          fence_async_smem();
+          asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+          __syncwarp();
+          if (!pair) {
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {
+              const int row = 64 * w + 32 * i + lane;
+              ctrl->rowf[us * 128 + row] = convert_query<D>(a, q_sm + us * S::kOperand, row);
+            }
+            fence_async_smem();
+          }
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&ctrl->qfull[us]));
+          mbar_arrive(smem_u32(pair ? &ctrl->qraw : &ctrl->qfull[us]));
           mbar_arrive(smem_u32(&ctrl->uempty[us]));
         }
       }
@@ -908,14 +923,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
       if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
-      if (!mbar_wait(smem_u32(&ctrl->qfull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const bool twice = !pair && u.rows <= 64;
       const int row = pair ? x * kTileRows + r : twice ? r & 63 : r;
       const bool live = row < u.rows && (!twice || (r >> 6) == x);
       const bool warp_live = __any_sync(0xFFFFFFFFu, live);
       const int mine = pair ? (x == 0 || u.rows > kTileRows ? u.n_tiles : 0) : x == 0 ? (u.n_tiles + 1) >> 1 : u.n_tiles >> 1;
       const int pos = live ? (SEL ? u.pos0 : u.pos0 + (u.row0 + row) / a.group) : -1;
-      const float f = live && mine > 0 ? (pair ? ctrl->rowf[us * 256 + row] : ctrl->rowf[us * 128 + r]) : 0.f;
+      float f = 0.f;                     // scores to base-2 exponents
+      if (pair) {
+        if (!mbar_wait(smem_u32(&ctrl->qraw), un & 1, abort_flag, status)) break;
+        if (mine > 0) {
+          f = convert_query<D>(a, q_sm + x * S::kOperand, r);
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->qfull[us]));
+      } else {
+        if (!mbar_wait(smem_u32(&ctrl->qfull[us]), (un >> 1) & 1, abort_flag, status)) break;
+        if (mine > 0) f = ctrl->rowf[us * 128 + r];
+      }
+      if (!live) f = 0.f;
       float M = kMinusHuge, l = 0.f;
       bool ok = true;
 #pragma unroll 1

@@ -72,9 +72,15 @@ def check_batch(page_table, seq_lens, cu_q, n: int, device) -> KvBatch:
     if len(shape) != 2:
         _fail("page_table", f"expected a 2-D tensor, got shape {tuple(shape)}")
     b, width = shape
-    _ints(page_table, "page_table", (b, width), device)
-    _ints(seq_lens, "seq_lens", (b,), device)
-    _ints(cu_q, "cu_q", (b + 1,), device)
+    kind = page_table.dtype
+    # one look when all is well (this is on the path of every decode step), else say what is not
+    if not (kind is seq_lens.dtype and kind is cu_q.dtype and str(kind) == "torch.int32"
+            and seq_lens.shape == (b,) and cu_q.shape == (b + 1,)
+            and page_table.is_contiguous() and seq_lens.is_contiguous() and cu_q.is_contiguous()
+            and page_table.device == device and seq_lens.device == device and cu_q.device == device):
+        _ints(page_table, "page_table", (b, width), device)
+        _ints(seq_lens, "seq_lens", (b,), device)
+        _ints(cu_q, "cu_q", (b + 1,), device)
     return KvBatch(page_table.data_ptr(), width, seq_lens.data_ptr(), cu_q.data_ptr(), b, n)
 
 
@@ -134,22 +140,22 @@ class PagedKVCache:
                 t.record_stream(stream)
         return stream.cuda_stream
 
-    def _new(self, stream, shape, like, dtype=None):
+    def _new(self, stream, shape, dtype):
         """An output that belongs to the stream the call runs on."""
         if stream is None:
-            return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+            return self._torch.empty(shape, dtype=dtype, device=self.device)
         with self._torch.cuda.stream(stream):
-            return like.new_empty(shape, dtype=dtype or like.dtype)
+            return self._torch.empty(shape, dtype=dtype, device=self.device)
 
     def _outputs(self, stream, q, n, heads, out, lse):
         f32 = self._torch.float32
         shape = (n, heads, self.dim)
         if out is None:
-            out = self._new(stream, shape, q)
+            out = self._new(stream, shape, q.dtype)
         elif tuple(out.shape) != shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
             _fail("out", f"expected a contiguous {q.dtype} tensor of shape {shape} on {q.device}")
         if lse is None:
-            lse = self._new(stream, (n, heads), q, f32)
+            lse = self._new(stream, (n, heads), f32)
         elif tuple(lse.shape) != (n, heads) or lse.dtype != f32 or not lse.is_contiguous() or lse.device != q.device:
             _fail("lse", f"expected a contiguous float32 tensor of shape {(n, heads)} on {q.device}")
         return out, lse
@@ -189,7 +195,7 @@ class PagedKVCache:
         st = self._begin(stream, (k, v, page_table, seq_lens, cu_q, cos, sin, q, q_out, self.k_codes,
                                   self.v_codes, self.k_scale, self.v_scale))
         if q is not None and q_out is None:
-            q_out = self._new(stream, (n, qh, self.dim), q)
+            q_out = self._new(stream, (n, qh, self.dim), q.dtype)
         ltk._check(self.lib.ltk_kv_append(
             self.h, ctypes.byref(batch), DTYPES[str(k.dtype)], k.data_ptr(), ks, v.data_ptr(), vs,
             None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(), rows, rot,
