@@ -32,9 +32,13 @@ constexpr int kTileRows = 128;
 constexpr int kKeys = 128;
 constexpr int kThreads = 20 * 32;
 constexpr int kLoaders = 4;              // warps for each operand, 32 keys of a tile each
-// Registers a thread: 96 at launch, moved from the loaders and the last warpgroup to the softmax.
-constexpr int kRegsSoftmax = 120, kRegsLoad = 72, kRegsRest = 96;
-static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsRest <= 5 * 96, "register split");
+// Registers a thread: 96 at launch, moved from the loaders (D = 64: and the last
+// warpgroup) to the softmax, so that no role spills in its loop.
+template <int D>
+struct Regs {
+  static constexpr int kSoftmax = D == 64 ? 128 : 120, kLoad = 72, kRest = D == 64 ? 80 : 96;
+  static_assert(2 * kSoftmax + 2 * kLoad + kRest <= 5 * 96, "register split");
+};
 constexpr float kMinusHuge = -1e30f;
 constexpr float kBoost = 8.f;            // as in the kernel for few rows
 constexpr float kSlack = 7.f;
@@ -311,18 +315,29 @@ __device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u,
   constexpr int LPR = D / 8, RPP = 32 / LPR;
   const AttnParams& a = p.a;
   const int j = lane % LPR;
-#pragma unroll 1
-  for (int local = 64 * w + lane / LPR; local < 64 * w + 64; local += RPP) {
-    const int r = r0 + (local & mask);
+  // row0 + r = qi * group + gi, carried along without a division a row
+  const int first = 64 * w + lane / LPR;
+  int local = first, r = r0 + (first & mask);
+  int qi = (u.row0 + r) / a.group, gi = u.row0 + r - qi * a.group;
+#pragma unroll 4
+  for (int i = 0; i < 64 / RPP; ++i) {
     const bool on = r < u.rows;
-    const int row = on ? u.row0 + r : 0;
-    const int qi = row / a.group;
-    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + (static_cast<size_t>(u.q0) + qi) * a.q_stride +
-                          static_cast<size_t>(u.head * a.group + row - qi * a.group) * D + j * 8;
+    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q);
+    if (on) src += (static_cast<size_t>(u.q0) + qi) * a.q_stride + static_cast<size_t>(u.head * a.group + gi) * D + j * 8;
     const uint32_t to = base + (j >> 3) * (kTileRows * 128) + local * 128 + (((j & 7) ^ (local & 7)) << 4);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(on ? src : reinterpret_cast<const uint16_t*>(a.q)),
-                 "r"(on ? 16 : 0)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
+    local += RPP;
+    r += RPP;
+    gi += RPP;
+    if ((local & mask) < RPP && i + 1 < 64 / RPP) {            // the period starts again
+      r = r0 + (local & mask);
+      qi = (u.row0 + r) / a.group;
+      gi = u.row0 + r - qi * a.group;
+    }
+    while (gi >= a.group) {
+      gi -= a.group;
+      ++qi;
+    }
   }
 }
 // Step 2, one thread for a row of the tile: the row times a power of two that takes its
@@ -331,33 +346,30 @@ __device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u,
 template <int D>
 __device__ __forceinline__ float convert_query(const AttnParams& a, uint32_t base, int row) {
   auto at = [&](int c) { return base + (c >> 3) * (kTileRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
-  auto load = [&](int c, uint32_t (&w)[4]) {
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at(c)));
-  };
+  uint32_t w[D / 8][4];
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3]) : "r"(at(c)));
   float amax = 0.f;
-#pragma unroll 4
-  for (int c = 0; c < D / 8; ++c) {
-    uint32_t w[4];
-    load(c, w);
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 f = kv_unpack16(w[e], a.bf16);
+      const float2 f = kv_unpack16(w[c][e], a.bf16);
       amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
     }
-  }
   int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8;
   e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
   const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll 4
+#pragma unroll
   for (int c = 0; c < D / 8; ++c) {
-    uint32_t w[4];
-    load(c, w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = kv_unpack16(w[i], a.bf16);
-      w[i] = kv_pack16(f.x * by, f.y * by, false);
+      const float2 f = kv_unpack16(w[c][i], a.bf16);
+      w[c][i] = kv_pack16(f.x * by, f.y * by, false);
     }
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(c)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(c)), "r"(w[c][0]), "r"(w[c][1]), "r"(w[c][2]), "r"(w[c][3])
+                 : "memory");
   }
   return a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
@@ -503,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
   const uint32_t tmem = ctrl->tmem;
 
   if (warp >= 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D>::kRest));
     if (warp == 17) {
       // ================= the CTA's pieces, one after the other =================
       if (lane == 0) {
@@ -737,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
     __syncwarp();
   } else if (warp >= 8) {
     // ================= loaders =================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D>::kLoad));
     const bool values = warp >= 8 + kLoaders;
     const int w = (warp - 8) & (kLoaders - 1);
     const KvCache& c = a.cache;
@@ -910,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
     }
   } else {
     // ================= softmax =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<D>::kSoftmax));
     const int x = warp >> 2;             // stream
     const int r = tid & 127;             // tensor-memory lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;

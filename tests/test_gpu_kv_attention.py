@@ -124,6 +124,20 @@ def test_bad_page_is_reported(hint):
     assert out[:20].isnan().all() and not out[20:].isnan().any()
 
 
+@pytest.mark.parametrize("hint", [1, 64])
+def test_bad_page_reaches_only_the_queries_that_see_it(hint):
+    """The page after the first ten queries' positions is outside the pool."""
+    s = ref.Setup([90], [40], 4, 1, 128, 16, "bf16", seed=27)
+    cache, ints = s.gpu()
+    ints[0][0, 4] = -3                      # positions 64 .. 79; queries at 50 .. 89
+    out, _ = cache.attention(s.q.cuda(), *ints, max_q=hint)
+    assert cache.status() == 1
+    bad = out.isnan()
+    assert not bad[:14].any() and bad[14:].all()
+    want = s.c.attend(s.q64()[:14], s.table, [64], [0, 14])
+    ref.check(out[:14].double().cpu().numpy(), np.zeros((14, 4)), (want[0], np.zeros((14, 4)), want[2]), "bf16")
+
+
 @pytest.mark.parametrize("lens,new,hq,hkv,d,page,dtype,k", [
     ([1], [1], 4, 1, 128, 64, "bf16", 1),
     ([900], [1], 64, 1, 128, 64, "bf16", 300),
