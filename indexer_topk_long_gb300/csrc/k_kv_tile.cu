@@ -30,14 +30,20 @@ namespace {
 
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;
-constexpr int kThreads = 20 * 32;
-constexpr int kLoaders = 4;              // warps for each operand, 32 keys of a tile each
-// Registers a thread: 96 at launch, moved from the loaders (D = 64: and the last
-// warpgroup) to the softmax, so that no role spills in its loop.
-template <int D>
-struct Regs {
-  static constexpr int kSoftmax = D == 64 ? 128 : 120, kLoad = 72, kRest = D == 64 ? 80 : 96;
-  static_assert(2 * kSoftmax + 2 * kLoad + kRest <= 5 * 96, "register split");
+constexpr int kLoaders = 4;              // warps that load a tile of an operand, 32 keys each
+// Warps of each role and registers a thread (launched evenly, then moved between the
+// warpgroups so that no role spills in its loop).  Narrow form (at most 64 rows): the two
+// streams' rows lie in the two halves of one row tile, so one warpgroup serves both, and
+// its place goes to a second set of loaders, one set for each stream.
+template <int D, bool NARROW>
+struct Roles {
+  static constexpr int kSoftmaxWarps = NARROW ? 4 : 8, kStreamWarps = kSoftmaxWarps / 2;
+  static constexpr int kSets = NARROW ? 2 : 1;                // of key and value loaders
+  static constexpr int kLoad = kSoftmaxWarps, kRest = kLoad + kSets * 2 * kLoaders;
+  static constexpr int kThreads = (kRest + 4) * 32;
+  static constexpr int kLaunchRegs = NARROW ? 80 : 96;
+  static constexpr int kSoftmaxRegs = NARROW ? 112 : D == 64 ? 128 : 120, kLoadRegs = 72, kRestRegs = NARROW || D == 64 ? 80 : 96;
+  static_assert(kSoftmaxWarps / 4 * kSoftmaxRegs + kSets * 2 * kLoadRegs + kRestRegs <= kThreads / 128 * kLaunchRegs, "register split");
 };
 constexpr float kMinusHuge = -1e30f;
 constexpr float kBoost = 8.f;            // as in the kernel for few rows
@@ -179,16 +185,16 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
 struct TileParams {
   AttnParams a;
   int pair;                              // 1: pair mode
+  int rows;                              // rows of a unit
   int row_tiles;                         // listed keys: row tiles of a group
   int slots;                             // row tiles over all sequences (an upper bound when dense)
 };
 
-__device__ __forceinline__ int unit_rows(const TileParams& p) { return p.pair ? 2 * kTileRows : kTileRows; }
 
 // Dense row tiles are numbered without a scan: sequence b's start at
 // cu_q[b] * group / rows + b, which leaves room for every row tile.
 __device__ __forceinline__ long long slot_start(const TileParams& p, int b) {
-  return static_cast<long long>(__ldg(p.a.batch.cu_q + b)) * p.a.group / unit_rows(p) + b;
+  return static_cast<long long>(__ldg(p.a.batch.cu_q + b)) * p.a.group / p.rows + b;
 }
 
 // Row tile `slot`: its fields, and the number of its key tiles (at least 1 on the
@@ -199,8 +205,8 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
   const AttnParams& a = p.a;
   if constexpr (SEL) {
     const int n = slot / p.row_tiles;
-    u.row0 = (slot - n * p.row_tiles) * kTileRows;
-    u.rows = min(a.group - u.row0, kTileRows);
+    u.row0 = (slot - n * p.row_tiles) * p.rows;
+    u.rows = min(a.group - u.row0, p.rows);
     u.b = kv_seq_of_query(a.batch, n);
     const KvSeq q = kv_seq(a.batch, a.cache, u.b);
     u.q0 = n;
@@ -223,12 +229,12 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
     }
     u.b = b;
     const KvSeq q = kv_seq(a.batch, a.cache, b);
-    const long long row0 = (slot - slot_start(p, b)) * unit_rows(p);
+    const long long row0 = (slot - slot_start(p, b)) * p.rows;
     const long long all = static_cast<long long>(q.nq) * a.group;
     tiles = 0;
     if (row0 < 0 || row0 >= all) return 0;
     u.row0 = static_cast<int>(row0);
-    u.rows = static_cast<int>(min(all - row0, static_cast<long long>(unit_rows(p))));
+    u.rows = static_cast<int>(min(all - row0, static_cast<long long>(p.rows)));
     u.q0 = q.q0;
     u.pos0 = q.pos0;
     u.p_lo = q.pos0 + u.row0 / a.group;
@@ -401,9 +407,11 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-template <int D, bool SEL>
-__global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_constant__ TileParams p) {
+template <int D, bool SEL, bool NARROW>
+__global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(const __grid_constant__ TileParams p) {
   using S = TileShape<D>;
+  using R = Roles<D, NARROW>;
+  constexpr int kThreads = R::kThreads;
   constexpr int NI = Map<D>::NI;
   extern __shared__ __align__(1024) unsigned char smem[];
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(smem + S::kQ + 2 * S::kStage + S::kMerge);
@@ -411,11 +419,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
   float* merge = reinterpret_cast<float*>(smem + S::kQ + 2 * S::kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);   // uniform
   const AttnParams& a = p.a;
-  const bool pair = p.pair != 0;
+  const bool pair = !NARROW && p.pair != 0;
   volatile int* abort_flag = &ctrl->abort_flag;
   int* status = a.status;
 
-  if (warp == 16) {
+  if (warp == R::kRest) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(smem_u32(&ctrl->kfull[i]), kLoaders);
@@ -423,17 +431,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         mbar_init(smem_u32(&ctrl->vfull[i]), kLoaders);
         mbar_init(smem_u32(&ctrl->vempty[i]), 1);
         mbar_init(smem_u32(&ctrl->sfull[i]), 2);
-        mbar_init(smem_u32(&ctrl->pfull[i]), 4);
+        mbar_init(smem_u32(&ctrl->pfull[i]), R::kStreamWarps);
         mbar_init(smem_u32(&ctrl->ofull[i]), 1);
         mbar_init(smem_u32(&ctrl->ufull[i]), 1);
-        mbar_init(smem_u32(&ctrl->uempty[i]), 8 + 2 * kLoaders + 2 + 2);
+        mbar_init(smem_u32(&ctrl->uempty[i]), R::kSoftmaxWarps + R::kSets * 2 * kLoaders + 2 + 2);
         mbar_init(smem_u32(&ctrl->qfull[i]), pair ? 8 : 2);
-        mbar_init(smem_u32(&ctrl->wg[i]), 128);
+        mbar_init(smem_u32(&ctrl->wg[i]), 32 * R::kStreamWarps);
       }
       mbar_init(smem_u32(&ctrl->qempty), 1);
       mbar_init(smem_u32(&ctrl->qraw), 2);
-      mbar_init(smem_u32(&ctrl->mfull), 4);
-      mbar_init(smem_u32(&ctrl->mempty), 4);
+      mbar_init(smem_u32(&ctrl->mfull), R::kStreamWarps);
+      mbar_init(smem_u32(&ctrl->mempty), R::kStreamWarps);
       mbar_init(smem_u32(&ctrl->drained), 1);
       ctrl->abort_flag = 0;
       mbar_fence_init();
@@ -450,14 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
     int tiles;
     if constexpr (SEL) {
       tiles = (a.k + kKeys - 1) / kKeys;
-      total = static_cast<long long>(p.slots) * a.cache.heads * tiles;
-      n_cta = static_cast<int>(min(static_cast<long long>(n_cta), total));
+      // Whole units in turn for as many waves as there are (neighbouring queries choose many
+      // of the same keys, so they run at the same time and L2 serves them); the line holds the rest.
+      const long long units = static_cast<long long>(p.slots) * a.cache.heads;
+      const long long whole = units / gridDim.x * gridDim.x;
+      total = (units - whole) * tiles;
+      n_cta = static_cast<int>(min(static_cast<long long>(n_cta), max(total, 1ll)));
       if (tid == 0) {
         const long long at = blockIdx.x * total / n_cta;
-        const long long unit = at / tiles;
+        const long long unit = whole + at / tiles;
         ctrl->at = at;
         ctrl->left = blockIdx.x < n_cta ? (blockIdx.x + 1) * total / n_cta - at : 0;
-        ctrl->t = static_cast<int>(at - unit * tiles);
+        ctrl->t = static_cast<int>(at % tiles);
         ctrl->head = static_cast<int>(unit % a.cache.heads);
         ctrl->slot = static_cast<int>(unit / a.cache.heads);
       }
@@ -514,17 +526,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
   tc_fence_after();
   const uint32_t tmem = ctrl->tmem;
 
-  if (warp >= 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D>::kRest));
-    if (warp == 17) {
+  if (warp >= R::kRest) {
+    if constexpr (R::kRestRegs < R::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kRestRegs));
+    if (warp == R::kRest + 1) {
       // ================= the CTA's pieces, one after the other =================
       if (lane == 0) {
         long long at = ctrl->at, left = ctrl->left;
         int slot = ctrl->slot, head = ctrl->head, t = ctrl->t, b = -1;
+        const int waves = SEL ? static_cast<int>(static_cast<long long>(p.slots) * a.cache.heads / gridDim.x) : 0;
         for (int un = 0;; ++un) {
           Unit u{};
           int tiles = 0, n = 0;
-          if (left > 0) {
+          if (un < waves) {
+            const long long unit = static_cast<long long>(un) * gridDim.x + blockIdx.x;
+            const int at_slot = static_cast<int>(unit / a.cache.heads);
+            u.n_tiles = decode_slot<SEL>(p, at_slot, -1, u, tiles);
+            u.head = static_cast<int>(unit - static_cast<long long>(at_slot) * a.cache.heads);
+            u.part = -1;
+          } else if (left > 0) {
             while ((n = decode_slot<SEL>(p, slot, b, u, tiles)) == 0) b = u.b, ++slot;   // a live slot lies ahead
             b = u.b;
             const int end = static_cast<int>(min(static_cast<long long>(n), t + left));
@@ -571,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
           if (u.n_tiles < 0) break;
         }
       }
-    } else if (warp >= 18) {
+    } else if (warp >= R::kRest + 2) {
       // ================= queries =================
       for (int un = 0;; ++un) {
         const int us = un & 1;
@@ -579,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         const Unit& u = ctrl->unit[us];
         if (u.n_tiles < 0) break;
         if (u.n_tiles > 0) {
-          const int w = warp - 18;
+          const int w = warp - R::kRest - 2;
           if (pair) {                    // one buffer; the softmax threads convert their rows
             if (un >= 1 && !mbar_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
             copy_queries<D>(p, u, q_sm, 0, 127, w, lane);
@@ -747,11 +766,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
       mbar_drain(smem_u32(&ctrl->drained), 0);
     }
     __syncwarp();
-  } else if (warp >= 8) {
+  } else if (warp >= R::kLoad) {
     // ================= loaders =================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D>::kLoad));
-    const bool values = warp >= 8 + kLoaders;
-    const int w = (warp - 8) & (kLoaders - 1);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kLoadRegs));
+    const int set = NARROW ? (warp - R::kLoad) / (2 * kLoaders) : 0;   // narrow: the stream it loads for
+    const bool values = ((warp - R::kLoad) / kLoaders & 1) != 0;
+    const int w = (warp - R::kLoad) & (kLoaders - 1);
     const KvCache& c = a.cache;
     const uint8_t* codes = values ? c.v_codes : c.k_codes;
     uint64_t* full = values ? ctrl->vfull : ctrl->kfull;
@@ -767,7 +787,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
       const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
       const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width;
-      const int end = u.first + u.n_tiles;
+      const int begin = u.first + set, end = u.first + u.n_tiles;
+      constexpr int kStep = R::kSets;    // a set's tiles lie that far apart
       // A tile's lookups run ahead of its data, each a whole tile ahead of its use: its
       // page (listed: first its key) is asked for two tiles before its codes are.
       struct Look {
@@ -858,27 +879,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
       Place cur{};
       Look near{}, far{};                // of the next tile and the one after it
       int far_key = -1;                  // listed: of the tile after those
-      if (u.n_tiles > 0) {
+      if (begin < end) {
         int key = -1, near_key = -1, then_key = -1;
         if constexpr (SEL) {
-          key = key_of(u.first);
-          near_key = key_of(u.first + 1);
-          then_key = key_of(u.first + 2);
-          far_key = key_of(u.first + 3);
+          key = key_of(begin);
+          near_key = key_of(begin + kStep);
+          then_key = key_of(begin + 2 * kStep);
+          far_key = key_of(begin + 3 * kStep);
         }
-        const Look first = look(u.first, key);
-        near = look(u.first + 1, near_key);
-        far = look(u.first + 2, then_key);
-        cur = place_tile(u.first, first);
+        const Look first = look(begin, key);
+        near = look(begin + kStep, near_key);
+        far = look(begin + 2 * kStep, then_key);
+        cur = place_tile(begin, first);
         load_tile(cur);
       }
 #pragma unroll 1
-      for (int ord = u.first; ord < end; ++ord) {
-        const int sx = pair ? 0 : (ord - u.first) & 1;
+      for (int ord = begin; ord < end; ord += kStep) {
+        const int sx = NARROW ? set : pair ? 0 : (ord - begin) & 1;
         const int n = cnt[sx];
         const int st = pair ? n & 1 : sx, use = pair ? n >> 1 : n;
         Place next{};
-        if (ord + 1 < end) next = place_tile(ord + 1, near);
+        if (ord + kStep < end) next = place_tile(ord + kStep, near);
         uint32_t factor = 0;
         float kg = cur.ks, vg = cur.vs;
         if constexpr (SEL) {
@@ -909,10 +930,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&full[st]));
-        if (ord + 1 < end) load_tile(next);
+        if (ord + kStep < end) load_tile(next);
         near = far;
-        far = look(ord + 3, far_key);
-        if constexpr (SEL) far_key = key_of(ord + 4);
+        far = look(ord + 3 * kStep, far_key);
+        if constexpr (SEL) far_key = key_of(ord + 4 * kStep);
         cur = next;
         ++cnt[sx];
       }
@@ -922,8 +943,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
     }
   } else {
     // ================= softmax =================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<D>::kSoftmax));
-    const int x = warp >> 2;             // stream
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftmaxRegs));
+    const int x = NARROW ? warp >> 1 : warp >> 2;             // stream
     const int r = tid & 127;             // tensor-memory lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + x * kKeys, o_col = tmem + lanes + 256 + x * D;
@@ -935,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
       if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
-      const bool twice = !pair && u.rows <= 64;
+      const bool twice = NARROW || (!pair && u.rows <= 64);
       const int row = pair ? x * kTileRows + r : twice ? r & 63 : r;
       const bool live = row < u.rows && (!twice || (r >> 6) == x);
       const bool warp_live = __any_sync(0xFFFFFFFFu, live);
@@ -1153,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
       if (writer) {
         // this thread's row goes out: whole result, or a piece to be joined
         const bool part = u.part >= 0;
-        const int rows_max = unit_rows(p);
+        const int rows_max = p.rows;
         constexpr int kRowFloats = D + 2;
         float* pd = a.part + static_cast<size_t>(max(u.part, 0)) * rows_max * kRowFloats;
         size_t at = 0;
@@ -1289,7 +1310,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
     // dense: queries that belong to no sequence have no unit
     if constexpr (!SEL) {
       if (x == 1) {
-        for (long long n = blockIdx.x * 128ll + r; n < a.batch.N; n += gridDim.x * 128ll) {
+        constexpr int kMine = 32 * R::kStreamWarps;             // this stream's threads
+        for (long long n = blockIdx.x * static_cast<long long>(kMine) + (r & (kMine - 1)); n < a.batch.N;
+             n += gridDim.x * static_cast<long long>(kMine)) {
           const KvSeq q = kv_seq(a.batch, a.cache, kv_seq_of_query(a.batch, static_cast<int>(n)));
           if (n >= q.q0 && n < q.q0 + q.nq) continue;
           uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + n * a.q_heads * D;
@@ -1302,21 +1325,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tile_kernel(const __grid_const
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == R::kRest) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D, bool SEL>
+template <int D, bool SEL, bool NARROW>
 cudaError_t init_tile() {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_tile_kernel<D, SEL>), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              TileShape<D>::kBytes);
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_tile_kernel<D, SEL, NARROW>),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, TileShape<D>::kBytes);
 }
 
 template <int D, bool SEL>
 cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
-  kv_tile_kernel<D, SEL><<<num_sms, kThreads, TileShape<D>::kBytes, stream>>>(p);
+  if (p.rows <= 64)
+    kv_tile_kernel<D, SEL, true><<<num_sms, Roles<D, true>::kThreads, TileShape<D>::kBytes, stream>>>(p);
+  else
+    kv_tile_kernel<D, SEL, false><<<num_sms, Roles<D, false>::kThreads, TileShape<D>::kBytes, stream>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -1327,24 +1353,28 @@ size_t kv_tile_part_floats(int num_sms) { return static_cast<size_t>(2) * num_sm
 int kv_tile_counters(int num_sms) { return 2 * num_sms; }
 
 cudaError_t kv_tile_init() {
-  cudaError_t e = init_tile<128, false>();
-  if (e == cudaSuccess) e = init_tile<128, true>();
-  if (e == cudaSuccess) e = init_tile<64, false>();
-  if (e == cudaSuccess) e = init_tile<64, true>();
-  return e;
+  const cudaError_t e[8] = {init_tile<128, false, false>(), init_tile<128, false, true>(), init_tile<128, true, false>(),
+                            init_tile<128, true, true>(),   init_tile<64, false, false>(), init_tile<64, false, true>(),
+                            init_tile<64, true, false>(),   init_tile<64, true, true>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
 }
 
 cudaError_t launch_kv_tile(const AttnParams& a, int max_q, int num_sms, cudaStream_t stream) {
   TileParams p{};
   p.a = a;
   const bool sel = a.idx != nullptr;
+  // Rows that one KV head's keys meet at a time: pairs of 128-row tiles where a sequence has
+  // that many, one tile, or a narrow one (max_q is a hint: more rows make more units).
+  const long long most = static_cast<long long>(a.group) * (sel ? 1 : max_q);
+  p.pair = !sel && most > kTileRows;
+  p.rows = p.pair ? 2 * kTileRows : most <= 64 ? 64 : kTileRows;
   if (sel) {
-    p.row_tiles = (a.group + kTileRows - 1) / kTileRows;
+    p.row_tiles = (a.group + p.rows - 1) / p.rows;
     p.slots = a.batch.N * p.row_tiles;
   } else {
-    p.pair = static_cast<long long>(max_q) * a.group > kTileRows;
-    const int rows = p.pair ? 2 * kTileRows : kTileRows;
-    p.slots = static_cast<int>(static_cast<long long>(a.batch.N) * a.group / rows) + a.batch.B;
+    p.slots = static_cast<int>(static_cast<long long>(a.batch.N) * a.group / p.rows) + a.batch.B;
   }
   if (a.dim == 128) return sel ? launch_tile<128, true>(p, num_sms, stream) : launch_tile<128, false>(p, num_sms, stream);
   return sel ? launch_tile<64, true>(p, num_sms, stream) : launch_tile<64, false>(p, num_sms, stream);

@@ -52,7 +52,7 @@ def test_many_rows(lens, new, hq, hkv, d, page, dtype):
     _dense(s)
 
 
-@pytest.mark.parametrize("max_q", [0, 1, 300])
+@pytest.mark.parametrize("max_q", [0, 1, 5, 15, 300])
 def test_any_hint_gives_the_same_answer(max_q):
     _dense(ref.Setup([260, 77, 1], [70, 1, 1], 6, 2, 128, 32, "bf16", seed=13), max_q=max_q)
 
@@ -90,7 +90,7 @@ def test_large_scores(new):
 def test_sequence_shorter_than_its_queries_and_empty():
     """Queries before the first token (and of an empty sequence) see nothing: 0 and -inf."""
     import torch
-    for hint in (1, 60):
+    for hint in (1, 12, 25, 60):
         s = ref.Setup([30, 30], [50, 4], 4, 1, 128, 16, "bf16", seed=17)
         s.lens = [30, 0]
         cache, ints = s.gpu()
