@@ -22,7 +22,9 @@
 namespace ltk {
 namespace {
 
-constexpr int kQPasses = 4;              // head rows per lane group in a rotation unit
+// Head rows per lane group in a rotation unit: few for a decode step (latency), more for
+// chunks (bytes in flight; a unit's look at its token's position is paid once).
+constexpr int kQPassesFew = 4, kQPassesMany = 8;
 
 struct Chunk {                           // 8 consecutive elements of one row, fp32
   float x[8];
@@ -122,8 +124,8 @@ __device__ __forceinline__ uint2 rescale_codes(uint2 w, float by) {
 
 // Queries: one warp rotates kQPasses * (32 / LPR) head rows of one token, the
 // table's row read once for all of them.
-template <int D>
-__device__ void rotate_queries(const AppendParams& p, long long unit) {
+template <int D, int kQPasses>
+__device__ __forceinline__ void rotate_queries(const AppendParams& p, long long unit) {
   constexpr int LPR = D / 8, RPP = 32 / LPR;
   const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR;
   const int per_token = (p.q_heads + kQPasses * RPP - 1) / (kQPasses * RPP);
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(128) kv_append_few_kernel(const AppendParams p
   constexpr int LPR = D / 8, RPP = 32 / LPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x >= kv_blocks) {
-    rotate_queries<D>(p, (blockIdx.x - kv_blocks) * 4 + warp);
+    rotate_queries<D, kQPassesFew>(p, (blockIdx.x - kv_blocks) * 4 + warp);
     return;
   }
   const KvCache& c = p.cache;
@@ -291,11 +293,11 @@ __global__ void __launch_bounds__(128) kv_append_few_kernel(const AppendParams p
 // pages, so its numbers start at (cu_q[b] + b (2 page - 2)) / page; numbers
 // beyond what it touches are empty.
 template <int D>
-__global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams p, long long kv_blocks) {
+__global__ void __launch_bounds__(256, 3) kv_append_kernel(const AppendParams p, long long kv_blocks) {
   constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = 16 / RPP;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (blockIdx.x >= kv_blocks) {
-    rotate_queries<D>(p, (blockIdx.x - kv_blocks) * warps + warp);
+    rotate_queries<D, kQPassesMany>(p, (blockIdx.x - kv_blocks) * warps + warp);
     return;
   }
   const KvCache& c = p.cache;
@@ -335,27 +337,27 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams p,
   const int j = lane % LPR, sub = lane / LPR;
   const uint16_t* k = reinterpret_cast<const uint16_t*>(p.k) + static_cast<size_t>(head) * D;
   const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + static_cast<size_t>(head) * D;
-  uint4 kr[PASSES], vr[PASSES];
-#pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = warp * 16 + i * RPP + sub;
-    kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-    if (r >= r_lo && r < r_hi) {
-      const size_t n = static_cast<size_t>(s.q0 + (p0 + r - s.pos0));
-      kr[i] = __ldcs(reinterpret_cast<const uint4*>(k + n * p.k_stride) + j);
-      vr[i] = __ldcs(reinterpret_cast<const uint4*>(v + n * p.v_stride) + j);
-    }
-  }
   const int h = p.rot >> 4;
   const float limit = 448.f * pow2f(kKvMaxExp);
   float k_max = 0.f, v_max = 0.f;
   uint32_t bad_rows = 0;
-  // Row r's rotated keys; done twice (for the maximum and for the codes), so that the raw
-  // 16-bit rows are all that stays in registers: 16 warps an SM instead of 12.
-  auto keys = [&](int i, bool& fine) {
+  // Rows are read and rotated twice, for the maximum and for the codes (the second time
+  // from L2): kept in registers, 64 of them, they left room for half the warps, and the
+  // queries' rotation in the same launch lives on warps (8192 tokens: 53 -> 45 us).
+  constexpr int AT_ONCE = 4;             // passes whose loads are in flight together
+  auto load = [&](int i, uint4& kr, uint4& vr) {
+    const int r = warp * 16 + i * RPP + sub;
+    kr = vr = make_uint4(0, 0, 0, 0);
+    if (r >= r_lo && r < r_hi) {
+      const size_t n = static_cast<size_t>(s.q0 + (p0 + r - s.pos0));
+      kr = __ldg(reinterpret_cast<const uint4*>(k + n * p.k_stride) + j);
+      vr = __ldg(reinterpret_cast<const uint4*>(v + n * p.v_stride) + j);
+    }
+  };
+  auto keys = [&](int i, const uint4& kr, bool& fine) {
     const int r = warp * 16 + i * RPP + sub;
     const bool live = r >= r_lo && r < r_hi;
-    Chunk kc = unpack(kr[i], p.bf16);
+    Chunk kc = unpack(kr, p.bf16);
     fine = true;
     if (p.cos != nullptr) {
       fine = !live || p0 + r < p.table_rows;
@@ -366,27 +368,33 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams p,
     }
     return kc;
   };
+#pragma unroll 1
+  for (int i0 = 0; i0 < PASSES; i0 += AT_ONCE) {
+    uint4 kr[AT_ONCE], vr[AT_ONCE];
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    bool fine;
-    const Chunk kc = keys(i, fine);
-    if (!fine) raise_status(p.status, kDevArg);
-    const Chunk vc = unpack(vr[i], p.bf16);
-    float ka = 0.f, va = 0.f;
+    for (int i = 0; i < AT_ONCE; ++i) load(i0 + i, kr[i], vr[i]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float a = fabsf(kc.x[e]), z = fabsf(vc.x[e]);
-      fine = fine && a <= limit && z <= limit;
-      ka = fmaxf(ka, a);
-      va = fmaxf(va, z);
-    }
-    const uint32_t votes = __ballot_sync(0xFFFFFFFFu, fine);
-    constexpr uint32_t row_mask = LPR == 32 ? 0xFFFFFFFFu : (1u << LPR) - 1u;
-    if (((votes >> (sub * LPR)) & row_mask) != row_mask) {
-      bad_rows |= 1u << i;
-    } else {
-      k_max = fmaxf(k_max, ka);
-      v_max = fmaxf(v_max, va);
+    for (int i = 0; i < AT_ONCE; ++i) {
+      bool fine;
+      const Chunk kc = keys(i0 + i, kr[i], fine);
+      if (!fine) raise_status(p.status, kDevArg);
+      const Chunk vc = unpack(vr[i], p.bf16);
+      float ka = 0.f, va = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = fabsf(kc.x[e]), z = fabsf(vc.x[e]);
+        fine = fine && a <= limit && z <= limit;
+        ka = fmaxf(ka, a);
+        va = fmaxf(va, z);
+      }
+      const uint32_t votes = __ballot_sync(0xFFFFFFFFu, fine);
+      constexpr uint32_t row_mask = LPR == 32 ? 0xFFFFFFFFu : (1u << LPR) - 1u;
+      if (((votes >> (sub * LPR)) & row_mask) != row_mask) {
+        bad_rows |= 1u << (i0 + i);
+      } else {
+        k_max = fmaxf(k_max, ka);
+        v_max = fmaxf(v_max, va);
+      }
     }
   }
   __shared__ float red[2][8];
@@ -418,25 +426,31 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams p,
     c.k_scale[block] = pow2f(ke);
     c.v_scale[block] = pow2f(ve);
   }
+#pragma unroll 1
+  for (int i0 = 0; i0 < PASSES; i0 += AT_ONCE) {
+    uint4 kr[AT_ONCE], vr[AT_ONCE];
 #pragma unroll
-  for (int i = 0; i < PASSES; ++i) {
-    const int r = warp * 16 + i * RPP + sub;
-    const size_t o = (block * c.page + r) * D + j * 8;
-    bool fine;
-    const Chunk kc = keys(i, fine);
-    if (r >= r_lo && r < r_hi) {
-      const bool bad = (bad_rows >> i) & 1u;
-      const Chunk vc = unpack(vr[i], p.bf16);
-      *reinterpret_cast<uint2*>(c.k_codes + o) = bad ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : encode(kc, k_inv);
-      *reinterpret_cast<uint2*>(c.v_codes + o) = bad ? make_uint2(0u, 0u) : encode(vc, v_inv);
-    } else if (r < r_lo) {
-      if (k_by != 1.f) {
-        uint2* w = reinterpret_cast<uint2*>(c.k_codes + o);
-        *w = rescale_codes(*w, k_by);
-      }
-      if (v_by != 1.f) {
-        uint2* w = reinterpret_cast<uint2*>(c.v_codes + o);
-        *w = rescale_codes(*w, v_by);
+    for (int i = 0; i < AT_ONCE; ++i) load(i0 + i, kr[i], vr[i]);
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int r = warp * 16 + (i0 + i) * RPP + sub;
+      const size_t o = (block * c.page + r) * D + j * 8;
+      bool fine;
+      const Chunk kc = keys(i0 + i, kr[i], fine);
+      if (r >= r_lo && r < r_hi) {
+        const bool bad = (bad_rows >> (i0 + i)) & 1u;
+        const Chunk vc = unpack(vr[i], p.bf16);
+        *reinterpret_cast<uint2*>(c.k_codes + o) = bad ? make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu) : encode(kc, k_inv);
+        *reinterpret_cast<uint2*>(c.v_codes + o) = bad ? make_uint2(0u, 0u) : encode(vc, v_inv);
+      } else if (r < r_lo) {
+        if (k_by != 1.f) {
+          uint2* w = reinterpret_cast<uint2*>(c.k_codes + o);
+          *w = rescale_codes(*w, k_by);
+        }
+        if (v_by != 1.f) {
+          uint2* w = reinterpret_cast<uint2*>(c.v_codes + o);
+          *w = rescale_codes(*w, v_by);
+        }
       }
     }
   }
@@ -454,7 +468,7 @@ cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t st
   const long long slots = (p.batch.N + static_cast<long long>(p.batch.B) * (2 * page - 2)) / page;
   const long long kv_blocks = few ? (static_cast<long long>(p.batch.N) * p.cache.heads + 3) / 4 : slots * p.cache.heads;
   const int warps = few ? 4 : page / 16;
-  const int rows = kQPasses * (32 / (p.dim / 8));
+  const int rows = (few ? kQPassesFew : kQPassesMany) * (32 / (p.dim / 8));
   const long long units = p.q != nullptr ? static_cast<long long>(p.batch.N) * ((p.q_heads + rows - 1) / rows) : 0;
   const long long blocks = kv_blocks + (units + warps - 1) / warps;
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
