@@ -84,6 +84,7 @@ struct Ctrl {
   float rowf[512];
   long long at, left;                    // the CTA's piece of the line
   int slot, head, t;                     // where it begins
+  Unit first;                            // dense: the row tile there, decoded
 };
 
 template <int D>
@@ -321,29 +322,24 @@ __device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u,
   constexpr int LPR = D / 8, RPP = 32 / LPR;
   const AttnParams& a = p.a;
   const int j = lane % LPR;
-  // row0 + r = qi * group + gi, carried along without a division a row
-  const int first = 64 * w + lane / LPR;
-  int local = first, r = r0 + (first & mask);
-  int qi = (u.row0 + r) / a.group, gi = u.row0 + r - qi * a.group;
+  // row0 + r is head (row0 % group + r) % group of query row0 / group + (row0 % group + r) / group:
+  // one division, then products with 2^32 / group rounded up, exact for the at most
+  // 256 + group rows meant here while group^2 stays below 2^31
+  const int q0 = u.row0 / a.group, g0 = u.row0 - q0 * a.group;
+  const uint32_t magic = static_cast<uint32_t>((0x100000000ull + a.group - 1) / a.group);   // group 1: wraps to 0
+  const uint16_t* head = reinterpret_cast<const uint16_t*>(a.q) + (static_cast<size_t>(u.q0) + q0) * a.q_stride +
+                         static_cast<size_t>(u.head) * a.group * D + j * 8;
+  const uint32_t column = base + (j >> 3) * (kTileRows * 128);
 #pragma unroll 4
   for (int i = 0; i < 64 / RPP; ++i) {
+    const int local = 64 * w + lane / LPR + i * RPP;
+    const int r = r0 + (local & mask);
     const bool on = r < u.rows;
-    const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q);
-    if (on) src += (static_cast<size_t>(u.q0) + qi) * a.q_stride + static_cast<size_t>(u.head * a.group + gi) * D + j * 8;
-    const uint32_t to = base + (j >> 3) * (kTileRows * 128) + local * 128 + (((j & 7) ^ (local & 7)) << 4);
+    const int x = g0 + r;
+    const int qi = a.group == 1 ? x : a.group > 32768 ? x / a.group : static_cast<int>(__umulhi(static_cast<uint32_t>(x), magic));
+    const uint16_t* src = on ? head + qi * a.q_stride + (x - qi * a.group) * D : reinterpret_cast<const uint16_t*>(a.q);
+    const uint32_t to = column + local * 128 + (((j & 7) ^ (local & 7)) << 4);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
-    local += RPP;
-    r += RPP;
-    gi += RPP;
-    if ((local & mask) < RPP && i + 1 < 64 / RPP) {            // the period starts again
-      r = r0 + (local & mask);
-      qi = (u.row0 + r) / a.group;
-      gi = u.row0 + r - qi * a.group;
-    }
-    while (gi >= a.group) {
-      gi -= a.group;
-      ++qi;
-    }
   }
 }
 // Step 2, one thread for a row of the tile: the row times a power of two that takes its
@@ -478,9 +474,10 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       const int each = (p.slots + kThreads - 1) / kThreads;
       const int s0 = min(tid * each, p.slots), s1 = min(s0 + each, p.slots);
       long long mine = 0;
-      int b = -1;
+      int b = -1, n = 0;
       for (int s = s0; s < s1; ++s) {
-        mine += decode_slot<SEL>(p, s, b, u, tiles);
+        n = decode_slot<SEL>(p, s, b, u, tiles);
+        mine += n;
         b = u.b;
       }
       long long incl = mine;
@@ -505,9 +502,12 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           long long x = before;
           b = -1;
           for (int s = s0; s < s1; ++s) {
-            const int n = decode_slot<SEL>(p, s, b, u, tiles);
+            if (each > 1) n = decode_slot<SEL>(p, s, b, u, tiles);   // else still at hand
             b = u.b;
             if (in < x + n) {
+              u.n_tiles = n;             // on the line, and to see
+              u.first = tiles;
+              ctrl->first = u;
               ctrl->at = at;
               ctrl->left = (blockIdx.x + 1) * total / n_cta - at;
               ctrl->t = static_cast<int>(in - x);
@@ -544,7 +544,13 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
             u.head = static_cast<int>(unit - static_cast<long long>(at_slot) * a.cache.heads);
             u.part = -1;
           } else if (left > 0) {
-            while ((n = decode_slot<SEL>(p, slot, b, u, tiles)) == 0) b = u.b, ++slot;   // a live slot lies ahead
+            if (!SEL && un == 0) {
+              u = ctrl->first;
+              n = u.n_tiles;
+              tiles = u.first;
+            } else {
+              while ((n = decode_slot<SEL>(p, slot, b, u, tiles)) == 0) b = u.b, ++slot;   // a live slot lies ahead
+            }
             b = u.b;
             const int end = static_cast<int>(min(static_cast<long long>(n), t + left));
             const long long u0 = at - t, u1 = u0 + n;
@@ -993,8 +999,8 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           } else {
             masked = !(key0 + kKeys - 1 <= u.p_lo && (a.window <= 0 || key0 > u.p_hi - a.window || key0 + kKeys <= a.sinks));
           }
-          // Columns from here on still want their weights: all when the tile is masked or the
-          // unit's first, else none, or those from where a weight outgrew the slack.
+          // 32-column pieces from here on still want their weights: all when the tile is masked
+          // or the unit's first, else none, or those from where a weight outgrew the slack.
           int from = masked || i == 0 ? 0 : 4;
           if (from != 0) {
             // One pass with the maximum as it stands, half a tile at a time; a half's weights
@@ -1041,89 +1047,76 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
               }
             }
           }
-          if (from < 4) {
-            // this row's visible keys of 32 columns as bits
-            auto seen_of = [&](int c) -> uint32_t {
-              if (!masked) return 0xFFFFFFFFu;
+          // The general form: 32 columns at a time with masks, the maximum moving as it must.
+#pragma unroll 1
+          for (int c = from; c < 4; ++c) {
+            float s[32];
+            tmem_ld32(s_col + 32 * c, s);
+            uint32_t seen = 0xFFFFFFFFu;   // this row's visible keys of the 32
+            if (masked) {
               if constexpr (SEL) {
-                return m.valid[c];
+                seen = m.valid[c];
               } else {
                 auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };   // keys < n
                 const int k0 = key0 + 32 * c;
-                uint32_t seen = below(pos + 1 - k0);
+                seen = below(pos + 1 - k0);
                 if (a.window > 0) seen &= ~below(pos - a.window + 1 - k0) | below(a.sinks - k0);
-                return seen;
               }
-            };
-            float mx = -inf;
-            float s[16];
-#pragma unroll 1
-            for (int c = 2 * from; c < 8; ++c) {
-              tmem_ld32x16(s_col + 16 * c, s);
-              const uint32_t seen = seen_of(c >> 1) >> (16 * (c & 1));
-              tmem_wait_ld_tied(s);
-              float g = -inf;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) g = fmaxf(g, (seen >> e) & 1u ? s[e] : -inf);
-              mx = fmaxf(mx, fmaf(g, f * m.ks[c], m.lv[c]));
             }
-            if (__any_sync(0xFFFFFFFFu, mx > M + (kBoost + kSlack))) {
-              const float top = fmaxf(M, mx - kBoost);
+            const float fa0 = f * m.ks[2 * c], fa1 = f * m.ks[2 * c + 1], fb0 = m.lv[2 * c], fb1 = m.lv[2 * c + 1];
+            tmem_ld32_wait(s);
+            float mx[4] = {-inf, -inf, -inf, -inf};
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float t = fmaf(s[e], e < 16 ? fa0 : fa1, e < 16 ? fb0 : fb1);
+              s[e] = (seen >> e) & 1u ? t : -inf;   // after the scale, which may be NaN (a page outside the pool)
+              mx[e & 3] = fmaxf(mx[e & 3], s[e]);
+            }
+            const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (__any_sync(0xFFFFFFFFu, most > M + (kBoost + kSlack))) {
+              // what was summed and stored so far follows the new maximum
+              const float top = fmaxf(M, most - kBoost);
               const float by = exp2_approx(M - top);
               M = top;
               l *= by;
+              uint32_t w[16];
+              float v[16];
               if (i > 0) {               // scores are complete, so the last value product is too
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                  tmem_ld32x16(o_col + 16 * c, s);
-                  tmem_wait_ld_tied(s);
-                  uint32_t w[16];
+                for (int q = 0; q < D / 16; ++q) {
+                  tmem_ld32x16(o_col + 16 * q, v);
+                  tmem_wait_ld_tied(v);
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(s[e] * by);
-                  tmem_st16(o_col + 16 * c, w);
+                  for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * by);
+                  tmem_st16(o_col + 16 * q, w);
                 }
               }
-              if (from != 0) {           // the first half's weights are there already
-                const __half2 by2 = __float2half2_rn(by);
+              const __half2 by2 = __float2half2_rn(by);
 #pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                  tmem_st_wait();
-                  tmem_ld32x16(s_col + 16 * c, s);
-                  tmem_wait_ld_tied(s);
-                  uint32_t w[16];
+              for (int q = 0; q < c; ++q) {        // weights of this tile
+                tmem_st_wait();
+                tmem_ld32x16(s_col + 16 * q, v);
+                tmem_wait_ld_tied(v);
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) {
-                    const uint32_t x2 = __float_as_uint(s[e]);
-                    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&x2), by2);
-                    w[e] = *reinterpret_cast<const uint32_t*>(&v);
-                  }
-                  tmem_st16(s_col + 16 * c, w);
+                for (int e = 0; e < 16; ++e) {
+                  const uint32_t x2 = __float_as_uint(v[e]);
+                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x2), by2);
+                  w[e] = *reinterpret_cast<const uint32_t*>(&y);
                 }
+                tmem_st16(s_col + 16 * q, w);
               }
             }
-#pragma unroll 1
-            for (int c = 2 * from; c < 8; c += 2) {
-              uint32_t pk[16];
+            uint32_t pk[16];
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                tmem_ld32x16(s_col + 16 * (c + h), s);
-                const uint32_t seen = seen_of(c >> 1) >> (16 * h);
-                const float fa = f * m.ks[c + h], fb = m.lv[c + h] - M;
-                tmem_wait_ld_tied(s);
-                float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  const float s0 = (seen >> e) & 1u ? fmaf(s[e], fa, fb) : -inf;
-                  const float s1 = (seen >> (e + 1)) & 1u ? fmaf(s[e + 1], fa, fb) : -inf;
-                  const float w0 = exp2_approx(s0), w1 = exp2_approx(s1);
-                  sum0 += w0;
-                  sum1 += w1;
-                  pk[8 * h + e / 2] = pack_f16(w0, w1);
-                }
-                l = fmaf(sum0 + sum1, m.iv[c + h], l);
-              }
-              tmem_st16(s_col + 8 * c, pk);
+            for (int e = 0; e < 32; e += 2) {
+              const float w0 = exp2_approx(s[e] - M), w1 = exp2_approx(s[e + 1] - M);
+              sum[(e >> 4) * 2] += w0;
+              sum[(e >> 4) * 2 + 1] += w1;
+              pk[e / 2] = pack_f16(w0, w1);
             }
+            l = fmaf(sum[0] + sum[1], m.iv[2 * c], fmaf(sum[2] + sum[3], m.iv[2 * c + 1], l));
+            tmem_st16(s_col + 16 * c, pk);
           }
           tmem_st_wait();
         }
