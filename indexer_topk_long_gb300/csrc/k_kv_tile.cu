@@ -187,6 +187,7 @@ struct TileParams {
   AttnParams a;
   int pair;                              // 1: pair mode
   int rows;                              // rows of a unit
+  uint32_t group_magic;                  // 2^32 / group rounded up (0 for a group of 1)
   int row_tiles;                         // listed keys: row tiles of a group
   int slots;                             // row tiles over all sequences (an upper bound when dense)
 };
@@ -326,7 +327,6 @@ __device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u,
   // one division, then products with 2^32 / group rounded up, exact for the at most
   // 256 + group rows meant here while group^2 stays below 2^31
   const int q0 = u.row0 / a.group, g0 = u.row0 - q0 * a.group;
-  const uint32_t magic = static_cast<uint32_t>((0x100000000ull + a.group - 1) / a.group);   // group 1: wraps to 0
   const uint16_t* head = reinterpret_cast<const uint16_t*>(a.q) + (static_cast<size_t>(u.q0) + q0) * a.q_stride +
                          static_cast<size_t>(u.head) * a.group * D + j * 8;
   const uint32_t column = base + (j >> 3) * (kTileRows * 128);
@@ -336,7 +336,7 @@ __device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u,
     const int r = r0 + (local & mask);
     const bool on = r < u.rows;
     const int x = g0 + r;
-    const int qi = a.group == 1 ? x : a.group > 32768 ? x / a.group : static_cast<int>(__umulhi(static_cast<uint32_t>(x), magic));
+    const int qi = a.group == 1 ? x : a.group > 32768 ? x / a.group : static_cast<int>(__umulhi(static_cast<uint32_t>(x), p.group_magic));
     const uint16_t* src = on ? head + qi * a.q_stride + (x - qi * a.group) * D : reinterpret_cast<const uint16_t*>(a.q);
     const uint32_t to = column + local * 128 + (((j & 7) ^ (local & 7)) << 4);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
@@ -576,6 +576,11 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           } else {
             u.n_tiles = -1;
           }
+          const int us = un & 1;
+          if (un >= 2 && !mbar_wait(smem_u32(&ctrl->uempty[us]), ((un >> 1) - 1) & 1, abort_flag, status)) break;
+          ctrl->unit[us] = u;
+          mbar_arrive(smem_u32(&ctrl->ufull[us]));
+          if (u.n_tiles < 0) break;
           if (!SEL && left > 0) {
             // the rest of the row tiles may be empty up to the next head
             Unit v;
@@ -589,11 +594,6 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
               }
             }
           }
-          const int us = un & 1;
-          if (un >= 2 && !mbar_wait(smem_u32(&ctrl->uempty[us]), ((un >> 1) - 1) & 1, abort_flag, status)) break;
-          ctrl->unit[us] = u;
-          mbar_arrive(smem_u32(&ctrl->ufull[us]));
-          if (u.n_tiles < 0) break;
         }
       }
     } else if (warp >= R::kRest + 2) {
@@ -1264,6 +1264,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
             __threadfence();
             const size_t slot_floats = static_cast<size_t>(rows_max) * kRowFloats;
             float top = kMinusHuge, sum = 0.f;
+#pragma unroll 4
             for (int cta = u.c0; cta <= u.c1; ++cta) {
               const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part + (2 * cta + (cta == u.c0 ? 1 : 0)) * slot_floats) + row);
               const float next = fmaxf(top, v.x);
@@ -1357,6 +1358,7 @@ cudaError_t kv_tile_init() {
 cudaError_t launch_kv_tile(const AttnParams& a, int max_q, int num_sms, cudaStream_t stream) {
   TileParams p{};
   p.a = a;
+  p.group_magic = static_cast<uint32_t>((0x100000000ull + a.group - 1) / a.group);
   const bool sel = a.idx != nullptr;
   // Rows that one KV head's keys meet at a time: pairs of 128-row tiles where a sequence has
   // that many, one tile, or a narrow one (max_q is a hint: more rows make more units).
