@@ -24,7 +24,8 @@ namespace ltk {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 2;            // one merges a piece while the other streams
+// 12 warps an SM: with 8, the dependent arithmetic of two warps a scheduler bound the kernel.
+constexpr int kCtasPerSm = 3;
 constexpr int kThreads = kWarps * 32;
 constexpr int kGroups = 2;               // 16-key groups a warp takes from a tile
 constexpr int kWarpKeys = 16 * kGroups;
@@ -41,13 +42,17 @@ struct RowsSmem {
   static constexpr int kStageBytes = kWarpKeys * D * 2;
   static constexpr int kMetaFloats = 3 * kWarpKeys;           // ks, vs, valid of each key
   static constexpr int kWarpBytes = kStages * (kStageBytes + kMetaFloats * 4);
-  static constexpr int kMergeBytes = kWarps * kRowsPerUnit * (D + 2) * 4;
-  static constexpr int kBytes = kWarps * kWarpBytes + kMergeBytes;
+  static constexpr int kBytes = kWarps * kWarpBytes + kWarps * kRowsPerUnit * 2 * 4;   // and each row's (M, l)
+  // at a piece's end a warp's results take the place of the stage it has just read
+  static_assert(kStageBytes == kRowsPerUnit * D * 4, "merge buffer");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
   const int n = on ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -77,6 +82,12 @@ __device__ __forceinline__ int place(int r, int chunk) {
     const int slot = (r & ~1) | ((r ^ (r >> 1)) & 1);
     return slot * 64 + ((chunk ^ (((slot >> 2) & 1) << 1)) << 4);
   }
+}
+
+// The place of row i * (rows a warp copies at once) + r, given row r's: `at` = place(r, chunk).
+template <int D>
+__device__ __forceinline__ uint32_t place_next(uint32_t at, int i) {
+  return (D == 128 ? at ^ ((i & 1) << 6) : at) + i * 512;
 }
 
 struct Unit {
@@ -259,8 +270,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
   unsigned char* ring = smem + warp * S::kWarpBytes;
   float* meta = reinterpret_cast<float*>(ring + kStages * S::kStageBytes);
   const uint32_t ring_u = smem_u32(ring), meta_u = smem_u32(meta);
-  float* merge_o = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);     // [warp][16][D]
-  float* merge_ml = merge_o + kWarps * kRowsPerUnit * D;                        // [warp][16][2]
+  float* merge_ml = reinterpret_cast<float*>(smem + kWarps * S::kWarpBytes);    // [warp][16][2]
 
   // --- producer: one tile's 32 keys of this warp into a stage -----------------------------
   Cursor pc = head;                      // producer cursor
@@ -290,6 +300,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       const uint32_t mu = meta_u + stage_in * S::kMetaFloats * 4;
       constexpr int kPer = CPR / 2;      // copies of a group, lane and operand
       const int cr = lane / CPR, ch = lane % CPR;
+      const uint32_t at0 = place<D>(cr, ch);
       if constexpr (SEL) {
         const int key = feed.key <= pc.w.pos0 ? feed.key : -1;
         int page = -1;
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
             const int r = i * (32 / CPR) + cr;
             const long long rr = __shfl_sync(0xFFFFFFFFu, row, 16 * h + r);
             const size_t o = rr >= 0 ? static_cast<size_t>(rr) * D + ch * 16 : 0;
-            const uint32_t at = 16 * h * D + place<D>(r, ch);
+            const uint32_t at = 16 * h * D + place_next<D>(at0, i);
             cp_async16(kd + at, p.cache.k_codes + o, rr >= 0);
             cp_async16(vd + at, p.cache.v_codes + o, rr >= 0);
           }
@@ -342,15 +353,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
             }
           }
           const size_t o = (blk * p.cache.page + (first & (p.cache.page - 1))) * D + lane * 16;
+          const uint8_t *ks = p.cache.k_codes + o, *vs = p.cache.v_codes + o;
           const int rows = known ? pc.w.len - first : 0;      // of the group's 16
+          if (rows >= 16) {
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int r = i * (32 / CPR) + cr;
-            const bool on = r < rows;
-            const size_t oo = on ? o + i * 512 : 0;
-            const uint32_t at = 16 * h * D + place<D>(r, ch);
-            cp_async16(kd + at, p.cache.k_codes + oo, on);
-            cp_async16(vd + at, p.cache.v_codes + oo, on);
+            for (int i = 0; i < kPer; ++i) {
+              const uint32_t at = 16 * h * D + place_next<D>(at0, i);
+              cp_async16(kd + at, ks + i * 512);
+              cp_async16(vd + at, vs + i * 512);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+              const bool on = i * (32 / CPR) + cr < rows;
+              const uint32_t at = 16 * h * D + place_next<D>(at0, i);
+              cp_async16(kd + at, on ? ks + i * 512 : p.cache.k_codes, on);
+              cp_async16(vd + at, on ? vs + i * 512 : p.cache.v_codes, on);
+            }
           }
         }
       }
@@ -598,6 +617,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     }
 
     // --- the piece's end: warps of the CTA, then CTAs of the unit -------------------------
+    // All warps have read the same number of stages, so the free one is the same for all.
+    const int spare = stage_out == 0 ? kStages - 1 : stage_out - 1;
+    auto merge_of = [&](int w) { return reinterpret_cast<float*>(smem + w * S::kWarpBytes + spare * S::kStageBytes); };
+    __syncwarp();
 #pragma unroll
     for (int hlf = 0; hlf < 2; ++hlf) {
       l[hlf] += __shfl_xor_sync(0xFFFFFFFFu, l[hlf], 1);
@@ -609,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
         merge_ml[(warp * kRowsPerUnit + r) * 2 + 1] = l[hlf];
       }
       // element e of n-tile nt is column (2 cq + e) * NT + nt
-      float* dst = merge_o + (warp * kRowsPerUnit + r) * D;
+      float* dst = merge_of(warp) + r * D;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -651,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
         const float by = exp2_approx(merge_ml[(w * kRowsPerUnit + r) * 2] - mx);
         sum = fmaf(merge_ml[(w * kRowsPerUnit + r) * 2 + 1], by, sum);
         const int at = ch ^ (((ch >> 3) & 3) | ((r & 1) << 2));
-        const float4 v = *reinterpret_cast<const float4*>(merge_o + (w * kRowsPerUnit + r) * D + at * 4);
+        const float4 v = *reinterpret_cast<const float4*>(merge_of(w) + r * D + at * 4);
         acc.x = fmaf(v.x, by, acc.x);
         acc.y = fmaf(v.y, by, acc.y);
         acc.z = fmaf(v.z, by, acc.z);
