@@ -51,15 +51,29 @@ bool rows_ok(const void* p, long long stride, int heads, int dim) {
   return kv_aligned(p) && stride >= static_cast<long long>(heads) * dim && stride % 8 == 0;
 }
 
-// The kernel for few rows reads a head's keys once for every 16 rows, the tile kernel once
-// for 128, at some 25 us more to start.  Listed keys: the first takes 16-row, 256-key pieces
-// at 3.5 us each and SM.
+// The kernel for few rows goes over a head's keys once for every 16 rows, the tile kernel once
+// for 64, 128 or 256, at some 20 us more to start, meet and part.  Measured in microseconds
+// that one SM takes for 128 keys: 0.85 for 16 rows by the first, 1.62 for a narrow tile (64
+// rows), 1.8 for a whole one or a pair by the second.  For instance (D = 128, one KV head of
+// 64 query heads, 2048 listed keys): 48 queries 33 us by the first and 37 by the second, 128
+// queries 62 and 47; 16 rows, 8 KV heads, 512 queries of 2048 listed keys 376 and 726; 112
+// rows, 16 sequences of 1024 tokens 25 and 37; chunks of 2048 queries 10 times the second's.
+// How long sequences are is only known on the device: a third of the page table is assumed.
 bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
-  const long long rows = static_cast<long long>(p.group) * (p.idx != nullptr ? 1 : max_q);
+  const double rows = static_cast<double>(p.group) * (p.idx != nullptr ? 1 : max_q);
   if (rows <= kRowsPerUnit) return true;
-  if (p.idx == nullptr) return false;
-  const long long pieces = static_cast<long long>(p.batch.N) * p.cache.heads * ((p.group + 15) / 16) * ((p.k + 255) / 256);
-  return pieces <= 8ll * num_sms;
+  const double by_rows = 0.85 * std::ceil(rows / 16.0);
+  const double by_tiles = rows <= 64 ? 1.62 : 1.8 * std::ceil(rows / 256.0);
+  double units = p.cache.heads, keys;
+  if (p.idx != nullptr) {
+    units *= p.batch.N;
+    keys = p.k;
+  } else {
+    units *= p.batch.B;
+    keys = static_cast<double>(p.batch.width) * p.cache.page / 3.0;
+    if (p.window > 0) keys = std::min(keys, static_cast<double>(p.window) + p.sinks + max_q);
+  }
+  return units * std::ceil(keys / 128.0) * (by_rows - by_tiles) <= 15.0 * num_sms;
 }
 
 KvBatch batch_of(const ltk_kv_batch* b) {
