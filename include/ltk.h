@@ -323,6 +323,8 @@ typedef struct {
   int heads;
   int dim;
   int page;
+  int engine;        /* attention kernel: 0 chosen by measured costs (see kv_api.cu),
+                        1 the one for few rows per KV head, 2 the tensor-core tiles */
   void* k_codes;
   void* v_codes;
   float* k_scale;

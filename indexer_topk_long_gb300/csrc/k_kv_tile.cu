@@ -109,6 +109,26 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Bounded wait of a whole warp, the same answer for all its lanes: false when another role
+// gave up or the wait exceeds kWaitLimitNs (then this one gives up: abort flag and status).
+// It sleeps from the second look on, since polling takes issue slots from the softmax.
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      raise_status(status, kDevTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  return __all_sync(0xFFFFFFFFu, lane_wait(bar, parity, abort_flag, status)) != 0;
+}
+
 // MMAs are issued by one lane that elect.sync picks.  Behind elect.sync the compiler
 // keeps descriptors in uniform registers and an MMA costs four instructions; behind
 // `lane == 0` it moved each operand there first, and with busy softmax warps on the
@@ -471,6 +491,12 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       }
     } else {
       long long* sums = reinterpret_cast<long long*>(smem);   // free until the first queries come
+      // Row tiles are numbered by cu_q, so it has to rise within [0, N]; else nothing is done.
+      bool rises = true;
+      for (int i = tid; i < a.batch.B; i += kThreads) {
+        const int at = __ldg(a.batch.cu_q + i), to = __ldg(a.batch.cu_q + i + 1);
+        rises = rises && at >= 0 && at <= to && to <= a.batch.N;
+      }
       const int each = (p.slots + kThreads - 1) / kThreads;
       const int s0 = min(tid * each, p.slots), s1 = min(s0 + each, p.slots);
       long long mine = 0;
@@ -487,13 +513,14 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       }
       if (lane == 31) sums[warp] = incl;
       if (tid == 0) ctrl->left = 0;
-      __syncthreads();
+      const bool wrong = __syncthreads_or(rises ? 0 : 1) != 0;
+      if (wrong && tid == 0) raise_status(status, kDevArg);
       long long before = incl - mine, one = 0;                // one: a head's tiles
       for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += sums[w];
         one += sums[w];
       }
-      total = one * a.cache.heads;
+      total = wrong ? 0 : one * a.cache.heads;
       n_cta = static_cast<int>(min(static_cast<long long>(n_cta), max(total, 1ll)));
       if (total > 0 && blockIdx.x < n_cta) {
         const long long at = blockIdx.x * total / n_cta;
@@ -549,7 +576,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
               n = u.n_tiles;
               tiles = u.first;
             } else {
-              while ((n = decode_slot<SEL>(p, slot, b, u, tiles)) == 0) b = u.b, ++slot;   // a live slot lies ahead
+              n = decode_slot<SEL>(p, slot, b, u, tiles);
             }
             b = u.b;
             const int end = static_cast<int>(min(static_cast<long long>(n), t + left));
@@ -577,15 +604,15 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
             u.n_tiles = -1;
           }
           const int us = un & 1;
-          if (un >= 2 && !mbar_wait(smem_u32(&ctrl->uempty[us]), ((un >> 1) - 1) & 1, abort_flag, status)) break;
+          if (un >= 2 && !lane_wait(smem_u32(&ctrl->uempty[us]), ((un >> 1) - 1) & 1, abort_flag, status)) break;
           ctrl->unit[us] = u;
           mbar_arrive(smem_u32(&ctrl->ufull[us]));
           if (u.n_tiles < 0) break;
           if (!SEL && left > 0) {
-            // the rest of the row tiles may be empty up to the next head
+            // on to the next row tile with something in it (there is one: the line goes on)
             Unit v;
             int vt;
-            while (decode_slot<SEL>(p, slot, b, v, vt) == 0) {
+            for (int looked = 0; looked <= p.slots && decode_slot<SEL>(p, slot, b, v, vt) == 0; ++looked) {
               b = v.b;
               if (++slot == p.slots) {
                 slot = 0;
@@ -600,13 +627,13 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       // ================= queries =================
       for (int un = 0;; ++un) {
         const int us = un & 1;
-        if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
+        if (!warp_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
         const Unit& u = ctrl->unit[us];
         if (u.n_tiles < 0) break;
         if (u.n_tiles > 0) {
           const int w = warp - R::kRest - 2;
           if (pair) {                    // one buffer; the softmax threads convert their rows
-            if (un >= 1 && !mbar_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
+            if (un >= 1 && !warp_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
             copy_queries<D>(p, u, q_sm, 0, 127, w, lane);
             if (u.rows > kTileRows) copy_queries<D>(p, u, q_sm + S::kOperand, kTileRows, 127, w, lane);
           } else {                       // two buffers, converted here ahead of their use
@@ -633,7 +660,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       // ================= MMA issue =================
       auto commit = [&](uint64_t* bar) { tc_commit(smem_u32(bar)); };
       auto arrive = [&](uint64_t* bar) { mbar_arrive(smem_u32(bar)); };
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(smem_u32(bar), parity, abort_flag, status); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return lane_wait(smem_u32(bar), parity, abort_flag, status); };
       auto test = [&](uint64_t* bar, uint32_t parity) { return mbar_test(smem_u32(bar), parity); };
       constexpr uint32_t id_qk = idesc_f16(kTileRows, kKeys, false), id_pv = idesc_f16(kTileRows, D, true);
       auto qk = [&](int x, uint32_t q_tile, int st) {
@@ -789,7 +816,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
     bool ok = true;
     for (int un = 0; ok; ++un) {
       const int us = un & 1;
-      if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
+      if (!warp_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
       const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width;
@@ -918,7 +945,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           }
         }
         const float lv = __log2f(vg) + kBoost, iv = __frcp_rn(vg);
-        if (use > 0 && !mbar_wait(smem_u32(&empty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
+        if (use > 0 && !warp_wait(smem_u32(&empty[st]), (use - 1) & 1, abort_flag, status)) { ok = false; break; }
         if (!values) {                   // the tile's scales go with its keys
           Meta& m = ctrl->meta[pair ? n & 3 : sx * 2 + (n & 1)];
           if constexpr (SEL) {
@@ -959,7 +986,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
     int pc = 0;                          // pair mode: tiles seen by the CTA
     for (int un = 0;; ++un) {
       const int us = un & 1;
-      if (!mbar_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
+      if (!warp_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
       const bool twice = NARROW || (!pair && u.rows <= 64);
@@ -970,7 +997,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       const int pos = live ? (SEL ? u.pos0 : u.pos0 + (u.row0 + row) / a.group) : -1;
       float f = 0.f;                     // scores to base-2 exponents
       if (pair) {
-        if (!mbar_wait(smem_u32(&ctrl->qraw), un & 1, abort_flag, status)) break;
+        if (!warp_wait(smem_u32(&ctrl->qraw), un & 1, abort_flag, status)) break;
         if (mine > 0) {
           f = convert_query<D>(a, q_sm + x * S::kOperand, r);
           fence_async_smem();
@@ -978,7 +1005,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctrl->qfull[us]));
       } else {
-        if (!mbar_wait(smem_u32(&ctrl->qfull[us]), (un >> 1) & 1, abort_flag, status)) break;
+        if (!warp_wait(smem_u32(&ctrl->qfull[us]), (un >> 1) & 1, abort_flag, status)) break;
         if (mine > 0) f = ctrl->rowf[us * 128 + r];
       }
       if (!live) f = 0.f;
@@ -988,7 +1015,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       for (int i = 0; i < mine; ++i) {
         const int ord = u.first + (pair ? i : 2 * i + x);
         const Meta& m = ctrl->meta[pair ? (pc + i) & 3 : x * 2 + (sn & 1)];
-        if (!mbar_wait(smem_u32(&ctrl->sfull[x]), sn & 1, abort_flag, status)) { ok = false; break; }
+        if (!warp_wait(smem_u32(&ctrl->sfull[x]), sn & 1, abort_flag, status)) { ok = false; break; }
         ++sn;
         tc_fence_after();
         if (warp_live) {
@@ -1127,7 +1154,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       if (!ok) break;
       pc += u.n_tiles;
       if (mine > 0) {
-        if (!mbar_wait(smem_u32(&ctrl->ofull[x]), on & 1, abort_flag, status)) break;
+        if (!warp_wait(smem_u32(&ctrl->ofull[x]), on & 1, abort_flag, status)) break;
         ++on;
         tc_fence_after();
       }
@@ -1141,7 +1168,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       if (merged && x == 1) {
         const int cols = D / rounds;
         for (int h = 0; h < rounds && ok; ++h) {
-          if (mn > 0 && !mbar_wait(smem_u32(&ctrl->mempty), (mn - 1) & 1, abort_flag, status)) { ok = false; break; }
+          if (mn > 0 && !warp_wait(smem_u32(&ctrl->mempty), (mn - 1) & 1, abort_flag, status)) { ok = false; break; }
           ++mn;
           if (h == 0 && (!twice || r >= 64)) {
             ml[2 * partner] = M;
@@ -1188,7 +1215,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
         for (int h = 0; h < (merged ? rounds : 1) && ok; ++h) {
           const int cols = merged ? D / rounds : D;
           if (merged) {
-            if (!mbar_wait(smem_u32(&ctrl->mfull), mn & 1, abort_flag, status)) { ok = false; break; }
+            if (!warp_wait(smem_u32(&ctrl->mfull), mn & 1, abort_flag, status)) { ok = false; break; }
             ++mn;
             if (h == 0) {
               const float M1 = ml[2 * partner], l1 = ml[2 * partner + 1];
@@ -1249,7 +1276,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           // the last of the unit's CTAs joins the pieces in their order
           __threadfence();
           mbar_arrive(smem_u32(&ctrl->wg[x]));
-          if (!mbar_wait(smem_u32(&ctrl->wg[x]), wn & 1, abort_flag, status)) break;
+          if (!warp_wait(smem_u32(&ctrl->wg[x]), wn & 1, abort_flag, status)) break;
           ++wn;
           if (r == 0) {
             int* count = a.counters + 2 * u.c0 + x;
@@ -1258,7 +1285,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
             ctrl->last[x] = last;
           }
           mbar_arrive(smem_u32(&ctrl->wg[x]));
-          if (!mbar_wait(smem_u32(&ctrl->wg[x]), wn & 1, abort_flag, status)) break;
+          if (!warp_wait(smem_u32(&ctrl->wg[x]), wn & 1, abort_flag, status)) break;
           ++wn;
           if (*reinterpret_cast<volatile int*>(&ctrl->last[x]) && live) {
             __threadfence();

@@ -15,10 +15,12 @@ using namespace ltk;
 struct ltk_kv {
   KvCache cache;
   int dim = 0;
+  int engine = 0;
   int device = 0;
   int num_sms = 0;
   float* part = nullptr;
   int* counters = nullptr;
+  int num_counters = 0;
   int* status = nullptr;
 };
 
@@ -89,6 +91,7 @@ ltk_status ltk_kv_create(const ltk_kv_config* cfg, ltk_kv** out) {
   *out = nullptr;
   if (cfg == nullptr || cfg->num_pages < 1 || cfg->heads < 1) return LTK_ERR_ARG;
   if (cfg->num_pages > INT_MAX || cfg->heads > 65535) return LTK_ERR_ARG;
+  if (cfg->engine < 0 || cfg->engine > 2) return LTK_ERR_ARG;
   if (cfg->page != 16 && cfg->page != 32 && cfg->page != 64 && cfg->page != 128) return LTK_ERR_UNSUPPORTED;
   // a code row's number is 32 bits in the kernels (more rows than that do not fit the device)
   if (cfg->num_pages * cfg->heads > 0xFFFFFFFEll / cfg->page) return LTK_ERR_UNSUPPORTED;
@@ -106,10 +109,12 @@ ltk_status ltk_kv_create(const ltk_kv_config* cfg, ltk_kv** out) {
   h->cache.page = cfg->page;
   h->cache.page_log2 = cfg->page == 16 ? 4 : cfg->page == 32 ? 5 : cfg->page == 64 ? 6 : 7;
   h->dim = cfg->dim;
+  h->engine = cfg->engine;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
   const size_t part_floats = std::max(kv_rows_part_floats(h->num_sms), kv_tile_part_floats(h->num_sms));
-  const size_t counters = static_cast<size_t>(std::max(kv_rows_counters(h->num_sms), kv_tile_counters(h->num_sms))) * 4;
+  h->num_counters = std::max(kv_rows_counters(h->num_sms), kv_tile_counters(h->num_sms));
+  const size_t counters = static_cast<size_t>(h->num_counters) * 4;
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part), part_floats * 4);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->counters), counters);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->status), 4);
@@ -214,8 +219,9 @@ static ltk_status kv_attend(ltk_kv* h, const ltk_kv_batch* batch, int dtype, con
   p.status = h->status;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int most_q = max_q > 0 ? max_q : batch->N;
-  const cudaError_t e = kv_use_rows(p, most_q, h->num_sms) ? launch_kv_rows(p, h->num_sms, st)
-                                                           : launch_kv_tile(p, most_q, h->num_sms, st);
+  const bool by_rows = h->engine == 0 ? kv_use_rows(p, most_q, h->num_sms) : h->engine == 1;
+  const cudaError_t e = by_rows ? launch_kv_rows(p, h->num_sms, st)
+                                : launch_kv_tile(p, most_q, h->num_sms, st);
   return kv_cuda_fail(e, "kv attention");
 }
 
@@ -240,6 +246,9 @@ ltk_status ltk_kv_status(ltk_kv* h, int* device_status, void* stream) {
   cudaError_t e = cudaMemcpyAsync(&value, h->status, 4, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, 4, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  // a call that gave up half way may have left its counters
+  if (e == cudaSuccess && value == LTK_ERR_TIMEOUT)
+    e = cudaMemset(h->counters, 0, static_cast<size_t>(h->num_counters) * 4);
   if (e != cudaSuccess) return kv_cuda_fail(e, "ltk_kv_status");
   *device_status = value;
   return LTK_OK;

@@ -89,10 +89,11 @@ class PagedKVCache:
 
     Without the four buffers the cache is allocated, zeroed.  ``k_codes`` and
     ``v_codes`` are uint8 (or float8_e4m3fn) [num_pages, heads, page, dim],
-    ``k_scale`` and ``v_scale`` fp32 [num_pages, heads]."""
+    ``k_scale`` and ``v_scale`` fp32 [num_pages, heads].  ``engine`` 0 lets measured costs
+    choose the attention kernel, 1 takes the one for few rows, 2 the tensor-core tiles."""
 
     def __init__(self, num_pages: int, heads: int, dim: int, page: int = 64, k_codes=None, v_codes=None,
-                 k_scale=None, v_scale=None):
+                 k_scale=None, v_scale=None, engine: int = 0):
         import torch
         self.h = None
         self.lib = ltk.load_library()
@@ -118,7 +119,7 @@ class PagedKVCache:
                 _fail(name, "must be contiguous")
             _device_ok(t, name, self.device)
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
-        cfg = KvConfig(self.num_pages, self.heads, self.dim, self.page, k_codes.data_ptr(), v_codes.data_ptr(),
+        cfg = KvConfig(self.num_pages, self.heads, self.dim, self.page, int(engine), k_codes.data_ptr(), v_codes.data_ptr(),
                        k_scale.data_ptr(), v_scale.data_ptr())
         # the handle's workspace must not be set up before the buffers' own stream has made them
         torch.cuda.current_stream().synchronize()

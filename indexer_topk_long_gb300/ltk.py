@@ -52,7 +52,7 @@ class Stats(ctypes.Structure):
 
 class KvConfig(ctypes.Structure):
     _fields_ = [("num_pages", ctypes.c_longlong), ("heads", ctypes.c_int), ("dim", ctypes.c_int),
-                ("page", ctypes.c_int), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("page", ctypes.c_int), ("engine", ctypes.c_int), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 

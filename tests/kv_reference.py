@@ -196,13 +196,13 @@ class Setup:
     def q64(self):
         return self.q.double().numpy()
 
-    def gpu(self):
+    def gpu(self, engine=0):
         """The framework's cache on the same data, and the batch's tensors."""
         import torch
         from indexer_topk_long_gb300 import PagedKVCache
         dev = {n: torch.from_numpy(self.c.codes[n]).cuda() for n in "kv"}
         scl = {n: torch.from_numpy(self.c.scale[n]).cuda() for n in "kv"}
         cache = PagedKVCache(self.pages, self.c.heads, self.c.dim, page=self.c.page, k_codes=dev["k"],
-                             v_codes=dev["v"], k_scale=scl["k"], v_scale=scl["v"])
+                             v_codes=dev["v"], k_scale=scl["k"], v_scale=scl["v"], engine=engine)
         ints = [torch.tensor(np.asarray(x), dtype=torch.int32).cuda() for x in (self.table, self.lens, self.cu)]
         return cache, ints

@@ -7,21 +7,32 @@ import kv_reference as ref
 pytestmark = pytest.mark.gpu
 
 
+# (engine, rows the hint speaks of): the kernel for few rows, then narrow, whole and paired tiles
+KERNELS = [(1, 16), (2, 64), (2, 128), (2, 1000)]
+
+
+def _hint(s, rows):
+    return max(1, rows // (s.q.shape[1] // s.c.heads))
+
+
 def _dense(s, window=0, sinks=0, max_q=None, scale=None):
-    cache, ints = s.gpu()
-    out, lse = cache.attention(s.q.cuda(), *ints, window=window, sinks=sinks, max_q=max_q, scale=scale)
-    assert cache.status() == 0
     want = s.c.attend(s.q64(), s.table, s.lens, s.cu, window, sinks, scale=scale)
-    ref.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, s.dtype)
+    for engine, rows in [(0, None)] + KERNELS:
+        cache, ints = s.gpu(engine)
+        out, lse = cache.attention(s.q.cuda(), *ints, window=window, sinks=sinks, scale=scale,
+                                   max_q=max_q if rows is None else _hint(s, rows))
+        assert cache.status() == 0
+        ref.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, s.dtype)
 
 
 def _selected(s, idx):
     import torch
-    cache, ints = s.gpu()
-    out, lse = cache.attention_selected(s.q.cuda(), torch.from_numpy(idx).cuda(), *ints)
-    assert cache.status() == 0
     want = s.c.attend(s.q64(), s.table, s.lens, s.cu, idx=idx)
-    ref.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, s.dtype)
+    for engine in (0, 1, 2):
+        cache, ints = s.gpu(engine)
+        out, lse = cache.attention_selected(s.q.cuda(), torch.from_numpy(idx).cuda(), *ints)
+        assert cache.status() == 0
+        ref.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, s.dtype)
 
 
 @pytest.mark.parametrize("lens,new,hq,hkv,d,page,dtype", [
@@ -90,47 +101,47 @@ def test_large_scores(new):
 def test_sequence_shorter_than_its_queries_and_empty():
     """Queries before the first token (and of an empty sequence) see nothing: 0 and -inf."""
     import torch
-    for hint in (1, 12, 25, 60):
+    for engine, rows in KERNELS:
         s = ref.Setup([30, 30], [50, 4], 4, 1, 128, 16, "bf16", seed=17)
         s.lens = [30, 0]
-        cache, ints = s.gpu()
-        out, lse = cache.attention(s.q.cuda(), *ints, max_q=hint)
+        cache, ints = s.gpu(engine)
+        out, lse = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
         assert (out[:20] == 0).all() and torch.isneginf(lse[:20]).all()
         assert (out[50:] == 0).all() and torch.isneginf(lse[50:]).all()
         want = s.c.attend(s.q64()[20:50], s.table[:1], [30], [0, 30])
         ref.check(out[20:50].double().cpu().numpy(), lse[20:50].double().cpu().numpy(), want, "bf16")
 
 
-@pytest.mark.parametrize("hint", [1, 40])
-def test_a_poisoned_token_reaches_only_the_queries_that_see_it(hint):
+@pytest.mark.parametrize("engine,rows", KERNELS)
+def test_a_poisoned_token_reaches_only_the_queries_that_see_it(engine, rows):
     s = ref.Setup([100], [40], 4, 1, 128, 16, "bf16", seed=18)
     s.c.codes["k"][s.table[0, 80 // 16], 0, 80 % 16] = 0x7F
     s.c.codes["v"][s.table[0, 80 // 16], 0, 80 % 16] = 0
-    cache, ints = s.gpu()
-    out, _ = cache.attention(s.q.cuda(), *ints, max_q=hint)
+    cache, ints = s.gpu(engine)
+    out, _ = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
     bad = out.isnan()
     assert not bad[:20].any() and bad[20:].all()
     want = s.c.attend(s.q64()[:20], s.table, [80], [0, 20])
     ref.check(out[:20].double().cpu().numpy(), np.zeros((20, 4)), (want[0], np.zeros((20, 4)), want[2]), "bf16")
 
 
-@pytest.mark.parametrize("hint", [1, 64])
-def test_bad_page_is_reported(hint):
+@pytest.mark.parametrize("engine,rows", KERNELS)
+def test_bad_page_is_reported(engine, rows):
     s = ref.Setup([100, 64], [20, 20], 4, 1, 128, 16, "bf16", seed=19)
-    cache, ints = s.gpu()
+    cache, ints = s.gpu(engine)
     ints[0][0, 2] = s.pages + 7
-    out, _ = cache.attention(s.q.cuda(), *ints, max_q=hint)
+    out, _ = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
     assert cache.status() == 1 and cache.status() == 0
     assert out[:20].isnan().all() and not out[20:].isnan().any()
 
 
-@pytest.mark.parametrize("hint", [1, 64])
-def test_bad_page_reaches_only_the_queries_that_see_it(hint):
+@pytest.mark.parametrize("engine,rows", KERNELS)
+def test_bad_page_reaches_only_the_queries_that_see_it(engine, rows):
     """The page after the first ten queries' positions is outside the pool."""
     s = ref.Setup([90], [40], 4, 1, 128, 16, "bf16", seed=27)
-    cache, ints = s.gpu()
+    cache, ints = s.gpu(engine)
     ints[0][0, 4] = -3                      # positions 64 .. 79; queries at 50 .. 89
-    out, _ = cache.attention(s.q.cuda(), *ints, max_q=hint)
+    out, _ = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
     assert cache.status() == 1
     bad = out.isnan()
     assert not bad[:14].any() and bad[14:].all()
@@ -159,10 +170,54 @@ def test_selected(lens, new, hq, hkv, d, page, dtype, k):
     _selected(s, idx)
 
 
+@pytest.mark.parametrize("new,hq,hkv,d,k", [(1500, 64, 1, 64, 130), (700, 40, 1, 64, 300), (160, 128, 1, 64, 260),
+                                             (400, 200, 1, 64, 128), (330, 96, 2, 64, 140)])
+def test_selected_more_units_than_sms(new, hq, hkv, d, k):
+    """Whole units in turn, then a rest that is cut; more than 128 rows a KV head."""
+    s = ref.Setup([new + 300], [new], hq, hkv, d, 32, "f16", seed=28)
+    rng = np.random.RandomState(3)
+    idx = np.stack([rng.permutation(300)[:k] for _ in range(new)]).astype(np.int32)
+    import torch
+    pick = np.unique(np.concatenate([rng.randint(0, new, 12), [0, new - 1]]))
+    for engine in (1, 2):
+        cache, ints = s.gpu(engine)
+        out, lse = cache.attention_selected(s.q.cuda(), torch.from_numpy(idx).cuda(), *ints)
+        assert cache.status() == 0
+        for i, p in zip(pick, 300 + pick):  # each alone, as a sequence's last token
+            want = s.c.attend(s.q64()[i:i + 1], s.table, [p + 1], [0, 1], idx=idx[i:i + 1])
+            ref.check(out[i:i + 1].double().cpu().numpy(), lse[i:i + 1].double().cpu().numpy(), want, "f16")
+
+
+def test_many_sequences_and_heads():
+    """More row tiles than threads look at in one go, empty sequences among them."""
+    rng = np.random.RandomState(4)
+    lens = rng.randint(1, 40, 900)
+    new = np.minimum(lens, rng.choice([0, 0, 1, 2, 5], 900))
+    _dense(ref.Setup(lens, new, 6, 3, 64, 16, "bf16", seed=29))
+
+
+def test_cu_q_that_does_not_rise():
+    """Reported; nothing is read or written out of bounds, and the next call is right."""
+    import torch
+    s = ref.Setup([60, 50], [40, 30], 4, 1, 128, 16, "bf16", seed=30)
+    want = s.c.attend(s.q64(), s.table, s.lens, s.cu)
+    for engine, rows in KERNELS:
+        cache, ints = s.gpu(engine)
+        for bad in ([0, 50, 30], [0, 40, 1 << 30], [-7, 40, 70]):
+            cu = torch.tensor(bad, dtype=torch.int32).cuda()
+            cache.attention(s.q.cuda(), ints[0], ints[1], cu, max_q=_hint(s, rows))
+            assert cache.status() == (1 if engine == 2 else 0)      # the few-row kernel clamps
+        out, lse = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
+        ref.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, "bf16")
+    x = s.q.cuda()
+    cache.append(x[:, :1], x[:, 1:2], ints[0], ints[1], torch.tensor([0, 50, 30], dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+
+
 def test_selected_empty_slots_anywhere():
     """Empty slots between the others, whole empty tiles, a row of nothing but empty slots,
     entries past the query's position."""
-    for hq in (4, 64):
+    for hq, engine in ((4, 1), (4, 2), (64, 1), (64, 2), (100, 2)):
         s = ref.Setup([600], [6], hq, 1, 128, 64, "bf16", seed=22)
         rng = np.random.RandomState(2)
         idx = np.full((6, 400), -1, np.int32)
@@ -173,7 +228,7 @@ def test_selected_empty_slots_anywhere():
         idx[3, :10] = 599                   # not visible to query 3 (position 597)
         idx[3, 10:20] = 1 << 30
         idx[4, 1:] = -1
-        cache, ints = s.gpu()
+        cache, ints = s.gpu(engine)
         import torch
         out, lse = cache.attention_selected(s.q.cuda(), torch.from_numpy(idx).cuda(), *ints)
         want = s.c.attend(s.q64(), s.table, s.lens, s.cu, idx=idx)
@@ -184,9 +239,9 @@ def test_selected_empty_slots_anywhere():
 def test_same_bits_every_time_and_under_capture():
     """Splits are merged in a fixed order; a replayed graph reads its buffers anew."""
     import torch
-    for hq, new in ((8, 1), (8, 100), (64, 3)):
+    for hq, new, engine in ((8, 1, 1), (8, 100, 2), (64, 3, 1), (64, 3, 2), (100, 1, 2)):
         s = ref.Setup([3000], [new], hq, 1, 128, 64, "bf16", seed=23)
-        cache, ints = s.gpu()
+        cache, ints = s.gpu(engine)
         q = s.q.cuda()
         idx = torch.randperm(2900, device="cuda")[:500].to(torch.int32).expand(new, 500).contiguous()
         first = [t.clone() for t in cache.attention(q, *ints) + cache.attention_selected(q, idx, *ints)]
@@ -248,7 +303,10 @@ def test_cache_beyond_32_bit_offsets():
     lens, cu = (torch.tensor(x, dtype=torch.int32).cuda() for x in (s.lens, s.cu))
     want = s.c.attend(s.q64(), s.table, s.lens, s.cu)
     idx = torch.randperm(300, device="cuda")[None].to(torch.int32)
+    tiles = PagedKVCache(pages, heads, d, page=page, k_codes=cache.k_codes, v_codes=cache.v_codes,
+                         k_scale=cache.k_scale, v_scale=cache.v_scale, engine=2)
     for out, lse in (cache.attention(s.q.cuda(), table, lens, cu),
-                     cache.attention(s.q.cuda(), table, lens, cu, max_q=200),
-                     cache.attention_selected(s.q.cuda(), idx, table, lens, cu)):
+                     tiles.attention(s.q.cuda(), table, lens, cu, max_q=200),
+                     cache.attention_selected(s.q.cuda(), idx, table, lens, cu),
+                     tiles.attention_selected(s.q.cuda(), idx, table, lens, cu)):
         ref.check(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, "bf16")

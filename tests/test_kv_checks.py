@@ -11,7 +11,7 @@ CPU = torch.device("cpu")
 
 
 def _config(**kw):
-    cfg = ltk.KvConfig(4, 2, 128, 64, 1 << 12, 1 << 13, 1 << 14, 1 << 15)
+    cfg = ltk.KvConfig(4, 2, 128, 64, 0, 1 << 12, 1 << 13, 1 << 14, 1 << 15)
     for k, v in kw.items():
         setattr(cfg, k, v)
     return cfg
@@ -19,7 +19,7 @@ def _config(**kw):
 
 @pytest.mark.parametrize("field,value,status", [
     ("num_pages", 0, 1), ("num_pages", 1 << 31, 1), ("heads", 0, 1), ("heads", 1 << 17, 1), ("page", 8, 6),
-    ("page", 48, 6), ("page", 256, 6), ("dim", 96, 6), ("dim", 0, 6), ("k_codes", None, 1), ("v_codes", 8, 1),
+    ("page", 48, 6), ("page", 256, 6), ("dim", 96, 6), ("dim", 0, 6), ("engine", -1, 1), ("engine", 3, 1), ("k_codes", None, 1), ("v_codes", 8, 1),
     ("k_scale", None, 1), ("v_scale", 4, 1)])
 def test_create_refuses(ltk_lib, field, value, status):
     h = ctypes.c_void_p()
