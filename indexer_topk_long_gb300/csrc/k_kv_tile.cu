@@ -23,13 +23,11 @@
 // CTA's work, warps 18 and 19 bring the queries.
 // Work: all units' key tiles form one line, cut into equal pieces, one per CTA; a
 // unit cut by a border is merged by the last of its CTAs in a fixed order.
-#include "kv_internal.cuh"
+#include "kv_tensor.cuh"
 
 namespace ltk {
 namespace {
 
-constexpr int kTileRows = 128;
-constexpr int kKeys = 128;
 constexpr int kLoaders = 4;              // warps that load a tile of an operand, 32 keys each
 // Warps of each role and registers a thread (launched evenly, then moved between the
 // warpgroups so that no role spills in its loop).  Narrow form (at most 64 rows): the two
@@ -45,9 +43,6 @@ struct Roles {
   static constexpr int kSoftmaxRegs = NARROW ? 112 : D == 64 ? 128 : 120, kLoadRegs = 72, kRestRegs = NARROW || D == 64 ? 80 : 96;
   static_assert(kSoftmaxWarps / 4 * kSoftmaxRegs + kSets * 2 * kLoadRegs + kRestRegs <= kThreads / 128 * kLaunchRegs, "register split");
 };
-constexpr float kMinusHuge = -1e30f;
-constexpr float kBoost = 8.f;            // as in the kernel for few rows
-constexpr float kSlack = 7.f;
 
 struct Unit {                            // a piece of a work unit
   int n_tiles;                           // key tiles; -1: no more pieces
@@ -96,112 +91,6 @@ struct TileShape {
   static constexpr int kBytes = kQ + 2 * kStage + kMerge + static_cast<int>(sizeof(Ctrl));
 };
 static_assert(TileShape<128>::kBytes <= 232448, "shared memory of a CTA");
-
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\tmbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\tselp.u32 %0, 1, 0, P;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait of a whole warp, the same answer for all its lanes: false when another role
-// gave up or the wait exceeds kWaitLimitNs (then this one gives up: abort flag and status).
-// It sleeps from the second look on, since polling takes issue slots from the softmax.
-__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      raise_status(status, kDevTimeout);
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  return __all_sync(0xFFFFFFFFu, lane_wait(bar, parity, abort_flag, status)) != 0;
-}
-
-// MMAs are issued by one lane that elect.sync picks.  Behind elect.sync the compiler
-// keeps descriptors in uniform registers and an MMA costs four instructions; behind
-// `lane == 0` it moved each operand there first, and with busy softmax warps on the
-// scheduler a 128-cube took 780 to 2800 cycles to issue instead of 513 to 590.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
-  return p != 0;
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t a, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-        "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-        "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(a));
-}
-__device__ __forceinline__ void tmem_ld32_wait(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
-                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
-                 "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
-                 "+f"(v[30]), "+f"(v[31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(v[0]),
-      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
-      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(a)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32f(uint32_t a, const float (&v)[32]) {
-  uint32_t w[16];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * h + i]);
-    tmem_st16(a + 16 * h, w);
-  }
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Descriptor of an operand in 128-byte-swizzled rows (8-row atoms 1024 bytes apart).
-// Scores' operands have the contraction contiguous (leading offset unused); the value
-// operand's rows of 128 bytes hold 64 consecutive d of one key (N contiguous), and its
-// 128-byte-wide halves lie `lead` bytes apart along d.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr, uint32_t lead) {
-  return static_cast<uint64_t>(((saddr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16)) |
-         (static_cast<uint64_t>((1024u >> 4) | (1u << 14) | (2u << 29)) << 32);
-}
-// f16 operands, fp32 result; the second operand with N contiguous when b_mn.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
 
 struct TileParams {
   AttnParams a;
@@ -334,9 +223,9 @@ __device__ __forceinline__ void store_rows(uint32_t at, int lane, const uint4 (&
 
 // Queries come in two steps, since a round trip to memory for every few rows would hold
 // up the next unit: all rows by asynchronous copies to where their f16 form will stand
-// (16-bit elements either way), then converted in place.
+// (16-bit elements either way), then converted in place by convert_query.
 //
-// Step 1, warps w = 0, 1: rows [r0, r0 + 128) of the unit; rows repeat with period mask + 1,
+// The copies, by warps w = 0, 1: rows [r0, r0 + 128) of the unit; rows repeat with period mask + 1,
 // rows past the unit's are zero.
 template <int D>
 __device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u, uint32_t base, int r0, int mask, int w, int lane) {
@@ -362,67 +251,6 @@ __device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u,
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
   }
 }
-// Step 2, one thread for a row of the tile: the row times a power of two that takes its
-// largest element to [2^8, 2^9), as f16; returns what turns the products into base-2
-// exponents.
-template <int D>
-__device__ __forceinline__ float convert_query(const AttnParams& a, uint32_t base, int row) {
-  auto at = [&](int c) { return base + (c >> 3) * (kTileRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
-  uint32_t w[D / 8][4];
-#pragma unroll
-  for (int c = 0; c < D / 8; ++c)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3]) : "r"(at(c)));
-  float amax = 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 8; ++c)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = kv_unpack16(w[c][e], a.bf16);
-      amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-    }
-  int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8;
-  e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
-  const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-  for (int c = 0; c < D / 8; ++c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = kv_unpack16(w[c][i], a.bf16);
-      w[c][i] = kv_pack16(f.x * by, f.y * by, false);
-    }
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(c)), "r"(w[c][0]), "r"(w[c][1]), "r"(w[c][2]), "r"(w[c][3])
-                 : "memory");
-  }
-  return a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-}
-
-// Two fp32 products and sums at once.
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 template <int D, bool SEL, bool NARROW>
 __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(const __grid_constant__ TileParams p) {
   using S = TileShape<D>;
@@ -645,7 +473,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
               const int row = 64 * w + 32 * i + lane;
-              ctrl->rowf[us * 128 + row] = convert_query<D>(a, q_sm + us * S::kOperand, row);
+              ctrl->rowf[us * 128 + row] = convert_query<D, kTileRows>(a, q_sm + us * S::kOperand, row);
             }
             fence_async_smem();
           }
@@ -999,7 +827,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       if (pair) {
         if (!warp_wait(smem_u32(&ctrl->qraw), un & 1, abort_flag, status)) break;
         if (mine > 0) {
-          f = convert_query<D>(a, q_sm + x * S::kOperand, r);
+          f = convert_query<D, kTileRows>(a, q_sm + x * S::kOperand, r);
           fence_async_smem();
         }
         __syncwarp();
@@ -1360,10 +1188,14 @@ cudaError_t init_tile() {
 
 template <int D, bool SEL>
 cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
-  if (p.rows <= 64)
-    kv_tile_kernel<D, SEL, true><<<num_sms, Roles<D, true>::kThreads, TileShape<D>::kBytes, stream>>>(p);
-  else
-    kv_tile_kernel<D, SEL, false><<<num_sms, Roles<D, false>::kThreads, TileShape<D>::kBytes, stream>>>(p);
+  if constexpr (!SEL) {
+    if (p.rows <= 64) {
+      kv_tile_kernel<D, SEL, true><<<num_sms, Roles<D, true>::kThreads, TileShape<D>::kBytes, stream>>>(p);
+      count_launches(1);
+      return cudaGetLastError();
+    }
+  }
+  kv_tile_kernel<D, SEL, false><<<num_sms, Roles<D, false>::kThreads, TileShape<D>::kBytes, stream>>>(p);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -1374,9 +1206,8 @@ size_t kv_tile_part_floats(int num_sms) { return static_cast<size_t>(2) * num_sm
 int kv_tile_counters(int num_sms) { return 2 * num_sms; }
 
 cudaError_t kv_tile_init() {
-  const cudaError_t e[8] = {init_tile<128, false, false>(), init_tile<128, false, true>(), init_tile<128, true, false>(),
-                            init_tile<128, true, true>(),   init_tile<64, false, false>(), init_tile<64, false, true>(),
-                            init_tile<64, true, false>(),   init_tile<64, true, true>()};
+  const cudaError_t e[6] = {init_tile<128, false, false>(), init_tile<128, false, true>(), init_tile<128, true, false>(),
+                            init_tile<64, false, false>(),  init_tile<64, false, true>(),  init_tile<64, true, false>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -1391,7 +1222,7 @@ cudaError_t launch_kv_tile(const AttnParams& a, int max_q, int num_sms, cudaStre
   // that many, one tile, or a narrow one (max_q is a hint: more rows make more units).
   const long long most = static_cast<long long>(a.group) * (sel ? 1 : max_q);
   p.pair = !sel && most > kTileRows;
-  p.rows = p.pair ? 2 * kTileRows : most <= 64 ? 64 : kTileRows;
+  p.rows = p.pair ? 2 * kTileRows : most <= 64 && !sel ? 64 : kTileRows;
   if (sel) {
     p.row_tiles = (a.group + p.rows - 1) / p.rows;
     p.slots = a.batch.N * p.row_tiles;

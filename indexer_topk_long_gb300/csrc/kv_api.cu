@@ -112,8 +112,8 @@ ltk_status ltk_kv_create(const ltk_kv_config* cfg, ltk_kv** out) {
   h->engine = cfg->engine;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
-  const size_t part_floats = std::max(kv_rows_part_floats(h->num_sms), kv_tile_part_floats(h->num_sms));
-  h->num_counters = std::max(kv_rows_counters(h->num_sms), kv_tile_counters(h->num_sms));
+  const size_t part_floats = std::max({kv_rows_part_floats(h->num_sms), kv_tile_part_floats(h->num_sms), kv_list_part_floats(h->num_sms)});
+  h->num_counters = std::max({kv_rows_counters(h->num_sms), kv_tile_counters(h->num_sms), kv_list_counters(h->num_sms)});
   const size_t counters = static_cast<size_t>(h->num_counters) * 4;
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->part), part_floats * 4);
   if (e == cudaSuccess) e = cudaMalloc(reinterpret_cast<void**>(&h->counters), counters);
@@ -122,6 +122,7 @@ ltk_status ltk_kv_create(const ltk_kv_config* cfg, ltk_kv** out) {
   if (e == cudaSuccess) e = cudaMemset(h->status, 0, 4);
   if (e == cudaSuccess) e = kv_rows_init();
   if (e == cudaSuccess) e = kv_tile_init();
+  if (e == cudaSuccess) e = kv_list_init();
   if (e == cudaSuccess) e = cudaDeviceSynchronize();   // the workspace is zero for calls on any stream
   if (e != cudaSuccess) {
     const ltk_status s = kv_cuda_fail(e, "ltk_kv_create");
@@ -220,8 +221,10 @@ static ltk_status kv_attend(ltk_kv* h, const ltk_kv_batch* batch, int dtype, con
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int most_q = max_q > 0 ? max_q : batch->N;
   const bool by_rows = h->engine == 0 ? kv_use_rows(p, most_q, h->num_sms) : h->engine == 1;
-  const cudaError_t e = by_rows ? launch_kv_rows(p, h->num_sms, st)
-                                : launch_kv_tile(p, most_q, h->num_sms, st);
+  const bool by_list = idx != nullptr && p.group <= kListRows;
+  const cudaError_t e = by_rows   ? launch_kv_rows(p, h->num_sms, st)
+                        : by_list ? launch_kv_list(p, h->num_sms, st)
+                                  : launch_kv_tile(p, most_q, h->num_sms, st);
   return kv_cuda_fail(e, "kv attention");
 }
 

@@ -163,4 +163,12 @@ int kv_tile_counters(int num_sms);
 cudaError_t kv_tile_init();
 cudaError_t launch_kv_tile(const AttnParams& p, int max_q, int num_sms, cudaStream_t stream);
 
+// Attention over listed keys for up to kListRows rows per KV head, on the tensor cores
+// (k_kv_list.cu).
+constexpr int kListRows = 64;
+size_t kv_list_part_floats(int num_sms);
+int kv_list_counters(int num_sms);
+cudaError_t kv_list_init();
+cudaError_t launch_kv_list(const AttnParams& p, int num_sms, cudaStream_t stream);
+
 }  // namespace ltk
