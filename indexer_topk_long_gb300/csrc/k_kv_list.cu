@@ -146,20 +146,28 @@ __device__ __forceinline__ int code_at(int row, int c) {
 // turns the products into base-2 exponents.
 template <int D>
 __device__ __forceinline__ float convert_queries(const AttnParams& a, uint32_t q_sm, int lane) {
-  float amax = 0.f;
+  // magnitudes compare as integers, infinities and NaN above a bound
+  const uint32_t bound = a.bf16 ? 0x7F80u : 0x7C00u;
+  uint32_t most = 0;
 #pragma unroll 4
   for (int i = lane; i < kRows * D / 8; i += 32) {
     const uint4 x = lds128(q_sm + i * 16);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = kv_unpack16(w[e], a.bf16);
-      const float m0 = fabsf(f.x), m1 = fabsf(f.y);
-      if (m0 < __int_as_float(0x7F800000)) amax = fmaxf(amax, m0);
-      if (m1 < __int_as_float(0x7F800000)) amax = fmaxf(amax, m1);
+    for (int e = 0; e < 4; ++e) most = __vmaxu2(most, w[e] & 0x7FFF7FFFu);
+  }
+  if (__any_sync(0xFFFFFFFFu, (most & 0xFFFFu) >= bound || most >> 16 >= bound)) {
+    most = 0;                            // some are not finite: without them
+#pragma unroll 1
+    for (int i = lane; i < kRows * D / 2; i += 32) {
+      uint32_t w;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(q_sm + i * 4));
+      const uint32_t lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
+      most = __vmaxu2(most, (lo < bound ? lo : 0u) | (hi < bound ? hi : 0u) << 16);
     }
   }
-  amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(amax)));
+  most = __reduce_max_sync(0xFFFFFFFFu, max(most & 0xFFFFu, most >> 16));
+  const float amax = kv_unpack16(most, a.bf16).x;
   const int e = amax > 0.f ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -118) : 0;
   const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll 4
@@ -522,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
         tc_fence_after();
         const uint32_t from = codes_sm + n % kRingK * S::kCodes;
         const uint32_t to = k_col + (n & 1) * (D / 2) + (static_cast<uint32_t>(w * 32) << 16);
-#pragma unroll 1
+#pragma unroll 2
         for (int j = 0; j < D / 32; ++j) {
           uint32_t h[16];
 #pragma unroll
