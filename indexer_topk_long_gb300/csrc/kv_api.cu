@@ -53,29 +53,39 @@ bool rows_ok(const void* p, long long stride, int heads, int dim) {
   return kv_aligned(p) && stride >= static_cast<long long>(heads) * dim && stride % 8 == 0;
 }
 
-// The kernel for few rows goes over a head's keys once for every 16 rows, the tile kernel once
-// for 64, 128 or 256, at some 20 us more to start, meet and part.  Measured in microseconds
-// that one SM takes for 128 keys: 0.85 for 16 rows by the first, 1.62 for a narrow tile (64
-// rows), 1.8 for a whole one or a pair by the second.  For instance (D = 128, one KV head of
-// 64 query heads, 2048 listed keys): 48 queries 33 us by the first and 37 by the second, 128
-// queries 62 and 47; 16 rows, 8 KV heads, 512 queries of 2048 listed keys 376 and 726; 112
-// rows, 16 sequences of 1024 tokens 25 and 37; chunks of 2048 queries 10 times the second's.
-// How long sequences are is only known on the device: a third of the page table is assumed.
+// Which kernel.  The one for few rows goes over a head's keys once for every 16 rows; the tile
+// kernels once for 64 (narrow, listed), 128 or 256, but take longer to start, meet and part.
+// Each side is a measured cost in microseconds of one SM, by tiles of 128 keys, against what the
+// tile kernels' start takes on all of them.
+//
+// Dense: 0.85 a tile for 16 rows against 1.62 for a narrow tile, 1.8 for a whole one or a pair,
+// and 15 to start.  For instance (D = 128): 16 rows, 8 KV heads 376 us by the first and 726 by
+// the second; 112 rows, 16 sequences of 1024 tokens 25 and 37; chunks of 2048 queries 10 times
+// the second's.  How long sequences are is only known on the device: a third of the page table
+// is assumed.
+//
+// Listed, up to 64 rows: a unit (query, KV head) of T tiles takes 2.0 + 0.75 T for every 16
+// rows (D = 64: 1.4 + 0.51 T) against 5.0 + 0.96 T (4.5 + 0.94 T), and 7 to start.  For instance
+// (D = 128, k = 2048, one KV head): 64 rows, 32 queries 27 us by the first and 29 by the second,
+// 128 queries 62 and 37, 4096 queries 1497 and 549; 32 rows, 64 queries 27 and 29, 4096 queries
+// 755 and 511; 16 rows, 8 KV heads, 1024 queries 799 and 1018.
 bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
   const double rows = static_cast<double>(p.group) * (p.idx != nullptr ? 1 : max_q);
   if (rows <= kRowsPerUnit) return true;
-  const double by_rows = 0.85 * std::ceil(rows / 16.0);
-  const double by_tiles = rows <= 64 ? 1.62 : 1.8 * std::ceil(rows / 256.0);
-  double units = p.cache.heads, keys;
+  const double sixteens = std::ceil(rows / 16.0);
   if (p.idx != nullptr) {
-    units *= p.batch.N;
-    keys = p.k;
-  } else {
-    units *= p.batch.B;
-    keys = static_cast<double>(p.batch.width) * p.cache.page / 3.0;
-    if (p.window > 0) keys = std::min(keys, static_cast<double>(p.window) + p.sinks + max_q);
+    const double units = static_cast<double>(p.cache.heads) * p.batch.N, tiles = std::ceil(p.k / 128.0);
+    if (p.group <= kListRows) {
+      const double by_rows = sixteens * (p.dim == 128 ? 2.0 + 0.75 * tiles : 1.4 + 0.51 * tiles);
+      const double by_list = p.dim == 128 ? 5.0 + 0.96 * tiles : 4.5 + 0.94 * tiles;
+      return units * (by_rows - by_list) <= 7.0 * num_sms;
+    }
+    return units * tiles * (0.85 * sixteens - 1.8 * std::ceil(rows / 256.0)) <= 15.0 * num_sms;
   }
-  return units * std::ceil(keys / 128.0) * (by_rows - by_tiles) <= 15.0 * num_sms;
+  double keys = static_cast<double>(p.batch.width) * p.cache.page / 3.0;
+  if (p.window > 0) keys = std::min(keys, static_cast<double>(p.window) + p.sinks + max_q);
+  const double by_tiles = rows <= 64 ? 1.62 : 1.8 * std::ceil(rows / 256.0);
+  return static_cast<double>(p.cache.heads) * p.batch.B * std::ceil(keys / 128.0) * (0.85 * sixteens - by_tiles) <= 15.0 * num_sms;
 }
 
 KvBatch batch_of(const ltk_kv_batch* b) {

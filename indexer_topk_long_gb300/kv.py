@@ -15,11 +15,15 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from . import ltk
 from .ltk import KvBatch, KvConfig, LTK_BF16, LTK_F16
 
 DTYPES = {"torch.bfloat16": LTK_BF16, "torch.float16": LTK_F16}
+# A KvBatch as bytes: a decode step is host-bound, and packing takes a third of a ctypes structure's time.
+_PACK = struct.Struct("@PiPPii").pack
+assert struct.calcsize("@PiPPii") == ctypes.sizeof(KvBatch)
 
 
 def _fail(name: str, what: str):
@@ -59,10 +63,11 @@ def _rows(t, name: str, n: int, dim: int, device, dtype=None) -> tuple[int, int]
     if heads < 1:
         _fail(name, "has no heads")
     s0, s1, s2 = t.stride()
-    stride = s0 if n > 1 else heads * dim
-    if s2 != 1 or (heads > 1 and s1 != dim):
+    width = heads * dim
+    stride = s0 if n > 1 else width
+    if s2 != 1 or (s1 != dim and heads > 1):
         _fail(name, "each token's heads must be contiguous")
-    if stride % 8 or stride < heads * dim or t.data_ptr() % 16:
+    if stride & 7 or stride < width or t.data_ptr() & 15:
         _fail(name, "tokens must start on 16-byte boundaries and not overlap")
     return heads, stride
 
@@ -84,6 +89,18 @@ def check_batch(page_table, seq_lens, cu_q, n: int, device) -> KvBatch:
     return KvBatch(page_table.data_ptr(), width, seq_lens.data_ptr(), cu_q.data_ptr(), b, n)
 
 
+def _batch(page_table, seq_lens, cu_q, n: int, device, int32):
+    """check_batch's checks, and the batch packed; (how many sequences, packed)."""
+    shape = page_table.shape
+    if (len(shape) == 2 and page_table.dtype is int32 and seq_lens.dtype is int32 and cu_q.dtype is int32
+            and seq_lens.shape == shape[:1] and cu_q.shape == (shape[0] + 1,)
+            and page_table.is_contiguous() and seq_lens.is_contiguous() and cu_q.is_contiguous()
+            and page_table.device == device and seq_lens.device == device and cu_q.device == device):
+        return shape[0], _PACK(page_table.data_ptr(), shape[1], seq_lens.data_ptr(), cu_q.data_ptr(), shape[0], n)
+    check_batch(page_table, seq_lens, cu_q, n, device)   # says what is wrong
+    raise AssertionError("unreachable")
+
+
 class PagedKVCache:
     """One layer's cache and its ``ltk_kv`` handle on the current device.
 
@@ -103,6 +120,8 @@ class PagedKVCache:
             raise ValueError("k_codes, v_codes, k_scale, v_scale: give all four or none")
         self.device = torch.device("cuda", torch.cuda.current_device())
         self._torch, self._index, self._raw_stream = torch, self.device.index, torch._C._cuda_getCurrentRawStream
+        self._int32, self._float32 = torch.int32, torch.float32
+        self._codes = {torch.bfloat16: LTK_BF16, torch.float16: LTK_F16}
         codes, scales = (self.num_pages, self.heads, self.page, self.dim), (self.num_pages, self.heads)
         if not all(given):
             k_codes, v_codes = (torch.zeros(codes, dtype=torch.uint8, device=self.device) for _ in range(2))
@@ -128,17 +147,17 @@ class PagedKVCache:
         self.h = h
 
     # -- helpers ---------------------------------------------------------------
-    def _begin(self, stream, tensors) -> int:
+    def _begin(self, stream, *tensors) -> int:
         """The stream to launch on (its handle).  Tensors of the caller's that another
         stream than the current one reads or writes are kept from reuse until it has."""
         if self.h is None:
             raise ValueError("the cache is closed")
-        current = self._raw_stream(self._index)
-        if stream is None or stream.cuda_stream == current:
-            return current
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+        if stream is None:
+            return self._raw_stream(self._index)
+        if stream.cuda_stream != self._raw_stream(self._index):
+            for t in (*tensors, self.k_codes, self.v_codes, self.k_scale, self.v_scale):
+                if t is not None:
+                    t.record_stream(stream)
         return stream.cuda_stream
 
     def _new(self, stream, shape, dtype):
@@ -170,7 +189,7 @@ class PagedKVCache:
         """Stores the new tokens' k, v [N, heads, dim]; keys and q are rotated by the rows
         of cos, sin [positions, rot / 2] when given.  Returns the rotated q (None without q)."""
         n = k.shape[0]
-        batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
+        B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, self._int32)
         kh, ks = _rows(k, "k", n, self.dim, self.device)
         vh, vs = _rows(v, "v", n, self.dim, self.device, k.dtype)
         if kh != self.heads or vh != self.heads:
@@ -179,11 +198,13 @@ class PagedKVCache:
         if (cos is None) != (sin is None):
             raise ValueError("cos, sin: give both or neither")
         if cos is not None:
-            for t, name in ((cos, "cos"), (sin, "sin")):
-                if t.dim() != 2 or t.shape != cos.shape or t.dtype != self._torch.float32 or not t.is_contiguous():
-                    _fail(name, "expected contiguous float32 tables of equal shape [positions, rot / 2]")
-                _device_ok(t, name, self.device)
-            rows, rot = cos.shape[0], 2 * cos.shape[1]
+            table = cos.shape
+            if len(table) != 2 or sin.shape != table or cos.dtype is not self._float32 or sin.dtype is not self._float32 \
+                    or not (cos.is_contiguous() and sin.is_contiguous()):
+                raise ValueError("cos, sin: expected contiguous float32 tables of equal shape [positions, rot / 2]")
+            _device_ok(cos, "cos", self.device)
+            _device_ok(sin, "sin", self.device)
+            rows, rot = table[0], 2 * table[1]
         qh = qs = 0
         if q is not None:
             qh, qs = _rows(q, "q", n, self.dim, self.device, k.dtype)
@@ -193,12 +214,11 @@ class PagedKVCache:
             if tuple(q_out.shape) != (n, qh, self.dim) or q_out.dtype != q.dtype or not q_out.is_contiguous() \
                     or q_out.device != q.device:
                 _fail("q_out", f"expected a contiguous {q.dtype} tensor of shape {(n, qh, self.dim)}")
-        st = self._begin(stream, (k, v, page_table, seq_lens, cu_q, cos, sin, q, q_out, self.k_codes,
-                                  self.v_codes, self.k_scale, self.v_scale))
+        st = self._begin(stream, k, v, page_table, seq_lens, cu_q, cos, sin, q, q_out)
         if q is not None and q_out is None:
             q_out = self._new(stream, (n, qh, self.dim), q.dtype)
         ltk._check(self.lib.ltk_kv_append(
-            self.h, ctypes.byref(batch), DTYPES[str(k.dtype)], k.data_ptr(), ks, v.data_ptr(), vs,
+            self.h, batch, self._codes[k.dtype], k.data_ptr(), ks, v.data_ptr(), vs,
             None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(), rows, rot,
             1 if interleaved else 0, None if q is None else q.data_ptr(), qs, qh,
             None if q_out is None else q_out.data_ptr(), st), "ltk_kv_append")
@@ -210,15 +230,14 @@ class PagedKVCache:
         query at p sees keys j > p - window and the first ``sinks`` keys.  ``max_q`` (the most
         queries of one sequence) only helps choose a kernel.  Returns (out, lse)."""
         n = q.shape[0]
-        batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
+        B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, self._int32)
         heads, qs = _rows(q, "q", n, self.dim, self.device)
         if max_q is None:
-            max_q = -(-n // max(batch.B, 1))
-        st = self._begin(stream, (q, page_table, seq_lens, cu_q, out, lse, self.k_codes, self.v_codes, self.k_scale,
-                                  self.v_scale))
+            max_q = -(-n // max(B, 1))
+        st = self._begin(stream, q, page_table, seq_lens, cu_q, out, lse)
         out, lse = self._outputs(stream, q, n, heads, out, lse)
         ltk._check(self.lib.ltk_kv_attention(
-            self.h, ctypes.byref(batch), DTYPES[str(q.dtype)], q.data_ptr(), qs, heads, max_q, self._scale(scale),
+            self.h, batch, self._codes[q.dtype], q.data_ptr(), qs, heads, max_q, self._scale(scale),
             window, sinks, out.data_ptr(), lse.data_ptr(), st), "ltk_kv_attention")
         return out, lse
 
@@ -227,22 +246,21 @@ class PagedKVCache:
         """Attention of each query over its own key positions idx [N, k] (int32, -1 = empty
         slot), e.g. the indices IndexerTopK returns.  Returns (out, lse)."""
         n = q.shape[0]
-        batch = check_batch(page_table, seq_lens, cu_q, n, self.device)
+        B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, self._int32)
         heads, qs = _rows(q, "q", n, self.dim, self.device)
         if idx.dim() != 2:
             _fail("idx", f"expected a 2-D [queries, k] tensor, got shape {tuple(idx.shape)}")
         _ints(idx, "idx", (n, idx.shape[1]), self.device)
-        st = self._begin(stream, (q, idx, page_table, seq_lens, cu_q, out, lse, self.k_codes, self.v_codes, self.k_scale,
-                                  self.v_scale))
+        st = self._begin(stream, q, idx, page_table, seq_lens, cu_q, out, lse)
         out, lse = self._outputs(stream, q, n, heads, out, lse)
         ltk._check(self.lib.ltk_kv_attention_selected(
-            self.h, ctypes.byref(batch), DTYPES[str(q.dtype)], q.data_ptr(), qs, heads, idx.data_ptr(), idx.shape[1],
+            self.h, batch, self._codes[q.dtype], q.data_ptr(), qs, heads, idx.data_ptr(), idx.shape[1],
             self._scale(scale), out.data_ptr(), lse.data_ptr(), st), "ltk_kv_attention_selected")
         return out, lse
 
     def status(self, stream=None) -> int:
         """First error the device raised since the last call (0: none); synchronises the stream."""
-        st = self._begin(stream, ())
+        st = self._begin(stream)
         value = ctypes.c_int(0)
         ltk._check(self.lib.ltk_kv_status(self.h, ctypes.byref(value), st), "ltk_kv_status")
         return value.value

@@ -84,10 +84,11 @@ _SIGS = {
     "ltk_litedsa_pack": (_I, [_P, _I, _I, _I, _P, _P, _P, _P]),
     "ltk_kv_create": (_I, [ctypes.POINTER(KvConfig), ctypes.POINTER(_P)]),
     "ltk_kv_destroy": (None, [_P]),
-    "ltk_kv_append": (_I, [_P, ctypes.POINTER(KvBatch), _I, _P, _LL, _P, _LL, _P, _P, _I, _I, _I, _P, _LL,
+    # (the batch as an address: a KvBatch or its packed bytes, see kv.py)
+    "ltk_kv_append": (_I, [_P, _P, _I, _P, _LL, _P, _LL, _P, _P, _I, _I, _I, _P, _LL,
                            _I, _P, _P]),
-    "ltk_kv_attention": (_I, [_P, ctypes.POINTER(KvBatch), _I, _P, _LL, _I, _I, _F, _I, _I, _P, _P, _P]),
-    "ltk_kv_attention_selected": (_I, [_P, ctypes.POINTER(KvBatch), _I, _P, _LL, _I, _P, _I, _F, _P, _P,
+    "ltk_kv_attention": (_I, [_P, _P, _I, _P, _LL, _I, _I, _F, _I, _I, _P, _P, _P]),
+    "ltk_kv_attention_selected": (_I, [_P, _P, _I, _P, _LL, _I, _P, _I, _F, _P, _P,
                                        _P]),
     "ltk_kv_status": (_I, [_P, ctypes.POINTER(_I), _P]),
 }
