@@ -461,10 +461,11 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(const AppendParams p,
 cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream) {
   (void)num_sms;
   const int page = p.cache.page;
-  // Up to four tokens a sequence (on average): a warp for each token.  Beyond, a block
-  // for each page, whose rows share the loads' latency (8192 tokens of one sequence:
-  // 62 us against 91 with a warp for each token).
-  const bool few = p.batch.N <= 4ll * p.batch.B;
+  // Up to eight tokens a sequence (on average): a warp for each token and head.  Beyond, a
+  // block for each page, whose rows share the loads' latency.  64 sequences (8 KV heads, 32
+  // query heads of 128, in us): 1 token each 6.3 by warps and 15.6 by pages, 8 each 10.4 and
+  // 16.6, 16 each 16.9 and 17.2, 64 each 40 and 31; 8192 tokens of one sequence 81 and 45.
+  const bool few = p.batch.N <= 8ll * p.batch.B;
   const long long slots = (p.batch.N + static_cast<long long>(p.batch.B) * (2 * page - 2)) / page;
   const long long kv_blocks = few ? (static_cast<long long>(p.batch.N) * p.cache.heads + 3) / 4 : slots * p.cache.heads;
   const int warps = few ? 4 : page / 16;

@@ -196,8 +196,9 @@ class Setup:
     def q64(self):
         return self.q.double().numpy()
 
-    def gpu(self, engine=0):
-        """The framework's cache on the same data, and the batch's tensors."""
+    def gpu(self, engine=0, columns=0):
+        """The framework's cache on the same data, and the batch's tensors; the page table
+        padded to ``columns`` (its width is what the choice of kernel knows of lengths)."""
         import torch
         from indexer_topk_long_gb300 import PagedKVCache
         dev = {n: torch.from_numpy(self.c.codes[n]).cuda() for n in "kv"}
@@ -205,4 +206,6 @@ class Setup:
         cache = PagedKVCache(self.pages, self.c.heads, self.c.dim, page=self.c.page, k_codes=dev["k"],
                              v_codes=dev["v"], k_scale=scl["k"], v_scale=scl["v"], engine=engine)
         ints = [torch.tensor(np.asarray(x), dtype=torch.int32).cuda() for x in (self.table, self.lens, self.cu)]
+        if columns > ints[0].shape[1]:
+            ints[0] = torch.nn.functional.pad(ints[0], (0, columns - ints[0].shape[1]), value=-1)
         return cache, ints

@@ -11,6 +11,11 @@ pytestmark = pytest.mark.gpu
 KERNELS = [(1, 16), (2, 64), (2, 128), (2, 1000)]
 
 
+def _gpu(s, engine, rows):
+    """Pairs of tiles are for long sequences: the page table says so."""
+    return s.gpu(engine, 20000 if rows > 256 else 0)
+
+
 def _hint(s, rows):
     return max(1, rows // (s.q.shape[1] // s.c.heads))
 
@@ -18,7 +23,7 @@ def _hint(s, rows):
 def _dense(s, window=0, sinks=0, max_q=None, scale=None):
     want = s.c.attend(s.q64(), s.table, s.lens, s.cu, window, sinks, scale=scale)
     for engine, rows in [(0, None)] + KERNELS:
-        cache, ints = s.gpu(engine)
+        cache, ints = _gpu(s, engine, rows or 0)
         out, lse = cache.attention(s.q.cuda(), *ints, window=window, sinks=sinks, scale=scale,
                                    max_q=max_q if rows is None else _hint(s, rows))
         assert cache.status() == 0
@@ -104,7 +109,7 @@ def test_sequence_shorter_than_its_queries_and_empty():
     for engine, rows in KERNELS:
         s = ref.Setup([30, 30], [50, 4], 4, 1, 128, 16, "bf16", seed=17)
         s.lens = [30, 0]
-        cache, ints = s.gpu(engine)
+        cache, ints = _gpu(s, engine, rows)
         out, lse = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
         assert (out[:20] == 0).all() and torch.isneginf(lse[:20]).all()
         assert (out[50:] == 0).all() and torch.isneginf(lse[50:]).all()
@@ -117,7 +122,7 @@ def test_a_poisoned_token_reaches_only_the_queries_that_see_it(engine, rows):
     s = ref.Setup([100], [40], 4, 1, 128, 16, "bf16", seed=18)
     s.c.codes["k"][s.table[0, 80 // 16], 0, 80 % 16] = 0x7F
     s.c.codes["v"][s.table[0, 80 // 16], 0, 80 % 16] = 0
-    cache, ints = s.gpu(engine)
+    cache, ints = _gpu(s, engine, rows)
     out, _ = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
     bad = out.isnan()
     assert not bad[:20].any() and bad[20:].all()
@@ -128,7 +133,7 @@ def test_a_poisoned_token_reaches_only_the_queries_that_see_it(engine, rows):
 @pytest.mark.parametrize("engine,rows", KERNELS)
 def test_bad_page_is_reported(engine, rows):
     s = ref.Setup([100, 64], [20, 20], 4, 1, 128, 16, "bf16", seed=19)
-    cache, ints = s.gpu(engine)
+    cache, ints = _gpu(s, engine, rows)
     ints[0][0, 2] = s.pages + 7
     out, _ = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
     assert cache.status() == 1 and cache.status() == 0
@@ -139,7 +144,7 @@ def test_bad_page_is_reported(engine, rows):
 def test_bad_page_reaches_only_the_queries_that_see_it(engine, rows):
     """The page after the first ten queries' positions is outside the pool."""
     s = ref.Setup([90], [40], 4, 1, 128, 16, "bf16", seed=27)
-    cache, ints = s.gpu(engine)
+    cache, ints = _gpu(s, engine, rows)
     ints[0][0, 4] = -3                      # positions 64 .. 79; queries at 50 .. 89
     out, _ = cache.attention(s.q.cuda(), *ints, max_q=_hint(s, rows))
     assert cache.status() == 1
@@ -202,7 +207,7 @@ def test_cu_q_that_does_not_rise():
     s = ref.Setup([60, 50], [40, 30], 4, 1, 128, 16, "bf16", seed=30)
     want = s.c.attend(s.q64(), s.table, s.lens, s.cu)
     for engine, rows in KERNELS:
-        cache, ints = s.gpu(engine)
+        cache, ints = _gpu(s, engine, rows)
         for bad in ([0, 50, 30], [0, 40, 1 << 30], [-7, 40, 70]):
             cu = torch.tensor(bad, dtype=torch.int32).cuda()
             cache.attention(s.q.cuda(), ints[0], ints[1], cu, max_q=_hint(s, rows))
@@ -241,7 +246,7 @@ def test_same_bits_every_time_and_under_capture():
     import torch
     for hq, new, engine in ((8, 1, 1), (8, 100, 2), (64, 3, 1), (64, 3, 2), (100, 1, 2)):
         s = ref.Setup([3000], [new], hq, 1, 128, 64, "bf16", seed=23)
-        cache, ints = s.gpu(engine)
+        cache, ints = _gpu(s, engine, new * hq)
         q = s.q.cuda()
         idx = torch.randperm(2900, device="cuda")[:500].to(torch.int32).expand(new, 500).contiguous()
         first = [t.clone() for t in cache.attention(q, *ints) + cache.attention_selected(q, idx, *ints)]
