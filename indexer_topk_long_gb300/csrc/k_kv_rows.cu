@@ -44,14 +44,15 @@ constexpr float kMinusHuge = -1e30f;     // running maximum of a row that has se
 constexpr float kBoost = 8.f;
 constexpr float kSlack = 7.f;
 
-template <int D>
+template <int D, int RT>
 struct RowsSmem {
+  static constexpr int kRows = 8 * RT;                        // of a unit
   static constexpr int kStageBytes = kWarpKeys * D * 2;
   static constexpr int kMetaFloats = 3 * kWarpKeys;           // ks, vs, valid of each key
   static constexpr int kWarpBytes = kStages * (kStageBytes + kMetaFloats * 4);
-  static constexpr int kBytes = kWarps * kWarpBytes + kWarps * kRowsPerUnit * 2 * 4;   // and each row's (M, l)
+  static constexpr int kBytes = kWarps * kWarpBytes + kWarps * kRows * 2 * 4;   // and each row's (M, l)
   // at a piece's end a warp's results take the place of the stage it has just read
-  static_assert(kStageBytes == kRowsPerUnit * D * 4, "merge buffer");
+  static_assert(kStageBytes >= kRows * D * 4, "merge buffer");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
@@ -75,6 +76,19 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit elements across the warp (row lane / 4, columns 2 (lane % 4) ..), transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Where 16-byte chunk `chunk` of row r of a warp's results lies in its row of the merge buffer:
+// a quarter warp's stores are two chunks of every other row of eight.
+template <int D>
+__device__ __forceinline__ int merge_place(int r, int chunk) {
+  return chunk ^ (D == 128 ? (r >> 1) & 3 : ((r >> 1) & 1) | ((r >> 2) & 1) << 2);
 }
 
 // Row r of a 16-key group and 16-byte chunk: byte offset in the group's codes.  Lanes
@@ -118,7 +132,8 @@ struct Cursor {
   Unit w;
 };
 
-__device__ __forceinline__ int groups_of(int rows) { return (rows + kRowsPerUnit - 1) / kRowsPerUnit; }
+template <int RT>
+__device__ __forceinline__ int groups_of(int rows) { return (rows + 8 * RT - 1) / (8 * RT); }
 
 // Key tiles of sequence s that some query sees: sinks' tiles, then from the first
 // query's window start to the end.
@@ -135,10 +150,10 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, const KvSeq& s, int
   return sk + n - lo;
 }
 
-template <bool SEL>
+template <bool SEL, int RT>
 __device__ __forceinline__ void enter_unit(const AttnParams& p, Cursor& c) {
   if constexpr (SEL) {
-    const int rg = groups_of(p.group);
+    const int rg = groups_of<RT>(p.group);
     const int per = rg * p.cache.heads;
     const int n = static_cast<int>(c.unit / per), r = static_cast<int>(c.unit % per);
     const int b = kv_seq_of_query(p.batch, n);
@@ -149,13 +164,13 @@ __device__ __forceinline__ void enter_unit(const AttnParams& p, Cursor& c) {
     c.w.pos0 = (n >= s.q0 && n < s.q0 + s.nq) ? min(s.pos0 + n - s.q0, s.len - 1) : -1;
     c.w.len = p.k;
     c.w.head = r / rg;
-    c.w.row0 = (r % rg) * kRowsPerUnit;
+    c.w.row0 = (r % rg) * 8 * RT;
     c.w.skip = c.w.tile0 = 0;
     c.n_tiles = (p.k + kTileKeys - 1) / kTileKeys;
   } else {
-    const int rg = groups_of(c.w.nq * p.group);
+    const int rg = groups_of<RT>(c.w.nq * p.group);
     c.w.head = c.u / rg;
-    c.w.row0 = (c.u % rg) * kRowsPerUnit;
+    c.w.row0 = (c.u % rg) * 8 * RT;
   }
 }
 
@@ -171,23 +186,23 @@ __device__ __forceinline__ void enter_seq(const AttnParams& p, Cursor& c, int b)
 }
 
 // One tile forward.
-template <bool SEL>
+template <bool SEL, int RT>
 __device__ __forceinline__ void advance(const AttnParams& p, Cursor& c) {
   --c.left;
   if (++c.t < c.n_tiles || c.left <= 0) return;
   c.t = 0;
   if constexpr (SEL) {
     ++c.unit;
-    enter_unit<SEL>(p, c);
+    enter_unit<SEL, RT>(p, c);
   } else {
-    if (++c.u >= groups_of(c.w.nq * p.group) * p.cache.heads) {
+    if (++c.u >= groups_of<RT>(c.w.nq * p.group) * p.cache.heads) {
       c.u = 0;
       int b = c.w.b;
       do {
         enter_seq(p, c, ++b);
       } while (c.n_tiles == 0 && b + 1 < p.batch.B);
     }
-    enter_unit<SEL>(p, c);
+    enter_unit<SEL, RT>(p, c);
   }
 }
 
@@ -196,14 +211,15 @@ struct Feed {            // what the next tile's copies need, fetched a step ahe
   int page[kGroups];     // dense: the groups' pages, -1 beyond the length
 };
 
-template <int D, bool SEL>
+template <int D, bool SEL, int RT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const AttnParams p, const int grid) {
-  using S = RowsSmem<D>;
+  using S = RowsSmem<D, RT>;
+  constexpr int kRows = S::kRows;
   constexpr int KS = D / 16;             // k-steps of the score product
-  constexpr int NT = D / 8;              // n-tiles of the value product
+  constexpr int NT = D / 8;              // elements of a row's result that a lane holds
   constexpr int CPR = D / 16;            // 16-byte chunks in a row of codes
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ long long sh_total, sh_start;
+  __shared__ long long sh_start;
   __shared__ long long sh_warp[kWarps];
   __shared__ int sh_b;
   __shared__ int sh_last;
@@ -216,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
   Cursor head{};
   if constexpr (SEL) {
     const int tiles = (p.k + kTileKeys - 1) / kTileKeys;
-    total = static_cast<long long>(p.batch.N) * groups_of(p.group) * p.cache.heads * tiles;
+    total = static_cast<long long>(p.batch.N) * groups_of<RT>(p.group) * p.cache.heads * tiles;
     n_cta = static_cast<int>(min(static_cast<long long>(grid), total));
   } else {
     const int each = (p.batch.B + kThreads - 1) / kThreads;
@@ -225,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     int sk, t0;
     for (int b = b0; b < b1; ++b) {
       const KvSeq s = kv_seq(p.batch, p.cache, b);
-      mine += static_cast<long long>(tiles_of(p, s, &sk, &t0)) * groups_of(s.nq * p.group) * p.cache.heads;
+      mine += static_cast<long long>(tiles_of(p, s, &sk, &t0)) * groups_of<RT>(s.nq * p.group) * p.cache.heads;
     }
     long long incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
@@ -246,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       long long x = before;
       for (int b = b0; b < b1; ++b) {
         const KvSeq s = kv_seq(p.batch, p.cache, b);
-        const long long n = static_cast<long long>(tiles_of(p, s, &sk, &t0)) * groups_of(s.nq * p.group) * p.cache.heads;
+        const long long n = static_cast<long long>(tiles_of(p, s, &sk, &t0)) * groups_of<RT>(s.nq * p.group) * p.cache.heads;
         if (start < x + n) {
           sh_b = b;
           sh_start = x;
@@ -271,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       head.u = static_cast<int>(in / head.n_tiles);
       head.t = static_cast<int>(in % head.n_tiles);
     }
-    enter_unit<SEL>(p, head);
+    enter_unit<SEL, RT>(p, head);
   }
 
   unsigned char* ring = smem + warp * S::kWarpBytes;
@@ -380,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
           }
         }
       }
-      advance<SEL>(p, pc);
+      advance<SEL, RT>(p, pc);
       fetch();
     }
     cp_commit();
@@ -402,10 +418,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
   }
 
   // --- consumer ---------------------------------------------------------------------------
-  uint32_t qf[KS][4];
-  float o[NT][4];
-  float M[2], l[2], crow[2];
-  int prow[2];                           // query position of rows g, g + 8
+  // Rows of tile x: 8 x + 2 cq and the next; results: elements g NT .. of both.
+  uint32_t qf[RT][KS][2];
+  float o[RT][NT / 2][4];                // [.][i]: elements 2 i of both rows, then 2 i + 1
+  float M[RT][2], l[RT][2], crow[RT][2];
+  int prow[RT][2];                       // the rows' query positions, -1: no such row
   int stage_out = 0;
   long long at = start;                  // where head stands on the line
 
@@ -416,11 +433,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     const int t_end = min(head.n_tiles, head.t + head.left);
     const int rows_all = head.w.nq * p.group;
 #pragma unroll
-    for (int hlf = 0; hlf < 2; ++hlf) {
-      const int r = head.w.row0 + g + 8 * hlf;
+    for (int x = 0; x < RT; ++x) {
+      // as an operand a lane holds row 8 x + g
+      const int r = head.w.row0 + g + 8 * x;
       const bool on = r < rows_all;
       const int qi = r / p.group;
-      prow[hlf] = on ? (SEL ? head.w.pos0 : head.w.pos0 + qi) : -1;
       uint4 raw[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
@@ -447,7 +464,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 8;
       e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
       const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      crow[hlf] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      const float scale = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      const int pos = on ? (SEL ? head.w.pos0 : head.w.pos0 + qi) : -1;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        crow[x][n] = __shfl_sync(0xFFFFFFFFu, scale, (2 * cq + n) * 4);
+        prow[x][n] = __shfl_sync(0xFFFFFFFFu, pos, (2 * cq + n) * 4);
+      }
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint32_t ws[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -456,18 +479,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
           const float2 f = kv_unpack16(ws[j], p.bf16);
           // words 2 i' and 2 i' + 1 of a chunk are k-step i' (bytes 0-1 and 2-3 of a code word)
           const int word = i * 4 + j;
-          qf[word >> 1][hlf + 2 * (word & 1)] = kv_pack16(f.x * by, f.y * by, false);
+          qf[x][word >> 1][word & 1] = kv_pack16(f.x * by, f.y * by, false);
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int x = 0; x < RT; ++x) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-    M[0] = M[1] = kMinusHuge;
-    l[0] = l[1] = 0.f;
+      for (int i = 0; i < NT / 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[x][i][j] = 0.f;
+      M[x][0] = M[x][1] = kMinusHuge;
+      l[x][0] = l[x][1] = 0.f;
+    }
     const int p_lo = SEL ? 0 : head.w.pos0 + head.w.row0 / p.group;
-    const int p_hi = SEL ? 0 : head.w.pos0 + min(head.w.row0 + kRowsPerUnit - 1, rows_all - 1) / p.group;
+    const int p_hi = SEL ? 0 : head.w.pos0 + min(head.w.row0 + kRows - 1, rows_all - 1) / p.group;
 
 #pragma unroll 1
     for (int t = t_begin; t < t_end; ++t) {
@@ -483,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       const int key0 = tile * kTileKeys + warp * kWarpKeys;
       if (!SEL && (key0 >= head.w.len || key0 > p_hi)) continue;
 
-      float s[kGroups][2][4] = {};
+      float s[RT][kGroups][4] = {};
 #pragma unroll
       for (int half = 0; half < D / 64; ++half)
 #pragma unroll
@@ -493,100 +519,95 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
           const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t a0, a1, b0, b1;
-            e4m3x4_to_f16(aw[i], a0, a1);
-            e4m3x4_to_f16(bw[i], b0, b1);
-            mma_f16(s[h][0], qf[half * 4 + i], a0, a1);
-            mma_f16(s[h][1], qf[half * 4 + i], b0, b1);
+            uint32_t k[4];
+            e4m3x4_to_f16(aw[i], k[0], k[2]);
+            e4m3x4_to_f16(bw[i], k[1], k[3]);
+#pragma unroll
+            for (int x = 0; x < RT; ++x) mma_f16(s[x][h], k, qf[x][half * 4 + i][0], qf[x][half * 4 + i][1]);
           }
         }
-      // element e of s[h][n]: row g + 8 (e >> 1), key 16 h + 8 n + 2 cq + (e & 1)
+      // element e of s[x][h]: key 16 h + g + 8 (e >> 1), row 8 x + 2 cq + (e & 1)
       const bool inside = !SEL && key0 + kWarpKeys - 1 <= p_lo &&
                           (p.window <= 0 || key0 > p_hi - p.window || key0 + kWarpKeys <= p.sinks);
-      float iv[kGroups][SEL ? 4 : 1];    // 1 / vs: of each of the lane's keys, or of the group
-      float mx[2] = {-__int_as_float(0x7F800000), -__int_as_float(0x7F800000)};
+      float iv[kGroups][2];              // 1 / vs of the lane's keys
+      float mx[RT][2];
+#pragma unroll
+      for (int x = 0; x < RT; ++x) mx[x][0] = mx[x][1] = -__int_as_float(0x7F800000);
 #pragma unroll
       for (int h = 0; h < kGroups; ++h) {
-        float ks[4], lv[4];
-        bool valid[4];
+        float ks[2], lv[2];
+        bool valid[2] = {true, true};
         if constexpr (SEL) {
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const int at0 = 16 * h + 8 * n + 2 * cq;
-            const float2 a = *reinterpret_cast<const float2*>(m + at0);
-            const float2 b = *reinterpret_cast<const float2*>(m + kWarpKeys + at0);
-            const float2 z = *reinterpret_cast<const float2*>(m + 2 * kWarpKeys + at0);
-            ks[2 * n] = a.x;
-            ks[2 * n + 1] = a.y;
-            lv[2 * n] = __log2f(b.x) + kBoost;
-            lv[2 * n + 1] = __log2f(b.y) + kBoost;
-            iv[h][2 * n] = __frcp_rn(b.x);
-            iv[h][2 * n + 1] = __frcp_rn(b.y);
-            valid[2 * n] = z.x != 0.f;
-            valid[2 * n + 1] = z.y != 0.f;
+            const int at0 = 16 * h + 8 * n + g;
+            const float vs = m[kWarpKeys + at0];
+            ks[n] = m[at0];
+            lv[n] = __log2f(vs) + kBoost;
+            iv[h][n] = __frcp_rn(vs);
+            valid[n] = m[2 * kWarpKeys + at0] != 0.f;
           }
         } else {
           // a group beyond the length was not copied: its keys are masked, its values skipped
           const float2 sc = key0 + 16 * h < head.w.len ? *reinterpret_cast<const float2*>(m + 2 * h) : make_float2(1.f, 1.f);
-          const float lg = __log2f(sc.y) + kBoost;
-          iv[h][0] = __frcp_rn(sc.y);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            ks[i] = sc.x;
-            lv[i] = lg;
-          }
+          ks[0] = ks[1] = sc.x;
+          lv[0] = lv[1] = __log2f(sc.y) + kBoost;
+          iv[h][0] = iv[h][1] = __frcp_rn(sc.y);
         }
-        const float f0 = ks[0] * crow[0], f1 = ks[0] * crow[1];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int x = 0; x < RT; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int hlf = e >> 1, kk = 2 * n + (e & 1);
-            float x = SEL ? fmaf(s[h][n][e] * ks[kk], crow[hlf], lv[kk]) : fmaf(s[h][n][e], hlf ? f1 : f0, lv[0]);
+            const int kk = e >> 1, n = e & 1;
+            float t = fmaf(s[x][h][e], ks[kk] * crow[x][n], lv[kk]);
             if constexpr (SEL) {
-              if (!valid[kk]) x = -__int_as_float(0x7F800000);
+              if (!valid[kk]) t = -__int_as_float(0x7F800000);
             } else if (!inside) {
-              const int key = key0 + 16 * h + 8 * n + 2 * cq + (e & 1);
-              const bool seen = key <= prow[hlf] && (p.window <= 0 || key > prow[hlf] - p.window || key < p.sinks);
-              if (!seen) x = -__int_as_float(0x7F800000);
+              const int key = key0 + 16 * h + g + 8 * kk;
+              const bool seen = key <= prow[x][n] && (p.window <= 0 || key > prow[x][n] - p.window || key < p.sinks);
+              if (!seen) t = -__int_as_float(0x7F800000);
             }
-            s[h][n][e] = x;
-            mx[hlf] = fmaxf(mx[hlf], x);
+            s[x][h][e] = t;
+            mx[x][n] = fmaxf(mx[x][n], t);
           }
       }
-      if (__any_sync(0xFFFFFFFFu, mx[0] > M[0] + (kSlack + kBoost) || mx[1] > M[1] + (kSlack + kBoost))) {
+      bool outgrown = false;
 #pragma unroll
-        for (int hlf = 0; hlf < 2; ++hlf) {
-          float top = mx[hlf] - kBoost;
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          const float next = fmaxf(M[hlf], top);
-          const float by = exp2_approx(M[hlf] - next);
-          M[hlf] = next;
-          l[hlf] *= by;
+      for (int x = 0; x < RT; ++x)
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            o[i][2 * hlf] *= by;
-            o[i][2 * hlf + 1] *= by;
+        for (int n = 0; n < 2; ++n) outgrown = outgrown || mx[x][n] > M[x][n] + (kSlack + kBoost);
+      if (__any_sync(0xFFFFFFFFu, outgrown)) {
+#pragma unroll
+        for (int x = 0; x < RT; ++x)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float top = mx[x][n] - kBoost;
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            const float next = fmaxf(M[x][n], top);
+            const float by = exp2_approx(M[x][n] - next);
+            M[x][n] = next;
+            l[x][n] *= by;
+#pragma unroll
+            for (int i = 0; i < NT / 2; ++i) {
+              o[x][i][n] *= by;
+              o[x][i][2 + n] *= by;
+            }
           }
-        }
       }
 #pragma unroll
       for (int h = 0; h < kGroups; ++h) {
         if (!SEL && key0 + 16 * h >= head.w.len) break;       // not copied
-        uint32_t pf[4];
+        uint32_t pf[RT][2];
 #pragma unroll
-        for (int hlf = 0; hlf < 2; ++hlf) {
-          float sum = 0.f;
+        for (int x = 0; x < RT; ++x)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float w0 = exp2_approx(s[h][n][2 * hlf] - M[hlf]), w1 = exp2_approx(s[h][n][2 * hlf + 1] - M[hlf]);
-            if constexpr (SEL) l[hlf] = fmaf(w0, iv[h][2 * n], fmaf(w1, iv[h][2 * n + 1], l[hlf]));
-            else sum += w0 + w1;
-            pf[hlf + 2 * n] = kv_pack16(w0, w1, false);
+          for (int kk = 0; kk < 2; ++kk) {
+            const float w0 = exp2_approx(s[x][h][2 * kk] - M[x][0]), w1 = exp2_approx(s[x][h][2 * kk + 1] - M[x][1]);
+            l[x][0] = fmaf(w0, iv[h][kk], l[x][0]);
+            l[x][1] = fmaf(w1, iv[h][kk], l[x][1]);
+            pf[x][kk] = transposed(kv_pack16(w0, w1, false));
           }
-          if constexpr (!SEL) l[hlf] = fmaf(sum, iv[h][0], l[hlf]);
-        }
         // values: this lane's keys 2 cq, 2 cq + 1 (and + 8), its g-th D / 8 elements
         uint32_t vw[4][D / 32];
 #pragma unroll
@@ -594,31 +615,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
           const int r = 2 * cq + (i & 1) + 8 * (i >> 1);
           const unsigned char* row = vp + 16 * h * D;
           if constexpr (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(row + place<D>(r, g));
-            vw[i][0] = x.x;
-            vw[i][1] = x.y;
-            vw[i][2] = x.z;
-            vw[i][3] = x.w;
+            const uint4 v = *reinterpret_cast<const uint4*>(row + place<D>(r, g));
+            vw[i][0] = v.x;
+            vw[i][1] = v.y;
+            vw[i][2] = v.z;
+            vw[i][3] = v.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(row + place<D>(r, g >> 1) + (g & 1) * 8);
-            vw[i][0] = x.x;
-            vw[i][1] = x.y;
+            const uint2 v = *reinterpret_cast<const uint2*>(row + place<D>(r, g >> 1) + (g & 1) * 8);
+            vw[i][0] = v.x;
+            vw[i][1] = v.y;
           }
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-          const uint32_t x[4] = {vw[0][w], vw[1][w], vw[2][w], vw[3][w]};
-          const uint32_t a01 = __byte_perm(x[0], x[1], 0x5140), a23 = __byte_perm(x[0], x[1], 0x7362);
-          const uint32_t b01 = __byte_perm(x[2], x[3], 0x5140), b23 = __byte_perm(x[2], x[3], 0x7362);
-          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-          e4m3x4_to_f16(a01, a0, a1);
-          e4m3x4_to_f16(a23, a2, a3);
-          e4m3x4_to_f16(b01, b0, b1);
-          e4m3x4_to_f16(b23, b2, b3);
-          mma_f16(o[w * 4], pf, a0, b0);
-          mma_f16(o[w * 4 + 1], pf, a1, b1);
-          mma_f16(o[w * 4 + 2], pf, a2, b2);
-          mma_f16(o[w * 4 + 3], pf, a3, b3);
+          // elements 4 w .. 4 w + 3 of the lane's, each of two neighbouring keys
+          const uint32_t v[4] = {vw[0][w], vw[1][w], vw[2][w], vw[3][w]};
+          const uint32_t a01 = __byte_perm(v[0], v[1], 0x5140), a23 = __byte_perm(v[0], v[1], 0x7362);
+          const uint32_t b01 = __byte_perm(v[2], v[3], 0x5140), b23 = __byte_perm(v[2], v[3], 0x7362);
+          uint32_t e01[4], e23[4];
+          e4m3x4_to_f16(a01, e01[0], e01[1]);
+          e4m3x4_to_f16(b01, e01[2], e01[3]);
+          e4m3x4_to_f16(a23, e23[0], e23[1]);
+          e4m3x4_to_f16(b23, e23[2], e23[3]);
+#pragma unroll
+          for (int x = 0; x < RT; ++x) {
+            mma_f16(o[x][2 * w], e01, pf[x][0], pf[x][1]);
+            mma_f16(o[x][2 * w + 1], e23, pf[x][0], pf[x][1]);
+          }
         }
       }
     }
@@ -629,34 +652,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     auto merge_of = [&](int w) { return reinterpret_cast<float*>(smem + w * S::kWarpBytes + spare * S::kStageBytes); };
     __syncwarp();
 #pragma unroll
-    for (int hlf = 0; hlf < 2; ++hlf) {
-      l[hlf] += __shfl_xor_sync(0xFFFFFFFFu, l[hlf], 1);
-      l[hlf] += __shfl_xor_sync(0xFFFFFFFFu, l[hlf], 2);
-      const int r = g + 8 * hlf;
-      if (head.w.row0 + r >= rows_all) continue;               // no such row
-      if (cq == 0) {
-        merge_ml[(warp * kRowsPerUnit + r) * 2] = M[hlf];
-        merge_ml[(warp * kRowsPerUnit + r) * 2 + 1] = l[hlf];
-      }
-      // element e of n-tile nt is column (2 cq + e) * NT + nt
-      float* dst = merge_of(warp) + r * D;
+    for (int x = 0; x < RT; ++x)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int n = 0; n < 2; ++n) {
 #pragma unroll
-        for (int nt = 0; nt < NT; nt += 4) {
-          const int chunk = ((2 * cq + e) * NT + nt) >> 2;
-          const int at = chunk ^ (((chunk >> 3) & 3) | ((r & 1) << 2));
-          *reinterpret_cast<float4*>(dst + at * 4) =
-              make_float4(o[nt][2 * hlf + e], o[nt + 1][2 * hlf + e], o[nt + 2][2 * hlf + e], o[nt + 3][2 * hlf + e]);
+        for (int d = 4; d < 32; d <<= 1) l[x][n] += __shfl_xor_sync(0xFFFFFFFFu, l[x][n], d);
+        const int r = 8 * x + 2 * cq + n;
+        if (head.w.row0 + r >= rows_all) continue;             // no such row
+        if (g == 0) {
+          merge_ml[(warp * kRows + r) * 2] = M[x][n];
+          merge_ml[(warp * kRows + r) * 2 + 1] = l[x][n];
         }
-    }
+        float* dst = merge_of(warp) + r * D;
+#pragma unroll
+        for (int i = 0; i < NT / 2; i += 2)
+          *reinterpret_cast<float4*>(dst + merge_place<D>(r, (g * NT + 2 * i) >> 2) * 4) =
+              make_float4(o[x][i][n], o[x][i][2 + n], o[x][i + 1][n], o[x][i + 1][2 + n]);
+      }
     __syncthreads();
-    const int rows = min(rows_all - head.w.row0, kRowsPerUnit);
+    const int rows = min(rows_all - head.w.row0, kRows);
     const bool whole = t_begin == 0 && t_end == head.n_tiles;
     // Contributors of this unit and its place in the workspace.
     const long long u0 = at - t_begin, u1 = u0 + head.n_tiles;       // the unit on the line
     const int c0 = static_cast<int>(((u0 + 1) * n_cta - 1) / total), c1 = static_cast<int>((u1 * n_cta - 1) / total);
-    constexpr int kSlot = kRowsPerUnit * (D + 2);
+    constexpr int kSlot = kRows * (D + 2);
     float* mine = p.part + static_cast<size_t>(2 * blockIdx.x + (t_begin == 0 ? 1 : 0)) * kSlot;
     auto write_row = [&](int r, int ch, float4 v, float m2, float sum) {
       const int row = head.w.row0 + r;
@@ -673,14 +692,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       const int r = i / (D / 4), ch = i % (D / 4);
       float mx = kMinusHuge;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, merge_ml[(w * kRowsPerUnit + r) * 2]);
+      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, merge_ml[(w * kRows + r) * 2]);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float by = exp2_approx(merge_ml[(w * kRowsPerUnit + r) * 2] - mx);
-        sum = fmaf(merge_ml[(w * kRowsPerUnit + r) * 2 + 1], by, sum);
-        const int at = ch ^ (((ch >> 3) & 3) | ((r & 1) << 2));
+        const float by = exp2_approx(merge_ml[(w * kRows + r) * 2] - mx);
+        sum = fmaf(merge_ml[(w * kRows + r) * 2 + 1], by, sum);
+        const int at = merge_place<D>(r, ch);
         const float4 v = *reinterpret_cast<const float4*>(merge_of(w) + r * D + at * 4);
         acc.x = fmaf(v.x, by, acc.x);
         acc.y = fmaf(v.y, by, acc.y);
@@ -690,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       if (whole) {
         write_row(r, ch, acc, mx, sum);
       } else {
-        __stcg(reinterpret_cast<float4*>(mine + kRowsPerUnit * 2 + r * D) + ch, acc);
+        __stcg(reinterpret_cast<float4*>(mine + kRows * 2 + r * D) + ch, acc);
         if (ch == 0) __stcg(reinterpret_cast<float2*>(mine) + r, make_float2(mx, sum));
       }
     }
@@ -708,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
           for (int cta = c0; cta <= c1; ++cta) {
             const float* src = p.part + static_cast<size_t>(2 * cta + (cta == c0 ? 1 : 0)) * kSlot;
             const float2 ml = __ldcg(reinterpret_cast<const float2*>(src) + r);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + kRowsPerUnit * 2 + r * D) + ch);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + kRows * 2 + r * D) + ch);
             const float next = fmaxf(mx, ml.x);
             const float a = exp2_approx(mx - next), b = exp2_approx(ml.x - next);
             mx = next;
@@ -729,14 +748,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     at += n;
     head.left -= n - 1;
     head.t = t_end - 1;
-    advance<SEL>(p, head);
+    advance<SEL, RT>(p, head);
   }
   cp_wait<0>();
 }
 
+template <int D, bool SEL, int RT>
+cudaError_t init_rows() {
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_rows_kernel<D, SEL, RT>),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, RowsSmem<D, RT>::kBytes);
+}
+
 template <int D, bool SEL>
-const void* rows_fn() {
-  return reinterpret_cast<const void*>(kv_rows_kernel<D, SEL>);
+void launch_rows(const AttnParams& p, bool narrow, int grid, cudaStream_t stream) {
+  if (narrow) kv_rows_kernel<D, SEL, 1><<<grid, kThreads, RowsSmem<D, 1>::kBytes, stream>>>(p, grid);
+  else kv_rows_kernel<D, SEL, 2><<<grid, kThreads, RowsSmem<D, 2>::kBytes, stream>>>(p, grid);
 }
 
 }  // namespace
@@ -745,24 +771,24 @@ size_t kv_rows_part_floats(int num_sms) { return static_cast<size_t>(2) * kCtasP
 int kv_rows_counters(int num_sms) { return kCtasPerSm * num_sms; }
 
 cudaError_t kv_rows_init() {
-  const void* fns[4] = {rows_fn<128, false>(), rows_fn<128, true>(), rows_fn<64, false>(), rows_fn<64, true>()};
-  for (int i = 0; i < 4; ++i) {
-    const cudaError_t e = cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               i < 2 ? RowsSmem<128>::kBytes : RowsSmem<64>::kBytes);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e[8] = {init_rows<128, false, 1>(), init_rows<128, false, 2>(), init_rows<128, true, 1>(),
+                            init_rows<128, true, 2>(),  init_rows<64, false, 1>(),  init_rows<64, false, 2>(),
+                            init_rows<64, true, 1>(),   init_rows<64, true, 2>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
   return cudaSuccess;
 }
 
-cudaError_t launch_kv_rows(const AttnParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_kv_rows(const AttnParams& p, int max_q, int num_sms, cudaStream_t stream) {
   const bool sel = p.idx != nullptr;
   const int grid = kCtasPerSm * num_sms;
+  const bool narrow = static_cast<long long>(p.group) * (sel ? 1 : max_q) <= 8;
   if (p.dim == 128) {
-    if (sel) kv_rows_kernel<128, true><<<grid, kThreads, RowsSmem<128>::kBytes, stream>>>(p, grid);
-    else kv_rows_kernel<128, false><<<grid, kThreads, RowsSmem<128>::kBytes, stream>>>(p, grid);
+    if (sel) launch_rows<128, true>(p, narrow, grid, stream);
+    else launch_rows<128, false>(p, narrow, grid, stream);
   } else {
-    if (sel) kv_rows_kernel<64, true><<<grid, kThreads, RowsSmem<64>::kBytes, stream>>>(p, grid);
-    else kv_rows_kernel<64, false><<<grid, kThreads, RowsSmem<64>::kBytes, stream>>>(p, grid);
+    if (sel) launch_rows<64, true>(p, narrow, grid, stream);
+    else launch_rows<64, false>(p, narrow, grid, stream);
   }
   count_launches(1);
   return cudaGetLastError();

@@ -232,7 +232,7 @@ static ltk_status kv_attend(ltk_kv* h, const ltk_kv_batch* batch, int dtype, con
   const int most_q = max_q > 0 ? max_q : batch->N;
   const bool by_rows = h->engine == 0 ? kv_use_rows(p, most_q, h->num_sms) : h->engine == 1;
   const bool by_list = idx != nullptr && p.group <= kListRows;
-  const cudaError_t e = by_rows   ? launch_kv_rows(p, h->num_sms, st)
+  const cudaError_t e = by_rows   ? launch_kv_rows(p, most_q, h->num_sms, st)
                         : by_list ? launch_kv_list(p, h->num_sms, st)
                                   : launch_kv_tile(p, most_q, h->num_sms, st);
   return kv_cuda_fail(e, "kv attention");

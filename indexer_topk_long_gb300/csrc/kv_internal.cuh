@@ -155,7 +155,7 @@ constexpr int kRowsPerUnit = 16;
 size_t kv_rows_part_floats(int num_sms);   // workspace floats
 int kv_rows_counters(int num_sms);
 cudaError_t kv_rows_init();                // kernel attributes on the current device
-cudaError_t launch_kv_rows(const AttnParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_rows(const AttnParams& p, int max_q, int num_sms, cudaStream_t stream);
 
 // Attention for many rows per KV head, on the tensor cores (k_kv_tile.cu).
 size_t kv_tile_part_floats(int num_sms);

@@ -7,8 +7,8 @@ import kv_reference as ref
 pytestmark = pytest.mark.gpu
 
 
-# (engine, rows the hint speaks of): the kernel for few rows, then narrow, whole and paired tiles
-KERNELS = [(1, 16), (2, 64), (2, 128), (2, 1000)]
+# (engine, rows the hint speaks of): the kernel for few rows (8 or 16 a unit), then narrow, whole and paired tiles
+KERNELS = [(1, 8), (1, 16), (2, 64), (2, 128), (2, 1000)]
 
 
 def _gpu(s, engine, rows):
