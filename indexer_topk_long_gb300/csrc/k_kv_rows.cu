@@ -19,12 +19,17 @@
 // CTAs in a fixed order.  Each of a CTA's 4 warps takes 32 keys of a tile through
 // its own ring of asynchronous 16-byte copies (no block barrier in the loop).
 //
-// Measured (8 KV heads of 4 query heads, D = 128): one sequence of 262144 tokens 97 us, 537 MB
-// at 5.5 TB/s, 81% of the copy rate; 64 sequences of 128 to 32768 tokens 154 us, 795 MB at 5.2
-// TB/s, 76%; 2048 listed keys for 64 heads of one KV head 16 us, which is latency.  What bounds
-// it is the arithmetic of the 12 warps that fit an SM (codes to f16, then m16n8k16 products of
-// 16 rows, half of them empty at 8 rows): half of all issue slots are used and warps hardly
-// ever wait for memory.
+// Keys are the products' rows (S^T = K Q^T, O^T = V^T P) and the query rows their columns, 8 or
+// 16: a small group leaves few columns empty, and a lane's weights are of few keys.  P comes
+// from the scores' layout by an 8 x 8 transposition across the warp.
+//
+// Measured (8 KV heads of 4 query heads, D = 128): one sequence of 262144 tokens 95 us, 537 MB
+// at 5.6 TB/s, 83% of the copy rate; 64 sequences of 128 to 32768 tokens 139 us, 795 MB at 5.7
+// TB/s, 84% (query rows as the products' rows, 16 with 12 of them empty: 97 and 153 us); 16 x 2
+// queries of 1000 listed keys 25 us; 2048 listed keys for 64 heads of one KV head 15 us, which is
+// latency.  What is left of long streams: the first data come after 5 us, since all SMs ask at
+// once, and of an SM's three CTAs the last gets the least of its issue slots and ends up to 10%
+// after the first, alone and too few to fill memory.
 #include "kv_internal.cuh"
 
 namespace ltk {
