@@ -183,6 +183,7 @@ template <int D>
 __global__ void __launch_bounds__(128) kv_append_few_kernel(const AppendParams p, long long kv_blocks) {
   constexpr int LPR = D / 8, RPP = 32 / LPR;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  begin_after_previous();
   if (blockIdx.x >= kv_blocks) {
     rotate_queries<D, kQPassesFew>(p, (blockIdx.x - kv_blocks) * 4 + warp);
     return;
@@ -302,6 +303,7 @@ template <int D>
 __global__ void __launch_bounds__(256, 3) kv_append_kernel(const AppendParams p, long long kv_blocks) {
   constexpr int LPR = D / 8, RPP = 32 / LPR, PASSES = 16 / RPP;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  begin_after_previous();
   if (blockIdx.x >= kv_blocks) {
     rotate_queries<D, kQPassesMany>(p, (blockIdx.x - kv_blocks) * warps + warp);
     return;
@@ -481,15 +483,16 @@ cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t st
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   if (blocks == 0) return cudaSuccess;
   const unsigned grid = static_cast<unsigned>(blocks);
+  cudaError_t e;
   if (p.dim == 128) {
-    if (few) kv_append_few_kernel<128><<<grid, 128, 0, stream>>>(p, kv_blocks);
-    else kv_append_kernel<128><<<grid, warps * 32, 0, stream>>>(p, kv_blocks);
+    e = few ? launch_overlapped(kv_append_few_kernel<128>, grid, 128, 0, stream, p, kv_blocks)
+            : launch_overlapped(kv_append_kernel<128>, grid, warps * 32, 0, stream, p, kv_blocks);
   } else {
-    if (few) kv_append_few_kernel<64><<<grid, 128, 0, stream>>>(p, kv_blocks);
-    else kv_append_kernel<64><<<grid, warps * 32, 0, stream>>>(p, kv_blocks);
+    e = few ? launch_overlapped(kv_append_few_kernel<64>, grid, 128, 0, stream, p, kv_blocks)
+            : launch_overlapped(kv_append_kernel<64>, grid, warps * 32, 0, stream, p, kv_blocks);
   }
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace ltk

@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
     __syncwarp();
     tmem_alloc(smem_u32(&ctrl->tmem), 512);
   }
+  begin_after_previous();
   const long long units = static_cast<long long>(a.batch.N) * c.heads;
   const int waves = static_cast<int>(units / gridDim.x);
   const long long whole = static_cast<long long>(waves) * gridDim.x, total = (units - whole) * p.tiles;
@@ -839,12 +840,9 @@ cudaError_t launch_kv_list(const AttnParams& a, int num_sms, cudaStream_t stream
   ListParams p;
   p.a = a;
   p.tiles = (a.k + kKeys - 1) / kKeys;
-  if (a.dim == 128)
-    kv_list_kernel<128><<<num_sms, kThreads, Shape<128>::kBytes, stream>>>(p);
-  else
-    kv_list_kernel<64><<<num_sms, kThreads, Shape<64>::kBytes, stream>>>(p);
   count_launches(1);
-  return cudaGetLastError();
+  return a.dim == 128 ? launch_overlapped(kv_list_kernel<128>, num_sms, kThreads, Shape<128>::kBytes, stream, p)
+                      : launch_overlapped(kv_list_kernel<64>, num_sms, kThreads, Shape<64>::kBytes, stream, p);
 }
 
 }  // namespace ltk

@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, cq = lane & 3;
 
+  begin_after_previous();
   // --- this CTA's piece of the line -------------------------------------------------------
   long long total;
   int n_cta = grid;                      // CTAs with work: every one has a tile at least
@@ -765,9 +766,9 @@ cudaError_t init_rows() {
 }
 
 template <int D, bool SEL>
-void launch_rows(const AttnParams& p, bool narrow, int grid, cudaStream_t stream) {
-  if (narrow) kv_rows_kernel<D, SEL, 1><<<grid, kThreads, RowsSmem<D, 1>::kBytes, stream>>>(p, grid);
-  else kv_rows_kernel<D, SEL, 2><<<grid, kThreads, RowsSmem<D, 2>::kBytes, stream>>>(p, grid);
+cudaError_t launch_rows(const AttnParams& p, bool narrow, int grid, cudaStream_t stream) {
+  return narrow ? launch_overlapped(kv_rows_kernel<D, SEL, 1>, grid, kThreads, RowsSmem<D, 1>::kBytes, stream, p, grid)
+                : launch_overlapped(kv_rows_kernel<D, SEL, 2>, grid, kThreads, RowsSmem<D, 2>::kBytes, stream, p, grid);
 }
 
 }  // namespace
@@ -788,15 +789,9 @@ cudaError_t launch_kv_rows(const AttnParams& p, int max_q, int num_sms, cudaStre
   const bool sel = p.idx != nullptr;
   const int grid = kCtasPerSm * num_sms;
   const bool narrow = static_cast<long long>(p.group) * (sel ? 1 : max_q) <= 8;
-  if (p.dim == 128) {
-    if (sel) launch_rows<128, true>(p, narrow, grid, stream);
-    else launch_rows<128, false>(p, narrow, grid, stream);
-  } else {
-    if (sel) launch_rows<64, true>(p, narrow, grid, stream);
-    else launch_rows<64, false>(p, narrow, grid, stream);
-  }
   count_launches(1);
-  return cudaGetLastError();
+  if (p.dim == 128) return sel ? launch_rows<128, true>(p, narrow, grid, stream) : launch_rows<128, false>(p, narrow, grid, stream);
+  return sel ? launch_rows<64, true>(p, narrow, grid, stream) : launch_rows<64, false>(p, narrow, grid, stream);
 }
 
 }  // namespace ltk

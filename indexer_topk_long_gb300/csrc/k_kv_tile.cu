@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
     tmem_alloc(smem_u32(&ctrl->tmem), 512);
   }
 
+  begin_after_previous();
+
   // --- this CTA's piece of the line (head, row tile, key tile), every CTA one tile at least ---
   long long total;
   int n_cta = gridDim.x;
@@ -1195,16 +1197,12 @@ cudaError_t init_tile() {
 
 template <int D, bool SEL>
 cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
-  if constexpr (!SEL) {
-    if (p.rows <= 64) {
-      kv_tile_kernel<D, SEL, true><<<num_sms, Roles<D, true>::kThreads, TileShape<D>::kBytes, stream>>>(p);
-      count_launches(1);
-      return cudaGetLastError();
-    }
-  }
-  kv_tile_kernel<D, SEL, false><<<num_sms, Roles<D, false>::kThreads, TileShape<D>::kBytes, stream>>>(p);
   count_launches(1);
-  return cudaGetLastError();
+  if constexpr (!SEL) {
+    if (p.rows <= 64)
+      return launch_overlapped(kv_tile_kernel<D, SEL, true>, num_sms, Roles<D, true>::kThreads, TileShape<D>::kBytes, stream, p);
+  }
+  return launch_overlapped(kv_tile_kernel<D, SEL, false>, num_sms, Roles<D, false>::kThreads, TileShape<D>::kBytes, stream, p);
 }
 
 }  // namespace

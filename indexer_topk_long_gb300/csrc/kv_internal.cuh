@@ -108,6 +108,29 @@ __device__ __forceinline__ uint32_t kv_pack16(float lo, float hi, bool bf16) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// A kernel's start overlaps the end of the one before it on the stream: begin_after_previous
+// waits until that one is done and its writes can be seen, so a kernel calls it, in every
+// thread, before it touches global memory; the next kernel may then start in its turn, as
+// soon as every CTA of this one has, and wait at its own.
+__device__ __forceinline__ void begin_after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class... Params, class... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), unsigned grid, int threads, int smem, cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 struct AppendParams {
   KvCache cache;
   KvBatch batch;
