@@ -1218,23 +1218,28 @@ cudaError_t kv_tile_init() {
   return cudaSuccess;
 }
 
+// Pairs where a sequence has more rows than a tile and there is work for all SMs.  A pair takes
+// as long for a key tile as a single one, but there are half as many units to spread, their
+// queries have one buffer, and so each costs more to begin and end.  Two KV heads of 8 query
+// heads, D = 128, in us: 16 x 256 queries of 1100 keys (15 pairs' tiles an SM) 82 in pairs and 104
+// in single tiles, 1 x 1024 of 4096 (13.5) 66 and 61, 4 x 256 of 1100 (3.8) 50 and 43, 1 x 64 of
+// 16384 (3.4) 111 and 66.
+bool kv_tile_pairs(const AttnParams& a, int max_q, int num_sms) {
+  double keys = static_cast<double>(a.batch.width) * a.cache.page;
+  if (a.window > 0) keys = fmin(keys, static_cast<double>(a.window) + a.sinks + max_q);
+  const double pairs = a.cache.heads * (static_cast<double>(a.batch.N) * a.group / (2 * kTileRows) + 0.5 * a.batch.B);
+  return static_cast<long long>(a.group) * max_q > kTileRows && pairs * (keys / kKeys) >= 14.0 * num_sms;
+}
+
 cudaError_t launch_kv_tile(const AttnParams& a, int max_q, int num_sms, cudaStream_t stream) {
   TileParams p{};
   p.a = a;
   p.group_magic = static_cast<uint32_t>((0x100000000ull + a.group - 1) / a.group);
   const bool sel = a.idx != nullptr;
-  // Rows that one KV head's keys meet at a time: pairs of 128-row tiles where a sequence has
-  // that many and there is work for all SMs, one tile, or a narrow one (max_q is a hint: more
-  // rows make more units).  A pair takes as long for a key tile as a single one, but there are
-  // half as many units to spread, their queries have one buffer, and so each costs more to
-  // begin and end.  Two KV heads of 8 query heads, D = 128, in us: 16 x 256 queries of 1100
-  // keys (15 pairs' tiles an SM) 82 in pairs and 104 in single tiles, 1 x 1024 of 4096 (13.5) 66
-  // and 61, 4 x 256 of 1100 (3.8) 50 and 43, 1 x 64 of 16384 (3.4) 111 and 66.
+  // Rows that one KV head's keys meet at a time: a pair of tiles, one tile, or a narrow one
+  // (max_q is a hint: more rows make more units).
   const long long most = static_cast<long long>(a.group) * (sel ? 1 : max_q);
-  double keys = static_cast<double>(a.batch.width) * a.cache.page;
-  if (a.window > 0) keys = fmin(keys, static_cast<double>(a.window) + a.sinks + max_q);
-  const double pairs = a.cache.heads * (static_cast<double>(a.batch.N) * a.group / (2 * kTileRows) + 0.5 * a.batch.B);
-  p.pair = !sel && most > kTileRows && pairs * (keys / kKeys) >= 14.0 * num_sms;
+  p.pair = !sel && kv_tile_pairs(a, max_q, num_sms);
   p.rows = p.pair ? 2 * kTileRows : most <= 64 && !sel ? 64 : kTileRows;
   if (sel) {
     p.row_tiles = (a.group + p.rows - 1) / p.rows;

@@ -54,38 +54,46 @@ bool rows_ok(const void* p, long long stride, int heads, int dim) {
 }
 
 // Which kernel.  The one for few rows goes over a head's keys once for every 16 rows; the tile
-// kernels once for 64 (narrow, listed), 128 or 256, but take longer to start, meet and part.
-// Each side is a measured cost in microseconds of one SM, by tiles of 128 keys, against what the
-// tile kernels' start takes on all of them.
-//
-// Dense: 0.85 a tile for 16 rows against 1.62 for a narrow tile, 1.8 for a whole one or a pair,
-// and 15 to start.  For instance (D = 128): 16 rows, 8 KV heads 376 us by the first and 726 by
-// the second; 112 rows, 16 sequences of 1024 tokens 25 and 37; chunks of 2048 queries 10 times
-// the second's.  How long sequences are is only known on the device: a third of the page table
-// is assumed.
-//
-// Listed, up to 64 rows: a unit (query, KV head) of T tiles takes 2.0 + 0.75 T for every 16
-// rows (D = 64: 1.4 + 0.51 T) against 5.0 + 0.96 T (4.5 + 0.94 T), and 7 to start.  For instance
-// (D = 128, k = 2048, one KV head): 64 rows, 32 queries 27 us by the first and 29 by the second,
-// 128 queries 62 and 37, 4096 queries 1497 and 549; 32 rows, 64 queries 27 and 29, 4096 queries
-// 755 and 511; 16 rows, 8 KV heads, 1024 queries 799 and 1018.
+// kernels once for 64 (narrow, listed), 128 or 256 (pairs), but each of their units, and the
+// kernel as a whole, takes longer to begin and end.  Both are estimated in microseconds of one
+// SM, T tiles of 128 keys a unit, and shared out over the SMs:
+//   few rows    2.0 + 0.75 T for 16 rows (D = 64: 1.4 + 0.51 T)
+//   listed      5.0 + 0.96 T (4.5 + 0.94 T), and 7 for the kernel
+//   dense       3.0 + 1.8 T for 64 or 128 rows, 8 + 1.8 T for a pair (D = 64: 1.4 T), and 12
+//               for the kernel
+// For instance (D = 128), by few rows and by tiles: listed, k = 2048, one KV head of 64 rows, 32
+// queries 26 and 27 us, 128 queries 57 and 35, 4096 queries 1398 and 542; of 32 rows, 64 queries
+// 26 and 27, 4096 queries 706 and 514; dense, a window of 1024 over 24 ragged chunks (D = 64) 72
+// and 41, chunks of 2048 queries ten times as long by few rows.
+// How long sequences are is only known on the device: 0.6 of the page table is assumed.  Over
+// 130 dense batches (1 to 128 sequences, even and ragged, 98 to 32768 tokens) what this takes
+// is 2% more on average than the better of the two.
 bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
   const double rows = static_cast<double>(p.group) * (p.idx != nullptr ? 1 : max_q);
   if (rows <= kRowsPerUnit) return true;
-  const double sixteens = std::ceil(rows / 16.0);
-  if (p.idx != nullptr) {
-    const double units = static_cast<double>(p.cache.heads) * p.batch.N, tiles = std::ceil(p.k / 128.0);
-    if (p.group <= kListRows) {
-      const double by_rows = sixteens * (p.dim == 128 ? 2.0 + 0.75 * tiles : 1.4 + 0.51 * tiles);
-      const double by_list = p.dim == 128 ? 5.0 + 0.96 * tiles : 4.5 + 0.94 * tiles;
-      return units * (by_rows - by_list) <= 7.0 * num_sms;
-    }
-    return units * tiles * (0.85 * sixteens - 1.8 * std::ceil(rows / 256.0)) <= 15.0 * num_sms;
+  double keys = p.k;
+  if (p.idx == nullptr) {
+    keys = static_cast<double>(p.batch.width) * p.cache.page * 0.6;
+    if (p.window > 0) keys = std::min(keys, static_cast<double>(p.window) + p.sinks + max_q);
   }
-  double keys = static_cast<double>(p.batch.width) * p.cache.page / 3.0;
-  if (p.window > 0) keys = std::min(keys, static_cast<double>(p.window) + p.sinks + max_q);
-  const double by_tiles = rows <= 64 ? 1.62 : 1.8 * std::ceil(rows / 256.0);
-  return static_cast<double>(p.cache.heads) * p.batch.B * std::ceil(keys / 128.0) * (0.85 * sixteens - by_tiles) <= 15.0 * num_sms;
+  const double T = std::ceil(keys / 128.0);
+  // units of r rows: every query its own (listed), or every sequence's queries, at least one
+  auto units = [&](double r) {
+    if (p.idx != nullptr) return p.batch.N * std::ceil(p.group / r);
+    return std::max<double>(p.batch.B, static_cast<double>(p.batch.N) * p.group / r + 0.5 * p.batch.B);
+  };
+  const bool wide = p.dim == 128;
+  const double by_rows = units(16) * (wide ? 2.0 + 0.75 * T : 1.4 + 0.51 * T);
+  double by_tiles, start;
+  if (p.idx != nullptr && p.group <= kListRows) {
+    by_tiles = units(64) * (wide ? 5.0 + 0.96 * T : 4.5 + 0.94 * T);
+    start = 7.0;
+  } else {
+    const bool pair = p.idx == nullptr && kv_tile_pairs(p, max_q, num_sms);
+    by_tiles = units(pair ? 256 : rows <= 64 ? 64 : 128) * ((pair ? 8.0 : 3.0) + (wide ? 1.8 : 1.4) * T);
+    start = 12.0;
+  }
+  return p.cache.heads * (by_rows - by_tiles) <= start * num_sms;
 }
 
 KvBatch batch_of(const ltk_kv_batch* b) {

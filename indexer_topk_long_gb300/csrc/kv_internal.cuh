@@ -184,6 +184,7 @@ cudaError_t launch_kv_rows(const AttnParams& p, int max_q, int num_sms, cudaStre
 size_t kv_tile_part_floats(int num_sms);
 int kv_tile_counters(int num_sms);
 cudaError_t kv_tile_init();
+bool kv_tile_pairs(const AttnParams& p, int max_q, int num_sms);   // whether its units are pairs of row tiles
 cudaError_t launch_kv_tile(const AttnParams& p, int max_q, int num_sms, cudaStream_t stream);
 
 // Attention over listed keys for up to kListRows rows per KV head, on the tensor cores
