@@ -26,8 +26,8 @@
 // Measured (8 KV heads of 4 query heads, D = 128): one sequence of 262144 tokens 95 us, 537 MB
 // at 5.6 TB/s, 83% of the copy rate; 64 sequences of 128 to 32768 tokens 139 us, 795 MB at 5.7
 // TB/s, 84% (query rows as the products' rows, 16 with 12 of them empty: 97 and 153 us); 16 x 2
-// queries of 1000 listed keys 25 us; 2048 listed keys for 64 heads of one KV head 15 us, which is
-// latency.  What is left of long streams: the first data come after 5 us, since all SMs ask at
+// queries of 1000 listed keys 23 us; 2048 listed keys for 64 heads of one KV head 14 us and 777
+// tokens 8 us, which is latency.  What is left of long streams: the first data come after 5 us, since all SMs ask at
 // once, and of an SM's three CTAs the last gets the least of its issue slots and ends up to 10%
 // after the first, alone and too few to fill memory.
 #include "kv_internal.cuh"

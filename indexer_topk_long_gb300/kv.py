@@ -93,10 +93,10 @@ def _batch(page_table, seq_lens, cu_q, n: int, device, int32):
     """check_batch's checks, and the batch packed; (how many sequences, packed)."""
     shape = page_table.shape
     if (len(shape) == 2 and page_table.dtype is int32 and seq_lens.dtype is int32 and cu_q.dtype is int32
-            and seq_lens.shape == shape[:1] and cu_q.shape == (shape[0] + 1,)
+            and seq_lens.shape == ((b := shape[0]),) and cu_q.shape == (b + 1,)
             and page_table.is_contiguous() and seq_lens.is_contiguous() and cu_q.is_contiguous()
             and page_table.device == device and seq_lens.device == device and cu_q.device == device):
-        return shape[0], _PACK(page_table.data_ptr(), shape[1], seq_lens.data_ptr(), cu_q.data_ptr(), shape[0], n)
+        return b, _PACK(page_table.data_ptr(), shape[1], seq_lens.data_ptr(), cu_q.data_ptr(), b, n)
     check_batch(page_table, seq_lens, cu_q, n, device)   # says what is wrong
     raise AssertionError("unreachable")
 
@@ -121,7 +121,10 @@ class PagedKVCache:
         self.device = torch.device("cuda", torch.cuda.current_device())
         self._torch, self._index, self._raw_stream = torch, self.device.index, torch._C._cuda_getCurrentRawStream
         self._int32, self._float32 = torch.int32, torch.float32
+        self._default_scale = 1.0 / math.sqrt(self.dim)
         self._codes = {torch.bfloat16: LTK_BF16, torch.float16: LTK_F16}
+        self._append, self._attend = self.lib.ltk_kv_append, self.lib.ltk_kv_attention
+        self._attend_selected = self.lib.ltk_kv_attention_selected
         codes, scales = (self.num_pages, self.heads, self.page, self.dim), (self.num_pages, self.heads)
         if not all(given):
             k_codes, v_codes = (torch.zeros(codes, dtype=torch.uint8, device=self.device) for _ in range(2))
@@ -160,6 +163,17 @@ class PagedKVCache:
                     t.record_stream(stream)
         return stream.cuda_stream
 
+    def _queries(self, q, n: int, kind=None) -> tuple[int, int]:
+        """_rows' checks of q (elements of ``kind``, or any the library takes); the usual case
+        in one look, since a decode step is bound by what the host does."""
+        shape = q.shape
+        if len(shape) == 3 and shape[0] == n and shape[2] == self.dim and (
+                q.dtype in self._codes if kind is None else q.dtype is kind) and q.device == self.device:
+            s0, s1, s2 = q.stride()
+            if (s1 == self.dim and s2 == 1 and s0 >= shape[1] * s1 and s0 & 7 == 0 and q.data_ptr() & 15 == 0):
+                return shape[1], s0
+        return _rows(q, "q", n, self.dim, self.device, kind)
+
     def _new(self, stream, shape, dtype):
         """An output that belongs to the stream the call runs on."""
         if stream is None:
@@ -168,7 +182,10 @@ class PagedKVCache:
             return self._torch.empty(shape, dtype=dtype, device=self.device)
 
     def _outputs(self, stream, q, n, heads, out, lse):
-        f32 = self._torch.float32
+        f32 = self._float32
+        if out is None and lse is None and stream is None:
+            empty, device = self._torch.empty, self.device
+            return empty((n, heads, self.dim), dtype=q.dtype, device=device), empty((n, heads), dtype=f32, device=device)
         shape = (n, heads, self.dim)
         if out is None:
             out = self._new(stream, shape, q.dtype)
@@ -180,48 +197,60 @@ class PagedKVCache:
             _fail("lse", f"expected a contiguous float32 tensor of shape {(n, heads)} on {q.device}")
         return out, lse
 
-    def _scale(self, scale) -> float:
-        return 1.0 / math.sqrt(self.dim) if scale is None else float(scale)
-
     # -- API -------------------------------------------------------------------
     def append(self, k, v, page_table, seq_lens, cu_q, cos=None, sin=None, interleaved: bool = False, q=None,
                q_out=None, stream=None):
         """Stores the new tokens' k, v [N, heads, dim]; keys and q are rotated by the rows
         of cos, sin [positions, rot / 2] when given.  Returns the rotated q (None without q)."""
-        n = k.shape[0]
-        B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, self._int32)
-        kh, ks = _rows(k, "k", n, self.dim, self.device)
-        vh, vs = _rows(v, "v", n, self.dim, self.device, k.dtype)
-        if kh != self.heads or vh != self.heads:
-            _fail("k" if kh != self.heads else "v", f"expected {self.heads} heads")
+        dim, device = self.dim, self.device
+        shape, kind = k.shape, k.dtype
+        n = shape[0]
+        B, batch = _batch(page_table, seq_lens, cu_q, n, device, self._int32)
+        kp, vp = k.data_ptr(), v.data_ptr()
+        if (kind in self._codes and shape == (n, self.heads, dim) and v.shape == shape and v.dtype is kind
+                and k.device == device and v.device == device and (kp | vp) & 15 == 0
+                and k.stride()[1:] == (dim, 1) and v.stride()[1:] == (dim, 1)
+                and (ks := k.stride(0)) & 7 == 0 and (vs := v.stride(0)) & 7 == 0 and ks >= self.heads * dim <= vs):
+            pass                               # the usual case in one look; else what is wrong
+        else:
+            kh, ks = _rows(k, "k", n, dim, device)
+            vh, vs = _rows(v, "v", n, dim, device, kind)
+            if kh != self.heads or vh != self.heads:
+                _fail("k" if kh != self.heads else "v", f"expected {self.heads} heads")
         rot = rows = 0
         if (cos is None) != (sin is None):
             raise ValueError("cos, sin: give both or neither")
         if cos is not None:
-            table = cos.shape
-            if len(table) != 2 or sin.shape != table or cos.dtype is not self._float32 or sin.dtype is not self._float32 \
+            table, f32 = cos.shape, self._float32
+            if len(table) != 2 or sin.shape != table or cos.dtype is not f32 or sin.dtype is not f32 \
                     or not (cos.is_contiguous() and sin.is_contiguous()):
                 raise ValueError("cos, sin: expected contiguous float32 tables of equal shape [positions, rot / 2]")
-            _device_ok(cos, "cos", self.device)
-            _device_ok(sin, "sin", self.device)
+            if cos.device != device or sin.device != device:
+                _device_ok(cos, "cos", device)
+                _device_ok(sin, "sin", device)
             rows, rot = table[0], 2 * table[1]
         qh = qs = 0
         if q is not None:
-            qh, qs = _rows(q, "q", n, self.dim, self.device, k.dtype)
+            qh, qs = self._queries(q, n, kind)
         if q_out is not None:
             if q is None:
                 raise ValueError("q_out: given without q")
             if tuple(q_out.shape) != (n, qh, self.dim) or q_out.dtype != q.dtype or not q_out.is_contiguous() \
                     or q_out.device != q.device:
                 _fail("q_out", f"expected a contiguous {q.dtype} tensor of shape {(n, qh, self.dim)}")
-        st = self._begin(stream, k, v, page_table, seq_lens, cu_q, cos, sin, q, q_out)
+        if stream is None and self.h is not None:
+            st = self._raw_stream(self._index)
+        else:
+            st = self._begin(stream, k, v, page_table, seq_lens, cu_q, cos, sin, q, q_out)
         if q is not None and q_out is None:
-            q_out = self._new(stream, (n, qh, self.dim), q.dtype)
-        ltk._check(self.lib.ltk_kv_append(
-            self.h, batch, self._codes[k.dtype], k.data_ptr(), ks, v.data_ptr(), vs,
+            q_out = self._new(stream, (n, qh, dim), kind)
+        failed = self._append(
+            self.h, batch, self._codes[kind], kp, ks, vp, vs,
             None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(), rows, rot,
             1 if interleaved else 0, None if q is None else q.data_ptr(), qs, qh,
-            None if q_out is None else q_out.data_ptr(), st), "ltk_kv_append")
+            None if q_out is None else q_out.data_ptr(), st)
+        if failed:
+            ltk._check(failed, "ltk_kv_append")
         return q_out
 
     def attention(self, q, page_table, seq_lens, cu_q, max_q: int | None = None, scale: float | None = None,
@@ -231,14 +260,19 @@ class PagedKVCache:
         queries of one sequence) only helps choose a kernel.  Returns (out, lse)."""
         n = q.shape[0]
         B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, self._int32)
-        heads, qs = _rows(q, "q", n, self.dim, self.device)
+        heads, qs = self._queries(q, n)
         if max_q is None:
             max_q = -(-n // max(B, 1))
-        st = self._begin(stream, q, page_table, seq_lens, cu_q, out, lse)
+        if stream is None and self.h is not None:
+            st = self._raw_stream(self._index)
+        else:
+            st = self._begin(stream, q, page_table, seq_lens, cu_q, out, lse)
         out, lse = self._outputs(stream, q, n, heads, out, lse)
-        ltk._check(self.lib.ltk_kv_attention(
-            self.h, batch, self._codes[q.dtype], q.data_ptr(), qs, heads, max_q, self._scale(scale),
-            window, sinks, out.data_ptr(), lse.data_ptr(), st), "ltk_kv_attention")
+        failed = self._attend(
+            self.h, batch, self._codes[q.dtype], q.data_ptr(), qs, heads, max_q,
+            self._default_scale if scale is None else float(scale), window, sinks, out.data_ptr(), lse.data_ptr(), st)
+        if failed:
+            ltk._check(failed, "ltk_kv_attention")
         return out, lse
 
     def attention_selected(self, q, idx, page_table, seq_lens, cu_q, scale: float | None = None, out=None,
@@ -247,15 +281,22 @@ class PagedKVCache:
         slot), e.g. the indices IndexerTopK returns.  Returns (out, lse)."""
         n = q.shape[0]
         B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, self._int32)
-        heads, qs = _rows(q, "q", n, self.dim, self.device)
-        if idx.dim() != 2:
-            _fail("idx", f"expected a 2-D [queries, k] tensor, got shape {tuple(idx.shape)}")
-        _ints(idx, "idx", (n, idx.shape[1]), self.device)
-        st = self._begin(stream, q, idx, page_table, seq_lens, cu_q, out, lse)
+        heads, qs = self._queries(q, n)
+        listed = idx.shape
+        if len(listed) != 2:
+            _fail("idx", f"expected a 2-D [queries, k] tensor, got shape {tuple(listed)}")
+        if listed[0] != n or idx.dtype is not self._int32 or not idx.is_contiguous() or idx.device != self.device:
+            _ints(idx, "idx", (n, listed[1]), self.device)
+        if stream is None and self.h is not None:
+            st = self._raw_stream(self._index)
+        else:
+            st = self._begin(stream, q, idx, page_table, seq_lens, cu_q, out, lse)
         out, lse = self._outputs(stream, q, n, heads, out, lse)
-        ltk._check(self.lib.ltk_kv_attention_selected(
-            self.h, batch, self._codes[q.dtype], q.data_ptr(), qs, heads, idx.data_ptr(), idx.shape[1],
-            self._scale(scale), out.data_ptr(), lse.data_ptr(), st), "ltk_kv_attention_selected")
+        failed = self._attend_selected(
+            self.h, batch, self._codes[q.dtype], q.data_ptr(), qs, heads, idx.data_ptr(), listed[1],
+            self._default_scale if scale is None else float(scale), out.data_ptr(), lse.data_ptr(), st)
+        if failed:
+            ltk._check(failed, "ltk_kv_attention_selected")
         return out, lse
 
     def status(self, stream=None) -> int:
