@@ -675,21 +675,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
               }
             }
             __half2 top = __float2half2_rn(0.f);
+            uint32_t h[kHalf / 2];       // stored at the end: a store would hold back the loads of maxima after it
 #pragma unroll
-            for (int g = 0; g < kHalf / 8; ++g) {
-              uint32_t h[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = 8 * g + 2 * e;
-                const float4 m = *reinterpret_cast<const float4*>(&minus_max[r & ~3]);
-                const float2 z = unpack2(fma2(pack2(s[r], s[r + 1]), ks2, add2(lv2, r & 2 ? pack2(m.z, m.w) : pack2(m.x, m.y))));
-                const float w0 = exp2_approx(z.x), w1 = exp2_approx(z.y);
-                w2[r >> 1] = pack2(w0, w1);
-                h[e] = pack_f16(w0, w1);
-                top = __hmax2(top, *reinterpret_cast<const __half2*>(&h[e]));
-              }
-              sts128(p_at + (((x * (kHalf / 8) + g) ^ (t & 7)) << 4), h[0], h[1], h[2], h[3]);
+            for (int r = 0; r < kHalf; r += 2) {
+              const float4 m = *reinterpret_cast<const float4*>(&minus_max[r & ~3]);
+              const float2 z = unpack2(fma2(pack2(s[r], s[r + 1]), ks2, add2(lv2, r & 2 ? pack2(m.z, m.w) : pack2(m.x, m.y))));
+              const float w0 = exp2_approx(z.x), w1 = exp2_approx(z.y);
+              w2[r >> 1] = pack2(w0, w1);
+              h[r >> 1] = pack_f16(w0, w1);
+              top = __hmax2(top, *reinterpret_cast<const __half2*>(&h[r >> 1]));
             }
+#pragma unroll
+            for (int g = 0; g < kHalf / 8; ++g)
+              sts128(p_at + (((x * (kHalf / 8) + g) ^ (t & 7)) << 4), h[4 * g], h[4 * g + 1], h[4 * g + 2], h[4 * g + 3]);
             fence_async_smem();
             tc_fence_before();
             // a weight past its range: once more with new maxima (they hold for this tile)
