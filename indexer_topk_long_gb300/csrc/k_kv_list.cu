@@ -688,8 +688,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
 #pragma unroll
             for (int g = 0; g < kHalf / 8; ++g)
               sts128(p_at + (((x * (kHalf / 8) + g) ^ (t & 7)) << 4), h[4 * g], h[4 * g + 1], h[4 * g + 2], h[4 * g + 3]);
-            fence_async_smem();
-            tc_fence_before();
             // a weight past its range: once more with new maxima (they hold for this tile)
             if (!fresh) break;
             const bool big = __half2float(__hmax(__low2half(top), __high2half(top))) > 32768.f;
@@ -697,6 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
             fresh = false;
           }
           if (!ok) break;
+          fence_async_smem();
+          tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive(&ctrl->pfull[n & 1]);
 #pragma unroll
