@@ -26,14 +26,15 @@
 // cut into equal pieces, a unit cut by a border being joined by the last of its CTAs.
 //
 // 8192 queries of 2048 keys each, 64 heads on one KV head, D = 128, in a cache of 1M tokens:
-// 1108 us, 0.50 PFLOP/s and 4.3 GB of code rows at 3.9 TB/s out of L2.  Bound by the softmax
-// warps: a tile takes them some 2000 cycles (scores from tensor memory, 32 rows' weights, the
+// 1075 us, 0.51 PFLOP/s and 4.3 GB of code rows at 4.0 TB/s out of L2.  Bound by the softmax
+// warps: a tile takes them some 1900 cycles (scores from tensor memory, 32 rows' weights, the
 // vote, P to shared memory) while the products need 640 and the conversions 1300; then a unit
 // costs as much as another two tiles to end and begin.  What was tried: 128 query rows a product,
 // half of them empty, with both codes converted through registers 1764 us; rows gathered by TMA,
 // four to an instruction, 2960 (an instruction took 60 cycles); 16 softmax warps of 16 rows 1318
 // against 1255 for 8 of 32; scores asked for a tile ahead 1193 against 1132; loops unrolled less,
-// so that the roles' code stays near the schedulers, 1630 -> 1300.
+// so that the roles' code stays near the schedulers, 1630 -> 1300; P stored after all weights are
+// made, its fence behind the vote, 1107 -> 1075.
 #include <cstddef>
 
 #include "kv_tensor.cuh"
