@@ -170,7 +170,7 @@ class PagedKVCache:
         if len(shape) == 3 and shape[0] == n and shape[2] == self.dim and (
                 q.dtype in self._codes if kind is None else q.dtype is kind) and q.device == self.device:
             s0, s1, s2 = q.stride()
-            if (s1 == self.dim and s2 == 1 and s0 >= shape[1] * s1 and s0 & 7 == 0 and q.data_ptr() & 15 == 0):
+            if s1 == self.dim and s2 == 1 and s0 >= shape[1] * s1 > 0 and s0 & 7 == 0 and q.data_ptr() & 15 == 0:
                 return shape[1], s0
         return _rows(q, "q", n, self.dim, self.device, kind)
 
