@@ -57,11 +57,11 @@ __device__ __forceinline__ void load_turn(Turn& t, const AppendParams& p, int po
   const int at = p.interleaved ? j * 4 : (j < h ? j : j - h) * 8;
   const float4* c = reinterpret_cast<const float4*>(p.cos + static_cast<size_t>(pos) * half + at);
   const float4* s = reinterpret_cast<const float4*>(p.sin + static_cast<size_t>(pos) * half + at);
-  const float4 c0 = __ldg(c), s0 = __ldg(s);
+  const float4 c0 = kv_load(c), s0 = kv_load(s);
   t.c[0] = c0.x; t.c[1] = c0.y; t.c[2] = c0.z; t.c[3] = c0.w;
   t.s[0] = s0.x; t.s[1] = s0.y; t.s[2] = s0.z; t.s[3] = s0.w;
   if (!p.interleaved) {
-    const float4 c1 = __ldg(c + 1), s1 = __ldg(s + 1);
+    const float4 c1 = kv_load(c + 1), s1 = kv_load(s + 1);
     t.c[4] = c1.x; t.c[5] = c1.y; t.c[6] = c1.z; t.c[7] = c1.w;
     t.s[4] = s1.x; t.s[5] = s1.y; t.s[6] = s1.z; t.s[7] = s1.w;
   }
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(128) kv_append_few_kernel(const AppendParams p
   const int r_lo = pos & (c.page - 1);
   if (r_lo != 0 && pos != s.pos0) return;
   const int p0 = pos - r_lo, r_hi = min(s.len - p0, c.page);
-  const int page = __ldg(p.batch.page_table + static_cast<size_t>(b) * p.batch.width + (pos >> c.page_log2));
+  const int page = kv_load(p.batch.page_table + static_cast<size_t>(b) * p.batch.width + (pos >> c.page_log2));
   if (page < 0 || page >= c.num_pages) {
     if (lane == 0) raise_status(p.status, kDevArg);
     return;
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(128) kv_append_few_kernel(const AppendParams p
     bool on = false, fine = true;
     if (live) {
       const size_t tok = static_cast<size_t>(s.q0 + (p0 + r - s.pos0));
-      kr = __ldg(reinterpret_cast<const uint4*>(k + tok * p.k_stride) + j);
-      vr = __ldg(reinterpret_cast<const uint4*>(v + tok * p.v_stride) + j);
+      kr = kv_load(reinterpret_cast<const uint4*>(k + tok * p.k_stride) + j);
+      vr = kv_load(reinterpret_cast<const uint4*>(v + tok * p.v_stride) + j);
       if (p.cos != nullptr) {
         fine = p0 + r < p.table_rows;
         if (!fine) raise_status(p.status, kDevArg);
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(const AppendParams p,
   int lo = 0, hi = p.batch.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((__ldg(p.batch.cu_q + mid) + static_cast<long long>(mid) * step) >> c.page_log2 <= slot) lo = mid;
+    if ((kv_load(p.batch.cu_q + mid) + static_cast<long long>(mid) * step) >> c.page_log2 <= slot) lo = mid;
     else hi = mid - 1;
   }
   const int b = lo;
@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(const AppendParams p,
     return;
   }
   const long long first_page = s.pos0 >> c.page_log2;
-  const long long at = first_page + slot - ((__ldg(p.batch.cu_q + b) + static_cast<long long>(b) * step) >> c.page_log2);
+  const long long at = first_page + slot - ((kv_load(p.batch.cu_q + b) + static_cast<long long>(b) * step) >> c.page_log2);
   if (at < first_page || at << c.page_log2 >= s.len) return;
-  const int page = __ldg(p.batch.page_table + static_cast<size_t>(b) * p.batch.width + at);
+  const int page = kv_load(p.batch.page_table + static_cast<size_t>(b) * p.batch.width + at);
   if (page < 0 || page >= c.num_pages) {
     if (threadIdx.x == 0) raise_status(p.status, kDevArg);
     return;
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(const AppendParams p,
     kr = vr = make_uint4(0, 0, 0, 0);
     if (r >= r_lo && r < r_hi) {
       const size_t n = static_cast<size_t>(s.q0 + (p0 + r - s.pos0));
-      kr = __ldg(reinterpret_cast<const uint4*>(k + n * p.k_stride) + j);
-      vr = __ldg(reinterpret_cast<const uint4*>(v + n * p.v_stride) + j);
+      kr = kv_load(reinterpret_cast<const uint4*>(k + n * p.k_stride) + j);
+      vr = kv_load(reinterpret_cast<const uint4*>(v + n * p.v_stride) + j);
     }
   };
   auto keys = [&](int i, const uint4& kr, bool& fine) {

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = ord * kKeys + 4 * lane + e;
-            key[e] = ord < end && i < a.k ? __ldg(list + i) : -1;
+            key[e] = ord < end && i < a.k ? kv_load(list + i) : -1;
           }
         };
         // a key past its query's position does not count
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (key[e] > u.pos) key[e] = -1;
-            page[e] = key[e] >= 0 ? __ldg(table + (key[e] >> c.page_log2)) : -1;
+            page[e] = key[e] >= 0 ? kv_load(table + (key[e] >> c.page_log2)) : -1;
           }
         };
         struct Rows {
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
               if (page[e] >= 0 && page[e] < c.num_pages) {
                 const uint32_t blk = static_cast<uint32_t>(page[e]) * c.heads + u.head;
                 r.row[e] = blk * c.page + (key[e] & (c.page - 1));
-                r.ks[e] = __ldg(c.k_scale + blk);
-                r.vs[e] = __ldg(c.v_scale + blk);
+                r.ks[e] = kv_load(c.k_scale + blk);
+                r.vs[e] = kv_load(c.v_scale + blk);
               } else {
                 raise_status(status, kDevArg);
                 r.ks[e] = __int_as_float(0x7FC00000);

@@ -311,14 +311,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     if (pc.left <= 0) return;
     if constexpr (SEL) {
       const int slot = pc.t * kTileKeys + warp * kWarpKeys + lane;
-      if (slot < p.k) feed.key = __ldg(p.idx + static_cast<size_t>(pc.w.q0) * p.k + slot);
+      if (slot < p.k) feed.key = kv_load(p.idx + static_cast<size_t>(pc.w.q0) * p.k + slot);
     } else {
       const int tile = pc.t < pc.w.skip ? pc.t : pc.t - pc.w.skip + pc.w.tile0;
       const int key0 = tile * kTileKeys + warp * kWarpKeys;
       const int* table = p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width;
 #pragma unroll
       for (int h = 0; h < kGroups; ++h)
-        if (key0 + 16 * h < pc.w.len) feed.page[h] = __ldg(table + ((key0 + 16 * h) >> p.cache.page_log2));
+        if (key0 + 16 * h < pc.w.len) feed.page[h] = kv_load(table + ((key0 + 16 * h) >> p.cache.page_log2));
     }
   };
   int stage_in = 0;
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
         const int key = feed.key <= pc.w.pos0 ? feed.key : -1;
         int page = -1;
         if (key >= 0) {
-          page = __ldg(p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (key >> p.cache.page_log2));
+          page = kv_load(p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (key >> p.cache.page_log2));
           if (page < 0 || page >= p.cache.num_pages) {
             raise_status(p.status, kDevArg);
             page = -2;
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
                               static_cast<size_t>(head.w.head * p.group + r % p.group) * D;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i)   // chunk cq of each 64 elements: 16 elements, 32 bytes
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (i >> 1) * 64 + cq * 16) + (i & 1));
+          raw[i] = kv_load(reinterpret_cast<const uint4*>(src + (i >> 1) * 64 + cq * 16) + (i & 1));
       }
       float amax = 0.f;
 #pragma unroll

@@ -112,7 +112,7 @@ struct TileParams {
 // Dense row tiles are numbered without a scan: sequence b's start at
 // cu_q[b] * group / rows + b, which leaves room for every row tile.
 __device__ __forceinline__ long long slot_start(const TileParams& p, int b) {
-  return static_cast<long long>(__ldg(p.a.batch.cu_q + b)) * p.a.group / p.rows + b;
+  return static_cast<long long>(kv_load(p.a.batch.cu_q + b)) * p.a.group / p.rows + b;
 }
 
 // Row tile `slot`: its fields, and the number of its key tiles (at least 1 on the
@@ -199,7 +199,7 @@ __device__ __forceinline__ float group_scale(float s) {
 // Codes pass the little L1 that the operands leave: page tables and indices stay in it.
 __device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       // Row tiles are numbered by cu_q, so it has to rise within [0, N]; else nothing is done.
       bool rises = true;
       for (int i = tid; i < a.batch.B; i += kThreads) {
-        const int at = __ldg(a.batch.cu_q + i), to = __ldg(a.batch.cu_q + i + 1);
+        const int at = kv_load(a.batch.cu_q + i), to = kv_load(a.batch.cu_q + i + 1);
         rises = rises && at >= 0 && at <= to && to <= a.batch.N;
       }
       const int each = (p.slots + kThreads - 1) / kThreads;
@@ -667,17 +667,17 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       };
       auto key_of = [&](int ord) {
         const int i = ord * kKeys + 32 * w + lane;
-        return ord < end && i < a.k ? __ldg(a.idx + static_cast<size_t>(u.q0) * a.k + i) : -1;
+        return ord < end && i < a.k ? kv_load(a.idx + static_cast<size_t>(u.q0) * a.k + i) : -1;
       };
       auto look = [&](int ord, int key) {
         Look k{-1, -1, -1};
         if constexpr (SEL) {
           k.key = key <= u.pos0 ? key : -1;
-          if (k.key >= 0) k.page = __ldg(table + (k.key >> c.page_log2));
+          if (k.key >= 0) k.page = kv_load(table + (k.key >> c.page_log2));
         } else if (ord < end) {
           const int first = tile_of(u, ord) * kKeys + 32 * w;
-          if (first < u.len) k.page = __ldg(table + (first >> c.page_log2));
-          if (first + 16 < u.len) k.page2 = __ldg(table + ((first + 16) >> c.page_log2));
+          if (first < u.len) k.page = kv_load(table + (first >> c.page_log2));
+          if (first + 16 < u.len) k.page2 = kv_load(table + ((first + 16) >> c.page_log2));
         }
         return k;
       };
@@ -697,8 +697,8 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
             if (k.page >= 0 && k.page < c.num_pages) {
               const uint32_t blk = static_cast<uint32_t>(k.page) * c.heads + u.head;
               t.row = blk * c.page + (k.key & (c.page - 1));
-              t.ks = __ldg(c.k_scale + blk);
-              t.vs = __ldg(c.v_scale + blk);
+              t.ks = kv_load(c.k_scale + blk);
+              t.vs = kv_load(c.v_scale + blk);
             } else {
               raise_status(status, kDevArg);
               t.ks = __int_as_float(0x7FC00000);
@@ -715,8 +715,8 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           const int h = lane & 1;
           t.ks = t.vs = 1.f;
           if (h ? known2 : known1) {
-            t.ks = __ldg(c.k_scale + (h ? b2 : b1));
-            t.vs = __ldg(c.v_scale + (h ? b2 : b1));
+            t.ks = kv_load(c.k_scale + (h ? b2 : b1));
+            t.vs = kv_load(c.v_scale + (h ? b2 : b1));
           } else if (key + 16 * h < u.len) {
             raise_status(status, kDevArg);
             t.ks = __int_as_float(0x7FC00000);

@@ -42,6 +42,12 @@ struct KvBatch {
   int N;
 };
 
+// A load that sees what the kernel before on the stream wrote.  Kernels here start while that one
+// still runs (see begin_after_previous), so nothing it writes is read-only for their lifetime, and
+// the non-coherent path (ld.global.nc, __ldg) may answer from lines that were read before the wait.
+template <class T>
+__device__ __forceinline__ T kv_load(const T* p) { return *p; }
+
 // Queries [q0, q0 + nq) of sequence b, its length and the position of its
 // first query.  Values outside the tables' bounds are clamped to them.
 struct KvSeq {
@@ -49,10 +55,10 @@ struct KvSeq {
 };
 __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int b) {
   KvSeq s;
-  s.q0 = min(max(__ldg(bt.cu_q + b), 0), bt.N);
-  s.nq = min(max(__ldg(bt.cu_q + b + 1), s.q0), bt.N) - s.q0;
+  s.q0 = min(max(kv_load(bt.cu_q + b), 0), bt.N);
+  s.nq = min(max(kv_load(bt.cu_q + b + 1), s.q0), bt.N) - s.q0;
   const long long room = static_cast<long long>(bt.width) << c.page_log2;
-  s.len = static_cast<int>(min(static_cast<long long>(max(__ldg(bt.seq_lens + b), 0)), room));
+  s.len = static_cast<int>(min(static_cast<long long>(max(kv_load(bt.seq_lens + b), 0)), room));
   s.pos0 = s.len - s.nq;                 // negative when a sequence is shorter than its queries
   return s;
 }
@@ -61,12 +67,12 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int
 // when every sequence has as many queries (a decode step: one look, no search).
 __device__ __forceinline__ int kv_seq_of_query(const KvBatch& bt, int n) {
   const int guess = static_cast<int>(static_cast<long long>(n) * bt.B / bt.N);
-  const int at = __ldg(bt.cu_q + guess), next = __ldg(bt.cu_q + guess + 1);
+  const int at = kv_load(bt.cu_q + guess), next = kv_load(bt.cu_q + guess + 1);
   if (at <= n && n < next) return guess;
   int lo = 0, hi = bt.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(bt.cu_q + mid) <= n) lo = mid; else hi = mid - 1;
+    if (kv_load(bt.cu_q + mid) <= n) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
