@@ -310,7 +310,8 @@ ltk_status ltk_litedsa_pack(const int* topk_idx, int T, int k, int group, int* u
  *
  * Cache of one layer (device memory, owned by the caller):
  *   k_codes, v_codes  e4m3 codes [num_pages, heads, page, dim];
- *   k_scale, v_scale  fp32 [num_pages, heads]; the value held is code * scale.
+ *   k_scale, v_scale  fp32 [num_pages, heads], 0 or positive; the value held is
+ *                     code * scale (a scale of 0: zeros).
  * page is 16, 32, 64 or 128 tokens, dim 64 or 128.
  *
  * A handle binds the four buffers and owns a workspace of a few tens of MiB on

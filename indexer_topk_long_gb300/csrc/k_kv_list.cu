@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
             v_row[e] = now.row[e];
             if (now.row[e] != kNoRow && !(now.vs[e] > 0.f)) {   // a block without a scale holds zeros
               v_row[e] = kNoRow;
-              now.vs[e] = 1.f;
+              now.vs[e] = kKvLeastScale;
             }
           }
 #pragma unroll

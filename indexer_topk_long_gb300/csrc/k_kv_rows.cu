@@ -507,13 +507,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       produce();
       cp_wait<kStages - 1>();
       __syncwarp();
-      const unsigned char* kp = ring + stage_out * S::kStageBytes;
-      const unsigned char* vp = kp + kWarpKeys * D;
-      const float* m = meta + stage_out * S::kMetaFloats;
+      unsigned char* kp = ring + stage_out * S::kStageBytes;
+      unsigned char* vp = kp + kWarpKeys * D;
+      float* m = meta + stage_out * S::kMetaFloats;
       stage_out = stage_out + 1 == kStages ? 0 : stage_out + 1;
       const int tile = SEL ? t : (t < head.w.skip ? t : t - head.w.skip + head.w.tile0);
       const int key0 = tile * kTileKeys + warp * kWarpKeys;
       if (!SEL && (key0 >= head.w.len || key0 > p_hi)) continue;
+      {
+        // a key of a block without a value scale: zeros, see kKvLeastScale
+        float* vs = SEL ? m + kWarpKeys + lane : m + 2 * (lane >> 4) + 1;
+        const bool zeros = (SEL || key0 + (lane & 16) < head.w.len) && !(*vs > 0.f);
+        if (__any_sync(0xFFFFFFFFu, zeros)) {
+          if (zeros) {
+            *vs = kKvLeastScale;
+#pragma unroll 1
+            for (int i = 0; i < CPR; ++i)
+              *reinterpret_cast<uint4*>(vp + (lane & 16) * D + place<D>(lane & 15, i)) = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+        }
+      }
 
       float s[RT][kGroups][4] = {};
 #pragma unroll

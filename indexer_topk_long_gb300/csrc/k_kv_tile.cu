@@ -193,7 +193,7 @@ __device__ __forceinline__ float group_scale(float s) {
   float m = fmaxf(s, 0.f);               // a NaN (page outside the pool) counts as 0
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return m > 0.f ? m : 1.f;
+  return m > 0.f ? m : kKvLeastScale;
 }
 
 // Codes pass the little L1 that the operands leave: page tables and indices stay in it.
@@ -779,6 +779,15 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           if (!values) {
             kg = top * (1.f / 64.f);
             vg = group_scale(cur.vs) * (1.f / 64.f);
+          }
+        }
+        if constexpr (!SEL) {            // groups whose values are zeros, see kKvLeastScale
+          const uint32_t zeros = __ballot_sync(0xFFFFFFFFu, !(vg > 0.f));
+          if (zeros != 0) {
+            if (!(vg > 0.f)) vg = kKvLeastScale;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+              if (values && (zeros >> (i < NI / 2 ? 0 : 1) & 1u) != 0) x[i] = make_uint4(0, 0, 0, 0);
           }
         }
         const float lv = __log2f(vg) + kBoost, iv = __frcp_rn(vg);

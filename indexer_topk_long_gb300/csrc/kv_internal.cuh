@@ -20,6 +20,10 @@ namespace ltk {
 // attention kernels, which fold log2(v_scale) into the exponent of a weight).
 constexpr int kKvMinExp = -40;
 constexpr int kKvMaxExp = 40;
+// A block whose value scale is 0 holds zeros.  Its keys count like any others: their weights are
+// made as if the scale were this one, the smallest that append writes, so that they push no other
+// weight out of its range, and meet zeros instead of the block's codes.
+constexpr float kKvLeastScale = 0x1p-40f;
 constexpr int kDevArg = 1;               // device status: an index outside its table
 
 struct KvCache {
