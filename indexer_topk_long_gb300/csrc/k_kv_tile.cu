@@ -467,10 +467,12 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
         if (!warp_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
         const Unit& u = ctrl->unit[us];
         if (u.n_tiles < 0) break;
+        // Pair mode: one buffer.  Also a unit without tiles waits for the one before it to be done
+        // with, or qraw could complete a second phase before a softmax warp has seen the first.
+        if (pair && un >= 1 && !warp_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
         if (u.n_tiles > 0) {
           const int w = warp - R::kRest - 2;
-          if (pair) {                    // one buffer; the softmax threads convert their rows
-            if (un >= 1 && !warp_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
+          if (pair) {                    // the softmax threads convert their rows
             copy_queries<D>(p, u, q_sm, 0, 127, w, lane);
             if (u.rows > kTileRows) copy_queries<D>(p, u, q_sm + S::kOperand, kTileRows, 127, w, lane);
           } else {                       // two buffers, converted here ahead of their use
