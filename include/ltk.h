@@ -343,9 +343,10 @@ typedef struct ltk_kv ltk_kv;
  *               sequence b's (0 of them is allowed), cu_q[B] = N.
  * New token i of sequence b has position seq_lens[b] - n_b + i, n_b its number
  * of new tokens.  Its position p is row p % page of page page_table[b, p / page].
- * A page number outside [0, num_pages), a negative position or one past a
- * rotation table sets the handle's device status to LTK_ERR_ARG: nothing is
- * written for such a page, and queries that see it get NaN.
+ * A page number outside [0, num_pages), a position past the page table's
+ * columns, a negative position or one past a rotation table sets the handle's
+ * device status to LTK_ERR_ARG: nothing is written for such a page, and queries
+ * that see it get NaN.
  */
 typedef struct {
   const int* page_table;

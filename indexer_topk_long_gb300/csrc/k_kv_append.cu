@@ -196,14 +196,14 @@ __global__ void __launch_bounds__(128) kv_append_few_kernel(const AppendParams p
   const KvSeq s = kv_seq(p.batch, c, b);
   const int pos = s.pos0 + n - s.q0;
   if (n < s.q0 || n >= s.q0 + s.nq) return;
-  if (s.pos0 < 0) {
+  if (s.pos0 < 0 || pos >= s.len) {
     if (lane == 0) raise_status(p.status, kDevArg);
     return;
   }
   const int r_lo = pos & (c.page - 1);
   if (r_lo != 0 && pos != s.pos0) return;
   const int p0 = pos - r_lo, r_hi = min(s.len - p0, c.page);
-  const int page = kv_load(p.batch.page_table + static_cast<size_t>(b) * p.batch.width + (pos >> c.page_log2));
+  const int page = kv_page(p.batch, c, b, pos);
   if (page < 0 || page >= c.num_pages) {
     if (lane == 0) raise_status(p.status, kDevArg);
     return;
@@ -321,9 +321,10 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(const AppendParams p,
   const int b = lo;
   const KvSeq s = kv_seq(p.batch, c, b);
   if (s.nq == 0) return;
-  if (s.pos0 < 0) {
+  const bool past = s.pos0 > s.len - s.nq;                    // its last tokens have no page
+  if (s.pos0 < 0 || past) {
     if (threadIdx.x == 0) raise_status(p.status, kDevArg);
-    return;
+    if (!past) return;
   }
   const long long first_page = s.pos0 >> c.page_log2;
   const long long at = first_page + slot - ((kv_load(p.batch.cu_q + b) + static_cast<long long>(b) * step) >> c.page_log2);

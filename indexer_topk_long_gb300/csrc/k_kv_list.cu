@@ -345,7 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
           break;
         }
         const int* list = a.idx + static_cast<size_t>(u.q) * a.k;
-        const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width;
         const int end = u.first + u.n_tiles;
         auto keys_of = [&](int ord, int (&key)[4]) {
 #pragma unroll
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (key[e] > u.pos) key[e] = -1;
-            page[e] = key[e] >= 0 ? kv_load(table + (key[e] >> c.page_log2)) : -1;
+            page[e] = key[e] >= 0 ? kv_page(a.batch, c, u.b, key[e]) : -1;
           }
         };
         struct Rows {

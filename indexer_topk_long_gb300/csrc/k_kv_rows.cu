@@ -148,7 +148,7 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, const KvSeq& s, int
   *skip = 0;
   *tile0 = 0;
   if (p.window <= 0) return n;
-  const int lo = max(s.pos0 - p.window + 1, 0) / kTileKeys;
+  const int lo = min(max(s.pos0 - p.window + 1, 0) / kTileKeys, n - 1);   // (queries past the table see none of them)
   const int sk = min((min(p.sinks, s.len) + kTileKeys - 1) / kTileKeys, lo);
   *skip = sk;
   *tile0 = lo;
@@ -166,7 +166,7 @@ __device__ __forceinline__ void enter_unit(const AttnParams& p, Cursor& c) {
     c.w.b = b;
     c.w.q0 = n;
     c.w.nq = 1;
-    c.w.pos0 = (n >= s.q0 && n < s.q0 + s.nq) ? min(s.pos0 + n - s.q0, s.len - 1) : -1;
+    c.w.pos0 = (n >= s.q0 && n < s.q0 + s.nq) ? s.pos0 + n - s.q0 : -1;
     c.w.len = p.k;
     c.w.head = r / rg;
     c.w.row0 = (r % rg) * 8 * RT;
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
         const int key = feed.key <= pc.w.pos0 ? feed.key : -1;
         int page = -1;
         if (key >= 0) {
-          page = kv_load(p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (key >> p.cache.page_log2));
+          page = kv_page(p.batch, p.cache, pc.w.b, key);
           if (page < 0 || page >= p.cache.num_pages) {
             raise_status(p.status, kDevArg);
             page = -2;
@@ -496,10 +496,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[x][i][j] = 0.f;
       M[x][0] = M[x][1] = kMinusHuge;
-      l[x][0] = l[x][1] = 0.f;
+      // a query past the page table sees a page that is not there: NaN
+#pragma unroll
+      for (int n = 0; n < 2; ++n) l[x][n] = !SEL && prow[x][n] >= head.w.len ? __int_as_float(0x7FC00000) : 0.f;
     }
     const int p_lo = SEL ? 0 : head.w.pos0 + head.w.row0 / p.group;
     const int p_hi = SEL ? 0 : head.w.pos0 + min(head.w.row0 + kRows - 1, rows_all - 1) / p.group;
+    if (!SEL && p_hi >= head.w.len && tid == 0) raise_status(p.status, kDevArg);
 
 #pragma unroll 1
     for (int t = t_begin; t < t_end; ++t) {

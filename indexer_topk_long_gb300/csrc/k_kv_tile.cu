@@ -159,10 +159,11 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
     u.p_hi = q.pos0 + (u.row0 + u.rows - 1) / a.group;
     u.len = q.len;
     u.skip = u.tile0 = 0;
-    tiles = u.p_hi >= 0 ? u.p_hi / kKeys + 1 : 0;
+    const int last = min(u.p_hi, u.len - 1);                  // (queries past the table: see kv_seq)
+    tiles = last >= 0 ? last / kKeys + 1 : 0;
     if (tiles > 0 && a.window > 0) {
-      u.tile0 = max(u.p_lo - a.window + 1, 0) / kKeys;
-      u.skip = min((min(a.sinks, u.p_hi + 1) + kKeys - 1) / kKeys, u.tile0);
+      u.tile0 = min(max(u.p_lo - a.window + 1, 0) / kKeys, tiles);
+      u.skip = min((min(a.sinks, last + 1) + kKeys - 1) / kKeys, u.tile0);
       tiles = u.skip + tiles - u.tile0;
     }
     return max(tiles, 1);
@@ -442,6 +443,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           }
           const int us = un & 1;
           if (un >= 2 && !lane_wait(smem_u32(&ctrl->uempty[us]), ((un >> 1) - 1) & 1, abort_flag, status)) break;
+          if (!SEL && u.n_tiles >= 0 && u.p_hi >= u.len && u.p_hi >= 0) raise_status(status, kDevArg);
           ctrl->unit[us] = u;
           mbar_arrive(smem_u32(&ctrl->ufull[us]));
           if (u.n_tiles < 0) break;
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
         Look k{-1, -1, -1};
         if constexpr (SEL) {
           k.key = key <= u.pos0 ? key : -1;
-          if (k.key >= 0) k.page = kv_load(table + (k.key >> c.page_log2));
+          if (k.key >= 0) k.page = kv_page(a.batch, c, u.b, k.key);
         } else if (ord < end) {
           const int first = tile_of(u, ord) * kKeys + 32 * w;
           if (first < u.len) k.page = kv_load(table + (first >> c.page_log2));
@@ -857,7 +859,8 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
         if (mine > 0) f = ctrl->rowf[us * 128 + r];
       }
       if (!live) f = 0.f;
-      float M = kMinusHuge, l = 0.f;
+      // a query past the page table sees a page that is not there: NaN
+      float M = kMinusHuge, l = !SEL && pos >= u.len ? __int_as_float(0x7FC00000) : 0.f;
       bool ok = true;
 #pragma unroll 1
       for (int i = 0; i < mine; ++i) {

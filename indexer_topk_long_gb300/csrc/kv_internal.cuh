@@ -52,8 +52,9 @@ struct KvBatch {
 template <class T>
 __device__ __forceinline__ T kv_load(const T* p) { return *p; }
 
-// Queries [q0, q0 + nq) of sequence b, its length and the position of its
-// first query.  Values outside the tables' bounds are clamped to them.
+// Queries [q0, q0 + nq) of sequence b, the position of its first query, and how many of its
+// tokens have a column in the page table.  cu_q is clamped to the batch.  A sequence that is
+// longer than its table has queries at positions len and beyond.
 struct KvSeq {
   int q0, nq, len, pos0;
 };
@@ -62,8 +63,9 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int
   s.q0 = min(max(kv_load(bt.cu_q + b), 0), bt.N);
   s.nq = min(max(kv_load(bt.cu_q + b + 1), s.q0), bt.N) - s.q0;
   const long long room = static_cast<long long>(bt.width) << c.page_log2;
-  s.len = static_cast<int>(min(static_cast<long long>(max(kv_load(bt.seq_lens + b), 0)), room));
-  s.pos0 = s.len - s.nq;                 // negative when a sequence is shorter than its queries
+  const int tokens = max(kv_load(bt.seq_lens + b), 0);
+  s.len = static_cast<int>(min(static_cast<long long>(tokens), room));
+  s.pos0 = tokens - s.nq;                // negative when a sequence is shorter than its queries
   return s;
 }
 
@@ -79,6 +81,12 @@ __device__ __forceinline__ int kv_seq_of_query(const KvBatch& bt, int n) {
     if (kv_load(bt.cu_q + mid) <= n) lo = mid; else hi = mid - 1;
   }
   return lo;
+}
+
+// Page of position pos of sequence b; -1, which is no page, past the table.
+__device__ __forceinline__ int kv_page(const KvBatch& bt, const KvCache& c, int b, int pos) {
+  const int at = pos >> c.page_log2;
+  return at < bt.width ? kv_load(bt.page_table + static_cast<size_t>(b) * bt.width + at) : -1;
 }
 
 // Codes (byte offset) of row `off` of (page, head).
