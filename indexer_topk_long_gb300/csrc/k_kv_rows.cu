@@ -148,7 +148,7 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, const KvSeq& s, int
   *skip = 0;
   *tile0 = 0;
   if (p.window <= 0) return n;
-  const int lo = min(max(s.pos0 - p.window + 1, 0) / kTileKeys, n - 1);   // (queries past the table see none of them)
+  const int lo = min(max(max(s.pos0, 0) - p.window + 1, 0) / kTileKeys, n - 1);   // (queries past the table see none of them)
   const int sk = min((min(p.sinks, s.len) + kTileKeys - 1) / kTileKeys, lo);
   *skip = sk;
   *tile0 = lo;
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
       const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       const float scale = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      const int pos = on ? (SEL ? head.w.pos0 : head.w.pos0 + qi) : -1;
+      const int pos = on ? (SEL ? head.w.pos0 : max(head.w.pos0 + qi, -1)) : -1;   // (from -1 any window is within 32 bits)
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         crow[x][n] = __shfl_sync(0xFFFFFFFFu, scale, (2 * cq + n) * 4);

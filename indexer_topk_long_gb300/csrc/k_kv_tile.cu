@@ -162,7 +162,7 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
     const int last = min(u.p_hi, u.len - 1);                  // (queries past the table: see kv_seq)
     tiles = last >= 0 ? last / kKeys + 1 : 0;
     if (tiles > 0 && a.window > 0) {
-      u.tile0 = min(max(u.p_lo - a.window + 1, 0) / kKeys, tiles);
+      u.tile0 = min(max(max(u.p_lo, 0) - a.window + 1, 0) / kKeys, tiles);
       u.skip = min((min(a.sinks, last + 1) + kKeys - 1) / kKeys, u.tile0);
       tiles = u.skip + tiles - u.tile0;
     }
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       const bool live = row < u.rows && (!twice || (r >> 6) == x);
       const bool warp_live = __any_sync(0xFFFFFFFFu, live);
       const int mine = pair ? (x == 0 || u.rows > kTileRows ? u.n_tiles : 0) : x == 0 ? (u.n_tiles + 1) >> 1 : u.n_tiles >> 1;
-      const int pos = live ? (SEL ? u.pos0 : u.pos0 + (u.row0 + row) / a.group) : -1;
+      const int pos = live ? (SEL ? u.pos0 : max(u.pos0 + (u.row0 + row) / a.group, -1)) : -1;
       float f = 0.f;                     // scores to base-2 exponents
       if (pair) {
         if (!warp_wait(smem_u32(&ctrl->qraw), un & 1, abort_flag, status)) break;
@@ -938,7 +938,8 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
                 auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };   // keys < n
                 const int k0 = key0 + 32 * c;
                 seen = below(pos + 1 - k0);
-                if (a.window > 0) seen &= ~below(pos - a.window + 1 - k0) | below(a.sinks - k0);
+                const int gone = pos - a.window;       // the last key before the window; within 32 bits, pos >= -1
+                if (a.window > 0 && gone >= k0) seen &= ~below(gone - k0 + 1) | below(a.sinks - k0);
               }
             }
             const float fa0 = f * m.ks[2 * c], fa1 = f * m.ks[2 * c + 1], fb0 = m.lv[2 * c], fb1 = m.lv[2 * c + 1];

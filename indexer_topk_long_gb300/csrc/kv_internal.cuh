@@ -62,7 +62,8 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int
   KvSeq s;
   s.q0 = min(max(kv_load(bt.cu_q + b), 0), bt.N);
   s.nq = min(max(kv_load(bt.cu_q + b + 1), s.q0), bt.N) - s.q0;
-  const long long room = static_cast<long long>(bt.width) << c.page_log2;
+  // (a tile's last key and the one after it stay within 32 bits)
+  const long long room = min(static_cast<long long>(bt.width) << c.page_log2, 0x7FFFFF00ll);
   const int tokens = max(kv_load(bt.seq_lens + b), 0);
   s.len = static_cast<int>(min(static_cast<long long>(tokens), room));
   s.pos0 = tokens - s.nq;                // negative when a sequence is shorter than its queries
