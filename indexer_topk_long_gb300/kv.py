@@ -30,6 +30,13 @@ def _fail(name: str, what: str):
     raise ValueError(f"{name}: {what}")
 
 
+def _int32s(**values) -> None:
+    """ctypes cuts whole numbers to 32 bits without a word."""
+    for name, x in values.items():
+        if not -2**31 <= x < 2**31:
+            _fail(name, f"expected a 32-bit whole number, got {x}")
+
+
 def _device_ok(t, name: str, device) -> None:
     if t.device != device:
         _fail(name, f"expected a tensor on {device}, got one on {t.device}")
@@ -115,6 +122,7 @@ class PagedKVCache:
         self.h = None
         self.lib = ltk.load_library()
         self.num_pages, self.heads, self.dim, self.page = int(num_pages), int(heads), int(dim), int(page)
+        _int32s(heads=self.heads, dim=self.dim, page=self.page, engine=int(engine))
         given = [t is not None for t in (k_codes, v_codes, k_scale, v_scale)]
         if any(given) and not all(given):
             raise ValueError("k_codes, v_codes, k_scale, v_scale: give all four or none")
@@ -263,6 +271,8 @@ class PagedKVCache:
         heads, qs = self._queries(q, n)
         if max_q is None:
             max_q = -(-n // max(B, 1))
+        if (window | sinks | max_q) >> 31:
+            _int32s(window=window, sinks=sinks, max_q=max_q)
         if stream is None and self.h is not None:
             st = self._raw_stream(self._index)
         else:
