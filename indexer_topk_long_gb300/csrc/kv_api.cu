@@ -267,9 +267,12 @@ ltk_status ltk_kv_status(ltk_kv* h, int* device_status, void* stream) {
   cudaError_t e = cudaMemcpyAsync(&value, h->status, 4, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, 4, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-  // a call that gave up half way may have left its counters
-  if (e == cudaSuccess && value == LTK_ERR_TIMEOUT)
-    e = cudaMemset(h->counters, 0, static_cast<size_t>(h->num_counters) * 4);
+  // A call that gave up half way may have left its counters, and the status holds the first error
+  // only, so any error clears them: on the stream, ahead of the calls that come after.
+  if (e == cudaSuccess && value != LTK_OK) {
+    e = cudaMemsetAsync(h->counters, 0, static_cast<size_t>(h->num_counters) * 4, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  }
   if (e != cudaSuccess) return kv_cuda_fail(e, "ltk_kv_status");
   *device_status = value;
   return LTK_OK;
