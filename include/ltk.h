@@ -382,7 +382,8 @@ void ltk_kv_destroy(ltk_kv* h);
  *               q_out == q with contiguous tokens rotates in place.
  * Each touched (page, head) gets the scale 2^e, e the smallest exponent >= -40
  * with max|x| <= 448 * 2^e over its tokens; a page that already held tokens
- * never lowers e, and when e grows its held codes are rounded again.  A token
+ * never lowers e, and when e grows its held codes are rounded again (also when a
+ * scale of the caller's own is no power of two: e is then the next one above).  A token
  * whose key or value row of a head holds a NaN, an infinity or a value beyond
  * 448 * 2^40 is held in that head as a NaN key row and a zero value row: every
  * query that sees it gets NaN, no other query does.

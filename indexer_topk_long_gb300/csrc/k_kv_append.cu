@@ -9,7 +9,8 @@
 // precision is the same at every exponent, so nothing is lost against 448 / max,
 // x * 2^-e is exact, and when a later token raises a partly filled page's
 // exponent its held codes are re-rounded by a power of two (exact but for
-// subnormal codes).  Products and sums are rounded one by one in fp32 (no
+// subnormal codes).  A page that was filled by others under a scale that is no
+// power of two gets the next one above, its codes rounded once more.  Products and sums are rounded one by one in fp32 (no
 // fused multiply-add), so codes do not depend on the compiler's contraction.
 //
 // A token whose key or value row holds a NaN, an infinity or a value beyond
@@ -101,7 +102,11 @@ __device__ __forceinline__ int scale_exp(float amax) {
   return min(max(e, kKvMinExp), kKvMaxExp);
 }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-__device__ __forceinline__ int exp_of(float pow2) { return static_cast<int>((__float_as_uint(pow2) >> 23) & 0xFF) - 127; }
+// Smallest e >= kKvMinExp with s <= 2^e, for the scale of what a page holds (by append a power of two).
+__device__ __forceinline__ int exp_above(float s) {
+  const uint32_t b = __float_as_uint(fmaxf(s, 0.f));
+  return min(max(static_cast<int>(b >> 23) - 127 + ((b & 0x7FFFFFu) != 0 ? 1 : 0), kKvMinExp), 126);
+}
 
 __device__ __forceinline__ uint2 encode(const Chunk& c, float inv) {
   uint32_t w[4];
@@ -263,18 +268,17 @@ __global__ void __launch_bounds__(128) kv_append_few_kernel(const AppendParams p
     v_max = fmaxf(v_max, __shfl_xor_sync(0xFFFFFFFFu, v_max, o));
   }
   int ke = scale_exp(k_max), ve = scale_exp(v_max);
-  if (r_lo > 0) {                        // tokens held before: their codes follow a larger exponent
-    const int ko = exp_of(k_held), vo = exp_of(v_held);
-    ke = max(ke, ko);
-    ve = max(ve, vo);
-    const float k_by = pow2f(max(ko - ke, -126)), v_by = pow2f(max(vo - ve, -126));
-    for (int r = sub; r < r_lo && (ke > ko || ve > vo); r += RPP) {
+  if (r_lo > 0) {                        // tokens held before: their codes follow a larger scale
+    ke = max(ke, exp_above(k_held));
+    ve = max(ve, exp_above(v_held));
+    const float k_by = k_held * pow2f(-ke), v_by = v_held * pow2f(-ve);
+    for (int r = sub; r < r_lo && (k_by != 1.f || v_by != 1.f); r += RPP) {
       const size_t o = (block * c.page + r) * D + j * 8;
-      if (ke > ko) {
+      if (k_by != 1.f) {
         uint2* w = reinterpret_cast<uint2*>(c.k_codes + o);
         *w = rescale_codes(*w, k_by);
       }
-      if (ve > vo) {
+      if (v_by != 1.f) {
         uint2* w = reinterpret_cast<uint2*>(c.v_codes + o);
         *w = rescale_codes(*w, v_by);
       }
@@ -424,11 +428,10 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(const AppendParams p,
   int ke = scale_exp(k_max), ve = scale_exp(v_max);
   float k_by = 1.f, v_by = 1.f;
   if (r_lo > 0) {                                             // tokens held before
-    const int ko = exp_of(k_held), vo = exp_of(v_held);
-    ke = max(ke, ko);
-    ve = max(ve, vo);
-    k_by = pow2f(max(ko - ke, -126));
-    v_by = pow2f(max(vo - ve, -126));
+    ke = max(ke, exp_above(k_held));
+    ve = max(ve, exp_above(v_held));
+    k_by = k_held * pow2f(-ke);
+    v_by = v_held * pow2f(-ve);
   }
   const float k_inv = pow2f(-ke), v_inv = pow2f(-ve);
   if (threadIdx.x == 0) {
