@@ -43,7 +43,7 @@ constexpr int kGroups = 2;               // 16-key groups a warp takes from a ti
 constexpr int kWarpKeys = 16 * kGroups;
 constexpr int kTileKeys = kWarps * kWarpKeys;
 constexpr int kStages = 2;               // 8 KB each and warp at D = 128: 64 KB in flight an SM
-constexpr float kMinusHuge = -1e30f;     // running maximum of a row that has seen nothing
+constexpr float kMinusHuge = -3e38f;     // running maximum of a row that has seen nothing
 // A weight at the running maximum is 2^kBoost; the maximum is only moved when a
 // score exceeds it by more than kSlack, so weights stay below 2^15 < f16's 65504.
 constexpr float kBoost = 8.f;
