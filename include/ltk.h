@@ -343,7 +343,7 @@ typedef struct ltk_kv ltk_kv;
  *               sequence b's (0 of them is allowed), cu_q[B] = N.
  * New token i of sequence b has position seq_lens[b] - n_b + i, n_b its number
  * of new tokens.  Its position p is row p % page of page page_table[b, p / page].
- * table_width * page is below 2^31; positions from 2^31 - 256 on count as past
+ * table_width * page is below 2^31; positions from 2^31 - 1024 on count as past
  * the table.
  * A page number outside [0, num_pages), a position past the page table's
  * columns, a negative position or one past a rotation table sets the handle's

@@ -938,8 +938,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
                 auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };   // keys < n
                 const int k0 = key0 + 32 * c;
                 seen = below(pos + 1 - k0);
-                const int gone = pos - a.window;       // the last key before the window; within 32 bits, pos >= -1
-                if (a.window > 0 && gone >= k0) seen &= ~below(gone - k0 + 1) | below(a.sinks - k0);
+                if (a.window > 0) seen &= ~below(static_cast<int>(static_cast<uint32_t>(pos) - a.window + 1 - k0)) | below(a.sinks - k0);
               }
             }
             const float fa0 = f * m.ks[2 * c], fa1 = f * m.ks[2 * c + 1], fb0 = m.lv[2 * c], fb1 = m.lv[2 * c + 1];

@@ -227,7 +227,7 @@ static ltk_status kv_attend(ltk_kv* h, const ltk_kv_batch* batch, int dtype, con
   p.q_heads = q_heads;
   p.group = q_heads / h->cache.heads;
   p.scale_log2 = scale * 1.44269504088896340736f;
-  p.window = window;
+  p.window = std::min(window, kKvMaxPos);
   p.sinks = sinks;
   p.idx = idx;
   p.k = k;

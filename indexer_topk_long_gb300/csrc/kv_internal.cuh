@@ -24,6 +24,9 @@ constexpr int kKvMaxExp = 40;
 // made as if the scale were this one, the smallest that append writes, so that they push no other
 // weight out of its range, and meet zeros instead of the block's codes.
 constexpr float kKvLeastScale = 0x1p-40f;
+// Positions are below this, and no window is larger (it would hide nothing more), so that what is
+// made of a row's position, a window and a tile near it stays within 32 bits.
+constexpr int kKvMaxPos = 0x7FFFFC00;
 constexpr int kDevArg = 1;               // device status: an index outside its table
 
 struct KvCache {
@@ -62,8 +65,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int
   KvSeq s;
   s.q0 = min(max(kv_load(bt.cu_q + b), 0), bt.N);
   s.nq = min(max(kv_load(bt.cu_q + b + 1), s.q0), bt.N) - s.q0;
-  // (a tile's last key and the one after it stay within 32 bits)
-  const long long room = min(static_cast<long long>(bt.width) << c.page_log2, 0x7FFFFF00ll);
+  const long long room = min(static_cast<long long>(bt.width) << c.page_log2, static_cast<long long>(kKvMaxPos));
   const int tokens = max(kv_load(bt.seq_lens + b), 0);
   s.len = static_cast<int>(min(static_cast<long long>(tokens), room));
   s.pos0 = tokens - s.nq;                // negative when a sequence is shorter than its queries
