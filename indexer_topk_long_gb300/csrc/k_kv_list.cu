@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
               if (t < kHalf) {
                 const int r = x * kHalf + t;
                 const float high = fmaxf(fmaxf(most[0][r], most[1][r]), fmaxf(most[2][r], most[3][r]));
-                const float old = -minus_max[t], next = fmaxf(old, high - kBoost);
+                const float old = -minus_max[t], next = fmaxf(old, below_top(high, high - kBoost));
                 by[t] = exp2_approx(old - next);
                 minus_max[t] = -next;
               }
@@ -679,7 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
 #pragma unroll
             for (int r = 0; r < kHalf; r += 2) {
               const float4 m = *reinterpret_cast<const float4*>(&minus_max[r & ~3]);
-              const float2 z = unpack2(fma2(pack2(s[r], s[r + 1]), ks2, add2(lv2, r & 2 ? pack2(m.z, m.w) : pack2(m.x, m.y))));
+              // (rounded as the maxima are, before they are taken off)
+              const float2 z = unpack2(add2(fma2(pack2(s[r], s[r + 1]), ks2, lv2), r & 2 ? pack2(m.z, m.w) : pack2(m.x, m.y)));
               const float w0 = exp2_approx(z.x), w1 = exp2_approx(z.y);
               w2[r >> 1] = pack2(w0, w1);
               h[r >> 1] = pack_f16(w0, w1);

@@ -96,6 +96,10 @@ __device__ __forceinline__ int merge_place(int r, int chunk) {
   return chunk ^ (D == 128 ? (r >> 1) & 3 : ((r >> 1) & 1) | ((r >> 2) & 1) << 2);
 }
 
+// A row's new running maximum, kBoost below its largest score; where fp32 holds scores to 16 and
+// rounding put it too far below for f16 weights, the largest score itself.
+__device__ __forceinline__ float below_top(float top, float next) { return top - next > kSlack + kBoost ? top : next; }
+
 // Row r of a 16-key group and 16-byte chunk: byte offset in the group's codes.  Lanes
 // of one quarter warp read chunks of two neighbouring rows (K) or one or two
 // chunks of four rows of equal parity (V); the placement keeps each on distinct
@@ -598,16 +602,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
 #pragma unroll
       for (int x = 0; x < RT; ++x)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) outgrown = outgrown || mx[x][n] > M[x][n] + (kSlack + kBoost);
+        for (int n = 0; n < 2; ++n) outgrown = outgrown || mx[x][n] - M[x][n] > kSlack + kBoost;
       if (__any_sync(0xFFFFFFFFu, outgrown)) {
 #pragma unroll
         for (int x = 0; x < RT; ++x)
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            float top = mx[x][n] - kBoost;
+            float top = mx[x][n];
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            const float next = fmaxf(M[x][n], top);
+            const float next = fmaxf(M[x][n], below_top(top, top - kBoost));
             const float by = exp2_approx(M[x][n] - next);
             M[x][n] = next;
             l[x][n] *= by;

@@ -951,10 +951,10 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
               mx[e & 3] = fmaxf(mx[e & 3], s[e]);
             }
             const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (__any_sync(0xFFFFFFFFu, most > M + (kBoost + kSlack))) {
+            if (__any_sync(0xFFFFFFFFu, most - M > kBoost + kSlack)) {
               // What was summed and stored so far follows the new maximum, by a power of two, so
               // that the tile's stored f16 weights are not rounded again (but for subnormal ones).
-              const float top = fmaxf(M, ceilf(most - kBoost));
+              const float top = fmaxf(M, below_top(most, ceilf(most - kBoost)));
               const float by = exp2_approx(M - top);
               M = top;
               l *= by;

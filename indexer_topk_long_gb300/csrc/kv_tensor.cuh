@@ -15,6 +15,10 @@ constexpr float kMinusHuge = -3e38f;     // running maximum of a row that has se
 constexpr float kBoost = 8.f;
 constexpr float kSlack = 7.f;
 
+// A row's new running maximum, kBoost below its largest score; where fp32 holds scores to 16 and
+// rounding put it too far below for f16 weights, the largest score itself.
+__device__ __forceinline__ float below_top(float top, float next) { return top - next > kSlack + kBoost ? top : next; }
+
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
