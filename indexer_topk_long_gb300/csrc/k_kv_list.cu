@@ -6,7 +6,7 @@
 //
 // as in the other attention kernels: each key's value scale is folded into its weights'
 // exponent, weights meet the value codes as f16 of at most 2^15, codes become f16 exactly,
-// queries after a power-of-two scaling of their row; M, l and O are fp32.
+// queries after a power-of-two scaling; M, l and O are fp32.
 //
 // Every query has keys of its own, so a product's 128 rows cannot be filled with queries;
 // they are filled with keys instead, and the (at most 64) query rows are its columns:
@@ -86,10 +86,11 @@ struct Ctrl {
   int last[2];
   Piece piece[kPieces];
   Meta meta[kMetas];
-  float factor[kPieces];                 // scores to base-2 exponents, for key scales of 1
+  float factor[kPieces];                 // scores to base-2 exponents, for key scales of 1; negative: see row_exp
   alignas(16) float minus_max[kRows];    // by row: minus the running maximum
   float most[4][kRows];                  // by warp: maxima, and at the end sums
   float by[kRows];                       // what rows' sums are multiplied by
+  alignas(16) uint8_t row_exp[kPieces][kRows];       // exponents of rows scaled by themselves, see convert_queries
 };
 
 static_assert(offsetof(Ctrl, meta) % 16 == 0 && sizeof(Meta) % 16 == 0 && offsetof(Meta, vs) % 16 == 0 &&
@@ -150,49 +151,81 @@ template <int D>
 __device__ __forceinline__ int code_at(int row, int c) {
   return row * D + ((c ^ (D == 128 ? row & 7 : (row >> 1) & 3)) << 4);
 }
-// The unit's queries, copied as they are, to f16 in place, by one warp: all times one power of
-// two that takes the largest (finite) element to [2^14, 2^15).  Elements from 2^-29 of the
-// largest on keep f16's 11 bits, smaller ones an error of 2^-40 of the largest: in a score
-// that is 2^-29 of what f16 inputs' own last bit is worth in the largest row.  Returns what
-// turns the products into base-2 exponents.
-template <int D>
-__device__ __forceinline__ float convert_queries(const AttnParams& a, uint32_t q_sm, int lane) {
-  // magnitudes compare as integers, infinities and NaN above a bound
-  const uint32_t bound = a.bf16 ? 0x7F80u : 0x7C00u;
+// Largest of a chunk's eight 16-bit magnitudes, which compare as integers, infinities and NaN from
+// `bound` on; those count as 0 when `finite`.
+__device__ __forceinline__ uint32_t chunk_most(const uint4& x, bool finite, uint32_t bound) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t most = 0;
-#pragma unroll 4
-  for (int i = lane; i < kRows * D / 8; i += 32) {
-    const uint4 x = lds128(q_sm + i * 16);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) most = __vmaxu2(most, w[e] & 0x7FFF7FFFu);
+  for (int e = 0; e < 4; ++e) {
+    uint32_t m = w[e] & 0x7FFF7FFFu;
+    if (finite) m = ((m & 0xFFFFu) < bound ? m & 0xFFFFu : 0u) | ((m >> 16) < bound ? m & 0xFFFF0000u : 0u);
+    most = __vmaxu2(most, m);
   }
-  if (__any_sync(0xFFFFFFFFu, (most & 0xFFFFu) >= bound || most >> 16 >= bound)) {
-    most = 0;                            // some are not finite: without them
-#pragma unroll 1
-    for (int i = lane; i < kRows * D / 2; i += 32) {
-      uint32_t w;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(q_sm + i * 4));
-      const uint32_t lo = w & 0x7FFFu, hi = w >> 16 & 0x7FFFu;
-      most = __vmaxu2(most, (lo < bound ? lo : 0u) | (hi < bound ? hi : 0u) << 16);
-    }
-  }
-  most = __reduce_max_sync(0xFFFFFFFFu, max(most & 0xFFFFu, most >> 16));
-  const float amax = kv_unpack16(most, a.bf16).x;
-  const int e = amax > 0.f ? max(static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14, -118) : 0;
+  return max(most & 0xFFFFu, most >> 16);
+}
+// Exponent of the power of two that takes a largest element to [2^14, 2^15).
+__device__ __forceinline__ int query_exp(uint32_t most, bool bf16) {
+  return max(static_cast<int>(__float_as_uint(kv_unpack16(most, bf16).x) >> 23) - 127 - 14, -118);
+}
+__device__ __forceinline__ void scale_chunk(uint32_t at, const uint4& x, int e, bool bf16) {
   const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll 4
-  for (int i = lane; i < kRows * D / 8; i += 32) {
-    const uint4 x = lds128(q_sm + i * 16);
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = kv_unpack16(w[j], a.bf16);
-      w[j] = kv_pack16(f.x * by, f.y * by, false);
-    }
-    sts128(q_sm + i * 16, w[0], w[1], w[2], w[3]);
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = kv_unpack16(w[j], bf16);
+    w[j] = kv_pack16(f.x * by, f.y * by, false);
   }
-  return a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  sts128(at, w[0], w[1], w[2], w[3]);
+}
+// The unit's queries, copied as they are, to f16 in place, by one warp.  As a rule all times one
+// power of two, for the largest (finite) element: elements from 2^-29 of the largest on keep f16's
+// 11 bits, smaller ones an error of 2^-40 of the largest, which in a row whose own largest is 2^-16
+// of that is 2^-24.  Where eight elements lie below 2^-16 together (and not all are 0) every row gets
+// a power of its own, and row_exp what turns its scores into the others', as biased fp32 exponents;
+// a head's results do not depend on how large the others' queries are.  Returns what turns the
+// products into base-2 exponents, negative in the second case.
+template <int D>
+__device__ __forceinline__ float convert_queries(const AttnParams& a, uint32_t q_sm, uint8_t* row_exp, int lane) {
+  const uint32_t bound = a.bf16 ? 0x7F80u : 0x7C00u;
+  constexpr int kChunks = kRows * D / 8;
+  uint32_t most = 0, least = ~0u;        // least: less 1, so that zeros are left out
+#pragma unroll 4
+  for (int i = lane; i < kChunks; i += 32) {
+    const uint32_t m = chunk_most(lds128(q_sm + i * 16), false, bound);
+    most = max(most, m);
+    least = min(least, m - 1);
+  }
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (most >= bound) {                   // some are not finite: without them
+    most = 0;
+#pragma unroll 1
+    for (int i = lane; i < kChunks; i += 32) most = max(most, chunk_most(lds128(q_sm + i * 16), true, bound));
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+  }
+  least = __reduce_min_sync(0xFFFFFFFFu, least);
+  const int e = most != 0 ? query_exp(most, a.bf16) : 0;
+  const float factor = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  if (least < most && kv_unpack16(least + 1, a.bf16).x < kv_unpack16(most, a.bf16).x * 0x1p-16f) {
+    // eight lanes to a row (of 64 elements; D = 128: then the other 64), four rows a step
+#pragma unroll 1
+    for (int i = lane; i < kRows * 8; i += 32) {
+      const uint4 x = lds128(q_sm + i * 16);
+      uint4 y = make_uint4(0, 0, 0, 0);
+      if constexpr (D == 128) y = lds128(q_sm + kRows * 128 + i * 16);
+      uint32_t m = max(chunk_most(x, true, bound), chunk_most(y, true, bound));
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      const int er = m != 0 ? max(query_exp(m, a.bf16), e - 126) : e;
+      scale_chunk(q_sm + i * 16, x, er, a.bf16);
+      if constexpr (D == 128) scale_chunk(q_sm + kRows * 128 + i * 16, y, er, a.bf16);
+      if ((lane & 7) == 0) row_exp[i >> 3] = static_cast<uint8_t>(127 + er - e);
+    }
+    return -factor;
+  }
+#pragma unroll 4
+  for (int i = lane; i < kChunks; i += 32) scale_chunk(q_sm + i * 16, lds128(q_sm + i * 16), e, a.bf16);
+  return factor;
 }
 // A copying lane's rows (lanes of a row share them) lie side by side: kStep rows to an
 // instruction, key % kStep which of them, key % 32 / kStep which instruction.
@@ -320,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
         }
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         __syncwarp();
-        const float factor = convert_queries<D>(a, q_sm, lane);
+        const float factor = convert_queries<D>(a, q_sm, ctrl->row_exp[us], lane);
         if (lane == 0) ctrl->factor[us] = factor;
         fence_async_smem();
         __syncwarp();
@@ -611,7 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
       ok = wait(&ctrl->qfull[un & 1], un >> 1);
       if (t < kHalf) minus_max[t] = -kMinusHuge;
       if (meet_any(x, !ok)) break;
-      const float factor = ctrl->factor[us];
+      const float factor = fabsf(ctrl->factor[us]);
+      const bool uneven = ctrl->factor[us] < 0.f;
       uint64_t l2[kHalf / 2];            // this thread's keys' share of l
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) l2[i] = 0;
@@ -630,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
           const float ks = meta.ks[t] * factor, vs = meta.vs[t];
           const float lv = vs > 0.f ? __log2f(vs) + kBoost : -inf, iv = vs > 0.f ? __frcp_rn(vs) : 0.f;
           const uint64_t ks2 = pack2(ks, ks), lv2 = pack2(lv, lv), iv2 = pack2(iv, iv);
-          bool fresh = i > 0;            // the maxima may do
+          // the maxima may do (with rows scaled by themselves they are found anew for every tile, so
+          // that only that path, and not the usual one, has to bring their scores into line)
+          bool fresh = i > 0 && !uneven;
           uint64_t w2[kHalf / 2];
 #pragma unroll 1
           while (true) {
@@ -638,6 +674,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_list_kernel(const __grid_const
             tmem_ld32(s_at, s);
             tmem_ld32_wait(s);
             if (!fresh) {
+              if (uneven) {
+#pragma unroll
+                for (int g = 0; g < kHalf / 4; ++g) {
+                  const uint32_t e4 = reinterpret_cast<const uint32_t*>(ctrl->row_exp[us] + x * kHalf)[g];
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) s[4 * g + r] *= __uint_as_float((e4 >> (8 * r) & 0xFFu) << 23);
+                }
+              }
               // new maxima: over the tile's keys by warp, then over the warps
               float v[32];
 #pragma unroll
