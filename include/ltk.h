@@ -345,10 +345,16 @@ typedef struct ltk_kv ltk_kv;
  * of new tokens.  Its position p is row p % page of page page_table[b, p / page].
  * table_width * page is below 2^31; positions from 2^31 - 1024 on count as past
  * the table.
- * A page number outside [0, num_pages), a position past the page table's
- * columns, a negative position or one past a rotation table sets the handle's
- * device status to LTK_ERR_ARG: nothing is written for such a page, and queries
- * that see it get NaN.
+ * Set the handle's device status to LTK_ERR_ARG: a page number outside
+ * [0, num_pages) and a position past the page table's columns (append writes
+ * nothing there, queries that see it get NaN); in append also a sequence shorter
+ * than its new tokens (none of them is stored) and a position past the rotation
+ * table (the token is held as NaN).  In attention the queries before a sequence's
+ * first token see nothing (0 and -inf) and are not reported.
+ * A cu_q that does not rise from 0 to N is clamped to that range: no call reads
+ * or writes outside the buffers and the pages of the table for it, but what its
+ * tokens get is not defined, and only the dense tensor-core kernel (never chosen for 16
+ * rows per KV head or fewer; engine 2) reports it.
  */
 typedef struct {
   const int* page_table;
