@@ -92,11 +92,6 @@ __device__ __forceinline__ int kv_page(const KvBatch& bt, const KvCache& c, int 
   return at < bt.width ? kv_load(bt.page_table + static_cast<size_t>(b) * bt.width + at) : -1;
 }
 
-// Codes (byte offset) of row `off` of (page, head).
-__device__ __forceinline__ size_t kv_row(const KvCache& c, long long page, int head, int off, int dim) {
-  return ((static_cast<size_t>(page) * c.heads + head) * c.page + off) * dim;
-}
-
 // Four e4m3 codes to four f16 values (exact), in order: lo holds the first two.
 __device__ __forceinline__ void e4m3x4_to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
@@ -111,10 +106,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-__device__ __forceinline__ float kv_load16(const void* p, size_t i, bool bf16) {
-  return bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i])
-              : __half2float(reinterpret_cast<const __half*>(p)[i]);
-}
 // Two packed 16-bit values to fp32.
 __device__ __forceinline__ float2 kv_unpack16(uint32_t w, bool bf16) {
   if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));

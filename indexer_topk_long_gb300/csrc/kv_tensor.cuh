@@ -101,15 +101,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&v)[16]) {
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(a)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32f(uint32_t a, const float (&v)[32]) {
-  uint32_t w[16];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * h + i]);
-    tmem_st16(a + 16 * h, w);
-  }
-}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Descriptor of an operand in 128-byte-swizzled rows (8-row atoms 1024 bytes apart).
