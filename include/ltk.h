@@ -310,8 +310,8 @@ ltk_status ltk_litedsa_pack(const int* topk_idx, int T, int k, int group, int* u
  *
  * Cache of one layer (device memory, owned by the caller):
  *   k_codes, v_codes  e4m3 codes [num_pages, heads, page, dim];
- *   k_scale, v_scale  fp32 [num_pages, heads], 0 or positive; the value held is
- *                     code * scale (a scale of 0: zeros).
+ *   k_scale, v_scale  fp32 [num_pages, heads], 0 or 2^-64 to 2^64; the value held
+ *                     is code * scale (a scale of 0: zeros).
  * page is 16, 32, 64 or 128 tokens, dim 64 or 128.
  *
  * A handle binds the four buffers and owns a workspace of a few tens of MiB on
@@ -408,11 +408,20 @@ ltk_status ltk_kv_append(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const 
  *               q_heads a multiple of the cache's heads; query head i reads KV
  *               head i / (q_heads / heads).
  *   max_q       the largest number of queries of one sequence, as a hint for the
- *               choice of kernel (0: unknown); results are right for any value.
+ *               choice of kernel (0: unknown); results are right for any value, but
+ *               one far from the truth can take a slower kernel.
  *   out         device [N, q_heads, dim] in dtype;  lse device fp32 [N, q_heads]
  *               (natural logarithm of the sum of exponentials) or NULL.
  * A query that sees no key gets 0 and -inf.  Value codes must not be NaN
  * (ltk_kv_append never writes one); rows past a sequence's length are not read.
+ * out must not overlap q.
+ * Arithmetic: products of f16 numbers (codes exactly, queries after a scaling by
+ * powers of two, weights rounded to f16); sums and softmax statistics in fp32.
+ * Keys whose weight times value scale is below 2^-21 of the row's largest keep
+ * fewer bits, below 2^-31 none.  For listed keys and more than 64 query heads a
+ * KV head the same holds of block scales below 2^-21 of the largest among 16
+ * entries of the list.  A value scale is added to the score as its logarithm, so
+ * weights carry the score's rounding to fp32, which passes f16's at scores of 10^4.
  */
 ltk_status ltk_kv_attention(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q,
                             long long q_stride, int q_heads, int max_q, float scale, int window,

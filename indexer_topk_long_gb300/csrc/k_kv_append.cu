@@ -19,11 +19,12 @@
 // row of a matrix product through 0 * NaN).  So is a token whose position lies
 // past the rotation table.
 //
-// Bound by bytes for chunks (keys, values and queries read, codes and rotated queries written),
-// by latency for decode steps.  A page's rows are read twice, for its largest and for its codes
-// (the second time from L2), since rows held in registers left too few warps: 8192 tokens of 8
-// KV and 32 query heads of 128 take 42 us, 189 MB at 4.5 TB/s, 66% of the copy rate; one token
-// of each of 256 sequences 4.5 us, one token 3.4 (calls back to back).
+// Bound by latency: of decode steps by that of one token, of chunks by the loads' with a third of
+// the warps resident and 61% of the issue slots used (DRAM is at 38%).  A page's rows are read
+// twice, for its largest and for its codes (the second time from L2), since rows held in
+// registers left still fewer warps: 8192 tokens of 8 KV and 32 query heads of 128 take 42 us, 189
+// MB at 4.5 TB/s, 66% of the copy rate; one token of each of 256 sequences 4.3 us, one token 3.0
+// (calls back to back).
 #include "kv_internal.cuh"
 
 namespace ltk {

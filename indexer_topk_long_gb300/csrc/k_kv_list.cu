@@ -26,7 +26,7 @@
 // cut into equal pieces, a unit cut by a border being joined by the last of its CTAs.
 //
 // 8192 queries of 2048 keys each, 64 heads on one KV head, D = 128, in a cache of 1M tokens:
-// 1075 us, 0.51 PFLOP/s and 4.3 GB of code rows at 4.0 TB/s out of L2.  Bound by the softmax
+// 1063 us, 0.52 PFLOP/s and 4.3 GB of code rows at 4.0 TB/s out of L2.  Bound by the softmax
 // warps: a tile takes them some 1900 cycles (scores from tensor memory, 32 rows' weights, the
 // vote, P to shared memory) while the products need 640 and the conversions 1300; then a unit
 // costs as much as another two tiles to end and begin.  What was tried: 128 query rows a product,

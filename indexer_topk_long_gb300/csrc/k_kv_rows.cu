@@ -8,7 +8,7 @@
 //
 // ks, vs are the blocks' scales.  Folding log2(vs) into the exponent keeps the
 // weights that meet the value codes at most 2^(kBoost + kSlack) for any scales,
-// so they go to the matrix product as f16: 11 significant bits down to 2^-24 of
+// so they go to the matrix product as f16: 11 significant bits down to 2^-22 of
 // the running maximum's weight.  Sums, M and l are fp32.  K and V codes become f16
 // exactly; queries (bf16 or f16) become f16 after a power-of-two scaling of the
 // row, exact but for elements below 2^-22 of the row's largest.
@@ -23,13 +23,14 @@
 // 16: a small group leaves few columns empty, and a lane's weights are of few keys.  P comes
 // from the scores' layout by an 8 x 8 transposition across the warp.
 //
-// Measured (8 KV heads of 4 query heads, D = 128): one sequence of 262144 tokens 95 us, 537 MB
-// at 5.6 TB/s, 83% of the copy rate; 64 sequences of 128 to 32768 tokens 139 us, 795 MB at 5.7
-// TB/s, 84% (query rows as the products' rows, 16 with 12 of them empty: 97 and 153 us); 16 x 2
-// queries of 1000 listed keys 23 us; 2048 listed keys for 64 heads of one KV head 14 us and 777
-// tokens 8 us, which is latency.  What is left of long streams: the first data come after 5 us, since all SMs ask at
-// once, and of an SM's three CTAs the last gets the least of its issue slots and ends up to 10%
-// after the first, alone and too few to fill memory.
+// Measured (8 KV heads of 4 query heads, D = 128): one sequence of 262144 tokens 94 us, 537 MB
+// at 5.7 TB/s, 84% of the copy rate; 64 sequences of 128 to 32768 tokens 141 us, 795 MB at 5.6
+// TB/s, 83% (query rows as the products' rows, 16 with 12 of them empty: 97 and 153 us); 16 x 2
+// queries of 1000 listed keys 24 us; 2048 listed keys for 64 heads of one KV head 14 us and 777
+// tokens 8 us, which is latency.  The look for blocks of zeros is 0.3% of long streams and up to
+// 2% of listed keys.  What is left of long streams: the first data come after 5 us, since all SMs
+// ask at once, and of an SM's three CTAs the last gets the least of its issue slots and ends up to
+// 10% after the first, alone and too few to fill memory.
 #include "kv_internal.cuh"
 
 namespace ltk {

@@ -27,9 +27,10 @@
 // Bound by the products, and by the softmax that feeds them: a pair's key tile takes four
 // 128-cubes, 2050 cycles of the tensor cores at D = 128, and 2 x 128 x 128 exponentials, 1024
 // cycles of each scheduler's exp2 unit.  2048 queries at the end of 32768 tokens, 8 KV heads of
-// 4: 774 us, 1.38 PFLOP/s, 72% of the matrix rate.  Small work is bound by what a unit costs to
+// 4: 778 us, 1.37 PFLOP/s, 72% of the matrix rate (some 20 us of it is that a warp's lanes agree on
+// whether a wait was given up).  Small work is bound by what a unit costs to
 // begin and end (lookups, queries, the first tile's maxima, the joining of pieces: some 20 us):
-// 24 ragged chunks of 1362 tokens with a window of 1024, D = 64, 41 us.
+// 24 ragged chunks of 1362 tokens with a window of 1024, D = 64, 42 us.
 #include "kv_tensor.cuh"
 
 namespace ltk {

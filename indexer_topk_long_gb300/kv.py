@@ -113,7 +113,8 @@ class PagedKVCache:
 
     Without the four buffers the cache is allocated, zeroed.  ``k_codes`` and
     ``v_codes`` are uint8 (or float8_e4m3fn) [num_pages, heads, page, dim],
-    ``k_scale`` and ``v_scale`` fp32 [num_pages, heads].  ``engine`` 0 lets measured costs
+    ``k_scale`` and ``v_scale`` fp32 [num_pages, heads] (0: a block of zeros; append
+    writes powers of two).  ``engine`` 0 lets measured costs
     choose the attention kernel, 1 takes the one for few rows, 2 the tensor-core tiles."""
 
     def __init__(self, num_pages: int, heads: int, dim: int, page: int = 64, k_codes=None, v_codes=None,
@@ -265,7 +266,8 @@ class PagedKVCache:
                   window: int = 0, sinks: int = 0, out=None, lse=None, stream=None):
         """Causal attention of q [N, q_heads, dim] over the cached tokens; with ``window`` > 0 a
         query at p sees keys j > p - window and the first ``sinks`` keys.  ``max_q`` (the most
-        queries of one sequence) only helps choose a kernel.  Returns (out, lse)."""
+        queries of one sequence) only helps choose a kernel; left out, the batch's mean stands in,
+        which can choose a slower one where lengths differ much.  Returns (out, lse)."""
         n = q.shape[0]
         B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, self._int32)
         heads, qs = self._queries(q, n)
