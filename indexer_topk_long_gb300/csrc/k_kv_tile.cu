@@ -971,17 +971,15 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
                   tmem_st16(o_col + 16 * q, w);
                 }
               }
-              const __half2 by2 = __float2half2_rn(by);
 #pragma unroll 1
-              for (int q = 0; q < c; ++q) {        // weights of this tile
+              for (int q = 0; q < c; ++q) {        // weights of this tile (f16 would end the factor at 2^-24)
                 tmem_st_wait();
                 tmem_ld32x16(s_col + 16 * q, v);
                 tmem_wait_ld_tied(v);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                  const uint32_t x2 = __float_as_uint(v[e]);
-                  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x2), by2);
-                  w[e] = *reinterpret_cast<const uint32_t*>(&y);
+                  const float2 y = kv_unpack16(__float_as_uint(v[e]), false);
+                  w[e] = pack_f16(y.x * by, y.y * by);
                 }
                 tmem_st16(s_col + 16 * q, w);
               }
