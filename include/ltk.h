@@ -353,8 +353,8 @@ typedef struct ltk_kv ltk_kv;
  * first token see nothing (0 and -inf) and are not reported.
  * A cu_q that does not rise from 0 to N is clamped to that range: no call reads
  * or writes outside the buffers and the pages of the table for it, but what its
- * tokens get is not defined, and only the dense tensor-core kernel (never chosen for 16
- * rows per KV head or fewer; engine 2) reports it.
+ * tokens get is not defined, and only the dense tensor-core kernel (engine 2;
+ * never chosen for 16 rows per KV head or fewer) reports it.
  */
 typedef struct {
   const int* page_table;
@@ -389,9 +389,9 @@ void ltk_kv_destroy(ltk_kv* h);
  * Each touched (page, head) gets the scale 2^e, e the smallest exponent >= -40
  * with max|x| <= 448 * 2^e over its tokens; a page that already held tokens
  * never lowers e, and when e grows its held codes are rounded again (also when a
- * scale of the caller's own is no power of two: e is then the next one above).  A token
- * whose key or value row of a head holds a NaN, an infinity or a value beyond
- * 448 * 2^40 is held in that head as a NaN key row and a zero value row: every
+ * scale of the caller's own is no power of two: e is then the next one above).
+ * A token whose key or value row of a head holds a NaN, an infinity or a value
+ * beyond 448 * 2^40 is held in that head as a NaN key row and a zero value row: every
  * query that sees it gets NaN, no other query does.
  */
 ltk_status ltk_kv_append(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* k,

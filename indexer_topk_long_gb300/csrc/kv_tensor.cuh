@@ -10,7 +10,8 @@ namespace ltk {
 constexpr int kTileRows = 128;           // rows of a product
 constexpr int kKeys = 128;               // keys of a tile
 // Weights are 2^(t - M + kBoost), so that f16 holds those down to 2^-22 of the largest to 11
-// bits (2^-21 where M moves by whole powers of two only); M moves once a weight passes 2^kSlack times its first place (at most 2^15 in f16).
+// bits (2^-21 where M moves by whole powers of two only); M moves once a weight passes 2^kSlack
+// times its first place (at most 2^15 in f16).
 constexpr float kMinusHuge = -3e38f;     // running maximum of a row that has seen nothing
 constexpr float kBoost = 8.f;
 constexpr float kSlack = 7.f;
