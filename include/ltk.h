@@ -55,8 +55,8 @@ typedef enum {
   LTK_ERR_UNSUPPORTED = 6   /* shape or mode the library does not implement   */
 } ltk_status;
 
-/* LTK_F16 is a type of the paged cache's inputs only. */
-typedef enum { LTK_BF16 = 0, LTK_FP8_E4M3 = 1, LTK_F16 = 2 } ltk_dtype;
+/* LTK_F16 is a type of the paged cache's inputs and of logits only, LTK_F32 of logits. */
+typedef enum { LTK_BF16 = 0, LTK_FP8_E4M3 = 1, LTK_F16 = 2, LTK_F32 = 3 } ltk_dtype;
 
 /*
  * Handle configuration (fixed at ltk_create).
@@ -436,9 +436,94 @@ ltk_status ltk_kv_attention_selected(ltk_kv* h, const ltk_kv_batch* batch, int d
                                      long long q_stride, int q_heads, const int* idx, int k,
                                      float scale, void* out, float* lse, void* stream);
 
+/*
+ * Attention of sequences that begin with the same pages, their common part read
+ * once for all of them (many continuations of one prompt, requests behind one
+ * document).  Arguments and results are those of ltk_kv_attention without a
+ * window; only the work is shared out differently.
+ *   groups      device int32 [num_groups + 1], rising from 0 to B: sequences
+ *               groups[g] .. groups[g+1]-1 are group g; NULL: all are one group.
+ *   workspace   device, 16-byte aligned, workspace_bytes long, at least what
+ *               ltk_kv_shared_bytes says; its contents do not outlast the call.
+ * What a group shares is found on the device: the pages with which the table
+ * rows of its sequences begin alike, cut to whole pages that all their queries
+ * see.  A sequence without queries, without a whole page before its first query
+ * or with another first page than the group's first that has one takes no part
+ * (it is attended to by itself).  Groups that do not rise from 0 to B set the
+ * device status to LTK_ERR_ARG, and nothing is shared.
+ * The shared and the own part of a row are joined in fp32; each is rounded as
+ * in ltk_kv_attention.
+ */
+ltk_status ltk_kv_attention_shared(ltk_kv* h, const ltk_kv_batch* batch, const int* groups, int num_groups,
+                                   int dtype, const void* q, long long q_stride, int q_heads, int max_q,
+                                   float scale, void* out, float* lse, void* workspace,
+                                   unsigned long long workspace_bytes, void* stream);
+
+/* Bytes of workspace that a call with B sequences and N queries of q_heads heads needs. */
+ltk_status ltk_kv_shared_bytes(const ltk_kv* h, int B, int N, int q_heads, unsigned long long* bytes);
+
+/*
+ * Reads tokens back: of each sequence the last cu_q[b+1] - cu_q[b] of its
+ * seq_lens[b] tokens, in the batch's order (the batch of an append, or one with
+ * cu_q the running sum of seq_lens for whole sequences).
+ *   dtype        LTK_BF16 or LTK_F16: type of k_out and v_out;
+ *   cos_table ..  as in ltk_kv_append: keys are rotated back by their positions'
+ *                angles; NULL: keys as they are held;
+ *   k_out, v_out device [N, heads, dim], contiguous.
+ * Values are code * scale in fp32 (zeros where the scale is 0), rounded once.  A
+ * token whose page is outside the pool or past the table, that lies before its
+ * sequence's first (more tokens asked for than there are) or past the rotation
+ * table is NaN, and the device status is set to LTK_ERR_ARG.  Rows of no
+ * sequence are left as they were.
+ */
+ltk_status ltk_kv_read(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const float* cos_table,
+                       const float* sin_table, int table_rows, int rot, int interleaved, void* k_out,
+                       void* v_out, void* stream);
+
 /* First error raised on the device by the handle's calls so far (0: none) and
  * clears it; synchronises the stream. */
 ltk_status ltk_kv_status(ltk_kv* h, int* device_status, void* stream);
+
+/*
+ * Draws a token for each row of logits from a given random number.
+ *   logits  device [B, V] of LTK_BF16, LTK_F16 or LTK_F32, rows row_stride
+ *           elements apart, aligned to their elements; up to 360,000 tokens of 32
+ *           bits or 720,000 of 16 (else LTK_ERR_UNSUPPORTED);
+ *   s       the settings, for each row (device pointers [B]) or, where a pointer
+ *           is NULL, one for all;
+ *   u       device fp32 [B]: random numbers in [0, 1);
+ *   token   device int32 [B];  logp  device fp32 [B]: the natural logarithm of the
+ *           token's probability among those it was drawn from.
+ * With w_i = exp((x_i - max x) / temperature) and tokens ordered by (x descending,
+ * index ascending), the following are left, each step among those of the one before:
+ *   min_p   those with w_i >= min_p (0: all);
+ *   top_k   the first top_k (0 or less, or V or more: all);
+ *   top_p   the fewest first ones whose weights sum to top_p of the total or
+ *           more, at least one (1 or more: all).
+ * The token is the first of these, in the order of indices, at which the running
+ * sum of weights exceeds u times their total (u below 0 counts as 0, from 1 on as
+ * the largest below 1).  Temperature 0 (and any below 2^-127) takes the largest
+ * logit, the first of equal ones, with logp 0.  Logits of -inf are never drawn; a row of nothing else gives
+ * -1 and -inf, a row with a NaN or +inf, or with a setting out of range
+ * (temperature below 0, infinite or NaN, top_p below 0 or NaN, min_p outside
+ * [0, 1], u NaN), -1 and NaN.
+ * Weights are whole numbers in units of 2^-44 of the largest, right to 2^-32 of
+ * themselves, their sums exact: a row's result depends on its logits and settings
+ * only.  Needs no handle or workspace, neither allocates nor synchronises.
+ */
+typedef struct {
+  const float* temperature;
+  const int* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all;
+  int top_k_all;
+  float top_p_all;
+  float min_p_all;
+} ltk_sampling;
+
+ltk_status ltk_sample_tokens(const void* logits, int dtype, long long row_stride, int B, int V,
+                             const ltk_sampling* s, const float* u, int* token, float* logp, void* stream);
 
 /* Statistics of the last compute call (synchronises its stream). */
 ltk_status ltk_get_stats(ltk_handle* h, ltk_stats* out);

@@ -131,6 +131,7 @@ struct Unit {
   int tile0;       // first tile of the unit's window
   int skip;        // tiles [0, skip) are the sinks'
   int b;
+  int page0;       // see KvSeq
 };
 
 // Where a cursor stands: unit u of its sequence, key tile t of n_tiles.
@@ -192,6 +193,7 @@ __device__ __forceinline__ void enter_seq(const AttnParams& p, Cursor& c, int b)
   c.w.nq = s.nq;
   c.w.pos0 = s.pos0;
   c.w.len = s.len;
+  c.w.page0 = s.page0;
   c.n_tiles = tiles_of(p, s, &c.w.skip, &c.w.tile0);
 }
 
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     } else {
       const int tile = pc.t < pc.w.skip ? pc.t : pc.t - pc.w.skip + pc.w.tile0;
       const int key0 = tile * kTileKeys + warp * kWarpKeys;
-      const int* table = p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width;
+      const int* table = p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + pc.w.page0;
 #pragma unroll
       for (int h = 0; h < kGroups; ++h)
         if (key0 + 16 * h < pc.w.len) feed.page[h] = kv_load(table + ((key0 + 16 * h) >> p.cache.page_log2));
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
 
   // Dense: rows of sequences whose queries see no token have no tile on the line.
   if constexpr (!SEL) {
-    for (long long n = blockIdx.x; n < p.batch.N; n += grid) {
+    for (long long n = blockIdx.x; n < p.batch.N && p.step != 1; n += grid) {
       const KvSeq s = kv_seq(p.batch, p.cache, kv_seq_of_query(p.batch, static_cast<int>(n)));
       if (s.len > 0 && n >= s.q0 && n < s.q0 + s.nq) continue;
       for (int i = tid; i < p.q_heads * D; i += kThreads) reinterpret_cast<uint16_t*>(p.out)[n * p.q_heads * D + i] = 0;
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
       const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       const float scale = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      const int pos = on ? (SEL ? head.w.pos0 : max(head.w.pos0 + qi, -1)) : -1;   // (from -1 any window is within 32 bits)
+      const int pos = on ? (SEL ? head.w.pos0 : max(head.w.pos0 + qi * p.batch.advance, -1)) : -1;   // (from -1 any window is within 32 bits)
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         crow[x][n] = __shfl_sync(0xFFFFFFFFu, scale, (2 * cq + n) * 4);
@@ -505,8 +507,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
 #pragma unroll
       for (int n = 0; n < 2; ++n) l[x][n] = !SEL && prow[x][n] >= head.w.len ? __int_as_float(0x7FC00000) : 0.f;
     }
-    const int p_lo = SEL ? 0 : head.w.pos0 + head.w.row0 / p.group;
-    const int p_hi = SEL ? 0 : head.w.pos0 + min(head.w.row0 + kRows - 1, rows_all - 1) / p.group;
+    const int p_lo = SEL ? 0 : head.w.pos0 + head.w.row0 / p.group * p.batch.advance;
+    const int p_hi = SEL ? 0 : head.w.pos0 + min(head.w.row0 + kRows - 1, rows_all - 1) / p.group * p.batch.advance;
     if (!SEL && p_hi >= head.w.len && tid == 0) raise_status(p.status, kDevArg);
 
 #pragma unroll 1
@@ -708,13 +710,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     auto write_row = [&](int r, int ch, float4 v, float m2, float sum) {
       const int row = head.w.row0 + r;
       const size_t at = (static_cast<size_t>(head.w.q0) + row / p.group) * p.q_heads + head.w.head * p.group + row % p.group;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const bool joined = !SEL && p.step == 2 && head.w.page0 > 0;
+      const RowEnd e = row_end(p, at, joined, m2 - kBoost, sum);
+      v = make_float4(v.x * e.own, v.y * e.own, v.z * e.own, v.w * e.own);
+      if (!SEL && p.step == 1) {
+        reinterpret_cast<float4*>(p.mid + at * D)[ch] = v;
+        if (ch == 0) p.mid_lse[at] = e.lse2;
+        return;
+      }
+      if (joined) {
+        const float4 o = kv_load(reinterpret_cast<const float4*>(p.mid + at * D) + ch);
+        v = make_float4(fmaf(o.x, e.mid, v.x), fmaf(o.y, e.mid, v.y), fmaf(o.z, e.mid, v.z), fmaf(o.w, e.mid, v.w));
+      }
       uint2 w;
-      w.x = kv_pack16(v.x * inv, v.y * inv, p.bf16);
-      w.y = kv_pack16(v.z * inv, v.w * inv, p.bf16);
+      w.x = kv_pack16(v.x, v.y, p.bf16);
+      w.y = kv_pack16(v.z, v.w, p.bf16);
       reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at * D)[ch] = w;
-      if (ch == 0 && p.lse != nullptr)
-        p.lse[at] = sum == 0.f ? -__int_as_float(0x7F800000) : (m2 - kBoost + log2f(sum)) * 0.69314718055994530942f;
+      if (ch == 0 && p.lse != nullptr) p.lse[at] = e.lse2 * 0.69314718055994530942f;
     };
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), ch = i % (D / 4);

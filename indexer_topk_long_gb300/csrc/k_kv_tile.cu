@@ -66,6 +66,7 @@ struct Unit {                            // a piece of a work unit
   int len;                               // cached tokens (listed: list length)
   int part;                              // -1: the whole unit; else its place in the workspace
   int c0, c1;                            // CTAs that hold the unit's pieces
+  int page0;                             // see KvSeq
 };
 
 struct Meta {                            // scales of a key tile's eight 16-key groups
@@ -131,7 +132,7 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
     u.q0 = n;
     u.pos0 = (n >= q.q0 && n < q.q0 + q.nq) ? q.pos0 + n - q.q0 : -1;
     u.p_lo = u.p_hi = u.pos0;
-    u.skip = u.tile0 = 0;
+    u.skip = u.tile0 = u.page0 = 0;
     u.len = a.k;
     tiles = (a.k + kKeys - 1) / kKeys;
     return tiles;
@@ -151,14 +152,15 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
     const long long row0 = (slot - slot_start(p, b)) * p.rows;
     const long long all = static_cast<long long>(q.nq) * a.group;
     tiles = 0;
-    if (row0 < 0 || row0 >= all) return 0;
+    if (row0 < 0 || row0 >= all || (a.step == 1 && q.len == 0)) return 0;   // (nothing shared: no first step)
     u.row0 = static_cast<int>(row0);
     u.rows = static_cast<int>(min(all - row0, static_cast<long long>(p.rows)));
     u.q0 = q.q0;
     u.pos0 = q.pos0;
-    u.p_lo = q.pos0 + u.row0 / a.group;
-    u.p_hi = q.pos0 + (u.row0 + u.rows - 1) / a.group;
+    u.p_lo = q.pos0 + u.row0 / a.group * a.batch.advance;
+    u.p_hi = q.pos0 + (u.row0 + u.rows - 1) / a.group * a.batch.advance;
     u.len = q.len;
+    u.page0 = q.page0;
     u.skip = u.tile0 = 0;
     const int last = min(u.p_hi, u.len - 1);                  // (queries past the table: see kv_seq)
     tiles = last >= 0 ? last / kKeys + 1 : 0;
@@ -661,7 +663,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       if (!warp_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
-      const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width;
+      const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width + u.page0;
       const int begin = u.first + set, end = u.first + u.n_tiles;
       constexpr int kStep = R::kSets;    // a set's tiles lie that far apart
       // A tile's lookups run ahead of its data, each a whole tile ahead of its use: its
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       const bool live = row < u.rows && (!twice || (r >> 6) == x);
       const bool warp_live = __any_sync(0xFFFFFFFFu, live);
       const int mine = pair ? (x == 0 || u.rows > kTileRows ? u.n_tiles : 0) : x == 0 ? (u.n_tiles + 1) >> 1 : u.n_tiles >> 1;
-      const int pos = live ? (SEL ? u.pos0 : max(u.pos0 + (u.row0 + row) / a.group, -1)) : -1;
+      const int pos = live ? (SEL ? u.pos0 : max(u.pos0 + (u.row0 + row) / a.group * a.batch.advance, -1)) : -1;
       float f = 0.f;                     // scores to base-2 exponents
       if (pair) {
         if (!warp_wait(smem_u32(&ctrl->qraw), un & 1, abort_flag, status)) break;
@@ -1054,15 +1056,35 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           const int qi = rr / a.group;
           at = (static_cast<size_t>(u.q0) + qi) * a.q_heads + u.head * a.group + (rr - qi * a.group);
         }
-        auto write_out = [&](int col, const float (&s)[32], float inv) {
+        const bool joined = !SEL && a.step == 2 && u.page0 > 0;
+        // 32 columns of the row's sums
+        auto write_out = [&](int col, float (&s)[32], const RowEnd& end) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) s[e] *= end.own;
+          if (!SEL && a.step == 1) {
+            float4* dst = reinterpret_cast<float4*>(a.mid + at * D + col);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
+            return;
+          }
+          if (joined) {
+            const float4* src = reinterpret_cast<const float4*>(a.mid + at * D + col);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 o = kv_load(src + e);
+              s[4 * e] = fmaf(o.x, end.mid, s[4 * e]);
+              s[4 * e + 1] = fmaf(o.y, end.mid, s[4 * e + 1]);
+              s[4 * e + 2] = fmaf(o.z, end.mid, s[4 * e + 2]);
+              s[4 * e + 3] = fmaf(o.w, end.mid, s[4 * e + 3]);
+            }
+          }
           uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + at * D + col);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(kv_pack16(s[8 * e] * inv, s[8 * e + 1] * inv, a.bf16),
-                                kv_pack16(s[8 * e + 2] * inv, s[8 * e + 3] * inv, a.bf16),
-                                kv_pack16(s[8 * e + 4] * inv, s[8 * e + 5] * inv, a.bf16),
-                                kv_pack16(s[8 * e + 6] * inv, s[8 * e + 7] * inv, a.bf16));
+            dst[e] = make_uint4(kv_pack16(s[8 * e], s[8 * e + 1], a.bf16), kv_pack16(s[8 * e + 2], s[8 * e + 3], a.bf16),
+                                kv_pack16(s[8 * e + 4], s[8 * e + 5], a.bf16), kv_pack16(s[8 * e + 6], s[8 * e + 7], a.bf16));
         };
+        RowEnd end{};
         for (int h = 0; h < (merged ? rounds : 1) && ok; ++h) {
           const int cols = merged ? D / rounds : D;
           if (merged) {
@@ -1077,7 +1099,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
               l = l * by0 + l1 * by1;
             }
           }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
+          if (h == 0 && live && !part) end = row_end(a, at, joined, M - kBoost, l);
           if (warp_live) {
 #pragma unroll 1
             for (int c = 0; c < cols / 32; ++c) {
@@ -1108,7 +1130,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
                   for (int e = 0; e < 8; ++e)
                     __stcg(dst + static_cast<size_t>(e) * rows_max, make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]));
                 } else {
-                  write_out(col, s, inv);
+                  write_out(col, s, end);
                 }
               }
             }
@@ -1117,11 +1139,12 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           if (merged && lane == 0) mbar_arrive(smem_u32(&ctrl->mempty));
         }
         if (!ok) break;
-        auto write_lse = [&](float m2, float sum) {
-          if (a.lse != nullptr) a.lse[at] = sum == 0.f ? -inf : (m2 - kBoost + log2f(sum)) * 0.69314718055994530942f;
+        auto write_lse = [&](float lse2) {
+          if (!SEL && a.step == 1) a.mid_lse[at] = lse2;
+          else if (a.lse != nullptr) a.lse[at] = lse2 * 0.69314718055994530942f;
         };
         if (!part) {
-          if (live) write_lse(M, l);
+          if (live) write_lse(end.lse2);
         } else {
           if (live) __stcg(reinterpret_cast<float2*>(pd) + row, make_float2(M, l));
           // the last of the unit's CTAs joins the pieces in their order
@@ -1149,7 +1172,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
               sum = sum * exp2_approx(top - next) + v.y * exp2_approx(v.x - next);
               top = next;
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            end = row_end(a, at, joined, top - kBoost, sum);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float s[32];
@@ -1169,9 +1192,9 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
                   s[4 * e + 3] = fmaf(v.w, by, s[4 * e + 3]);
                 }
               }
-              write_out(32 * c, s, inv);
+              write_out(32 * c, s, end);
             }
-            write_lse(top, sum);
+            write_lse(end.lse2);
           }
         }
       }
@@ -1181,7 +1204,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
     }
     // dense: queries that belong to no sequence have no unit
     if constexpr (!SEL) {
-      if (x == 1) {
+      if (x == 1 && a.step != 1) {
         constexpr int kMine = 32 * R::kStreamWarps;             // this stream's threads
         for (long long n = blockIdx.x * static_cast<long long>(kMine) + (r & (kMine - 1)); n < a.batch.N;
              n += gridDim.x * static_cast<long long>(kMine)) {
@@ -1241,7 +1264,7 @@ cudaError_t kv_tile_init() {
 bool kv_tile_pairs(const AttnParams& a, int max_q, int num_sms) {
   double keys = static_cast<double>(a.batch.width) * a.cache.page;
   if (a.window > 0) keys = fmin(keys, static_cast<double>(a.window) + a.sinks + max_q);
-  const double pairs = a.cache.heads * (static_cast<double>(a.batch.N) * a.group / (2 * kTileRows) + 0.5 * a.batch.B);
+  const double pairs = a.cache.heads * (static_cast<double>(a.batch.N) * a.group / (2 * kTileRows) + 0.5 * a.units);
   return static_cast<long long>(a.group) * max_q > kTileRows && pairs * (keys / kKeys) >= 14.0 * num_sms;
 }
 

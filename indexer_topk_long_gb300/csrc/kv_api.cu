@@ -12,19 +12,7 @@
 
 using namespace ltk;
 
-struct ltk_kv {
-  KvCache cache;
-  int dim = 0;
-  int engine = 0;
-  int device = 0;
-  int num_sms = 0;
-  float* part = nullptr;
-  int* counters = nullptr;
-  int num_counters = 0;
-  int* status = nullptr;
-};
-
-namespace {
+namespace ltk {
 
 ltk_status kv_cuda_fail(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return LTK_OK;
@@ -33,10 +21,7 @@ ltk_status kv_cuda_fail(cudaError_t e, const char* what) {
   return e == cudaErrorMemoryAllocation ? LTK_ERR_NOMEM : LTK_ERR_CUDA;
 }
 
-bool kv_aligned(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool kv_aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-ltk_status check_batch(const ltk_kv* h, const ltk_kv_batch* b) {
+ltk_status kv_check_batch(const ltk_kv* h, const ltk_kv_batch* b) {
   if (h == nullptr || b == nullptr) return LTK_ERR_ARG;
   if (b->B < 0 || b->N < 0 || b->table_width < 0) return LTK_ERR_ARG;
   if (b->N == 0) return LTK_OK;
@@ -47,6 +32,10 @@ ltk_status check_batch(const ltk_kv* h, const ltk_kv_batch* b) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev != h->device) return LTK_ERR_ARG;
   return LTK_OK;
 }
+
+}  // namespace ltk
+
+namespace {
 
 // Rows of 16-bit elements, each row a whole number of 16-byte pieces.
 bool rows_ok(const void* p, long long stride, int heads, int dim) {
@@ -80,7 +69,7 @@ bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
   // units of r rows: every query its own (listed), or every sequence's queries, at least one
   auto units = [&](double r) {
     if (p.idx != nullptr) return p.batch.N * std::ceil(p.group / r);
-    return std::max<double>(p.batch.B, static_cast<double>(p.batch.N) * p.group / r + 0.5 * p.batch.B);
+    return std::max<double>(p.units, static_cast<double>(p.batch.N) * p.group / r + 0.5 * p.units);
   };
   const bool wide = p.dim == 128;
   const double by_rows = units(16) * (wide ? 2.0 + 0.75 * T : 1.4 + 0.51 * T);
@@ -96,11 +85,48 @@ bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
   return p.cache.heads * (by_rows - by_tiles) <= start * num_sms;
 }
 
-KvBatch batch_of(const ltk_kv_batch* b) {
-  return KvBatch{b->page_table, b->seq_lens, b->cu_q, b->table_width, b->B, b->N};
+}  // namespace
+
+namespace ltk {
+
+ltk_status kv_attention_params(const ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q, long long q_stride,
+                               int q_heads, int max_q, float scale, AttnParams* p) {
+  const ltk_status s = kv_check_batch(h, batch);
+  if (s != LTK_OK) return s;
+  if (dtype != LTK_BF16 && dtype != LTK_F16) return LTK_ERR_ARG;
+  if (q_heads < 1 || q_heads % h->cache.heads != 0) return LTK_ERR_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return LTK_ERR_ARG;
+  if (max_q < 0) return LTK_ERR_ARG;
+  if (q_heads > (1 << 20) || static_cast<long long>(batch->N) * (q_heads / h->cache.heads) > INT_MAX / 2)
+    return LTK_ERR_UNSUPPORTED;
+  *p = AttnParams{};
+  if (batch->N == 0) return LTK_OK;
+  if (!rows_ok(q, q_stride, q_heads, h->dim)) return LTK_ERR_ARG;
+  p->cache = h->cache;
+  p->batch = kv_batch_of(batch);
+  p->dim = h->dim;
+  p->bf16 = dtype == LTK_BF16;
+  p->q = q;
+  p->q_stride = q_stride;
+  p->q_heads = q_heads;
+  p->group = q_heads / h->cache.heads;
+  p->scale_log2 = scale * 1.44269504088896340736f;
+  p->units = batch->B;
+  p->part = h->part;
+  p->counters = h->counters;
+  p->status = h->status;
+  return LTK_OK;
 }
 
-}  // namespace
+cudaError_t kv_launch_attention(const ltk_kv* h, const AttnParams& p, int max_q, cudaStream_t stream) {
+  const int most_q = max_q > 0 ? max_q : p.batch.N;
+  const bool by_rows = h->engine == 0 ? kv_use_rows(p, most_q, h->num_sms) : h->engine == 1;
+  if (by_rows) return launch_kv_rows(p, most_q, h->num_sms, stream);
+  return p.idx != nullptr && p.group <= kListRows ? launch_kv_list(p, h->num_sms, stream)
+                                                  : launch_kv_tile(p, most_q, h->num_sms, stream);
+}
+
+}  // namespace ltk
 
 extern "C" {
 
@@ -164,7 +190,7 @@ ltk_status ltk_kv_append(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const 
                          const void* v, long long v_stride, const float* cos_table, const float* sin_table,
                          int table_rows, int rot, int interleaved, const void* q, long long q_stride, int q_heads,
                          void* q_out, void* stream) {
-  const ltk_status s = check_batch(h, batch);
+  const ltk_status s = kv_check_batch(h, batch);
   if (s != LTK_OK) return s;
   if (dtype != LTK_BF16 && dtype != LTK_F16) return LTK_ERR_ARG;
   if ((cos_table == nullptr) != (sin_table == nullptr)) return LTK_ERR_ARG;
@@ -181,7 +207,7 @@ ltk_status ltk_kv_append(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const 
   if (q != nullptr && (!rows_ok(q, q_stride, q_heads, h->dim) || !kv_aligned(q_out))) return LTK_ERR_ARG;
   AppendParams p{};
   p.cache = h->cache;
-  p.batch = batch_of(batch);
+  p.batch = kv_batch_of(batch);
   p.dim = h->dim;
   p.bf16 = dtype == LTK_BF16;
   p.k = k;
@@ -206,44 +232,20 @@ ltk_status ltk_kv_append(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const 
 static ltk_status kv_attend(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q, long long q_stride,
                             int q_heads, int max_q, float scale, int window, int sinks, const int* idx, int k,
                             void* out, float* lse, void* stream) {
-  const ltk_status s = check_batch(h, batch);
+  AttnParams p;
+  const ltk_status s = kv_attention_params(h, batch, dtype, q, q_stride, q_heads, max_q, scale, &p);
   if (s != LTK_OK) return s;
-  if (dtype != LTK_BF16 && dtype != LTK_F16) return LTK_ERR_ARG;
-  if (q_heads < 1 || q_heads % h->cache.heads != 0) return LTK_ERR_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return LTK_ERR_ARG;
-  if (window < 0 || sinks < 0 || max_q < 0) return LTK_ERR_ARG;
-  if (q_heads > (1 << 20) || static_cast<long long>(batch->N) * (q_heads / h->cache.heads) > INT_MAX / 2)
-    return LTK_ERR_UNSUPPORTED;
+  if (window < 0 || sinks < 0) return LTK_ERR_ARG;
   if (batch->N == 0) return LTK_OK;
-  if (!rows_ok(q, q_stride, q_heads, h->dim) || !kv_aligned(out)) return LTK_ERR_ARG;
+  if (!kv_aligned(out)) return LTK_ERR_ARG;
   if (lse != nullptr && !kv_aligned4(lse)) return LTK_ERR_ARG;
-  AttnParams p{};
-  p.cache = h->cache;
-  p.batch = batch_of(batch);
-  p.dim = h->dim;
-  p.bf16 = dtype == LTK_BF16;
-  p.q = q;
-  p.q_stride = q_stride;
-  p.q_heads = q_heads;
-  p.group = q_heads / h->cache.heads;
-  p.scale_log2 = scale * 1.44269504088896340736f;
   p.window = std::min(window, kKvMaxPos);
   p.sinks = sinks;
   p.idx = idx;
   p.k = k;
   p.out = out;
   p.lse = lse;
-  p.part = h->part;
-  p.counters = h->counters;
-  p.status = h->status;
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int most_q = max_q > 0 ? max_q : batch->N;
-  const bool by_rows = h->engine == 0 ? kv_use_rows(p, most_q, h->num_sms) : h->engine == 1;
-  const bool by_list = idx != nullptr && p.group <= kListRows;
-  const cudaError_t e = by_rows   ? launch_kv_rows(p, most_q, h->num_sms, st)
-                        : by_list ? launch_kv_list(p, h->num_sms, st)
-                                  : launch_kv_tile(p, most_q, h->num_sms, st);
-  return kv_cuda_fail(e, "kv attention");
+  return kv_cuda_fail(kv_launch_attention(h, p, max_q, static_cast<cudaStream_t>(stream)), "kv attention");
 }
 
 ltk_status ltk_kv_attention(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q, long long q_stride,

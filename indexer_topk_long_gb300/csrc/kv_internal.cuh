@@ -47,6 +47,11 @@ struct KvBatch {
   int width;
   int B;
   int N;
+  // Attention in two steps (see AttnParams::step): tokens at each sequence's start that are left
+  // out, whole pages (null: none), and how far a query's position lies behind the one before: 1, or
+  // 0 where every query of a sequence sees all of its keys.
+  const int* start;
+  int advance;
 };
 
 // A load that sees what the kernel before on the stream wrote.  Kernels here start while that one
@@ -58,17 +63,21 @@ __device__ __forceinline__ T kv_load(const T* p) { return *p; }
 // Queries [q0, q0 + nq) of sequence b, the position of its first query, and how many of its
 // tokens have a column in the page table.  cu_q is clamped to the batch.  A sequence that is
 // longer than its table has queries at positions len and beyond.
+// With left-out tokens, lengths and positions count from the first one that is not.
 struct KvSeq {
   int q0, nq, len, pos0;
+  int page0;                             // column of the page table that holds position 0
 };
 __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int b) {
   KvSeq s;
   s.q0 = min(max(kv_load(bt.cu_q + b), 0), bt.N);
   s.nq = min(max(kv_load(bt.cu_q + b + 1), s.q0), bt.N) - s.q0;
-  const long long room = min(static_cast<long long>(bt.width) << c.page_log2, static_cast<long long>(kKvMaxPos));
-  const int tokens = max(kv_load(bt.seq_lens + b), 0);
+  const int start = bt.start != nullptr ? kv_load(bt.start + b) : 0;
+  const long long room = min(static_cast<long long>(bt.width) << c.page_log2, static_cast<long long>(kKvMaxPos)) - start;
+  const int tokens = max(kv_load(bt.seq_lens + b), 0) - start;
   s.len = static_cast<int>(min(static_cast<long long>(tokens), room));
-  s.pos0 = tokens - s.nq;                // negative when a sequence is shorter than its queries
+  s.pos0 = tokens - (bt.advance ? s.nq : 1);                  // negative when a sequence is shorter than its queries
+  s.page0 = start >> c.page_log2;
   return s;
 }
 
@@ -164,6 +173,41 @@ struct AppendParams {
 };
 cudaError_t launch_kv_append(const AppendParams& p, int num_sms, cudaStream_t stream);
 
+struct ReadParams {
+  KvCache cache;
+  KvBatch batch;                         // cu_q: the rows of each sequence's last tokens
+  int dim;
+  int bf16;
+  const float* cos;                      // [table_rows, rot / 2], null: keys as they are held
+  const float* sin;
+  int rot;
+  int table_rows;
+  int interleaved;
+  void* k_out;                           // [N, heads, dim] contiguous
+  void* v_out;
+  int* status;
+};
+cudaError_t launch_kv_read(const ReadParams& p, int num_sms, cudaStream_t stream);
+
+// What sequences share (k_kv_share.cu): from the page tables to the two batches of an attention in
+// two steps.  All arrays are of the workspace.
+struct ShareParams {
+  KvCache cache;
+  KvBatch batch;
+  const int* groups;                     // [num_groups + 1] first sequence of each, null: one group of all
+  int num_groups;
+  int* common;                           // [B] pages in common with the group's first sharing sequence
+  int* lead;                             // [num_groups] that sequence
+  int* least;                            // [num_groups] pages that all sharing sequences have in common
+  int* sharing;                          // [num_groups] how many these are
+  int* start;                            // [B] second step: tokens left out
+  int* lens;                             // [B] first step: the lead's shared tokens, others 0
+  int* cu;                               // [B + 1] first step: all of a group's queries are its lead's
+  int* counter;                          // zero between calls
+  int* status;
+};
+cudaError_t launch_kv_share(const ShareParams& p, cudaStream_t stream);
+
 struct AttnParams {
   KvCache cache;
   KvBatch batch;
@@ -180,10 +224,39 @@ struct AttnParams {
   int k;
   void* out;                             // [N, q_heads, dim]
   float* lse;                            // [N, q_heads] or null
+  // Attention in two steps, over keys that sequences share and over each one's own: the first
+  // leaves its results here in fp32, the second joins them with its own.
+  int step;                              // 0: all at once, 1: the first, 2: the second
+  float* mid;                            // [N, q_heads, dim]
+  float* mid_lse;                        // [N, q_heads], base 2
+  int units;                             // sequences that have queries, for the choice of kernel
   float* part;                           // workspace: partial results
   int* counters;                         // workspace: zero between calls
   int* status;
 };
+
+// What turns a row's sum over values into its result: result = own * (weighted sum) + mid * (the
+// first step's result).  m2, sum: base-2 maximum and sum of weights; at: the row's place.
+struct RowEnd {
+  float own, mid;
+  float lse2;                            // base-2 logarithm of the sum of exponentials
+};
+__device__ __forceinline__ RowEnd row_end(const AttnParams& p, size_t at, bool joined, float m2, float sum) {
+  RowEnd e;
+  e.own = sum == 0.f ? 0.f : 1.f / sum;
+  e.lse2 = sum == 0.f ? -__int_as_float(0x7F800000) : m2 + log2f(sum);
+  e.mid = 0.f;
+  if (joined) {
+    const float before = kv_load(p.mid_lse + at), top = fmaxf(before, e.lse2);
+    if (top > -__int_as_float(0x7F800000)) {
+      const float a = exp2_approx(before - top), b = exp2_approx(e.lse2 - top), by = 1.f / (a + b);
+      e.mid = a * by;
+      e.own *= b * by;
+      e.lse2 = top + log2f(a + b);
+    }
+  }
+  return e;
+}
 
 // Attention for few rows per KV head (k_kv_rows.cu).
 constexpr int kRowsPerUnit = 16;
@@ -206,5 +279,35 @@ size_t kv_list_part_floats(int num_sms);
 int kv_list_counters(int num_sms);
 cudaError_t kv_list_init();
 cudaError_t launch_kv_list(const AttnParams& p, int num_sms, cudaStream_t stream);
+}  // namespace ltk
+
+struct ltk_kv {
+  ltk::KvCache cache;
+  int dim = 0;
+  int engine = 0;
+  int device = 0;
+  int num_sms = 0;
+  float* part = nullptr;
+  int* counters = nullptr;
+  int num_counters = 0;
+  int* status = nullptr;
+};
+
+namespace ltk {
+
+// What the entry points share (kv_api.cu).
+ltk_status kv_cuda_fail(cudaError_t e, const char* what);
+ltk_status kv_check_batch(const ltk_kv* h, const ltk_kv_batch* b);
+// Checks of an attention call and its parameters, all but the results' places; LTK_OK with
+// p->batch.N 0: nothing to do.
+ltk_status kv_attention_params(const ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q, long long q_stride,
+                               int q_heads, int max_q, float scale, AttnParams* p);
+// Chooses the kernel and starts it.
+cudaError_t kv_launch_attention(const ltk_kv* h, const AttnParams& p, int max_q, cudaStream_t stream);
+inline bool kv_aligned(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool kv_aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline KvBatch kv_batch_of(const ltk_kv_batch* b) {
+  return KvBatch{b->page_table, b->seq_lens, b->cu_q, b->table_width, b->B, b->N, nullptr, 1};
+}
 
 }  // namespace ltk

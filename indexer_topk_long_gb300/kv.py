@@ -5,6 +5,8 @@ over the ``ltk_kv_*`` entry points (argument checks and marshalling only).
     q = cache.append(k, v, page_table, seq_lens, cu_q, cos, sin, q=q)      # rotate, quantise, store
     out, lse = cache.attention(q, page_table, seq_lens, cu_q)              # causal, optional window
     out, lse = cache.attention_selected(q, idx, page_table, seq_lens, cu_q)  # the indexer's keys
+    out, lse = cache.attention_shared(q, page_table, seq_lens, cu_q)       # common first pages read once
+    k, v = cache.read(page_table, seq_lens, cu_q, n)                       # back in 16 bits
 
 The batch is three int32 CUDA tensors: ``page_table`` [B, width], ``seq_lens``
 [B] (cached tokens, this step's among them) and ``cu_q`` [B + 1] (first new
@@ -134,6 +136,7 @@ class PagedKVCache:
         self._codes = {torch.bfloat16: LTK_BF16, torch.float16: LTK_F16}
         self._append, self._attend = self.lib.ltk_kv_append, self.lib.ltk_kv_attention
         self._attend_selected = self.lib.ltk_kv_attention_selected
+        self._attend_shared, self._read = self.lib.ltk_kv_attention_shared, self.lib.ltk_kv_read
         codes, scales = (self.num_pages, self.heads, self.page, self.dim), (self.num_pages, self.heads)
         if not all(given):
             k_codes, v_codes = (torch.zeros(codes, dtype=torch.uint8, device=self.device) for _ in range(2))
@@ -310,6 +313,77 @@ class PagedKVCache:
         if failed:
             ltk._check(failed, "ltk_kv_attention_selected")
         return out, lse
+
+    def attention_shared(self, q, page_table, seq_lens, cu_q, groups=None, max_q: int | None = None,
+                         scale: float | None = None, out=None, lse=None, stream=None):
+        """``attention`` without a window for sequences that begin with the same pages: what a
+        group of consecutive sequences has in common is found in the page table and read once
+        for all of its queries.  ``groups`` [G + 1] (int32) holds the first sequence of each group
+        and, at the end, B; None makes one group of all.  Returns (out, lse)."""
+        n, int32 = q.shape[0], self._int32
+        B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, int32)
+        heads, qs = self._queries(q, n)
+        G = 0
+        if groups is not None:
+            if len(groups.shape) != 1 or not 2 <= groups.shape[0] <= B + 1:
+                _fail("groups", f"expected 2 to {B + 1} first sequences, got shape {tuple(groups.shape)}")
+            _ints(groups, "groups", tuple(groups.shape), self.device)
+            G = groups.shape[0] - 1
+        if max_q is None:
+            max_q = -(-n // max(B, 1))
+        if max_q >> 31:
+            _int32s(max_q=max_q)
+        if stream is None and self.h is not None:
+            st = self._raw_stream(self._index)
+        else:
+            st = self._begin(stream, q, page_table, seq_lens, cu_q, groups, out, lse)
+        out, lse = self._outputs(stream, q, n, heads, out, lse)
+        size = ctypes.c_ulonglong(0)
+        ltk._check(self.lib.ltk_kv_shared_bytes(self.h, B, n, heads, ctypes.byref(size)), "ltk_kv_shared_bytes")
+        space = self._new(stream, (size.value,), self._torch.uint8)
+        failed = self._attend_shared(
+            self.h, batch, None if groups is None else groups.data_ptr(), G, self._codes[q.dtype], q.data_ptr(), qs, heads,
+            max_q, self._default_scale if scale is None else float(scale), out.data_ptr(), lse.data_ptr(), space.data_ptr(),
+            size.value, st)
+        if failed:
+            ltk._check(failed, "ltk_kv_attention_shared")
+        return out, lse
+
+    def read(self, page_table, seq_lens, cu, n: int, dtype=None, cos=None, sin=None, interleaved: bool = False,
+             k_out=None, v_out=None, stream=None):
+        """Tokens back in 16 bits: of each sequence the last cu[b + 1] - cu[b], ``n`` in all (cu[B]; the host
+        does not look).  With cos, sin keys are rotated back by their positions' rows.  Returns k, v
+        [n, heads, dim] of ``dtype`` (bfloat16 by default)."""
+        n, device = int(n), self.device
+        _int32s(n=n)
+        if n < 0:
+            _fail("n", f"expected the number of tokens, got {n}")
+        B, batch = _batch(page_table, seq_lens, cu, n, device, self._int32)
+        rot = rows = 0
+        if (cos is None) != (sin is None):
+            raise ValueError("cos, sin: give both or neither")
+        if cos is not None:
+            table, f32 = cos.shape, self._float32
+            if len(table) != 2 or sin.shape != table or cos.dtype is not f32 or sin.dtype is not f32 \
+                    or not (cos.is_contiguous() and sin.is_contiguous()):
+                raise ValueError("cos, sin: expected contiguous float32 tables of equal shape [positions, rot / 2]")
+            _device_ok(cos, "cos", device)
+            _device_ok(sin, "sin", device)
+            rows, rot = table[0], 2 * table[1]
+        if dtype is None:
+            dtype = self._torch.bfloat16 if k_out is None else k_out.dtype
+        if dtype not in self._codes:
+            _fail("dtype", f"expected bfloat16 or float16, got {dtype}")
+        shape = (n, self.heads, self.dim)
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() or t.device != device):
+                _fail(name, f"expected a contiguous {dtype} tensor of shape {shape} on {device}")
+        st = self._begin(stream, page_table, seq_lens, cu, cos, sin, k_out, v_out)
+        k_out = self._new(stream, shape, dtype) if k_out is None else k_out
+        v_out = self._new(stream, shape, dtype) if v_out is None else v_out
+        ltk._check(self._read(self.h, batch, self._codes[dtype], ltk._ptr(cos), ltk._ptr(sin), rows, rot,
+                              1 if interleaved else 0, k_out.data_ptr(), v_out.data_ptr(), st), "ltk_kv_read")
+        return k_out, v_out
 
     def status(self, stream=None) -> int:
         """First error the device raised since the last call (0: none); synchronises the stream."""

@@ -15,7 +15,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 HEADER = os.path.join(ROOT, "include", "ltk.h")
 
-LTK_BF16, LTK_FP8_E4M3, LTK_F16 = 0, 1, 2
+LTK_BF16, LTK_FP8_E4M3, LTK_F16, LTK_F32 = 0, 1, 2, 3
 STATUS = {0: "LTK_OK", 1: "LTK_ERR_ARG", 2: "LTK_ERR_CUDA", 3: "LTK_ERR_NOMEM",
           4: "LTK_ERR_OVERFLOW", 5: "LTK_ERR_TIMEOUT", 6: "LTK_ERR_UNSUPPORTED"}
 
@@ -62,6 +62,12 @@ class KvBatch(ctypes.Structure):
                 ("N", ctypes.c_int)]
 
 
+class Sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
@@ -90,7 +96,12 @@ _SIGS = {
     "ltk_kv_attention": (_I, [_P, _P, _I, _P, _LL, _I, _I, _F, _I, _I, _P, _P, _P]),
     "ltk_kv_attention_selected": (_I, [_P, _P, _I, _P, _LL, _I, _P, _I, _F, _P, _P,
                                        _P]),
+    "ltk_kv_attention_shared": (_I, [_P, _P, _P, _I, _I, _P, _LL, _I, _I, _F, _P, _P, _P,
+                                     ctypes.c_ulonglong, _P]),
+    "ltk_kv_shared_bytes": (_I, [_P, _I, _I, _I, ctypes.POINTER(ctypes.c_ulonglong)]),
+    "ltk_kv_read": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P]),
     "ltk_kv_status": (_I, [_P, ctypes.POINTER(_I), _P]),
+    "ltk_sample_tokens": (_I, [_P, _I, _LL, _I, _I, _P, _P, _P, _P, _P]),
 }
 
 _LIB = None
