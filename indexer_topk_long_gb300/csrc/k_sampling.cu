@@ -38,7 +38,7 @@ constexpr int kList = 2048;              // elements that one CTA sorts
 constexpr int kUnitBits = 44;            // weights are in units of 2^-44
 constexpr uint32_t kNoCut = 0xFFFFFFFFu;
 
-// 2^(j / 256) in units of 2^-31, rounded: by the exponential series in double, at compile time.
+// 2^(j / 256) in units of 2^-30, rounded: by the exponential series in double, at compile time.
 struct PowTable {
   uint32_t v[256];
 };
@@ -51,7 +51,7 @@ constexpr PowTable make_pow_table() {
       term *= z / i;
       sum += term;
     }
-    t.v[j] = static_cast<uint32_t>(sum * 2147483648.0 + 0.5);
+    t.v[j] = static_cast<uint32_t>(sum * 1073741824.0 + 0.5);
   }
   return t;
 }
@@ -60,7 +60,7 @@ __device__ constexpr PowTable kPow = make_pow_table();
 struct Shared {
   uint32_t pow[256];
   // what the CTAs of a cluster tell one another, by rank; two sets in turn where there is a next time
-  float top[kMaxCtas], bound[kMaxCtas];
+  float top[kMaxCtas], bound[2][kMaxCtas];
   int bad[kMaxCtas];
   unsigned long long mass[2][kMaxCtas];
   float lo[2][kMaxCtas], hi[2][kMaxCtas];
@@ -72,6 +72,8 @@ struct Shared {
   uint32_t warp_n[kWarps];
   uint32_t listed;
   uint32_t found;
+  float reached[2];
+  float min_hi, min_lo;                  // T ln(min_p)
   unsigned long long found_before;
   union {
     struct {
@@ -103,26 +105,73 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[16 / sizeof(E)
   }
 }
 
-// Weights.  (x - max) * c in two fp32 numbers, its nearest multiple of 1/256 by the table and the
-// rest, at most 2^-9 + 2^-30, by three terms of the series (the fourth is below 2^-42).
-struct Weigher {
-  float m, ch, cl;                       // the row's maximum; log2(e) / T
-  const uint32_t* pow;
-  __device__ __forceinline__ unsigned long long operator()(float x) const {
-    const float s = x - m, b = s - x;    // s + e = x - m exactly
-    const float e = (x - (s - b)) + (-m - b);
-    const float yh = s * ch;
-    if (!(yh > -46.f)) return 0;
-    const float yl = fmaf(s, ch, -yh) + fmaf(s, cl, e * ch);
-    const float t = fmaf(yh, 256.f, 12582912.f);
-    const int k = __float_as_int(t) - 0x4B400000;
-    const float r = fmaf(t - 12582912.f, -1.f / 256.f, yh) + yl;
-    const float q = r * fmaf(r, fmaf(r, 0.05550410866f, 0.2402265070f), 0.6931471806f);
-    const uint32_t p = pow[k & 255];
-    const uint32_t w = p + __float2int_rn(__uint2float_rn(p) * q);
-    return (static_cast<unsigned long long>(w) << (kUnitBits - 31)) >> -(k >> 8);
+// The largest of many elements, two at a time where they are of 16 bits; NaN if any is.
+template <typename E>
+struct Largest {
+  uint32_t v = std::is_same<E, float>::value ? 0xFF800000u : std::is_same<E, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+  __device__ __forceinline__ void one(uint32_t w) {
+    if constexpr (std::is_same<E, float>::value) {
+      float m = __uint_as_float(v);
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(__uint_as_float(w)));
+      v = __float_as_uint(m);
+    }
+    else if constexpr (std::is_same<E, __half>::value) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(v) : "r"(w));
+    else asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(w));
+  }
+  __device__ __forceinline__ void add(const uint4& w) {
+    one(w.x);
+    one(w.y);
+    one(w.z);
+    one(w.w);
+  }
+  __device__ __forceinline__ float get() const {
+    if constexpr (std::is_same<E, float>::value) return __uint_as_float(v);
+    const float2 f = kv_unpack16(v, std::is_same<E, __nv_bfloat16>::value);
+    return f.x != f.x || f.y != f.y ? __int_as_float(0x7FC00000) : fmaxf(f.x, f.y);
   }
 };
+
+// Weights: w = 2^(x c - top), top the whole number next above max c, so that the largest is in (1/2, 1].
+//
+// x c is rounded to a multiple of 1/256, whose power comes from the table; what is left, below 2^-9, is
+// fma(x, ch, -that) + x cl with one rounding of 2^-34, and three terms of its exponential series are within
+// 2^-42.  This holds while |x c| < 2^14.  Where max c is beyond 2^13, weights above 0 belong to x within 1% of
+// the maximum, whose difference from it is exact in fp32, and that takes the place of x.
+struct Weigher {
+  float ref, least;                      // subtracted from x; smaller x have no weight
+  float ch, cl;                          // log2(e) / T in two fp32 numbers
+  int top;
+  const uint32_t* pow;
+
+  __device__ __forceinline__ Weigher(float m, float T, const uint32_t* table) : pow(table) {
+    constexpr float kLog2e = 1.44269502162933349609375f, kRest = 1.92596299112661746887e-8f;
+    ch = kLog2e / T;
+    cl = (fmaf(-ch, T, kLog2e) + kRest) / T;
+    const bool far = !(fabsf(m * ch) < 8192.f);
+    ref = far ? m : 0.f;
+    top = far ? 0 : static_cast<int>(ceilf(m * ch));
+    // x c >= top - kUnitBits and a little: what is below rounds to 0 in any case
+    least = m - (kUnitBits + 1) / ch;
+  }
+  __device__ __forceinline__ unsigned long long operator()(float x) const {
+    const float s = x - ref;
+    const float t = fmaf(s, ch, 49152.f);                    // 1.5 * 2^15: its last bit is 1/256
+    const int k = __float_as_int(t) - 0x47400000;
+    const float r = fmaf(s, cl, fmaf(s, ch, 49152.f - t));
+    // 2^30 (2^r - 1), at most 2^21.4
+    const float q = r * fmaf(r, fmaf(r, 0x1p30f * 0.05550410866f, 0x1p30f * 0.2402265070f), 0x1p30f * 0.6931471806f);
+    const uint32_t p = pow[k & 255];
+    const float f = __uint_as_float((p >> 7) + 0x3F000000u); // p in units of 2^30, to 24 bits
+    const uint32_t w = p + (__float_as_uint(fmaf(f, q, 12582912.f)) - 0x4B400000u);
+    return x >= least ? (static_cast<unsigned long long>(w) << (kUnitBits - 30)) >> min(top - (k >> 8), 63) : 0ull;
+  }
+};
+
+// Whether element i comes before or at the one with key `cut`: ckey(x, i) >= cut.
+__device__ __forceinline__ bool not_before(float x, uint32_t i, unsigned long long cut) {
+  const float at = ckey_score(cut);
+  return x > at || (x == at && i <= static_cast<uint32_t>(ckey_idx(cut)));
+}
 
 __device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
 #pragma unroll
@@ -265,12 +314,12 @@ struct Row {
     for (int c = 0; c < ctas; ++c) n += sh.count[set][c];   // (of at most 2^20 elements)
     if (n > kList || ctas == 1) return n;
     if (rank == 0) {
-      uint32_t at = sh.count[set][0];
-      for (int c = 1; c < ctas; ++c) {
-        const unsigned long long* from = cluster.map_shared_rank(&sh, c)->list;
-        const uint32_t m = sh.count[set][c];
-        for (uint32_t i = tid; i < m; i += kThreads) sh.list[at + i] = from[i];
-        at += m;
+      const uint32_t own = sh.count[set][0];
+      for (uint32_t at = own + tid; at < n; at += kThreads) {
+        uint32_t i = at - own;
+        int c = 1;
+        while (i >= sh.count[set][c]) i -= sh.count[set][c++];
+        sh.list[at] = cluster.map_shared_rank(&sh, c)->list[i];
       }
     }
     cluster.sync();
@@ -315,7 +364,7 @@ struct Row {
       const float half = hi - lo < __int_as_float(0x7F800000) ? 1.f : 0.5f, range = half * hi - half * lo;
       const float up = range < 1e-30f ? 0x1p100f : 1.f, by = static_cast<float>(kBins) / (range * up);
       auto bin_at = [&](float x) { return min(__float2int_rz((half * hi - half * x) * up * by), kBins - 1); };
-      auto inside = [&](float x, uint32_t i) { return x >= lo && x <= hi && ckey(x, static_cast<int>(i)) >= cut; };
+      auto inside = [&](float x, uint32_t i) { return x >= lo && x <= hi && not_before(x, i, cut); };
       int bin = 0;
       if (lo < hi) {
         for (int i = tid; i < 3 * kBins; i += kThreads) sh.hist[i / kBins][i % kBins] = 0;
@@ -423,29 +472,65 @@ struct Row {
     }
   }
 
-  // A bound that at least k of this CTA's elements reach, by their threads' largest; -inf: none.
-  __device__ float reached_by(int k, float most) {
-    const uint32_t key = ord_f32(most) >> 12;
-    uint32_t at = 0;
+  // Bounds that at least need[0] and need[1] of this CTA's elements reach, by their threads' largest, at
+  // sh.reached; -inf: none.  Warps 0 and 1 look for them bit by bit, from the first in which they differ.
+  __device__ void reached_by(int need0, int need1, float most) {
+    uint32_t* keys = &sh.hist[0][0];
+    keys[tid] = ord_f32(most) >> 12;
+    __syncthreads();
+    if (warp < 2) {
+      const int need = warp == 0 ? need0 : need1;
+      uint32_t key[kThreads / 32], hi = 0, lo = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) {
+        key[i] = keys[i * 32 + lane];
+        hi = max(hi, key[i]);
+        lo = min(lo, key[i]);
+      }
+      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+      const int bits = 32 - __clz(hi ^ lo);
+      uint32_t at = hi >> bits << bits;
 #pragma unroll 1
-    for (int bit = 19; bit >= 0; --bit) {
-      const uint32_t next = at | (1u << bit);
-      if (__syncthreads_count(key >= next) >= k) at = next;
+      for (int bit = bits - 1; bit >= 0; --bit) {
+        const uint32_t next = at | (1u << bit);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) n += key[i] >= next ? 1 : 0;
+        if (__reduce_add_sync(0xFFFFFFFFu, n) >= need) at = next;
+      }
+      if (lane == 0)
+        sh.reached[warp] = at <= (ord_f32(-__int_as_float(0x7F800000)) >> 12) ? -__int_as_float(0x7F800000) : unord_f32(at << 12);
     }
-    return at <= (ord_f32(-__int_as_float(0x7F800000)) >> 12) ? -__int_as_float(0x7F800000) : unord_f32(at << 12);
+    __syncthreads();
   }
 };
 
-// The random number's place among `total` units of weight (u: at most the largest number below 1,
-// and total * u may be rounded up to total where that passes double's 53 bits).
-__device__ __forceinline__ unsigned long long place_of(float u, unsigned long long total) {
-  const unsigned long long at = static_cast<unsigned long long>(static_cast<double>(u) * static_cast<double>(total));
-  return at < total ? at : total - 1;
+// floor(u * total), 0 <= u < 1, in whole numbers (u is 24 bits times a power of two; the few double
+// units of an SM would hold up 512 threads); *exact: whether that is u * total.
+__device__ __forceinline__ unsigned long long part_of(float u, unsigned long long total, bool* exact) {
+  const uint32_t bits = __float_as_uint(u), e = bits >> 23;
+  const unsigned long long mantissa = (bits & 0x7FFFFFu) | (e > 0 ? 0x800000u : 0u);
+  const int shift = 150 - static_cast<int>(e > 0 ? e : 1);  // u = mantissa * 2^-shift, shift >= 24
+  const unsigned long long lo = mantissa * total, hi = __umul64hi(mantissa, total);
+  if (shift >= 64) {
+    const unsigned long long up = shift - 64 < 64 ? hi >> (shift - 64) : 0;
+    *exact = lo == 0 && (shift - 64 < 64 ? (hi & ((1ull << (shift - 64)) - 1)) == 0 : hi == 0);
+    return up;
+  }
+  *exact = (lo & ((1ull << shift) - 1)) == 0;
+  return (lo >> shift) | (hi << (64 - shift));
 }
-// The weight that a share p of `total` has to reach.
+// The random number's place among `total` units of weight.
+__device__ __forceinline__ unsigned long long place_of(float u, unsigned long long total) {
+  bool exact;
+  return part_of(u, total, &exact);
+}
+// The weight that a share p < 1 of `total` has to reach, at least 1.
 __device__ __forceinline__ unsigned long long share_of(float p, unsigned long long total) {
-  const unsigned long long t = static_cast<unsigned long long>(ceil(static_cast<double>(p) * static_cast<double>(total)));
-  return t < 1 ? 1 : t < total ? t : total;
+  bool exact;
+  const unsigned long long t = part_of(p, total, &exact) + (exact ? 0 : 1);
+  return t < 1 ? 1 : t;
 }
 
 // All that is kept is in the first CTA's list: filters, draw and results, by that CTA.
@@ -470,6 +555,22 @@ __device__ void finish_list(Row<E>& row, uint32_t n, int k, float top_p, float u
     // the kept ones' order in the vocabulary: the list's places, by index
     sh.weights[tid * P + e] = w[e];
     v[e] = w[e] != 0 ? (v[e] << 32) | static_cast<uint32_t>(tid * P + e) : 0;
+  }
+  if constexpr (P == 1) {
+    // few: each finds its own place, from the others' indices
+    constexpr int kFew = 64;
+    const int left = __syncthreads_count(w[0] != 0);         // (they are the first of the sorted)
+    if (left <= kFew) {
+      if (tid < left) sh.list[tid] = v[0];
+      const unsigned long long sum = row.block_total(w[0]), at = place_of(u, sum);
+      if (tid < left) {
+        unsigned long long before = 0;
+        for (int j = 0; j < left; ++j)
+          if (sh.list[j] > v[0]) before += sh.weights[j];    // (larger keys: smaller indices)
+        if (before <= at && at < before + w[0]) hit(0xFFFFFFFFu - static_cast<uint32_t>(v[0] >> 32), sum);
+      }
+      return;
+    }
   }
   __syncthreads();
   block_sort_regs<P, true>(v, sh.list);
@@ -507,6 +608,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
   const float given = kv_load(p.u + b), u = fminf(fmaxf(given, 0.f), 1.f - 0x1p-24f);
   const bool settings = T >= 0.f && T < inf && top_p >= 0.f && min_p >= 0.f && min_p <= 1.f && given == given;
   if (k < 0 || k >= p.V) k = 0;
+  if (tid == kThreads - 1 && min_p > 0.f) {
+    const double by = log(static_cast<double>(min_p)) * static_cast<double>(T);
+    sh.min_hi = static_cast<float>(by);
+    sh.min_lo = static_cast<float>(by - static_cast<double>(sh.min_hi));
+  }
 
   // --- the row's slice, and its largest ---------------------------------------------------
   // Pieces of 16 aligned bytes; elements before the row and behind it are -inf.
@@ -517,8 +623,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
   const int per_warp = (mine + kWarps - 1) / kWarps;
   Row<E> row{p, sh, slice, cluster, tid, lane, warp, rank, ctas, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
              first * VEC - shift};
-  float most = -inf;
-  bool bad = false;
+  Largest<E> largest;
   {
     constexpr int kUnroll = 4;
     const E* from = logits + row.index0;
@@ -553,21 +658,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
         const int i = i0 + 32 * j;
         if (i >= row.end) continue;
         slice[i] = v[j];
-        float x[VEC];
-        unpack<E>(v[j], x);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          bad = bad || !(x[e] < inf);    // a NaN or +inf
-          most = fmaxf(most, x[e]);
-        }
+        largest.add(v[j]);
       }
     }
   }
-  bad = __syncthreads_or(bad ? 1 : 0) != 0;
-  // Few enough are kept to be sorted by one CTA: all of a small vocabulary, or a small top-k, whose bound
-  // some k ctas / 0.87 elements reach (512 threads' largest, k of them above it).
-  const bool all_listed = p.V <= kList, few = k > 0 && k <= 384 && k * ctas <= 1024;
-  const float bound = few && !all_listed && !bad ? row.reached_by(k, most) : -inf;
+  const float most = largest.get();      // NaN if any element is
+  bool bad = __syncthreads_or(most < inf ? 0 : 1) != 0;
+  // Few enough are kept to be sorted by one CTA: all of a small vocabulary, or a small top-k.  For that each
+  // CTA finds what its share of k elements reach, and what k of them do: k elements of the row reach the least of
+  // the CTAs' former bounds, and any of the latter.
+  const bool all_listed = p.V <= kList, few = k > 0 && k <= kThreads / 2;
+  if (few && !all_listed) row.reached_by((k + ctas - 1) / ctas, k, bad ? -inf : most);
   float cta_most = most;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) cta_most = fmaxf(cta_most, __shfl_xor_sync(0xFFFFFFFFu, cta_most, o));
@@ -580,17 +681,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
     if (lane < ctas) {
       Shared* o = cluster.map_shared_rank(&sh, lane);
       o->top[rank] = cta_most;
-      o->bound[rank] = bound;
+      o->bound[0][rank] = few && !all_listed ? sh.reached[0] : -inf;
+      o->bound[1][rank] = few && !all_listed ? sh.reached[1] : -inf;
       o->bad[rank] = bad;
     }
   }
   cluster.sync();
-  float m = -inf, floor_x = -inf;
+  float m = -inf, floor_x = inf, by_one = -inf;
   for (int c = 0; c < ctas; ++c) {
     m = fmaxf(m, sh.top[c]);
-    floor_x = fmaxf(floor_x, sh.bound[c]);
+    floor_x = fminf(floor_x, sh.bound[0][c]);
+    by_one = fmaxf(by_one, sh.bound[1][c]);
     bad = bad || sh.bad[c] != 0;
   }
+  floor_x = fmaxf(floor_x, by_one);
   int* token = p.token + b;
   float* logp = p.logp + b;
   if (!settings || bad || m == -inf) {
@@ -611,19 +715,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
     }
     return;
   }
-  const double c = 1.4426950408889634 / static_cast<double>(T);
-  Weigher weigh{m, static_cast<float>(c), 0.f, sh.pow};
-  weigh.cl = static_cast<float>(c - static_cast<double>(weigh.ch));
+  const Weigher weigh(m, T, sh.pow);
   // the result: its logarithm from x itself, which small weights hold to a few bits only
   auto hit = [&](uint32_t i, unsigned long long total) {
-    const double x = static_cast<double>(as_float(kv_load(logits + i)));
+    const double x = static_cast<double>(as_float(kv_load(logits + i))) - static_cast<double>(weigh.ref);
     *token = static_cast<int>(i);
-    *logp = static_cast<float>((x - static_cast<double>(m)) * c * 0.6931471805599453 -
-                               log(static_cast<double>(total) * (1.0 / (1ull << kUnitBits))));
+    *logp = static_cast<float>(x / static_cast<double>(T) - log(static_cast<double>(total)) - (weigh.top - kUnitBits) * 0.69314718055994530942);
   };
   // min-p is a bound on x; -inf is never kept
   float least = -__int_as_float(0x7F7FFFFF);
-  if (min_p > 0.f) least = fmaxf(least, fminf(m, __double2float_ru(static_cast<double>(m) + log(static_cast<double>(min_p)) * static_cast<double>(T))));
+  if (min_p > 0.f) {
+    // max + T ln(min_p), rounded up: from two fp32 numbers by an exact sum
+    const float by = sh.min_hi, s = m + by, z = s - m, rest = ((m - (s - z)) + (by - z)) + sh.min_lo;
+    const float up = rest > 0.f ? nextafterf(s, inf) : s;
+    least = fmaxf(least, fminf(m, up));
+  }
   if (all_listed || few) {
     const float from = fmaxf(floor_x, least);
     const uint32_t n = row.gather(most >= from, [&](float x, uint32_t) { return x >= from; });
@@ -636,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
     }
   }
   unsigned long long cut = ckey(least, -1);                  // (index 2^32 - 1: all of equal value)
-  auto kept = [&](float x, uint32_t i) { return ckey(x, static_cast<int>(i)) >= cut; };
+  auto kept = [&](float x, uint32_t i) { return not_before(x, i, cut); };
   if (k > 0) {
     // how many there are, and the smallest
     uint32_t n = 0;
@@ -704,9 +810,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
     }
     const unsigned long long target = share_of(top_p, total);
     // n elements of less than (total - target) / n each cannot hold the rest, so the cut is above that
-    const double small = static_cast<double>(total - target) / n;
+    // (fp32 logarithms and products here are right to 2^-20, the bound is taken 2^-7 lower)
     float lo = fmaxf(least, ckey_score(cut));
-    if (small > 1.0) lo = fmaxf(lo, fminf(m, __double2float_rd(static_cast<double>(m) + (log2(small) - kUnitBits - 1e-6) / c)));
+    const float rest = static_cast<float>(total - target) / n;
+    if (rest > 1.f) lo = fmaxf(lo, fminf(m, weigh.ref + (weigh.top + log2f(rest) - kUnitBits - 0x1p-7f) / weigh.ch - 0x1p-20f * fabsf(weigh.ref)));
     cut = row.template select<true>(lo, m, cut, target, weigh);
   }
   row.find([&](float x, uint32_t i) { return kept(x, i) ? weigh(x) : 0ull; },
