@@ -6,88 +6,86 @@
 //   vocabulary, at which the running sum of kept weights exceeds u * total.
 //
 // Which token that is depends on sums over a whole vocabulary being right to far better than one
-// token's share, so weights are whole numbers in units of 2^-44 of the largest, right to 2^-32 of
-// themselves, and every sum of them is exact in 64 bits, in any order: the result does not depend
+// token's share, so weights are whole numbers in units of 2^-44 of (about) the largest, right to 2^-30.5 of
+// themselves (those below 2^-42 are nothing), and every sum of them is exact in 64 bits, in any order: the result does not depend
 // on how a row is split.  (fp32 weights would put one in a hundred draws from a flat vocabulary of
 // 100000 on the neighbouring token.)
 //
 // A cluster of 1 to 8 CTAs holds a row in its shared memory, so that logits are read once; what has
 // to be known of the whole row (maximum, counts, sums) goes from CTA to CTA through distributed
-// shared memory.  Small top-k: each thread's largest element gives a bound that k elements reach,
-// the few at or above it go to one CTA, which sorts them and finishes.  Else the cut is found by
-// histograms over ever smaller ranges of x, of counts (top-k) or weights (top-p), until what is
-// left can be sorted; the draw then takes one pass over the row.
+// shared memory.  Small top-k: each thread's largest element gives bounds that k elements reach, and
+// the few at or above them go to one CTA, which compares them with one another and finishes.  Else the cut is
+// found by histograms over ever smaller ranges of x, of counts (top-k) or weights (top-p), until one CTA can
+// take what is left; the draw then takes one pass over the row.
 #include <cooperative_groups.h>
 
 #include <atomic>
 
 #include "block_sort.cuh"
-#include "kv_internal.cuh"
+#include "kv_tensor.cuh"
 #include "sampling_internal.cuh"
 
 namespace ltk {
 namespace {
 
 namespace cg = cooperative_groups;
+using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
 constexpr int kBins = 1024;
-constexpr int kList = 2048;              // elements that one CTA sorts
+constexpr int kList = 1024;              // elements that one CTA takes
+constexpr int kPairs = 256;              // of them, that are all compared with one another
 constexpr int kUnitBits = 44;            // weights are in units of 2^-44
-constexpr uint32_t kNoCut = 0xFFFFFFFFu;
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 
-// 2^(j / 256) in units of 2^-30, rounded: by the exponential series in double, at compile time.
+// 2^(j / 512) in units of 2^-31, rounded: by the exponential series in double, at compile time.
 struct PowTable {
-  uint32_t v[256];
+  uint32_t v[512];
 };
 constexpr PowTable make_pow_table() {
   PowTable t{};
-  for (int j = 0; j < 256; ++j) {
-    const double z = j * (0.693147180559945309417232 / 256.0);
+  for (int j = 0; j < 512; ++j) {
+    const double z = j * (0.693147180559945309417232 / 512.0);
     double term = 1.0, sum = 1.0;
     for (int i = 1; i < 30; ++i) {
       term *= z / i;
       sum += term;
     }
-    t.v[j] = static_cast<uint32_t>(sum * 1073741824.0 + 0.5);
+    t.v[j] = static_cast<uint32_t>(sum * 2147483648.0 + 0.5);
   }
   return t;
 }
 __device__ constexpr PowTable kPow = make_pow_table();
 
 struct Shared {
-  uint32_t pow[256];
+  uint32_t pow[512];
   // what the CTAs of a cluster tell one another, by rank; two sets in turn where there is a next time
-  float top[kMaxCtas], bound[2][kMaxCtas];
-  int bad[kMaxCtas];
-  unsigned long long mass[2][kMaxCtas];
-  float lo[2][kMaxCtas], hi[2][kMaxCtas];
-  uint32_t count[2][kMaxCtas];
-  unsigned long long answer;
+  uint32_t top[kMaxCtas], bound[2][kMaxCtas];
+  u64 mass[2][kMaxCtas];
+  uint32_t count[2][kMaxCtas], lo[2][kMaxCtas], hi[2][kMaxCtas];
+  u64 answer;
   // a CTA's own
-  unsigned long long warp_sum[kWarps];
-  float warp_a[kWarps], warp_b[kWarps];
-  uint32_t warp_n[kWarps];
+  u64 warp_sum[kWarps];
+  uint32_t warp_a[kWarps], warp_b[kWarps];
   uint32_t listed;
   uint32_t found;
-  float reached[2];
+  u64 found_before;
   float min_hi, min_lo;                  // T ln(min_p)
-  unsigned long long found_before;
   union {
     struct {
       uint32_t hist[3][kBins];           // counts, or weights in pieces of 15, 15 and 15 bits
-      unsigned long long merged[kBins];
+      u64 merged[kBins];
     };
-    unsigned long long weights[kList];   // of a sorted list
+    struct {
+      u64 weights[kList];                // the list's
+      u64 part_mass[kThreads];
+      uint32_t part_rank[kThreads];
+    };
   };
-  unsigned long long list[kList];
+  u64 list[kList];                       // keys (ckey)
 };
-
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 // Elements of 16 bytes to fp32.
 template <typename E>
@@ -114,9 +112,11 @@ struct Largest {
       float m = __uint_as_float(v);
       asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(__uint_as_float(w)));
       v = __float_as_uint(m);
+    } else if constexpr (std::is_same<E, __half>::value) {
+      asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(v) : "r"(w));
+    } else {
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(w));
     }
-    else if constexpr (std::is_same<E, __half>::value) asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(v) : "r"(w));
-    else asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(v) : "r"(w));
   }
   __device__ __forceinline__ void add(const uint4& w) {
     one(w.x);
@@ -133,64 +133,147 @@ struct Largest {
 
 // Weights: w = 2^(x c - top), top the whole number next above max c, so that the largest is in (1/2, 1].
 //
-// x c is rounded to a multiple of 1/256, whose power comes from the table; what is left, below 2^-9, is
-// fma(x, ch, -that) + x cl with one rounding of 2^-34, and three terms of its exponential series are within
-// 2^-42.  This holds while |x c| < 2^14.  Where max c is beyond 2^13, weights above 0 belong to x within 1% of
+// x c is rounded to a multiple of 1/512, whose power comes from the table; what is left, below 2^-10, is
+// fma(x, ch, -that) + x cl with one rounding of 2^-35, and three terms of its exponential series are within
+// 2^-46.  This holds while |x c| < 2^13.  Where max c is beyond 2^12, weights above 0 belong to x within 1% of
 // the maximum, whose difference from it is exact in fp32, and that takes the place of x.
 struct Weigher {
-  float ref, least;                      // subtracted from x; smaller x have no weight
+  float ref, least;                      // subtracted from x; smaller x weigh nothing
   float ch, cl;                          // log2(e) / T in two fp32 numbers
   int top;
   const uint32_t* pow;
+  static constexpr float kRound = 24576.f;                   // 1.5 * 2^14: its last bit is 1/512
+  static constexpr int kRoundBits = 0x46C00000;
 
   __device__ __forceinline__ Weigher(float m, float T, const uint32_t* table) : pow(table) {
     constexpr float kLog2e = 1.44269502162933349609375f, kRest = 1.92596299112661746887e-8f;
     ch = kLog2e / T;
     cl = (fmaf(-ch, T, kLog2e) + kRest) / T;
-    const bool far = !(fabsf(m * ch) < 8192.f);
+    const bool far = !(fabsf(m * ch) < 4096.f);
     ref = far ? m : 0.f;
     top = far ? 0 : static_cast<int>(ceilf(m * ch));
-    // x c >= top - kUnitBits and a little: what is below rounds to 0 in any case
-    least = m - (kUnitBits + 1) / ch;
+    least = m - (kUnitBits - 2) / ch;    // x c >= top - kUnitBits + 1
+    if ((least - m) * ch < 1.5f - kUnitBits) least = nextafterf(least, __int_as_float(0x7F800000));   // (rounded too far down)
   }
-  __device__ __forceinline__ unsigned long long operator()(float x) const {
-    const float s = x - ref;
-    const float t = fmaf(s, ch, 49152.f);                    // 1.5 * 2^15: its last bit is 1/256
-    const int k = __float_as_int(t) - 0x47400000;
-    const float r = fmaf(s, cl, fmaf(s, ch, 49152.f - t));
-    // 2^30 (2^r - 1), at most 2^21.4
-    const float q = r * fmaf(r, fmaf(r, 0x1p30f * 0.05550410866f, 0x1p30f * 0.2402265070f), 0x1p30f * 0.6931471806f);
-    const uint32_t p = pow[k & 255];
-    const float f = __uint_as_float((p >> 7) + 0x3F000000u); // p in units of 2^30, to 24 bits
-    const uint32_t w = p + (__float_as_uint(fmaf(f, q, 12582912.f)) - 0x4B400000u);
-    return x >= least ? (static_cast<unsigned long long>(w) << (kUnitBits - 30)) >> min(top - (k >> 8), 63) : 0ull;
+  // The weight of an element not below `least`: bits is what x c was rounded to, w what that leaves, in
+  // units of 2^-31.
+  __device__ __forceinline__ u64 shifted(uint32_t w, int bits) const {
+    return (static_cast<u64>(w) << 32) >> (top + (kRoundBits >> 9) + (63 - kUnitBits) - (bits >> 9));
+  }
+  __device__ __forceinline__ float power(int bits, uint32_t* p) const {
+    *p = pow[bits & 511];
+    return __uint_as_float((*p >> 8) + 0x3F000000u);         // in units of 2^31, to 24 bits
+  }
+  // q = 2^31 (2^r - 1), at most 2^20.5
+  static constexpr float kA = 0x1p31f * 0.6931471806f, kB = 0x1p31f * 0.2402265070f, kC = 0x1p31f * 0.05550410866f;
+  static constexpr float kWhole = 12582912.f;                // 1.5 * 2^23: its last bit is 1
+  static constexpr uint32_t kWholeBits = 0x4B400000u;
+  __device__ __forceinline__ u64 operator()(float x) const {
+    const float s = x - ref, t = fmaf(s, ch, kRound);
+    const float r = fmaf(s, cl, fmaf(s, ch, kRound - t));
+    const float q = r * fmaf(r, fmaf(r, kC, kB), kA);
+    uint32_t p;
+    const float f = power(__float_as_int(t), &p);
+    const uint32_t w = p + (__float_as_uint(fmaf(f, q, kWhole)) - kWholeBits);
+    return x >= least ? shifted(w, __float_as_int(t)) : 0ull;
+  }
+  // Two elements' weights, of those not below `from` (>= least), onto a sum: the same numbers, with the
+  // arithmetic two at a time.
+  __device__ __forceinline__ void add2_to(u64& sum, float x0, float x1, float from) const {
+    const uint64_t c = pack2(ch, ch), s = add2(pack2(x0, x1), pack2(-ref, -ref));
+    const uint64_t t = fma2(s, c, pack2(kRound, kRound));
+    const uint64_t d = fma2(t, pack2(-1.f, -1.f), pack2(kRound, kRound));
+    const uint64_t r = fma2(s, pack2(cl, cl), fma2(s, c, d));
+    const uint64_t q = mul2(r, fma2(r, fma2(r, pack2(kC, kC), pack2(kB, kB)), pack2(kA, kA)));
+    const float2 tt = unpack2(t);
+    const int b0 = __float_as_int(tt.x), b1 = __float_as_int(tt.y);
+    uint32_t p0, p1;
+    const float f0 = power(b0, &p0), f1 = power(b1, &p1);
+    const float2 v = unpack2(fma2(pack2(f0, f1), q, pack2(kWhole, kWhole)));
+    if (x0 >= from) sum += shifted(p0 + (__float_as_uint(v.x) - kWholeBits), b0);
+    if (x1 >= from) sum += shifted(p1 + (__float_as_uint(v.y) - kWholeBits), b1);
+  }
+  // ln of the share of x (with a weight) in `total`, right to 2^-24 of itself + 2^-30: x c and log2(total) are each
+  // split into a multiple of 1/512, exact, and a rest.
+  __device__ float log_share(float x, u64 total) const {
+    const float s = x - ref, t = fmaf(s, ch, kRound);
+    const float r = fmaf(s, cl, fmaf(s, ch, kRound - t));
+    const int e = 63 - __clzll(total);
+    const u64 z = total << (63 - e);     // [1, 2) in units of 2^-63
+    const int j = min(max(__float2int_rn(log2f(__ull2float_rz(z >> 40) * 0x1p-23f) * 512.f), 0), 511);
+    const float by = static_cast<float>(static_cast<long long>(z >> 23) - (static_cast<long long>(pow[j]) << 9)) /
+                     (static_cast<float>(pow[j]) * 512.f);
+    const float l = by * fmaf(by, fmaf(by, 0.4808983470f, -0.7213475204f), 1.442695041f);
+    const float a = (t - kRound) - static_cast<float>(top - kUnitBits + e) - static_cast<float>(j) * (1.f / 512.f);
+    return fmaf(a, 0.693147182464599609375f, fmaf(a, -1.904654299957768e-9f, (r - l) * 0.6931471806f));
   }
 };
 
-// Whether element i comes before or at the one with key `cut`: ckey(x, i) >= cut.
-__device__ __forceinline__ bool not_before(float x, uint32_t i, unsigned long long cut) {
-  const float at = ckey_score(cut);
-  return x > at || (x == at && i <= static_cast<uint32_t>(ckey_idx(cut)));
-}
+// What is kept: elements before or at one in the order (x descending, index ascending).
+struct Cut {
+  float x;
+  uint32_t i;                            // kNone: all elements of that x
+  __device__ __forceinline__ bool operator()(float y, uint32_t j) const { return y > x || (y == x && j <= i); }
+};
+__device__ __forceinline__ Cut cut_at(u64 key) { return Cut{ckey_score(key), static_cast<uint32_t>(ckey_idx(key))}; }
 
-__device__ __forceinline__ unsigned long long warp_total(unsigned long long v) {
+// Equal bins from hi down to lo < hi: halves where the range passes fp32's, and a range too small to
+// divide by scaled up, so that hi is always in the first bin and lo in the last.
+struct Bins {
+  float half, hi, up, by;
+  __device__ __forceinline__ Bins(float lo, float top) : hi(top) {
+    half = hi - lo < __int_as_float(0x7F800000) ? 1.f : 0.5f;
+    const float range = half * hi - half * lo;
+    up = range < 1e-30f ? 0x1p100f : 1.f;
+    by = static_cast<float>(kBins) / (range * up);
+  }
+  __device__ __forceinline__ int operator()(float x) const { return min(__float2int_rz((half * hi - half * x) * up * by), kBins - 1); }
+};
+
+__device__ __forceinline__ u64 warp_total(u64 v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += shfl_xor_key(v, o);
   return v;
 }
-__device__ __forceinline__ unsigned long long warp_running(unsigned long long v, int lane) {
+__device__ __forceinline__ u64 warp_running(u64 v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long u = __shfl_up_sync(0xFFFFFFFFu, v, o);
-    if (lane >= o) v += u;
+    const u64 x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += x;
   }
   return v;
+}
+
+// floor(u * total), 0 <= u < 1, in whole numbers (u is 24 bits times a power of two; the few double
+// units of an SM would hold up 512 threads); *exact: whether that is u * total.
+__device__ __forceinline__ u64 part_of(float u, u64 total, bool* exact) {
+  const uint32_t bits = __float_as_uint(u), e = bits >> 23;
+  const u64 mantissa = (bits & 0x7FFFFFu) | (e > 0 ? 0x800000u : 0u);
+  const int shift = 150 - static_cast<int>(e > 0 ? e : 1);  // u = mantissa * 2^-shift, shift >= 24
+  const u64 lo = mantissa * total, hi = __umul64hi(mantissa, total);
+  if (shift >= 64) {
+    const int rest = shift - 64;
+    *exact = lo == 0 && (rest < 64 ? (hi & ((1ull << rest) - 1)) == 0 : hi == 0);
+    return rest < 64 ? hi >> rest : 0;
+  }
+  *exact = (lo & ((1ull << shift) - 1)) == 0;
+  return (lo >> shift) | (hi << (64 - shift));
+}
+// The random number's place among `total` units of weight.
+__device__ __forceinline__ u64 place_of(float u, u64 total) {
+  bool exact;
+  return part_of(u, total, &exact);
+}
+// The weight that a share p < 1 of `total` has to reach, at least 1.
+__device__ __forceinline__ u64 share_of(float p, u64 total) {
+  bool exact;
+  const u64 t = part_of(p, total, &exact) + (exact ? 0 : 1);
+  return t < 1 ? 1 : t;
 }
 
 template <typename E>
 struct Row {
   static constexpr int VEC = 16 / sizeof(E);
-  const SamplingParams& p;
   Shared& sh;
   const uint4* slice;
   cg::cluster_group cluster;
@@ -198,6 +281,8 @@ struct Row {
   int begin, end;                        // this warp's 16-byte pieces of the slice
   int index0;                            // vocabulary index of the slice's first element
   int turn = 0;                          // which set of `mass`, `count`, `lo`, `hi` is next
+
+  __device__ __forceinline__ Shared* at(int c) const { return cluster.map_shared_rank(&sh, c); }
 
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
@@ -208,82 +293,107 @@ struct Row {
       for (int e = 0; e < VEC; ++e) f(x[e], static_cast<uint32_t>(index0 + i * VEC + e));
     }
   }
+  // The weight of what is kept of this thread's elements.
+  __device__ __forceinline__ u64 mass_of(const Weigher& weigh, const Cut& kept) const {
+    u64 sum = 0;
+    if (kept.x < weigh.least) {
+      // all that weigh anything
+      for (int i = begin + lane; i < end; i += 32) {
+        float x[VEC];
+        unpack<E>(slice[i], x);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) weigh.add2_to(sum, x[e], x[e + 1], weigh.least);
+      }
+    } else {
+      each([&](float x, uint32_t i) {
+        if (kept(x, i)) sum += weigh(x);
+      });
+    }
+    return sum;
+  }
 
-  // Sums of v over the CTA, at every thread.
-  __device__ __forceinline__ unsigned long long block_total(unsigned long long v) {
+  // Sum of v over the CTA, at every thread.
+  __device__ __forceinline__ u64 block_total(u64 v) {
     v = warp_total(v);
     __syncthreads();
     if (lane == 0) sh.warp_sum[warp] = v;
     __syncthreads();
-    unsigned long long sum = 0;
+    u64 sum = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) sum += sh.warp_sum[w];
     return sum;
   }
-  // Sum of v over the threads before this one; *total over all.
-  __device__ __forceinline__ unsigned long long block_before(unsigned long long v, unsigned long long* total) {
-    const unsigned long long run = warp_running(v, lane);
+  // Sum of v over the threads before this one.
+  __device__ __forceinline__ u64 block_before(u64 v) {
+    const u64 run = warp_running(v, lane);
     __syncthreads();
     if (lane == 31) sh.warp_sum[warp] = run;
     __syncthreads();
-    unsigned long long before = run - v, sum = 0;
+    u64 before = run - v;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w)
       if (w < warp) before += sh.warp_sum[w];
-      sum += sh.warp_sum[w];
-    }
-    *total = sum;
     return before;
   }
+  // The smallest a and the largest b over the CTA, at every thread.
+  __device__ __forceinline__ void block_range(uint32_t& a, uint32_t& b) {
+    a = __reduce_min_sync(0xFFFFFFFFu, a);
+    b = __reduce_max_sync(0xFFFFFFFFu, b);
+    __syncthreads();
+    if (lane == 0) {
+      sh.warp_a[warp] = a;
+      sh.warp_b[warp] = b;
+    }
+    __syncthreads();
+    a = __reduce_min_sync(0xFFFFFFFFu, sh.warp_a[lane % kWarps]);
+    b = __reduce_max_sync(0xFFFFFFFFu, sh.warp_b[lane % kWarps]);
+  }
 
-  // The first element, in the vocabulary's order, at which the running sum of f exceeds the target
-  // that `target` makes of the total; `hit` is called by the one thread that holds it.  One
-  // meeting of the cluster.
+  // The first element, in the vocabulary's order, at which the running sum of f exceeds the target that
+  // `target` makes of the total; `hit` is called by the one thread that holds it.  mine: the sum of f over
+  // this thread's elements.  One meeting of the cluster.
   template <typename F, typename T, typename H>
-  __device__ void find(F f, T target, H hit) {
-    unsigned long long mine = 0;
-    each([&](float x, uint32_t i) { mine += f(x, i); });
-    mine = warp_total(mine);
-    __syncthreads();
-    if (lane == 0) sh.warp_sum[warp] = mine;
-    __syncthreads();
-    unsigned long long sum = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += sh.warp_sum[w];
+  __device__ __forceinline__ void find(u64 mine, F f, T target, H hit) {
+    const u64 sum = block_total(mine);
     const int set = turn++ & 1;
-    if (tid < ctas) cluster.map_shared_rank(&sh, tid)->mass[set][rank] = sum;
+    if (tid < ctas) at(tid)->mass[set][rank] = sum;
     cluster.sync();
-    unsigned long long total = 0, before = 0;
+    u64 total = 0, before = 0;
     for (int c = 0; c < ctas; ++c) {
       if (c < rank) before += sh.mass[set][c];
       total += sh.mass[set][c];
     }
-    const unsigned long long t = target(total);
+    const u64 t = target(total);
     if (t < before || t >= before + sum) return;
     for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-    if (t < before || t >= before + mine) return;
+    if (t < before || t >= before + sh.warp_sum[warp]) return;
+#pragma unroll 1
     for (int i0 = begin; i0 < end; i0 += 32) {
       const int i = i0 + lane;
-      float x[VEC];
-      unsigned long long own = 0;
+      u64 own = 0;
       if (i < end) {
+        float x[VEC];
         unpack<E>(slice[i], x);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) own += f(x[e], static_cast<uint32_t>(index0 + i * VEC + e));
       }
-      const unsigned long long run = before + warp_running(own, lane);
+      const u64 run = before + warp_running(own, lane);
       const uint32_t over = __ballot_sync(0xFFFFFFFFu, run > t);
       if (over != 0) {
         if (lane == __ffs(over) - 1) {
-          unsigned long long at = run - own;
-          bool done = false;
-#pragma unroll
+          u64 upto = run - own;
+#pragma unroll 1
           for (int e = 0; e < VEC; ++e) {
+            float x;
+            const E* piece = reinterpret_cast<const E*>(slice + i);
+            if constexpr (sizeof(E) == 4) x = piece[e];
+            else if constexpr (std::is_same<E, __half>::value) x = __half2float(piece[e]);
+            else x = __bfloat162float(piece[e]);
             const uint32_t index = static_cast<uint32_t>(index0 + i * VEC + e);
-            at += f(x[e], index);
-            if (!done && at > t) {
-              done = true;
-              hit(x[e], index, total);
+            upto += f(x, index);
+            if (upto > t) {
+              hit(x, index, total);
+              break;
             }
           }
         }
@@ -293,42 +403,71 @@ struct Row {
     }
   }
 
-  // Elements that `take` accepts into the first CTA's list (their keys), and how many there are; nothing
-  // is listed when they are too many.  Meetings: one, and a second when they fit.
+  // Elements that `take` accepts into the first CTA's list, and how many there are; nothing is listed when they are
+  // too many.  Meetings: one, and a second when they fit.
   template <typename F>
-  __device__ uint32_t gather(bool scan, F take) {
+  __device__ __forceinline__ uint32_t gather(F take) {
     if (tid == 0) sh.listed = 0;
     __syncthreads();
-    if (scan)
-      each([&](float x, uint32_t i) {
-        if (take(x, i)) {
-          const uint32_t at = atomicAdd(&sh.listed, 1u);
-          if (at < kList) sh.list[at] = ckey(x, static_cast<int>(i));
-        }
-      });
+    each([&](float x, uint32_t i) {
+      if (take(x, i)) {
+        const uint32_t to = atomicAdd(&sh.listed, 1u);
+        if (to < kList) sh.list[to] = ckey(x, static_cast<int>(i));
+      }
+    });
     __syncthreads();
     const int set = turn++ & 1;
-    if (tid < ctas) cluster.map_shared_rank(&sh, tid)->count[set][rank] = sh.listed;
+    if (tid < ctas) at(tid)->count[set][rank] = sh.listed;
     cluster.sync();
     uint32_t n = 0;
     for (int c = 0; c < ctas; ++c) n += sh.count[set][c];   // (of at most 2^20 elements)
     if (n > kList || ctas == 1) return n;
     if (rank == 0) {
       const uint32_t own = sh.count[set][0];
-      for (uint32_t at = own + tid; at < n; at += kThreads) {
-        uint32_t i = at - own;
+      for (uint32_t to = own + tid; to < n; to += kThreads) {
+        uint32_t i = to - own;
         int c = 1;
         while (i >= sh.count[set][c]) i -= sh.count[set][c++];
-        sh.list[at] = cluster.map_shared_rank(&sh, c)->list[i];
+        sh.list[to] = at(c)->list[i];
       }
     }
     cluster.sync();
     return n;
   }
 
-  // The list's n keys, descending; thread t gets places [E t, E t + E).  The list's memory is used.
-  template <int P>
-  __device__ __forceinline__ void sort_list(uint32_t n, unsigned long long (&v)[P]) {
+  // Of each of the list's n <= kPairs elements, by thread i < n: how many of the others come before it and what
+  // they weigh; before: by key, or by index.
+  __device__ void pair_sums(uint32_t n, bool by_index, uint32_t* rank_of, u64* before) {
+    const int log = n <= 32 ? 5 : n <= 64 ? 6 : n <= 128 ? 7 : 8, parts = kThreads >> log;
+    const uint32_t i = tid & ((1 << log) - 1), part = tid >> log;
+    __syncthreads();
+    u64 sum = 0;
+    uint32_t count = 0;
+    if (i < n) {
+      const u64 mask = by_index ? 0xFFFFFFFFull : ~0ull, key = sh.list[i] & mask;
+#pragma unroll 4
+      for (uint32_t j = part; j < n; j += parts)
+        if ((sh.list[j] & mask) > key) {             // (a larger key: a larger value, or a smaller index)
+          sum += sh.weights[j];
+          ++count;
+        }
+    }
+    sh.part_mass[tid] = sum;
+    sh.part_rank[tid] = count;
+    __syncthreads();
+    if (tid < (1 << log)) {
+      for (int x = 1; x < parts; ++x) {
+        sum += sh.part_mass[tid + (x << log)];
+        count += sh.part_rank[tid + (x << log)];
+      }
+    }
+    *rank_of = count;
+    *before = sum;
+  }
+
+  // The list's n keys, descending; thread t gets places [P t, P t + P).  The list's memory is used.
+  static constexpr int P = kList / kThreads;
+  __device__ __forceinline__ void sort_list(uint32_t n, u64 (&v)[P]) {
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < P; ++e) v[e] = tid * P + e < n ? sh.list[tid * P + e] : 0;
@@ -336,256 +475,252 @@ struct Row {
     block_sort_regs<P, true>(v, sh.list);
   }
 
-  // The key of the list's element at which the running sum (of ones or weights, in the keys'
-  // descending order, from `above`) reaches `target`.  First CTA only; result at sh.answer.
-  template <int P, typename F>
-  __device__ void cut_list(uint32_t n, unsigned long long above, unsigned long long target, F f) {
-    unsigned long long v[P], w[P], own = 0, total;
-    sort_list<P>(n, v);
+  // The key of the list's element at which the running sum of f, in descending order and from `above`, reaches
+  // `target`, to sh.answer.  First CTA only.  Long lists are cut by a histogram first.
+  template <bool MASS, typename F>
+  __device__ void cut_list(uint32_t n, u64 above, u64 target, F f) {
+    u64 v[P];
+    __syncthreads();
+#pragma unroll 1
+    while (n > kPairs) {
+      uint32_t a = kNone, b = 0;
 #pragma unroll
-    for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < n ? f(ckey_score(v[e])) : 0;
-    unsigned long long run = above + block_before(own, &total);
+      for (int e = 0; e < P; ++e) {
+        v[e] = tid + e * kThreads < n ? sh.list[tid + e * kThreads] : 0;
+        if (v[e] != 0) {
+          a = min(a, static_cast<uint32_t>(v[e] >> 32));
+          b = max(b, static_cast<uint32_t>(v[e] >> 32));
+        }
+      }
+      block_range(a, b);
+      if (a == b) break;
+      const Bins bins(unord_f32(a), unord_f32(b));
+      if (tid == 0) sh.listed = 0;
+      clear_bins();
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      if (run < target && run + w[e] >= target) sh.answer = v[e];
-      run += w[e];
+      for (int e = 0; e < P; ++e)
+        if (v[e] != 0) add_to_bin<MASS>(bins(ckey_score(v[e])), f(ckey_score(v[e])));
+      __syncthreads();
+      for (int i = tid; i < kBins; i += kThreads) sh.merged[i] = bin_sum<MASS>(sh, i);
+      above = find_bin(above, target);
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        if (v[e] != 0 && bins(ckey_score(v[e])) == static_cast<int>(sh.found)) sh.list[atomicAdd(&sh.listed, 1u)] = v[e];
+      __syncthreads();
+      n = sh.listed;
+      __syncthreads();
+    }
+    if (n > kPairs) {                    // equal values
+      sort_list(n, v);
+      u64 w[P], own = 0;
+#pragma unroll
+      for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < n ? f(ckey_score(v[e])) : 0;
+      u64 run = above + block_before(own);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        if (run < target && run + w[e] >= target) sh.answer = v[e];
+        run += w[e];
+      }
+    } else {
+      uint32_t ignored;
+      u64 before = 0, own = 0;
+      if (tid < n) own = sh.weights[tid] = f(ckey_score(sh.list[tid]));
+      pair_sums(n, false, &ignored, &before);
+      before += above;
+      if (tid < n && before < target && before + own >= target) sh.answer = sh.list[tid];
     }
     __syncthreads();
   }
 
-  // Of the elements with ckey >= cut and lo <= x <= hi, in descending order: the key of the one at which the
-  // running sum of f reaches `target` (the sum over all of them does).  MASS: f are weights, else ones.
+  __device__ __forceinline__ void clear_bins() {
+    for (int i = tid; i < 3 * kBins; i += kThreads) sh.hist[i / kBins][i % kBins] = 0;
+    __syncthreads();
+  }
+  template <bool MASS>
+  __device__ __forceinline__ void add_to_bin(int b, u64 w) {
+    if constexpr (MASS) {
+      const uint32_t w0 = static_cast<uint32_t>(w) & 0x7FFFu, w1 = static_cast<uint32_t>(w >> 15) & 0x7FFFu;
+      const uint32_t w2 = static_cast<uint32_t>(w >> 30);
+      atomicAdd(&sh.hist[0][b], w0);
+      atomicAdd(&sh.hist[1][b], w1);
+      if (w2 != 0) atomicAdd(&sh.hist[2][b], w2);
+    } else {
+      atomicAdd(&sh.hist[0][b], 1u);
+    }
+  }
+  template <bool MASS>
+  __device__ __forceinline__ u64 bin_sum(const Shared& of, int b) const {
+    u64 sum = of.hist[0][b];
+    if (MASS) sum += (static_cast<u64>(of.hist[1][b]) << 15) + (static_cast<u64>(of.hist[2][b]) << 30);
+    return sum;
+  }
+  // The first of the merged bins, from the top, at which the running sum from `above` reaches the target: at
+  // sh.found; returns the sum before it.
+  __device__ __forceinline__ u64 find_bin(u64 above, u64 target) {
+    constexpr int kEach = kBins / kThreads;
+    __syncthreads();
+    u64 own = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) own += sh.merged[tid * kEach + e];
+    u64 run = above + block_before(own);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const u64 w = sh.merged[tid * kEach + e];
+      if (run < target && run + w >= target) {
+        sh.found = tid * kEach + e;
+        sh.found_before = run;
+      }
+      run += w;
+    }
+    __syncthreads();
+    return sh.found_before;
+  }
+
+  // Of the kept elements with lo <= x <= hi, in descending order: where the running sum of f reaches `target`
+  // (the sum over all of them does).  MASS: f are weights, else ones.
   template <bool MASS, typename F>
-  __device__ unsigned long long select(float lo, float hi, unsigned long long cut, unsigned long long target, F f) {
-    unsigned long long above = 0;
+  __device__ Cut select(float lo, float hi, const Cut kept, u64 target, F f) {
+    u64 above = 0;
+#pragma unroll 1
     while (true) {
-      // equal bins from hi down to lo; halves where the range passes fp32's, and a range too small to
-      // divide by is scaled up (so the largest is always in the first bin, the smallest in the last)
-      const float half = hi - lo < __int_as_float(0x7F800000) ? 1.f : 0.5f, range = half * hi - half * lo;
-      const float up = range < 1e-30f ? 0x1p100f : 1.f, by = static_cast<float>(kBins) / (range * up);
-      auto bin_at = [&](float x) { return min(__float2int_rz((half * hi - half * x) * up * by), kBins - 1); };
-      auto inside = [&](float x, uint32_t i) { return x >= lo && x <= hi && not_before(x, i, cut); };
+      const Bins bins(lo, hi);
+      auto inside = [&](float x, uint32_t i) { return x >= lo && x <= hi && kept(x, i); };
       int bin = 0;
       if (lo < hi) {
-        for (int i = tid; i < 3 * kBins; i += kThreads) sh.hist[i / kBins][i % kBins] = 0;
-        __syncthreads();
+        clear_bins();
         each([&](float x, uint32_t i) {
-          if (!inside(x, i)) return;
-          const int b = bin_at(x);
-          if constexpr (MASS) {
-            const unsigned long long w = f(x);
-            const uint32_t w0 = static_cast<uint32_t>(w) & 0x7FFFu, w1 = static_cast<uint32_t>(w >> 15) & 0x7FFFu;
-            atomicAdd(&sh.hist[0][b], w0);
-            atomicAdd(&sh.hist[1][b], w1);
-            const uint32_t w2 = static_cast<uint32_t>(w >> 30);
-            if (w2 != 0) atomicAdd(&sh.hist[2][b], w2);
-          } else {
-            atomicAdd(&sh.hist[0][b], 1u);
-          }
+          if (inside(x, i)) add_to_bin<MASS>(bins(x), f(x));
         });
         cluster.sync();
         const int share = kBins / ctas;
         for (int b = rank * share + tid; b < (rank + 1) * share; b += kThreads) {
-          unsigned long long sum = 0;
-          for (int c = 0; c < ctas; ++c) {
-            const Shared* o = cluster.map_shared_rank(&sh, c);
-            sum += o->hist[0][b];
-            if (MASS) sum += (static_cast<unsigned long long>(o->hist[1][b]) << 15) + (static_cast<unsigned long long>(o->hist[2][b]) << 30);
-          }
-          for (int c = 0; c < ctas; ++c) cluster.map_shared_rank(&sh, c)->merged[b] = sum;
+          u64 sum = 0;
+          for (int c = 0; c < ctas; ++c) sum += bin_sum<MASS>(*at(c), b);
+          for (int c = 0; c < ctas; ++c) at(c)->merged[b] = sum;
         }
         cluster.sync();
-        // the first bin, from the top, at which the running sum reaches the target
-        constexpr int kEach = kBins / kThreads;
-        unsigned long long own = 0, total;
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) own += sh.merged[tid * kEach + e];
-        unsigned long long run = above + block_before(own, &total);
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-          const unsigned long long w = sh.merged[tid * kEach + e];
-          if (run < target && run + w >= target) {
-            sh.found = tid * kEach + e;
-            sh.found_before = run;
-          }
-          run += w;
-        }
-        __syncthreads();
+        above = find_bin(above, target);
         bin = sh.found;
-        above = sh.found_before;
       }
-      auto there = [&](float x, uint32_t i) { return inside(x, i) && (!(lo < hi) || bin_at(x) == bin); };
-      const uint32_t n = gather(true, there);
+      auto there = [&](float x, uint32_t i) { return inside(x, i) && (!(lo < hi) || bins(x) == bin); };
+      const uint32_t n = gather(there);
       if (n <= kList) {
         if (rank == 0) {
-          if (n <= kThreads) cut_list<1>(n, above, target, f); else cut_list<kList / kThreads>(n, above, target, f);
-          if (tid > 0 && tid < ctas) cluster.map_shared_rank(&sh, tid)->answer = sh.answer;
+          cut_list<MASS>(n, above, target, f);
+          if (tid > 0 && tid < ctas) at(tid)->answer = sh.answer;
         }
         cluster.sync();
-        return sh.answer;
+        return cut_at(sh.answer);
       }
       if (!(lo < hi)) {
         // equal values, more than a list holds: the last one is found by its index
-        const unsigned long long one = f(lo), need = (target - above + one - 1) / one;
-        find([&](float x, uint32_t i) { return inside(x, i) ? 1ull : 0ull; },
-             [&](unsigned long long) { return need - 1; },
-             [&](float x, uint32_t i, unsigned long long) {
-               for (int c = 0; c < ctas; ++c) cluster.map_shared_rank(&sh, c)->answer = ckey(x, static_cast<int>(i));
+        const u64 one = f(lo), need = (target - above + one - 1) / one;
+        u64 mine = 0;
+        each([&](float x, uint32_t i) { mine += inside(x, i) ? 1 : 0; });
+        find(mine, [&](float x, uint32_t i) { return inside(x, i) ? 1ull : 0ull; }, [&](u64) { return need - 1; },
+             [&](float x, uint32_t i, u64) {
+               for (int c = 0; c < ctas; ++c) at(c)->answer = ckey(x, static_cast<int>(i));
              });
         cluster.sync();
-        return sh.answer;
+        return cut_at(sh.answer);
       }
       // the bin's own range is the next one
-      float least = hi, most = lo;
+      uint32_t a = kNone, b = 0;
       each([&](float x, uint32_t i) {
         if (there(x, i)) {
-          least = fminf(least, x);
-          most = fmaxf(most, x);
+          a = min(a, ord_f32(x));
+          b = max(b, ord_f32(x));
         }
       });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
-        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
-      }
-      if (lane == 0) {
-        sh.warp_a[warp] = least;
-        sh.warp_b[warp] = most;
-      }
-      __syncthreads();
-      for (int w = 0; w < kWarps; ++w) {
-        least = fminf(least, sh.warp_a[w]);
-        most = fmaxf(most, sh.warp_b[w]);
-      }
+      block_range(a, b);
       const int set = turn++ & 1;
       if (tid < ctas) {
-        cluster.map_shared_rank(&sh, tid)->lo[set][rank] = least;
-        cluster.map_shared_rank(&sh, tid)->hi[set][rank] = most;
+        at(tid)->lo[set][rank] = a;
+        at(tid)->hi[set][rank] = b;
       }
       cluster.sync();
       for (int c = 0; c < ctas; ++c) {
-        least = fminf(least, sh.lo[set][c]);
-        most = fmaxf(most, sh.hi[set][c]);
+        a = min(a, sh.lo[set][c]);
+        b = max(b, sh.hi[set][c]);
       }
-      lo = least;
-      hi = most;
+      lo = unord_f32(a);
+      hi = unord_f32(b);
     }
   }
 
-  // Bounds that at least need[0] and need[1] of this CTA's elements reach, by their threads' largest, at
-  // sh.reached; -inf: none.  Warps 0 and 1 look for them bit by bit, from the first in which they differ.
-  __device__ void reached_by(int need0, int need1, float most) {
-    uint32_t* keys = &sh.hist[0][0];
-    keys[tid] = ord_f32(most) >> 12;
-    __syncthreads();
-    if (warp < 2) {
-      const int need = warp == 0 ? need0 : need1;
-      uint32_t key[kThreads / 32], hi = 0, lo = 0xFFFFFFFFu;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) {
-        key[i] = keys[i * 32 + lane];
-        hi = max(hi, key[i]);
-        lo = min(lo, key[i]);
-      }
-      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-      const int bits = 32 - __clz(hi ^ lo);
-      uint32_t at = hi >> bits << bits;
+  // The largest of bounds of 20 bits that at least `need` threads' elements (ord_f32 in [lo, hi], by its 20 bits)
+  // reach.
+  __device__ __forceinline__ uint32_t reached_by(int need, uint32_t key, uint32_t lo, uint32_t hi) {
+    key >>= 12;
+    const int bits = 32 - __clz((hi ^ lo) >> 12);
+    uint32_t reached = hi >> 12 >> bits << bits;
 #pragma unroll 1
-      for (int bit = bits - 1; bit >= 0; --bit) {
-        const uint32_t next = at | (1u << bit);
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) n += key[i] >= next ? 1 : 0;
-        if (__reduce_add_sync(0xFFFFFFFFu, n) >= need) at = next;
-      }
-      if (lane == 0)
-        sh.reached[warp] = at <= (ord_f32(-__int_as_float(0x7F800000)) >> 12) ? -__int_as_float(0x7F800000) : unord_f32(at << 12);
+    for (int bit = bits - 1; bit >= 0; --bit) {
+      const uint32_t next = reached | (1u << bit);
+      if (__syncthreads_count(key >= next) >= need) reached = next;
     }
-    __syncthreads();
+    return reached << 12;
   }
-};
 
-// floor(u * total), 0 <= u < 1, in whole numbers (u is 24 bits times a power of two; the few double
-// units of an SM would hold up 512 threads); *exact: whether that is u * total.
-__device__ __forceinline__ unsigned long long part_of(float u, unsigned long long total, bool* exact) {
-  const uint32_t bits = __float_as_uint(u), e = bits >> 23;
-  const unsigned long long mantissa = (bits & 0x7FFFFFu) | (e > 0 ? 0x800000u : 0u);
-  const int shift = 150 - static_cast<int>(e > 0 ? e : 1);  // u = mantissa * 2^-shift, shift >= 24
-  const unsigned long long lo = mantissa * total, hi = __umul64hi(mantissa, total);
-  if (shift >= 64) {
-    const unsigned long long up = shift - 64 < 64 ? hi >> (shift - 64) : 0;
-    *exact = lo == 0 && (shift - 64 < 64 ? (hi & ((1ull << (shift - 64)) - 1)) == 0 : hi == 0);
-    return up;
-  }
-  *exact = (lo & ((1ull << shift) - 1)) == 0;
-  return (lo >> shift) | (hi << (64 - shift));
-}
-// The random number's place among `total` units of weight.
-__device__ __forceinline__ unsigned long long place_of(float u, unsigned long long total) {
-  bool exact;
-  return part_of(u, total, &exact);
-}
-// The weight that a share p < 1 of `total` has to reach, at least 1.
-__device__ __forceinline__ unsigned long long share_of(float p, unsigned long long total) {
-  bool exact;
-  const unsigned long long t = part_of(p, total, &exact) + (exact ? 0 : 1);
-  return t < 1 ? 1 : t;
-}
-
-// All that is kept is in the first CTA's list: filters, draw and results, by that CTA.
-template <int P, typename E, typename W, typename H>
-__device__ void finish_list(Row<E>& row, uint32_t n, int k, float top_p, float u, const W& weigh, H hit) {
-  Shared& sh = row.sh;
-  const int tid = row.tid;
-  unsigned long long v[P], w[P], own = 0, total;
-  row.template sort_list<P>(n, v);
-  const uint32_t most = k > 0 ? min(n, static_cast<uint32_t>(k)) : n;
-#pragma unroll
-  for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < most ? weigh(ckey_score(v[e])) : 0;
-  unsigned long long run = row.block_before(own, &total);
-  const unsigned long long enough = top_p < 1.f ? share_of(top_p, total) : total;
-  own = 0;
-#pragma unroll
-  for (int e = 0; e < P; ++e) {
-    const unsigned long long x = w[e];
-    if (run >= enough) w[e] = 0;
-    run += x;
-    own += w[e];
-    // the kept ones' order in the vocabulary: the list's places, by index
-    sh.weights[tid * P + e] = w[e];
-    v[e] = w[e] != 0 ? (v[e] << 32) | static_cast<uint32_t>(tid * P + e) : 0;
-  }
-  if constexpr (P == 1) {
-    // few: each finds its own place, from the others' indices
-    constexpr int kFew = 64;
-    const int left = __syncthreads_count(w[0] != 0);         // (they are the first of the sorted)
-    if (left <= kFew) {
-      if (tid < left) sh.list[tid] = v[0];
-      const unsigned long long sum = row.block_total(w[0]), at = place_of(u, sum);
-      if (tid < left) {
-        unsigned long long before = 0;
-        for (int j = 0; j < left; ++j)
-          if (sh.list[j] > v[0]) before += sh.weights[j];    // (larger keys: smaller indices)
-        if (before <= at && at < before + w[0]) hit(0xFFFFFFFFu - static_cast<uint32_t>(v[0] >> 32), sum);
+  // All that is kept is in the list: filters and draw, by the first CTA.
+  template <typename H>
+  __device__ void finish(uint32_t n, int k, float top_p, float u, const Weigher& weigh, H hit) {
+    if (n <= kPairs) {
+      uint32_t place = 0;
+      u64 before = 0, w = 0, key = 0;
+      if (tid < n) {
+        key = sh.list[tid];
+        w = sh.weights[tid] = weigh(ckey_score(key));
       }
+      pair_sums(n, false, &place, &before);
+      if (k > 0 && place >= static_cast<uint32_t>(k)) w = 0;
+      if (top_p < 1.f && before >= share_of(top_p, block_total(w))) w = 0;
+      const u64 total = block_total(w), to = place_of(u, total);
+      if (tid < n) sh.weights[tid] = w;
+      pair_sums(n, true, &place, &before);
+      if (before <= to && to < before + w) hit(ckey_score(key), static_cast<uint32_t>(ckey_idx(key)), total);
       return;
     }
-  }
-  __syncthreads();
-  block_sort_regs<P, true>(v, sh.list);
-  // (the low half of a key is 2^32 - 1 - index, so descending keys are ascending indices)
-  own = 0;
+    u64 v[P], w[P], own = 0;
+    sort_list(n, v);
+    const uint32_t most = k > 0 ? min(n, static_cast<uint32_t>(k)) : n;
 #pragma unroll
-  for (int e = 0; e < P; ++e) own += w[e] = v[e] != 0 ? sh.weights[static_cast<uint32_t>(v[e])] : 0;
-  run = row.block_before(own, &total);
-  const unsigned long long at = place_of(u, total);
+    for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < most ? weigh(ckey_score(v[e])) : 0;
+    u64 run = block_before(own);
+    const u64 enough = top_p < 1.f ? share_of(top_p, block_total(own)) : ~0ull;
+    own = 0;
 #pragma unroll
-  for (int e = 0; e < P; ++e) {
-    if (run <= at && at < run + w[e]) hit(0xFFFFFFFFu - static_cast<uint32_t>(v[e] >> 32), total);
-    run += w[e];
+    for (int e = 0; e < P; ++e) {
+      const u64 x = w[e];
+      if (run >= enough) w[e] = 0;
+      run += x;
+      own += w[e];
+      sh.weights[tid * P + e] = w[e];
+    }
+    const u64 total = block_total(own), to = place_of(u, total);
+    // again in the vocabulary's order (the low half of a key is 2^32 - 1 - index), each with its place before
+    u64 x[P];
+#pragma unroll
+    for (int e = 0; e < P; ++e) x[e] = w[e] != 0 ? (v[e] << 32) | static_cast<uint32_t>(tid * P + e) : 0;
+    __syncthreads();
+    block_sort_regs<P, true>(x, sh.list);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < P; ++e) sh.list[tid * P + e] = v[e];
+    own = 0;
+#pragma unroll
+    for (int e = 0; e < P; ++e) own += w[e] = x[e] != 0 ? sh.weights[static_cast<uint32_t>(x[e])] : 0;
+    run = block_before(own);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      if (run <= to && to < run + w[e]) {
+        const u64 key = sh.list[static_cast<uint32_t>(x[e])];
+        hit(ckey_score(key), static_cast<uint32_t>(ckey_idx(key)), total);
+      }
+      run += w[e];
+    }
   }
-}
+};
 
 template <typename E>
 __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid_constant__ SamplingParams p) {
@@ -597,8 +732,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = p.ctas, rank = static_cast<int>(blockIdx.x) % ctas, b = static_cast<int>(blockIdx.x) / ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < 256) sh.pow[tid] = kPow.v[tid];
-  if (tid == 0) sh.found = kNoCut;
+  sh.pow[tid] = kPow.v[tid];
+  if (tid == 0) {
+    sh.found = kNone;
+    sh.listed = 0;
+  }
 
   begin_after_previous();
   const float T = p.temperature != nullptr ? kv_load(p.temperature + b) : p.temperature_all;
@@ -621,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
   const int pieces = (p.V + shift + VEC - 1) / VEC;
   const int first = min(rank * p.per, pieces), mine = min(p.per, pieces - first);
   const int per_warp = (mine + kWarps - 1) / kWarps;
-  Row<E> row{p, sh, slice, cluster, tid, lane, warp, rank, ctas, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
+  Row<E> row{sh, slice, cluster, tid, lane, warp, rank, ctas, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
              first * VEC - shift};
   Largest<E> largest;
   {
@@ -663,51 +801,47 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
     }
   }
   const float most = largest.get();      // NaN if any element is
-  bool bad = __syncthreads_or(most < inf ? 0 : 1) != 0;
-  // Few enough are kept to be sorted by one CTA: all of a small vocabulary, or a small top-k.  For that each
-  // CTA finds what its share of k elements reach, and what k of them do: k elements of the row reach the least of
-  // the CTAs' former bounds, and any of the latter.
-  const bool all_listed = p.V <= kList, few = k > 0 && k <= kThreads / 2;
-  if (few && !all_listed) row.reached_by((k + ctas - 1) / ctas, k, bad ? -inf : most);
-  float cta_most = most;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) cta_most = fmaxf(cta_most, __shfl_xor_sync(0xFFFFFFFFu, cta_most, o));
-  if (lane == 0) sh.warp_a[warp] = cta_most;
-  __syncthreads();
-  if (warp == 0) {
-    cta_most = lane < kWarps ? sh.warp_a[lane] : -inf;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) cta_most = fmaxf(cta_most, __shfl_xor_sync(0xFFFFFFFFu, cta_most, o));
-    if (lane < ctas) {
-      Shared* o = cluster.map_shared_rank(&sh, lane);
-      o->top[rank] = cta_most;
-      o->bound[0][rank] = few && !all_listed ? sh.reached[0] : -inf;
-      o->bound[1][rank] = few && !all_listed ? sh.reached[1] : -inf;
-      o->bad[rank] = bad;
+  // Few enough are kept for one CTA: all of a small vocabulary, or a small top-k.  For that each CTA finds
+  // what its share of k elements reach, and what k of them do, by its threads' largest: k elements of the row reach
+  // the least of the CTAs' former bounds, and any of the latter.
+  const bool all_listed = p.V <= kList, few = k > 0 && k <= kPairs;
+  {
+    const uint32_t key = most == most ? ord_f32(most) : kNone;   // (above +inf)
+    uint32_t lo = key, hi = key;
+    row.block_range(lo, hi);
+    const bool look = few && !all_listed && hi < ord_f32(inf);
+    const uint32_t share = look ? row.reached_by((k + ctas - 1) / ctas, key, lo, hi) : 0;
+    const uint32_t by_all = look && ctas > 1 ? row.reached_by(k, key, lo, hi) : share;
+    if (tid < ctas) {
+      Shared* o = row.at(tid);
+      o->top[rank] = hi;
+      o->bound[0][rank] = share;
+      o->bound[1][rank] = by_all;
     }
   }
   cluster.sync();
-  float m = -inf, floor_x = inf, by_one = -inf;
+  uint32_t m_key = 0, floor_key = kNone, by_one = 0;
   for (int c = 0; c < ctas; ++c) {
-    m = fmaxf(m, sh.top[c]);
-    floor_x = fminf(floor_x, sh.bound[0][c]);
-    by_one = fmaxf(by_one, sh.bound[1][c]);
-    bad = bad || sh.bad[c] != 0;
+    m_key = max(m_key, sh.top[c]);
+    floor_key = min(floor_key, sh.bound[0][c]);
+    by_one = max(by_one, sh.bound[1][c]);
   }
-  floor_x = fmaxf(floor_x, by_one);
+  floor_key = max(floor_key, by_one);
+  const bool bad = m_key >= ord_f32(inf);
   int* token = p.token + b;
   float* logp = p.logp + b;
-  if (!settings || bad || m == -inf) {
+  if (!settings || bad || m_key == ord_f32(-inf)) {
     if (rank == 0 && tid == 0) {
       *token = -1;
       *logp = settings && !bad ? -inf : __int_as_float(0x7FC00000);
     }
     return;
   }
+  const float m = unord_f32(m_key);
   if (T < 0x1p-127f) {                   // (1 / T would pass fp32) the largest, the first of equal ones
-    uint32_t at = kNoCut;
+    uint32_t at = kNone;
     if (most == m) row.each([&](float x, uint32_t i) { at = x == m && i < at ? i : at; });
-    if (at != kNoCut) atomicMin(cluster.map_shared_rank(&sh.found, 0), at);
+    if (at != kNone) atomicMin(cluster.map_shared_rank(&sh.found, 0), at);
     cluster.sync();
     if (rank == 0 && tid == 0) {
       *token = static_cast<int>(sh.found);
@@ -716,11 +850,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
     return;
   }
   const Weigher weigh(m, T, sh.pow);
-  // the result: its logarithm from x itself, which small weights hold to a few bits only
-  auto hit = [&](uint32_t i, unsigned long long total) {
-    const double x = static_cast<double>(as_float(kv_load(logits + i))) - static_cast<double>(weigh.ref);
+  auto hit = [&](float x, uint32_t i, u64 total) {
     *token = static_cast<int>(i);
-    *logp = static_cast<float>(x / static_cast<double>(T) - log(static_cast<double>(total)) - (weigh.top - kUnitBits) * 0.69314718055994530942);
+    *logp = weigh.log_share(x, total);
   };
   // min-p is a bound on x; -inf is never kept
   float least = -__int_as_float(0x7F7FFFFF);
@@ -731,99 +863,99 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
     least = fmaxf(least, fminf(m, up));
   }
   if (all_listed || few) {
-    const float from = fmaxf(floor_x, least);
-    const uint32_t n = row.gather(most >= from, [&](float x, uint32_t) { return x >= from; });
-    if (n <= kList) {
+    // each CTA's straight into its part of the first one's list
+    const float from = fmaxf(unord_f32(floor_key), least);
+    const uint32_t room = kList / ctas;
+    if (most >= from) {
+      u64* list = row.at(0)->list + rank * room;
+      row.each([&](float x, uint32_t i) {
+        if (x >= from) {
+          const uint32_t to = atomicAdd(&sh.listed, 1u);
+          if (to < room) list[to] = ckey(x, static_cast<int>(i));
+        }
+      });
+    }
+    __syncthreads();
+    const int set = row.turn++ & 1;
+    if (tid < ctas) row.at(tid)->count[set][rank] = sh.listed;
+    cluster.sync();
+    uint32_t n = 0;
+    bool fits = true;
+    for (int c = 0; c < ctas; ++c) {
+      n += sh.count[set][c];
+      fits = fits && sh.count[set][c] <= room;
+    }
+    if (fits) {
       if (rank == 0) {
-        if (n <= kThreads) finish_list<1>(row, n, k, top_p, u, weigh, hit);
-        else finish_list<kList / kThreads>(row, n, k, top_p, u, weigh, hit);
+        if (ctas > 1) {                  // close the gaps
+          u64 v[kList / kThreads];
+#pragma unroll
+          for (int e = 0; e < kList / kThreads; ++e) {
+            uint32_t i = tid + e * kThreads;
+            if (i >= n) continue;
+            int c = 0;
+            while (i >= sh.count[set][c]) i -= sh.count[set][c++];
+            v[e] = sh.list[c * room + i];
+          }
+          __syncthreads();
+#pragma unroll
+          for (int e = 0; e < kList / kThreads; ++e)
+            if (tid + e * kThreads < n) sh.list[tid + e * kThreads] = v[e];
+          __syncthreads();
+        }
+        row.finish(n, k, top_p, u, weigh, hit);
       }
       return;
     }
   }
-  unsigned long long cut = ckey(least, -1);                  // (index 2^32 - 1: all of equal value)
-  auto kept = [&](float x, uint32_t i) { return not_before(x, i, cut); };
+  Cut kept{least, kNone};
   if (k > 0) {
     // how many there are, and the smallest
-    uint32_t n = 0;
-    float lo = m;
+    uint32_t n = 0, lo = m_key, ignored = 0;
     row.each([&](float x, uint32_t) {
       if (x >= least) {
         ++n;
-        lo = fminf(lo, x);
+        lo = min(lo, ord_f32(x));
       }
     });
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-    if (lane == 0) {
-      sh.warp_n[warp] = n;
-      sh.warp_a[warp] = lo;
-    }
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      n += sh.warp_n[w];
-      lo = fminf(lo, sh.warp_a[w]);
-    }
+    n = static_cast<uint32_t>(row.block_total(n));
+    row.block_range(lo, ignored);
     const int set = row.turn++ & 1;
     if (tid < ctas) {
-      Shared* o = cluster.map_shared_rank(&sh, tid);
+      Shared* o = row.at(tid);
       o->count[set][rank] = n;
       o->lo[set][rank] = lo;
     }
     cluster.sync();
     n = 0;
-    for (int x = 0; x < ctas; ++x) {
-      n += sh.count[set][x];
-      lo = fminf(lo, sh.lo[set][x]);
+    for (int c = 0; c < ctas; ++c) {
+      n += sh.count[set][c];
+      lo = min(lo, sh.lo[set][c]);
     }
-    if (n > static_cast<uint32_t>(k)) cut = row.template select<false>(lo, m, cut, k, [](float) { return 1ull; });
+    if (n > static_cast<uint32_t>(k)) kept = row.template select<false>(unord_f32(lo), m, kept, k, [](float) { return 1ull; });
   }
   if (top_p < 1.f) {
-    unsigned long long own = 0;
-    uint32_t n = 0;
-    row.each([&](float x, uint32_t i) {
-      if (kept(x, i)) {
-        own += weigh(x);
-        ++n;
-      }
-    });
-    own = row.block_total(own);
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (lane == 0) sh.warp_n[warp] = n;
-    __syncthreads();
-    n = 0;
-    for (int w = 0; w < kWarps; ++w) n += sh.warp_n[w];
+    const u64 own = row.block_total(row.mass_of(weigh, kept));
     const int set = row.turn++ & 1;
-    if (tid < ctas) {
-      Shared* o = cluster.map_shared_rank(&sh, tid);
-      o->mass[set][rank] = own;
-      o->count[set][rank] = n;
-    }
+    if (tid < ctas) row.at(tid)->mass[set][rank] = own;
     cluster.sync();
-    unsigned long long total = 0;
-    n = 0;
-    for (int x = 0; x < ctas; ++x) {
-      total += sh.mass[set][x];
-      n += sh.count[set][x];
-    }
-    const unsigned long long target = share_of(top_p, total);
-    // n elements of less than (total - target) / n each cannot hold the rest, so the cut is above that
-    // (fp32 logarithms and products here are right to 2^-20, the bound is taken 2^-7 lower)
-    float lo = fmaxf(least, ckey_score(cut));
-    const float rest = static_cast<float>(total - target) / n;
+    u64 total = 0;
+    for (int c = 0; c < ctas; ++c) total += sh.mass[set][c];
+    const u64 target = share_of(top_p, total);
+    // V elements of less than (total - target) / V each cannot hold the rest, so the cut is above that
+    // (fp32 logarithms and products here are right to 2^-10, the bound is taken 2^-7 lower)
+    float lo = fmaxf(kept.x, weigh.least);
+    const float rest = static_cast<float>(total - target) / p.V;
     if (rest > 1.f) lo = fmaxf(lo, fminf(m, weigh.ref + (weigh.top + log2f(rest) - kUnitBits - 0x1p-7f) / weigh.ch - 0x1p-20f * fabsf(weigh.ref)));
-    cut = row.template select<true>(lo, m, cut, target, weigh);
+    kept = row.template select<true>(lo, m, kept, target, weigh);
   }
-  row.find([&](float x, uint32_t i) { return kept(x, i) ? weigh(x) : 0ull; },
-           [&](unsigned long long total) { return place_of(u, total); },
-           [&](float, uint32_t i, unsigned long long total) { hit(i, total); });
+  row.find(row.mass_of(weigh, kept), [&](float x, uint32_t i) { return kept(x, i) ? weigh(x) : 0ull; },
+           [&](u64 total) { return place_of(u, total); }, hit);
 }
 
 template <typename E>
 cudaError_t launch_sampling(const SamplingParams& p, int device, cudaStream_t stream) {
-  static std::atomic<unsigned long long> ready{0};           // devices whose kernel may use all its shared memory
+  static std::atomic<u64> ready{0};           // devices whose kernel may use all its shared memory
   const int smem = static_cast<int>((sizeof(Shared) + 15) / 16 * 16) + p.per * 16;
   if (device > 63 || (ready.load() >> device & 1) == 0) {
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(sample_tokens_kernel<E>),
@@ -853,10 +985,10 @@ cudaError_t launch_sampling(const SamplingParams& p, int device, cudaStream_t st
 bool sampling_plan(SamplingParams& p, int num_sms) {
   const long long size = p.dtype == LTK_F32 ? 4 : 2, vec = 16 / size;
   const long long pieces = (p.V + 2 * vec - 2) / vec;        // wherever the row begins
-  // CTAs of a row: as few as hold it in 64 KB each (two fit an SM), more where SMs would be idle and
+  // CTAs of a row: as few as hold it in 76 KB each (two fit an SM), more where SMs would be idle and
   // a CTA still has 8 KB to read.
   int ctas = 1;
-  while (ctas < kMaxCtas && (pieces * 16 > ctas * 65536ll ||
+  while (ctas < kMaxCtas && (pieces * 16 > ctas * 77824ll ||
                              (static_cast<long long>(p.B) * ctas * 2 <= num_sms && pieces * 16 > ctas * 8192ll)))
     ctas *= 2;
   p.ctas = ctas;
