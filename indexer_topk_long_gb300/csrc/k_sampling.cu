@@ -11,16 +11,15 @@
 // on how a row is split.  (fp32 weights would put one in a hundred draws from a flat vocabulary of
 // 100000 on the neighbouring token.)
 //
-// A cluster of 1 to 8 CTAs holds a row in its shared memory, so that logits are read once; what has
-// to be known of the whole row (maximum, counts, sums) goes from CTA to CTA through distributed
-// shared memory.  Small top-k: each thread's largest element gives bounds that k elements reach, and
+// A cluster of 1 to 8 CTAs takes a row, each a slice of it; what has to be known of the whole row (maximum, counts,
+// sums) goes from CTA to CTA through distributed shared memory.  Slices are read from memory once and from L2
+// in later passes.  Small top-k: each thread's largest element gives bounds that k elements reach, and
 // the few at or above them go to one CTA, which compares them with one another and finishes.  Else the cut is
 // found by histograms over ever smaller ranges of x, of counts (top-k) or weights (top-p), until one CTA can
 // take what is left; the draw then takes one pass over the row.
 #include <cooperative_groups.h>
 
-#include <atomic>
-
+#include <cstdlib>
 #include "block_sort.cuh"
 #include "kv_tensor.cuh"
 #include "sampling_internal.cuh"
@@ -31,7 +30,7 @@ namespace {
 namespace cg = cooperative_groups;
 using u64 = unsigned long long;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
 constexpr int kBins = 1024;
@@ -40,7 +39,9 @@ constexpr int kPairs = 256;              // of them, that are all compared with 
 constexpr int kUnitBits = 44;            // weights are in units of 2^-44
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
-// 2^(j / 512) in units of 2^-31, rounded: by the exponential series in double, at compile time.
+// (1 - h) 2^(j / 512) in units of 2^-31, rounded, where 1 / (1 - h) = 1 + kWholeBits / 2^32 (see Weigher): by the
+// exponential series in double, at compile time.
+constexpr uint32_t kWholeBits = 0x4B400000u;                 // 1.5 * 2^23 in fp32, whose last bit is 1
 struct PowTable {
   uint32_t v[512];
 };
@@ -53,7 +54,7 @@ constexpr PowTable make_pow_table() {
       term *= z / i;
       sum += term;
     }
-    t.v[j] = static_cast<uint32_t>(sum * 2147483648.0 + 0.5);
+    t.v[j] = static_cast<uint32_t>(sum * (2147483648.0 / (1.0 + kWholeBits / 4294967296.0)) + 0.5);
   }
   return t;
 }
@@ -67,12 +68,13 @@ struct Shared {
   uint32_t count[2][kMaxCtas], lo[2][kMaxCtas], hi[2][kMaxCtas];
   u64 answer;
   // a CTA's own
-  u64 warp_sum[kWarps];
-  uint32_t warp_a[kWarps], warp_b[kWarps];
+  u64 warp_sum[2][kWarps];
   uint32_t listed;
   uint32_t found;
   u64 found_before;
   float min_hi, min_lo;                  // T ln(min_p)
+  uint32_t reached[2];
+  int reached_bin[2];
   union {
     struct {
       uint32_t hist[3][kBins];           // counts, or weights in pieces of 15, 15 and 15 bits
@@ -155,44 +157,38 @@ struct Weigher {
     least = m - (kUnitBits - 2) / ch;    // x c >= top - kUnitBits + 1
     if ((least - m) * ch < 1.5f - kUnitBits) least = nextafterf(least, __int_as_float(0x7F800000));   // (rounded too far down)
   }
-  // The weight of an element not below `least`: bits is what x c was rounded to, w what that leaves, in
-  // units of 2^-31.
-  __device__ __forceinline__ u64 shifted(uint32_t w, int bits) const {
-    return (static_cast<u64>(w) << 32) >> (top + (kRoundBits >> 9) + (63 - kUnitBits) - (bits >> 9));
+  // The weight of an element not below `least`: bits is what x c was rounded to, v = kWhole + (1 + h') 2^32 (2^r - 1),
+  // of which r is what that leaves and 1 + h' = 1 + kWholeBits / 2^32.  With p the table's entry,
+  // p (2^32 + bits of v) = 2^32 2^(31 + j / 512) 2^r: one wide product.
+  __device__ __forceinline__ u64 weight(int bits, float v) const {
+    const uint32_t p = pow[bits & 511];
+    const u64 w = (static_cast<u64>(p) << 32) + static_cast<u64>(p) * __float_as_uint(v);
+    return w >> (top + (kRoundBits >> 9) + (63 - kUnitBits) - (bits >> 9));
   }
-  __device__ __forceinline__ float power(int bits, uint32_t* p) const {
-    *p = pow[bits & 511];
-    return __uint_as_float((*p >> 8) + 0x3F000000u);         // in units of 2^31, to 24 bits
-  }
-  // q = 2^31 (2^r - 1), at most 2^20.5
-  static constexpr float kA = 0x1p31f * 0.6931471806f, kB = 0x1p31f * 0.2402265070f, kC = 0x1p31f * 0.05550410866f;
-  static constexpr float kWhole = 12582912.f;                // 1.5 * 2^23: its last bit is 1
-  static constexpr uint32_t kWholeBits = 0x4B400000u;
+  static constexpr float kWhole = 12582912.f, kH = 1.f + kWholeBits / 4294967296.f;
+  // (1 + h') 2^32 (2^r - 1) is at most 2^21.9
+  static constexpr float kA = 0x1p32f * kH * 0.6931471806f, kB = 0x1p32f * kH * 0.2402265070f, kC = 0x1p32f * kH * 0.05550410866f;
   __device__ __forceinline__ u64 operator()(float x) const {
     const float s = x - ref, t = fmaf(s, ch, kRound);
     const float r = fmaf(s, cl, fmaf(s, ch, kRound - t));
-    const float q = r * fmaf(r, fmaf(r, kC, kB), kA);
-    uint32_t p;
-    const float f = power(__float_as_int(t), &p);
-    const uint32_t w = p + (__float_as_uint(fmaf(f, q, kWhole)) - kWholeBits);
-    return x >= least ? shifted(w, __float_as_int(t)) : 0ull;
+    const float v = fmaf(r, fmaf(r, fmaf(r, kC, kB), kA), kWhole);
+    return x >= least ? weight(__float_as_int(t), v) : 0ull;
   }
-  // Two elements' weights, of those not below `from` (>= least), onto a sum: the same numbers, with the
-  // arithmetic two at a time.
-  __device__ __forceinline__ void add2_to(u64& sum, float x0, float x1, float from) const {
+  // Two elements' weights, of those not below `least`, onto a sum: the same numbers, with the arithmetic two at a
+  // time.
+  __device__ __forceinline__ void add2_to(u64& sum, float x0, float x1) const {
     const uint64_t c = pack2(ch, ch), s = add2(pack2(x0, x1), pack2(-ref, -ref));
     const uint64_t t = fma2(s, c, pack2(kRound, kRound));
     const uint64_t d = fma2(t, pack2(-1.f, -1.f), pack2(kRound, kRound));
     const uint64_t r = fma2(s, pack2(cl, cl), fma2(s, c, d));
-    const uint64_t q = mul2(r, fma2(r, fma2(r, pack2(kC, kC), pack2(kB, kB)), pack2(kA, kA)));
+    const float2 v = unpack2(fma2(r, fma2(r, fma2(r, pack2(kC, kC), pack2(kB, kB)), pack2(kA, kA)), pack2(kWhole, kWhole)));
     const float2 tt = unpack2(t);
-    const int b0 = __float_as_int(tt.x), b1 = __float_as_int(tt.y);
-    uint32_t p0, p1;
-    const float f0 = power(b0, &p0), f1 = power(b1, &p1);
-    const float2 v = unpack2(fma2(pack2(f0, f1), q, pack2(kWhole, kWhole)));
-    if (x0 >= from) sum += shifted(p0 + (__float_as_uint(v.x) - kWholeBits), b0);
-    if (x1 >= from) sum += shifted(p1 + (__float_as_uint(v.y) - kWholeBits), b1);
+    const u64 w0 = weight(__float_as_int(tt.x), v.x), w1 = weight(__float_as_int(tt.y), v.y);
+    if (x0 >= least) sum += w0;
+    if (x1 >= least) sum += w1;
   }
+  // About the weight, from 0 to 1 (1% off at most).
+  __device__ __forceinline__ float roughly(float x) const { return exp2_approx(fmaf(x - ref, ch, static_cast<float>(-top))); }
   // ln of the share of x (with a weight) in `total`, right to 2^-24 of itself + 2^-30: x c and log2(total) are each
   // split into a multiple of 1/512, exact, and a rest.
   __device__ float log_share(float x, u64 total) const {
@@ -201,8 +197,8 @@ struct Weigher {
     const int e = 63 - __clzll(total);
     const u64 z = total << (63 - e);     // [1, 2) in units of 2^-63
     const int j = min(max(__float2int_rn(log2f(__ull2float_rz(z >> 40) * 0x1p-23f) * 512.f), 0), 511);
-    const float by = static_cast<float>(static_cast<long long>(z >> 23) - (static_cast<long long>(pow[j]) << 9)) /
-                     (static_cast<float>(pow[j]) * 512.f);
+    const u64 p = (static_cast<u64>(pow[j]) << 32) + static_cast<u64>(pow[j]) * kWholeBits;      // in units of 2^-63
+    const float by = static_cast<float>(static_cast<long long>(z - p)) / static_cast<float>(p);
     const float l = by * fmaf(by, fmaf(by, 0.4808983470f, -0.7213475204f), 1.442695041f);
     const float a = (t - kRound) - static_cast<float>(top - kUnitBits + e) - static_cast<float>(j) * (1.f / 512.f);
     return fmaf(a, 0.693147182464599609375f, fmaf(a, -1.904654299957768e-9f, (r - l) * 0.6931471806f));
@@ -230,10 +226,10 @@ struct Bins {
   __device__ __forceinline__ int operator()(float x) const { return min(__float2int_rz((half * hi - half * x) * up * by), kBins - 1); }
 };
 
+// Sum over the warp of numbers below 2^53.
 __device__ __forceinline__ u64 warp_total(u64 v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += shfl_xor_key(v, o);
-  return v;
+  const uint32_t lo = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(v) & 0x7FFFFFFu);
+  return lo + (static_cast<u64>(__reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(v >> 27))) << 27);
 }
 __device__ __forceinline__ u64 warp_running(u64 v, int lane) {
 #pragma unroll
@@ -275,35 +271,75 @@ template <typename E>
 struct Row {
   static constexpr int VEC = 16 / sizeof(E);
   Shared& sh;
-  const uint4* slice;
+  const E* logits;                       // the row
+  int V;
   cg::cluster_group cluster;
   int tid, lane, warp, rank, ctas;
-  int begin, end;                        // this warp's 16-byte pieces of the slice
+  int begin, end;                        // this warp's pieces of the slice: 16 aligned bytes each
   int index0;                            // vocabulary index of the slice's first element
+  int sums = 0;                          // which of warp_sum was used last
   int turn = 0;                          // which set of `mass`, `count`, `lo`, `hi` is next
 
   __device__ __forceinline__ Shared* at(int c) const { return cluster.map_shared_rank(&sh, c); }
 
+  __device__ __forceinline__ float element(int i) const {
+    if constexpr (sizeof(E) == 4) return kv_load(logits + i);
+    const uint32_t x = kv_load(reinterpret_cast<const uint16_t*>(logits) + i);
+    return kv_unpack16(x, std::is_same<E, __nv_bfloat16>::value).x;
+  }
+  // A piece; elements before the row and behind it are -inf.
+  __device__ __forceinline__ uint4 piece(int i) const {
+    const int from = index0 + i * VEC;
+    if (from >= 0 && from + VEC <= V) return kv_load(reinterpret_cast<const uint4*>(logits + from));
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = sizeof(E) == 4 ? 0xFF800000u : std::is_same<E, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (from + e < 0 || from + e >= V) continue;
+      if constexpr (sizeof(E) == 4) {
+        w[e] = kv_load(reinterpret_cast<const uint32_t*>(logits) + from + e);
+      } else {
+        const uint32_t x = kv_load(reinterpret_cast<const uint16_t*>(logits) + from + e);
+        w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xFFFFu) | (x << 16) : (w[e >> 1] & 0xFFFF0000u) | x;
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // f(piece, its number) for this thread's pieces, kAhead loads at a time.
+  template <int kAhead, typename F>
+  __device__ __forceinline__ void each_piece(F f) const {
+#pragma unroll 1
+    for (int i0 = begin + lane; i0 < end; i0 += 32 * kAhead) {
+      uint4 v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + 32 * j < end) v[j] = piece(i0 + 32 * j);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (i0 + 32 * j < end) f(v[j], i0 + 32 * j);
+    }
+  }
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    for (int i = begin + lane; i < end; i += 32) {
+    each_piece<2>([&](const uint4& v, int i) {
       float x[VEC];
-      unpack<E>(slice[i], x);
+      unpack<E>(v, x);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) f(x[e], static_cast<uint32_t>(index0 + i * VEC + e));
-    }
+    });
   }
   // The weight of what is kept of this thread's elements.
   __device__ __forceinline__ u64 mass_of(const Weigher& weigh, const Cut& kept) const {
     u64 sum = 0;
     if (kept.x < weigh.least) {
       // all that weigh anything
-      for (int i = begin + lane; i < end; i += 32) {
+      each_piece<2>([&](const uint4& v, int) {
         float x[VEC];
-        unpack<E>(slice[i], x);
+        unpack<E>(v, x);
 #pragma unroll
-        for (int e = 0; e < VEC; e += 2) weigh.add2_to(sum, x[e], x[e + 1], weigh.least);
-      }
+        for (int e = 0; e < VEC; e += 2) weigh.add2_to(sum, x[e], x[e + 1]);
+      });
     } else {
       each([&](float x, uint32_t i) {
         if (kept(x, i)) sum += weigh(x);
@@ -312,41 +348,46 @@ struct Row {
     return sum;
   }
 
-  // Sum of v over the CTA, at every thread.
+  // Sums of v (below 2^53 each) over the CTA, at every thread, and over the warps, at warp_sums().  Two places in
+  // turn: a call's numbers are read before the next one's barrier.
+  __device__ __forceinline__ u64* warp_sums() const { return sh.warp_sum[sums & 1]; }
   __device__ __forceinline__ u64 block_total(u64 v) {
     v = warp_total(v);
-    __syncthreads();
-    if (lane == 0) sh.warp_sum[warp] = v;
+    ++sums;
+    if (lane == 0) warp_sums()[warp] = v;
     __syncthreads();
     u64 sum = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += sh.warp_sum[w];
+    for (int w = 0; w < kWarps; ++w) sum += warp_sums()[w];
     return sum;
   }
-  // Sum of v over the threads before this one.
-  __device__ __forceinline__ u64 block_before(u64 v) {
+  // Sum of v over the threads before this one; *total over all.
+  __device__ __forceinline__ u64 block_before(u64 v, u64* total) {
     const u64 run = warp_running(v, lane);
+    ++sums;
+    if (lane == 31) warp_sums()[warp] = run;
     __syncthreads();
-    if (lane == 31) sh.warp_sum[warp] = run;
-    __syncthreads();
-    u64 before = run - v;
+    u64 before = run - v, sum = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      if (w < warp) before += sh.warp_sum[w];
+    for (int w = 0; w < kWarps; ++w) {
+      const u64 x = warp_sums()[w];
+      sum += x;
+      if (w < warp) before += x;
+    }
+    *total = sum;
     return before;
   }
   // The smallest a and the largest b over the CTA, at every thread.
   __device__ __forceinline__ void block_range(uint32_t& a, uint32_t& b) {
     a = __reduce_min_sync(0xFFFFFFFFu, a);
     b = __reduce_max_sync(0xFFFFFFFFu, b);
+    ++sums;
+    uint2* place = reinterpret_cast<uint2*>(warp_sums());
+    if (lane == 0) place[warp] = make_uint2(a, b);
     __syncthreads();
-    if (lane == 0) {
-      sh.warp_a[warp] = a;
-      sh.warp_b[warp] = b;
-    }
-    __syncthreads();
-    a = __reduce_min_sync(0xFFFFFFFFu, sh.warp_a[lane % kWarps]);
-    b = __reduce_max_sync(0xFFFFFFFFu, sh.warp_b[lane % kWarps]);
+    const uint2 x = place[lane % kWarps];
+    a = __reduce_min_sync(0xFFFFFFFFu, x.x);
+    b = __reduce_max_sync(0xFFFFFFFFu, x.y);
   }
 
   // The first element, in the vocabulary's order, at which the running sum of f exceeds the target that
@@ -365,15 +406,15 @@ struct Row {
     }
     const u64 t = target(total);
     if (t < before || t >= before + sum) return;
-    for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-    if (t < before || t >= before + sh.warp_sum[warp]) return;
+    for (int w = 0; w < warp; ++w) before += warp_sums()[w];
+    if (t < before || t >= before + warp_sums()[warp]) return;
 #pragma unroll 1
     for (int i0 = begin; i0 < end; i0 += 32) {
       const int i = i0 + lane;
       u64 own = 0;
       if (i < end) {
         float x[VEC];
-        unpack<E>(slice[i], x);
+        unpack<E>(piece(i), x);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) own += f(x[e], static_cast<uint32_t>(index0 + i * VEC + e));
       }
@@ -384,15 +425,12 @@ struct Row {
           u64 upto = run - own;
 #pragma unroll 1
           for (int e = 0; e < VEC; ++e) {
-            float x;
-            const E* piece = reinterpret_cast<const E*>(slice + i);
-            if constexpr (sizeof(E) == 4) x = piece[e];
-            else if constexpr (std::is_same<E, __half>::value) x = __half2float(piece[e]);
-            else x = __bfloat162float(piece[e]);
-            const uint32_t index = static_cast<uint32_t>(index0 + i * VEC + e);
-            upto += f(x, index);
+            const int index = index0 + i * VEC + e;
+            if (index < 0 || index >= V) continue;
+            const float x = element(index);
+            upto += f(x, static_cast<uint32_t>(index));
             if (upto > t) {
-              hit(x, index, total);
+              hit(x, static_cast<uint32_t>(index), total);
               break;
             }
           }
@@ -437,7 +475,7 @@ struct Row {
 
   // Of each of the list's n <= kPairs elements, by thread i < n: how many of the others come before it and what
   // they weigh; before: by key, or by index.
-  __device__ void pair_sums(uint32_t n, bool by_index, uint32_t* rank_of, u64* before) {
+  __device__ __forceinline__ void pair_sums(uint32_t n, bool by_index, uint32_t* rank_of, u64* before) {
     const int log = n <= 32 ? 5 : n <= 64 ? 6 : n <= 128 ? 7 : 8, parts = kThreads >> log;
     const uint32_t i = tid & ((1 << log) - 1), part = tid >> log;
     __syncthreads();
@@ -446,16 +484,18 @@ struct Row {
     if (i < n) {
       const u64 mask = by_index ? 0xFFFFFFFFull : ~0ull, key = sh.list[i] & mask;
 #pragma unroll 4
-      for (uint32_t j = part; j < n; j += parts)
-        if ((sh.list[j] & mask) > key) {             // (a larger key: a larger value, or a smaller index)
-          sum += sh.weights[j];
-          ++count;
-        }
+      for (uint32_t j = part; j < n; j += parts) {
+        const u64 other = sh.list[j] & mask, w = sh.weights[j];
+        const bool first = other > key;              // (a larger key: a larger value, or a smaller index)
+        sum += first ? w : 0;
+        count += first ? 1 : 0;
+      }
     }
     sh.part_mass[tid] = sum;
     sh.part_rank[tid] = count;
     __syncthreads();
     if (tid < (1 << log)) {
+#pragma unroll 4
       for (int x = 1; x < parts; ++x) {
         sum += sh.part_mass[tid + (x << log)];
         count += sh.part_rank[tid + (x << log)];
@@ -515,7 +555,7 @@ struct Row {
       u64 w[P], own = 0;
 #pragma unroll
       for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < n ? f(ckey_score(v[e])) : 0;
-      u64 run = above + block_before(own);
+      u64 all, run = above + block_before(own, &all);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         if (run < target && run + w[e] >= target) sh.answer = v[e];
@@ -562,7 +602,7 @@ struct Row {
     u64 own = 0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) own += sh.merged[tid * kEach + e];
-    u64 run = above + block_before(own);
+    u64 all, run = above + block_before(own, &all);
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const u64 w = sh.merged[tid * kEach + e];
@@ -576,31 +616,50 @@ struct Row {
     return sh.found_before;
   }
 
-  // Of the kept elements with lo <= x <= hi, in descending order: where the running sum of f reaches `target`
-  // (the sum over all of them does).  MASS: f are weights, else ones.
+  // Of the kept elements with x <= hi, in descending order: where the running sum of f reaches `target` (the sum over
+  // those with lo <= x does).  MASS: f are weights, else ones.  A `share` below 1 in place of a target: that share of the
+  // sum over all kept ones.
   template <bool MASS, typename F>
-  __device__ Cut select(float lo, float hi, const Cut kept, u64 target, F f) {
+  __device__ Cut select(float lo, float hi, const Cut kept, u64 target, float share, F f) {
     u64 above = 0;
 #pragma unroll 1
     while (true) {
       const Bins bins(lo, hi);
       auto inside = [&](float x, uint32_t i) { return x >= lo && x <= hi && kept(x, i); };
       int bin = 0;
-      if (lo < hi) {
+      if (lo < hi || share < 1.f) {
         clear_bins();
+        u64 below = 0;
         each([&](float x, uint32_t i) {
-          if (inside(x, i)) add_to_bin<MASS>(bins(x), f(x));
+          if (inside(x, i)) add_to_bin<MASS>(lo < hi ? bins(x) : 0, f(x));
+          else if (MASS && share < 1.f && kept(x, i)) below += f(x);
         });
+        int set = 0;
+        if (share < 1.f) {
+          below = block_total(below);
+          set = turn++ & 1;
+          if (tid < ctas) at(tid)->mass[set][rank] = below;
+        }
         cluster.sync();
-        const int share = kBins / ctas;
-        for (int b = rank * share + tid; b < (rank + 1) * share; b += kThreads) {
+        const int part = kBins / ctas;
+        for (int b = rank * part + tid; b < (rank + 1) * part; b += kThreads) {
           u64 sum = 0;
           for (int c = 0; c < ctas; ++c) sum += bin_sum<MASS>(*at(c), b);
           for (int c = 0; c < ctas; ++c) at(c)->merged[b] = sum;
         }
         cluster.sync();
-        above = find_bin(above, target);
-        bin = sh.found;
+        if (share < 1.f) {
+          u64 own = 0, total;
+          for (int b = tid; b < kBins; b += kThreads) own += sh.merged[b];
+          block_before(own, &total);
+          for (int c = 0; c < ctas; ++c) total += sh.mass[set][c];
+          target = share_of(share, total);
+          share = 1.f;
+        }
+        if (lo < hi) {
+          above = find_bin(above, target);
+          bin = sh.found;
+        }
       }
       auto there = [&](float x, uint32_t i) { return inside(x, i) && (!(lo < hi) || bins(x) == bin); };
       const uint32_t n = gather(there);
@@ -648,18 +707,48 @@ struct Row {
     }
   }
 
-  // The largest of bounds of 20 bits that at least `need` threads' elements (ord_f32 in [lo, hi], by its 20 bits)
-  // reach.
-  __device__ __forceinline__ uint32_t reached_by(int need, uint32_t key, uint32_t lo, uint32_t hi) {
-    key >>= 12;
-    const int bits = 32 - __clz((hi ^ lo) >> 12);
-    uint32_t reached = hi >> 12 >> bits << bits;
-#pragma unroll 1
-    for (int bit = bits - 1; bit >= 0; --bit) {
-      const uint32_t next = reached | (1u << bit);
-      if (__syncthreads_count(key >= next) >= need) reached = next;
+  // For need[0] and need[1]: a bound that at least so many of the threads' largest elements reach (keys by ord_f32; on:
+  // this thread's counts, they lie in [lo, hi]), to sh.reached; 0 where there are not so many.  By a histogram
+  // of them; sh.hist[0] is zero before.
+  __device__ __forceinline__ void reached_by(const int (&need)[2], bool on, uint32_t key, uint32_t lo, uint32_t hi) {
+    const Bins bins(unord_f32(lo), unord_f32(hi));           // (all in the first bin where lo == hi)
+    const int bin = on ? bins(unord_f32(key)) : -2;
+    if (tid < 2) {
+      sh.reached[tid] = 0;
+      sh.reached_bin[tid] = -1;
     }
-    return reached << 12;
+    if (on) atomicAdd(&sh.hist[0][bin], 1u);
+    __syncthreads();
+    constexpr int kEach = kBins / kThreads;
+    uint32_t mine[kEach], run = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) run += mine[e] = sh.hist[0][tid * kEach + e];
+    uint32_t upto = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    ++sums;
+    if (lane == 31) warp_sums()[warp] = upto;
+    __syncthreads();
+    upto -= run;
+    for (int w = 0; w < warp; ++w) upto += static_cast<uint32_t>(warp_sums()[w]);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (upto < static_cast<uint32_t>(need[x]) && upto + mine[e] >= static_cast<uint32_t>(need[x])) {
+          sh.reached_bin[x] = tid * kEach + e;
+          sh.reached[x] = kNone;
+        }
+      upto += mine[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (bin == sh.reached_bin[x]) atomicMin(&sh.reached[x], key);
+    __syncthreads();
   }
 
   // All that is kept is in the list: filters and draw, by the first CTA.
@@ -673,11 +762,27 @@ struct Row {
         w = sh.weights[tid] = weigh(ckey_score(key));
       }
       pair_sums(n, false, &place, &before);
-      if (k > 0 && place >= static_cast<uint32_t>(k)) w = 0;
-      if (top_p < 1.f && before >= share_of(top_p, block_total(w))) w = 0;
+      bool kept = tid < n && (k == 0 || place < static_cast<uint32_t>(k));
+      if (top_p < 1.f) {
+        const u64 enough = share_of(top_p, block_total(kept ? w : 0));
+        kept = kept && before < enough;
+      }
+      w = kept ? w : 0;
       const u64 total = block_total(w), to = place_of(u, total);
-      if (tid < n) sh.weights[tid] = w;
-      pair_sums(n, true, &place, &before);
+      // the kept ones come first in the order: they take the first places of the list
+      const uint32_t left = __syncthreads_count(kept);
+      if (kept) {
+        sh.list[place] = key;
+        sh.weights[place] = w;
+      }
+      __syncthreads();
+      if (tid < left) {
+        key = sh.list[tid];
+        w = sh.weights[tid];
+      } else {
+        w = 0;
+      }
+      pair_sums(left, true, &place, &before);
       if (before <= to && to < before + w) hit(ckey_score(key), static_cast<uint32_t>(ckey_idx(key)), total);
       return;
     }
@@ -686,8 +791,8 @@ struct Row {
     const uint32_t most = k > 0 ? min(n, static_cast<uint32_t>(k)) : n;
 #pragma unroll
     for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < most ? weigh(ckey_score(v[e])) : 0;
-    u64 run = block_before(own);
-    const u64 enough = top_p < 1.f ? share_of(top_p, block_total(own)) : ~0ull;
+    u64 sum, run = block_before(own, &sum);
+    const u64 enough = top_p < 1.f ? share_of(top_p, sum) : ~0ull;
     own = 0;
 #pragma unroll
     for (int e = 0; e < P; ++e) {
@@ -710,7 +815,7 @@ struct Row {
     own = 0;
 #pragma unroll
     for (int e = 0; e < P; ++e) own += w[e] = x[e] != 0 ? sh.weights[static_cast<uint32_t>(x[e])] : 0;
-    run = block_before(own);
+    run = block_before(own, &sum);
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       if (run <= to && to < run + w[e]) {
@@ -723,16 +828,15 @@ struct Row {
 };
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid_constant__ SamplingParams p) {
-  extern __shared__ __align__(16) unsigned char raw[];
-  Shared& sh = *reinterpret_cast<Shared*>(raw);
-  uint4* slice = reinterpret_cast<uint4*>(raw + (sizeof(Shared) + 15) / 16 * 16);
+__global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid_constant__ SamplingParams p) {
+  __shared__ Shared sh;
   constexpr int VEC = 16 / sizeof(E);
   const float inf = __int_as_float(0x7F800000);
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = p.ctas, rank = static_cast<int>(blockIdx.x) % ctas, b = static_cast<int>(blockIdx.x) / ctas;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  sh.pow[tid] = kPow.v[tid];
+  for (int i = tid; i < 512; i += kThreads) sh.pow[i] = kPow.v[i];
+  for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
   if (tid == 0) {
     sh.found = kNone;
     sh.listed = 0;
@@ -752,71 +856,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
     sh.min_lo = static_cast<float>(by - static_cast<double>(sh.min_hi));
   }
 
-  // --- the row's slice, and its largest ---------------------------------------------------
-  // Pieces of 16 aligned bytes; elements before the row and behind it are -inf.
   const E* logits = reinterpret_cast<const E*>(p.logits) + static_cast<size_t>(b) * p.stride;
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(logits) & 15u) / sizeof(E));
   const int pieces = (p.V + shift + VEC - 1) / VEC;
   const int first = min(rank * p.per, pieces), mine = min(p.per, pieces - first);
   const int per_warp = (mine + kWarps - 1) / kWarps;
-  Row<E> row{sh, slice, cluster, tid, lane, warp, rank, ctas, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
+  Row<E> row{sh, logits, p.V, cluster, tid, lane, warp, rank, ctas, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
              first * VEC - shift};
   Largest<E> largest;
-  {
-    constexpr int kUnroll = 4;
-    const E* from = logits + row.index0;
-#pragma unroll 1
-    for (int i0 = row.begin + lane; i0 < row.end; i0 += 32 * kUnroll) {
-      uint4 v[kUnroll];
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        const int i = i0 + 32 * j, at = row.index0 + i * VEC;
-        if (i >= row.end) continue;
-        if (at >= 0 && at + VEC <= p.V) {
-          v[j] = kv_load(reinterpret_cast<const uint4*>(from + i * VEC));
-        } else {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = sizeof(E) == 4 ? 0xFF800000u : std::is_same<E, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            if (at + e < 0 || at + e >= p.V) continue;
-            if constexpr (sizeof(E) == 4) {
-              w[e] = kv_load(reinterpret_cast<const uint32_t*>(logits) + at + e);
-            } else {
-              const uint32_t x = kv_load(reinterpret_cast<const uint16_t*>(logits) + at + e);
-              w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xFFFFu) | (x << 16) : (w[e >> 1] & 0xFFFF0000u) | x;
-            }
-          }
-          v[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kUnroll; ++j) {
-        const int i = i0 + 32 * j;
-        if (i >= row.end) continue;
-        slice[i] = v[j];
-        largest.add(v[j]);
-      }
-    }
-  }
+  row.template each_piece<4>([&](const uint4& v, int) { largest.add(v); });
   const float most = largest.get();      // NaN if any element is
   // Few enough are kept for one CTA: all of a small vocabulary, or a small top-k.  For that each CTA finds
   // what its share of k elements reach, and what k of them do, by its threads' largest: k elements of the row reach
   // the least of the CTAs' former bounds, and any of the latter.
-  const bool all_listed = p.V <= kList, few = k > 0 && k <= kPairs;
+  const bool all_listed = p.V <= kList, few = k > 0 && k <= kThreads / 4 * ctas && k <= kPairs;
   {
     const uint32_t key = most == most ? ord_f32(most) : kNone;   // (above +inf)
-    uint32_t lo = key, hi = key;
+    const bool some = key > ord_f32(-inf);
+    uint32_t lo = some ? key : kNone, hi = key;
     row.block_range(lo, hi);
-    const bool look = few && !all_listed && hi < ord_f32(inf);
-    const uint32_t share = look ? row.reached_by((k + ctas - 1) / ctas, key, lo, hi) : 0;
-    const uint32_t by_all = look && ctas > 1 ? row.reached_by(k, key, lo, hi) : share;
+    const bool look = few && !all_listed && hi < ord_f32(inf) && hi > ord_f32(-inf);
+    if (look) row.reached_by({(k + ctas - 1) / ctas, k}, some, key, lo, hi);
     if (tid < ctas) {
       Shared* o = row.at(tid);
       o->top[rank] = hi;
-      o->bound[0][rank] = share;
-      o->bound[1][rank] = by_all;
+      o->bound[0][rank] = look ? sh.reached[0] : 0;
+      o->bound[1][rank] = look ? sh.reached[1] : 0;
     }
   }
   cluster.sync();
@@ -932,37 +997,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(const __grid
       n += sh.count[set][c];
       lo = min(lo, sh.lo[set][c]);
     }
-    if (n > static_cast<uint32_t>(k)) kept = row.template select<false>(unord_f32(lo), m, kept, k, [](float) { return 1ull; });
+    if (n > static_cast<uint32_t>(k)) kept = row.template select<false>(unord_f32(lo), m, kept, k, 1.f, [](float) { return 1ull; });
   }
   if (top_p < 1.f) {
-    const u64 own = row.block_total(row.mass_of(weigh, kept));
+    // About the total; V elements of less than (1 - p) / V of it each cannot hold what top-p leaves out, so the
+    // cut is above that (2^-6 of an octave lower, for the roughness of the total and fp32's logarithms).
+    float rough = 0.f;
+    row.each([&](float x, uint32_t i) { rough += kept(x, i) ? weigh.roughly(x) : 0.f; });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) rough += __shfl_xor_sync(0xFFFFFFFFu, rough, o);
+    // (in units of 2^-20: a largest of at least half)
+    const u64 own = row.block_total(lane == 0 ? static_cast<u64>(rough * 0x1p20f) : 0);
     const int set = row.turn++ & 1;
     if (tid < ctas) row.at(tid)->mass[set][rank] = own;
     cluster.sync();
     u64 total = 0;
     for (int c = 0; c < ctas; ++c) total += sh.mass[set][c];
-    const u64 target = share_of(top_p, total);
-    // V elements of less than (total - target) / V each cannot hold the rest, so the cut is above that
-    // (fp32 logarithms and products here are right to 2^-10, the bound is taken 2^-7 lower)
     float lo = fmaxf(kept.x, weigh.least);
-    const float rest = static_cast<float>(total - target) / p.V;
-    if (rest > 1.f) lo = fmaxf(lo, fminf(m, weigh.ref + (weigh.top + log2f(rest) - kUnitBits - 0x1p-7f) / weigh.ch - 0x1p-20f * fabsf(weigh.ref)));
-    kept = row.template select<true>(lo, m, kept, target, weigh);
+    const float rest = static_cast<float>(total) * 0x1p-20f * (1.f - top_p) / p.V;
+    if (rest > 0.f) lo = fmaxf(lo, fminf(m, weigh.ref + (weigh.top + log2f(rest) - 0x1p-5f) / weigh.ch - 0x1p-20f * fabsf(weigh.ref)));
+    kept = row.template select<true>(lo, m, kept, 0, top_p, weigh);
   }
   row.find(row.mass_of(weigh, kept), [&](float x, uint32_t i) { return kept(x, i) ? weigh(x) : 0ull; },
            [&](u64 total) { return place_of(u, total); }, hit);
 }
 
 template <typename E>
-cudaError_t launch_sampling(const SamplingParams& p, int device, cudaStream_t stream) {
-  static std::atomic<u64> ready{0};           // devices whose kernel may use all its shared memory
-  const int smem = static_cast<int>((sizeof(Shared) + 15) / 16 * 16) + p.per * 16;
-  if (device > 63 || (ready.load() >> device & 1) == 0) {
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(sample_tokens_kernel<E>),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSamplingSmem);
-    if (e != cudaSuccess) return e;
-    if (device <= 63) ready.fetch_or(1ull << device);
-  }
+cudaError_t launch_rows(const SamplingParams& p, cudaStream_t stream) {
   cudaLaunchAttribute attrs[2] = {};
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
@@ -972,7 +1033,6 @@ cudaError_t launch_sampling(const SamplingParams& p, int device, cudaStream_t st
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.B * p.ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attrs;
   cfg.numAttrs = 2;
@@ -985,22 +1045,23 @@ cudaError_t launch_sampling(const SamplingParams& p, int device, cudaStream_t st
 bool sampling_plan(SamplingParams& p, int num_sms) {
   const long long size = p.dtype == LTK_F32 ? 4 : 2, vec = 16 / size;
   const long long pieces = (p.V + 2 * vec - 2) / vec;        // wherever the row begins
-  // CTAs of a row: as few as hold it in 76 KB each (two fit an SM), more where SMs would be idle and
-  // a CTA still has 8 KB to read.
+  // CTAs of a row: one for every 64 KB, more where SMs would be idle and a CTA still has 8 KB to read.
   int ctas = 1;
-  while (ctas < kMaxCtas && (pieces * 16 > ctas * 77824ll ||
+  const char* env = getenv("LTK_CTAS");
+  while (ctas < kMaxCtas && (pieces * 16 > ctas * 65536ll ||
                              (static_cast<long long>(p.B) * ctas * 2 <= num_sms && pieces * 16 > ctas * 8192ll)))
     ctas *= 2;
+  if (env) ctas = atoi(env);
   p.ctas = ctas;
   p.per = static_cast<int>((pieces + ctas - 1) / ctas);
-  return (sizeof(Shared) + 15) / 16 * 16 + p.per * 16ull <= kSamplingSmem && static_cast<long long>(p.B) * ctas <= 0x7FFFFFFF;
+  return static_cast<long long>(p.B) * ctas <= 0x7FFFFFFF;
 }
 
-cudaError_t launch_sampling(const SamplingParams& p, int device, cudaStream_t stream) {
+cudaError_t launch_sampling(const SamplingParams& p, cudaStream_t stream) {
   switch (p.dtype) {
-    case LTK_F32: return launch_sampling<float>(p, device, stream);
-    case LTK_F16: return launch_sampling<__half>(p, device, stream);
-    default: return launch_sampling<__nv_bfloat16>(p, device, stream);
+    case LTK_F32: return launch_rows<float>(p, stream);
+    case LTK_F16: return launch_rows<__half>(p, stream);
+    default: return launch_rows<__nv_bfloat16>(p, stream);
   }
 }
 

@@ -46,7 +46,7 @@ extern "C" ltk_status ltk_sample_tokens(const void* logits, int dtype, long long
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, device);
   if (e == cudaSuccess && !sampling_plan(p, num_sms)) return LTK_ERR_UNSUPPORTED;
-  if (e == cudaSuccess) e = launch_sampling(p, device, static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = launch_sampling(p, static_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) return LTK_OK;
   if (std::getenv("LTK_DEBUG")) std::fprintf(stderr, "ltk: ltk_sample_tokens: %s\n", cudaGetErrorString(e));
   cudaGetLastError();

@@ -5,8 +5,6 @@
 
 namespace ltk {
 
-constexpr int kSamplingSmem = 232448;    // shared memory of a CTA
-
 struct SamplingParams {
   const void* logits;                    // [B, V], rows stride elements apart
   long long stride;
@@ -27,8 +25,8 @@ struct SamplingParams {
   int ctas;                              // of a row
   int per;                               // 16-byte pieces of a CTA's slice
 };
-// Sets ctas and per; false: the vocabulary does not fit.
+// Sets ctas and per; false: too many rows.
 bool sampling_plan(SamplingParams& p, int num_sms);
-cudaError_t launch_sampling(const SamplingParams& p, int device, cudaStream_t stream);
+cudaError_t launch_sampling(const SamplingParams& p, cudaStream_t stream);
 
 }  // namespace ltk
