@@ -507,9 +507,9 @@ ltk_status ltk_kv_status(ltk_kv* h, int* device_status, void* stream);
  * -1 and -inf, a row with a NaN or +inf, or with a setting out of range
  * (temperature below 0, infinite or NaN, top_p below 0 or NaN, min_p outside
  * [0, 1], u NaN), -1 and NaN.
- * Weights are whole numbers in units of 2^-44 of the largest, right to 2^-32 of
- * themselves, their sums exact: a row's result depends on its logits and settings
- * only.  Needs no handle or workspace, neither allocates nor synchronises.
+ * Weights are whole numbers in units of 2^-44 of (about) the largest, right to
+ * 2^-30 of themselves (those below 2^-42 are never drawn), their sums exact: a row's
+ * result depends on its logits and settings only.  Needs no handle or workspace, neither allocates nor synchronises.
  */
 typedef struct {
   const float* temperature;

@@ -19,7 +19,8 @@
 // take what is left; the draw then takes one pass over the row.
 #include <cooperative_groups.h>
 
-#include <cstdlib>
+#include <cmath>
+
 #include "block_sort.cuh"
 #include "kv_tensor.cuh"
 #include "sampling_internal.cuh"
@@ -38,6 +39,8 @@ constexpr int kList = 1024;              // elements that one CTA takes
 constexpr int kPairs = 256;              // of them, that are all compared with one another
 constexpr int kUnitBits = 44;            // weights are in units of 2^-44
 constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr int kRun = 8;                  // 16-byte pieces that a thread reads at a time at first, and remembers the largest of
+constexpr int kRuns = 16;                // of these, at most
 
 // (1 - h) 2^(j / 512) in units of 2^-31, rounded, where 1 / (1 - h) = 1 + kWholeBits / 2^32 (see Weigher): by the
 // exponential series in double, at compile time.
@@ -66,6 +69,8 @@ struct Shared {
   uint32_t top[kMaxCtas], bound[2][kMaxCtas];
   u64 mass[2][kMaxCtas];
   uint32_t count[2][kMaxCtas], lo[2][kMaxCtas], hi[2][kMaxCtas];
+  u64 all[kMaxCtas];
+  float rough[kMaxCtas];
   u64 answer;
   // a CTA's own
   u64 warp_sum[2][kWarps];
@@ -75,10 +80,15 @@ struct Shared {
   float min_hi, min_lo;                  // T ln(min_p)
   uint32_t reached[2];
   int reached_bin[2];
+  float edge[2];
   union {
     struct {
-      uint32_t hist[3][kBins];           // counts, or weights in pieces of 15, 15 and 15 bits
+      uint32_t hist[3][kBins];           // counts, rough weights, or weights in pieces of 15, 15 and 15 bits
       u64 merged[kBins];
+    };
+    struct {                             // while the largest are looked for
+      uint32_t first_hist[kBins];
+      float run_top[kRuns][kThreads];    // of each run of pieces
     };
     struct {
       u64 weights[kList];                // the list's
@@ -126,6 +136,7 @@ struct Largest {
     one(w.z);
     one(w.w);
   }
+  __device__ __forceinline__ void with(const Largest& o) { one(o.v); }
   __device__ __forceinline__ float get() const {
     if constexpr (std::is_same<E, float>::value) return __uint_as_float(v);
     const float2 f = kv_unpack16(v, std::is_same<E, __nv_bfloat16>::value);
@@ -177,15 +188,29 @@ struct Weigher {
   // Two elements' weights, of those not below `least`, onto a sum: the same numbers, with the arithmetic two at a
   // time.
   __device__ __forceinline__ void add2_to(u64& sum, float x0, float x1) const {
+    u64 w0, w1;
+    two(x0, x1, w0, w1);
+    if (x0 >= least) sum += w0;
+    if (x1 >= least) sum += w1;
+  }
+  // The same, and those of elements above `over` (>= least) onto another.
+  __device__ __forceinline__ void add2_to(u64& sum, u64& above, float over, float x0, float x1) const {
+    u64 w0, w1;
+    two(x0, x1, w0, w1);
+    if (x0 >= least) sum += w0;
+    if (x1 >= least) sum += w1;
+    if (x0 > over) above += w0;
+    if (x1 > over) above += w1;
+  }
+  __device__ __forceinline__ void two(float x0, float x1, u64& w0, u64& w1) const {
     const uint64_t c = pack2(ch, ch), s = add2(pack2(x0, x1), pack2(-ref, -ref));
     const uint64_t t = fma2(s, c, pack2(kRound, kRound));
     const uint64_t d = fma2(t, pack2(-1.f, -1.f), pack2(kRound, kRound));
     const uint64_t r = fma2(s, pack2(cl, cl), fma2(s, c, d));
     const float2 v = unpack2(fma2(r, fma2(r, fma2(r, pack2(kC, kC), pack2(kB, kB)), pack2(kA, kA)), pack2(kWhole, kWhole)));
     const float2 tt = unpack2(t);
-    const u64 w0 = weight(__float_as_int(tt.x), v.x), w1 = weight(__float_as_int(tt.y), v.y);
-    if (x0 >= least) sum += w0;
-    if (x1 >= least) sum += w1;
+    w0 = weight(__float_as_int(tt.x), v.x);
+    w1 = weight(__float_as_int(tt.y), v.y);
   }
   // About the weight, from 0 to 1 (1% off at most).
   __device__ __forceinline__ float roughly(float x) const { return exp2_approx(fmaf(x - ref, ch, static_cast<float>(-top))); }
@@ -275,7 +300,8 @@ struct Row {
   int V;
   cg::cluster_group cluster;
   int tid, lane, warp, rank, ctas;
-  int begin, end;                        // this warp's pieces of the slice: 16 aligned bytes each
+  int slice;                             // pieces of this CTA's slice, 16 aligned bytes each
+  int begin, end;                        // this warp's of them
   int index0;                            // vocabulary index of the slice's first element
   int sums = 0;                          // which of warp_sum was used last
   int turn = 0;                          // which set of `mass`, `count`, `lo`, `hi` is next
@@ -287,13 +313,15 @@ struct Row {
     const uint32_t x = kv_load(reinterpret_cast<const uint16_t*>(logits) + i);
     return kv_unpack16(x, std::is_same<E, __nv_bfloat16>::value).x;
   }
+  static __device__ __forceinline__ uint4 nothing() {
+    const uint32_t w = sizeof(E) == 4 ? 0xFF800000u : std::is_same<E, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    return make_uint4(w, w, w, w);
+  }
   // A piece; elements before the row and behind it are -inf.
   __device__ __forceinline__ uint4 piece(int i) const {
     const int from = index0 + i * VEC;
     if (from >= 0 && from + VEC <= V) return kv_load(reinterpret_cast<const uint4*>(logits + from));
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = sizeof(E) == 4 ? 0xFF800000u : std::is_same<E, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+    uint32_t w[4] = {nothing().x, nothing().x, nothing().x, nothing().x};
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       if (from + e < 0 || from + e >= V) continue;
@@ -395,24 +423,43 @@ struct Row {
   // this thread's elements.  One meeting of the cluster.
   template <typename F, typename T, typename H>
   __device__ __forceinline__ void find(u64 mine, F f, T target, H hit) {
-    const u64 sum = block_total(mine);
-    const int set = turn++ & 1;
-    if (tid < ctas) at(tid)->mass[set][rank] = sum;
-    cluster.sync();
-    u64 total = 0, before = 0;
-    for (int c = 0; c < ctas; ++c) {
-      if (c < rank) before += sh.mass[set][c];
-      total += sh.mass[set][c];
-    }
-    const u64 t = target(total);
+    u64 before, total;
+    const u64 sum = block_total(mine), t = place_in_row(sum, target, &before, &total);
     if (t < before || t >= before + sum) return;
-    for (int w = 0; w < warp; ++w) before += warp_sums()[w];
-    if (t < before || t >= before + warp_sums()[warp]) return;
+    // All warps take a part of the one's that has it, a second time of that part's.
+    int from = 0, to = 0;
 #pragma unroll 1
-    for (int i0 = begin; i0 < end; i0 += 32) {
+    for (int level = 0; level < 3; ++level) {
+      int w = 0;
+      for (; w < kWarps - 1 && t >= before + warp_sums()[w]; ++w) before += warp_sums()[w];
+      if (level == 0) {
+        const int each_warp = (slice + kWarps - 1) / kWarps;
+        from = min(w * each_warp, slice);
+        to = min(from + each_warp, slice);
+      } else {
+        const int part = (to - from + kWarps - 1) / kWarps;
+        from = min(from + w * part, to);
+        to = min(from + part, to);
+      }
+      if (to - from <= 32) break;
+      const int part = (to - from + kWarps - 1) / kWarps;
+      const int a = min(from + warp * part, to), b = min(a + part, to);
+      u64 own = 0;
+#pragma unroll 1
+      for (int i = a + lane; i < b; i += 32) {
+        float x[VEC];
+        unpack<E>(piece(i), x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) own += f(x[e], static_cast<uint32_t>(index0 + i * VEC + e));
+      }
+      block_total(own);
+    }
+    if (warp != 0) return;
+#pragma unroll 1
+    for (int i0 = from; i0 < to; i0 += 32) {
       const int i = i0 + lane;
       u64 own = 0;
-      if (i < end) {
+      if (i < to) {
         float x[VEC];
         unpack<E>(piece(i), x);
 #pragma unroll
@@ -440,6 +487,20 @@ struct Row {
       before = __shfl_sync(0xFFFFFFFFu, run, 31);
     }
   }
+  // What `target` makes of the total over the CTAs, that total, and the sum over the CTAs before this one.  One
+  // meeting of the cluster.
+  template <typename T>
+  __device__ __forceinline__ u64 place_in_row(u64 sum, T target, u64* before, u64* total) {
+    const int set = turn++ & 1;
+    if (tid < ctas) at(tid)->mass[set][rank] = sum;
+    cluster.sync();
+    *total = *before = 0;
+    for (int c = 0; c < ctas; ++c) {
+      if (c < rank) *before += sh.mass[set][c];
+      *total += sh.mass[set][c];
+    }
+    return target(*total);
+  }
 
   // Elements that `take` accepts into the first CTA's list, and how many there are; nothing is listed when they are
   // too many.  Meetings: one, and a second when they fit.
@@ -448,15 +509,20 @@ struct Row {
     if (tid == 0) sh.listed = 0;
     __syncthreads();
     each([&](float x, uint32_t i) {
-      if (take(x, i)) {
-        const uint32_t to = atomicAdd(&sh.listed, 1u);
-        if (to < kList) sh.list[to] = ckey(x, static_cast<int>(i));
-      }
+      if (take(x, i)) enlist(x, i);
     });
     __syncthreads();
     const int set = turn++ & 1;
     if (tid < ctas) at(tid)->count[set][rank] = sh.listed;
     cluster.sync();
+    return lists_to_first(set);
+  }
+  __device__ __forceinline__ void enlist(float x, uint32_t i) {
+    const uint32_t to = atomicAdd(&sh.listed, 1u);
+    if (to < kList) sh.list[to] = ckey(x, static_cast<int>(i));
+  }
+  // The CTAs' lists, of sh.count[set] elements, to the first one's; how many they are.
+  __device__ __forceinline__ uint32_t lists_to_first(int set) {
     uint32_t n = 0;
     for (int c = 0; c < ctas; ++c) n += sh.count[set][c];   // (of at most 2^20 elements)
     if (n > kList || ctas == 1) return n;
@@ -471,6 +537,40 @@ struct Row {
     }
     cluster.sync();
     return n;
+  }
+  // The smallest and largest element that `take` accepts (by ord_f32), over the row.  One meeting.
+  template <typename F>
+  __device__ __forceinline__ void range_of(F take, uint32_t* least, uint32_t* most) {
+    uint32_t a = kNone, b = 0;
+    each([&](float x, uint32_t i) {
+      if (take(x, i)) {
+        a = min(a, ord_f32(x));
+        b = max(b, ord_f32(x));
+      }
+    });
+    block_range(a, b);
+    const int set = turn++ & 1;
+    if (tid < ctas) {
+      at(tid)->lo[set][rank] = a;
+      at(tid)->hi[set][rank] = b;
+    }
+    cluster.sync();
+    for (int c = 0; c < ctas; ++c) {
+      a = min(a, sh.lo[set][c]);
+      b = max(b, sh.hi[set][c]);
+    }
+    *least = a;
+    *most = b;
+  }
+  // The cut that the first CTA finds in its list of n.  One meeting.
+  template <bool MASS, typename F>
+  __device__ __forceinline__ Cut cut_of_list(uint32_t n, u64 above, u64 target, F f) {
+    if (rank == 0) {
+      cut_list<MASS>(n, above, target, f);
+      if (tid > 0 && tid < ctas) at(tid)->answer = sh.answer;
+    }
+    cluster.sync();
+    return cut_at(sh.answer);
   }
 
   // Of each of the list's n <= kPairs elements, by thread i < n: how many of the others come before it and what
@@ -616,61 +716,39 @@ struct Row {
     return sh.found_before;
   }
 
-  // Of the kept elements with x <= hi, in descending order: where the running sum of f reaches `target` (the sum over
-  // those with lo <= x does).  MASS: f are weights, else ones.  A `share` below 1 in place of a target: that share of the
-  // sum over all kept ones.
+  // The CTAs' histograms, summed into every CTA's `merged`.  Two meetings.
+  template <bool MASS>
+  __device__ __forceinline__ void merge_bins() {
+    cluster.sync();
+    const int part = (kBins + ctas - 1) / ctas;
+    for (int b = rank * part + tid; b < min((rank + 1) * part, kBins); b += kThreads) {
+      u64 sum = 0;
+      for (int c = 0; c < ctas; ++c) sum += bin_sum<MASS>(*at(c), b);
+      for (int c = 0; c < ctas; ++c) at(c)->merged[b] = sum;
+    }
+    cluster.sync();
+  }
+  // Of the kept elements with lo <= x <= hi, in descending order: where the running sum of f, from `above`, reaches
+  // `target` (with all of them it does).  MASS: f are weights, else ones.
   template <bool MASS, typename F>
-  __device__ Cut select(float lo, float hi, const Cut kept, u64 target, float share, F f) {
-    u64 above = 0;
+  __device__ Cut select(float lo, float hi, const Cut kept, u64 above, u64 target, F f) {
 #pragma unroll 1
     while (true) {
       const Bins bins(lo, hi);
       auto inside = [&](float x, uint32_t i) { return x >= lo && x <= hi && kept(x, i); };
       int bin = 0;
-      if (lo < hi || share < 1.f) {
+      if (lo < hi) {
         clear_bins();
-        u64 below = 0;
         each([&](float x, uint32_t i) {
-          if (inside(x, i)) add_to_bin<MASS>(lo < hi ? bins(x) : 0, f(x));
-          else if (MASS && share < 1.f && kept(x, i)) below += f(x);
+          if (inside(x, i)) add_to_bin<MASS>(bins(x), f(x));
         });
-        int set = 0;
-        if (share < 1.f) {
-          below = block_total(below);
-          set = turn++ & 1;
-          if (tid < ctas) at(tid)->mass[set][rank] = below;
-        }
-        cluster.sync();
-        const int part = kBins / ctas;
-        for (int b = rank * part + tid; b < (rank + 1) * part; b += kThreads) {
-          u64 sum = 0;
-          for (int c = 0; c < ctas; ++c) sum += bin_sum<MASS>(*at(c), b);
-          for (int c = 0; c < ctas; ++c) at(c)->merged[b] = sum;
-        }
-        cluster.sync();
-        if (share < 1.f) {
-          u64 own = 0, total;
-          for (int b = tid; b < kBins; b += kThreads) own += sh.merged[b];
-          block_before(own, &total);
-          for (int c = 0; c < ctas; ++c) total += sh.mass[set][c];
-          target = share_of(share, total);
-          share = 1.f;
-        }
-        if (lo < hi) {
-          above = find_bin(above, target);
-          bin = sh.found;
-        }
+        merge_bins<MASS>();
+        above = find_bin(above, target);
+        bin = sh.found;
       }
       auto there = [&](float x, uint32_t i) { return inside(x, i) && (!(lo < hi) || bins(x) == bin); };
       const uint32_t n = gather(there);
-      if (n <= kList) {
-        if (rank == 0) {
-          cut_list<MASS>(n, above, target, f);
-          if (tid > 0 && tid < ctas) at(tid)->answer = sh.answer;
-        }
-        cluster.sync();
-        return cut_at(sh.answer);
-      }
+      if (n <= kList) return cut_of_list<MASS>(n, above, target, f);
       if (!(lo < hi)) {
         // equal values, more than a list holds: the last one is found by its index
         const u64 one = f(lo), need = (target - above + one - 1) / one;
@@ -684,27 +762,140 @@ struct Row {
         return cut_at(sh.answer);
       }
       // the bin's own range is the next one
-      uint32_t a = kNone, b = 0;
-      each([&](float x, uint32_t i) {
-        if (there(x, i)) {
-          a = min(a, ord_f32(x));
-          b = max(b, ord_f32(x));
-        }
-      });
-      block_range(a, b);
-      const int set = turn++ & 1;
-      if (tid < ctas) {
-        at(tid)->lo[set][rank] = a;
-        at(tid)->hi[set][rank] = b;
-      }
-      cluster.sync();
-      for (int c = 0; c < ctas; ++c) {
-        a = min(a, sh.lo[set][c]);
-        b = max(b, sh.hi[set][c]);
-      }
+      uint32_t a, b;
+      range_of(there, &a, &b);
       lo = unord_f32(a);
       hi = unord_f32(b);
     }
+  }
+
+  // The end of what `bins` puts into bins from `bin` on (up: or into those up to `bin`): the largest x (smallest x) of
+  // those, by ord_f32, between lo and hi, of which one is there at least.  By a whole warp.
+  __device__ __forceinline__ float edge_of(const Bins& bins, uint32_t lo, uint32_t hi, int bin, bool up) const {
+    while (lo < hi) {
+      // 32 places up to the other end; those that are in come first
+      const uint32_t step = static_cast<uint32_t>((static_cast<u64>(hi - lo) * (lane + 1) + 31) / 32);
+      const uint32_t x = up ? hi - step : lo + step;
+      const int n = __popc(__ballot_sync(0xFFFFFFFFu, up ? bins(unord_f32(x)) <= bin : bins(unord_f32(x)) >= bin));
+      const uint32_t last = __shfl_sync(0xFFFFFFFFu, x, max(n - 1, 0)), next = __shfl_sync(0xFFFFFFFFu, x, min(n, 31));
+      if (up) {
+        if (n > 0) hi = last;
+        if (n < 32) lo = next + 1;
+      } else {
+        if (n > 0) lo = last;
+        if (n < 32) hi = next - 1;
+      }
+    }
+    return unord_f32(up ? hi : lo);
+  }
+
+  // Where the weights of the kept elements, in descending order, reach the share p of their sum.  *mine: the
+  // weight of this thread's that are kept then.
+  //
+  // A histogram of rough weights (fp32, right to 2^-17, in whole units of 2^-30 of their sum) shows in which few bins
+  // the cut can be; one pass with exact weights then sums what lies above them and all, and lists what is in them.
+  __device__ Cut select_share(float hi, const Cut kept, float p, const Weigher& weigh, u64* mine) {
+    const bool simple = kept.i == kNone; // no cut among equal elements so far
+    const float least = fmaxf(kept.x, fmaxf(weigh.least, -__int_as_float(0x7F7FFFFF)));
+    auto counts = [&](float x, uint32_t i) { return x >= least && (simple || kept(x, i)); };
+    float rough = 0.f;
+    each([&](float x, uint32_t i) { rough += counts(x, i) ? weigh.roughly(x) : 0.f; });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) rough += __shfl_xor_sync(0xFFFFFFFFu, rough, o);
+    // (in units of 2^-20: the largest is at least half)
+    const u64 cta = block_total(lane == 0 ? static_cast<u64>(rough * 0x1p20f) : 0);
+    if (tid < ctas) at(tid)->rough[rank] = static_cast<float>(cta);
+    clear_bins();
+    cluster.sync();
+    rough = 0.f;
+    for (int c = 0; c < ctas; ++c) rough += sh.rough[c];
+    const float unit = 0x1p50f / rough;                      // 2^30 / (rough 2^-20)
+    // V elements of less than (1 - p) / V of the sum cannot hold what is left out, so the cut is above that
+    float lo = least;
+    const float rest = rough * 0x1p-20f * (1.f - p) / V;
+    if (rest > 0.f) lo = fmaxf(lo, fminf(hi, weigh.ref + (weigh.top + log2f(rest) - 0x1p-5f) / weigh.ch - 0x1p-20f * fabsf(weigh.ref)));
+    const Bins bins(fminf(lo, hi), hi);
+    each([&](float x, uint32_t i) {
+      if (x >= lo && (simple || kept(x, i))) atomicAdd(&sh.hist[0][bins(x)], __float2uint_rz(weigh.roughly(x) * unit));
+    });
+    merge_bins<false>();
+    {
+      u64 own = 0, total;
+      constexpr int kEach = kBins / kThreads;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) own += sh.merged[tid * kEach + e];
+      u64 run = block_before(own, &total);
+      // weights are off by 2^-17 of themselves and one unit each, their sum by 2^-17 of itself
+      const float t = 0x1p30f * p, off = 0x1p15f + V;
+      if (tid == 0) {
+        sh.reached_bin[0] = kBins - 1;
+        sh.reached_bin[1] = kBins - 1;
+        sh.listed = 0;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const float a = static_cast<float>(run);
+        run += sh.merged[tid * kEach + e];
+        const float b = static_cast<float>(run);
+        if (a < t - off && b >= t - off) sh.reached_bin[0] = tid * kEach + e;
+        if (a < t + off && b >= t + off) sh.reached_bin[1] = tid * kEach + e;
+        if (tid + e == 0 && !(0.f < t - off)) sh.reached_bin[0] = 0;
+      }
+      __syncthreads();
+      // those bins as a range of x: above it is what lies in bins before them
+      if (warp < 2) {
+        const float x = edge_of(bins, ord_f32(fminf(lo, hi)), ord_f32(hi), sh.reached_bin[warp], warp == 1);
+        if (lane == 0) sh.edge[warp] = x;
+      }
+      __syncthreads();
+    }
+    // (a first bin without any x: the edge is that of the bins after it)
+    const float from = sh.edge[1], upto = sh.edge[0];
+    u64 all = 0, above = 0;
+    if (simple && kept.x <= weigh.least) {
+      each_piece<2>([&](const uint4& v, int i) {
+        float x[VEC];
+        unpack<E>(v, x);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) weigh.add2_to(all, above, upto, x[e], x[e + 1]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (x[e] >= from && x[e] <= upto) enlist(x[e], static_cast<uint32_t>(index0 + i * VEC + e));
+      });
+    } else {
+      each([&](float x, uint32_t i) {
+        if (!counts(x, i)) return;
+        const u64 w = weigh(x);
+        all += w;
+        if (x > upto) above += w;
+        else if (x >= from) enlist(x, i);
+      });
+    }
+    *mine = above;
+    const u64 cta_above = block_total(above), cta_all = block_total(all);
+    const int set = turn++ & 1;
+    if (tid < ctas) {
+      at(tid)->mass[set][rank] = cta_above;
+      at(tid)->all[rank] = cta_all;
+      at(tid)->count[set][rank] = sh.listed;
+    }
+    cluster.sync();
+    above = 0;
+    u64 total = 0;
+    for (int c = 0; c < ctas; ++c) {
+      above += sh.mass[set][c];
+      total += sh.all[c];
+    }
+    const u64 target = share_of(p, total);
+    const uint32_t n = lists_to_first(set);
+    Cut end;
+    if (n <= kList) end = cut_of_list<true>(n, above, target, weigh);
+    else end = select<true>(from, upto, kept, above, target, weigh);
+    each([&](float x, uint32_t i) {
+      if (x >= from && x <= upto && counts(x, i) && end(x, i)) *mine += weigh(x);
+    });
+    return end;
   }
 
   // For need[0] and need[1]: a bound that at least so many of the threads' largest elements reach (keys by ord_f32; on:
@@ -861,10 +1052,23 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
   const int pieces = (p.V + shift + VEC - 1) / VEC;
   const int first = min(rank * p.per, pieces), mine = min(p.per, pieces - first);
   const int per_warp = (mine + kWarps - 1) / kWarps;
-  Row<E> row{sh, logits, p.V, cluster, tid, lane, warp, rank, ctas, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
+  Row<E> row{sh, logits, p.V, cluster, tid, lane, warp, rank, ctas, mine, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
              first * VEC - shift};
   Largest<E> largest;
-  row.template each_piece<4>([&](const uint4& v, int) { largest.add(v); });
+  {
+    int run = 0;
+#pragma unroll 1
+    for (int i0 = row.begin + lane; i0 < row.end; i0 += 32 * kRun, ++run) {
+      uint4 v[kRun];
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) v[j] = i0 + 32 * j < row.end ? row.piece(i0 + 32 * j) : row.nothing();
+      Largest<E> of_run;
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) of_run.add(v[j]);
+      sh.run_top[run][tid] = of_run.get();
+      largest.with(of_run);
+    }
+  }
   const float most = largest.get();      // NaN if any element is
   // Few enough are kept for one CTA: all of a small vocabulary, or a small top-k.  For that each CTA finds
   // what its share of k elements reach, and what k of them do, by its threads' largest: k elements of the row reach
@@ -933,12 +1137,27 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
     const uint32_t room = kList / ctas;
     if (most >= from) {
       u64* list = row.at(0)->list + rank * room;
-      row.each([&](float x, uint32_t i) {
-        if (x >= from) {
-          const uint32_t to = atomicAdd(&sh.listed, 1u);
-          if (to < room) list[to] = ckey(x, static_cast<int>(i));
+      int run = 0;
+#pragma unroll 1
+      for (int i0 = row.begin + lane; i0 < row.end; i0 += 32 * kRun, ++run) {
+        if (!(sh.run_top[run][tid] >= from)) continue;
+        uint4 v[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) v[j] = i0 + 32 * j < row.end ? row.piece(i0 + 32 * j) : row.nothing();
+#pragma unroll 1
+        for (int j = 0; j < kRun; ++j) {
+          float x[VEC];
+          unpack<E>(v[0], x);
+#pragma unroll
+          for (int q = 1; q < kRun; ++q) v[q - 1] = v[q];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (x[e] >= from) {
+              const uint32_t to = atomicAdd(&sh.listed, 1u);
+              if (to < room) list[to] = ckey(x[e], row.index0 + (i0 + 32 * j) * VEC + e);
+            }
         }
-      });
+      }
     }
     __syncthreads();
     const int set = row.turn++ & 1;
@@ -997,28 +1216,12 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
       n += sh.count[set][c];
       lo = min(lo, sh.lo[set][c]);
     }
-    if (n > static_cast<uint32_t>(k)) kept = row.template select<false>(unord_f32(lo), m, kept, k, 1.f, [](float) { return 1ull; });
+    if (n > static_cast<uint32_t>(k)) kept = row.template select<false>(unord_f32(lo), m, kept, 0, k, [](float) { return 1ull; });
   }
-  if (top_p < 1.f) {
-    // About the total; V elements of less than (1 - p) / V of it each cannot hold what top-p leaves out, so the
-    // cut is above that (2^-6 of an octave lower, for the roughness of the total and fp32's logarithms).
-    float rough = 0.f;
-    row.each([&](float x, uint32_t i) { rough += kept(x, i) ? weigh.roughly(x) : 0.f; });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rough += __shfl_xor_sync(0xFFFFFFFFu, rough, o);
-    // (in units of 2^-20: a largest of at least half)
-    const u64 own = row.block_total(lane == 0 ? static_cast<u64>(rough * 0x1p20f) : 0);
-    const int set = row.turn++ & 1;
-    if (tid < ctas) row.at(tid)->mass[set][rank] = own;
-    cluster.sync();
-    u64 total = 0;
-    for (int c = 0; c < ctas; ++c) total += sh.mass[set][c];
-    float lo = fmaxf(kept.x, weigh.least);
-    const float rest = static_cast<float>(total) * 0x1p-20f * (1.f - top_p) / p.V;
-    if (rest > 0.f) lo = fmaxf(lo, fminf(m, weigh.ref + (weigh.top + log2f(rest) - 0x1p-5f) / weigh.ch - 0x1p-20f * fabsf(weigh.ref)));
-    kept = row.template select<true>(lo, m, kept, 0, top_p, weigh);
-  }
-  row.find(row.mass_of(weigh, kept), [&](float x, uint32_t i) { return kept(x, i) ? weigh(x) : 0ull; },
+  u64 mass;
+  if (top_p < 1.f) kept = row.select_share(m, kept, top_p, weigh, &mass);
+  else mass = row.mass_of(weigh, kept);
+  row.find(mass, [&](float x, uint32_t i) { return kept(x, i) ? weigh(x) : 0ull; },
            [&](u64 total) { return place_of(u, total); }, hit);
 }
 
@@ -1045,13 +1248,18 @@ cudaError_t launch_rows(const SamplingParams& p, cudaStream_t stream) {
 bool sampling_plan(SamplingParams& p, int num_sms) {
   const long long size = p.dtype == LTK_F32 ? 4 : 2, vec = 16 / size;
   const long long pieces = (p.V + 2 * vec - 2) / vec;        // wherever the row begins
-  // CTAs of a row: one for every 64 KB, more where SMs would be idle and a CTA still has 8 KB to read.
+  // CTAs of a row: as many as make the rounds of all rows' CTAs (four an SM, and clusters leave some places empty)
+  // the shortest; a CTA has some 5 us to spend on what does not grow with its slice, and 15 us for 64 KB.
   int ctas = 1;
-  const char* env = getenv("LTK_CTAS");
-  while (ctas < kMaxCtas && (pieces * 16 > ctas * 65536ll ||
-                             (static_cast<long long>(p.B) * ctas * 2 <= num_sms && pieces * 16 > ctas * 8192ll)))
-    ctas *= 2;
-  if (env) ctas = atoi(env);
+  double best = 0;
+  for (int c = 1; c <= kMaxCtas; ++c) {
+    const double rounds = std::ceil(p.B * static_cast<double>(c) / (3.8 * num_sms)), time = rounds * (5.0 + pieces * 16.0 / c * (15.0 / 65536.0));
+    if (pieces * 16 > static_cast<long long>(c) * kRuns * kRun * kThreads * 16) continue;
+    if (best == 0 || time < best) {
+      best = time;
+      ctas = c;
+    }
+  }
   p.ctas = ctas;
   p.per = static_cast<int>((pieces + ctas - 1) / ctas);
   return static_cast<long long>(p.B) * ctas <= 0x7FFFFFFF;
