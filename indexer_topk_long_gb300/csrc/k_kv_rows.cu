@@ -186,8 +186,9 @@ __device__ __forceinline__ void enter_unit(const AttnParams& p, Cursor& c) {
 }
 
 // Dense: stand on unit u of sequence b (whose tile count is known to be > 0).
+template <bool STEPS>
 __device__ __forceinline__ void enter_seq(const AttnParams& p, Cursor& c, int b) {
-  const KvSeq s = kv_seq(p.batch, p.cache, b);
+  const KvSeq s = kv_seq<STEPS>(p.batch, p.cache, b);
   c.w.b = b;
   c.w.q0 = s.q0;
   c.w.nq = s.nq;
@@ -198,7 +199,7 @@ __device__ __forceinline__ void enter_seq(const AttnParams& p, Cursor& c, int b)
 }
 
 // One tile forward.
-template <bool SEL, int RT>
+template <bool SEL, bool STEPS, int RT>
 __device__ __forceinline__ void advance(const AttnParams& p, Cursor& c) {
   --c.left;
   if (++c.t < c.n_tiles || c.left <= 0) return;
@@ -211,7 +212,7 @@ __device__ __forceinline__ void advance(const AttnParams& p, Cursor& c) {
       c.u = 0;
       int b = c.w.b;
       do {
-        enter_seq(p, c, ++b);
+        enter_seq<STEPS>(p, c, ++b);
       } while (c.n_tiles == 0 && b + 1 < p.batch.B);
     }
     enter_unit<SEL, RT>(p, c);
@@ -223,7 +224,7 @@ struct Feed {            // what the next tile's copies need, fetched a step ahe
   int page[kGroups];     // dense: the groups' pages, -1 beyond the length
 };
 
-template <int D, bool SEL, int RT>
+template <int D, bool SEL, bool STEPS, int RT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const AttnParams p, const int grid) {
   using S = RowsSmem<D, RT>;
   constexpr int kRows = S::kRows;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     long long mine = 0;
     int sk, t0;
     for (int b = b0; b < b1; ++b) {
-      const KvSeq s = kv_seq(p.batch, p.cache, b);
+      const KvSeq s = kv_seq<STEPS>(p.batch, p.cache, b);
       mine += static_cast<long long>(tiles_of(p, s, &sk, &t0)) * groups_of<RT>(s.nq * p.group) * p.cache.heads;
     }
     long long incl = mine;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     if (mine > 0 && start >= before && start < before + mine) {
       long long x = before;
       for (int b = b0; b < b1; ++b) {
-        const KvSeq s = kv_seq(p.batch, p.cache, b);
+        const KvSeq s = kv_seq<STEPS>(p.batch, p.cache, b);
         const long long n = static_cast<long long>(tiles_of(p, s, &sk, &t0)) * groups_of<RT>(s.nq * p.group) * p.cache.heads;
         if (start < x + n) {
           sh_b = b;
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       head.unit = start / tiles;
       head.t = static_cast<int>(start % tiles);
     } else {
-      enter_seq(p, head, sh_b);
+      enter_seq<STEPS>(p, head, sh_b);
       const long long in = start - sh_start;
       head.u = static_cast<int>(in / head.n_tiles);
       head.t = static_cast<int>(in % head.n_tiles);
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     } else {
       const int tile = pc.t < pc.w.skip ? pc.t : pc.t - pc.w.skip + pc.w.tile0;
       const int key0 = tile * kTileKeys + warp * kWarpKeys;
-      const int* table = p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + pc.w.page0;
+      const int* table = p.batch.page_table + static_cast<size_t>(pc.w.b) * p.batch.width + (STEPS ? pc.w.page0 : 0);
 #pragma unroll
       for (int h = 0; h < kGroups; ++h)
         if (key0 + 16 * h < pc.w.len) feed.page[h] = kv_load(table + ((key0 + 16 * h) >> p.cache.page_log2));
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
           }
         }
       }
-      advance<SEL, RT>(p, pc);
+      advance<SEL, STEPS, RT>(p, pc);
       fetch();
     }
     cp_commit();
@@ -421,8 +422,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
 
   // Dense: rows of sequences whose queries see no token have no tile on the line.
   if constexpr (!SEL) {
-    for (long long n = blockIdx.x; n < p.batch.N && p.step != 1; n += grid) {
-      const KvSeq s = kv_seq(p.batch, p.cache, kv_seq_of_query(p.batch, static_cast<int>(n)));
+    for (long long n = blockIdx.x; n < p.batch.N && !(STEPS && p.step == 1); n += grid) {
+      const KvSeq s = kv_seq<STEPS>(p.batch, p.cache, kv_seq_of_query(p.batch, static_cast<int>(n)));
       if (s.len > 0 && n >= s.q0 && n < s.q0 + s.nq) continue;
       for (int i = tid; i < p.q_heads * D; i += kThreads) reinterpret_cast<uint16_t*>(p.out)[n * p.q_heads * D + i] = 0;
       if (p.lse != nullptr)
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
       e = amax > 0.f && amax < __int_as_float(0x7F800000) ? max(e, -118) : 0;
       const float by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
       const float scale = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      const int pos = on ? (SEL ? head.w.pos0 : max(head.w.pos0 + qi * p.batch.advance, -1)) : -1;   // (from -1 any window is within 32 bits)
+      const int pos = on ? (SEL ? head.w.pos0 : max(head.w.pos0 + (STEPS ? qi * p.batch.advance : qi), -1)) : -1;   // (from -1 any window is within 32 bits)
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
         crow[x][n] = __shfl_sync(0xFFFFFFFFu, scale, (2 * cq + n) * 4);
@@ -507,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
 #pragma unroll
       for (int n = 0; n < 2; ++n) l[x][n] = !SEL && prow[x][n] >= head.w.len ? __int_as_float(0x7FC00000) : 0.f;
     }
-    const int p_lo = SEL ? 0 : head.w.pos0 + head.w.row0 / p.group * p.batch.advance;
-    const int p_hi = SEL ? 0 : head.w.pos0 + min(head.w.row0 + kRows - 1, rows_all - 1) / p.group * p.batch.advance;
+    const int p_lo = SEL ? 0 : head.w.pos0 + head.w.row0 / p.group * (STEPS ? p.batch.advance : 1);
+    const int p_hi = SEL ? 0 : head.w.pos0 + min(head.w.row0 + kRows - 1, rows_all - 1) / p.group * (STEPS ? p.batch.advance : 1);
     if (!SEL && p_hi >= head.w.len && tid == 0) raise_status(p.status, kDevArg);
 
 #pragma unroll 1
@@ -710,10 +711,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     auto write_row = [&](int r, int ch, float4 v, float m2, float sum) {
       const int row = head.w.row0 + r;
       const size_t at = (static_cast<size_t>(head.w.q0) + row / p.group) * p.q_heads + head.w.head * p.group + row % p.group;
-      const bool joined = !SEL && p.step == 2 && head.w.page0 > 0;
+      const bool joined = STEPS && p.step == 2 && head.w.page0 > 0;
       const RowEnd e = row_end(p, at, joined, m2 - kBoost, sum);
       v = make_float4(v.x * e.own, v.y * e.own, v.z * e.own, v.w * e.own);
-      if (!SEL && p.step == 1) {
+      if (STEPS && p.step == 1) {
         reinterpret_cast<float4*>(p.mid + at * D)[ch] = v;
         if (ch == 0) p.mid_lse[at] = e.lse2;
         return;
@@ -788,21 +789,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     at += n;
     head.left -= n - 1;
     head.t = t_end - 1;
-    advance<SEL, RT>(p, head);
+    advance<SEL, STEPS, RT>(p, head);
   }
   cp_wait<0>();
 }
 
-template <int D, bool SEL, int RT>
+template <int D, bool SEL, bool STEPS, int RT>
 cudaError_t init_rows() {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_rows_kernel<D, SEL, RT>),
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_rows_kernel<D, SEL, STEPS, RT>),
                               cudaFuncAttributeMaxDynamicSharedMemorySize, RowsSmem<D, RT>::kBytes);
 }
 
-template <int D, bool SEL>
+template <int D, bool SEL, bool STEPS>
 cudaError_t launch_rows(const AttnParams& p, bool narrow, int grid, cudaStream_t stream) {
-  return narrow ? launch_overlapped(kv_rows_kernel<D, SEL, 1>, grid, kThreads, RowsSmem<D, 1>::kBytes, stream, p, grid)
-                : launch_overlapped(kv_rows_kernel<D, SEL, 2>, grid, kThreads, RowsSmem<D, 2>::kBytes, stream, p, grid);
+  return narrow ? launch_overlapped(kv_rows_kernel<D, SEL, STEPS, 1>, grid, kThreads, RowsSmem<D, 1>::kBytes, stream, p, grid)
+                : launch_overlapped(kv_rows_kernel<D, SEL, STEPS, 2>, grid, kThreads, RowsSmem<D, 2>::kBytes, stream, p, grid);
+}
+template <int D>
+cudaError_t launch_rows(const AttnParams& p, bool narrow, int grid, cudaStream_t stream) {
+  if (p.idx != nullptr) return launch_rows<D, true, false>(p, narrow, grid, stream);
+  return p.step != 0 ? launch_rows<D, false, true>(p, narrow, grid, stream) : launch_rows<D, false, false>(p, narrow, grid, stream);
 }
 
 }  // namespace
@@ -811,9 +817,10 @@ size_t kv_rows_part_floats(int num_sms) { return static_cast<size_t>(2) * kCtasP
 int kv_rows_counters(int num_sms) { return kCtasPerSm * num_sms; }
 
 cudaError_t kv_rows_init() {
-  const cudaError_t e[8] = {init_rows<128, false, 1>(), init_rows<128, false, 2>(), init_rows<128, true, 1>(),
-                            init_rows<128, true, 2>(),  init_rows<64, false, 1>(),  init_rows<64, false, 2>(),
-                            init_rows<64, true, 1>(),   init_rows<64, true, 2>()};
+  const cudaError_t e[] = {init_rows<128, false, false, 1>(), init_rows<128, false, false, 2>(), init_rows<128, true, false, 1>(),
+                           init_rows<128, true, false, 2>(),  init_rows<128, false, true, 1>(),  init_rows<128, false, true, 2>(),
+                           init_rows<64, false, false, 1>(),  init_rows<64, false, false, 2>(),  init_rows<64, true, false, 1>(),
+                           init_rows<64, true, false, 2>(),   init_rows<64, false, true, 1>(),   init_rows<64, false, true, 2>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -824,8 +831,7 @@ cudaError_t launch_kv_rows(const AttnParams& p, int max_q, int num_sms, cudaStre
   const int grid = kCtasPerSm * num_sms;
   const bool narrow = static_cast<long long>(p.group) * (sel ? 1 : max_q) <= 8;
   count_launches(1);
-  if (p.dim == 128) return sel ? launch_rows<128, true>(p, narrow, grid, stream) : launch_rows<128, false>(p, narrow, grid, stream);
-  return sel ? launch_rows<64, true>(p, narrow, grid, stream) : launch_rows<64, false>(p, narrow, grid, stream);
+  return p.dim == 128 ? launch_rows<128>(p, narrow, grid, stream) : launch_rows<64>(p, narrow, grid, stream);
 }
 
 }  // namespace ltk

@@ -120,7 +120,7 @@ __device__ __forceinline__ long long slot_start(const TileParams& p, int b) {
 // Row tile `slot`: its fields, and the number of its key tiles (at least 1 on the
 // line, so that rows that see nothing are written too); 0: nothing there.  `b`:
 // where to begin looking for the sequence, -1 anywhere.
-template <bool SEL>
+template <bool SEL, bool STEPS>
 __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& tiles) {
   const AttnParams& a = p.a;
   if constexpr (SEL) {
@@ -148,17 +148,17 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
       while (b + 1 < a.batch.B && slot_start(p, b + 1) <= slot) ++b;
     }
     u.b = b;
-    const KvSeq q = kv_seq(a.batch, a.cache, b);
+    const KvSeq q = kv_seq<STEPS>(a.batch, a.cache, b);
     const long long row0 = (slot - slot_start(p, b)) * p.rows;
     const long long all = static_cast<long long>(q.nq) * a.group;
     tiles = 0;
-    if (row0 < 0 || row0 >= all || (a.step == 1 && q.len == 0)) return 0;   // (nothing shared: no first step)
+    if (row0 < 0 || row0 >= all || (STEPS && a.step == 1 && q.len == 0)) return 0;   // (nothing shared: no first step)
     u.row0 = static_cast<int>(row0);
     u.rows = static_cast<int>(min(all - row0, static_cast<long long>(p.rows)));
     u.q0 = q.q0;
     u.pos0 = q.pos0;
-    u.p_lo = q.pos0 + u.row0 / a.group * a.batch.advance;
-    u.p_hi = q.pos0 + (u.row0 + u.rows - 1) / a.group * a.batch.advance;
+    u.p_lo = q.pos0 + u.row0 / a.group * (STEPS ? a.batch.advance : 1);
+    u.p_hi = q.pos0 + (u.row0 + u.rows - 1) / a.group * (STEPS ? a.batch.advance : 1);
     u.len = q.len;
     u.page0 = q.page0;
     u.skip = u.tile0 = 0;
@@ -262,7 +262,7 @@ __device__ __forceinline__ void copy_queries(const TileParams& p, const Unit& u,
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
   }
 }
-template <int D, bool SEL, bool NARROW>
+template <int D, bool SEL, bool STEPS, bool NARROW>
 __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(const __grid_constant__ TileParams p) {
   using S = TileShape<D>;
   using R = Roles<D, NARROW>;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       long long mine = 0;
       int b = -1, n = 0;
       for (int s = s0; s < s1; ++s) {
-        n = decode_slot<SEL>(p, s, b, u, tiles);
+        n = decode_slot<SEL, STEPS>(p, s, b, u, tiles);
         mine += n;
         b = u.b;
       }
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           long long x = before;
           b = -1;
           for (int s = s0; s < s1; ++s) {
-            if (each > 1) n = decode_slot<SEL>(p, s, b, u, tiles);   // else still at hand
+            if (each > 1) n = decode_slot<SEL, STEPS>(p, s, b, u, tiles);   // else still at hand
             b = u.b;
             if (in < x + n) {
               u.n_tiles = n;             // on the line, and to see
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           if (un < waves) {
             const long long unit = static_cast<long long>(un) * gridDim.x + blockIdx.x;
             const int at_slot = static_cast<int>(unit / a.cache.heads);
-            u.n_tiles = decode_slot<SEL>(p, at_slot, -1, u, tiles);
+            u.n_tiles = decode_slot<SEL, STEPS>(p, at_slot, -1, u, tiles);
             u.head = static_cast<int>(unit - static_cast<long long>(at_slot) * a.cache.heads);
             u.part = -1;
           } else if (left > 0) {
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
               n = u.n_tiles;
               tiles = u.first;
             } else {
-              n = decode_slot<SEL>(p, slot, b, u, tiles);
+              n = decode_slot<SEL, STEPS>(p, slot, b, u, tiles);
             }
             b = u.b;
             const int end = static_cast<int>(min(static_cast<long long>(n), t + left));
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
             // on to the next row tile with something in it (there is one: the line goes on)
             Unit v;
             int vt;
-            for (int looked = 0; looked <= p.slots && decode_slot<SEL>(p, slot, b, v, vt) == 0; ++looked) {
+            for (int looked = 0; looked <= p.slots && decode_slot<SEL, STEPS>(p, slot, b, v, vt) == 0; ++looked) {
               b = v.b;
               if (++slot == p.slots) {
                 slot = 0;
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       if (!warp_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
       const Unit& u = ctrl->unit[us];   // stays in shared memory: a spilled copy would be read back from L2
       if (u.n_tiles < 0) break;
-      const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width + u.page0;
+      const int* table = a.batch.page_table + static_cast<size_t>(u.b) * a.batch.width + (STEPS ? u.page0 : 0);
       const int begin = u.first + set, end = u.first + u.n_tiles;
       constexpr int kStep = R::kSets;    // a set's tiles lie that far apart
       // A tile's lookups run ahead of its data, each a whole tile ahead of its use: its
@@ -847,7 +847,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       const bool live = row < u.rows && (!twice || (r >> 6) == x);
       const bool warp_live = __any_sync(0xFFFFFFFFu, live);
       const int mine = pair ? (x == 0 || u.rows > kTileRows ? u.n_tiles : 0) : x == 0 ? (u.n_tiles + 1) >> 1 : u.n_tiles >> 1;
-      const int pos = live ? (SEL ? u.pos0 : max(u.pos0 + (u.row0 + row) / a.group * a.batch.advance, -1)) : -1;
+      const int pos = live ? (SEL ? u.pos0 : max(u.pos0 + (u.row0 + row) / a.group * (STEPS ? a.batch.advance : 1), -1)) : -1;
       float f = 0.f;                     // scores to base-2 exponents
       if (pair) {
         if (!warp_wait(smem_u32(&ctrl->qraw), un & 1, abort_flag, status)) break;
@@ -1056,12 +1056,12 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           const int qi = rr / a.group;
           at = (static_cast<size_t>(u.q0) + qi) * a.q_heads + u.head * a.group + (rr - qi * a.group);
         }
-        const bool joined = !SEL && a.step == 2 && u.page0 > 0;
+        const bool joined = STEPS && a.step == 2 && u.page0 > 0;
         // 32 columns of the row's sums
         auto write_out = [&](int col, float (&s)[32], const RowEnd& end) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) s[e] *= end.own;
-          if (!SEL && a.step == 1) {
+          if (STEPS && a.step == 1) {
             float4* dst = reinterpret_cast<float4*>(a.mid + at * D + col);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e] = make_float4(s[4 * e], s[4 * e + 1], s[4 * e + 2], s[4 * e + 3]);
@@ -1140,7 +1140,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
         }
         if (!ok) break;
         auto write_lse = [&](float lse2) {
-          if (!SEL && a.step == 1) a.mid_lse[at] = lse2;
+          if (STEPS && a.step == 1) a.mid_lse[at] = lse2;
           else if (a.lse != nullptr) a.lse[at] = lse2 * 0.69314718055994530942f;
         };
         if (!part) {
@@ -1204,11 +1204,11 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
     }
     // dense: queries that belong to no sequence have no unit
     if constexpr (!SEL) {
-      if (x == 1 && a.step != 1) {
+      if (x == 1 && !(STEPS && a.step == 1)) {
         constexpr int kMine = 32 * R::kStreamWarps;             // this stream's threads
         for (long long n = blockIdx.x * static_cast<long long>(kMine) + (r & (kMine - 1)); n < a.batch.N;
              n += gridDim.x * static_cast<long long>(kMine)) {
-          const KvSeq q = kv_seq(a.batch, a.cache, kv_seq_of_query(a.batch, static_cast<int>(n)));
+          const KvSeq q = kv_seq<STEPS>(a.batch, a.cache, kv_seq_of_query(a.batch, static_cast<int>(n)));
           if (n >= q.q0 && n < q.q0 + q.nq) continue;
           uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + n * a.q_heads * D;
           for (int i = 0; i < a.q_heads * D; ++i) o[i] = 0;
@@ -1226,20 +1226,25 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
   }
 }
 
-template <int D, bool SEL, bool NARROW>
+template <int D, bool SEL, bool STEPS, bool NARROW>
 cudaError_t init_tile() {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_tile_kernel<D, SEL, NARROW>),
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_tile_kernel<D, SEL, STEPS, NARROW>),
                               cudaFuncAttributeMaxDynamicSharedMemorySize, TileShape<D>::kBytes);
 }
 
-template <int D, bool SEL>
+template <int D, bool SEL, bool STEPS>
 cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
   count_launches(1);
   if constexpr (!SEL) {
     if (p.rows <= 64)
-      return launch_overlapped(kv_tile_kernel<D, SEL, true>, num_sms, Roles<D, true>::kThreads, TileShape<D>::kBytes, stream, p);
+      return launch_overlapped(kv_tile_kernel<D, SEL, STEPS, true>, num_sms, Roles<D, true>::kThreads, TileShape<D>::kBytes, stream, p);
   }
-  return launch_overlapped(kv_tile_kernel<D, SEL, false>, num_sms, Roles<D, false>::kThreads, TileShape<D>::kBytes, stream, p);
+  return launch_overlapped(kv_tile_kernel<D, SEL, STEPS, false>, num_sms, Roles<D, false>::kThreads, TileShape<D>::kBytes, stream, p);
+}
+template <int D>
+cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
+  if (p.a.idx != nullptr) return launch_tile<D, true, false>(p, num_sms, stream);
+  return p.a.step != 0 ? launch_tile<D, false, true>(p, num_sms, stream) : launch_tile<D, false, false>(p, num_sms, stream);
 }
 
 }  // namespace
@@ -1248,8 +1253,10 @@ size_t kv_tile_part_floats(int num_sms) { return static_cast<size_t>(2) * num_sm
 int kv_tile_counters(int num_sms) { return 2 * num_sms; }
 
 cudaError_t kv_tile_init() {
-  const cudaError_t e[6] = {init_tile<128, false, false>(), init_tile<128, false, true>(), init_tile<128, true, false>(),
-                            init_tile<64, false, false>(),  init_tile<64, false, true>(),  init_tile<64, true, false>()};
+  const cudaError_t e[] = {init_tile<128, false, false, false>(), init_tile<128, false, false, true>(), init_tile<128, true, false, false>(),
+                           init_tile<128, false, true, false>(),  init_tile<128, false, true, true>(),
+                           init_tile<64, false, false, false>(),  init_tile<64, false, false, true>(),  init_tile<64, true, false, false>(),
+                           init_tile<64, false, true, false>(),   init_tile<64, false, true, true>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -1284,8 +1291,7 @@ cudaError_t launch_kv_tile(const AttnParams& a, int max_q, int num_sms, cudaStre
   } else {
     p.slots = static_cast<int>(static_cast<long long>(a.batch.N) * a.group / p.rows) + a.batch.B;
   }
-  if (a.dim == 128) return sel ? launch_tile<128, true>(p, num_sms, stream) : launch_tile<128, false>(p, num_sms, stream);
-  return sel ? launch_tile<64, true>(p, num_sms, stream) : launch_tile<64, false>(p, num_sms, stream);
+  return a.dim == 128 ? launch_tile<128>(p, num_sms, stream) : launch_tile<64>(p, num_sms, stream);
 }
 
 }  // namespace ltk

@@ -63,20 +63,21 @@ __device__ __forceinline__ T kv_load(const T* p) { return *p; }
 // Queries [q0, q0 + nq) of sequence b, the position of its first query, and how many of its
 // tokens have a column in the page table.  cu_q is clamped to the batch.  A sequence that is
 // longer than its table has queries at positions len and beyond.
-// With left-out tokens, lengths and positions count from the first one that is not.
+// STEPS: one of the two steps of an attention.  With left-out tokens, lengths and positions count from the first one that is not.
 struct KvSeq {
   int q0, nq, len, pos0;
   int page0;                             // column of the page table that holds position 0
 };
+template <bool STEPS = false>
 __device__ __forceinline__ KvSeq kv_seq(const KvBatch& bt, const KvCache& c, int b) {
   KvSeq s;
   s.q0 = min(max(kv_load(bt.cu_q + b), 0), bt.N);
   s.nq = min(max(kv_load(bt.cu_q + b + 1), s.q0), bt.N) - s.q0;
-  const int start = bt.start != nullptr ? kv_load(bt.start + b) : 0;
+  const int start = STEPS && bt.start != nullptr ? kv_load(bt.start + b) : 0;
   const long long room = min(static_cast<long long>(bt.width) << c.page_log2, static_cast<long long>(kKvMaxPos)) - start;
   const int tokens = max(kv_load(bt.seq_lens + b), 0) - start;
   s.len = static_cast<int>(min(static_cast<long long>(tokens), room));
-  s.pos0 = tokens - (bt.advance ? s.nq : 1);                  // negative when a sequence is shorter than its queries
+  s.pos0 = tokens - (!STEPS || bt.advance ? s.nq : 1);                  // negative when a sequence is shorter than its queries
   s.page0 = start >> c.page_log2;
   return s;
 }
