@@ -38,9 +38,30 @@ __device__ __forceinline__ int group_of(const ShareParams& p, int b) {
   return lo;
 }
 
+// Whether this thread's groups rise from 0 to the number of sequences.
+__device__ __forceinline__ bool groups_rise(const ShareParams& p, int g0, int step) {
+  bool rises = true;
+  for (int g = g0; g < p.num_groups; g += step) {
+    const int at = first_of(p, g), to = first_of(p, g + 1);
+    rises = rises && at >= 0 && at <= to && to <= p.batch.B && (g > 0 || at == 0) && (g + 1 < p.num_groups || to == p.batch.B);
+  }
+  return rises;
+}
+
+// Nothing but that, where all is attended to in one step.
+__global__ void __launch_bounds__(kThreads) kv_groups_kernel(const ShareParams p) {
+  begin_after_previous();
+  const bool rises = groups_rise(p, threadIdx.x, kThreads);
+  if (__syncthreads_or(rises ? 0 : 1) != 0 && threadIdx.x == 0) raise_status(p.status, kDevArg);
+}
+
+// One thread block's results for groups that its shared memory holds; beyond, in the workspace.
+constexpr int kHeld = 1024;
+
 __global__ void __launch_bounds__(kThreads) kv_share_kernel(const ShareParams p) {
   __shared__ int found;
   __shared__ int last;
+  __shared__ int held[3][kHeld];
   const int tid = threadIdx.x, b = blockIdx.x, B = p.batch.B;
   begin_after_previous();
   {
@@ -50,27 +71,34 @@ __global__ void __launch_bounds__(kThreads) kv_share_kernel(const ShareParams p)
     // the lead is b itself or before it
     if (tid == 0) found = b;
     __syncthreads();
-    for (int x = b0 + tid; x < b; x += kThreads)
-      if (pages_seen(p, x) > 0) {
-        atomicMin(&found, x);
-        break;
-      }
-    __syncthreads();
+    for (int x0 = b0; x0 < b; x0 += kThreads) {
+      const bool on = x0 + tid < b && pages_seen(p, x0 + tid) > 0;
+      if (on) atomicMin(&found, x0 + tid);
+      if (__syncthreads_or(on ? 1 : 0)) break;
+    }
     const int lead = found;
-    __syncthreads();
     int same = seen;
     if (lead != b && seen > 0) {
-      if (tid == 0) found = min(seen, pages_seen(p, lead));
-      __syncthreads();
-      const int most = found;
+      const int most = min(seen, pages_seen(p, lead));
       const int* mine = p.batch.page_table + static_cast<size_t>(b) * p.batch.width;
       const int* its = p.batch.page_table + static_cast<size_t>(lead) * p.batch.width;
       int end = most;
-      for (int i = tid; i < most; i += kThreads)
-        if (kv_load(mine + i) != kv_load(its + i)) {
-          end = i;
-          break;
+      constexpr int kAhead = 8;          // a row's numbers in flight, for the latency
+      for (int i0 = tid; i0 < end; i0 += kThreads * kAhead) {
+        int x[kAhead], y[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int i = i0 + j * kThreads;
+          x[j] = i < most ? kv_load(mine + i) : 0;
+          y[j] = i < most ? kv_load(its + i) : 0;
         }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          if (x[j] != y[j]) end = min(end, i0 + j * kThreads);
+      }
+      __syncthreads();
+      if (tid == 0) found = most;
+      __syncthreads();
       if (end < most) atomicMin(&found, end);
       __syncthreads();
       same = found;
@@ -85,13 +113,15 @@ __global__ void __launch_bounds__(kThreads) kv_share_kernel(const ShareParams p)
   if (!last) return;
   __threadfence();
   if (tid == 0) *p.counter = 0;
-  bool rises = true;
+  const bool few = p.num_groups <= kHeld;
+  int* leads = few ? held[0] : p.lead;
+  int* least = few ? held[1] : p.least;
+  int* sharing = few ? held[2] : p.sharing;
+  const bool rises = groups_rise(p, tid, kThreads);
   for (int g = tid; g < p.num_groups; g += kThreads) {
-    const int at = first_of(p, g), to = first_of(p, g + 1);
-    rises = rises && at >= 0 && at <= to && to <= B && (g > 0 || at == 0) && (g + 1 < p.num_groups || to == B);
-    p.lead[g] = B;
-    p.least[g] = p.batch.width;
-    p.sharing[g] = 0;
+    leads[g] = B;
+    least[g] = p.batch.width;
+    sharing[g] = 0;
   }
   const bool wrong = __syncthreads_or(rises ? 0 : 1) != 0;
   if (wrong) {                           // nothing is shared
@@ -106,17 +136,19 @@ __global__ void __launch_bounds__(kThreads) kv_share_kernel(const ShareParams p)
     const int n = __ldcg(p.common + x);
     if (n == 0) continue;
     const int g = group_of(p, x);
-    atomicMin(p.lead + g, x);
-    atomicMin(p.least + g, n);
-    atomicAdd(p.sharing + g, 1);
+    atomicMin(leads + g, x);
+    atomicMin(least + g, n);
+    atomicAdd(sharing + g, 1);
   }
+  __threadfence_block();
   __syncthreads();
   for (int x = tid; x <= B; x += kThreads) {
     const int g = group_of(p, min(x, B - 1));
     const int b0 = first_of(p, g), b1 = first_of(p, g + 1);
-    const bool shares = __ldcg(p.sharing + g) > 1;
-    const int lead = shares ? __ldcg(p.lead + g) : b0;
-    const int tokens = shares ? __ldcg(p.least + g) << p.cache.page_log2 : 0;
+    auto of = [&](int* of_group) { return *static_cast<volatile int*>(of_group + g); };
+    const bool shares = of(sharing) > 1;
+    const int lead = shares ? of(leads) : b0;
+    const int tokens = shares ? of(least) << p.cache.page_log2 : 0;
     p.cu[x] = min(max(kv_load(p.batch.cu_q + (x <= lead ? b0 : b1)), 0), p.batch.N);
     if (x < B) {
       p.start[x] = __ldcg(p.common + x) > 0 ? tokens : 0;
@@ -126,6 +158,11 @@ __global__ void __launch_bounds__(kThreads) kv_share_kernel(const ShareParams p)
 }
 
 }  // namespace
+
+cudaError_t launch_kv_groups(const ShareParams& p, cudaStream_t stream) {
+  count_launches(1);
+  return launch_overlapped(kv_groups_kernel, 1, kThreads, 0, stream, p);
+}
 
 cudaError_t launch_kv_share(const ShareParams& p, cudaStream_t stream) {
   count_launches(1);

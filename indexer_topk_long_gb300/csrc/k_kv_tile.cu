@@ -103,6 +103,7 @@ static_assert(TileShape<128>::kBytes <= 232448, "shared memory of a CTA");
 
 struct TileParams {
   AttnParams a;
+  KvPiece* pieces;                       // first step: one for each CTA
   int pair;                              // 1: pair mode
   int rows;                              // rows of a unit
   uint32_t group_magic;                  // 2^32 / group rounded up (0 for a group of 1)
@@ -306,6 +307,9 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
   }
 
   begin_after_previous();
+  if constexpr (STEPS) {
+    if (a.step == 1 && tid == 0) p.pieces[blockIdx.x].last = -1;
+  }
 
   // --- this CTA's piece of the line (head, row tile, key tile), every CTA one tile at least ---
   long long total;
@@ -1147,6 +1151,13 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           if (live) write_lse(end.lse2);
         } else {
           if (live) __stcg(reinterpret_cast<float2*>(pd) + row, make_float2(M, l));
+          if (STEPS && a.step == 1) {    // joined by the kernel behind this one
+            if (x == 0 && r == 0 && (u.part & 1) != 0) p.pieces[blockIdx.x] = KvPiece{u.c1, u.rows, u.row0, u.q0, u.head};
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctrl->uempty[us]));
+            continue;
+          }
           // the last of the unit's CTAs joins the pieces in their order
           __threadfence();
           mbar_arrive(smem_u32(&ctrl->wg[x]));
@@ -1226,6 +1237,47 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
   }
 }
 
+// Joins the units of a first step that several CTAs hold, their pieces in order: 32 rows and 32 columns of one such
+// unit a block, a thread for a row and four columns.  By the unit's last CTA instead, a row to a thread, ten pieces of
+// 256 rows took some 50 us of 116 (128 queries of 4 heads, 32768 shared tokens, 8 KV heads).
+constexpr int kJoinRows = 32, kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ TileParams p, const int blocks) {
+  const AttnParams& a = p.a;
+  begin_after_previous();
+  constexpr int kParts = D / 32;         // blocks of columns
+  const int first = blockIdx.x / (blocks * kParts), part = blockIdx.x % kParts;
+  const int row = blockIdx.x / kParts % blocks * kJoinRows + (threadIdx.x & 31), quad = part * 8 + (threadIdx.x >> 5);
+  const KvPiece u = kv_load(p.pieces + first);
+  if (u.last < 0 || row >= u.rows) return;
+  const size_t slot = static_cast<size_t>(p.rows) * (D + 2);
+  auto piece = [&](int cta) { return a.part + (2 * cta + (cta == first ? 1 : 0)) * slot; };
+  float top = kMinusHuge, sum = 0.f;
+#pragma unroll 8
+  for (int cta = first; cta <= u.last; ++cta) {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(piece(cta)) + row);
+    const float next = fmaxf(top, v.x);
+    sum = sum * exp2_approx(top - next) + v.y * exp2_approx(v.x - next);
+    top = next;
+  }
+  const int rr = u.row0 + row, qi = rr / a.group;
+  const size_t at = (static_cast<size_t>(u.q0) + qi) * a.q_heads + u.head * a.group + (rr - qi * a.group);
+  const RowEnd end = row_end(a, at, false, top - kBoost, sum);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int cta = first; cta <= u.last; ++cta) {
+    const float* src = piece(cta);
+    const float by = exp2_approx(__ldcg(src + 2 * row) - top);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(src + p.rows * 2) + static_cast<size_t>(quad) * p.rows + row);
+    s.x = fmaf(v.x, by, s.x);
+    s.y = fmaf(v.y, by, s.y);
+    s.z = fmaf(v.z, by, s.z);
+    s.w = fmaf(v.w, by, s.w);
+  }
+  reinterpret_cast<float4*>(a.mid + at * D)[quad] = make_float4(s.x * end.own, s.y * end.own, s.z * end.own, s.w * end.own);
+  if (part == 0 && threadIdx.x < 32) a.mid_lse[at] = end.lse2;
+}
+
 template <int D, bool SEL, bool STEPS, bool NARROW>
 cudaError_t init_tile() {
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(kv_tile_kernel<D, SEL, STEPS, NARROW>),
@@ -1244,12 +1296,18 @@ cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
   if (p.a.idx != nullptr) return launch_tile<D, true, false>(p, num_sms, stream);
-  return p.a.step != 0 ? launch_tile<D, false, true>(p, num_sms, stream) : launch_tile<D, false, false>(p, num_sms, stream);
+  if (p.a.step == 0) return launch_tile<D, false, false>(p, num_sms, stream);
+  const cudaError_t e = launch_tile<D, false, true>(p, num_sms, stream);
+  if (e != cudaSuccess || p.a.step != 1) return e;
+  const int blocks = p.rows / kJoinRows;
+  count_launches(1);
+  return launch_overlapped(kv_join_kernel<D>, num_sms * blocks * (D / 32), kJoinThreads, 0, stream, p, blocks);
 }
 
 }  // namespace
 
-size_t kv_tile_part_floats(int num_sms) { return static_cast<size_t>(2) * num_sms * 2 * kTileRows * (128 + 2); }
+static size_t part_floats(int num_sms) { return static_cast<size_t>(2) * num_sms * 2 * kTileRows * (128 + 2); }
+size_t kv_tile_part_floats(int num_sms) { return part_floats(num_sms) + num_sms * sizeof(KvPiece) / sizeof(float); }
 int kv_tile_counters(int num_sms) { return 2 * num_sms; }
 
 cudaError_t kv_tile_init() {
@@ -1269,7 +1327,7 @@ cudaError_t kv_tile_init() {
 // in single tiles, 1 x 1024 of 4096 (13.5) 66 and 61, 4 x 256 of 1100 (3.8) 50 and 43, 1 x 64 of
 // 16384 (3.4) 111 and 66.
 bool kv_tile_pairs(const AttnParams& a, int max_q, int num_sms) {
-  double keys = static_cast<double>(a.batch.width) * a.cache.page;
+  double keys = static_cast<double>(a.batch.width) * a.cache.page * (a.share / 0.6);
   if (a.window > 0) keys = fmin(keys, static_cast<double>(a.window) + a.sinks + max_q);
   const double pairs = a.cache.heads * (static_cast<double>(a.batch.N) * a.group / (2 * kTileRows) + 0.5 * a.units);
   return static_cast<long long>(a.group) * max_q > kTileRows && pairs * (keys / kKeys) >= 14.0 * num_sms;
@@ -1278,6 +1336,7 @@ bool kv_tile_pairs(const AttnParams& a, int max_q, int num_sms) {
 cudaError_t launch_kv_tile(const AttnParams& a, int max_q, int num_sms, cudaStream_t stream) {
   TileParams p{};
   p.a = a;
+  p.pieces = reinterpret_cast<KvPiece*>(a.part + part_floats(num_sms));
   p.group_magic = static_cast<uint32_t>((0x100000000ull + a.group - 1) / a.group);
   const bool sel = a.idx != nullptr;
   // Rows that one KV head's keys meet at a time: a pair of tiles, one tile, or a narrow one

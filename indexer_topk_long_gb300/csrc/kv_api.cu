@@ -57,12 +57,15 @@ bool rows_ok(const void* p, long long stride, int heads, int dim) {
 // How long sequences are is only known on the device: 0.6 of the page table is assumed.  Over
 // 130 dense batches (1 to 128 sequences, even and ragged, 98 to 32768 tokens) what this takes
 // is 2% more on average than the better of the two.
-bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
+struct Estimate {
+  bool by_rows;
+  double us;                             // of the GPU
+};
+Estimate kv_estimate(const AttnParams& p, int max_q, int num_sms) {
   const double rows = static_cast<double>(p.group) * (p.idx != nullptr ? 1 : max_q);
-  if (rows <= kRowsPerUnit) return true;
   double keys = p.k;
   if (p.idx == nullptr) {
-    keys = static_cast<double>(p.batch.width) * p.cache.page * 0.6;
+    keys = static_cast<double>(p.batch.width) * p.cache.page * p.share;
     if (p.window > 0) keys = std::min(keys, static_cast<double>(p.window) + p.sinks + max_q);
   }
   const double T = std::ceil(keys / 128.0);
@@ -73,6 +76,7 @@ bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
   };
   const bool wide = p.dim == 128;
   const double by_rows = units(16) * (wide ? 2.0 + 0.75 * T : 1.4 + 0.51 * T);
+  if (rows <= kRowsPerUnit) return {true, p.cache.heads * by_rows / num_sms};
   double by_tiles, start;
   if (p.idx != nullptr && p.group <= kListRows) {
     by_tiles = units(64) * (wide ? 5.0 + 0.96 * T : 4.5 + 0.94 * T);
@@ -82,7 +86,8 @@ bool kv_use_rows(const AttnParams& p, int max_q, int num_sms) {
     by_tiles = units(pair ? 256 : rows <= 64 ? 64 : 128) * ((pair ? 8.0 : 3.0) + (wide ? 1.8 : 1.4) * T);
     start = 12.0;
   }
-  return p.cache.heads * (by_rows - by_tiles) <= start * num_sms;
+  if (p.cache.heads * (by_rows - by_tiles) <= start * num_sms) return {true, p.cache.heads * by_rows / num_sms};
+  return {false, p.cache.heads * by_tiles / num_sms + start};
 }
 
 }  // namespace
@@ -112,15 +117,20 @@ ltk_status kv_attention_params(const ltk_kv* h, const ltk_kv_batch* batch, int d
   p->group = q_heads / h->cache.heads;
   p->scale_log2 = scale * 1.44269504088896340736f;
   p->units = batch->B;
+  p->share = 0.6;
   p->part = h->part;
   p->counters = h->counters;
   p->status = h->status;
   return LTK_OK;
 }
 
+double kv_attention_us(const ltk_kv* h, const AttnParams& p, int max_q) {
+  return kv_estimate(p, max_q > 0 ? max_q : p.batch.N, h->num_sms).us;
+}
+
 cudaError_t kv_launch_attention(const ltk_kv* h, const AttnParams& p, int max_q, cudaStream_t stream) {
   const int most_q = max_q > 0 ? max_q : p.batch.N;
-  const bool by_rows = h->engine == 0 ? kv_use_rows(p, most_q, h->num_sms) : h->engine == 1;
+  const bool by_rows = h->engine == 0 ? kv_estimate(p, most_q, h->num_sms).by_rows : h->engine == 1;
   if (by_rows) return launch_kv_rows(p, most_q, h->num_sms, stream);
   return p.idx != nullptr && p.group <= kListRows ? launch_kv_list(p, h->num_sms, stream)
                                                   : launch_kv_tile(p, most_q, h->num_sms, stream);

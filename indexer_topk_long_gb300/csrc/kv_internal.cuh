@@ -208,6 +208,7 @@ struct ShareParams {
   int* status;
 };
 cudaError_t launch_kv_share(const ShareParams& p, cudaStream_t stream);
+cudaError_t launch_kv_groups(const ShareParams& p, cudaStream_t stream);   // checks the groups only
 
 struct AttnParams {
   KvCache cache;
@@ -231,9 +232,17 @@ struct AttnParams {
   float* mid;                            // [N, q_heads, dim]
   float* mid_lse;                        // [N, q_heads], base 2
   int units;                             // sequences that have queries, for the choice of kernel
+  double share;                          // of the tokens that a table has room for: how long sequences are taken to be
   float* part;                           // workspace: partial results
   int* counters;                         // workspace: zero between calls
   int* status;
+};
+
+// First step, tensor-core tiles: a unit whose key tiles several CTAs hold is not joined by the last of them, but by a
+// kernel of its own, from this, by the first of its CTAs.
+struct KvPiece {
+  int last;                              // the last of its CTAs; -1: no such unit begins here
+  int rows, row0, q0, head;
 };
 
 // What turns a row's sum over values into its result: result = own * (weighted sum) + mid * (the
@@ -267,7 +276,7 @@ cudaError_t kv_rows_init();                // kernel attributes on the current d
 cudaError_t launch_kv_rows(const AttnParams& p, int max_q, int num_sms, cudaStream_t stream);
 
 // Attention for many rows per KV head, on the tensor cores (k_kv_tile.cu).
-size_t kv_tile_part_floats(int num_sms);
+size_t kv_tile_part_floats(int num_sms);   // and behind them the pieces
 int kv_tile_counters(int num_sms);
 cudaError_t kv_tile_init();
 bool kv_tile_pairs(const AttnParams& p, int max_q, int num_sms);   // whether its units are pairs of row tiles
@@ -303,6 +312,8 @@ ltk_status kv_check_batch(const ltk_kv* h, const ltk_kv_batch* b);
 // p->batch.N 0: nothing to do.
 ltk_status kv_attention_params(const ltk_kv* h, const ltk_kv_batch* batch, int dtype, const void* q, long long q_stride,
                                int q_heads, int max_q, float scale, AttnParams* p);
+// About how long the chosen kernel takes, in us.
+double kv_attention_us(const ltk_kv* h, const AttnParams& p, int max_q);
 // Chooses the kernel and starts it.
 cudaError_t kv_launch_attention(const ltk_kv* h, const AttnParams& p, int max_q, cudaStream_t stream);
 inline bool kv_aligned(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

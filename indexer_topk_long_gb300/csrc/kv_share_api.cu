@@ -61,28 +61,42 @@ ltk_status ltk_kv_attention_shared(ltk_kv* h, const ltk_kv_batch* batch, const i
   if (workspace_bytes < w.bytes) return LTK_ERR_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int G = groups != nullptr ? num_groups : 1;
+  const int mean_q = static_cast<int>((static_cast<long long>(batch->N) + G - 1) / G);
   const ShareParams share{p.cache, p.batch, groups, G, w.common, w.lead, w.least, w.sharing, w.start, w.lens, w.cu, h->counters, h->status};
-  cudaError_t e = launch_kv_share(share, st);
-  if (e != cudaSuccess) return kv_cuda_fail(e, "kv shared attention");
-  // all of a group's queries over what it shares, without a mask
+  p.out = out;
+  p.lse = lse;
   AttnParams first = p;
-  first.batch.seq_lens = w.lens;
-  first.batch.cu_q = w.cu;
   first.batch.advance = 0;
   first.units = G;
   first.step = 1;
   first.mid = w.mid;
   first.mid_lse = w.mid_lse;
-  e = kv_launch_attention(h, first, static_cast<int>((static_cast<long long>(batch->N) + G - 1) / G), st);
+  AttnParams second = p;
+  second.batch.start = w.start;
+  second.step = 2;
+  second.mid = w.mid;
+  second.mid_lse = w.mid_lse;
+  // Two steps cost two launches more, the way through memory between them and units that begin and end twice, which
+  // little work does not repay, nor many rows a sequence: its own rows fill the tiles then, and L2 serves what
+  // sequences share.  Four fifths of the tokens are taken to be shared.  In one step and in two (us): 4 sequences of 1040
+  // tokens, 8 heads of 64, 9 and 18; 47 of up to 16700 in 6 groups, 14 query heads of 64 on 2, 33 and 44; 16 x 226
+  // queries behind 8192 tokens, 32 heads of 128 on 8, 489 and 530; 128 sequences of 33000 tokens 1014 and 106.
+  first.share = 0.8 * p.share;
+  second.share = 0.2 * p.share;
+  if (h->engine == 0 && kv_attention_us(h, p, max_q) <= kv_attention_us(h, first, mean_q) + kv_attention_us(h, second, max_q) + 10.0) {
+    cudaError_t e = groups != nullptr ? launch_kv_groups(share, st) : cudaSuccess;
+    if (e == cudaSuccess) e = kv_launch_attention(h, p, max_q, st);
+    return kv_cuda_fail(e, "kv shared attention");
+  }
+  cudaError_t e = launch_kv_share(share, st);
+  if (e != cudaSuccess) return kv_cuda_fail(e, "kv shared attention");
+  // all of a group's queries over what it shares, without a mask
+  first.batch.seq_lens = w.lens;
+  first.batch.cu_q = w.cu;
+  e = kv_launch_attention(h, first, mean_q, st);
   if (e != cudaSuccess) return kv_cuda_fail(e, "kv shared attention");
   // each sequence's rest, joined with that
-  p.batch.start = w.start;
-  p.step = 2;
-  p.mid = w.mid;
-  p.mid_lse = w.mid_lse;
-  p.out = out;
-  p.lse = lse;
-  return kv_cuda_fail(kv_launch_attention(h, p, max_q, st), "kv shared attention");
+  return kv_cuda_fail(kv_launch_attention(h, second, max_q, st), "kv shared attention");
 }
 
 ltk_status ltk_kv_read(ltk_kv* h, const ltk_kv_batch* batch, int dtype, const float* cos_table, const float* sin_table,

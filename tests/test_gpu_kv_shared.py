@@ -225,3 +225,15 @@ def test_refusals():
                                                  lse.data_ptr(), at, n, None) == 1
     empty = cache.attention_shared(q[:0], *ints[:2], torch.zeros(3, dtype=torch.int32, device="cuda"))
     assert empty[0].shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("hq,hkv,d,page,new", [(8, 2, 128, 64, 1), (32, 1, 64, 16, 3), (8, 1, 128, 32, 40)])
+def test_chosen_by_the_table(hq, hkv, d, page, new):
+    """A wide page table is taken for long sequences, which are attended to in two steps: few rows, a
+    tile's, pairs'."""
+    import torch
+    s = shared([6, 2], [9, 4], [new + i for i in range(8)], [new] * 8, hq, hkv, d, page)
+    out, lse, cache, ints = run(s, 0, max_q=new, columns=1 << 18)
+    check(s, out, lse)
+    before = cache.attention(s.q.cuda(), *ints, max_q=new)
+    assert not torch.equal(before[1], lse)           # (joined sums differ in the last bits)
