@@ -78,7 +78,7 @@ struct Meta {                            // scales of a key tile's eight 16-key 
 
 struct Ctrl {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pfull[2], ofull[2];
-  uint64_t ufull[2], uempty[2], qfull[2], qempty, qraw, mfull, mempty, drained, wg[2];
+  uint64_t ufull[2], uempty[2], qfull[2], mfull, mempty, drained, wg[2];
   uint32_t tmem;
   int abort_flag;
   int last[2];
@@ -114,15 +114,15 @@ struct TileParams {
 
 // Dense row tiles are numbered without a scan: sequence b's start at
 // cu_q[b] * group / rows + b, which leaves room for every row tile.
-__device__ __forceinline__ long long slot_start(const TileParams& p, int b) {
-  return static_cast<long long>(kv_load(p.a.batch.cu_q + b)) * p.a.group / p.rows + b;
+__device__ __forceinline__ long long slot_start(const TileParams& p, int b, const int* cu) {
+  return static_cast<long long>(kv_load((cu != nullptr ? cu : p.a.batch.cu_q) + b)) * p.a.group / p.rows + b;
 }
 
 // Row tile `slot`: its fields, and the number of its key tiles (at least 1 on the
 // line, so that rows that see nothing are written too); 0: nothing there.  `b`:
-// where to begin looking for the sequence, -1 anywhere.
+// where to begin looking for the sequence, -1 anywhere; `cu`: cu_q in shared memory, or null.
 template <bool SEL, bool STEPS>
-__device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& tiles) {
+__device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& tiles, const int* cu = nullptr) {
   const AttnParams& a = p.a;
   if constexpr (SEL) {
     const int n = slot / p.row_tiles;
@@ -142,15 +142,15 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
       int lo = 0, hi = a.batch.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (slot_start(p, mid) <= slot) lo = mid; else hi = mid - 1;
+        if (slot_start(p, mid, cu) <= slot) lo = mid; else hi = mid - 1;
       }
       b = lo;
     } else {
-      while (b + 1 < a.batch.B && slot_start(p, b + 1) <= slot) ++b;
+      while (b + 1 < a.batch.B && slot_start(p, b + 1, cu) <= slot) ++b;
     }
     u.b = b;
     const KvSeq q = kv_seq<STEPS>(a.batch, a.cache, b);
-    const long long row0 = (slot - slot_start(p, b)) * p.rows;
+    const long long row0 = (slot - slot_start(p, b, cu)) * p.rows;
     const long long all = static_cast<long long>(q.nq) * a.group;
     tiles = 0;
     if (row0 < 0 || row0 >= all || (STEPS && a.step == 1 && q.len == 0)) return 0;   // (nothing shared: no first step)
@@ -233,9 +233,10 @@ __device__ __forceinline__ void store_rows(uint32_t at, int lane, const uint4 (&
   }
 }
 
-// Queries come in two steps, since a round trip to memory for every few rows would hold
-// up the next unit: all rows by asynchronous copies to where their f16 form will stand
-// (16-bit elements either way), then converted in place by convert_query.
+// In pairs each softmax thread fetches its own row, all of it at a time, and converts it: 2 us, where two warps' copies
+// and the conversion behind them took 11.  Else queries come ahead of their use, in two steps, since a round
+// trip to memory for every few rows would hold up the next unit: all rows by asynchronous copies to where
+// their f16 form will stand (16-bit elements either way), then converted in place by convert_query.
 //
 // The copies, by warps w = 0, 1: rows [r0, r0 + 128) of the unit; rows repeat with period mask + 1,
 // rows past the unit's are zero.
@@ -294,8 +295,6 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
         mbar_init(smem_u32(&ctrl->qfull[i]), pair ? 8 : 2);
         mbar_init(smem_u32(&ctrl->wg[i]), 32 * R::kStreamWarps);
       }
-      mbar_init(smem_u32(&ctrl->qempty), 1);
-      mbar_init(smem_u32(&ctrl->qraw), 2);
       mbar_init(smem_u32(&ctrl->mfull), R::kStreamWarps);
       mbar_init(smem_u32(&ctrl->mempty), R::kStreamWarps);
       mbar_init(smem_u32(&ctrl->drained), 1);
@@ -337,17 +336,26 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
     } else {
       long long* sums = reinterpret_cast<long long*>(smem);   // free until the first queries come
       // Row tiles are numbered by cu_q, so it has to rise within [0, N]; else nothing is done.
+      // They are looked up many times, one after the other: in shared memory where there is room.
+      constexpr int kHeld = S::kQ / 4 - 256;
+      int* held = reinterpret_cast<int*>(smem) + 256;
+      const int* cu = a.batch.B < kHeld ? held : nullptr;
       bool rises = true;
       for (int i = tid; i < a.batch.B; i += kThreads) {
         const int at = kv_load(a.batch.cu_q + i), to = kv_load(a.batch.cu_q + i + 1);
         rises = rises && at >= 0 && at <= to && to <= a.batch.N;
+        if (cu != nullptr) {
+          held[i] = at;
+          if (i + 1 == a.batch.B) held[i + 1] = to;
+        }
       }
+      __syncthreads();
       const int each = (p.slots + kThreads - 1) / kThreads;
       const int s0 = min(tid * each, p.slots), s1 = min(s0 + each, p.slots);
       long long mine = 0;
       int b = -1, n = 0;
       for (int s = s0; s < s1; ++s) {
-        n = decode_slot<SEL, STEPS>(p, s, b, u, tiles);
+        n = decode_slot<SEL, STEPS>(p, s, b, u, tiles, cu);
         mine += n;
         b = u.b;
       }
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
           long long x = before;
           b = -1;
           for (int s = s0; s < s1; ++s) {
-            if (each > 1) n = decode_slot<SEL, STEPS>(p, s, b, u, tiles);   // else still at hand
+            if (each > 1) n = decode_slot<SEL, STEPS>(p, s, b, u, tiles, cu);   // else still at hand
             b = u.b;
             if (in < x + n) {
               u.n_tiles = n;             // on the line, and to see
@@ -476,31 +484,22 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
         if (!warp_wait(smem_u32(&ctrl->ufull[us]), (un >> 1) & 1, abort_flag, status)) break;
         const Unit& u = ctrl->unit[us];
         if (u.n_tiles < 0) break;
-        // Pair mode: one buffer.  Also a unit without tiles waits for the one before it to be done
-        // with, or qraw could complete a second phase before a softmax warp has seen the first.
-        if (pair && un >= 1 && !warp_wait(smem_u32(&ctrl->qempty), (un - 1) & 1, abort_flag, status)) break;
-        if (u.n_tiles > 0) {
+        // (in pairs the softmax threads fetch their rows)
+        if (u.n_tiles > 0 && !pair) {    // two buffers, converted here ahead of their use
           const int w = warp - R::kRest - 2;
-          if (pair) {                    // the softmax threads convert their rows
-            copy_queries<D>(p, u, q_sm, 0, 127, w, lane);
-            if (u.rows > kTileRows) copy_queries<D>(p, u, q_sm + S::kOperand, kTileRows, 127, w, lane);
-          } else {                       // two buffers, converted here ahead of their use
-            copy_queries<D>(p, u, q_sm + us * S::kOperand, 0, u.rows <= 64 ? 63 : 127, w, lane);
-          }
+          copy_queries<D>(p, u, q_sm + us * S::kOperand, 0, u.rows <= 64 ? 63 : 127, w, lane);
           asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
           __syncwarp();
-          if (!pair) {
 #pragma unroll 1
-            for (int i = 0; i < 2; ++i) {
-              const int row = 64 * w + 32 * i + lane;
-              ctrl->rowf[us * 128 + row] = convert_query<D, kTileRows>(a, q_sm + us * S::kOperand, row);
-            }
-            fence_async_smem();
+          for (int i = 0; i < 2; ++i) {
+            const int row = 64 * w + 32 * i + lane;
+            ctrl->rowf[us * 128 + row] = convert_query<D, kTileRows>(a, q_sm + us * S::kOperand, row);
           }
+          fence_async_smem();
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(pair ? &ctrl->qraw : &ctrl->qfull[us]));
+          if (!pair) mbar_arrive(smem_u32(&ctrl->qfull[us]));
           mbar_arrive(smem_u32(&ctrl->uempty[us]));
         }
       }
@@ -570,9 +569,6 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
               if (two && !next) commit(&ctrl->ofull[1]);
               if (next) commit(&ctrl->kempty[ns]);
             }
-            commit(&ctrl->qempty);
-          } else {
-            arrive(&ctrl->qempty);
           }
           arrive(&ctrl->uempty[us]);
           arrive(&ctrl->uempty[us]);
@@ -854,9 +850,12 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
       const int pos = live ? (SEL ? u.pos0 : max(u.pos0 + (u.row0 + row) / a.group * (STEPS ? a.batch.advance : 1), -1)) : -1;
       float f = 0.f;                     // scores to base-2 exponents
       if (pair) {
-        if (!warp_wait(smem_u32(&ctrl->qraw), un & 1, abort_flag, status)) break;
+        // (the products that read the stream's last rows are done: its results have been waited for)
         if (mine > 0) {
-          f = convert_query<D, kTileRows>(a, q_sm + x * S::kOperand, r);
+          const int rr = u.row0 + row, qi = rr / a.group;
+          const uint16_t* from = reinterpret_cast<const uint16_t*>(a.q) + (static_cast<size_t>(u.q0) + qi) * a.q_stride +
+                                 static_cast<size_t>(u.head * a.group + rr - qi * a.group) * D;
+          f = convert_query<D, kTileRows, false>(a, q_sm + x * S::kOperand, r, live ? from : nullptr);
           fence_async_smem();
         }
         __syncwarp();

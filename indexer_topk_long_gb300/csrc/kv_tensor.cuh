@@ -117,16 +117,26 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// A row of a ROWS-row operand of queries, copied there as it is, by one thread: the row times a power of two that takes its
+// A row of a ROWS-row operand of queries, by one thread: the row times a power of two that takes its
 // largest element to [2^8, 2^9), as f16; returns what turns the products into base-2
-// exponents.
-template <int D, int ROWS>
-__device__ __forceinline__ float convert_query(const AttnParams& a, uint32_t base, int row) {
+// exponents.  The row as it is: where its f16 form goes, copied there before, or at `from` in global memory
+// (null: zeros).
+template <int D, int ROWS, bool COPIED>
+__device__ __forceinline__ float convert_query(const AttnParams& a, uint32_t base, int row, const uint16_t* from) {
   auto at = [&](int c) { return base + (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4); };
   uint32_t w[D / 8][4];
 #pragma unroll
-  for (int c = 0; c < D / 8; ++c)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3]) : "r"(at(c)));
+  for (int c = 0; c < D / 8; ++c) {
+    if constexpr (COPIED) {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[c][0]), "=r"(w[c][1]), "=r"(w[c][2]), "=r"(w[c][3]) : "r"(at(c)));
+    } else {
+      const uint4 v = from != nullptr ? kv_load(reinterpret_cast<const uint4*>(from) + c) : make_uint4(0, 0, 0, 0);
+      w[c][0] = v.x;
+      w[c][1] = v.y;
+      w[c][2] = v.z;
+      w[c][3] = v.w;
+    }
+  }
   float amax = 0.f;
 #pragma unroll
   for (int c = 0; c < D / 8; ++c)
@@ -149,6 +159,12 @@ __device__ __forceinline__ float convert_query(const AttnParams& a, uint32_t bas
                  : "memory");
   }
   return a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+// The same of a row copied there before.
+template <int D, int ROWS>
+__device__ __forceinline__ float convert_query(const AttnParams& a, uint32_t base, int row) {
+  return convert_query<D, ROWS, true>(a, base, row, nullptr);
 }
 
 // Two fp32 products and sums at once.
