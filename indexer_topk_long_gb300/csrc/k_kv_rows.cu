@@ -708,11 +708,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     const int c0 = static_cast<int>(((u0 + 1) * n_cta - 1) / total), c1 = static_cast<int>((u1 * n_cta - 1) / total);
     constexpr int kSlot = kRows * (D + 2);
     float* mine = p.part + static_cast<size_t>(2 * blockIdx.x + (t_begin == 0 ? 1 : 0)) * kSlot;
-    auto write_row = [&](int r, int ch, float4 v, float m2, float sum) {
+    // the first step's result for a row's piece ch, asked for before it is needed
+    const bool joined = STEPS && p.step == 2 && head.w.page0 > 0;
+    struct Before {
+      float lse;
+      float4 o;
+    };
+    auto place_of = [&](int r) {
       const int row = head.w.row0 + r;
-      const size_t at = (static_cast<size_t>(head.w.q0) + row / p.group) * p.q_heads + head.w.head * p.group + row % p.group;
-      const bool joined = STEPS && p.step == 2 && head.w.page0 > 0;
-      const RowEnd e = row_end(p, at, joined, m2 - kBoost, sum);
+      return (static_cast<size_t>(head.w.q0) + row / p.group) * p.q_heads + head.w.head * p.group + row % p.group;
+    };
+    auto before_of = [&](int r, int ch) {
+      Before b{};
+      if (joined) {
+        const size_t at = place_of(r);
+        b.lse = kv_load(p.mid_lse + at);
+        b.o = kv_load(reinterpret_cast<const float4*>(p.mid + at * D) + ch);
+      }
+      return b;
+    };
+    auto write_row = [&](int r, int ch, float4 v, float m2, float sum, const Before& b) {
+      const size_t at = place_of(r);
+      const RowEnd e = row_end(b.lse, joined, m2 - kBoost, sum);
       v = make_float4(v.x * e.own, v.y * e.own, v.z * e.own, v.w * e.own);
       if (STEPS && p.step == 1) {
         reinterpret_cast<float4*>(p.mid + at * D)[ch] = v;
@@ -720,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
         return;
       }
       if (joined) {
-        const float4 o = kv_load(reinterpret_cast<const float4*>(p.mid + at * D) + ch);
+        const float4 o = b.o;
         v = make_float4(fmaf(o.x, e.mid, v.x), fmaf(o.y, e.mid, v.y), fmaf(o.z, e.mid, v.z), fmaf(o.w, e.mid, v.w));
       }
       uint2 w;
@@ -731,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
     };
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), ch = i % (D / 4);
+      const Before b = before_of(r, ch);
       float mx = kMinusHuge;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, merge_ml[(w * kRows + r) * 2]);
@@ -748,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
         acc.w = fmaf(v.w, by, acc.w);
       }
       if (whole) {
-        write_row(r, ch, acc, mx, sum);
+        write_row(r, ch, acc, mx, sum, b);
       } else {
         __stcg(reinterpret_cast<float4*>(mine + kRows * 2 + r * D) + ch, acc);
         if (ch == 0) __stcg(reinterpret_cast<float2*>(mine) + r, make_float2(mx, sum));
@@ -778,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_rows_kernel(const Att
             acc.z = acc.z * a + v.z * b;
             acc.w = acc.w * a + v.w * b;
           }
-          write_row(r, ch, acc, mx, sum);
+          write_row(r, ch, acc, mx, sum, before_of(r, ch));
         }
         if (tid == 0) p.counters[c0] = 0;
       }

@@ -105,7 +105,7 @@ struct TileParams {
   AttnParams a;
   KvPiece* pieces;                       // first step: one for each CTA
   int pair;                              // 1: pair mode
-  int rows;                              // rows of a unit
+  int rows, rows_log2;                   // rows of a unit
   uint32_t group_magic;                  // 2^32 / group rounded up (0 for a group of 1)
   int row_tiles;                         // listed keys: row tiles of a group
   int slots;                             // row tiles over all sequences (an upper bound when dense)
@@ -115,8 +115,14 @@ struct TileParams {
 // Dense row tiles are numbered without a scan: sequence b's start at
 // cu_q[b] * group / rows + b, which leaves room for every row tile.
 __device__ __forceinline__ long long slot_start(const TileParams& p, int b, const int* cu) {
-  return static_cast<long long>(kv_load((cu != nullptr ? cu : p.a.batch.cu_q) + b)) * p.a.group / p.rows + b;
+  return (static_cast<long long>(kv_load((cu != nullptr ? cu : p.a.batch.cu_q) + b)) * p.a.group >> p.rows_log2) + b;
 }
+
+// First step: what it takes to begin and end a unit's piece, in key tiles (9 us of 1.75).  They are counted on the
+// line, before the unit's own, so that a CTA with parts of two units is not the last: with 16 units of
+// 256 tiles over 152 CTAs it was 9 us behind the others.
+template <bool STEPS>
+__device__ __forceinline__ int begin_tiles(const TileParams& p) { return STEPS && p.a.step == 1 ? 5 : 0; }
 
 // Row tile `slot`: its fields, and the number of its key tiles (at least 1 on the
 // line, so that rows that see nothing are written too); 0: nothing there.  `b`:
@@ -170,7 +176,7 @@ __device__ int decode_slot(const TileParams& p, int slot, int b, Unit& u, int& t
       u.skip = min((min(a.sinks, last + 1) + kKeys - 1) / kKeys, u.tile0);
       tiles = u.skip + tiles - u.tile0;
     }
-    return max(tiles, 1);
+    return max(tiles, 1) + begin_tiles<STEPS>(p);
   }
 }
 
@@ -435,8 +441,8 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
             const int end = static_cast<int>(min(static_cast<long long>(n), t + left));
             const long long u0 = at - t, u1 = u0 + n;
             u.head = head;
-            u.first = t;
-            u.n_tiles = min(end, tiles) - t;
+            u.first = max(t - begin_tiles<STEPS>(p), 0);
+            u.n_tiles = max(min(end - begin_tiles<STEPS>(p), tiles) - u.first, 0);
             u.c0 = static_cast<int>(((u0 + 1) * n_cta - 1) / total);
             u.c1 = static_cast<int>((u1 * n_cta - 1) / total);
             u.part = t == 0 && end == n ? -1 : 2 * static_cast<int>(blockIdx.x) + (t == 0 ? 1 : 0);
@@ -1236,45 +1242,53 @@ __global__ void __launch_bounds__(Roles<D, NARROW>::kThreads, 1) kv_tile_kernel(
   }
 }
 
-// Joins the units of a first step that several CTAs hold, their pieces in order: 32 rows and 32 columns of one such
-// unit a block, a thread for a row and four columns.  By the unit's last CTA instead, a row to a thread, ten pieces of
+// Joins the units of a first step that several CTAs hold, their pieces in order: blocks take 8 rows of one such unit
+// at a time, a thread for a row and four columns.  By the unit's last CTA instead, a row to a thread, ten pieces of
 // 256 rows took some 50 us of 116 (128 queries of 4 heads, 32768 shared tokens, 8 KV heads).
-constexpr int kJoinRows = 32, kJoinThreads = 256;
+constexpr int kJoinRows = 8;
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ TileParams p, const int blocks) {
+__global__ void __launch_bounds__(kJoinRows * D / 4) kv_join_kernel(const __grid_constant__ TileParams p, const int ctas) {
+  constexpr int kMost = 1024;            // CTAs of the first step
+  __shared__ int first_of[kMost];        // the units: their first CTAs
+  __shared__ int units;
   const AttnParams& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31;
   begin_after_previous();
-  constexpr int kParts = D / 32;         // blocks of columns
-  const int first = blockIdx.x / (blocks * kParts), part = blockIdx.x % kParts;
-  const int row = blockIdx.x / kParts % blocks * kJoinRows + (threadIdx.x & 31), quad = part * 8 + (threadIdx.x >> 5);
-  const KvPiece u = kv_load(p.pieces + first);
-  if (u.last < 0 || row >= u.rows) return;
-  const size_t slot = static_cast<size_t>(p.rows) * (D + 2);
-  auto piece = [&](int cta) { return a.part + (2 * cta + (cta == first ? 1 : 0)) * slot; };
-  float top = kMinusHuge, sum = 0.f;
-#pragma unroll 8
-  for (int cta = first; cta <= u.last; ++cta) {
-    const float2 v = __ldcg(reinterpret_cast<const float2*>(piece(cta)) + row);
-    const float next = fmaxf(top, v.x);
-    sum = sum * exp2_approx(top - next) + v.y * exp2_approx(v.x - next);
-    top = next;
+  if (tid < 32) {
+    int n = 0;
+    for (int c0 = 0; c0 < min(ctas, kMost); c0 += 32) {
+      const bool on = c0 + lane < ctas && kv_load(&p.pieces[c0 + lane].last) >= 0;
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, on);
+      if (on) first_of[n + __popc(who & ((1u << lane) - 1))] = c0 + lane;
+      n += __popc(who);
+    }
+    if (lane == 0) units = n;
   }
-  const int rr = u.row0 + row, qi = rr / a.group;
-  const size_t at = (static_cast<size_t>(u.q0) + qi) * a.q_heads + u.head * a.group + (rr - qi * a.group);
-  const RowEnd end = row_end(a, at, false, top - kBoost, sum);
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  const int chunks = p.rows / kJoinRows;
+  for (int item = blockIdx.x; item < units * chunks; item += gridDim.x) {
+    const int first = first_of[item / chunks], row = item % chunks * kJoinRows + tid % kJoinRows, quad = tid / kJoinRows;
+    const KvPiece u = kv_load(p.pieces + first);
+    if (row >= u.rows) continue;
+    const size_t slot = static_cast<size_t>(p.rows) * (D + 2);
+    float top = kMinusHuge, sum = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int cta = first; cta <= u.last; ++cta) {
-    const float* src = piece(cta);
-    const float by = exp2_approx(__ldcg(src + 2 * row) - top);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(src + p.rows * 2) + static_cast<size_t>(quad) * p.rows + row);
-    s.x = fmaf(v.x, by, s.x);
-    s.y = fmaf(v.y, by, s.y);
-    s.z = fmaf(v.z, by, s.z);
-    s.w = fmaf(v.w, by, s.w);
+    for (int cta = first; cta <= u.last; ++cta) {
+      const float* src = a.part + (2 * cta + (cta == first ? 1 : 0)) * slot;
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(src) + row);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + p.rows * 2) + static_cast<size_t>(quad) * p.rows + row);
+      const float next = fmaxf(top, ml.x), before = exp2_approx(top - next), by = exp2_approx(ml.x - next);
+      top = next;
+      sum = sum * before + ml.y * by;
+      s = make_float4(fmaf(v.x, by, s.x * before), fmaf(v.y, by, s.y * before), fmaf(v.z, by, s.z * before), fmaf(v.w, by, s.w * before));
+    }
+    const int rr = u.row0 + row, qi = rr / a.group;
+    const size_t at = (static_cast<size_t>(u.q0) + qi) * a.q_heads + u.head * a.group + (rr - qi * a.group);
+    const RowEnd end = row_end(a, at, false, top - kBoost, sum);
+    reinterpret_cast<float4*>(a.mid + at * D)[quad] = make_float4(s.x * end.own, s.y * end.own, s.z * end.own, s.w * end.own);
+    if (quad == 0) a.mid_lse[at] = end.lse2;
   }
-  reinterpret_cast<float4*>(a.mid + at * D)[quad] = make_float4(s.x * end.own, s.y * end.own, s.z * end.own, s.w * end.own);
-  if (part == 0 && threadIdx.x < 32) a.mid_lse[at] = end.lse2;
 }
 
 template <int D, bool SEL, bool STEPS, bool NARROW>
@@ -1298,9 +1312,8 @@ cudaError_t launch_tile(const TileParams& p, int num_sms, cudaStream_t stream) {
   if (p.a.step == 0) return launch_tile<D, false, false>(p, num_sms, stream);
   const cudaError_t e = launch_tile<D, false, true>(p, num_sms, stream);
   if (e != cudaSuccess || p.a.step != 1) return e;
-  const int blocks = p.rows / kJoinRows;
   count_launches(1);
-  return launch_overlapped(kv_join_kernel<D>, num_sms * blocks * (D / 32), kJoinThreads, 0, stream, p, blocks);
+  return launch_overlapped(kv_join_kernel<D>, 4 * num_sms, kJoinRows * D / 4, 0, stream, p, num_sms);
 }
 
 }  // namespace
@@ -1343,6 +1356,7 @@ cudaError_t launch_kv_tile(const AttnParams& a, int max_q, int num_sms, cudaStre
   const long long most = static_cast<long long>(a.group) * (sel ? 1 : max_q);
   p.pair = !sel && kv_tile_pairs(a, max_q, num_sms);
   p.rows = p.pair ? 2 * kTileRows : most <= 64 && !sel ? 64 : kTileRows;
+  p.rows_log2 = p.pair ? 8 : most <= 64 && !sel ? 6 : 7;
   if (sel) {
     p.row_tiles = (a.group + p.rows - 1) / p.rows;
     p.slots = a.batch.N * p.row_tiles;

@@ -251,13 +251,18 @@ struct RowEnd {
   float own, mid;
   float lse2;                            // base-2 logarithm of the sum of exponentials
 };
+__device__ __forceinline__ RowEnd row_end(float before, bool joined, float m2, float sum);
 __device__ __forceinline__ RowEnd row_end(const AttnParams& p, size_t at, bool joined, float m2, float sum) {
+  return row_end(joined ? kv_load(p.mid_lse + at) : 0.f, joined, m2, sum);
+}
+// before: the first step's logarithm
+__device__ __forceinline__ RowEnd row_end(float before, bool joined, float m2, float sum) {
   RowEnd e;
   e.own = sum == 0.f ? 0.f : 1.f / sum;
   e.lse2 = sum == 0.f ? -__int_as_float(0x7F800000) : m2 + log2f(sum);
   e.mid = 0.f;
   if (joined) {
-    const float before = kv_load(p.mid_lse + at), top = fmaxf(before, e.lse2);
+    const float top = fmaxf(before, e.lse2);
     if (top > -__int_as_float(0x7F800000)) {
       const float a = exp2_approx(before - top), b = exp2_approx(e.lse2 - top), by = 1.f / (a + b);
       e.mid = a * by;
