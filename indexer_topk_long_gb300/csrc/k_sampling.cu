@@ -39,8 +39,8 @@ constexpr int kList = 1024;              // elements that one CTA takes
 constexpr int kPairs = 256;              // of them, that are all compared with one another
 constexpr int kUnitBits = 44;            // weights are in units of 2^-44
 constexpr uint32_t kNone = 0xFFFFFFFFu;
-constexpr int kRun = 8;                  // 16-byte pieces that a thread reads at a time at first, and remembers the largest of
-constexpr int kRuns = 16;                // of these, at most
+constexpr int kRun = 8;                  // 16-byte pieces that a thread reads at a time at first
+constexpr int kEarly = 2048;             // elements listed while a slice is first read
 
 // (1 - h) 2^(j / 512) in units of 2^-31, rounded, where 1 / (1 - h) = 1 + kWholeBits / 2^32 (see Weigher): by the
 // exponential series in double, at compile time.
@@ -74,7 +74,7 @@ struct Shared {
   u64 answer;
   // a CTA's own
   u64 warp_sum[2][kWarps];
-  uint32_t listed;
+  uint32_t listed, early;
   uint32_t found;
   u64 found_before;
   float min_hi, min_lo;                  // T ln(min_p)
@@ -88,7 +88,8 @@ struct Shared {
     };
     struct {                             // while the largest are looked for
       uint32_t first_hist[kBins];
-      float run_top[kRuns][kThreads];    // of each run of pieces
+      float early_x[kEarly];             // elements at or above a first bound, and their indices
+      uint32_t early_i[kEarly];
     };
     struct {
       u64 weights[kList];                // the list's
@@ -900,7 +901,7 @@ struct Row {
 
   // For need[0] and need[1]: a bound that at least so many of the threads' largest elements reach (keys by ord_f32; on:
   // this thread's counts, they lie in [lo, hi]), to sh.reached; 0 where there are not so many.  By a histogram
-  // of them; sh.hist[0] is zero before.
+  // of them; sh.hist[0] is zero before and after.
   __device__ __forceinline__ void reached_by(const int (&need)[2], bool on, uint32_t key, uint32_t lo, uint32_t hi) {
     const Bins bins(unord_f32(lo), unord_f32(hi));           // (all in the first bin where lo == hi)
     const int bin = on ? bins(unord_f32(key)) : -2;
@@ -913,7 +914,10 @@ struct Row {
     constexpr int kEach = kBins / kThreads;
     uint32_t mine[kEach], run = 0;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) run += mine[e] = sh.hist[0][tid * kEach + e];
+    for (int e = 0; e < kEach; ++e) {
+      run += mine[e] = sh.hist[0][tid * kEach + e];
+      sh.hist[0][tid * kEach + e] = 0;
+    }
     uint32_t upto = run;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -1031,6 +1035,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
   if (tid == 0) {
     sh.found = kNone;
     sh.listed = 0;
+    sh.early = 0;
   }
 
   begin_after_previous();
@@ -1055,25 +1060,58 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
   Row<E> row{sh, logits, p.V, cluster, tid, lane, warp, rank, ctas, mine, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
              first * VEC - shift};
   Largest<E> largest;
+  // A small top-k: what k threads' first elements reach is a bound that the cut is not below, and elements at or above it
+  // are listed while the rest of the slice is read, or what is kept would have to be looked for again.
+  const bool all_listed = p.V <= kList, few = k > 0 && k <= kThreads / 4 * ctas && k <= kPairs;
+  const bool early = few && !all_listed && per_warp > 32 * kRun;
+  float bound = inf, first_most;
+  auto run_at = [&](int i0, uint4 (&v)[kRun]) {
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) v[j] = i0 + 32 * j < row.end ? row.piece(i0 + 32 * j) : row.nothing();
+  };
   {
-    int run = 0;
+    uint4 v[kRun];
+    run_at(row.begin + lane, v);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) largest.add(v[j]);
+    first_most = largest.get();
+    if (early) {
+      const uint32_t key = first_most == first_most ? ord_f32(first_most) : kNone;
+      const bool some = key > ord_f32(-inf);
+      uint32_t lo = some ? key : kNone, hi = key;
+      row.block_range(lo, hi);
+      if (hi < ord_f32(inf) && hi > ord_f32(-inf)) {
+        row.reached_by({k, k}, some, key, lo, hi);
+        if (sh.reached[0] != 0) bound = unord_f32(sh.reached[0]);
+      }
+    }
 #pragma unroll 1
-    for (int i0 = row.begin + lane; i0 < row.end; i0 += 32 * kRun, ++run) {
-      uint4 v[kRun];
+    for (int i0 = row.begin + lane + 32 * kRun; i0 < row.end; i0 += 32 * kRun) {
+      run_at(i0, v);
 #pragma unroll
-      for (int j = 0; j < kRun; ++j) v[j] = i0 + 32 * j < row.end ? row.piece(i0 + 32 * j) : row.nothing();
-      Largest<E> of_run;
+      for (int j = 0; j < kRun; ++j) {
+        Largest<E> of_piece;
+        of_piece.add(v[j]);
+        largest.with(of_piece);
+        if (!(of_piece.get() >= bound)) continue;
+        float x[VEC];
+        unpack<E>(v[j], x);
 #pragma unroll
-      for (int j = 0; j < kRun; ++j) of_run.add(v[j]);
-      sh.run_top[run][tid] = of_run.get();
-      largest.with(of_run);
+        for (int e = 0; e < VEC; ++e)
+          if (x[e] >= bound) {
+            const uint32_t to = atomicAdd(&sh.early, 1u);
+            if (to < kEarly) {
+              sh.early_x[to] = x[e];
+              sh.early_i[to] = static_cast<uint32_t>(row.index0 + (i0 + 32 * j) * VEC + e);
+            }
+          }
+      }
     }
   }
   const float most = largest.get();      // NaN if any element is
   // Few enough are kept for one CTA: all of a small vocabulary, or a small top-k.  For that each CTA finds
   // what its share of k elements reach, and what k of them do, by its threads' largest: k elements of the row reach
   // the least of the CTAs' former bounds, and any of the latter.
-  const bool all_listed = p.V <= kList, few = k > 0 && k <= kThreads / 4 * ctas && k <= kPairs;
   {
     const uint32_t key = most == most ? ord_f32(most) : kNone;   // (above +inf)
     const bool some = key > ord_f32(-inf);
@@ -1135,29 +1173,34 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
     // each CTA's straight into its part of the first one's list
     const float from = fmaxf(unord_f32(floor_key), least);
     const uint32_t room = kList / ctas;
-    if (most >= from) {
-      u64* list = row.at(0)->list + rank * room;
-      int run = 0;
-#pragma unroll 1
-      for (int i0 = row.begin + lane; i0 < row.end; i0 += 32 * kRun, ++run) {
-        if (!(sh.run_top[run][tid] >= from)) continue;
-        uint4 v[kRun];
+    u64* list = row.at(0)->list + rank * room;
+    auto push = [&](float x, uint32_t i) {
+      const uint32_t to = atomicAdd(&sh.listed, 1u);
+      if (to < room) list[to] = ckey(x, static_cast<int>(i));
+    };
+    auto push_piece = [&](const uint4& v, int i) {
+      float x[VEC];
+      unpack<E>(v, x);
 #pragma unroll
-        for (int j = 0; j < kRun; ++j) v[j] = i0 + 32 * j < row.end ? row.piece(i0 + 32 * j) : row.nothing();
+      for (int e = 0; e < VEC; ++e)
+        if (x[e] >= from) push(x[e], static_cast<uint32_t>(row.index0 + i * VEC + e));
+    };
+    const bool again = bound == inf || sh.early > kEarly;    // (the same for all threads)
+    if (again) {
+      if (most >= from) row.template each_piece<kRun>(push_piece);
+    } else {
+      if (first_most >= from) {
+        uint4 v[kRun];
+        run_at(row.begin + lane, v);
 #pragma unroll 1
         for (int j = 0; j < kRun; ++j) {
-          float x[VEC];
-          unpack<E>(v[0], x);
+          push_piece(v[0], row.begin + lane + 32 * j);
 #pragma unroll
           for (int q = 1; q < kRun; ++q) v[q - 1] = v[q];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (x[e] >= from) {
-              const uint32_t to = atomicAdd(&sh.listed, 1u);
-              if (to < room) list[to] = ckey(x[e], row.index0 + (i0 + 32 * j) * VEC + e);
-            }
         }
       }
+      for (uint32_t j = tid; j < sh.early; j += kThreads)
+        if (sh.early_x[j] >= from) push(sh.early_x[j], sh.early_i[j]);
     }
     __syncthreads();
     const int set = row.turn++ & 1;
@@ -1254,7 +1297,6 @@ bool sampling_plan(SamplingParams& p, int num_sms) {
   double best = 0;
   for (int c = 1; c <= kMaxCtas; ++c) {
     const double rounds = std::ceil(p.B * static_cast<double>(c) / (3.8 * num_sms)), time = rounds * (5.0 + pieces * 16.0 / c * (15.0 / 65536.0));
-    if (pieces * 16 > static_cast<long long>(c) * kRuns * kRun * kThreads * 16) continue;
     if (best == 0 || time < best) {
       best = time;
       ctas = c;
