@@ -34,7 +34,7 @@ using u64 = unsigned long long;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
-constexpr int kBins = 1024;
+constexpr int kBins = 1024, kFineBins = 2048;  // (the latter of rough weights)
 constexpr int kList = 1024;              // elements that one CTA takes
 constexpr int kPairs = 256;              // of them, that are all compared with one another
 constexpr int kUnitBits = 44;            // weights are in units of 2^-44
@@ -70,10 +70,10 @@ struct Shared {
   u64 mass[2][kMaxCtas];
   uint32_t count[2][kMaxCtas], lo[2][kMaxCtas], hi[2][kMaxCtas];
   u64 all[kMaxCtas];
-  float rough[kMaxCtas];
+  uint32_t least[kMaxCtas];
   u64 answer;
   // a CTA's own
-  u64 warp_sum[2][kWarps];
+  u64 warp_sum[2][kWarps], listed_sum[kWarps];
   uint32_t listed, early;
   uint32_t found;
   u64 found_before;
@@ -83,8 +83,12 @@ struct Shared {
   float edge[2];
   union {
     struct {
-      uint32_t hist[3][kBins];           // counts, rough weights, or weights in pieces of 15, 15 and 15 bits
+      uint32_t hist[3][kBins];           // counts, or weights in pieces of 15, 15 and 15 bits
       u64 merged[kBins];
+    };
+    struct {
+      uint32_t fine[kFineBins];          // rough weights
+      u64 merged_fine[kFineBins];
     };
     struct {                             // while the largest are looked for
       uint32_t first_hist[kBins];
@@ -186,20 +190,20 @@ struct Weigher {
     const float v = fmaf(r, fmaf(r, fmaf(r, kC, kB), kA), kWhole);
     return x >= least ? weight(__float_as_int(t), v) : 0ull;
   }
-  // Two elements' weights, of those not below `least`, onto a sum: the same numbers, with the arithmetic two at a
-  // time.
-  __device__ __forceinline__ void add2_to(u64& sum, float x0, float x1) const {
+  // Two elements' weights, of those not below `from` (>= least), onto a sum: the same numbers, with the arithmetic
+  // two at a time.
+  __device__ __forceinline__ void add2_to(u64& sum, float from, float x0, float x1) const {
     u64 w0, w1;
     two(x0, x1, w0, w1);
-    if (x0 >= least) sum += w0;
-    if (x1 >= least) sum += w1;
+    if (x0 >= from) sum += w0;
+    if (x1 >= from) sum += w1;
   }
-  // The same, and those of elements above `over` (>= least) onto another.
-  __device__ __forceinline__ void add2_to(u64& sum, u64& above, float over, float x0, float x1) const {
+  // The same, and those of elements above `over` (>= from) onto another.
+  __device__ __forceinline__ void add2_to(u64& sum, u64& above, float from, float over, float x0, float x1) const {
     u64 w0, w1;
     two(x0, x1, w0, w1);
-    if (x0 >= least) sum += w0;
-    if (x1 >= least) sum += w1;
+    if (x0 >= from) sum += w0;
+    if (x1 >= from) sum += w1;
     if (x0 > over) above += w0;
     if (x1 > over) above += w1;
   }
@@ -213,8 +217,6 @@ struct Weigher {
     w0 = weight(__float_as_int(tt.x), v.x);
     w1 = weight(__float_as_int(tt.y), v.y);
   }
-  // About the weight, from 0 to 1 (1% off at most).
-  __device__ __forceinline__ float roughly(float x) const { return exp2_approx(fmaf(x - ref, ch, static_cast<float>(-top))); }
   // ln of the share of x (with a weight) in `total`, right to 2^-24 of itself + 2^-30: x c and log2(total) are each
   // split into a multiple of 1/512, exact, and a rest.
   __device__ float log_share(float x, u64 total) const {
@@ -241,16 +243,22 @@ __device__ __forceinline__ Cut cut_at(u64 key) { return Cut{ckey_score(key), sta
 
 // Equal bins from hi down to lo < hi: halves where the range passes fp32's, and a range too small to
 // divide by scaled up, so that hi is always in the first bin and lo in the last.
-struct Bins {
+template <int N>
+struct BinsOf {
   float half, hi, up, by;
-  __device__ __forceinline__ Bins(float lo, float top) : hi(top) {
+  __device__ __forceinline__ BinsOf(float lo, float top) : hi(top) {
     half = hi - lo < __int_as_float(0x7F800000) ? 1.f : 0.5f;
     const float range = half * hi - half * lo;
     up = range < 1e-30f ? 0x1p100f : 1.f;
-    by = static_cast<float>(kBins) / (range * up);
+    by = range > 0.f ? static_cast<float>(N) / (range * up) : 0.f;
   }
-  __device__ __forceinline__ int operator()(float x) const { return min(__float2int_rz((half * hi - half * x) * up * by), kBins - 1); }
+  // Where x <= hi lies, in bins from hi; of what lies below lo, the end of the last bin.
+  __device__ __forceinline__ float place(float x) const { return fminf((half * hi - half * x) * up * by, N - 0x1p-10f); }
+  // A place's bin, from the place rounded down in a sum with 2^23.
+  static __device__ __forceinline__ int number(float whole) { return __float_as_int(whole) & (N - 1); }
+  __device__ __forceinline__ int operator()(float x) const { return number(__fadd_rd(place(x), 0x1p23f)); }
 };
+using Bins = BinsOf<kBins>;
 
 // Sum over the warp of numbers below 2^53.
 __device__ __forceinline__ u64 warp_total(u64 v) {
@@ -289,7 +297,8 @@ __device__ __forceinline__ u64 place_of(float u, u64 total) {
 // The weight that a share p < 1 of `total` has to reach, at least 1.
 __device__ __forceinline__ u64 share_of(float p, u64 total) {
   bool exact;
-  const u64 t = part_of(p, total, &exact) + (exact ? 0 : 1);
+  u64 t = part_of(p, total, &exact);
+  if (!exact) ++t;
   return t < 1 ? 1 : t;
 }
 
@@ -301,7 +310,7 @@ struct Row {
   int V;
   cg::cluster_group cluster;
   int tid, lane, warp, rank, ctas;
-  int slice;                             // pieces of this CTA's slice, 16 aligned bytes each
+  int slice, longest;                    // pieces (16 aligned bytes) of this CTA's slice, and of the longest one
   int begin, end;                        // this warp's of them
   int index0;                            // vocabulary index of the slice's first element
   int sums = 0;                          // which of warp_sum was used last
@@ -361,19 +370,25 @@ struct Row {
   // The weight of what is kept of this thread's elements.
   __device__ __forceinline__ u64 mass_of(const Weigher& weigh, const Cut& kept) const {
     u64 sum = 0;
-    if (kept.x < weigh.least) {
-      // all that weigh anything
-      each_piece<2>([&](const uint4& v, int) {
-        float x[VEC];
-        unpack<E>(v, x);
+    const float from = fmaxf(kept.x, weigh.least);
+    each_piece<2>([&](const uint4& v, int i) {
+      float x[VEC];
+      unpack<E>(v, x);
+      if (kept.i == kNone) {
 #pragma unroll
-        for (int e = 0; e < VEC; e += 2) weigh.add2_to(sum, x[e], x[e + 1]);
-      });
-    } else {
-      each([&](float x, uint32_t i) {
-        if (kept(x, i)) sum += weigh(x);
-      });
-    }
+        for (int e = 0; e < VEC; e += 2) weigh.add2_to(sum, from, x[e], x[e + 1]);
+      } else {
+        const uint32_t index = static_cast<uint32_t>(index0 + i * VEC);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          u64 w[2];
+          weigh.two(x[e], x[e + 1], w[0], w[1]);
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (x[e + y] >= from && kept(x[e + y], index + e + y)) sum += w[y];
+        }
+      }
+    });
     return sum;
   }
 
@@ -420,8 +435,8 @@ struct Row {
   }
 
   // The first element, in the vocabulary's order, at which the running sum of f exceeds the target that
-  // `target` makes of the total; `hit` is called by the one thread that holds it.  mine: the sum of f over
-  // this thread's elements.  One meeting of the cluster.
+  // `target` makes of the total; `hit` is called by the one thread that holds it.  mine, summed over a warp: f of
+  // its elements.  One meeting of the cluster.
   template <typename F, typename T, typename H>
   __device__ __forceinline__ void find(u64 mine, F f, T target, H hit) {
     u64 before, total;
@@ -567,7 +582,7 @@ struct Row {
   template <bool MASS, typename F>
   __device__ __forceinline__ Cut cut_of_list(uint32_t n, u64 above, u64 target, F f) {
     if (rank == 0) {
-      cut_list<MASS>(n, above, target, f);
+      cut_list<MASS>(n, above, target, [&](u64 key) { return f(ckey_score(key)); });
       if (tid > 0 && tid < ctas) at(tid)->answer = sh.answer;
     }
     cluster.sync();
@@ -616,7 +631,7 @@ struct Row {
     block_sort_regs<P, true>(v, sh.list);
   }
 
-  // The key of the list's element at which the running sum of f, in descending order and from `above`, reaches
+  // The key of the list's element at which the running sum of f (of keys), in descending order and from `above`, reaches
   // `target`, to sh.answer.  First CTA only.  Long lists are cut by a histogram first.
   template <bool MASS, typename F>
   __device__ void cut_list(uint32_t n, u64 above, u64 target, F f) {
@@ -640,7 +655,7 @@ struct Row {
       clear_bins();
 #pragma unroll
       for (int e = 0; e < P; ++e)
-        if (v[e] != 0) add_to_bin<MASS>(bins(ckey_score(v[e])), f(ckey_score(v[e])));
+        if (v[e] != 0) add_to_bin<MASS>(bins(ckey_score(v[e])), f(v[e]));
       __syncthreads();
       for (int i = tid; i < kBins; i += kThreads) sh.merged[i] = bin_sum<MASS>(sh, i);
       above = find_bin(above, target);
@@ -655,7 +670,7 @@ struct Row {
       sort_list(n, v);
       u64 w[P], own = 0;
 #pragma unroll
-      for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < n ? f(ckey_score(v[e])) : 0;
+      for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < n ? f(v[e]) : 0;
       u64 all, run = above + block_before(own, &all);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -665,7 +680,7 @@ struct Row {
     } else {
       uint32_t ignored;
       u64 before = 0, own = 0;
-      if (tid < n) own = sh.weights[tid] = f(ckey_score(sh.list[tid]));
+      if (tid < n) own = sh.weights[tid] = f(sh.list[tid]);
       pair_sums(n, false, &ignored, &before);
       before += above;
       if (tid < n && before < target && before + own >= target) sh.answer = sh.list[tid];
@@ -770,9 +785,40 @@ struct Row {
     }
   }
 
+  // The first k of the elements with lo <= x <= hi, in descending order.  True: they and few others, n in all and none
+  // smaller, are in the first CTA's list.  Else *kept is cut, where there are more than k.  About all are above guess >= lo.
+  __device__ bool first_k(float lo, float guess, float hi, int k, Cut* kept, uint32_t* n) {
+    const Bins bins(guess, hi);
+    clear_bins();
+    each([&](float x, uint32_t) {
+      if (x >= lo) atomicAdd(&sh.hist[0][bins(x)], 1u);
+    });
+    merge_bins<false>();
+    u64 own = 0;
+    for (int i = tid; i < kBins; i += kThreads) own += sh.merged[i];
+    if (block_total(own) <= static_cast<u64>(k)) return false;
+    const u64 above = find_bin(0, k), there = sh.merged[sh.found];
+    const int bin = static_cast<int>(sh.found);
+    if (above + there <= kList) {
+      *n = gather([&](float x, uint32_t) { return x >= lo && bins(x) <= bin; });
+      return true;
+    }
+    auto one = [](float) { return 1ull; };
+    auto in_bin = [&](float x, uint32_t) { return x >= lo && bins(x) == bin; };
+    if (there <= kList) {
+      *kept = cut_of_list<false>(gather(in_bin), above, k, one);
+      return false;
+    }
+    uint32_t a, b;
+    range_of(in_bin, &a, &b);
+    *kept = select<false>(unord_f32(a), unord_f32(b), *kept, above, k, one);
+    return false;
+  }
+
   // The end of what `bins` puts into bins from `bin` on (up: or into those up to `bin`): the largest x (smallest x) of
   // those, by ord_f32, between lo and hi, of which one is there at least.  By a whole warp.
-  __device__ __forceinline__ float edge_of(const Bins& bins, uint32_t lo, uint32_t hi, int bin, bool up) const {
+  template <typename B>
+  __device__ __forceinline__ float edge_of(const B& bins, uint32_t lo, uint32_t hi, int bin, bool up) const {
     while (lo < hi) {
       // 32 places up to the other end; those that are in come first
       const uint32_t step = static_cast<uint32_t>((static_cast<u64>(hi - lo) * (lane + 1) + 31) / 32);
@@ -790,63 +836,74 @@ struct Row {
     return unord_f32(up ? hi : lo);
   }
 
-  // Where the weights of the kept elements, in descending order, reach the share p of their sum.  *mine: the
-  // weight of this thread's that are kept then.
+  // Where the weights of the kept elements, in descending order, reach the share p of their sum.  *mine, summed
+  // over a warp: what is kept then of its elements weighs.
   //
-  // A histogram of rough weights (fp32, right to 2^-17, in whole units of 2^-30 of their sum) shows in which few bins
-  // the cut can be; one pass with exact weights then sums what lies above them and all, and lists what is in them.
+  // A histogram of rough weights shows in which few bins the cut can be; one pass with exact weights then sums what lies
+  // above them and all, and lists what is in them.  A rough weight is that of the bin's upper edge, times a share of it
+  // for the place within the bin, by two terms of a series: no exponential, no conversion, and no sum needed first to
+  // scale them.  (With exponentials scaled by the row's sum, a pass of its own, top-p of 192 rows of 131071 took 162 us.)
   __device__ Cut select_share(float hi, const Cut kept, float p, const Weigher& weigh, u64* mine) {
     const bool simple = kept.i == kNone; // no cut among equal elements so far
     const float least = fmaxf(kept.x, fmaxf(weigh.least, -__int_as_float(0x7F7FFFFF)));
-    auto counts = [&](float x, uint32_t i) { return x >= least && (simple || kept(x, i)); };
-    float rough = 0.f;
-    each([&](float x, uint32_t i) { rough += counts(x, i) ? weigh.roughly(x) : 0.f; });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rough += __shfl_xor_sync(0xFFFFFFFFu, rough, o);
-    // (in units of 2^-20: the largest is at least half)
-    const u64 cta = block_total(lane == 0 ? static_cast<u64>(rough * 0x1p20f) : 0);
-    if (tid < ctas) at(tid)->rough[rank] = static_cast<float>(cta);
-    clear_bins();
-    cluster.sync();
-    rough = 0.f;
-    for (int c = 0; c < ctas; ++c) rough += sh.rough[c];
-    const float unit = 0x1p50f / rough;                      // 2^30 / (rough 2^-20)
-    // V elements of less than (1 - p) / V of the sum cannot hold what is left out, so the cut is above that
-    float lo = least;
-    const float rest = rough * 0x1p-20f * (1.f - p) / V;
-    if (rest > 0.f) lo = fmaxf(lo, fminf(hi, weigh.ref + (weigh.top + log2f(rest) - 0x1p-5f) / weigh.ch - 0x1p-20f * fabsf(weigh.ref)));
-    const Bins bins(fminf(lo, hi), hi);
+    // V elements of less than (1 - p) / V of the largest cannot hold what is left out, so the cut is above that; and
+    // of less than 2^-15 / V they do not count here
+    const float lo = fmaxf(least, fminf(hi, hi + (log2f(fminf(1.f - p, 0x1p-15f) / V) - 0x1p-5f) / weigh.ch - 0x1p-20f * fabsf(hi)));
+    const BinsOf<kFineBins> bins(lo, hi);
+    const float width = weigh.ch * (hi / kFineBins - lo / kFineBins);        // of a bin, in powers of two: 42 / 2048 at most
+    // a bin's sum in units of 2^-bits of its edge's weight stays below 2^32
+    const int bits = min(__clz(longest * VEC) - 1, 20);
+    const float one = __int_as_float((127 + bits) << 23), a1 = one * -0.6931471806f * width, a2 = one * 0.2402265070f * width * width;
+    for (int i = tid; i < kFineBins; i += kThreads) sh.fine[i] = 0;
+    __syncthreads();
     each([&](float x, uint32_t i) {
-      if (x >= lo && (simple || kept(x, i))) atomicAdd(&sh.hist[0][bins(x)], __float2uint_rz(weigh.roughly(x) * unit));
+      if (x >= lo && (simple || kept(x, i))) {
+        const float t = bins.place(x), whole = __fadd_rd(t, 0x1p23f), rest = t - (whole - 0x1p23f);
+        const float w = fmaf(rest, fmaf(rest, a2, a1), one) + 0x1p23f;
+        atomicAdd(&sh.fine[bins.number(whole)], __float_as_uint(w) & 0x7FFFFFu);
+      }
     });
-    merge_bins<false>();
+    cluster.sync();
     {
-      u64 own = 0, total;
-      constexpr int kEach = kBins / kThreads;
+      const int part = (kFineBins + ctas - 1) / ctas;
+      for (int b = rank * part + tid; b < min((rank + 1) * part, kFineBins); b += kThreads) {
+        u64 sum = 0;
+        for (int c = 0; c < ctas; ++c) sum += at(c)->fine[b];
+        // (all together below 2^34 units of 2^-bits of the largest weight, in 2^-16 of those)
+        const u64 w = __float2ull_rz(static_cast<float>(sum) * (0x1p16f * exp2_approx(-width * b)));
+        for (int c = 0; c < ctas; ++c) at(c)->merged_fine[b] = w;
+      }
+    }
+    cluster.sync();
+    {
+      constexpr int kEach = kFineBins / kThreads;
+      u64 w[kEach], own = 0, total;
 #pragma unroll
-      for (int e = 0; e < kEach; ++e) own += sh.merged[tid * kEach + e];
+      for (int e = 0; e < kEach; ++e) own += w[e] = sh.merged_fine[tid * kEach + e];
       u64 run = block_before(own, &total);
-      // weights are off by 2^-17 of themselves and one unit each, their sum by 2^-17 of itself
-      const float t = 0x1p30f * p, off = 0x1p15f + V;
+      // weights, and so their sum, are off by less than 2^-15 of themselves (the series 2^-21, places rounded three times
+      // 2^-16.5, the edges' weights 2^-18), and by their unit; 2^-15 of the sum may be missing
+      const float sum = static_cast<float>(total), off = sum * (0x1p-14f + 1.f / one);
+      const u64 at_least = __float2ull_rz(fmaxf(sum * p - off, 0.f)), at_most = __float2ull_ru(sum * p + off);
       if (tid == 0) {
-        sh.reached_bin[0] = kBins - 1;
-        sh.reached_bin[1] = kBins - 1;
+        sh.reached_bin[0] = kFineBins - 1;
+        sh.reached_bin[1] = kFineBins - 1;
         sh.listed = 0;
       }
+      if (tid < kWarps) sh.listed_sum[tid] = 0;
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        const float a = static_cast<float>(run);
-        run += sh.merged[tid * kEach + e];
-        const float b = static_cast<float>(run);
-        if (a < t - off && b >= t - off) sh.reached_bin[0] = tid * kEach + e;
-        if (a < t + off && b >= t + off) sh.reached_bin[1] = tid * kEach + e;
-        if (tid + e == 0 && !(0.f < t - off)) sh.reached_bin[0] = 0;
+        const u64 before = run;
+        run += w[e];
+        if (before < at_least && run >= at_least) sh.reached_bin[0] = tid * kEach + e;
+        if (before < at_most && run >= at_most) sh.reached_bin[1] = tid * kEach + e;
       }
+      if (tid == 0 && at_least == 0) sh.reached_bin[0] = 0;
       __syncthreads();
       // those bins as a range of x: above it is what lies in bins before them
       if (warp < 2) {
-        const float x = edge_of(bins, ord_f32(fminf(lo, hi)), ord_f32(hi), sh.reached_bin[warp], warp == 1);
+        const float x = edge_of(bins, ord_f32(lo), ord_f32(hi), sh.reached_bin[warp], warp == 1);
         if (lane == 0) sh.edge[warp] = x;
       }
       __syncthreads();
@@ -854,25 +911,31 @@ struct Row {
     // (a first bin without any x: the edge is that of the bins after it)
     const float from = sh.edge[1], upto = sh.edge[0];
     u64 all = 0, above = 0;
-    if (simple && kept.x <= weigh.least) {
-      each_piece<2>([&](const uint4& v, int i) {
-        float x[VEC];
-        unpack<E>(v, x);
+    each_piece<2>([&](const uint4& v, int i) {
+      float x[VEC];
+      unpack<E>(v, x);
+      const uint32_t index = static_cast<uint32_t>(index0 + i * VEC);
+      if (simple) {
 #pragma unroll
-        for (int e = 0; e < VEC; e += 2) weigh.add2_to(all, above, upto, x[e], x[e + 1]);
+        for (int e = 0; e < VEC; e += 2) weigh.add2_to(all, above, least, upto, x[e], x[e + 1]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e)
-          if (x[e] >= from && x[e] <= upto) enlist(x[e], static_cast<uint32_t>(index0 + i * VEC + e));
-      });
-    } else {
-      each([&](float x, uint32_t i) {
-        if (!counts(x, i)) return;
-        const u64 w = weigh(x);
-        all += w;
-        if (x > upto) above += w;
-        else if (x >= from) enlist(x, i);
-      });
-    }
+          if (x[e] >= from && x[e] <= upto) enlist(x[e], index + e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+          u64 w[2];
+          weigh.two(x[e], x[e + 1], w[0], w[1]);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            if (!(x[e + y] >= least && kept(x[e + y], index + e + y))) continue;
+            all += w[y];
+            if (x[e + y] > upto) above += w[y];
+            else if (x[e + y] >= from) enlist(x[e + y], index + e + y);
+          }
+        }
+      }
+    });
     *mine = above;
     const u64 cta_above = block_total(above), cta_all = block_total(all);
     const int set = turn++ & 1;
@@ -881,6 +944,10 @@ struct Row {
       at(tid)->all[rank] = cta_all;
       at(tid)->count[set][rank] = sh.listed;
     }
+    u64 own[P];                          // this CTA's listed ones (the first one's list is used up)
+    const uint32_t listed = sh.listed;
+#pragma unroll
+    for (int e = 0; e < P; ++e) own[e] = tid + e * kThreads < listed ? sh.list[tid + e * kThreads] : 0;
     cluster.sync();
     above = 0;
     u64 total = 0;
@@ -891,11 +958,20 @@ struct Row {
     const u64 target = share_of(p, total);
     const uint32_t n = lists_to_first(set);
     Cut end;
-    if (n <= kList) end = cut_of_list<true>(n, above, target, weigh);
-    else end = select<true>(from, upto, kept, above, target, weigh);
-    each([&](float x, uint32_t i) {
-      if (x >= from && x <= upto && counts(x, i) && end(x, i)) *mine += weigh(x);
-    });
+    if (n <= kList) {
+      end = cut_of_list<true>(n, above, target, weigh);
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        if (own[e] != 0 && end(ckey_score(own[e]), static_cast<uint32_t>(ckey_idx(own[e]))))
+          atomicAdd(&sh.listed_sum[(ckey_idx(own[e]) - index0) / VEC / ((slice + kWarps - 1) / kWarps)], weigh(ckey_score(own[e])));
+      __syncthreads();
+      if (lane == 0) *mine += sh.listed_sum[warp];
+    } else {
+      end = select<true>(from, upto, kept, above, target, weigh);
+      each([&](float x, uint32_t i) {
+        if (x >= from && x <= upto && x >= least && kept(x, i) && end(x, i)) *mine += weigh(x);
+      });
+    }
     return end;
   }
 
@@ -981,44 +1057,47 @@ struct Row {
       if (before <= to && to < before + w) hit(ckey_score(key), static_cast<uint32_t>(ckey_idx(key)), total);
       return;
     }
-    u64 v[P], w[P], own = 0;
-    sort_list(n, v);
-    const uint32_t most = k > 0 ? min(n, static_cast<uint32_t>(k)) : n;
+    // each thread keeps its keys, as the cuts use up the list
+    u64 v[P];
 #pragma unroll
-    for (int e = 0; e < P; ++e) own += w[e] = tid * P + e < most ? weigh(ckey_score(v[e])) : 0;
-    u64 sum, run = block_before(own, &sum);
-    const u64 enough = top_p < 1.f ? share_of(top_p, sum) : ~0ull;
-    own = 0;
+    for (int e = 0; e < P; ++e) v[e] = tid + e * kThreads < n ? sh.list[tid + e * kThreads] : 0;
+    auto total_of = [&]() {
+      u64 own = 0;
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-      const u64 x = w[e];
-      if (run >= enough) w[e] = 0;
-      run += x;
-      own += w[e];
-      sh.weights[tid * P + e] = w[e];
+      for (int e = 0; e < P; ++e) own += v[e] != 0 ? weigh(ckey_score(v[e])) : 0;
+      return block_total(own);
+    };
+    auto list_again = [&](auto key_of) {
+      __syncthreads();
+      if (tid == 0) sh.listed = 0;
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        if (v[e] != 0) sh.list[atomicAdd(&sh.listed, 1u)] = key_of(v[e]);
+      __syncthreads();
+      return sh.listed;
+    };
+    auto cut = [&]() {
+      const Cut c = cut_at(sh.answer);
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        if (v[e] != 0 && !c(ckey_score(v[e]), static_cast<uint32_t>(ckey_idx(v[e])))) v[e] = 0;
+    };
+    if (k > 0 && static_cast<uint32_t>(k) < n) {
+      cut_list<false>(n, 0, k, [](u64) { return 1ull; });
+      cut();
     }
-    const u64 total = block_total(own), to = place_of(u, total);
-    // again in the vocabulary's order (the low half of a key is 2^32 - 1 - index), each with its place before
-    u64 x[P];
-#pragma unroll
-    for (int e = 0; e < P; ++e) x[e] = w[e] != 0 ? (v[e] << 32) | static_cast<uint32_t>(tid * P + e) : 0;
-    __syncthreads();
-    block_sort_regs<P, true>(x, sh.list);
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < P; ++e) sh.list[tid * P + e] = v[e];
-    own = 0;
-#pragma unroll
-    for (int e = 0; e < P; ++e) own += w[e] = x[e] != 0 ? sh.weights[static_cast<uint32_t>(x[e])] : 0;
-    run = block_before(own, &sum);
-#pragma unroll
-    for (int e = 0; e < P; ++e) {
-      if (run <= to && to < run + w[e]) {
-        const u64 key = sh.list[static_cast<uint32_t>(x[e])];
-        hit(ckey_score(key), static_cast<uint32_t>(ckey_idx(key)), total);
-      }
-      run += w[e];
+    u64 total = total_of();
+    if (top_p < 1.f) {
+      cut_list<true>(list_again([](u64 key) { return key; }), 0, share_of(top_p, total), [&](u64 key) { return weigh(ckey_score(key)); });
+      cut();
+      total = total_of();
     }
+    // in the vocabulary's order: (-index, x) takes the place of (x, index); an index is exact in fp32
+    cut_list<true>(list_again([](u64 key) {
+                     return (static_cast<u64>(ord_f32(-static_cast<float>(ckey_idx(key)))) << 32) | (key >> 32);
+                   }), 0, place_of(u, total) + 1, [&](u64 key) { return weigh(unord_f32(static_cast<uint32_t>(key))); });
+    if (tid == 0) hit(unord_f32(static_cast<uint32_t>(sh.answer)), static_cast<uint32_t>(-ckey_score(sh.answer)), total);
   }
 };
 
@@ -1037,6 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
     sh.listed = 0;
     sh.early = 0;
   }
+  cluster.barrier_arrive();
 
   begin_after_previous();
   const float T = p.temperature != nullptr ? kv_load(p.temperature + b) : p.temperature_all;
@@ -1057,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
   const int pieces = (p.V + shift + VEC - 1) / VEC;
   const int first = min(rank * p.per, pieces), mine = min(p.per, pieces - first);
   const int per_warp = (mine + kWarps - 1) / kWarps;
-  Row<E> row{sh, logits, p.V, cluster, tid, lane, warp, rank, ctas, mine, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
+  Row<E> row{sh, logits, p.V, cluster, tid, lane, warp, rank, ctas, mine, p.per, min(warp * per_warp, mine), min((warp + 1) * per_warp, mine),
              first * VEC - shift};
   Largest<E> largest;
   // A small top-k: what k threads' first elements reach is a bound that the cut is not below, and elements at or above it
@@ -1075,6 +1155,21 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
 #pragma unroll
     for (int j = 0; j < kRun; ++j) largest.add(v[j]);
     first_most = largest.get();
+    cluster.barrier_wait();              // the others have begun, and their shared memory can be written
+    if (k > 0 && !few) {
+      // about the smallest
+      uint32_t lo = kNone, ignored = 0;
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) {
+        float x[VEC];
+        unpack<E>(v[j], x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (x[e] > -inf) lo = min(lo, ord_f32(x[e]));
+      }
+      row.block_range(lo, ignored);
+      if (tid < ctas) row.at(tid)->least[rank] = lo;
+    }
     if (early) {
       const uint32_t key = first_most == first_most ? ord_f32(first_most) : kNone;
       const bool some = key > ord_f32(-inf);
@@ -1237,29 +1332,20 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
   }
   Cut kept{least, kNone};
   if (k > 0) {
-    // how many there are, and the smallest
-    uint32_t n = 0, lo = m_key, ignored = 0;
-    row.each([&](float x, uint32_t) {
-      if (x >= least) {
-        ++n;
-        lo = min(lo, ord_f32(x));
-      }
-    });
-    n = static_cast<uint32_t>(row.block_total(n));
-    row.block_range(lo, ignored);
-    const int set = row.turn++ & 1;
-    if (tid < ctas) {
-      Shared* o = row.at(tid);
-      o->count[set][rank] = n;
-      o->lo[set][rank] = lo;
+    // (what weighs nothing need not be counted)
+    float lo = fmaxf(least, weigh.least), guess;
+    if (few) {
+      guess = lo = fmaxf(lo, unord_f32(floor_key));          // k elements reach that
+    } else {
+      uint32_t smallest = m_key;
+      for (int c = 0; c < ctas; ++c) smallest = min(smallest, sh.least[c]);
+      guess = fmaxf(lo, unord_f32(smallest));
     }
-    cluster.sync();
-    n = 0;
-    for (int c = 0; c < ctas; ++c) {
-      n += sh.count[set][c];
-      lo = min(lo, sh.lo[set][c]);
+    uint32_t n = 0;
+    if (row.first_k(lo, fminf(guess, m), m, k, &kept, &n)) {
+      if (rank == 0) row.finish(n, k, top_p, u, weigh, hit);
+      return;
     }
-    if (n > static_cast<uint32_t>(k)) kept = row.template select<false>(unord_f32(lo), m, kept, 0, k, [](float) { return 1ull; });
   }
   u64 mass;
   if (top_p < 1.f) kept = row.select_share(m, kept, top_p, weigh, &mass);
