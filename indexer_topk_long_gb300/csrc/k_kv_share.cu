@@ -8,7 +8,8 @@
 // results are those of the plain attention whatever the tables hold.
 //
 // One CTA a sequence compares its row of the table; the last of them makes the batches.  Bound by
-// latency: 128 sequences of 520 pages take 4 us, 16 of 4128 pages 5.
+// latency: 128 sequences of 520 pages add 6.5 us to what follows, of which the loads' way to memory, the
+// count of CTAs that are done and the last one's scan are three waits in turn.
 #include "kv_internal.cuh"
 
 namespace ltk {

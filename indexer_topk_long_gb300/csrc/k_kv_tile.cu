@@ -20,17 +20,25 @@
 // Roles: warps 0-3 and 4-7 softmax, 8-11 key loader, 12-15 value loader (codes from
 // global memory through registers, e4m3 to f16, 128-byte-swizzled shared memory; a
 // listed key is as good as a paged one), warp 16 issues the MMAs, warp 17 walks the
-// CTA's work, warps 18 and 19 bring the queries.
+// CTA's work, warps 18 and 19 bring the queries (in pairs each softmax thread brings its own row).
 // Work: all units' key tiles form one line, cut into equal pieces, one per CTA; a
 // unit cut by a border is merged by the last of its CTAs in a fixed order.
 //
 // Bound by the products, and by the softmax that feeds them: a pair's key tile takes four
 // 128-cubes, 2050 cycles of the tensor cores at D = 128, and 2 x 128 x 128 exponentials, 1024
 // cycles of each scheduler's exp2 unit.  2048 queries at the end of 32768 tokens, 8 KV heads of
-// 4: 778 us, 1.37 PFLOP/s, 72% of the matrix rate (some 20 us of it is that a warp's lanes agree on
-// whether a wait was given up).  Small work is bound by what a unit costs to
-// begin and end (lookups, queries, the first tile's maxima, the joining of pieces: some 20 us):
-// 24 ragged chunks of 1362 tokens with a window of 1024, D = 64, 42 us.
+// 4: 765 us, 1.39 PFLOP/s, 73% of the matrix rate (some 20 us of it is that a warp's lanes agree on
+// whether a wait was given up; 784 while other warps brought a pair's queries through shared
+// memory).  Small work is bound by what a unit costs to begin and end (lookups, queries, the first
+// tile's maxima, the joining of pieces: some 20 us): 24 ragged chunks of 1362 tokens with a window of
+// 1024, D = 64, 40 us.
+//
+// Attention in two steps (STEPS: the pages that sequences have in common, then each one's rest) writes the
+// first step's results in fp32 with their base-2 lse, and starts the second's rows from them.  In the
+// first step a unit's pieces are joined by a kernel of its own: with few, long units every CTA
+// has a piece of one, and a unit's last CTA would join a dozen of them by itself (128 continuations
+// of 32768 tokens: 144 us, so 126).  It is a template argument because as a run-time one it cost the
+// plain attention up to 2%.
 #include "kv_tensor.cuh"
 
 namespace ltk {

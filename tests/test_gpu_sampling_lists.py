@@ -1,0 +1,49 @@
+"""Tokens drawn where a few hundred elements are kept, and where top-p's cut lies anywhere in a row, against the 64-bit reference."""
+import pytest
+
+import sampling_reference as ref
+from test_gpu_sampling import KINDS, draw, logits_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("k", [255, 257, 600, 1023, 1024, 1025])
+@pytest.mark.parametrize("V", [1024, 1027, 4100, 50257])
+def test_some_hundreds(kind, k, V):
+    x, u = logits_of(4, V, kind, seed=k + V)
+    for settings in (dict(), dict(top_p=0.9), dict(min_p=0.01, top_p=0.5), dict(temperature=9.0, top_p=0.98), dict(temperature=0.02)):
+        ref.check(x, u, draw(x, u, top_k=k, **settings), top_k=k, **settings)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("settings", [dict(top_k=300), dict(top_k=900, top_p=0.7), dict(top_p=0.6), dict(top_k=20, top_p=0.9)], ids=str)
+def test_equal_values(kind, settings):
+    # steps of 1/2 from a spread of 2: hundreds of equal values around every cut; then rows that are mostly masked
+    import torch
+    x, u = logits_of(6, 20011, kind, spread=2.0, seed=5, lift=False)
+    x = (x.float() * 2).round().div(2)
+    x[3:, ::3] = float("-inf")
+    x[4, 700:] = float("-inf")
+    x[5, :] = 1.5
+    x = x.to(getattr(torch, kind))
+    ref.check(x, u, draw(x, u, **settings), **settings)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("spread", [0.0, 2.0 ** -9, 0.5, 8.0, 100.0])
+@pytest.mark.parametrize("V", [1500, 70001])
+def test_share_anywhere(kind, spread, V):
+    import torch
+    x, u = logits_of(5, V, kind, spread=spread, seed=V, lift=False)
+    p = torch.tensor([1e-6, 0.25, 0.75, 0.999999, 1 - 2.0 ** -24])
+    for settings in (dict(), dict(top_k=V // 2), dict(min_p=0.2), dict(temperature=0.3, top_k=V - 1, min_p=1e-5)):
+        ref.check(x, u, draw(x, u, top_p=p, **settings), top_p=p, **settings)
+
+
+def test_long_slices_of_many_rows():
+    # one CTA a row: the longest slices, and the coarsest rough weights
+    x, u = logits_of(640, 90001, "bfloat16", spread=1.0, seed=3, lift=False)
+    rows = range(0, 640, 61)
+    for settings in (dict(top_p=0.9), dict(top_k=1000), dict(top_k=30000, top_p=0.8)):
+        ref.check(x, u, draw(x, u, **settings), rows=rows, **settings)
