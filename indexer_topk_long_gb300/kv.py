@@ -137,6 +137,7 @@ class PagedKVCache:
         self._append, self._attend = self.lib.ltk_kv_append, self.lib.ltk_kv_attention
         self._attend_selected = self.lib.ltk_kv_attention_selected
         self._attend_shared, self._read = self.lib.ltk_kv_attention_shared, self.lib.ltk_kv_read
+        self._shared_sizes = {}          # workspace bytes by (sequences, queries, heads)
         codes, scales = (self.num_pages, self.heads, self.page, self.dim), (self.num_pages, self.heads)
         if not all(given):
             k_codes, v_codes = (torch.zeros(codes, dtype=torch.uint8, device=self.device) for _ in range(2))
@@ -338,16 +339,23 @@ class PagedKVCache:
         else:
             st = self._begin(stream, q, page_table, seq_lens, cu_q, groups, out, lse)
         out, lse = self._outputs(stream, q, n, heads, out, lse)
-        size = ctypes.c_ulonglong(0)
-        ltk._check(self.lib.ltk_kv_shared_bytes(self.h, B, n, heads, ctypes.byref(size)), "ltk_kv_shared_bytes")
-        space = self._new(stream, (size.value,), self._torch.uint8)
+        size = self._shared_sizes.get((B, n, heads)) or self._shared_size(B, n, heads)
+        space = self._new(stream, size, self._torch.uint8)
         failed = self._attend_shared(
             self.h, batch, None if groups is None else groups.data_ptr(), G, self._codes[q.dtype], q.data_ptr(), qs, heads,
             max_q, self._default_scale if scale is None else float(scale), out.data_ptr(), lse.data_ptr(), space.data_ptr(),
-            size.value, st)
+            size, st)
         if failed:
             ltk._check(failed, "ltk_kv_attention_shared")
         return out, lse
+
+    def _shared_size(self, B: int, n: int, heads: int) -> int:
+        size = ctypes.c_ulonglong(0)
+        ltk._check(self.lib.ltk_kv_shared_bytes(self.h, B, n, heads, ctypes.byref(size)), "ltk_kv_shared_bytes")
+        if len(self._shared_sizes) >= 1024:
+            self._shared_sizes.clear()
+        self._shared_sizes[B, n, heads] = size.value
+        return size.value
 
     def read(self, page_table, seq_lens, cu, n: int, dtype=None, cos=None, sin=None, interleaved: bool = False,
              k_out=None, v_out=None, stream=None):
@@ -381,8 +389,11 @@ class PagedKVCache:
         st = self._begin(stream, page_table, seq_lens, cu, cos, sin, k_out, v_out)
         k_out = self._new(stream, shape, dtype) if k_out is None else k_out
         v_out = self._new(stream, shape, dtype) if v_out is None else v_out
-        ltk._check(self._read(self.h, batch, self._codes[dtype], ltk._ptr(cos), ltk._ptr(sin), rows, rot,
-                              1 if interleaved else 0, k_out.data_ptr(), v_out.data_ptr(), st), "ltk_kv_read")
+        failed = self._read(self.h, batch, self._codes[dtype], None if cos is None else cos.data_ptr(),
+                            None if sin is None else sin.data_ptr(), rows, rot, 1 if interleaved else 0, k_out.data_ptr(),
+                            v_out.data_ptr(), st)
+        if failed:
+            ltk._check(failed, "ltk_kv_read")
         return k_out, v_out
 
     def status(self, stream=None) -> int:
