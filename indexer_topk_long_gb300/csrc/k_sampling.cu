@@ -1264,7 +1264,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
   const Weigher weigh(m, T, sh.pow);
   auto hit = [&](float x, uint32_t i, u64 total) {
     *token = static_cast<int>(i);
-    *logp = weigh.log_share(x, total);
+    *logp = weigh(x) == total ? 0.f : weigh.log_share(x, total);   // (the only one that is kept)
   };
   // min-p is a bound on x; -inf is never kept
   float least = -__int_as_float(0x7F7FFFFF);

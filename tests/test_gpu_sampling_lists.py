@@ -47,3 +47,14 @@ def test_long_slices_of_many_rows():
     rows = range(0, 640, 61)
     for settings in (dict(top_p=0.9), dict(top_k=1000), dict(top_k=30000, top_p=0.8)):
         ref.check(x, u, draw(x, u, **settings), rows=rows, **settings)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("settings", [dict(top_k=1), dict(top_p=0.0), dict(top_k=700, top_p=1e-9), dict(min_p=1.0), dict(temperature=1e-3)], ids=str)
+def test_a_single_token_is_certain(kind, settings):
+    # the largest stands alone: its probability is 1, so its logarithm is 0 and nothing near it
+    x, u = logits_of(7, 9001, kind, seed=11, lift=False)
+    x[:, 4321] = 40.0
+    token, logp = draw(x, u, **settings)
+    assert token.tolist() == [4321] * 7
+    assert logp.tolist() == [0.0] * 7
