@@ -1264,7 +1264,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
   const Weigher weigh(m, T, sh.pow);
   auto hit = [&](float x, uint32_t i, u64 total) {
     *token = static_cast<int>(i);
-    *logp = weigh(x) == total ? 0.f : weigh.log_share(x, total);   // (the only one that is kept)
+    // what is (nearly) certain by what is left, of which the weights know as many bits (nothing, for the only one kept)
+    const u64 rest = total - weigh(x);
+    *logp = rest < total >> 7 ? log1pf(-__ull2float_rn(rest) / __ull2float_rn(total)) + 0.f : weigh.log_share(x, total);
   };
   // min-p is a bound on x; -inf is never kept
   float least = -__int_as_float(0x7F7FFFFF);

@@ -58,3 +58,22 @@ def test_a_single_token_is_certain(kind, settings):
     token, logp = draw(x, u, **settings)
     assert token.tolist() == [4321] * 7
     assert logp.tolist() == [0.0] * 7
+
+
+@pytest.mark.parametrize("settings", [dict(), dict(top_k=5), dict(top_p=1 - 2.0 ** -24)], ids=str)
+def test_nearly_certain_tokens(settings):
+    # ln of a share near 1 to as many bits as fp32 has: what is left weighs w with w right to 2^-30.5, its quotient and
+    # log1p are off by 2^-23 at most, so 2^-22 of the result is allowed (and units of 2^-43 for each of the three others)
+    import torch
+    B = 6
+    x = torch.full((B, 3000), -float("inf"))
+    gap = torch.tensor([6.0, 8.0, 10.0, 13.0, 16.0, 20.0])
+    x[:, 17], x[:, 1500], x[:, 2999], x[:, 18] = gap, 0.0, -1.0, -0.5
+    token, logp = draw(x, torch.full((B,), 2.0 ** -20), **settings)
+    assert token.tolist() == [17] * B
+    # the others in descending order; top-p keeps one when what comes before it does not reach its share yet
+    w = torch.exp(x.double()[:, [1500, 18, 2999]] - gap[:, None].double())
+    before = 1 + w.cumsum(1) - w
+    kept = before < settings.get("top_p", 2.0) * (1 + w.sum(1, keepdim=True))
+    want = -torch.log1p((w * kept).sum(1))
+    assert ((logp.cpu().double() - want).abs() <= 2.0 ** -22 * want.abs() + 3 * 2.0 ** -43).all(), (logp, want)
