@@ -22,10 +22,10 @@
 //                      else the cut is looked for among those of one bin;
 //   top-p:             a histogram of rough weights, and a pass with exact ones (select_share).
 //
-// With 192 rows of 131071 in bf16 (50 MB, 7.5 us to read): greedy 17 us, no filter 52, min-p 55, top-k
-// of 50 37, of 1000 106, of 20000 139, top-p of 0.95 123.  Bound by instruction issue: an exact weight
+// With 192 rows of 131071 in bf16 (50 MB, 7.5 us to read): greedy 17 us, no filter 52, min-p 54, top-k
+// of 50 37, of 1000 98, of 20000 131, top-p of 0.95 120.  Bound by instruction issue: an exact weight
 // takes some 20 instructions (27 an element in all), a histogram's atomic with its bin as much time.
-// One row of 32000 in fp32, top-k of 50: 8.5 us, of which the cluster's three meetings and the lists
+// One row of 32000 in fp32, top-k of 50: 7.9 us, of which the cluster's three meetings and the lists
 // they pass on are latency.
 #include <cooperative_groups.h>
 
