@@ -23,9 +23,9 @@
 //   top-p:             a histogram of rough weights, and a pass with exact ones (select_share).
 //
 // With 192 rows of 131071 in bf16 (50 MB, 7.5 us to read): greedy 17 us, no filter 52, min-p 54, top-k
-// of 50 37, of 1000 98, of 20000 131, top-p of 0.95 120.  Bound by instruction issue: an exact weight
+// of 50 34, of 1000 98, of 20000 131, top-p of 0.95 120.  Bound by instruction issue: an exact weight
 // takes some 20 instructions (27 an element in all), a histogram's atomic with its bin as much time.
-// One row of 32000 in fp32, top-k of 50: 7.9 us, of which the cluster's three meetings and the lists
+// One row of 32000 in fp32, top-k of 50: 8 us, of which the cluster's three meetings and the lists
 // they pass on are latency.
 #include <cooperative_groups.h>
 
@@ -1151,10 +1151,11 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
              first * VEC - shift};
   Largest<E> largest;
   // A small top-k: what k threads' first elements reach is a bound that the cut is not below, and elements at or above it
-  // are listed while the rest of the slice is read, or what is kept would have to be looked for again.
+  // are listed while the slice is read, or what is kept would have to be looked for again (256 rows of 131072: 51 us, not 38).
   const bool all_listed = p.V <= kList, few = k > 0 && k <= kThreads / 4 * ctas && k <= kPairs;
-  const bool early = few && !all_listed && per_warp > 32 * kRun;
-  float bound = inf, first_most;
+  const bool early = few && !all_listed;
+  const int needs[2] = {(k + ctas - 1) / ctas, k};
+  float bound = inf;
   auto run_at = [&](int i0, uint4 (&v)[kRun]) {
 #pragma unroll
     for (int j = 0; j < kRun; ++j) v[j] = i0 + 32 * j < row.end ? row.piece(i0 + 32 * j) : row.nothing();
@@ -1162,9 +1163,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
   {
     uint4 v[kRun];
     run_at(row.begin + lane, v);
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) largest.add(v[j]);
-    first_most = largest.get();
     cluster.barrier_wait();              // the others have begun, and their shared memory can be written
     if (k > 0 && !few) {
       // about the smallest
@@ -1181,20 +1179,27 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
       if (tid < ctas) row.at(tid)->least[rank] = lo;
     }
     if (early) {
+      Largest<E> first;
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) first.add(v[j]);
+      const float first_most = first.get();
       const uint32_t key = first_most == first_most ? ord_f32(first_most) : kNone;
       const bool some = key > ord_f32(-inf);
       uint32_t lo = some ? key : kNone, hi = key;
       row.block_range(lo, hi);
       if (hi < ord_f32(inf) && hi > ord_f32(-inf)) {
-        row.reached_by({k, k}, some, key, lo, hi);
-        if (sh.reached[0] != 0) bound = unord_f32(sh.reached[0]);
+        row.reached_by(needs, some, key, lo, hi);
+        if (sh.reached[1] != 0) bound = unord_f32(sh.reached[1]);
       }
     }
 #pragma unroll 1
-    for (int i0 = row.begin + lane + 32 * kRun; i0 < row.end; i0 += 32 * kRun) {
-      run_at(i0, v);
+    for (int i0 = row.begin + lane;;) {
+      if (!early) {
 #pragma unroll
-      for (int j = 0; j < kRun; ++j) {
+        for (int j = 0; j < kRun; ++j) largest.add(v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kRun && early; ++j) {
         Largest<E> of_piece;
         of_piece.add(v[j]);
         largest.with(of_piece);
@@ -1211,6 +1216,9 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
             }
           }
       }
+      i0 += 32 * kRun;
+      if (i0 >= row.end) break;
+      run_at(i0, v);
     }
   }
   const float most = largest.get();      // NaN if any element is
@@ -1223,7 +1231,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
     uint32_t lo = some ? key : kNone, hi = key;
     row.block_range(lo, hi);
     const bool look = few && !all_listed && hi < ord_f32(inf) && hi > ord_f32(-inf);
-    if (look) row.reached_by({(k + ctas - 1) / ctas, k}, some, key, lo, hi);
+    if (look && per_warp > 32 * kRun) row.reached_by(needs, some, key, lo, hi);   // (else those are all elements)
     if (tid < ctas) {
       Shared* o = row.at(tid);
       o->top[rank] = hi;
@@ -1296,16 +1304,6 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
     if (again) {
       if (most >= from) row.each_piece(push_piece);
     } else {
-      if (first_most >= from) {
-        uint4 v[kRun];
-        run_at(row.begin + lane, v);
-#pragma unroll 1
-        for (int j = 0; j < kRun; ++j) {
-          push_piece(v[0], row.begin + lane + 32 * j);
-#pragma unroll
-          for (int q = 1; q < kRun; ++q) v[q - 1] = v[q];
-        }
-      }
       for (uint32_t j = tid; j < sh.early; j += kThreads)
         if (sh.early_x[j] >= from) push(sh.early_x[j], sh.early_i[j]);
     }
