@@ -57,6 +57,11 @@ bool rows_ok(const void* p, long long stride, int heads, int dim) {
 // How long sequences are is only known on the device: 0.6 of the page table is assumed.  Over
 // 130 dense batches (1 to 128 sequences, even and ragged, 98 to 32768 tokens) what this takes
 // is 2% more on average than the better of the two.
+// The first step of a shared attention has few and long units, whose keys many CTAs read in a row: 64 rows
+// take 1.16 T there (D = 64: 0.77 T), 128 rows 1.5 T (1.1 T), and as there is a step after it in any case, all but
+// 2 of what it takes to begin and end overlaps.  Both steps, the first by few rows and by tiles (us, 32 heads on 8):
+// 32 rows of 32768 tokens 70 and 57, of 131072 139 and 104; 4 groups of 48 rows, 8192 tokens 80 and 58, 131072 730
+// and 292 (D = 64: 55 and 45, 418 and 203); of 20 rows, 8192 tokens 57 and 55 (42 and 45).
 struct Estimate {
   bool by_rows;
   double us;                             // of the GPU
@@ -83,8 +88,10 @@ Estimate kv_estimate(const AttnParams& p, int max_q, int num_sms) {
     start = 7.0;
   } else {
     const bool pair = p.idx == nullptr && kv_tile_pairs(p, max_q, num_sms);
-    by_tiles = units(pair ? 256 : rows <= 64 ? 64 : 128) * ((pair ? 8.0 : 3.0) + (wide ? 1.8 : 1.4) * T);
-    start = 12.0;
+    const bool first = p.step == 1 && !pair;
+    const double tile = !first ? (wide ? 1.8 : 1.4) : rows <= 64 ? (wide ? 1.16 : 0.77) : (wide ? 1.5 : 1.1);
+    by_tiles = units(pair ? 256 : rows <= 64 ? 64 : 128) * ((pair ? 8.0 : 3.0) + tile * T);
+    start = p.step == 1 ? 2.0 : 12.0;
   }
   if (p.cache.heads * (by_rows - by_tiles) <= start * num_sms) return {true, p.cache.heads * by_rows / num_sms};
   return {false, p.cache.heads * by_tiles / num_sms + start};

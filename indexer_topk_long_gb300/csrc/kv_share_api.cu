@@ -76,14 +76,16 @@ ltk_status ltk_kv_attention_shared(ltk_kv* h, const ltk_kv_batch* batch, const i
   second.step = 2;
   second.mid = w.mid;
   second.mid_lse = w.mid_lse;
-  // Two steps cost two launches more, the way through memory between them and units that begin and end twice, which
-  // little work does not repay, nor many rows a sequence: its own rows fill the tiles then, and L2 serves what
+  // Two steps cost two launches more, the way through memory between them and units that begin and end twice, 20 us in
+  // all, which little work does not repay, nor many rows a sequence: its own rows fill the tiles then, and L2 serves what
   // sequences share.  Four fifths of the tokens are taken to be shared.  In one step and in two (us): 4 sequences of 1040
   // tokens, 8 heads of 64, 9 and 17; 47 of up to 16700 in 6 groups, 14 query heads of 64 on 2, 30 and 44; 16 x 226
-  // queries behind 8192 tokens, 32 heads of 128 on 8, 443 and 513; 128 sequences of 33000 tokens 1008 and 108.
+  // queries behind 8192 tokens, 32 heads of 128 on 8, 443 and 513; 128 sequences of 33000 tokens 1008 and 108.  Over
+  // 70 batches (2 to 121 sequences in 1 to 5 groups, prompts of 544 to 241270 tokens) what this and the choice of the first
+  // step's kernel take is 1.5% more on average than the best of the three, and more than 10% in three of them.
   first.share = 0.8 * p.share;
   second.share = 0.2 * p.share;
-  if (h->engine == 0 && kv_attention_us(h, p, max_q) <= kv_attention_us(h, first, mean_q) + kv_attention_us(h, second, max_q) + 10.0) {
+  if (h->engine == 0 && kv_attention_us(h, p, max_q) <= kv_attention_us(h, first, mean_q) + kv_attention_us(h, second, max_q) + 20.0) {
     cudaError_t e = groups != nullptr ? launch_kv_groups(share, st) : cudaSuccess;
     if (e == cudaSuccess) e = kv_launch_attention(h, p, max_q, st);
     return kv_cuda_fail(e, "kv shared attention");
