@@ -1387,12 +1387,20 @@ cudaError_t launch_rows(const SamplingParams& p, cudaStream_t stream) {
 bool sampling_plan(SamplingParams& p, int num_sms) {
   const long long size = p.dtype == LTK_F32 ? 4 : 2, vec = 16 / size;
   const long long pieces = (p.V + 2 * vec - 2) / vec;        // wherever the row begins
-  // CTAs of a row: as many as make the rounds of all rows' CTAs (four an SM, and clusters leave some places empty)
-  // the shortest; a CTA has some 5 us to spend on what does not grow with its slice, and 15 us for 64 KB.
+  // CTAs of a row: as many as are estimated to be the fastest.  An SM's CTAs (in rounds of four; clusters leave some places
+  // empty, those of no power of two more) share its issue slots for what each does whatever its slice, 1.5 us, and for 0.06 us
+  // a KB; a round waits 0.1 us a KB of a slice.  A small top-k has little to do but to read, and each CTA its bounds to
+  // find: 2 us, nothing, and 0.1 us a KB.  Over 180 batches (1 to 432 rows of 2000 to 262144) this is 3% behind the best
+  // number of CTAs, with a small top-k as without filters or with top-p.  In us with 1, 2, 4 and 8 CTAs a row: 2 rows of
+  // 145224 in fp32, top-k of 50, 35, 22, 15, 12; 52 of 7508 in bf16 9.0, 8.8, 9.7, 13.5; 228 of 146675 39, 32, 41, 56; 192 of
+  // 131071 without filters 64, 56, 53, 55.
+  const bool small_k = p.top_k == nullptr && p.top_k_all > 0 && p.top_k_all <= kPairs;
+  const double own = small_k ? 2.0 : 1.5, shared = small_k ? 0.0 : 0.06;
   int ctas = 1;
   double best = 0;
   for (int c = 1; c <= kMaxCtas; ++c) {
-    const double rounds = std::ceil(p.B * static_cast<double>(c) / (3.8 * num_sms)), time = rounds * (5.0 + pieces * 16.0 / c * (15.0 / 65536.0));
+    const double n = p.B * static_cast<double>(c), sm = std::ceil(1.05 * n / num_sms), rounds = std::ceil(n / (3.8 * num_sms));
+    const double time = (own * sm + pieces / 64.0 / c * (0.1 * rounds + shared * sm)) * ((c & (c - 1)) != 0 ? 1.1 : 1.0);
     if (best == 0 || time < best) {
       best = time;
       ctas = c;
