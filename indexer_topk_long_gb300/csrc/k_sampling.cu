@@ -50,6 +50,8 @@ constexpr int kPairs = 256;              // of them, that are all compared with 
 constexpr int kUnitBits = 44;            // weights are in units of 2^-44
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr int kRun = 8;                  // 16-byte pieces that a thread reads at a time at first
+constexpr int kMostElements = 131072;    // of a slice: a bin's sum of 15-bit pieces of weights stays below 2^32, a thread's sum of
+                                         // weights within 2^53
 constexpr int kEarly = 2048;             // elements listed while a slice is first read
 
 // (1 - h) 2^(j / 512) in units of 2^-31, rounded, where 1 / (1 - h) = 1 + kWholeBits / 2^32 (see Weigher): by the
@@ -1399,6 +1401,7 @@ bool sampling_plan(SamplingParams& p, int num_sms) {
   int ctas = 1;
   double best = 0;
   for (int c = 1; c <= kMaxCtas; ++c) {
+    if ((pieces + c - 1) / c * vec > kMostElements) continue;
     const double n = p.B * static_cast<double>(c), sm = std::ceil(1.05 * n / num_sms), rounds = std::ceil(n / (3.8 * num_sms));
     const double time = (own * sm + pieces / 64.0 / c * (0.1 * rounds + shared * sm)) * ((c & (c - 1)) != 0 ? 1.1 : 1.0);
     if (best == 0 || time < best) {

@@ -77,3 +77,30 @@ def test_nearly_certain_tokens(settings):
     kept = before < settings.get("top_p", 2.0) * (1 + w.sum(1, keepdim=True))
     want = -torch.log1p((w * kept).sum(1))
     assert ((logp.cpu().double() - want).abs() <= 2.0 ** -22 * want.abs() + 3 * 2.0 ** -43).all(), (logp, want)
+
+
+def test_long_rows_of_few_values():
+    # so many rows that one CTA might take each, and so many equal values that their weights' sums pass 32 bits
+    import torch
+    gen = torch.Generator().manual_seed(9)
+    x = torch.where(torch.rand((2, 400001), generator=gen) < 0.1, 1.0078125, 1.0).bfloat16()
+    x[:, 7] = 3.0
+    u = torch.rand(400, generator=gen)
+    for settings in (dict(top_p=0.5), dict(top_k=390000, top_p=0.7), dict(temperature=0.37, top_p=0.04)):
+        many = x.cuda()[torch.arange(400) % 2]
+        got = draw(many, u, **settings)
+        rows = [0, 1, 198, 399]
+        ref.check(x[[r % 2 for r in rows]], u[rows], [t[rows] for t in got], **settings)
+
+
+@pytest.mark.parametrize("V", [400001, 720000])
+def test_long_rows_of_one_value(V):
+    # every weight is the largest: each element holds 1 / V, which V equal whole numbers show without any error
+    import torch
+    u = torch.rand(300, generator=torch.Generator().manual_seed(2))
+    x = torch.full((300, V), -2.5, dtype=torch.float16, device="cuda")
+    token, logp = draw(x, u)
+    want = (u.double() * V).floor().int()            # (24 bits times V is exact in 64)
+    assert torch.equal(token.cpu(), want)
+    token, logp = draw(x, u, top_p=0.25)
+    assert torch.equal(token.cpu(), (u.double() * -(-V // 4)).floor().int())
