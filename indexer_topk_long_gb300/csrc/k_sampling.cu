@@ -163,10 +163,12 @@ struct Largest {
 
 // Weights: w = 2^(x c - top), top the whole number next above max c, so that the largest is in (1/2, 1].
 //
-// x c is rounded to a multiple of 1/512, whose power comes from the table; what is left, below 2^-10, is
-// fma(x, ch, -that) + x cl with one rounding of 2^-35, and three terms of its exponential series are within
-// 2^-46.  This holds while |x c| < 2^13.  Where max c is beyond 2^12, weights above 0 belong to x within 1% of
-// the maximum, whose difference from it is exact in fp32, and that takes the place of x.
+// x c is rounded to a multiple of 1/512, whose power comes from the table; what is left is
+// r = fma(x, ch, -that) + x cl, |r| <= 2^-10 + |x cl|, with one rounding of 2^-35, and three terms of its exponential series
+// are within 2^-46.  They are a whole number of units of 2^-32 only while (1 + h') 2^32 |2^r - 1| is below 2^22, which is
+// |r| < 1.114 * 2^-10, and |cl| is up to 2^-23.7 of ch: so |x c| has to stay below 1534.  Where max c is beyond 2^10,
+// weights above 0 belong to x within 5% of the maximum, whose difference from it is exact in fp32, and that takes
+// the place of x.  (A bound of 2^12 left weights off by up to 2^-13 with temperatures like 5 and logits near -10000.)
 struct Weigher {
   float ref, least;                      // subtracted from x; smaller x weigh nothing
   float ch, cl;                          // log2(e) / T in two fp32 numbers
@@ -179,7 +181,7 @@ struct Weigher {
     constexpr float kLog2e = 1.44269502162933349609375f, kRest = 1.92596299112661746887e-8f;
     ch = kLog2e / T;
     cl = (fmaf(-ch, T, kLog2e) + kRest) / T;
-    const bool far = !(fabsf(m * ch) < 4096.f);
+    const bool far = !(fabsf(m * ch) < 1024.f);
     ref = far ? m : 0.f;
     top = far ? 0 : static_cast<int>(ceilf(m * ch));
     least = m - (kUnitBits - 2) / ch;    // x c >= top - kUnitBits + 1
@@ -194,7 +196,7 @@ struct Weigher {
     return w >> (top + (kRoundBits >> 9) + (63 - kUnitBits) - (bits >> 9));
   }
   static constexpr float kWhole = 12582912.f, kH = 1.f + kWholeBits / 4294967296.f;
-  // (1 + h') 2^32 (2^r - 1) is at most 2^21.9
+  // (1 + h') 2^32 (2^r - 1) is at most 2^21.95: |x c| is at most 2^10 + 42 here, |r| 1.08 * 2^-10
   static constexpr float kA = 0x1p32f * kH * 0.6931471806f, kB = 0x1p32f * kH * 0.2402265070f, kC = 0x1p32f * kH * 0.05550410866f;
   __device__ __forceinline__ u64 operator()(float x) const {
     const float s = x - ref, t = fmaf(s, ch, kRound);
