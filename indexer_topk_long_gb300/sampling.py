@@ -91,7 +91,10 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None
         _per_row(token, "token", B, i32, device)
     if logp is not None:
         _per_row(logp, "logp", B, f32, device)
-    settings = _PACK(tp, kp, pp, mp, t, int(k), min(p, 1.0), m)
+    whole = int(k)
+    if whole != k:
+        _fail("top_k", f"expected a whole number, got {k}")
+    settings = _PACK(tp, kp, pp, mp, t, whole, min(p, 1.0), m)
     current = torch._C._cuda_getCurrentRawStream(index)
     if stream is None or stream.cuda_stream == current:
         st = current
