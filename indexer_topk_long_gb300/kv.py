@@ -362,10 +362,11 @@ class PagedKVCache:
         """Tokens back in 16 bits: of each sequence the last cu[b + 1] - cu[b], ``n`` in all (cu[B]; the host
         does not look).  With cos, sin keys are rotated back by their positions' rows.  Returns k, v
         [n, heads, dim] of ``dtype`` (bfloat16 by default)."""
-        n, device = int(n), self.device
-        _int32s(n=n)
-        if n < 0:
+        device, whole = self.device, int(n)
+        if whole != n or whole < 0:
             _fail("n", f"expected the number of tokens, got {n}")
+        n = whole
+        _int32s(n=n)
         B, batch = _batch(page_table, seq_lens, cu, n, device, self._int32)
         rot = rows = 0
         if (cos is None) != (sin is None):
