@@ -799,9 +799,9 @@ struct Row {
     }
   }
 
-  // The first k of the elements with lo <= x <= hi, in descending order; what lies below lo is not among the row's first k,
-  // or weighs nothing.  True: they and few others, n in all and none smaller, are in the first CTA's list.  Else *kept is cut
-  // to them.  About all are above guess >= lo.
+  // The first k of the elements with lo <= x <= hi, in descending order; nothing below lo that *kept lets through weighs
+  // anything.  True: they and few others, n in all and none smaller, are in the first CTA's list.  Else *kept is cut, where
+  // there are more than k.  About all are above guess >= lo.
   __device__ bool first_k(float lo, float guess, float hi, int k, Cut* kept, uint32_t* n) {
     const Bins bins(guess, hi);
     clear_bins();
@@ -811,11 +811,7 @@ struct Row {
     merge_bins<false>();
     u64 own = 0;
     for (int i = tid; i < kBins; i += kThreads) own += sh.merged[i];
-    if (block_total(own) <= static_cast<u64>(k)) {
-      // all of them (lo may be a bound that k elements reach: then others, with weights, lie below it)
-      *kept = Cut{lo, kNone};
-      return false;
-    }
+    if (block_total(own) <= static_cast<u64>(k)) return false;
     const u64 above = find_bin(0, k), there = sh.merged[sh.found];
     const int bin = static_cast<int>(sh.found);
     if (above + there <= kList) {
@@ -1354,7 +1350,8 @@ __global__ void __launch_bounds__(kThreads, 4) sample_tokens_kernel(const __grid
     // (what weighs nothing need not be counted)
     float lo = fmaxf(least, weigh.least), guess;
     if (few) {
-      guess = lo = fmaxf(lo, unord_f32(floor_key));          // k elements reach that
+      // k elements reach that; where no more do, others with weights lie below it, and nothing else cuts them off
+      kept.x = guess = lo = fmaxf(lo, unord_f32(floor_key));
     } else {
       uint32_t smallest = m_key;
       for (int c = 0; c < ctas; ++c) smallest = min(smallest, sh.least[c]);
