@@ -449,7 +449,9 @@ ltk_status ltk_kv_attention_selected(ltk_kv* h, const ltk_kv_batch* batch, int d
  * rows of its sequences begin alike, cut to whole pages that all their queries
  * see.  A sequence without queries, without a whole page before its first query
  * or with another first page than the group's first that has one takes no part
- * (it is attended to by itself).  Groups that do not rise from 0 to B set the
+ * (it is attended to by itself, though its queries go through the shared part's products too).  One
+ * part is shared by all that take part: a sequence with one page in common leaves one page
+ * for its whole group, so a group is best made of sequences that have about as much in common.  Groups that do not rise from 0 to B set the
  * device status to LTK_ERR_ARG, and nothing is shared.
  * The shared and the own part of a row are joined in fp32; each is rounded as
  * in ltk_kv_attention.
@@ -508,7 +510,8 @@ ltk_status ltk_kv_status(ltk_kv* h, int* device_status, void* stream);
  * (temperature below 0, infinite or NaN, top_p below 0 or NaN, min_p outside
  * [0, 1], u NaN), -1 and NaN.
  * Weights are whole numbers in units of 2^-44 of (about) the largest, right to
- * 2^-30 of themselves (those below 2^-42 are never drawn), their sums exact: a row's
+ * 2^-30.5 of themselves and that unit (those below 2^-42 are never drawn; with temperatures
+ * above 2^100, logits above 2^114 have weights of fewer bits), their sums exact: a row's
  * result depends on its logits and settings only.  Needs no handle or workspace, neither allocates nor synchronises.
  */
 typedef struct {

@@ -23,8 +23,10 @@
 //   top-p:             a histogram of rough weights, and a pass with exact ones (select_share).
 //
 // With 192 rows of 131071 in bf16 (50 MB, 7.5 us to read): greedy 17 us, no filter 52, min-p 54, top-k
-// of 50 34, of 1000 98, of 20000 131, top-p of 0.95 120.  Bound by instruction issue: an exact weight
-// takes some 20 instructions (27 an element in all), a histogram's atomic with its bin as much time.
+// of 50 34, of 1000 98, of 20000 131, top-p of 0.95 120.  No one thing bounds it: an exact weight takes some
+// 20 instructions (27 an element in all, 22 us of full issue without filters), a histogram's atomic with its bin as much
+// time; but half of the issue slots are empty, as a thread has one piece's load in flight (the largest stall) and
+// CTAs end unevenly.
 // One row of 32000 in fp32, top-k of 50: 8 us, of which the cluster's three meetings and the lists
 // they pass on are latency.
 #include <cooperative_groups.h>

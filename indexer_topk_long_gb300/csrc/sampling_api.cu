@@ -39,6 +39,8 @@ extern "C" ltk_status ltk_sample_tokens(const void* logits, int dtype, long long
   p.u = u;
   p.token = token;
   p.logp = logp;
+  // The entry point's own limits.  The kernel takes kMostElements of a row in each of kMaxCtas CTAs, and V weights of 2^44
+  // have to stay below 2^64 in all: 2^20 - 1 elements of any type.
   if (V > (dtype == LTK_F32 ? 360000 : 720000)) return LTK_ERR_UNSUPPORTED;
   if (B == 0) return LTK_OK;
   if (!aligned_to(logits, dtype == LTK_F32 ? 4 : 2) || !aligned_to(u, 4) || !aligned_to(token, 4) || !aligned_to(logp, 4)) return LTK_ERR_ARG;

@@ -320,7 +320,9 @@ class PagedKVCache:
         """``attention`` without a window for sequences that begin with the same pages: what a
         group of consecutive sequences has in common is found in the page table and read once
         for all of its queries.  ``groups`` [G + 1] (int32) holds the first sequence of each group
-        and, at the end, B; None makes one group of all.  Returns (out, lse)."""
+        and, at the end, B; None makes one group of all.  A group shares what all its members have in
+        common, however little that leaves of what some of them have: two documents behind one short
+        prompt are two groups.  Returns (out, lse)."""
         n, int32 = q.shape[0], self._int32
         B, batch = _batch(page_table, seq_lens, cu_q, n, self.device, int32)
         heads, qs = self._queries(q, n)
